@@ -24,6 +24,14 @@
  *   relu2_mul_bwd    dgate = dh up 2 ReLU(gate), dup = dh ReLU(gate)^2  (PR #1, FFN backward)
  *   lora_bwd         dA, dB of y = s B A x                             (PR #1, LoRA backward)
  *
+ * and, next to the softmax attention, the step before it and a second
+ * attention of linear cost (neither has a counterpart on those pages):
+ *
+ *   qk_norm_rope_fwd, qk_norm_rope_bwd  RMS norm of every query and key head with
+ *                    the position rotation in the same pass (one or several position axes)
+ *   lin_attn_fwd, lin_attn_bwd, lin_attn_decode  linear attention with a decay for each
+ *                    KV head: chunked over sequences, recurrent for single tokens
+ *
  * Conventions shared by every entry point
  *   - All pointers are DEVICE pointers (cudaMalloc'd or equivalent), owned by
  *     the caller.  The library never allocates device memory.  Scratch memory,
@@ -34,7 +42,10 @@
  *   - Inputs and outputs must not overlap, except where stated (rope_bwd allows
  *     dx == dy).
  *   - Every tensor is dense and row-major in the layout given, with its base
- *     address 16-byte aligned.
+ *     address 16-byte aligned, except where a token stride is stated: such a
+ *     tensor [B][T][H][D] has dense rows of H * D elements whose starts are
+ *     `stride` elements apart from token to token, over all B * T tokens (so
+ *     it may be a part of a packed projection); stride 0 means H * D.
  *   - A non-OK status leaves the outputs unspecified; abw_last_error() returns
  *     a message for the last non-OK status of the calling thread.
  *   - Nothing crosses the ABI as a C++ exception, and nothing aborts.
@@ -305,6 +316,131 @@ abw_status attn_bwd_causal_noalloc(const void *q, const void *k, const void *v, 
                                    float *dq, float *dk, float *dv,
                                    int B, int T, int Hq, int Hkv, int D, float scale,
                                    float rope_base, int pos0, abw_stream stream);
+
+/*
+ * qk_norm_rope_fwd -- what stands between the projections and an attention:
+ * per head row x of D components, of queries and keys,
+ *   rms = sqrt(sum_j x_j^2 / D + eps),  n_i = x_i gamma_i / rms,  y = R(theta) n,
+ * where R turns the pairs of the first rotary_dim components,
+ * (n0 cos t - n1 sin t, n0 sin t + n1 cos t), and leaves the others.
+ *   q [B][T][Hq][D], k [B][T][Hkv][D] dtype (f32 or bf16), token strides
+ *         q_stride, k_stride; Hkv == 0 (or Hq == 0): no keys (no queries)
+ *   gamma_q, gamma_k [D] f32, or NULL: no norm (the rotation alone)
+ *   q_out, k_out  dense, same dtype; computed in fp32 and rounded once
+ *   rope_base > 0: theta_i = pos rope_base^(-2i / rotary_dim); rope_base 0:
+ *         no rotation (rotary_dim, positions and sections are not looked at)
+ *   rotary_dim    even, 2 .. D
+ *   interleaved   1: pairs (2i, 2i+1);  0: pairs (i, i + rotary_dim / 2)
+ *   positions     [n_axes][B][T] int32 (any value, negative ones included), or
+ *         NULL: pos = pos0 + t on every axis
+ *   n_axes, sections   1 <= n_axes <= 4; sections is a HOST array of n_axes
+ *         counts >= 0 that add up to rotary_dim / 2: the first sections[0]
+ *         pairs turn by the position on axis 0, the next sections[1] by that on
+ *         axis 1, and so on (time, height and width of image and video
+ *         tokens).  NULL with n_axes == 1.
+ * Angles are exact to 2^-32 turns for every position; eps >= 0.
+ * Supported: D even, 2 <= D <= 512.
+ */
+abw_status qk_norm_rope_fwd(const void *q, const void *k, abw_dtype dtype, const float *gamma_q,
+                            const float *gamma_k, void *q_out, void *k_out, int B, int T, int Hq, int Hkv, int D,
+                            long long q_stride, long long k_stride, float eps, float rope_base, int rotary_dim,
+                            int interleaved, const int *positions, int n_axes, const int *sections, int pos0,
+                            abw_stream stream);
+
+/*
+ * qk_norm_rope_bwd -- gradients of qk_norm_rope_fwd: with dn = R(-theta) dy and
+ * c = sum_j dn_j gamma_j x_j,
+ *   dx_i = (dn_i gamma_i - x_i c / (D rms^2)) / rms,
+ *   dgamma_i = sum over tokens and heads of dn_i x_i / rms   (without a norm dx = dn).
+ *   q, k (and strides), gamma_q, gamma_k, the rotation: as in the forward
+ *   dq_out, dk_out  dense [B][T][Hq][D], [B][T][Hkv][D] dy_dtype (f32 as the
+ *         softmax attention's gradients, or bf16 as the linear attention's)
+ *   dq, dk        dtype, token strides dq_stride, dk_stride (so they may be parts
+ *         of a packed gradient); must not overlap q, k
+ *   dgamma_q, dgamma_k [D] f32, overwritten; each NULL where it is not wanted
+ *         or its gamma is NULL
+ *   workspace     at least qk_norm_rope_bwd_workspace_bytes(D) where a gamma is
+ *         given, else it may be NULL
+ * Sums are fp32 in a fixed order: equal calls on a device give equal bits.
+ */
+size_t qk_norm_rope_bwd_workspace_bytes(int D);
+abw_status qk_norm_rope_bwd(const void *q, const void *k, abw_dtype dtype, const void *dq_out, const void *dk_out,
+                            abw_dtype dy_dtype, const float *gamma_q, const float *gamma_k, void *dq, void *dk,
+                            float *dgamma_q, float *dgamma_k, int B, int T, int Hq, int Hkv, int D,
+                            long long q_stride, long long k_stride, long long dq_stride, long long dk_stride,
+                            float eps, float rope_base, int rotary_dim, int interleaved, const int *positions,
+                            int n_axes, const int *sections, int pos0, void *workspace, size_t workspace_bytes,
+                            abw_stream stream);
+
+/*
+ * lin_attn_fwd -- causal linear attention with a decay for each KV head: with
+ * a = exp(log_decay) of the head and its state S [D][D] (key component, value
+ * component),
+ *   S_t = a S_(t-1) + k_t v_t^T,   o_t = scale S_t^T q_t,
+ * evaluated over chunks of 128 tokens on the tensor core.
+ *   q [B][T][Hq][D], k, v [B][T][Hkv][D] bf16, token strides q_stride, k_stride,
+ *         v_stride; query head h reads KV head h / (Hq / Hkv)
+ *   log_decay     [Hkv] f32, <= 0 (0: no decay; -inf: only the token itself).  A
+ *         constant of the model: it has no gradient
+ *   initial_state [B][Hkv][D][D] f32 or NULL (zero)
+ *   lengths       [B] int32 or NULL: sequence b has min(max(lengths[b], 0), T)
+ *         tokens; what q, k, v hold behind them is not looked at (NaN included)
+ *         and o there is written as 0
+ *   o             [B][T][Hq][D] bf16, token stride o_stride
+ *   final_state   [B][Hkv][D][D] f32 or NULL: the state behind each sequence's last
+ *         token (may be the same buffer as initial_state)
+ *   workspace     at least lin_attn_fwd_workspace_bytes(); unspecified contents
+ * Scores and the chunk states that enter a product are rounded to bf16; sums
+ * and the states themselves are fp32, and final_state is good to fp32
+ * rounding.  Equal calls give equal bits.
+ * Supported: D == 64 or 128; T >= 0; Hq % Hkv == 0; strides multiples of 8.
+ */
+size_t lin_attn_fwd_workspace_bytes(int B, int T, int Hkv, int D);
+abw_status lin_attn_fwd(const void *q, const void *k, const void *v, const float *log_decay,
+                        const float *initial_state, const int *lengths, void *o, float *final_state, int B, int T,
+                        int Hq, int Hkv, int D, long long q_stride, long long k_stride, long long v_stride,
+                        long long o_stride, float scale, void *workspace, size_t workspace_bytes,
+                        abw_stream stream);
+
+/*
+ * lin_attn_bwd -- gradients of lin_attn_fwd.  With R_t the gradient of S_t,
+ *   R_t = a R_(t+1) + scale q_t do_t^T (summed over the query heads of the group),
+ *   dq_t = scale S_t do_t,   dk_t = R_t v_t,   dv_t = R_t^T k_t,
+ *   dinitial_state = a R_1,   R behind the last token = dfinal_state.
+ * The forward's states are formed again; nothing is saved by the forward.
+ *   q, k, v, log_decay, initial_state, lengths: as in the forward
+ *   dout          dense [B][T][Hq][D] bf16
+ *   dfinal_state  [B][Hkv][D][D] f32 or NULL (zero)
+ *   dq, dk, dv    bf16, token strides dq_stride, dk_stride, dv_stride; 0 behind
+ *         each sequence's last token
+ *   dinitial_state [B][Hkv][D][D] f32 or NULL (may be the same buffer as
+ *         dfinal_state)
+ *   workspace     at least lin_attn_bwd_workspace_bytes()
+ * Supported sizes and precision: as in the forward.
+ */
+size_t lin_attn_bwd_workspace_bytes(int B, int T, int Hkv, int D);
+abw_status lin_attn_bwd(const void *q, const void *k, const void *v, const void *dout, const float *log_decay,
+                        const float *initial_state, const float *dfinal_state, const int *lengths, void *dq, void *dk,
+                        void *dv, float *dinitial_state, int B, int T, int Hq, int Hkv, int D, long long q_stride,
+                        long long k_stride, long long v_stride, long long dq_stride, long long dk_stride,
+                        long long dv_stride, float scale, void *workspace, size_t workspace_bytes,
+                        abw_stream stream);
+
+/*
+ * lin_attn_decode -- one token per sequence: the recurrence of lin_attn_fwd,
+ *   S = a S + k v^T (in place),   o = scale S^T q.
+ *   q [B][Hq][D], k, v [B][Hkv][D], o [B][Hq][D] dtype (f32 or bf16)
+ *   state         [n_states][Hkv][D][D] f32, read and written
+ *   log_decay     [Hkv] f32, <= 0
+ *   slots         [B] int32 or NULL (then n_states >= B and row b works on state
+ *         b): row b works on state slots[b].  A row whose slot is not in
+ *         0 .. n_states - 1 is empty: o is 0 there and no state is touched.  Two rows
+ *         of a call must not name the same state
+ * Supported: D == 64 or 128; Hq % Hkv == 0 with Hq / Hkv <= 8.
+ */
+abw_status lin_attn_decode(const void *q, const void *k, const void *v, abw_dtype dtype, float *state,
+                           const float *log_decay, const int *slots, void *o, int B, int Hq, int Hkv, int D,
+                           int n_states, float scale, abw_stream stream);
 
 #ifdef __cplusplus
 }

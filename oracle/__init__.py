@@ -52,6 +52,8 @@ __all__ = [
     "chain_layer_backward",
     "relu2_mul_forward", "relu2_mul_backward",
     "lora_forward", "lora_backward",
+    "section_angles", "rope_turn", "qk_norm_rope_forward", "qk_norm_rope_backward",
+    "lin_attn_forward", "lin_attn_backward", "lin_attn_decode",
     "numerical_grad", "check_gradient",
 ]
 
@@ -466,6 +468,109 @@ def lora_backward(x, A, B, dy, scale):
     dh = scale * (dy @ B)
     dA = dh.T @ x
     return dA, dB
+
+
+# ==========================================================================
+# Per-head norm with rotation, and linear attention with a decay for each
+# head.  These steps are on none of the pages above: they are written from
+# their definitions (stated in each function).
+# ==========================================================================
+def section_angles(positions, rotary_dim, base, sections):
+    """theta[b, t, i] = positions[axis(i), b, t] base^(-2i / rotary_dim), the
+    first sections[0] pairs on axis 0, the next sections[1] on axis 1, ..."""
+    axis = np.repeat(np.arange(len(sections)), sections)
+    i = np.arange(rotary_dim // 2, dtype=np.float64)
+    return np.moveaxis(_f64(positions)[axis], 0, -1) * np.power(float(base), -2.0 * i / rotary_dim)
+
+
+def rope_turn(x, theta, rotary_dim, interleaved, sign=1.0):
+    """The pairs of the first rotary_dim components of x [B][T][H][D] turned
+    by sign * theta [B][T][rotary_dim / 2]; the others unchanged."""
+    x = _f64(x)
+    head = rope_forward(x[..., :rotary_dim], sign * _f64(theta), interleaved)
+    return np.concatenate([head, x[..., rotary_dim:]], axis=-1)
+
+
+def qk_norm_rope_forward(x, gamma, eps, theta=None, rotary_dim=0, interleaved=True):
+    """Per head row of x [B][T][H][D]: y = R(theta)(gamma x / rms), rms =
+    sqrt(mean x^2 + eps); gamma None: no norm; theta None: no rotation."""
+    y = _f64(x)
+    if gamma is not None:
+        y = rmsnorm_forward(y, gamma, eps)
+    return y if theta is None else rope_turn(y, theta, rotary_dim, interleaved)
+
+
+def qk_norm_rope_backward(x, gamma, dy, eps, theta=None, rotary_dim=0, interleaved=True):
+    """(dx, dgamma) of qk_norm_rope_forward: the rotation's transpose, then
+    the norm's backward; dgamma summed over every row (None without gamma)."""
+    dn = _f64(dy) if theta is None else rope_turn(dy, theta, rotary_dim, interleaved, -1.0)
+    if gamma is None:
+        return dn, None
+    x = _f64(x)
+    D = x.shape[-1]
+    return (rmsnorm_backward(x.reshape(-1, D), gamma, dn.reshape(-1, D), eps).reshape(x.shape),
+            rmsnorm_backward_gamma(x.reshape(-1, D), dn.reshape(-1, D), eps))
+
+
+def _lengths(lengths, B, T):
+    return [T] * B if lengths is None else [min(max(int(n), 0), T) for n in lengths]
+
+
+def lin_attn_forward(q, k, v, log_decay, scale, initial=None, lengths=None):
+    """Token by token: S = a S + k v^T, o = scale S^T q, a = exp(log_decay) of
+    the KV head; query head h reads KV head h // G.  Returns (o, final
+    state); o is 0 behind a sequence's length."""
+    q, k, v = _f64(q), _f64(k), _f64(v)
+    B, T, Hq, D = q.shape
+    Hkv = k.shape[2]
+    G = Hq // Hkv
+    a = np.exp(_f64(log_decay))[:, None, None]
+    o = np.zeros_like(q)
+    S = np.zeros((B, Hkv, D, D)) if initial is None else _f64(initial).copy()
+    for b, n in enumerate(_lengths(lengths, B, T)):
+        for t in range(n):
+            S[b] = a * S[b] + k[b, t, :, :, None] * v[b, t, :, None, :]
+            o[b, t] = scale * np.einsum("hgd,hde->hge", q[b, t].reshape(Hkv, G, D), S[b]).reshape(Hq, D)
+    return o, S
+
+
+def lin_attn_backward(q, k, v, dout, log_decay, scale, initial=None, dfinal=None, lengths=None):
+    """Adjoint of lin_attn_forward, token by token from the last: with R the
+    gradient of the state, R += scale q do^T, dq = scale S do, dk = R v,
+    dv = R^T k, R = a R.  Returns (dq, dk, dv, dinitial)."""
+    q, k, v, dout = _f64(q), _f64(k), _f64(v), _f64(dout)
+    B, T, Hq, D = q.shape
+    Hkv = k.shape[2]
+    G = Hq // Hkv
+    a = np.exp(_f64(log_decay))[:, None, None]
+    dq, dk, dv = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
+    S = np.zeros((B, Hkv, D, D)) if initial is None else _f64(initial).copy()
+    R = np.zeros((B, Hkv, D, D)) if dfinal is None else _f64(dfinal).copy()
+    for b, n in enumerate(_lengths(lengths, B, T)):
+        for t in range(n):
+            S[b] = a * S[b] + k[b, t, :, :, None] * v[b, t, :, None, :]
+            dq[b, t] = scale * np.einsum("hde,hge->hgd", S[b], dout[b, t].reshape(Hkv, G, D)).reshape(Hq, D)
+        for t in range(n - 1, -1, -1):
+            R[b] += scale * np.einsum("hgd,hge->hde", q[b, t].reshape(Hkv, G, D), dout[b, t].reshape(Hkv, G, D))
+            dk[b, t] = np.einsum("hde,he->hd", R[b], v[b, t])
+            dv[b, t] = np.einsum("hde,hd->he", R[b], k[b, t])
+            R[b] = a * R[b]
+    return dq, dk, dv, R
+
+
+def lin_attn_decode(q, k, v, state, log_decay, scale, slots=None):
+    """One step of lin_attn_forward for row b on state slots[b]; a row whose
+    slot is not a state's gives 0.  Returns (o, new states)."""
+    q, k, v, S = _f64(q), _f64(k), _f64(v), _f64(state).copy()
+    B, Hq, D = q.shape
+    Hkv = k.shape[1]
+    o = np.zeros_like(q)
+    for b in range(B):
+        at = b if slots is None else int(slots[b])
+        if 0 <= at < S.shape[0]:
+            S[at] = np.exp(_f64(log_decay))[:, None, None] * S[at] + k[b, :, :, None] * v[b, :, None, :]
+            o[b] = scale * np.einsum("hgd,hde->hge", q[b].reshape(Hkv, Hq // Hkv, D), S[at]).reshape(Hq, D)
+    return o, S
 
 
 # ==========================================================================

@@ -9,7 +9,9 @@ kernels; nothing here computes, and there is no fallback path.
 Functions (same names as the C ABI):
   softmax_bwd, rope_bwd, rmsnorm_bwd, rmsnorm_bwd_dgamma, relu2_mul_bwd,
   lora_bwd, attn_bwd_decode, attn_fwd_causal, attn_bwd_causal,
-  attn_bwd_causal_saved_p, attn_bwd_causal_workspace_bytes, device_check
+  attn_bwd_causal_saved_p, attn_bwd_causal_workspace_bytes, device_check,
+  qk_norm_rope_fwd, qk_norm_rope_bwd, lin_attn_fwd, lin_attn_bwd,
+  lin_attn_decode and their *_workspace_bytes
 """
 from __future__ import annotations
 
@@ -22,7 +24,9 @@ from . import _binding as _b
 
 __all__ = ["softmax_bwd", "rope_bwd", "rmsnorm_bwd", "rmsnorm_bwd_dgamma", "relu2_mul_bwd", "lora_bwd",
            "attn_bwd_decode", "attn_fwd_causal", "attn_bwd_causal", "attn_bwd_causal_saved_p",
-           "attn_bwd_causal_workspace_bytes", "device_check", "AbwError", "library"]
+           "attn_bwd_causal_workspace_bytes", "device_check", "AbwError", "library",
+           "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes", "lin_attn_fwd",
+           "lin_attn_fwd_workspace_bytes", "lin_attn_bwd", "lin_attn_bwd_workspace_bytes", "lin_attn_decode"]
 
 AbwError = _b.AbwError
 
@@ -289,3 +293,272 @@ def attn_bwd_causal_saved_p(q, k, v, p_attn, o, dout, scale=None, rope_base=0.0,
                                                _p(workspace), workspace.numel(), _s(stream)),
              "attn_bwd_causal_saved_p")
     return dq, dk, dv
+
+
+# --------------------------------------------------------------------------
+# Per-head norm with rotation, and linear attention
+# --------------------------------------------------------------------------
+def _rows(t, name, dtypes, shape):
+    """Checks a [B][T][H][D] tensor whose tokens may be apart (a part of a
+    packed projection) and returns its token stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} dtype {t.dtype} not in {dtypes}")
+    if t.shape != shape:
+        raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.is_contiguous():
+        return 0
+    B, T, H, D = shape
+    sb, stt, sh, sd = t.stride()
+    token = stt if T > 1 else sb
+    if (D > 1 and sd != 1) or (H > 1 and sh != D) or (B > 1 and T > 1 and sb != T * stt) or token < H * D:
+        raise ValueError(f"{name} must have dense [H][D] rows at one stride from token to token")
+    return token
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory for the launch stream (the caching allocator reuses a block in
+    the order of the stream it was allocated on)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _call(op, fn, tensors, stream, *args):
+    """Launches on the tensors' device, which they have to share."""
+    d = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != d:
+            raise ValueError(f"{op}: tensors on {d} and {t.device}")
+    if stream is not None and stream.device != d:
+        raise ValueError(f"{op}: stream on {stream.device}, tensors on {d}")
+    if d.index == torch.cuda.current_device():
+        status = fn(*args, _s(stream))
+    else:
+        with torch.cuda.device(d):
+            status = fn(*args, _s(stream))
+    if status != _b.OK:
+        _b.check(status, op)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rotation(B, T, D, rope_base, rotary_dim, positions, sections):
+    """(rotary_dim, n_axes, sections as a host array or None)."""
+    axes = 1 if sections is None else len(sections)
+    if not rope_base:
+        return 0, 1, None
+    if positions is not None:
+        _req(positions, "positions", (torch.int32,))
+        if tuple(positions.shape) != (axes, B, T) and not (axes == 1 and tuple(positions.shape) == (B, T)):
+            raise ValueError(f"positions shape {tuple(positions.shape)} != {(axes, B, T)}")
+    host = None if sections is None else (ctypes.c_int * axes)(*sections)
+    return D if rotary_dim is None else int(rotary_dim), axes, host
+
+
+def qk_norm_rope_fwd(q, k, gamma_q=None, gamma_k=None, eps=1e-6, rope_base=0.0, rotary_dim=None, interleaved=True,
+                     positions=None, sections=None, pos0=0, q_out=None, k_out=None, stream=None):
+    """RMS norm of every query and key head (gamma_q, gamma_k [D] fp32; None:
+    no norm) and the rotation of its first ``rotary_dim`` components (all, if
+    None; rope_base 0: none).  q [B][T][Hq][D], k [B][T][Hkv][D] or None,
+    fp32 or bf16, possibly parts of a packed projection.  positions
+    [axes][B][T] int32 (None: pos0 + t); ``sections`` gives each axis its
+    number of pairs.  Returns dense (q_out, k_out) of the inputs' dtype."""
+    dts = (torch.float32, torch.bfloat16)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be [B][T][Hq][D]")
+    B, T, Hq, D = q.shape
+    qs = _rows(q, "q", dts, q.shape)
+    Hkv = ks = 0
+    if k is not None:
+        Hkv = k.shape[2] if k.dim() == 4 else 0
+        ks = _rows(k, "k", (q.dtype,), (B, T, Hkv, D))
+    for g, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
+        if g is not None:
+            _req(g, name, (torch.float32,), (D,))
+    R, axes, host = _rotation(B, T, D, rope_base, rotary_dim, positions, sections)
+    q_out = _empty(q.shape, q.dtype, q.device, stream) if q_out is None else q_out
+    _req(q_out, "q_out", (q.dtype,), q.shape)
+    if k is not None:
+        k_out = _empty(k.shape, k.dtype, k.device, stream) if k_out is None else k_out
+        _req(k_out, "k_out", (k.dtype,), k.shape)
+    else:
+        k_out = None
+    _call("qk_norm_rope_fwd", library().qk_norm_rope_fwd, (q, k, gamma_q, gamma_k, q_out, k_out, positions), stream,
+          _addr(q), _addr(k), _DT[q.dtype], _addr(gamma_q), _addr(gamma_k), _addr(q_out), _addr(k_out), B, T, Hq, Hkv, D,
+          qs, ks, float(eps), float(rope_base), R, 1 if interleaved else 0, _addr(positions), axes, host, int(pos0))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd_workspace_bytes(D) -> int:
+    return int(library().qk_norm_rope_bwd_workspace_bytes(D))
+
+
+def qk_norm_rope_bwd(q, k, dq_out, dk_out, gamma_q=None, gamma_k=None, eps=1e-6, rope_base=0.0, rotary_dim=None,
+                     interleaved=True, positions=None, sections=None, pos0=0, dq=None, dk=None, dgamma_q=None,
+                     dgamma_k=None, workspace=None, stream=None):
+    """Gradients of qk_norm_rope_fwd.  dq_out, dk_out are dense, fp32 or bf16
+    (the same for both).  dq, dk have the inputs' dtype and may be parts of a
+    packed gradient.  Returns (dq, dk, dgamma_q, dgamma_k), None where there
+    is no k or no gamma."""
+    dts = (torch.float32, torch.bfloat16)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be [B][T][Hq][D]")
+    B, T, Hq, D = q.shape
+    qs = _rows(q, "q", dts, q.shape)
+    _req(dq_out, "dq_out", dts, q.shape)
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dqs = _rows(dq, "dq", (q.dtype,), q.shape)
+    Hkv = ks = dks = 0
+    if k is not None:
+        Hkv = k.shape[2] if k.dim() == 4 else 0
+        ks = _rows(k, "k", (q.dtype,), (B, T, Hkv, D))
+        _req(dk_out, "dk_out", (dq_out.dtype,), k.shape)
+        dk = _empty(k.shape, k.dtype, k.device, stream) if dk is None else dk
+        dks = _rows(dk, "dk", (q.dtype,), k.shape)
+    else:
+        dk_out = dk = gamma_k = None
+    if gamma_q is not None:
+        _req(gamma_q, "gamma_q", (torch.float32,), (D,))
+        dgamma_q = _empty((D,), torch.float32, q.device, stream) if dgamma_q is None else dgamma_q
+        _req(dgamma_q, "dgamma_q", (torch.float32,), (D,))
+    else:
+        dgamma_q = None
+    if gamma_k is not None:
+        _req(gamma_k, "gamma_k", (torch.float32,), (D,))
+        dgamma_k = _empty((D,), torch.float32, q.device, stream) if dgamma_k is None else dgamma_k
+        _req(dgamma_k, "dgamma_k", (torch.float32,), (D,))
+    else:
+        dgamma_k = None
+    R, axes, host = _rotation(B, T, D, rope_base, rotary_dim, positions, sections)
+    if workspace is None and (gamma_q is not None or gamma_k is not None):
+        workspace = _empty((qk_norm_rope_bwd_workspace_bytes(D),), torch.uint8, q.device, stream)
+    if workspace is not None:
+        _req(workspace, "workspace", (torch.uint8,))
+    _call("qk_norm_rope_bwd", library().qk_norm_rope_bwd,
+          (q, k, dq_out, dk_out, gamma_q, gamma_k, dq, dk, dgamma_q, dgamma_k, positions, workspace), stream, _addr(q),
+          _addr(k), _DT[q.dtype], _addr(dq_out), _addr(dk_out), _DT[dq_out.dtype], _addr(gamma_q), _addr(gamma_k),
+          _addr(dq), _addr(dk), _addr(dgamma_q), _addr(dgamma_k), B, T, Hq, Hkv, D, qs, ks, dqs, dks, float(eps),
+          float(rope_base), R, 1 if interleaved else 0, _addr(positions), axes, host, int(pos0), _addr(workspace),
+          0 if workspace is None else workspace.numel())
+    return dq, dk, dgamma_q, dgamma_k
+
+
+def lin_attn_fwd_workspace_bytes(B, T, Hkv, D) -> int:
+    return int(library().lin_attn_fwd_workspace_bytes(B, T, Hkv, D))
+
+
+def lin_attn_bwd_workspace_bytes(B, T, Hkv, D) -> int:
+    return int(library().lin_attn_bwd_workspace_bytes(B, T, Hkv, D))
+
+
+def _lin_inputs(q, k, v, log_decay, initial_state, lengths):
+    bf = (torch.bfloat16,)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be [B][T][Hq][D]")
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be [B][T][Hkv][D]")
+    B, T, Hq, D = q.shape
+    Hkv = k.shape[2]
+    strides = (_rows(q, "q", bf, q.shape), _rows(k, "k", bf, (B, T, Hkv, D)), _rows(v, "v", bf, (B, T, Hkv, D)))
+    _req(log_decay, "log_decay", (torch.float32,), (Hkv,))
+    if initial_state is not None:
+        _req(initial_state, "initial_state", (torch.float32,), (B, Hkv, D, D))
+    if lengths is not None:
+        _req(lengths, "lengths", (torch.int32,), (B,))
+    return (B, T, Hq, Hkv, D), strides
+
+
+def lin_attn_fwd(q, k, v, log_decay, scale=None, initial_state=None, lengths=None, want_final_state=False, o=None,
+                 final_state=None, workspace=None, stream=None):
+    """Causal linear attention with a decay for each KV head: S = a S + k v^T,
+    o = scale S^T q, a = exp(log_decay).  q [B][T][Hq][D], k, v
+    [B][T][Hkv][D] bf16 (possibly parts of a packed projection), log_decay
+    [Hkv] fp32 <= 0, initial_state [B][Hkv][D][D] fp32 or None, lengths [B]
+    int32 or None (tokens of each sequence; o is 0 behind them).  Returns
+    (o [B][T][Hq][D] bf16, final_state fp32 or None); final_state may be the
+    initial_state tensor."""
+    dims, strides = _lin_inputs(q, k, v, log_decay, initial_state, lengths)
+    B, T, Hq, Hkv, D = dims
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    o = _empty(q.shape, q.dtype, q.device, stream) if o is None else o
+    os = _rows(o, "o", (torch.bfloat16,), q.shape)
+    if final_state is None and want_final_state:
+        final_state = _empty((B, Hkv, D, D), torch.float32, q.device, stream)
+    if final_state is not None:
+        _req(final_state, "final_state", (torch.float32,), (B, Hkv, D, D))
+    if workspace is None:
+        workspace = _empty((lin_attn_fwd_workspace_bytes(B, T, Hkv, D),), torch.uint8, q.device, stream)
+    _req(workspace, "workspace", (torch.uint8,))
+    _call("lin_attn_fwd", library().lin_attn_fwd,
+          (q, k, v, log_decay, initial_state, lengths, o, final_state, workspace), stream, _addr(q), _addr(k), _addr(v),
+          _addr(log_decay), _addr(initial_state), _addr(lengths), _addr(o), _addr(final_state), *dims, *strides, os,
+          float(scale), _addr(workspace), workspace.numel())
+    return o, final_state
+
+
+def lin_attn_bwd(q, k, v, dout, log_decay, scale=None, initial_state=None, dfinal_state=None, lengths=None,
+                 want_dinitial_state=False, dq=None, dk=None, dv=None, dinitial_state=None, workspace=None, stream=None):
+    """Gradients of lin_attn_fwd: dout [B][T][Hq][D] bf16, dfinal_state
+    [B][Hkv][D][D] fp32 or None.  Returns (dq, dk, dv) bf16 (given ones may be
+    parts of a packed gradient) and dinitial_state fp32 or None."""
+    dims, strides = _lin_inputs(q, k, v, log_decay, initial_state, lengths)
+    B, T, Hq, Hkv, D = dims
+    bf = (torch.bfloat16,)
+    _req(dout, "dout", bf, q.shape)
+    if dfinal_state is not None:
+        _req(dfinal_state, "dfinal_state", (torch.float32,), (B, Hkv, D, D))
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty(k.shape, k.dtype, k.device, stream) if dk is None else dk
+    dv = _empty(v.shape, v.dtype, v.device, stream) if dv is None else dv
+    outs = (_rows(dq, "dq", bf, q.shape), _rows(dk, "dk", bf, k.shape), _rows(dv, "dv", bf, k.shape))
+    if dinitial_state is None and want_dinitial_state:
+        dinitial_state = _empty((B, Hkv, D, D), torch.float32, q.device, stream)
+    if dinitial_state is not None:
+        _req(dinitial_state, "dinitial_state", (torch.float32,), (B, Hkv, D, D))
+    if workspace is None:
+        workspace = _empty((lin_attn_bwd_workspace_bytes(B, T, Hkv, D),), torch.uint8, q.device, stream)
+    _req(workspace, "workspace", (torch.uint8,))
+    _call("lin_attn_bwd", library().lin_attn_bwd,
+          (q, k, v, dout, log_decay, initial_state, dfinal_state, lengths, dq, dk, dv, dinitial_state, workspace), stream,
+          _addr(q), _addr(k), _addr(v), _addr(dout), _addr(log_decay), _addr(initial_state), _addr(dfinal_state),
+          _addr(lengths), _addr(dq), _addr(dk), _addr(dv), _addr(dinitial_state), *dims, *strides, *outs, float(scale),
+          _addr(workspace), workspace.numel())
+    return dq, dk, dv, dinitial_state
+
+
+def lin_attn_decode(q, k, v, state, log_decay, scale=None, slots=None, o=None, stream=None):
+    """One token per sequence of lin_attn_fwd's recurrence: q [B][Hq][D], k, v
+    [B][Hkv][D] fp32 or bf16; state [n][Hkv][D][D] fp32 is updated in place.
+    slots [B] int32 or None: row b works on state slots[b] (None: b); a row
+    whose slot is outside 0 .. n - 1 is empty (o 0, no state touched).
+    Returns o [B][Hq][D] of q's dtype."""
+    dts = (torch.float32, torch.bfloat16)
+    _req(q, "q", dts)
+    _req(k, "k", (q.dtype,))
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [B][Hq][D], k [B][Hkv][D]")
+    B, Hq, D = q.shape
+    Hkv = k.shape[1]
+    _req(k, "k", (q.dtype,), (B, Hkv, D))
+    _req(v, "v", (q.dtype,), k.shape)
+    _req(state, "state", (torch.float32,))
+    n = state.shape[0] if state.dim() else 0
+    _req(state, "state", (torch.float32,), (n, Hkv, D, D))
+    _req(log_decay, "log_decay", (torch.float32,), (Hkv,))
+    if slots is not None:
+        _req(slots, "slots", (torch.int32,), (B,))
+    scale = 1.0 / math.sqrt(D) if scale is None else scale
+    o = _empty(q.shape, q.dtype, q.device, stream) if o is None else o
+    _req(o, "o", (q.dtype,), q.shape)
+    _call("lin_attn_decode", library().lin_attn_decode, (q, k, v, state, log_decay, slots, o), stream, _addr(q),
+          _addr(k), _addr(v), _DT[q.dtype], _addr(state), _addr(log_decay), _addr(slots), _addr(o), B, Hq, Hkv, D, n,
+          float(scale))
+    return o

@@ -21,6 +21,7 @@ STATUS_NAMES = {OK: "ABW_OK", EINVAL: "ABW_EINVAL", ENOTSUP: "ABW_ENOTSUP", ECUD
 
 # Every function the header declares, with (restype, argtypes).
 _vp, _i, _f, _sz, _ull = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_ulonglong
+_ll = ctypes.c_longlong
 SIGNATURES = {
     "abw_last_error": (ctypes.c_char_p, []),
     "abw_version": (_i, []),
@@ -43,6 +44,18 @@ SIGNATURES = {
                                      _vp, _sz, _vp]),
     "attn_bwd_causal_noalloc": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _f, _i,
                                      _vp]),
+    "qk_norm_rope_fwd": (_i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _ll, _ll, _f, _f, _i, _i, _vp, _i,
+                              _vp, _i, _vp]),
+    "qk_norm_rope_bwd_workspace_bytes": (_sz, [_i]),
+    "qk_norm_rope_bwd": (_i, [_vp, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _ll, _ll,
+                              _ll, _ll, _f, _f, _i, _i, _vp, _i, _vp, _i, _vp, _sz, _vp]),
+    "lin_attn_fwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "lin_attn_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _ll, _ll, _ll, _ll, _f, _vp, _sz,
+                          _vp]),
+    "lin_attn_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "lin_attn_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _ll, _ll, _ll,
+                          _ll, _ll, _ll, _f, _vp, _sz, _vp]),
+    "lin_attn_decode": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp]),
 }
 
 

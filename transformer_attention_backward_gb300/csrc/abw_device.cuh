@@ -25,7 +25,7 @@ struct WaitCtl {
 
 // Where a wait ran out, for the report: kernel (bits 28-31), barrier slot
 // (bits 20-27), warp (bits 16-19) and the low 16 bits of the block index.
-enum : unsigned int { kSiteKv = 1u, kSiteDq = 2u, kSiteFwd = 3u, kSiteDecode = 4u };
+enum : unsigned int { kSiteKv = 1u, kSiteDq = 2u, kSiteFwd = 3u, kSiteDecode = 4u, kSiteLinState = 5u, kSiteLinOut = 6u };
 __device__ __forceinline__ unsigned int wait_site(unsigned int kernel, unsigned int slot) {
   return (kernel << 28) | ((slot & 0xffu) << 20) | (((threadIdx.x >> 5) & 0xfu) << 16) | (blockIdx.x & 0xffffu);
 }

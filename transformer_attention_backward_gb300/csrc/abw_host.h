@@ -71,6 +71,45 @@ cudaError_t launch_attn_bwd_causal(const void *q, const void *k, const void *v, 
                                    int pos0, void *ws, size_t ws_bytes, const WaitCtl &w,
                                    cudaStream_t st, const char **why);
 
+// Per-head norm of queries (index 0) and keys (1) with the rotation.  H 0:
+// absent.  Strides are elements from token to token.
+struct QkNormRopeArgs {
+  const void *x[2], *dy[2];
+  void *out[2];
+  const float *gamma[2];
+  float *dgamma[2];
+  int backward, bf16, dy_bf16;
+  int B, T, H[2], D;
+  long long x_stride[2], out_stride[2];
+  float eps;
+  double base;
+  int rotary_dim, interleaved;        // rotary_dim 0: no rotation
+  const int *positions;               // device, [n_axes][B][T], or null
+  int n_axes, sections[4], pos0;
+  void *ws;
+};
+constexpr int kQkParts = 1216;        // most partial dgamma rows a backward call writes
+size_t qk_norm_rope_bwd_workspace_bytes(int D);
+cudaError_t launch_qk_norm_rope(const QkNormRopeArgs &a, cudaStream_t st);
+
+// Linear attention with a decay per KV head; dout null: forward.
+struct LinAttnArgs {
+  const void *q, *k, *v, *dout;
+  const float *log_decay, *initial_state, *dfinal_state;
+  const int *lengths;
+  void *o, *dq, *dk, *dv;
+  float *final_state, *dinitial_state;
+  int B, T, Hq, Hkv, D;
+  long long q_stride, k_stride, v_stride, o_stride, dq_stride, dk_stride, dv_stride;
+  float scale;
+  void *ws;
+};
+size_t lin_attn_workspace_bytes(int B, int T, int Hkv, int D, int backward);
+cudaError_t launch_lin_attn(const LinAttnArgs &a, const WaitCtl &w, cudaStream_t st, const char **why);
+cudaError_t launch_lin_attn_decode(const void *q, const void *k, const void *v, float *state, const float *log_decay,
+                                   const int *slots, void *o, int bf16, int B, int Hq, int Hkv, int D, int nstates,
+                                   float scale, cudaStream_t st);
+
 cudaError_t launch_selftest_wait(const WaitCtl &w, cudaStream_t st);
 
 // Size of the fixed device scratch behind attn_bwd_causal_noalloc.

@@ -76,6 +76,110 @@ abw_status check_buffers(const char *op, const Range *in, int nin, const Range *
   return ABW_OK;
 }
 
+// A buffer with a token stride: `n` rows of `row` bytes, `stride` bytes apart.
+struct Rows {
+  const char *name;
+  const void *p;
+  size_t n, row, stride, align;
+  size_t bytes() const { return n == 0 || row == 0 ? 0 : (n - 1) * stride + row; }
+};
+
+// Rows of one packed buffer interleave: with a common stride two of them
+// overlap only if their rows do.
+bool overlaps(const Rows &a, const Rows &b) {
+  if (!overlaps(Range{a.name, a.p, a.bytes()}, Range{b.name, b.p, b.bytes()})) return false;
+  if (a.stride != b.stride || a.row > a.stride || b.row > b.stride) return true;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  const size_t d = x >= y ? (x - y) % a.stride : (a.stride - (y - x) % a.stride) % a.stride;   // a behind b's row start
+  return d < b.row || a.stride - d < a.row;
+}
+
+abw_status check_rows(const char *op, const Rows *in, int nin, const Rows *out, int nout) {
+  for (int i = 0; i < nin + nout; ++i) {
+    const Rows &r = i < nin ? in[i] : out[i - nin];
+    if (r.bytes() == 0) continue;
+    if (r.p == nullptr) return fail(ABW_EINVAL, "%s: %s is NULL", op, r.name);
+    if (reinterpret_cast<uintptr_t>(r.p) % r.align != 0)
+      return fail(ABW_EINVAL, "%s: %s is not %zu-byte aligned", op, r.name, r.align);
+    if (r.n > 1 && r.stride < r.row) return fail(ABW_EINVAL, "%s: %s has a token stride below its row", op, r.name);
+    if (r.n > 1 && r.stride % r.align != 0)
+      return fail(ABW_ENOTSUP, "%s: %s has a token stride of %zu bytes, not a multiple of %zu", op, r.name, r.stride,
+                  r.align);
+  }
+  for (int i = 0; i < nout; ++i) {
+    for (int j = 0; j < nin; ++j)
+      if (overlaps(out[i], in[j]))
+        return fail(ABW_EINVAL, "%s: output %s overlaps input %s", op, out[i].name, in[j].name);
+    for (int j = i + 1; j < nout; ++j)
+      if (overlaps(out[i], out[j]))
+        return fail(ABW_EINVAL, "%s: outputs %s and %s overlap", op, out[i].name, out[j].name);
+  }
+  return ABW_OK;
+}
+
+Rows dense(const char *name, const void *p, size_t bytes, size_t align = 16) {
+  return Rows{name, p, bytes ? 1u : 0u, bytes, bytes, align};
+}
+
+// Argument checks that the linear attention's entry points share.
+abw_status check_lin(const char *op, int B, int T, int Hq, int Hkv, int D, float scale) {
+  if (B < 0 || T < 0 || Hq < 0 || Hkv < 0) return fail(ABW_EINVAL, "%s: negative size", op);
+  if (Hkv == 0 || Hq % Hkv != 0) return fail(ABW_EINVAL, "%s: Hq=%d not a multiple of Hkv=%d", op, Hq, Hkv);
+  if (D != 64 && D != 128) return fail(ABW_ENOTSUP, "%s: D=%d unsupported (D == 64 or 128)", op, D);
+  if (!(scale == scale)) return fail(ABW_EINVAL, "%s: scale is NaN", op);
+  return ABW_OK;
+}
+
+Rows lin_rows(const char *name, const void *p, int B, int T, int H, int D, long long stride) {
+  const size_t row = static_cast<size_t>(H) * D * 2;
+  return Rows{name, p, static_cast<size_t>(B) * T, row, stride == 0 ? row : static_cast<size_t>(stride) * 2, 16};
+}
+
+// Elements from token to token; a single token has no next one.
+long long token_stride(long long stride, int B, int T, long long row) {
+  return stride == 0 || static_cast<long long>(B) * T <= 1 ? row : stride;
+}
+
+// The rotation's arguments as both directions of qk_norm_rope take them.
+abw_status check_rotation(const char *op, abw::QkNormRopeArgs &a, float rope_base, int rotary_dim, int interleaved,
+                          const int *positions, int n_axes, const int *sections, int pos0) {
+  a.base = 1.0;
+  a.rotary_dim = 0;
+  a.interleaved = interleaved ? 1 : 0;
+  a.positions = nullptr;
+  a.n_axes = 1;
+  a.pos0 = pos0;
+  if (!(rope_base >= 0.0f)) return fail(ABW_EINVAL, "%s: rope_base must be >= 0 (0: no rotation)", op);
+  if (rope_base == 0.0f) return ABW_OK;
+  if (rope_base > 3.0e38f) return fail(ABW_EINVAL, "%s: rope_base is not finite", op);
+  if (rotary_dim < 2 || (rotary_dim & 1) || rotary_dim > a.D)
+    return fail(ABW_EINVAL, "%s: rotary_dim=%d must be even, 2 .. D=%d", op, rotary_dim, a.D);
+  if (n_axes < 1 || n_axes > 4) return fail(ABW_EINVAL, "%s: n_axes=%d (1 .. 4)", op, n_axes);
+  if (sections == nullptr && n_axes > 1) return fail(ABW_EINVAL, "%s: sections is NULL with n_axes=%d", op, n_axes);
+  long long sum = 0;
+  for (int i = 0; i < n_axes; ++i) {
+    a.sections[i] = sections ? sections[i] : rotary_dim / 2;
+    if (a.sections[i] < 0) return fail(ABW_EINVAL, "%s: sections[%d]=%d is negative", op, i, a.sections[i]);
+    sum += a.sections[i];
+  }
+  if (sum != rotary_dim / 2)
+    return fail(ABW_EINVAL, "%s: sections add up to %lld, not to rotary_dim / 2 = %d", op, sum, rotary_dim / 2);
+  a.base = static_cast<double>(rope_base);
+  a.rotary_dim = rotary_dim;
+  a.positions = positions;
+  a.n_axes = n_axes;
+  return ABW_OK;
+}
+
+abw_status check_qk(const char *op, int B, int T, int Hq, int Hkv, int D, abw_dtype dtype, float eps) {
+  if (B < 0 || T < 0 || Hq < 0 || Hkv < 0) return fail(ABW_EINVAL, "%s: negative size", op);
+  if (D < 2 || (D & 1)) return fail(ABW_EINVAL, "%s: D=%d must be even and >= 2", op, D);
+  if (D > 512) return fail(ABW_ENOTSUP, "%s: D=%d > 512", op, D);
+  if (dtype != ABW_F32 && dtype != ABW_BF16) return fail(ABW_EINVAL, "%s: bad dtype", op);
+  if (!(eps >= 0.0f)) return fail(ABW_EINVAL, "%s: eps must be >= 0", op);
+  return ABW_OK;
+}
+
 size_t dt_size(abw_dtype d) { return d == ABW_BF16 ? 2 : 4; }
 
 }  // namespace
@@ -212,12 +316,13 @@ abw_status abw_device_check(abw_stream stream) {
   if (e != cudaSuccess) return from_cuda(e, "abw_device_check");
   const unsigned int word = words[0], site = words[1];
   if (word & (abw::kErrWaitTimeout | abw::kErrSelfTest)) {
-    static const char *const kernels[] = {"?", "causal kv", "causal dq", "causal forward", "decode"};
+    static const char *const kernels[] = {"?", "causal kv", "causal dq", "causal forward", "decode",
+                                          "linear attention state", "linear attention output"};
     const unsigned int k = site >> 28;
     return fail(ABW_ETIMEOUT,
                 "a device-side bounded wait ran out (error word 0x%x; first in the %s kernel, barrier slot %u, "
                 "warp %u, block %u)",
-                word, kernels[k < 5 ? k : 0], (site >> 20) & 0xffu, (site >> 16) & 0xfu, site & 0xffffu);
+                word, kernels[k < 7 ? k : 0], (site >> 20) & 0xffu, (site >> 16) & 0xfu, site & 0xffffu);
   }
   if (word & abw::kErrSmemAlign)
     return fail(ABW_ECUDA, "a kernel's dynamic shared memory was not 1024-byte aligned; it did no work");
@@ -500,6 +605,230 @@ abw_status attn_bwd_causal_noalloc(const void *q, const void *k, const void *v, 
                                                scratch, abw::kNoAllocScratchBytes, w,
                                                reinterpret_cast<cudaStream_t>(stream), &why),
                    "attn_bwd_causal_noalloc", why);
+}
+
+abw_status qk_norm_rope_fwd(const void *q, const void *k, abw_dtype dtype, const float *gamma_q, const float *gamma_k,
+                            void *q_out, void *k_out, int B, int T, int Hq, int Hkv, int D, long long q_stride,
+                            long long k_stride, float eps, float rope_base, int rotary_dim, int interleaved,
+                            const int *positions, int n_axes, const int *sections, int pos0, abw_stream stream) {
+  abw_status st = check_qk("qk_norm_rope_fwd", B, T, Hq, Hkv, D, dtype, eps);
+  if (st != ABW_OK) return st;
+  if (q_stride < 0 || k_stride < 0) return fail(ABW_EINVAL, "qk_norm_rope_fwd: negative token stride");
+  abw::QkNormRopeArgs a = {};
+  a.D = D;
+  st = check_rotation("qk_norm_rope_fwd", a, rope_base, rotary_dim, interleaved, positions, n_axes, sections, pos0);
+  if (st != ABW_OK) return st;
+  if (B == 0 || T == 0 || Hq + Hkv == 0) return ABW_OK;
+  const size_t es = dt_size(dtype), ntok = static_cast<size_t>(B) * T;
+  const size_t qr = static_cast<size_t>(Hq) * D * es, kr = static_cast<size_t>(Hkv) * D * es;
+  const size_t gb = static_cast<size_t>(D) * 4;
+  Rows in[] = {{"q", q, ntok, qr, q_stride ? q_stride * es : qr, es},
+               {"k", k, ntok, kr, k_stride ? k_stride * es : kr, es},
+               dense("gamma_q", gamma_q, gamma_q && Hq ? gb : 0),
+               dense("gamma_k", gamma_k, gamma_k && Hkv ? gb : 0),
+               dense("positions", a.positions, a.positions ? ntok * 4 * a.n_axes : 0, 4)};
+  Rows out[] = {dense("q_out", q_out, ntok * qr), dense("k_out", k_out, ntok * kr)};
+  st = check_rows("qk_norm_rope_fwd", in, 5, out, 2);
+  if (st != ABW_OK) return st;
+  a.x[0] = q, a.x[1] = k;
+  a.out[0] = q_out, a.out[1] = k_out;
+  a.gamma[0] = gamma_q, a.gamma[1] = gamma_k;
+  a.bf16 = dtype == ABW_BF16;
+  a.B = B, a.T = T, a.H[0] = Hq, a.H[1] = Hkv;
+  a.x_stride[0] = token_stride(q_stride, B, T, static_cast<long long>(Hq) * D);
+  a.x_stride[1] = token_stride(k_stride, B, T, static_cast<long long>(Hkv) * D);
+  a.out_stride[0] = static_cast<long long>(Hq) * D;
+  a.out_stride[1] = static_cast<long long>(Hkv) * D;
+  a.eps = eps;
+  return from_cuda(abw::launch_qk_norm_rope(a, reinterpret_cast<cudaStream_t>(stream)), "qk_norm_rope_fwd");
+}
+
+size_t qk_norm_rope_bwd_workspace_bytes(int D) { return D < 1 || D > 512 ? 0 : abw::qk_norm_rope_bwd_workspace_bytes(D); }
+
+abw_status qk_norm_rope_bwd(const void *q, const void *k, abw_dtype dtype, const void *dq_out, const void *dk_out,
+                            abw_dtype dy_dtype, const float *gamma_q, const float *gamma_k, void *dq, void *dk,
+                            float *dgamma_q, float *dgamma_k, int B, int T, int Hq, int Hkv, int D, long long q_stride,
+                            long long k_stride, long long dq_stride, long long dk_stride, float eps, float rope_base,
+                            int rotary_dim, int interleaved, const int *positions, int n_axes, const int *sections,
+                            int pos0, void *workspace, size_t workspace_bytes, abw_stream stream) {
+  abw_status st = check_qk("qk_norm_rope_bwd", B, T, Hq, Hkv, D, dtype, eps);
+  if (st != ABW_OK) return st;
+  if (dy_dtype != ABW_F32 && dy_dtype != ABW_BF16) return fail(ABW_EINVAL, "qk_norm_rope_bwd: bad dy dtype");
+  if (q_stride < 0 || k_stride < 0 || dq_stride < 0 || dk_stride < 0)
+    return fail(ABW_EINVAL, "qk_norm_rope_bwd: negative token stride");
+  abw::QkNormRopeArgs a = {};
+  a.D = D;
+  st = check_rotation("qk_norm_rope_bwd", a, rope_base, rotary_dim, interleaved, positions, n_axes, sections, pos0);
+  if (st != ABW_OK) return st;
+  const bool norm = gamma_q || gamma_k;
+  const size_t need = norm ? abw::qk_norm_rope_bwd_workspace_bytes(D) : 0;
+  if (need && (workspace == nullptr || workspace_bytes < need))
+    return fail(ABW_EWORKSPACE, "qk_norm_rope_bwd: workspace %zu bytes at %p, need %zu", workspace_bytes, workspace,
+                need);
+  const size_t es = dt_size(dtype), ds = dt_size(dy_dtype), ntok = static_cast<size_t>(B) * T;
+  const size_t qn = static_cast<size_t>(Hq) * D, kn = static_cast<size_t>(Hkv) * D, gb = static_cast<size_t>(D) * 4;
+  Rows in[] = {{"q", q, ntok, qn * es, q_stride ? q_stride * es : qn * es, es},
+               {"k", k, ntok, kn * es, k_stride ? k_stride * es : kn * es, es},
+               dense("dq_out", dq_out, ntok * qn * ds),
+               dense("dk_out", dk_out, ntok * kn * ds),
+               dense("gamma_q", gamma_q, gamma_q && Hq ? gb : 0),
+               dense("gamma_k", gamma_k, gamma_k && Hkv ? gb : 0),
+               dense("positions", a.positions, a.positions ? ntok * 4 * a.n_axes : 0, 4)};
+  Rows out[] = {{"dq", dq, ntok, qn * es, dq_stride ? dq_stride * es : qn * es, es},
+                {"dk", dk, ntok, kn * es, dk_stride ? dk_stride * es : kn * es, es},
+                dense("dgamma_q", dgamma_q, dgamma_q ? gb : 0),
+                dense("dgamma_k", dgamma_k, dgamma_k ? gb : 0),
+                dense("workspace", workspace, need)};
+  st = check_rows("qk_norm_rope_bwd", in, 7, out, 5);
+  if (st != ABW_OK) return st;
+  if (Hq + Hkv == 0 && !dgamma_q && !dgamma_k) return ABW_OK;
+  a.x[0] = q, a.x[1] = k;
+  a.dy[0] = dq_out, a.dy[1] = dk_out;
+  a.out[0] = dq, a.out[1] = dk;
+  a.gamma[0] = gamma_q, a.gamma[1] = gamma_k;
+  a.dgamma[0] = gamma_q ? dgamma_q : nullptr;
+  a.dgamma[1] = gamma_k ? dgamma_k : nullptr;
+  a.backward = 1;
+  a.bf16 = dtype == ABW_BF16;
+  a.dy_bf16 = dy_dtype == ABW_BF16;
+  a.B = B, a.T = T, a.H[0] = Hq, a.H[1] = Hkv;
+  a.x_stride[0] = token_stride(q_stride, B, T, static_cast<long long>(qn));
+  a.x_stride[1] = token_stride(k_stride, B, T, static_cast<long long>(kn));
+  a.out_stride[0] = token_stride(dq_stride, B, T, static_cast<long long>(qn));
+  a.out_stride[1] = token_stride(dk_stride, B, T, static_cast<long long>(kn));
+  a.eps = eps;
+  a.ws = workspace;
+  return from_cuda(abw::launch_qk_norm_rope(a, reinterpret_cast<cudaStream_t>(stream)), "qk_norm_rope_bwd");
+}
+
+size_t lin_attn_fwd_workspace_bytes(int B, int T, int Hkv, int D) {
+  return B < 0 || T < 0 || Hkv < 0 || D < 0 ? 0 : abw::lin_attn_workspace_bytes(B, T, Hkv, D, 0);
+}
+
+size_t lin_attn_bwd_workspace_bytes(int B, int T, int Hkv, int D) {
+  return B < 0 || T < 0 || Hkv < 0 || D < 0 ? 0 : abw::lin_attn_workspace_bytes(B, T, Hkv, D, 1);
+}
+
+abw_status lin_attn_fwd(const void *q, const void *k, const void *v, const float *log_decay,
+                        const float *initial_state, const int *lengths, void *o, float *final_state, int B, int T,
+                        int Hq, int Hkv, int D, long long q_stride, long long k_stride, long long v_stride,
+                        long long o_stride, float scale, void *workspace, size_t workspace_bytes, abw_stream stream) {
+  abw_status st = check_lin("lin_attn_fwd", B, T, Hq, Hkv, D, scale);
+  if (st != ABW_OK) return st;
+  if (q_stride < 0 || k_stride < 0 || v_stride < 0 || o_stride < 0)
+    return fail(ABW_EINVAL, "lin_attn_fwd: negative token stride");
+  if (B == 0 || Hq == 0) return ABW_OK;
+  const size_t need = abw::lin_attn_workspace_bytes(B, T, Hkv, D, 0);
+  if (need && (workspace == nullptr || workspace_bytes < need))
+    return fail(ABW_EWORKSPACE, "lin_attn_fwd: workspace %zu bytes at %p, need %zu", workspace_bytes, workspace, need);
+  const size_t sbytes = static_cast<size_t>(B) * Hkv * D * D * 4;
+  Rows in[] = {lin_rows("q", q, B, T, Hq, D, q_stride),
+               lin_rows("k", k, B, T, Hkv, D, k_stride),
+               lin_rows("v", v, B, T, Hkv, D, v_stride),
+               dense("log_decay", log_decay, static_cast<size_t>(Hkv) * 4, 4),
+               dense("lengths", lengths, lengths ? static_cast<size_t>(B) * 4 : 0, 4),
+               dense("initial_state", initial_state, initial_state && initial_state != final_state ? sbytes : 0)};
+  Rows out[] = {lin_rows("o", o, B, T, Hq, D, o_stride),
+                dense("final_state", final_state, final_state ? sbytes : 0),
+                dense("workspace", workspace, need)};
+  st = check_rows("lin_attn_fwd", in, 6, out, 3);
+  if (st != ABW_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) {                                 // no tokens: the state passes through
+    if (!final_state || final_state == initial_state) return ABW_OK;
+    return from_cuda(initial_state ? cudaMemcpyAsync(final_state, initial_state, sbytes, cudaMemcpyDeviceToDevice, cs)
+                                   : cudaMemsetAsync(final_state, 0, sbytes, cs),
+                     "lin_attn_fwd");
+  }
+  abw::WaitCtl w = abw::wait_ctl();
+  if (!w.err) return fail(ABW_ECUDA, "lin_attn_fwd: no CUDA device");
+  abw::LinAttnArgs a = {};
+  a.q = q, a.k = k, a.v = v;
+  a.log_decay = log_decay, a.initial_state = initial_state, a.lengths = lengths;
+  a.o = o, a.final_state = final_state;
+  a.B = B, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.D = D;
+  const long long qn = static_cast<long long>(Hq) * D, kn = static_cast<long long>(Hkv) * D;
+  a.q_stride = token_stride(q_stride, B, T, qn), a.k_stride = token_stride(k_stride, B, T, kn);
+  a.v_stride = token_stride(v_stride, B, T, kn), a.o_stride = token_stride(o_stride, B, T, qn);
+  a.scale = scale;
+  a.ws = workspace;
+  const char *why = nullptr;
+  return from_cuda(abw::launch_lin_attn(a, w, cs, &why), "lin_attn_fwd", why);
+}
+
+abw_status lin_attn_bwd(const void *q, const void *k, const void *v, const void *dout, const float *log_decay,
+                        const float *initial_state, const float *dfinal_state, const int *lengths, void *dq, void *dk,
+                        void *dv, float *dinitial_state, int B, int T, int Hq, int Hkv, int D, long long q_stride,
+                        long long k_stride, long long v_stride, long long dq_stride, long long dk_stride,
+                        long long dv_stride, float scale, void *workspace, size_t workspace_bytes, abw_stream stream) {
+  abw_status st = check_lin("lin_attn_bwd", B, T, Hq, Hkv, D, scale);
+  if (st != ABW_OK) return st;
+  if (q_stride < 0 || k_stride < 0 || v_stride < 0 || dq_stride < 0 || dk_stride < 0 || dv_stride < 0)
+    return fail(ABW_EINVAL, "lin_attn_bwd: negative token stride");
+  if (B == 0 || Hq == 0) return ABW_OK;
+  const size_t need = abw::lin_attn_workspace_bytes(B, T, Hkv, D, 1);
+  if (need && (workspace == nullptr || workspace_bytes < need))
+    return fail(ABW_EWORKSPACE, "lin_attn_bwd: workspace %zu bytes at %p, need %zu", workspace_bytes, workspace, need);
+  const size_t sbytes = static_cast<size_t>(B) * Hkv * D * D * 4;
+  Rows in[] = {lin_rows("q", q, B, T, Hq, D, q_stride),
+               lin_rows("k", k, B, T, Hkv, D, k_stride),
+               lin_rows("v", v, B, T, Hkv, D, v_stride),
+               lin_rows("dout", dout, B, T, Hq, D, 0),
+               dense("log_decay", log_decay, static_cast<size_t>(Hkv) * 4, 4),
+               dense("lengths", lengths, lengths ? static_cast<size_t>(B) * 4 : 0, 4),
+               dense("initial_state", initial_state, initial_state ? sbytes : 0),
+               dense("dfinal_state", dfinal_state, dfinal_state && dfinal_state != dinitial_state ? sbytes : 0)};
+  Rows out[] = {lin_rows("dq", dq, B, T, Hq, D, dq_stride),
+                lin_rows("dk", dk, B, T, Hkv, D, dk_stride),
+                lin_rows("dv", dv, B, T, Hkv, D, dv_stride),
+                dense("dinitial_state", dinitial_state, dinitial_state ? sbytes : 0),
+                dense("workspace", workspace, need)};
+  st = check_rows("lin_attn_bwd", in, 8, out, 5);
+  if (st != ABW_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    if (!dinitial_state || dinitial_state == dfinal_state) return ABW_OK;
+    return from_cuda(dfinal_state ? cudaMemcpyAsync(dinitial_state, dfinal_state, sbytes, cudaMemcpyDeviceToDevice, cs)
+                                  : cudaMemsetAsync(dinitial_state, 0, sbytes, cs),
+                     "lin_attn_bwd");
+  }
+  abw::WaitCtl w = abw::wait_ctl();
+  if (!w.err) return fail(ABW_ECUDA, "lin_attn_bwd: no CUDA device");
+  abw::LinAttnArgs a = {};
+  a.q = q, a.k = k, a.v = v, a.dout = dout;
+  a.log_decay = log_decay, a.initial_state = initial_state, a.dfinal_state = dfinal_state, a.lengths = lengths;
+  a.dq = dq, a.dk = dk, a.dv = dv, a.dinitial_state = dinitial_state;
+  a.B = B, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.D = D;
+  const long long qn = static_cast<long long>(Hq) * D, kn = static_cast<long long>(Hkv) * D;
+  a.q_stride = token_stride(q_stride, B, T, qn), a.k_stride = token_stride(k_stride, B, T, kn);
+  a.v_stride = token_stride(v_stride, B, T, kn), a.dq_stride = token_stride(dq_stride, B, T, qn);
+  a.dk_stride = token_stride(dk_stride, B, T, kn), a.dv_stride = token_stride(dv_stride, B, T, kn);
+  a.scale = scale;
+  a.ws = workspace;
+  const char *why = nullptr;
+  return from_cuda(abw::launch_lin_attn(a, w, cs, &why), "lin_attn_bwd", why);
+}
+
+abw_status lin_attn_decode(const void *q, const void *k, const void *v, abw_dtype dtype, float *state,
+                           const float *log_decay, const int *slots, void *o, int B, int Hq, int Hkv, int D,
+                           int n_states, float scale, abw_stream stream) {
+  abw_status st = check_lin("lin_attn_decode", B, 1, Hq, Hkv, D, scale);
+  if (st != ABW_OK) return st;
+  if (Hq / Hkv > 8) return fail(ABW_ENOTSUP, "lin_attn_decode: Hq/Hkv=%d > 8", Hq / Hkv);
+  if (dtype != ABW_F32 && dtype != ABW_BF16) return fail(ABW_EINVAL, "lin_attn_decode: bad dtype");
+  if (n_states < 0 || (!slots && n_states < B))
+    return fail(ABW_EINVAL, "lin_attn_decode: n_states=%d with B=%d and %s", n_states, B, slots ? "slots" : "no slots");
+  if (B == 0 || Hq == 0) return ABW_OK;
+  const size_t es = dt_size(dtype), qb = static_cast<size_t>(B) * Hq * D * es, kb = static_cast<size_t>(B) * Hkv * D * es;
+  Rows in[] = {dense("q", q, qb), dense("k", k, kb), dense("v", v, kb),
+               dense("log_decay", log_decay, static_cast<size_t>(Hkv) * 4, 4),
+               dense("slots", slots, slots ? static_cast<size_t>(B) * 4 : 0, 4)};
+  Rows out[] = {dense("o", o, qb), dense("state", state, static_cast<size_t>(n_states) * Hkv * D * D * 4)};
+  st = check_rows("lin_attn_decode", in, 5, out, 2);
+  if (st != ABW_OK) return st;
+  return from_cuda(abw::launch_lin_attn_decode(q, k, v, state, log_decay, slots, o, dtype == ABW_BF16, B, Hq, Hkv, D,
+                                               n_states, scale, reinterpret_cast<cudaStream_t>(stream)),
+                   "lin_attn_decode");
 }
 
 }  // extern "C"

@@ -1,0 +1,918 @@
+// Linear attention with a decay for each KV head: chunked forward and
+// backward over whole sequences, and the recurrent form for single tokens.
+//
+//   S_t = a S_(t-1) + k_t v_t^T,   o_t = scale S_t^T q_t,   a = exp(log_decay)
+//
+// Over a chunk of 128 tokens that starts with the state S (local t, j; L
+// valid tokens):
+//   o_t = sum_(j<=t) scale a^(t-j) (q_t . k_j) v_j  +  scale a^(t+1) S^T q_t
+//   S' = a^L S + sum_j a^(L-1-j) k_j v_j^T
+// and for the gradients, with R the gradient of the state behind the chunk:
+//   dq_t = sum_(j<=t) scale a^(t-j) (do_t . v_j) k_j  +  scale a^(t+1) S do_t
+//   dk_j = sum_(t>=j) scale a^(t-j) (v_j . do_t) q_t  +  a^(L-1-j) R v_j
+//   dv_j = sum_(t>=j) scale a^(t-j) (k_j . q_t) do_t  +  a^(L-1-j) R^T k_j
+//   R' = a^L R + sum_t scale a^(t+1) q_t do_t^T        (towards earlier chunks)
+// So o, dq, dk and dv are one operation, out = mask(A B^T) C + row factor
+// (A S), on other operands, and S and R are one recurrence on other operands
+// and in the other direction.  Two launches:
+//   lin_state : walks the chunks of one (batch, KV head) and leaves the state
+//               that enters each of them as a bf16 tile in the workspace
+//   lin_out   : one item per 128 output rows; everything it needs is there,
+//               so items run in any order
+// No element of a decay power above a^0 is formed, so strong decays underflow
+// to 0 and never overflow.
+#include <math.h>
+
+#include "abw_host.h"
+#include "tcgen05.cuh"
+
+namespace abw {
+namespace {
+
+constexpr int kC = 128;               // tokens per chunk
+
+__device__ __forceinline__ uint32_t lpack2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&v);
+}
+
+// log2 of the decay, held above -1e30 so that 0 * log2 a is 0 for a = 0.
+__device__ __forceinline__ float log2_decay(float log_decay) {
+  const float l2 = log_decay * 1.4426950408889634f;
+  return l2 < -1e30f ? -1e30f : l2;
+}
+
+__device__ __forceinline__ int seq_len(const int *lengths, int b, int T) {
+  return lengths ? min(max(lengths[b], 0), T) : T;
+}
+
+struct LinSizes {
+  int B, T, Hq, Hkv, G, NC;
+  float scale;
+  const float *log_decay;             // [Hkv]
+  const int *lengths;                 // [B] or null
+};
+
+// ---------------------------------------------------------------------------
+// lin_state: the recurrence over the chunks of one (batch, KV head, 64-column
+// half of the state).  Role F: X = K, Y = V, weights a^(L-1-j), chunks in
+// order.  Role R: X = Q, Y = dO of every query head of the group, weights
+// scale a^(t+1), chunks from the last to the first.
+//   U = X^T (w o Y)    M = D state rows, N = 64 columns, K = 128 tokens
+// The fp32 product w o Y enters the tensor core as a sum of NS bf16 terms
+// (each the rounding of what the ones before leave): two terms are good to
+// 2^-17, which is far below the rounding of the bf16 state tiles; three are
+// good to 2^-25, for a state that leaves in fp32.  The state itself stays in
+// fp32 registers.  Warps: 0 TMA, 1 MMA, 2-9 weights, 10-13 state.
+// ---------------------------------------------------------------------------
+constexpr int kSThr = 448;
+constexpr int kSStage = 32768 + 16384 + 3 * 16384;   // X | Y | up to three terms of w o Y
+constexpr int kSOffBar = 2 * kSStage;
+enum { kSBarFull = 0, kSBarEmpty = 2, kSBarY = 4, kSBarU = 6, kSBarUEmpty = 8, kSBarFinal = 10, kSNumBars = 11 };
+constexpr int kSOffTmem = kSOffBar + kSNumBars * 8;
+constexpr int kSOffAbort = kSOffTmem + 4;
+constexpr int kSSmem = kSOffBar + 128 + 1024;        // + alignment slack
+static_assert(kSOffAbort + 4 <= kSOffBar + 128 && kSSmem <= 232448, "state kernel shared memory");
+
+struct LinStateParams {
+  LinSizes z;
+  int first_role, nroles;             // 0 F, 1 R
+  __nv_bfloat16 *tiles[2];            // [B][Hkv][NC][D * D], 128B-swizzled
+  const float *start[2];              // initial_state, dfinal_state (or null)
+  float *end[2];                      // final_state, dinitial_state (or null)
+  WaitCtl wait;
+};
+
+template <int D, int NS>
+__global__ void __launch_bounds__(kSThr, 1)
+    lin_state_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+                     const __grid_constant__ LinStateParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int NH = D / 64;
+  const int hf = blockIdx.x % NH, unit = blockIdx.x / NH;
+  const int nbh = p.z.B * p.z.Hkv;
+  const int role = p.first_role + unit / nbh, bh = unit % nbh;
+  const int b = bh / p.z.Hkv, kv = bh % p.z.Hkv;
+  const int len = seq_len(p.z.lengths, b, p.z.T);
+  const int ncb = (len + kC - 1) / kC;                        // chunks that hold tokens
+  const int nst = p.end[role] ? ncb : max(ncb - 1, 0);        // chunks to add
+  const int gi = role ? p.z.G : 1;                            // (X, Y) pairs per chunk
+  const float l2 = log2_decay(p.z.log_decay[kv]);
+  auto chunk = [&](int m) -> int { return role ? ncb - 1 - m : m; };
+
+  auto bar = [&](int i) -> uint32_t { return sb + kSOffBar + i * 8; };
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kSOffAbort);
+  auto wt = [&](uint32_t br, uint32_t parity) -> bool {
+    if (*abort_flag) return false;
+    if (mbar_wait_bounded(br, parity, p.wait.limit_ns)) return true;
+    *abort_flag = 1;
+    report_timeout(p.wait.err, kSiteLinState, (br - sb - kSOffBar) / 8);
+    return false;
+  };
+  auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return __shfl_sync(0xffffffffu, wt(br, parity), 0); };
+
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(kSBarFull + s), 1);
+      mbar_init(bar(kSBarEmpty + s), 1);
+      mbar_init(bar(kSBarY + s), 256);
+      mbar_init(bar(kSBarU + s), 1);
+      mbar_init(bar(kSBarUEmpty + s), 128);
+    }
+    mbar_init(bar(kSBarFinal), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tc::tmem_alloc(sb + kSOffTmem, 128);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kSOffTmem);
+
+  if (warp == 0) {
+    // ============================ TMA producer ============================
+    if (lane == 0) {
+      const CUtensorMap *mx = role ? &tmQ : &tmK, *my = role ? &tmDO : &tmV;
+      prefetch_tensormap(mx);
+      prefetch_tensormap(my);
+      int issued = 0;
+      for (int i = 0; i < nst * gi; ++i) {
+        const int s = i & 1;
+        if (!wt(bar(kSBarEmpty + s), ((i >> 1) & 1) ^ 1)) break;
+        const int h = role ? kv * p.z.G + i % gi : kv;
+        const int t0 = chunk(i / gi) * kC;
+        const uint32_t st = sb + s * kSStage, fb = bar(kSBarFull + s);
+        mbar_arrive_expect_tx(fb, (NH + 1) * 16384);
+        for (int x = 0; x < NH; ++x) tma_load_4d(st + x * 16384, mx, x * 64, h, t0, b, fb);
+        tma_load_4d(st + 32768, my, hf * 64, h, t0, b, fb);
+        issued = i + 1;
+      }
+      if (*abort_flag)
+        for (int i = (issued > 2 ? issued - 2 : 0); i < issued; ++i)
+          mbar_wait_bounded(bar(kSBarFull + (i & 1)), (i >> 1) & 1, 2000000000ull);
+    }
+  } else if (warp == 1) {
+    // ============================ MMA issuer ==============================
+    // X is the M-major A operand.  For D = 64 rows 64-127 of A come from the
+    // unused second half of the X slot; they only reach TMEM lanes 64-127,
+    // which nobody reads.
+    constexpr uint32_t id_u = tc::idesc_bf16_f32(128, 64, 1, 1);
+    const uint64_t dX = tc::sdesc_sw128(sb, 16384, 1024);
+    const uint64_t dY = tc::sdesc_sw128(sb + 49152, 16384, 1024);
+    for (int i = 0; i < nst * gi; ++i) {
+      const int s = i & 1;
+      if (!wtw(bar(kSBarUEmpty + s), ((i >> 1) & 1) ^ 1) || !wtw(bar(kSBarFull + s), (i >> 1) & 1) ||
+          !wtw(bar(kSBarY + s), (i >> 1) & 1))
+        break;
+      tc::fence_after_sync();
+      const uint64_t so = static_cast<uint64_t>(s * kSStage) >> 4;
+      // the small terms first: the tensor core's additions cut off bits of
+      // the accumulator's size (measured: 5 times the error the other way)
+#pragma unroll
+      for (int e = NS - 1; e >= 0; --e)
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_bf16_w(tmem + s * 64, dX + so + ((kk * 2048) >> 4), dY + so + ((e * 16384 + kk * 2048) >> 4), id_u,
+                         e < NS - 1 || kk > 0);
+      tc::commit_w(bar(kSBarEmpty + s));
+      tc::commit_w(bar(kSBarU + s));
+    }
+    tc::commit_w(bar(kSBarFinal));
+    mbar_wait_bounded(bar(kSBarFinal), 0, 2000000000ull);   // every MMA has completed
+  } else if (warp < 10) {
+    // ============================ weights =================================
+    const int wt_tid = tid - 64;
+    for (int i = 0; i < nst * gi; ++i) {
+      const int s = i & 1;
+      if (!wtw(bar(kSBarFull + s), (i >> 1) & 1)) break;
+      const int L = min(kC, len - chunk(i / gi) * kC);
+      unsigned char *st = smem + s * kSStage;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int id = wt_tid + 256 * c, row = id >> 3;       // 16-byte piece, token
+        uint4 out[NS];
+        if (row < L) {
+          const float w = role ? p.z.scale * exp2f(l2 * static_cast<float>(row + 1))
+                               : exp2f(l2 * static_cast<float>(L - 1 - row));
+          const uint4 y = *reinterpret_cast<const uint4 *>(st + 32768 + 16 * id);
+          const uint32_t yi[4] = {y.x, y.y, y.z, y.w};
+          uint32_t o[NS][4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float f0 = w * bf16_lo(yi[e]), f1 = w * bf16_hi(yi[e]);
+#pragma unroll
+            for (int t = 0; t < NS; ++t) {
+              o[t][e] = lpack2(f0, f1);
+              f0 -= bf16_lo(o[t][e]);
+              f1 -= bf16_hi(o[t][e]);
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < NS; ++t) out[t] = make_uint4(o[t][0], o[t][1], o[t][2], o[t][3]);
+        } else {
+#pragma unroll
+          for (int t = 0; t < NS; ++t) out[t] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int t = 0; t < NS; ++t) *reinterpret_cast<uint4 *>(st + 49152 + t * 16384 + 16 * id) = out[t];
+      }
+      if (L < kC) {
+        // rows behind the sequence may hold anything: 0 * NaN must not reach U
+        for (int id = wt_tid; id < NH * 1024; id += 256)
+          if (((id >> 3) & 127) >= L) *reinterpret_cast<uint4 *>(st + 16 * id) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(kSBarY + s));
+    }
+  } else {
+    // ============================ state ===================================
+    const int qd = warp & 3, row = 32 * qd + lane;            // TMEM lane quarter, state row
+    const uint32_t lanebase = static_cast<uint32_t>(32 * qd) << 16;
+    const bool live = row < D;
+    const size_t at = (static_cast<size_t>(bh) * D + row) * D + hf * 64;
+    float S[64];
+#pragma unroll
+    for (int c = 0; c < 64; ++c) S[c] = 0.f;
+    if (live && p.start[role]) {
+      const float4 *src = reinterpret_cast<const float4 *>(p.start[role] + at);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float4 v = src[c];
+        S[4 * c] = v.x, S[4 * c + 1] = v.y, S[4 * c + 2] = v.z, S[4 * c + 3] = v.w;
+      }
+    }
+    bool ok = true;
+    for (int m = 0; m < ncb; ++m) {
+      const int n = chunk(m);
+      if (live && p.tiles[role] && (m > 0 || p.start[role])) {
+        // the row's 128 bytes, in the order of a 128-byte swizzled tile
+        unsigned char *dst = reinterpret_cast<unsigned char *>(p.tiles[role]) +
+                             (static_cast<size_t>(bh) * p.z.NC + n) * (D * D * 2) + hf * (D * 128) + row * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4 *>(dst + ((c ^ (row & 7)) << 4)) =
+              make_uint4(lpack2(S[8 * c], S[8 * c + 1]), lpack2(S[8 * c + 2], S[8 * c + 3]),
+                         lpack2(S[8 * c + 4], S[8 * c + 5]), lpack2(S[8 * c + 6], S[8 * c + 7]));
+      }
+      if (m >= nst) break;
+      // each head's product is added in registers: sums over a group inside
+      // the tensor core would cut off bits at every step
+      for (int g = 0; g < gi; ++g) {
+        const int i = m * gi + g, u = i & 1;
+        if (!wtw(bar(kSBarU + u), (i >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        const float dec = g == 0 ? exp2f(l2 * static_cast<float>(min(kC, len - n * kC))) : 1.f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float v[32];
+          tc::ld32_wait(tmem + lanebase + u * 64 + x * 32, v);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) S[x * 32 + c] = fmaf(dec, S[x * 32 + c], v[c]);
+        }
+        tc::fence_before_sync();
+        mbar_arrive(bar(kSBarUEmpty + u));
+      }
+      if (!ok) break;
+    }
+    if (ok && live && p.end[role]) {
+      float4 *dst = reinterpret_cast<float4 *>(p.end[role] + at);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) dst[c] = make_float4(S[4 * c], S[4 * c + 1], S[4 * c + 2], S[4 * c + 3]);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 128);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// lin_out: out = mask(A B^T) C + factor (A S), one item per (output, batch,
+// head, chunk):
+//   role 0  o  : A = Q,  B = K,  C = V,  S
+//   role 1  dq : A = dO, B = V,  C = K,  S^T
+//   role 2  dk : A = V,  B = dO, C = Q,  R^T    summed over the group's heads
+//   role 3  dv : A = K,  B = Q,  C = dO, R      summed over the group's heads
+// Persistent, one CTA per SM.  Tiles of 32 KB: A, which stays for the whole
+// item, alternates between two slots; the others arrive through a ring of 5
+// in the order B, [S], C, B, C, ...  Both run on across items, so the loads of
+// the next item are in flight while this one computes.  The state
+// tile serves S and S^T: the first as an N-major, the second as a K-major B
+// operand.  Scores are rounded to bf16 as the next product's A operand (as in
+// the softmax attention), the state tile is bf16; products accumulate in fp32
+// and the two parts meet in fp32, each element rounded once on its way out.
+// TMEM: [0,256) two score / P buffers, [256,384) mask(A B^T) C, [384,512) A S.
+// Warps: 0 TMA, 1 MMA, 2-5 mask and output (thread = row).
+// ---------------------------------------------------------------------------
+constexpr int kOThr = 192;
+constexpr int kOSlots = 5;            // of the ring; the two slots of A follow
+constexpr int kOSlot = 32768;
+constexpr int kOOffA = kOSlots * kOSlot;
+constexpr int kOOffBar = kOOffA + 2 * kOSlot;
+enum {
+  kOBarFull = 0, kOBarEmpty = kOBarFull + kOSlots, kOBarAFull = kOBarEmpty + kOSlots, kOBarAEmpty = kOBarAFull + 2,
+  kOBarS = kOBarAEmpty + 2, kOBarP = kOBarS + 2,
+  kOBarO = kOBarP + 2, kOBarOEmpty = kOBarO + 1, kOBarFinal = kOBarOEmpty + 1, kONumBars = kOBarFinal + 1
+};
+constexpr int kOOffTmem = kOOffBar + kONumBars * 8;
+constexpr int kOOffAbort = kOOffTmem + 4;
+constexpr int kOSmem = kOOffBar + 256 + 1024;        // + alignment slack
+static_assert(kOOffAbort + 4 <= kOOffBar + 256 && kOSmem <= 232448, "output kernel shared memory");
+
+struct LinOutParams {
+  LinSizes z;
+  int backward;
+  int items;
+  int start[2];                       // a state enters the first chunk / comes from behind the last
+  const __nv_bfloat16 *tiles[2];
+  __nv_bfloat16 *out[4];              // o, dq, dk, dv
+  long long stride[4];                // elements between tokens of each output
+  WaitCtl wait;
+};
+
+struct LinItem {
+  int role, b, kv, h, n, L, gi;       // h: head of the output
+  bool st;                            // has a state tile
+};
+
+__device__ __forceinline__ LinItem lin_item(const LinOutParams &p, int i) {
+  LinItem it;
+  const int NC = p.z.NC, G = p.z.G;
+  int bh, g = 0;
+  if (!p.backward) {
+    it.role = 0;
+    g = i % G;
+    i /= G;
+  } else if (G == 1) {                // three outputs of one chunk next to each other: they share its tiles
+    it.role = 1 + i % 3;
+    i /= 3;
+  } else {                            // the items that sum over the group first
+    const int heavy = 2 * p.z.B * p.z.Hkv * NC;
+    if (i < heavy) {
+      it.role = 2 + (i & 1);
+      i >>= 1;
+    } else {
+      i -= heavy;
+      it.role = 1;
+      g = i % G;
+      i /= G;
+    }
+  }
+  it.n = i % NC;
+  bh = i / NC;
+  it.b = bh / p.z.Hkv;
+  it.kv = bh % p.z.Hkv;
+  const int len = seq_len(p.z.lengths, it.b, p.z.T);
+  it.L = min(kC, len - it.n * kC);
+  if (it.role < 2) {
+    it.h = it.kv * G + g;
+    it.gi = 1;
+    it.st = it.n > 0 || p.start[0];
+  } else {
+    it.h = it.kv;
+    it.gi = G;
+    it.st = (it.n + 1) * kC < len || p.start[1];
+  }
+  return it;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kOThr, 1)
+    lin_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+                   const __grid_constant__ LinOutParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int NH = D / 64;
+
+  auto bar = [&](int i) -> uint32_t { return sb + kOOffBar + i * 8; };
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOOffAbort);
+  auto wt = [&](uint32_t br, uint32_t parity) -> bool {
+    if (*abort_flag) return false;
+    if (mbar_wait_bounded(br, parity, p.wait.limit_ns)) return true;
+    *abort_flag = 1;
+    report_timeout(p.wait.err, kSiteLinOut, (br - sb - kOOffBar) / 8);
+    return false;
+  };
+  auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return __shfl_sync(0xffffffffu, wt(br, parity), 0); };
+  // load number q of the ring sits in slot q % kOSlots; its phase there
+  auto phase = [](int q) -> uint32_t { return static_cast<uint32_t>(q / kOSlots) & 1u; };
+
+  if (tid == 0) {
+    for (int s = 0; s < kOSlots; ++s) {
+      mbar_init(bar(kOBarFull + s), 1);
+      mbar_init(bar(kOBarEmpty + s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(kOBarAFull + s), 1);
+      mbar_init(bar(kOBarAEmpty + s), 1);
+      mbar_init(bar(kOBarS + s), 1);
+      mbar_init(bar(kOBarP + s), 128);
+    }
+    mbar_init(bar(kOBarO), 1);
+    mbar_init(bar(kOBarOEmpty), 128);
+    mbar_init(bar(kOBarFinal), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tc::tmem_alloc(sb + kOOffTmem, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kOOffTmem);
+
+  if (warp == 0) {
+    // ============================ TMA producer ============================
+    if (lane == 0) {
+      int q = 0, item = 0;
+      bool ok = true;
+      auto slot = [&](uint32_t bytes) -> bool {       // claims the next slot
+        const int s = q % kOSlots;
+        if (!wt(bar(kOBarEmpty + s), phase(q) ^ 1u)) return ok = false;
+        mbar_arrive_expect_tx(bar(kOBarFull + s), bytes);
+        ++q;
+        return true;
+      };
+      auto tile = [&](const CUtensorMap *m, const LinItem &it, int h) {
+        if (!ok || !slot(NH * 16384)) return;
+        const int s = (q - 1) % kOSlots;
+        for (int x = 0; x < NH; ++x)
+          tma_load_4d(sb + s * kOSlot + x * 16384, m, x * 64, h, it.n * kC, it.b, bar(kOBarFull + s));
+      };
+      for (int i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
+        const LinItem it = lin_item(p, i);
+        if (it.L <= 0) continue;
+        const CUtensorMap *ma = it.role == 0 ? &tmQ : it.role == 1 ? &tmDO : it.role == 2 ? &tmV : &tmK;
+        const CUtensorMap *mb = it.role == 0 ? &tmK : it.role == 1 ? &tmV : it.role == 2 ? &tmDO : &tmQ;
+        const CUtensorMap *mc = it.role == 0 ? &tmV : it.role == 1 ? &tmK : it.role == 2 ? &tmQ : &tmDO;
+        const int as = item & 1;
+        if (!wt(bar(kOBarAEmpty + as), ((item >> 1) & 1) ^ 1)) break;
+        mbar_arrive_expect_tx(bar(kOBarAFull + as), NH * 16384);
+        for (int x = 0; x < NH; ++x)
+          tma_load_4d(sb + kOOffA + as * kOSlot + x * 16384, ma, x * 64, it.h, it.n * kC, it.b, bar(kOBarAFull + as));
+        ++item;
+        for (int g = 0; g < it.gi; ++g) {
+          const int hg = it.role < 2 ? it.kv : it.kv * p.z.G + g;
+          tile(mb, it, hg);
+          if (g == 0 && it.st && ok && slot(D * D * 2)) {
+            const int s = (q - 1) % kOSlots;
+            const __nv_bfloat16 *src = p.tiles[it.role >> 1] +
+                                       (static_cast<size_t>(it.b * p.z.Hkv + it.kv) * p.z.NC + it.n) * (D * D);
+            bulk_load(sb + s * kOSlot, src, D * D * 2, bar(kOBarFull + s));
+          }
+          tile(mc, it, hg);
+        }
+      }
+      if (*abort_flag) {
+        for (int x = (q > kOSlots ? q - kOSlots : 0); x < q; ++x)
+          mbar_wait_bounded(bar(kOBarFull + x % kOSlots), phase(x), 2000000000ull);
+        for (int x = (item > 2 ? item - 2 : 0); x < item; ++x)
+          mbar_wait_bounded(bar(kOBarAFull + (x & 1)), (x >> 1) & 1, 2000000000ull);
+      }
+    }
+  } else if (warp == 1) {
+    // ============================ MMA issuer ==============================
+    constexpr uint32_t id_s = tc::idesc_bf16_f32(128, 128, 0, 0);   // A B^T
+    constexpr uint32_t id_n = tc::idesc_bf16_f32(128, D, 0, 1);     // P C and A S: B operand N-major
+    constexpr uint32_t id_k = tc::idesc_bf16_f32(128, D, 0, 0);     // A S^T: B operand K-major
+    auto kmaj = [&](int q) { return tc::sdesc_sw128(sb + (q % kOSlots) * kOSlot, 16, 1024); };
+    auto nmaj = [&](int q, uint32_t half) { return tc::sdesc_sw128(sb + (q % kOSlots) * kOSlot, half, 1024); };
+    auto kstep = [](int kk, int half) -> uint32_t { return static_cast<uint32_t>((kk >> 2) * half + (kk & 3) * 32) >> 4; };
+    int q = 0, ss = 0, item = 0;
+    bool ok = true;
+    auto full = [&](int x) -> bool { return wtw(bar(kOBarFull + x % kOSlots), phase(x)); };
+    for (int i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
+      const LinItem it = lin_item(p, i);
+      if (it.L <= 0) continue;
+      const int q0 = q, st = it.st ? 1 : 0, as = item & 1;
+      auto qb = [&](int g) { return q0 + (g ? st + 2 * g : 0); };
+      const uint64_t dA = tc::sdesc_sw128(sb + kOOffA + as * kOSlot, 16, 1024);
+      // A B^T into the score buffer that held P two steps ago (its product
+      // was issued before: the tensor core works in order)
+      auto scores = [&](int g) -> bool {
+        if (!full(qb(g))) return false;
+        tc::fence_after_sync();
+        const uint64_t dB = kmaj(qb(g));
+        const uint32_t tS = tmem + ((ss + g) & 1) * 128;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) tc::mma_bf16_w(tS, dA + kstep(kk, 16384), dB + kstep(kk, 16384), id_s, kk > 0);
+        tc::commit_w(bar(kOBarS + ((ss + g) & 1)));
+        tc::commit_w(bar(kOBarEmpty + qb(g) % kOSlots));
+        return true;
+      };
+      ok = wtw(bar(kOBarAFull + as), (item >> 1) & 1) && scores(0);
+      // the accumulators are free once the last item's rows have been read
+      if (ok) ok = wtw(bar(kOBarOEmpty), (item & 1) ^ 1);
+      if (ok && st) {
+        ok = full(q0 + 1);
+        if (ok) {
+          tc::fence_after_sync();
+          if (it.role == 0 || it.role == 3) {
+            const uint64_t dS = nmaj(q0 + 1, D * 128);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_bf16_w(tmem + 384, dA + kstep(kk, 16384), dS + ((kk * 2048) >> 4), id_n, kk > 0);
+          } else {
+            const uint64_t dS = kmaj(q0 + 1);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_bf16_w(tmem + 384, dA + kstep(kk, 16384), dS + kstep(kk, D * 128), id_k, kk > 0);
+          }
+          tc::commit_w(bar(kOBarEmpty + (q0 + 1) % kOSlots));
+        }
+      }
+      for (int g = 0; ok && g < it.gi; ++g) {
+        if (g + 1 < it.gi && !scores(g + 1)) {
+          ok = false;
+          break;
+        }
+        const int qc = g ? qb(g) + 1 : q0 + 1 + st, sbuf = (ss + g) & 1;
+        ok = full(qc) && wtw(bar(kOBarP + sbuf), ((ss + g) >> 1) & 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint64_t dC = nmaj(qc, 16384);
+        // P chunk c (16 columns) sits in the 8 columns 32 (c / 2) + 8 (c % 2)
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_bf16_ts_w(tmem + 256, tmem + sbuf * 128 + (kk >> 1) * 32 + (kk & 1) * 8, dC + ((kk * 2048) >> 4), id_n,
+                            g > 0 || kk > 0);
+        tc::commit_w(bar(kOBarEmpty + qc % kOSlots));
+      }
+      if (ok) {
+        tc::commit_w(bar(kOBarAEmpty + as));
+        tc::commit_w(bar(kOBarO));
+      }
+      q = q0 + st + 2 * it.gi;
+      ss += it.gi;
+      ++item;
+    }
+    tc::commit_w(bar(kOBarFinal));
+    mbar_wait_bounded(bar(kOBarFinal), 0, 2000000000ull);   // every MMA has completed
+  } else {
+    // ============================ mask and output =========================
+    const int qd = warp & 3, row = 32 * qd + lane;
+    const uint32_t lanebase = static_cast<uint32_t>(32 * qd) << 16;
+    int q = 0, ss = 0, item = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
+      const LinItem it = lin_item(p, i);
+      const int t = it.n * kC + row;
+      __nv_bfloat16 *dst = p.out[it.role] + (static_cast<size_t>(it.b) * p.z.T + t) * p.stride[it.role] + it.h * D;
+      if (it.L <= 0) {                                        // rows behind the sequence
+        if (t < p.z.T)
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4 *>(dst)[c] = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      const bool rev = it.role >= 2;
+      const float l2 = log2_decay(p.z.log_decay[it.kv]);
+      const int st = it.st ? 1 : 0;
+      float pw[16];                                           // a^0 .. a^15
+#pragma unroll
+      for (int e = 0; e < 16; ++e) pw[e] = exp2f(l2 * static_cast<float>(e));
+      for (int g = 0; ok && g < it.gi; ++g) {
+        const int sbuf = (ss + g) & 1;
+        if (!wtw(bar(kOBarS + sbuf), ((ss + g) >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        const uint32_t tS = tmem + lanebase + sbuf * 128;
+#pragma unroll 1
+        for (int c2 = 0; c2 < 4; ++c2) {                      // 32 columns at a time
+          float s[32];
+          tc::ld32_wait(tS + 32 * c2, s);
+          uint32_t pk[2][8];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int c0 = 32 * c2 + 16 * x;
+            // distance from the column block's nearest column to the warp's
+            // rows: whole blocks inside the mask factor into a power per row
+            // and a power per column
+            const bool inside = rev ? (c0 >= 32 * qd + 31 && c0 + 16 <= it.L) : c0 + 15 <= 32 * qd;
+            const bool outside = rev ? c0 + 15 < 32 * qd : c0 > 32 * qd + 31;
+            if (outside) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) pk[x][e] = 0;
+            } else if (inside) {
+              const float base = p.z.scale * exp2f(l2 * static_cast<float>(rev ? c0 - row : row - c0 - 15));
+#pragma unroll
+              for (int e = 0; e < 16; e += 2)
+                pk[x][e / 2] = rev ? lpack2(s[16 * x + e] * (base * pw[e]), s[16 * x + e + 1] * (base * pw[e + 1]))
+                                   : lpack2(s[16 * x + e] * (base * pw[15 - e]), s[16 * x + e + 1] * (base * pw[14 - e]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                float v[2];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const int col = c0 + e + y, gap = rev ? col - row : row - col;
+                  v[y] = (gap >= 0 && col < it.L) ? s[16 * x + e + y] * (p.z.scale * exp2f(l2 * static_cast<float>(gap))) : 0.f;
+                }
+                pk[x][e / 2] = lpack2(v[0], v[1]);
+              }
+            }
+          }
+          tc::st8x2_async(tS + 32 * c2, pk[0], tS + 32 * c2 + 8, pk[1]);
+        }
+        if (it.L < kC) {
+          // rows of C behind the sequence may hold anything: 0 * NaN must not reach the product
+          const int qc = q + 1 + st + 2 * g;
+          if (!wtw(bar(kOBarFull + qc % kOSlots), phase(qc))) {
+            ok = false;
+            break;
+          }
+          if (row >= it.L) {
+            unsigned char *cr = smem + (qc % kOSlots) * kOSlot + row * 128;
+#pragma unroll
+            for (int x = 0; x < NH; ++x)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(cr + x * 16384 + 16 * e) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tc::wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(bar(kOBarP + sbuf));
+      }
+      if (!ok || !wtw(bar(kOBarO), item & 1)) break;
+      tc::fence_after_sync();
+      const float fac = rev ? exp2f(l2 * static_cast<float>(max(it.L - 1 - row, 0)))
+                            : p.z.scale * exp2f(l2 * static_cast<float>(row + 1));
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float a[32], s[32];
+        if (st) {
+          tc::ld32x2_wait(tmem + lanebase + 256 + c, tmem + lanebase + 384 + c, a, s);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) a[e] = fmaf(fac, s[e], a[e]);
+        } else {
+          tc::ld32_wait(tmem + lanebase + 256 + c, a);
+        }
+        if (t < p.z.T) {
+          const bool in = row < it.L;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            reinterpret_cast<uint4 *>(dst + c)[e / 8] =
+                in ? make_uint4(lpack2(a[e], a[e + 1]), lpack2(a[e + 2], a[e + 3]), lpack2(a[e + 4], a[e + 5]),
+                                lpack2(a[e + 6], a[e + 7]))
+                   : make_uint4(0, 0, 0, 0);
+        }
+      }
+      tc::fence_before_sync();
+      mbar_arrive(bar(kOBarOEmpty));
+      q += st + 2 * it.gi;
+      ss += it.gi;
+      ++item;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// lin_decode: one token per sequence.  Bound by reading and writing the fp32
+// states.  A block takes 32 columns of one (batch row, KV head) state: 8
+// lanes of 4 columns span a row, 32 rows go at a time, every thread holds its
+// rows' pieces at once; the group's query products are summed over the rows
+// by shuffles and shared memory.
+// ---------------------------------------------------------------------------
+constexpr int kDThr = 256;
+constexpr int kDCols = 32;
+
+struct LinDecodeParams {
+  const void *q, *k, *v;
+  void *o;
+  float *state;
+  const float *log_decay;
+  const int *slots;
+  int Hq, Hkv, G, D, nstates;
+  float scale;
+};
+
+template <typename T>
+__device__ __forceinline__ float lin_ld(const void *p, size_t i) {
+  return static_cast<float>(reinterpret_cast<const T *>(p)[i]);
+}
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kDThr) lin_decode_kernel(const LinDecodeParams p) {
+  __shared__ float sk[D], sq[G][D];
+  __shared__ float red[kDThr / 32][G][kDCols];
+  constexpr int NSL = D / kDCols, R = D / 32;
+  const int slice = blockIdx.x % NSL, bh = blockIdx.x / NSL;
+  const int b = bh / p.Hkv, kv = bh % p.Hkv;
+  const int tid = threadIdx.x, c4 = tid & 7, r0 = tid >> 3;
+  const int slot = p.slots ? p.slots[b] : b;
+  const size_t ob = (static_cast<size_t>(b) * p.Hq + kv * p.G) * D + slice * kDCols;
+  if (slot < 0 || slot >= p.nstates) {                        // an empty row of the batch
+    for (int i = tid; i < p.G * kDCols; i += kDThr)
+      reinterpret_cast<T *>(p.o)[ob + static_cast<size_t>(i / kDCols) * D + i % kDCols] = static_cast<T>(0.f);
+    return;
+  }
+  float4 *st = reinterpret_cast<float4 *>(p.state + (static_cast<size_t>(slot) * p.Hkv + kv) * (D * D) + slice * kDCols);
+  float4 s[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) s[r] = st[(r0 + 32 * r) * (D / 4) + c4];
+  const float a = expf(p.log_decay[kv]);
+  if (tid < D) sk[tid] = lin_ld<T>(p.k, static_cast<size_t>(bh) * D + tid);
+  for (int i = tid; i < G * D; i += kDThr)
+    sq[i / D][i % D] = i / D < p.G ? lin_ld<T>(p.q, (static_cast<size_t>(b) * p.Hq + kv * p.G) * D + i) : 0.f;
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = lin_ld<T>(p.v, static_cast<size_t>(bh) * D + slice * kDCols + 4 * c4 + e);
+  __syncthreads();
+  float4 acc[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int d = r0 + 32 * r;
+    const float k = sk[d];
+    s[r].x = fmaf(a, s[r].x, k * v[0]);
+    s[r].y = fmaf(a, s[r].y, k * v[1]);
+    s[r].z = fmaf(a, s[r].z, k * v[2]);
+    s[r].w = fmaf(a, s[r].w, k * v[3]);
+    st[d * (D / 4) + c4] = s[r];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const float q = sq[g][d];
+      acc[g].x = fmaf(q, s[r].x, acc[g].x);
+      acc[g].y = fmaf(q, s[r].y, acc[g].y);
+      acc[g].z = fmaf(q, s[r].z, acc[g].z);
+      acc[g].w = fmaf(q, s[r].w, acc[g].w);
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+      acc[g].x += __shfl_xor_sync(0xffffffffu, acc[g].x, o);
+      acc[g].y += __shfl_xor_sync(0xffffffffu, acc[g].y, o);
+      acc[g].z += __shfl_xor_sync(0xffffffffu, acc[g].z, o);
+      acc[g].w += __shfl_xor_sync(0xffffffffu, acc[g].w, o);
+    }
+    if ((tid & 31) < 8) *reinterpret_cast<float4 *>(&red[tid >> 5][g][4 * c4]) = acc[g];
+  }
+  __syncthreads();
+  for (int i = tid; i < p.G * kDCols; i += kDThr) {
+    const int g = i / kDCols, c = i % kDCols;
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < kDThr / 32; ++w) t += red[w][g][c];
+    reinterpret_cast<T *>(p.o)[ob + static_cast<size_t>(g) * D + c] = static_cast<T>(p.scale * t);
+  }
+}
+
+template <typename T, int D>
+cudaError_t decode_groups(const LinDecodeParams &p, unsigned blocks, cudaStream_t st) {
+  if (p.G <= 1)
+    lin_decode_kernel<T, D, 1><<<blocks, kDThr, 0, st>>>(p);
+  else if (p.G <= 2)
+    lin_decode_kernel<T, D, 2><<<blocks, kDThr, 0, st>>>(p);
+  else if (p.G <= 4)
+    lin_decode_kernel<T, D, 4><<<blocks, kDThr, 0, st>>>(p);
+  else
+    lin_decode_kernel<T, D, 8><<<blocks, kDThr, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+// Rows of D elements at `stride` elements from token to token.
+bool lin_map(CUtensorMap *mp, const void *base, int D, int H, int T, int B, long long stride, const char **why) {
+  const uint64_t ts = static_cast<uint64_t>(stride) * 2;
+  const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(H), static_cast<uint64_t>(T),
+                            static_cast<uint64_t>(B)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, ts, ts * T};
+  const uint32_t box[4] = {64, 1, kC, 1};
+  return encode_tiled(mp, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                      why);
+}
+
+template <int D, int NS>
+cudaError_t launch_state(const CUtensorMap (&tm)[4], const LinStateParams &p, unsigned grid, cudaStream_t st) {
+  const auto kern = lin_state_kernel<D, NS>;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), kSSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kSThr, kSSmem, st>>>(tm[0], tm[1], tm[2], tm[3], p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_lin(const CUtensorMap (&tm)[4], const LinStateParams &sp, const LinOutParams &op, bool exact,
+                       int sms, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  if (sp.nroles) {
+    const unsigned grid = static_cast<unsigned>(sp.nroles) * sp.z.B * sp.z.Hkv * (D / 64);
+    e = exact ? launch_state<D, 3>(tm, sp, grid, st) : launch_state<D, 2>(tm, sp, grid, st);
+    if (e != cudaSuccess) return e;
+  }
+  const auto kern = lin_out_kernel<D>;
+  e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), kOSmem);
+  if (e != cudaSuccess) return e;
+  const int grid = op.items < sms ? op.items : sms;
+  kern<<<grid, kOThr, kOSmem, st>>>(tm[0], tm[1], tm[2], tm[3], op);
+  return cudaGetLastError();
+}
+
+size_t tiles_bytes(int B, int T, int Hkv, int D) {
+  const size_t nc = (static_cast<size_t>(T) + kC - 1) / kC;
+  return static_cast<size_t>(B) * Hkv * nc * D * D * 2;
+}
+
+}  // namespace
+
+size_t lin_attn_workspace_bytes(int B, int T, int Hkv, int D, int backward) {
+  return tiles_bytes(B, T, Hkv, D) * (backward ? 2 : 1);
+}
+
+cudaError_t launch_lin_attn(const LinAttnArgs &a, const WaitCtl &w, cudaStream_t st, const char **why) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const bool bwd = a.dout != nullptr;
+  LinOutParams op = {};
+  op.z.B = a.B, op.z.T = a.T, op.z.Hq = a.Hq, op.z.Hkv = a.Hkv, op.z.G = a.Hq / a.Hkv;
+  op.z.NC = (a.T + kC - 1) / kC;
+  op.z.scale = a.scale;
+  op.z.log_decay = a.log_decay;
+  op.z.lengths = a.lengths;
+  op.backward = bwd;
+  const long long items = static_cast<long long>(a.B) * op.z.NC * (bwd ? a.Hq + 2LL * a.Hkv : a.Hq);
+  if (items > 0x7ffffff0LL - sms || 4LL * a.B * a.Hkv > 0x7fffffffLL) {
+    *why = "grid too large";
+    return cudaErrorNotSupported;
+  }
+  op.items = static_cast<int>(items);
+  LinStateParams sp = {};
+  sp.z = op.z;
+  sp.start[0] = a.initial_state;
+  sp.start[1] = a.dfinal_state;
+  sp.end[0] = a.final_state;
+  sp.end[1] = a.dinitial_state;
+  // which recurrences anything reads: the tiles of more than one chunk or of
+  // a given start, and the states that leave
+  const bool tiles0 = op.z.NC > 1 || a.initial_state, tiles1 = bwd && (op.z.NC > 1 || a.dfinal_state);
+  const bool f = tiles0 || a.final_state, r = tiles1 || a.dinitial_state;
+  sp.first_role = f ? 0 : 1;
+  sp.nroles = (f ? 1 : 0) + (r ? 1 : 0);
+  sp.tiles[0] = tiles0 ? static_cast<__nv_bfloat16 *>(a.ws) : nullptr;
+  sp.tiles[1] = tiles1 ? reinterpret_cast<__nv_bfloat16 *>(static_cast<unsigned char *>(a.ws) +
+                                                           tiles_bytes(a.B, a.T, a.Hkv, a.D))
+                       : nullptr;
+  sp.wait = w;
+  for (int i = 0; i < 2; ++i) {
+    op.tiles[i] = sp.tiles[i];
+    op.start[i] = sp.start[i] != nullptr;
+  }
+  void *const out[4] = {a.o, a.dq, a.dk, a.dv};
+  const long long os[4] = {a.o_stride, a.dq_stride, a.dk_stride, a.dv_stride};
+  for (int i = 0; i < 4; ++i) {
+    op.out[i] = static_cast<__nv_bfloat16 *>(out[i]);
+    op.stride[i] = os[i];
+  }
+  op.wait = w;
+  CUtensorMap tm[4];
+  if (!lin_map(&tm[0], a.q, a.D, a.Hq, a.T, a.B, a.q_stride, why) ||
+      !lin_map(&tm[1], a.k, a.D, a.Hkv, a.T, a.B, a.k_stride, why) ||
+      !lin_map(&tm[2], a.v, a.D, a.Hkv, a.T, a.B, a.v_stride, why) ||
+      !lin_map(&tm[3], bwd ? a.dout : a.q, a.D, a.Hq, a.T, a.B, bwd ? static_cast<long long>(a.Hq) * a.D : a.q_stride,
+               why))
+    return cudaErrorInvalidValue;
+  const bool exact = a.final_state || a.dinitial_state;   // a state leaves in fp32
+  return a.D == 128 ? launch_lin<128>(tm, sp, op, exact, sms, st) : launch_lin<64>(tm, sp, op, exact, sms, st);
+}
+
+cudaError_t launch_lin_attn_decode(const void *q, const void *k, const void *v, float *state, const float *log_decay,
+                                   const int *slots, void *o, int bf16, int B, int Hq, int Hkv, int D, int nstates,
+                                   float scale, cudaStream_t st) {
+  LinDecodeParams p;
+  p.q = q, p.k = k, p.v = v, p.o = o;
+  p.state = state;
+  p.log_decay = log_decay;
+  p.slots = slots;
+  p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.D = D, p.nstates = nstates;
+  p.scale = scale;
+  const long long blocks = static_cast<long long>(B) * Hkv * (D / kDCols);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const unsigned n = static_cast<unsigned>(blocks);
+  if (bf16) return D == 128 ? decode_groups<__nv_bfloat16, 128>(p, n, st) : decode_groups<__nv_bfloat16, 64>(p, n, st);
+  return D == 128 ? decode_groups<float, 128>(p, n, st) : decode_groups<float, 64>(p, n, st);
+}
+
+}  // namespace abw
