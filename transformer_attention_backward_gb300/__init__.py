@@ -16,6 +16,7 @@ Functions (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -297,24 +298,56 @@ def attn_bwd_causal_saved_p(q, k, v, p_attn, o, dout, scale=None, rope_base=0.0,
 
 # --------------------------------------------------------------------------
 # Per-head norm with rotation, and linear attention
+#
+# A call on a few tokens takes the GPU some microseconds, so what the host
+# does for it counts: one pass of checks per tensor (the reason is looked for
+# only when one fails), the raw stream handle, cached workspace sizes.
 # --------------------------------------------------------------------------
-def _rows(t, name, dtypes, shape):
-    """Checks a [B][T][H][D] tensor whose tokens may be apart (a part of a
-    packed projection) and returns its token stride in elements."""
+_BF16, _F32 = torch.bfloat16, torch.float32
+_lib = None
+
+
+def _fns():
+    global _lib
+    if _lib is None:
+        _lib = library()
+    return _lib
+
+
+def _dense(t, name, dt, shape, dev):
+    """Checks a dense tensor and returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dt and t.shape == shape and t.device == dev and t.is_contiguous()):
+        _req(t, name, (dt,), shape)
+        raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
+    return t.data_ptr()
+
+
+def _first(t, name, dim, dtypes):
+    """Checks what the first tensor of a call decides: type, rank, device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} dtype {t.dtype} not in {dtypes}")
-    if t.shape != shape:
-        raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} axes, not {t.dim()}")
+    return t.device
+
+
+def _rows(t, name, dt, shape, dev):
+    """Checks a [B][T][H][D] tensor whose tokens may be apart (a part of a
+    packed projection) and returns its token stride in elements, 0 if dense."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dt and t.shape == shape and t.device == dev):
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dt and t.shape == shape:
+            raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
+        _req(t.contiguous() if isinstance(t, torch.Tensor) else t, name, (dt,), shape)
     if t.is_contiguous():
         return 0
     B, T, H, D = shape
-    sb, stt, sh, sd = t.stride()
-    token = stt if T > 1 else sb
-    if (D > 1 and sd != 1) or (H > 1 and sh != D) or (B > 1 and T > 1 and sb != T * stt) or token < H * D:
+    sb, st, sh, sd = t.stride()
+    token = st if T > 1 else sb
+    if (D > 1 and sd != 1) or (H > 1 and sh != D) or (B > 1 and T > 1 and sb != T * st) or token < H * D:
         raise ValueError(f"{name} must have dense [H][D] rows at one stride from token to token")
     return token
 
@@ -328,38 +361,37 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _call(op, fn, tensors, stream, *args):
-    """Launches on the tensors' device, which they have to share."""
-    d = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != d:
-            raise ValueError(f"{op}: tensors on {d} and {t.device}")
-    if stream is not None and stream.device != d:
-        raise ValueError(f"{op}: stream on {stream.device}, tensors on {d}")
-    if d.index == torch.cuda.current_device():
-        status = fn(*args, _s(stream))
+def _call(op, fn, dev, stream, *args):
+    """Launches on the tensors' device, on `stream` or its current stream."""
+    index = dev.index
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device == dev:
+        handle = stream.cuda_stream
     else:
-        with torch.cuda.device(d):
-            status = fn(*args, _s(stream))
-    if status != _b.OK:
+        raise ValueError(f"{op}: stream on {stream.device}, tensors on {dev}")
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status:
         _b.check(status, op)
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _rotation(B, T, D, rope_base, rotary_dim, positions, sections):
-    """(rotary_dim, n_axes, sections as a host array or None)."""
-    axes = 1 if sections is None else len(sections)
+def _rotation(B, T, D, rope_base, rotary_dim, positions, sections, dev):
+    """(rotary_dim, address of the positions, axes, sections as a host array)."""
     if not rope_base:
-        return 0, 1, None
+        return 0, None, 1, None
+    axes, host = 1, None
+    if sections is not None:
+        axes = len(sections)
+        host = (ctypes.c_int * axes)(*sections)
+    at = None
     if positions is not None:
-        _req(positions, "positions", (torch.int32,))
-        if tuple(positions.shape) != (axes, B, T) and not (axes == 1 and tuple(positions.shape) == (B, T)):
-            raise ValueError(f"positions shape {tuple(positions.shape)} != {(axes, B, T)}")
-    host = None if sections is None else (ctypes.c_int * axes)(*sections)
-    return D if rotary_dim is None else int(rotary_dim), axes, host
+        flat = axes == 1 and isinstance(positions, torch.Tensor) and positions.dim() == 2
+        at = _dense(positions, "positions", torch.int32, (B, T) if flat else (axes, B, T), dev)
+    return D if rotary_dim is None else int(rotary_dim), at, axes, host
 
 
 def qk_norm_rope_fwd(q, k, gamma_q=None, gamma_k=None, eps=1e-6, rope_base=0.0, rotary_dim=None, interleaved=True,
@@ -370,32 +402,32 @@ def qk_norm_rope_fwd(q, k, gamma_q=None, gamma_k=None, eps=1e-6, rope_base=0.0, 
     fp32 or bf16, possibly parts of a packed projection.  positions
     [axes][B][T] int32 (None: pos0 + t); ``sections`` gives each axis its
     number of pairs.  Returns dense (q_out, k_out) of the inputs' dtype."""
-    dts = (torch.float32, torch.bfloat16)
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be [B][T][Hq][D]")
-    B, T, Hq, D = q.shape
-    qs = _rows(q, "q", dts, q.shape)
+    dev = _first(q, "q", 4, (_F32, _BF16))
+    dt, qshape = q.dtype, q.shape
+    B, T, Hq, D = qshape
+    qs = _rows(q, "q", dt, qshape, dev)
+    q_out = _empty(qshape, dt, dev, stream) if q_out is None else q_out
+    qo = _dense(q_out, "q_out", dt, qshape, dev)
     Hkv = ks = 0
+    kp = ko = None
     if k is not None:
-        Hkv = k.shape[2] if k.dim() == 4 else 0
-        ks = _rows(k, "k", (q.dtype,), (B, T, Hkv, D))
-    for g, name in ((gamma_q, "gamma_q"), (gamma_k, "gamma_k")):
-        if g is not None:
-            _req(g, name, (torch.float32,), (D,))
-    R, axes, host = _rotation(B, T, D, rope_base, rotary_dim, positions, sections)
-    q_out = _empty(q.shape, q.dtype, q.device, stream) if q_out is None else q_out
-    _req(q_out, "q_out", (q.dtype,), q.shape)
-    if k is not None:
-        k_out = _empty(k.shape, k.dtype, k.device, stream) if k_out is None else k_out
-        _req(k_out, "k_out", (k.dtype,), k.shape)
+        Hkv = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+        kshape = (B, T, Hkv, D)
+        ks = _rows(k, "k", dt, kshape, dev)
+        kp = k.data_ptr()
+        k_out = _empty(kshape, dt, dev, stream) if k_out is None else k_out
+        ko = _dense(k_out, "k_out", dt, kshape, dev)
     else:
         k_out = None
-    _call("qk_norm_rope_fwd", library().qk_norm_rope_fwd, (q, k, gamma_q, gamma_k, q_out, k_out, positions), stream,
-          _addr(q), _addr(k), _DT[q.dtype], _addr(gamma_q), _addr(gamma_k), _addr(q_out), _addr(k_out), B, T, Hq, Hkv, D,
-          qs, ks, float(eps), float(rope_base), R, 1 if interleaved else 0, _addr(positions), axes, host, int(pos0))
+    gq = None if gamma_q is None else _dense(gamma_q, "gamma_q", _F32, (D,), dev)
+    gk = None if gamma_k is None else _dense(gamma_k, "gamma_k", _F32, (D,), dev)
+    R, pos, axes, host = _rotation(B, T, D, rope_base, rotary_dim, positions, sections, dev)
+    _call("qk_norm_rope_fwd", _fns().qk_norm_rope_fwd, dev, stream, q.data_ptr(), kp, _DT[dt], gq, gk, qo, ko, B, T, Hq,
+          Hkv, D, qs, ks, float(eps), float(rope_base), R, 1 if interleaved else 0, pos, axes, host, int(pos0))
     return q_out, k_out
 
 
+@functools.lru_cache(maxsize=None)
 def qk_norm_rope_bwd_workspace_bytes(D) -> int:
     return int(library().qk_norm_rope_bwd_workspace_bytes(D))
 
@@ -407,72 +439,79 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, gamma_q=None, gamma_k=None, eps=1e-6,
     (the same for both).  dq, dk have the inputs' dtype and may be parts of a
     packed gradient.  Returns (dq, dk, dgamma_q, dgamma_k), None where there
     is no k or no gamma."""
-    dts = (torch.float32, torch.bfloat16)
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be [B][T][Hq][D]")
-    B, T, Hq, D = q.shape
-    qs = _rows(q, "q", dts, q.shape)
-    _req(dq_out, "dq_out", dts, q.shape)
-    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
-    dqs = _rows(dq, "dq", (q.dtype,), q.shape)
+    dts = (_F32, _BF16)
+    dev = _first(q, "q", 4, dts)
+    _first(dq_out, "dq_out", 4, dts)
+    dt, yt, qshape = q.dtype, dq_out.dtype, q.shape
+    B, T, Hq, D = qshape
+    qs = _rows(q, "q", dt, qshape, dev)
+    yq = _dense(dq_out, "dq_out", yt, qshape, dev)
+    dq = _empty(qshape, dt, dev, stream) if dq is None else dq
+    dqs = _rows(dq, "dq", dt, qshape, dev)
     Hkv = ks = dks = 0
+    kp = yk = dkp = gq = gk = dgq = dgk = None
     if k is not None:
-        Hkv = k.shape[2] if k.dim() == 4 else 0
-        ks = _rows(k, "k", (q.dtype,), (B, T, Hkv, D))
-        _req(dk_out, "dk_out", (dq_out.dtype,), k.shape)
-        dk = _empty(k.shape, k.dtype, k.device, stream) if dk is None else dk
-        dks = _rows(dk, "dk", (q.dtype,), k.shape)
+        Hkv = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+        kshape = (B, T, Hkv, D)
+        ks = _rows(k, "k", dt, kshape, dev)
+        yk = _dense(dk_out, "dk_out", yt, kshape, dev)
+        dk = _empty(kshape, dt, dev, stream) if dk is None else dk
+        dks = _rows(dk, "dk", dt, kshape, dev)
+        kp, dkp = k.data_ptr(), dk.data_ptr()
     else:
-        dk_out = dk = gamma_k = None
+        dk = gamma_k = None
     if gamma_q is not None:
-        _req(gamma_q, "gamma_q", (torch.float32,), (D,))
-        dgamma_q = _empty((D,), torch.float32, q.device, stream) if dgamma_q is None else dgamma_q
-        _req(dgamma_q, "dgamma_q", (torch.float32,), (D,))
+        gq = _dense(gamma_q, "gamma_q", _F32, (D,), dev)
+        dgamma_q = _empty((D,), _F32, dev, stream) if dgamma_q is None else dgamma_q
+        dgq = _dense(dgamma_q, "dgamma_q", _F32, (D,), dev)
     else:
         dgamma_q = None
     if gamma_k is not None:
-        _req(gamma_k, "gamma_k", (torch.float32,), (D,))
-        dgamma_k = _empty((D,), torch.float32, q.device, stream) if dgamma_k is None else dgamma_k
-        _req(dgamma_k, "dgamma_k", (torch.float32,), (D,))
+        gk = _dense(gamma_k, "gamma_k", _F32, (D,), dev)
+        dgamma_k = _empty((D,), _F32, dev, stream) if dgamma_k is None else dgamma_k
+        dgk = _dense(dgamma_k, "dgamma_k", _F32, (D,), dev)
     else:
         dgamma_k = None
-    R, axes, host = _rotation(B, T, D, rope_base, rotary_dim, positions, sections)
-    if workspace is None and (gamma_q is not None or gamma_k is not None):
-        workspace = _empty((qk_norm_rope_bwd_workspace_bytes(D),), torch.uint8, q.device, stream)
-    if workspace is not None:
-        _req(workspace, "workspace", (torch.uint8,))
-    _call("qk_norm_rope_bwd", library().qk_norm_rope_bwd,
-          (q, k, dq_out, dk_out, gamma_q, gamma_k, dq, dk, dgamma_q, dgamma_k, positions, workspace), stream, _addr(q),
-          _addr(k), _DT[q.dtype], _addr(dq_out), _addr(dk_out), _DT[dq_out.dtype], _addr(gamma_q), _addr(gamma_k),
-          _addr(dq), _addr(dk), _addr(dgamma_q), _addr(dgamma_k), B, T, Hq, Hkv, D, qs, ks, dqs, dks, float(eps),
-          float(rope_base), R, 1 if interleaved else 0, _addr(positions), axes, host, int(pos0), _addr(workspace),
-          0 if workspace is None else workspace.numel())
+    R, pos, axes, host = _rotation(B, T, D, rope_base, rotary_dim, positions, sections, dev)
+    wp, wn = _workspace(workspace, qk_norm_rope_bwd_workspace_bytes(D) if gq or gk else 0, dev, stream)
+    _call("qk_norm_rope_bwd", _fns().qk_norm_rope_bwd, dev, stream, q.data_ptr(), kp, _DT[dt], yq, yk, _DT[yt], gq, gk,
+          dq.data_ptr(), dkp, dgq, dgk, B, T, Hq, Hkv, D, qs, ks, dqs, dks, float(eps), float(rope_base), R,
+          1 if interleaved else 0, pos, axes, host, int(pos0), wp if wp is None else wp.data_ptr(), wn)
     return dq, dk, dgamma_q, dgamma_k
 
 
+def _workspace(given, need, dev, stream):
+    """(tensor or None, bytes): the caller's workspace, or one for this call."""
+    if given is None:
+        return (None, 0) if need == 0 else (_empty((need,), torch.uint8, dev, stream), need)
+    _dense(given, "workspace", torch.uint8, given.shape if isinstance(given, torch.Tensor) else (need,), dev)
+    return given, given.numel()
+
+
+@functools.lru_cache(maxsize=1024)
 def lin_attn_fwd_workspace_bytes(B, T, Hkv, D) -> int:
     return int(library().lin_attn_fwd_workspace_bytes(B, T, Hkv, D))
 
 
+@functools.lru_cache(maxsize=1024)
 def lin_attn_bwd_workspace_bytes(B, T, Hkv, D) -> int:
     return int(library().lin_attn_bwd_workspace_bytes(B, T, Hkv, D))
 
 
 def _lin_inputs(q, k, v, log_decay, initial_state, lengths):
-    bf = (torch.bfloat16,)
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be [B][T][Hq][D]")
-    if not isinstance(k, torch.Tensor) or k.dim() != 4:
-        raise ValueError("k must be [B][T][Hkv][D]")
-    B, T, Hq, D = q.shape
+    """Checks what both directions take: (device, sizes, [B][T][Hkv][D],
+    [B][Hkv][D][D], strides, addresses)."""
+    dev = _first(q, "q", 4, (_BF16,))
+    _first(k, "k", 4, (_BF16,))
+    qshape = q.shape
+    B, T, Hq, D = qshape
     Hkv = k.shape[2]
-    strides = (_rows(q, "q", bf, q.shape), _rows(k, "k", bf, (B, T, Hkv, D)), _rows(v, "v", bf, (B, T, Hkv, D)))
-    _req(log_decay, "log_decay", (torch.float32,), (Hkv,))
-    if initial_state is not None:
-        _req(initial_state, "initial_state", (torch.float32,), (B, Hkv, D, D))
-    if lengths is not None:
-        _req(lengths, "lengths", (torch.int32,), (B,))
-    return (B, T, Hq, Hkv, D), strides
+    kshape, sshape = (B, T, Hkv, D), (B, Hkv, D, D)
+    strides = (_rows(q, "q", _BF16, qshape, dev), _rows(k, "k", _BF16, kshape, dev), _rows(v, "v", _BF16, kshape, dev))
+    at = (q.data_ptr(), k.data_ptr(), v.data_ptr(), _dense(log_decay, "log_decay", _F32, (Hkv,), dev),
+          None if initial_state is None else _dense(initial_state, "initial_state", _F32, sshape, dev),
+          None if lengths is None else _dense(lengths, "lengths", torch.int32, (B,), dev))
+    return dev, (B, T, Hq, Hkv, D), kshape, sshape, strides, at
 
 
 def lin_attn_fwd(q, k, v, log_decay, scale=None, initial_state=None, lengths=None, want_final_state=False, o=None,
@@ -484,22 +523,16 @@ def lin_attn_fwd(q, k, v, log_decay, scale=None, initial_state=None, lengths=Non
     int32 or None (tokens of each sequence; o is 0 behind them).  Returns
     (o [B][T][Hq][D] bf16, final_state fp32 or None); final_state may be the
     initial_state tensor."""
-    dims, strides = _lin_inputs(q, k, v, log_decay, initial_state, lengths)
+    dev, dims, _, sshape, strides, (qp, kp, vp, ldp, s0, ln) = _lin_inputs(q, k, v, log_decay, initial_state, lengths)
     B, T, Hq, Hkv, D = dims
-    scale = 1.0 / math.sqrt(D) if scale is None else scale
-    o = _empty(q.shape, q.dtype, q.device, stream) if o is None else o
-    os = _rows(o, "o", (torch.bfloat16,), q.shape)
+    o = _empty(q.shape, _BF16, dev, stream) if o is None else o
+    os = _rows(o, "o", _BF16, q.shape, dev)
     if final_state is None and want_final_state:
-        final_state = _empty((B, Hkv, D, D), torch.float32, q.device, stream)
-    if final_state is not None:
-        _req(final_state, "final_state", (torch.float32,), (B, Hkv, D, D))
-    if workspace is None:
-        workspace = _empty((lin_attn_fwd_workspace_bytes(B, T, Hkv, D),), torch.uint8, q.device, stream)
-    _req(workspace, "workspace", (torch.uint8,))
-    _call("lin_attn_fwd", library().lin_attn_fwd,
-          (q, k, v, log_decay, initial_state, lengths, o, final_state, workspace), stream, _addr(q), _addr(k), _addr(v),
-          _addr(log_decay), _addr(initial_state), _addr(lengths), _addr(o), _addr(final_state), *dims, *strides, os,
-          float(scale), _addr(workspace), workspace.numel())
+        final_state = _empty(sshape, _F32, dev, stream)
+    fin = None if final_state is None else _dense(final_state, "final_state", _F32, sshape, dev)
+    ws, wn = _workspace(workspace, lin_attn_fwd_workspace_bytes(B, T, Hkv, D), dev, stream)
+    _call("lin_attn_fwd", _fns().lin_attn_fwd, dev, stream, qp, kp, vp, ldp, s0, ln, o.data_ptr(), fin, *dims, *strides,
+          os, 1.0 / math.sqrt(D) if scale is None else float(scale), ws if ws is None else ws.data_ptr(), wn)
     return o, final_state
 
 
@@ -508,29 +541,21 @@ def lin_attn_bwd(q, k, v, dout, log_decay, scale=None, initial_state=None, dfina
     """Gradients of lin_attn_fwd: dout [B][T][Hq][D] bf16, dfinal_state
     [B][Hkv][D][D] fp32 or None.  Returns (dq, dk, dv) bf16 (given ones may be
     parts of a packed gradient) and dinitial_state fp32 or None."""
-    dims, strides = _lin_inputs(q, k, v, log_decay, initial_state, lengths)
+    dev, dims, kshape, sshape, strides, (qp, kp, vp, ldp, s0, ln) = _lin_inputs(q, k, v, log_decay, initial_state, lengths)
     B, T, Hq, Hkv, D = dims
-    bf = (torch.bfloat16,)
-    _req(dout, "dout", bf, q.shape)
-    if dfinal_state is not None:
-        _req(dfinal_state, "dfinal_state", (torch.float32,), (B, Hkv, D, D))
-    scale = 1.0 / math.sqrt(D) if scale is None else scale
-    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
-    dk = _empty(k.shape, k.dtype, k.device, stream) if dk is None else dk
-    dv = _empty(v.shape, v.dtype, v.device, stream) if dv is None else dv
-    outs = (_rows(dq, "dq", bf, q.shape), _rows(dk, "dk", bf, k.shape), _rows(dv, "dv", bf, k.shape))
+    dop = _dense(dout, "dout", _BF16, q.shape, dev)
+    dfp = None if dfinal_state is None else _dense(dfinal_state, "dfinal_state", _F32, sshape, dev)
+    dq = _empty(q.shape, _BF16, dev, stream) if dq is None else dq
+    dk = _empty(kshape, _BF16, dev, stream) if dk is None else dk
+    dv = _empty(kshape, _BF16, dev, stream) if dv is None else dv
+    outs = (_rows(dq, "dq", _BF16, q.shape, dev), _rows(dk, "dk", _BF16, kshape, dev), _rows(dv, "dv", _BF16, kshape, dev))
     if dinitial_state is None and want_dinitial_state:
-        dinitial_state = _empty((B, Hkv, D, D), torch.float32, q.device, stream)
-    if dinitial_state is not None:
-        _req(dinitial_state, "dinitial_state", (torch.float32,), (B, Hkv, D, D))
-    if workspace is None:
-        workspace = _empty((lin_attn_bwd_workspace_bytes(B, T, Hkv, D),), torch.uint8, q.device, stream)
-    _req(workspace, "workspace", (torch.uint8,))
-    _call("lin_attn_bwd", library().lin_attn_bwd,
-          (q, k, v, dout, log_decay, initial_state, dfinal_state, lengths, dq, dk, dv, dinitial_state, workspace), stream,
-          _addr(q), _addr(k), _addr(v), _addr(dout), _addr(log_decay), _addr(initial_state), _addr(dfinal_state),
-          _addr(lengths), _addr(dq), _addr(dk), _addr(dv), _addr(dinitial_state), *dims, *strides, *outs, float(scale),
-          _addr(workspace), workspace.numel())
+        dinitial_state = _empty(sshape, _F32, dev, stream)
+    dsp = None if dinitial_state is None else _dense(dinitial_state, "dinitial_state", _F32, sshape, dev)
+    ws, wn = _workspace(workspace, lin_attn_bwd_workspace_bytes(B, T, Hkv, D), dev, stream)
+    _call("lin_attn_bwd", _fns().lin_attn_bwd, dev, stream, qp, kp, vp, dop, ldp, s0, dfp, ln, dq.data_ptr(), dk.data_ptr(),
+          dv.data_ptr(), dsp, *dims, *strides, *outs, 1.0 / math.sqrt(D) if scale is None else float(scale),
+          ws if ws is None else ws.data_ptr(), wn)
     return dq, dk, dv, dinitial_state
 
 
@@ -540,25 +565,17 @@ def lin_attn_decode(q, k, v, state, log_decay, scale=None, slots=None, o=None, s
     slots [B] int32 or None: row b works on state slots[b] (None: b); a row
     whose slot is outside 0 .. n - 1 is empty (o 0, no state touched).
     Returns o [B][Hq][D] of q's dtype."""
-    dts = (torch.float32, torch.bfloat16)
-    _req(q, "q", dts)
-    _req(k, "k", (q.dtype,))
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q must be [B][Hq][D], k [B][Hkv][D]")
-    B, Hq, D = q.shape
-    Hkv = k.shape[1]
-    _req(k, "k", (q.dtype,), (B, Hkv, D))
-    _req(v, "v", (q.dtype,), k.shape)
-    _req(state, "state", (torch.float32,))
-    n = state.shape[0] if state.dim() else 0
-    _req(state, "state", (torch.float32,), (n, Hkv, D, D))
-    _req(log_decay, "log_decay", (torch.float32,), (Hkv,))
-    if slots is not None:
-        _req(slots, "slots", (torch.int32,), (B,))
-    scale = 1.0 / math.sqrt(D) if scale is None else scale
-    o = _empty(q.shape, q.dtype, q.device, stream) if o is None else o
-    _req(o, "o", (q.dtype,), q.shape)
-    _call("lin_attn_decode", library().lin_attn_decode, (q, k, v, state, log_decay, slots, o), stream, _addr(q),
-          _addr(k), _addr(v), _DT[q.dtype], _addr(state), _addr(log_decay), _addr(slots), _addr(o), B, Hq, Hkv, D, n,
-          float(scale))
+    dev = _first(q, "q", 3, (_F32, _BF16))
+    dt, qshape = q.dtype, q.shape
+    B, Hq, D = qshape
+    Hkv = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
+    n = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() == 4 else 0
+    kshape = (B, Hkv, D)
+    qp, kp, vp = (_dense(q, "q", dt, qshape, dev), _dense(k, "k", dt, kshape, dev), _dense(v, "v", dt, kshape, dev))
+    sp, lp = _dense(state, "state", _F32, (n, Hkv, D, D), dev), _dense(log_decay, "log_decay", _F32, (Hkv,), dev)
+    sl = None if slots is None else _dense(slots, "slots", torch.int32, (B,), dev)
+    o = _empty(qshape, dt, dev, stream) if o is None else o
+    _call("lin_attn_decode", _fns().lin_attn_decode, dev, stream, qp, kp, vp, _DT[dt], sp, lp, sl,
+          _dense(o, "o", dt, qshape, dev), B, Hq, Hkv, D, n,
+          1.0 / math.sqrt(D) if scale is None else float(scale))
     return o

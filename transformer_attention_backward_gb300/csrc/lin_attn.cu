@@ -30,10 +30,18 @@ namespace abw {
 namespace {
 
 constexpr int kC = 128;               // tokens per chunk
+constexpr int kSub = 64;              // tokens per TMA box: half a chunk
 
 __device__ __forceinline__ uint32_t lpack2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&v);
+}
+
+// 2^x to 2 ulp; results below the normal range are 0.
+__device__ __forceinline__ float lexp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // log2 of the decay, held above -1e30 so that 0 * log2 a is 0 for a = 0.
@@ -57,22 +65,33 @@ struct LinSizes {
 // lin_state: the recurrence over the chunks of one (batch, KV head, 64-column
 // half of the state).  Role F: X = K, Y = V, weights a^(L-1-j), chunks in
 // order.  Role R: X = Q, Y = dO of every query head of the group, weights
-// scale a^(t+1), chunks from the last to the first.
-//   U = X^T (w o Y)    M = D state rows, N = 64 columns, K = 128 tokens
+// scale a^(t+1), chunks from the last to the first.  In steps of 64 tokens:
+//   U = X^T (w o Y)    M = D state rows, N = 64 columns a term, K = 64 tokens
 // The fp32 product w o Y enters the tensor core as a sum of NS bf16 terms
 // (each the rounding of what the ones before leave): two terms are good to
 // 2^-17, which is far below the rounding of the bf16 state tiles; three are
 // good to 2^-25, for a state that leaves in fp32.  The state itself stays in
-// fp32 registers.  Warps: 0 TMA, 1 MMA, 2-9 weights, 10-13 state.
+// fp32 registers, and each step's U is added there: sums over steps or terms
+// inside the tensor core would cut off bits of the accumulator's size at every
+// one (measured: 5 times the error).
+// A step is short, so what counts is how many are under way: rings of 4 (X, Y)
+// stages with a buffer of weighted rows each, which two groups of warps fill
+// in turn, and two buffers of U.
+// Warps: 0 TMA, 1 MMA, 2-5 and 6-9 weights (even and odd steps), 10-13 state.
 // ---------------------------------------------------------------------------
 constexpr int kSThr = 448;
-constexpr int kSStage = 32768 + 16384 + 3 * 16384;   // X | Y | up to three terms of w o Y
-constexpr int kSOffBar = 2 * kSStage;
-enum { kSBarFull = 0, kSBarEmpty = 2, kSBarY = 4, kSBarU = 6, kSBarUEmpty = 8, kSBarFinal = 10, kSNumBars = 11 };
+constexpr int kSRing = 4;
+constexpr int kSStage = 3 * 8192;                    // X (two 64-column parts) | Y, 64 tokens each
+constexpr int kSOffW = kSRing * kSStage;             // weighted rows, up to three terms a buffer
+constexpr int kSOffBar = kSOffW + kSRing * 3 * 8192;
+enum {
+  kSBarFull = 0, kSBarW = kSBarFull + kSRing, kSBarDone = kSBarW + kSRing, kSBarUEmpty = kSBarDone + kSRing,
+  kSBarFinal = kSBarUEmpty + 2, kSNumBars = kSBarFinal + 1
+};
 constexpr int kSOffTmem = kSOffBar + kSNumBars * 8;
 constexpr int kSOffAbort = kSOffTmem + 4;
-constexpr int kSSmem = kSOffBar + 128 + 1024;        // + alignment slack
-static_assert(kSOffAbort + 4 <= kSOffBar + 128 && kSSmem <= 232448, "state kernel shared memory");
+constexpr int kSSmem = kSOffBar + 256 + 1024;        // + alignment slack
+static_assert(kSOffAbort + 4 <= kSOffBar + 256 && kSSmem <= 232448, "state kernel shared memory");
 
 struct LinStateParams {
   LinSizes z;
@@ -100,7 +119,7 @@ __global__ void __launch_bounds__(kSThr, 1)
   const int len = seq_len(p.z.lengths, b, p.z.T);
   const int ncb = (len + kC - 1) / kC;                        // chunks that hold tokens
   const int nst = p.end[role] ? ncb : max(ncb - 1, 0);        // chunks to add
-  const int gi = role ? p.z.G : 1;                            // (X, Y) pairs per chunk
+  const int gi = role ? 2 * p.z.G : 2;                        // steps per chunk: heads x halves
   const float l2 = log2_decay(p.z.log_decay[kv]);
   auto chunk = [&](int m) -> int { return role ? ncb - 1 - m : m; };
 
@@ -113,25 +132,31 @@ __global__ void __launch_bounds__(kSThr, 1)
     report_timeout(p.wait.err, kSiteLinState, (br - sb - kSOffBar) / 8);
     return false;
   };
-  auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return __shfl_sync(0xffffffffu, wt(br, parity), 0); };
+  // A barrier that has completed costs one access: shared memory is busy, and
+  // each access of a warp that has little else to do stands in its queue.
+  auto wtw = [&](uint32_t br, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_try_wait(br, parity)) || __shfl_sync(0xffffffffu, wt(br, parity), 0);
+  };
 
   if (tid == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kSRing; ++s) {
       mbar_init(bar(kSBarFull + s), 1);
-      mbar_init(bar(kSBarEmpty + s), 1);
-      mbar_init(bar(kSBarY + s), 256);
-      mbar_init(bar(kSBarU + s), 1);
-      mbar_init(bar(kSBarUEmpty + s), 128);
+      mbar_init(bar(kSBarW + s), 128);
+      mbar_init(bar(kSBarDone + s), 1);
     }
+    for (int s = 0; s < 2; ++s) mbar_init(bar(kSBarUEmpty + s), 128);
     mbar_init(bar(kSBarFinal), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 1) tc::tmem_alloc(sb + kSOffTmem, 128);
+  if (warp == 1) tc::tmem_alloc(sb + kSOffTmem, 512);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kSOffTmem);
+  const int steps = nst * gi;
+  // step i: tokens [64 (i & 1), 64 (i & 1) + 64) of chunk i / gi, head (i % gi) / 2
+  auto phase = [](int i) -> uint32_t { return static_cast<uint32_t>(i / kSRing) & 1u; };
 
   if (warp == 0) {
     // ============================ TMA producer ============================
@@ -140,65 +165,61 @@ __global__ void __launch_bounds__(kSThr, 1)
       prefetch_tensormap(mx);
       prefetch_tensormap(my);
       int issued = 0;
-      for (int i = 0; i < nst * gi; ++i) {
-        const int s = i & 1;
-        if (!wt(bar(kSBarEmpty + s), ((i >> 1) & 1) ^ 1)) break;
-        const int h = role ? kv * p.z.G + i % gi : kv;
-        const int t0 = chunk(i / gi) * kC;
+      for (int i = 0; i < steps; ++i) {
+        const int s = i % kSRing;
+        if (!wt(bar(kSBarDone + s), phase(i) ^ 1u)) break;
+        const int h = role ? kv * p.z.G + (i % gi) / 2 : kv;
+        const int t0 = chunk(i / gi) * kC + (i & 1) * kSub;
         const uint32_t st = sb + s * kSStage, fb = bar(kSBarFull + s);
-        mbar_arrive_expect_tx(fb, (NH + 1) * 16384);
-        for (int x = 0; x < NH; ++x) tma_load_4d(st + x * 16384, mx, x * 64, h, t0, b, fb);
-        tma_load_4d(st + 32768, my, hf * 64, h, t0, b, fb);
+        mbar_arrive_expect_tx(fb, (NH + 1) * 8192);
+        for (int x = 0; x < NH; ++x) tma_load_4d(st + x * 8192, mx, x * 64, h, t0, b, fb);
+        tma_load_4d(st + 16384, my, hf * 64, h, t0, b, fb);
         issued = i + 1;
       }
       if (*abort_flag)
-        for (int i = (issued > 2 ? issued - 2 : 0); i < issued; ++i)
-          mbar_wait_bounded(bar(kSBarFull + (i & 1)), (i >> 1) & 1, 2000000000ull);
+        for (int i = (issued > kSRing ? issued - kSRing : 0); i < issued; ++i)
+          mbar_wait_bounded(bar(kSBarFull + i % kSRing), phase(i), 2000000000ull);
     }
   } else if (warp == 1) {
     // ============================ MMA issuer ==============================
     // X is the M-major A operand.  For D = 64 rows 64-127 of A come from the
-    // unused second half of the X slot; they only reach TMEM lanes 64-127,
+    // unused second part of the X slot; they only reach TMEM lanes 64-127,
     // which nobody reads.
-    constexpr uint32_t id_u = tc::idesc_bf16_f32(128, 64, 1, 1);
-    const uint64_t dX = tc::sdesc_sw128(sb, 16384, 1024);
-    const uint64_t dY = tc::sdesc_sw128(sb + 49152, 16384, 1024);
-    for (int i = 0; i < nst * gi; ++i) {
-      const int s = i & 1;
-      if (!wtw(bar(kSBarUEmpty + s), ((i >> 1) & 1) ^ 1) || !wtw(bar(kSBarFull + s), (i >> 1) & 1) ||
-          !wtw(bar(kSBarY + s), (i >> 1) & 1))
-        break;
+    constexpr uint32_t id_u = tc::idesc_bf16_f32(128, NS * 64, 1, 1);
+    const uint64_t dX = tc::sdesc_sw128(sb, 8192, 1024);
+    const uint64_t dW = tc::sdesc_sw128(sb + kSOffW, 8192, 1024);
+    for (int i = 0; i < steps; ++i) {
+      const int s = i % kSRing, u = i & 1;
+      // (weighted rows that are there were formed from a stage that is there)
+      if (!wtw(bar(kSBarUEmpty + u), ((i >> 1) & 1) ^ 1) || !wtw(bar(kSBarW + s), phase(i))) break;
       tc::fence_after_sync();
-      const uint64_t so = static_cast<uint64_t>(s * kSStage) >> 4;
-      // the small terms first: the tensor core's additions cut off bits of
-      // the accumulator's size (measured: 5 times the error the other way)
+      const uint64_t so = static_cast<uint64_t>(s * kSStage) >> 4, wo = static_cast<uint64_t>(s * 3 * 8192) >> 4;
+      // the terms side by side as N: X is read once for all of them
 #pragma unroll
-      for (int e = NS - 1; e >= 0; --e)
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma_bf16_w(tmem + s * 64, dX + so + ((kk * 2048) >> 4), dY + so + ((e * 16384 + kk * 2048) >> 4), id_u,
-                         e < NS - 1 || kk > 0);
-      tc::commit_w(bar(kSBarEmpty + s));
-      tc::commit_w(bar(kSBarU + s));
+      for (int kk = 0; kk < 4; ++kk)
+        tc::mma_bf16_w(tmem + u * 256, dX + so + ((kk * 2048) >> 4), dW + wo + ((kk * 2048) >> 4), id_u, kk > 0);
+      // one signal for all who wait for the step: the stage and the weighted
+      // rows are free, U is there
+      tc::commit_w(bar(kSBarDone + s));
     }
     tc::commit_w(bar(kSBarFinal));
     mbar_wait_bounded(bar(kSBarFinal), 0, 2000000000ull);   // every MMA has completed
   } else if (warp < 10) {
     // ============================ weights =================================
-    const int wt_tid = tid - 64;
-    for (int i = 0; i < nst * gi; ++i) {
-      const int s = i & 1;
-      if (!wtw(bar(kSBarFull + s), (i >> 1) & 1)) break;
+    const int u = (warp - 2) >> 2, wtid = (tid - 64) & 127;
+    for (int i = u; i < steps; i += 2) {
+      const int s = i % kSRing;
+      if (!wtw(bar(kSBarFull + s), phase(i))) break;          // (loaded once step i - kSRing was done)
       const int L = min(kC, len - chunk(i / gi) * kC);
-      unsigned char *st = smem + s * kSStage;
+      unsigned char *st = smem + s * kSStage, *wb = smem + kSOffW + s * 3 * 8192;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const int id = wt_tid + 256 * c, row = id >> 3;       // 16-byte piece, token
+        const int id = wtid + 128 * c, row = (id >> 3) + u * kSub;      // 16-byte piece, token of the chunk
         uint4 out[NS];
         if (row < L) {
-          const float w = role ? p.z.scale * exp2f(l2 * static_cast<float>(row + 1))
-                               : exp2f(l2 * static_cast<float>(L - 1 - row));
-          const uint4 y = *reinterpret_cast<const uint4 *>(st + 32768 + 16 * id);
+          const float w = role ? p.z.scale * lexp2(l2 * static_cast<float>(row + 1))
+                               : lexp2(l2 * static_cast<float>(L - 1 - row));
+          const uint4 y = *reinterpret_cast<const uint4 *>(st + 16384 + 16 * id);
           const uint32_t yi[4] = {y.x, y.y, y.z, y.w};
           uint32_t o[NS][4];
 #pragma unroll
@@ -218,15 +239,15 @@ __global__ void __launch_bounds__(kSThr, 1)
           for (int t = 0; t < NS; ++t) out[t] = make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int t = 0; t < NS; ++t) *reinterpret_cast<uint4 *>(st + 49152 + t * 16384 + 16 * id) = out[t];
+        for (int t = 0; t < NS; ++t) *reinterpret_cast<uint4 *>(wb + t * 8192 + 16 * id) = out[t];
       }
       if (L < kC) {
         // rows behind the sequence may hold anything: 0 * NaN must not reach U
-        for (int id = wt_tid; id < NH * 1024; id += 256)
-          if (((id >> 3) & 127) >= L) *reinterpret_cast<uint4 *>(st + 16 * id) = make_uint4(0, 0, 0, 0);
+        for (int id = wtid; id < NH * 512; id += 128)
+          if (((id >> 3) & 63) + u * kSub >= L) *reinterpret_cast<uint4 *>(st + 16 * id) = make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async_smem();
-      mbar_arrive(bar(kSBarY + s));
+      mbar_arrive(bar(kSBarW + s));
     }
   } else {
     // ============================ state ===================================
@@ -259,22 +280,27 @@ __global__ void __launch_bounds__(kSThr, 1)
                          lpack2(S[8 * c + 4], S[8 * c + 5]), lpack2(S[8 * c + 6], S[8 * c + 7]));
       }
       if (m >= nst) break;
-      // each head's product is added in registers: sums over a group inside
-      // the tensor core would cut off bits at every step
       for (int g = 0; g < gi; ++g) {
         const int i = m * gi + g, u = i & 1;
-        if (!wtw(bar(kSBarU + u), (i >> 1) & 1)) {
+        if (!wtw(bar(kSBarDone + i % kSRing), phase(i))) {
           ok = false;
           break;
         }
         tc::fence_after_sync();
-        const float dec = g == 0 ? exp2f(l2 * static_cast<float>(min(kC, len - n * kC))) : 1.f;
+        const float dec = g == 0 ? lexp2(l2 * static_cast<float>(min(kC, len - n * kC))) : 1.f;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float v[32];
-          tc::ld32_wait(tmem + lanebase + u * 64 + x * 32, v);
+        for (int x = 0; x < 4; ++x) {
+          uint32_t at[NS], v[16 * NS];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) S[x * 32 + c] = fmaf(dec, S[x * 32 + c], v[c]);
+          for (int e = 0; e < NS; ++e) at[e] = tmem + lanebase + u * 256 + e * 64 + x * 16;
+          tc::ld16n_wait<NS>(at, v);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            float t = __uint_as_float(v[16 * (NS - 1) + c]);  // the small terms first
+#pragma unroll
+            for (int e = NS - 2; e >= 0; --e) t += __uint_as_float(v[16 * e + c]);
+            S[x * 16 + c] = fmaf(dec, S[x * 16 + c], t);
+          }
         }
         tc::fence_before_sync();
         mbar_arrive(bar(kSBarUEmpty + u));
@@ -291,7 +317,7 @@ __global__ void __launch_bounds__(kSThr, 1)
   __syncthreads();
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 128);
+    tc::tmem_dealloc(tmem, 512);
   }
 }
 
@@ -311,9 +337,13 @@ __global__ void __launch_bounds__(kSThr, 1)
 // the softmax attention), the state tile is bf16; products accumulate in fp32
 // and the two parts meet in fp32, each element rounded once on its way out.
 // TMEM: [0,256) two score / P buffers, [256,384) mask(A B^T) C, [384,512) A S.
-// Warps: 0 TMA, 1 MMA, 2-5 mask and output (thread = row).
+// Warps: 0 TMA loads, 1 MMA, 2-9 mask and output (thread = row and half of the
+// columns: what an item waits for is the length of this chain, and the halves
+// go side by side), 10 TMA stores.  The output tile is written over A, which
+// no product needs by then, and leaves from there by TMA (16-byte stores by
+// the rows' threads took 2,400 cycles of an item's 8,300).
 // ---------------------------------------------------------------------------
-constexpr int kOThr = 192;
+constexpr int kOThr = 352;
 constexpr int kOSlots = 5;            // of the ring; the two slots of A follow
 constexpr int kOSlot = 32768;
 constexpr int kOOffA = kOSlots * kOSlot;
@@ -321,7 +351,7 @@ constexpr int kOOffBar = kOOffA + 2 * kOSlot;
 enum {
   kOBarFull = 0, kOBarEmpty = kOBarFull + kOSlots, kOBarAFull = kOBarEmpty + kOSlots, kOBarAEmpty = kOBarAFull + 2,
   kOBarS = kOBarAEmpty + 2, kOBarP = kOBarS + 2,
-  kOBarO = kOBarP + 2, kOBarOEmpty = kOBarO + 1, kOBarFinal = kOBarOEmpty + 1, kONumBars = kOBarFinal + 1
+  kOBarStage = kOBarP + 2, kOBarO = kOBarStage + 2, kOBarOEmpty = kOBarO + 1, kOBarFinal = kOBarOEmpty + 1, kONumBars = kOBarFinal + 1
 };
 constexpr int kOOffTmem = kOOffBar + kONumBars * 8;
 constexpr int kOOffAbort = kOOffTmem + 4;
@@ -337,6 +367,7 @@ struct LinOutParams {
   __nv_bfloat16 *out[4];              // o, dq, dk, dv
   long long stride[4];                // elements between tokens of each output
   WaitCtl wait;
+  CUtensorMap map[4];                 // of the outputs
 };
 
 struct LinItem {
@@ -347,7 +378,7 @@ struct LinItem {
 __device__ __forceinline__ LinItem lin_item(const LinOutParams &p, int i) {
   LinItem it;
   const int NC = p.z.NC, G = p.z.G;
-  int bh, g = 0;
+  int g = 0;
   if (!p.backward) {
     it.role = 0;
     g = i % G;
@@ -367,10 +398,11 @@ __device__ __forceinline__ LinItem lin_item(const LinOutParams &p, int i) {
       i /= G;
     }
   }
+  // heads before chunks: the CTAs of one moment read whole token rows
+  it.kv = i % p.z.Hkv;
+  i /= p.z.Hkv;
   it.n = i % NC;
-  bh = i / NC;
-  it.b = bh / p.z.Hkv;
-  it.kv = bh % p.z.Hkv;
+  it.b = i / NC;
   const int len = seq_len(p.z.lengths, it.b, p.z.T);
   it.L = min(kC, len - it.n * kC);
   if (it.role < 2) {
@@ -405,7 +437,11 @@ __global__ void __launch_bounds__(kOThr, 1)
     report_timeout(p.wait.err, kSiteLinOut, (br - sb - kOOffBar) / 8);
     return false;
   };
-  auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return __shfl_sync(0xffffffffu, wt(br, parity), 0); };
+  // A barrier that has completed costs one access: shared memory is busy, and
+  // each access of a warp that has little else to do stands in its queue.
+  auto wtw = [&](uint32_t br, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_try_wait(br, parity)) || __shfl_sync(0xffffffffu, wt(br, parity), 0);
+  };
   // load number q of the ring sits in slot q % kOSlots; its phase there
   auto phase = [](int q) -> uint32_t { return static_cast<uint32_t>(q / kOSlots) & 1u; };
 
@@ -418,10 +454,11 @@ __global__ void __launch_bounds__(kOThr, 1)
       mbar_init(bar(kOBarAFull + s), 1);
       mbar_init(bar(kOBarAEmpty + s), 1);
       mbar_init(bar(kOBarS + s), 1);
-      mbar_init(bar(kOBarP + s), 128);
+      mbar_init(bar(kOBarP + s), 256);
+      mbar_init(bar(kOBarStage + s), 256);
     }
     mbar_init(bar(kOBarO), 1);
-    mbar_init(bar(kOBarOEmpty), 128);
+    mbar_init(bar(kOBarOEmpty), 256);
     mbar_init(bar(kOBarFinal), 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -447,8 +484,9 @@ __global__ void __launch_bounds__(kOThr, 1)
       auto tile = [&](const CUtensorMap *m, const LinItem &it, int h) {
         if (!ok || !slot(NH * 16384)) return;
         const int s = (q - 1) % kOSlots;
-        for (int x = 0; x < NH; ++x)
-          tma_load_4d(sb + s * kOSlot + x * 16384, m, x * 64, h, it.n * kC, it.b, bar(kOBarFull + s));
+        for (int x = 0; x < 2 * NH; ++x)
+          tma_load_4d(sb + s * kOSlot + x * 8192, m, (x >> 1) * 64, h, it.n * kC + (x & 1) * kSub, it.b,
+                      bar(kOBarFull + s));
       };
       for (int i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
         const LinItem it = lin_item(p, i);
@@ -459,8 +497,9 @@ __global__ void __launch_bounds__(kOThr, 1)
         const int as = item & 1;
         if (!wt(bar(kOBarAEmpty + as), ((item >> 1) & 1) ^ 1)) break;
         mbar_arrive_expect_tx(bar(kOBarAFull + as), NH * 16384);
-        for (int x = 0; x < NH; ++x)
-          tma_load_4d(sb + kOOffA + as * kOSlot + x * 16384, ma, x * 64, it.h, it.n * kC, it.b, bar(kOBarAFull + as));
+        for (int x = 0; x < 2 * NH; ++x)
+          tma_load_4d(sb + kOOffA + as * kOSlot + x * 8192, ma, (x >> 1) * 64, it.h, it.n * kC + (x & 1) * kSub, it.b,
+                      bar(kOBarAFull + as));
         ++item;
         for (int g = 0; g < it.gi; ++g) {
           const int hg = it.role < 2 ? it.kv : it.kv * p.z.G + g;
@@ -549,38 +588,59 @@ __global__ void __launch_bounds__(kOThr, 1)
                             g > 0 || kk > 0);
         tc::commit_w(bar(kOBarEmpty + qc % kOSlots));
       }
-      if (ok) {
-        tc::commit_w(bar(kOBarAEmpty + as));
-        tc::commit_w(bar(kOBarO));
-      }
+      if (ok) tc::commit_w(bar(kOBarO));
       q = q0 + st + 2 * it.gi;
       ss += it.gi;
       ++item;
     }
     tc::commit_w(bar(kOBarFinal));
     mbar_wait_bounded(bar(kOBarFinal), 0, 2000000000ull);   // every MMA has completed
+  } else if (warp == 10) {
+    // ============================ TMA stores ==============================
+    if (lane == 0) {
+      int item = 0;
+      for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
+        const LinItem it = lin_item(p, i);
+        if (it.L <= 0) continue;
+        const int as = item & 1;
+        if (!wt(bar(kOBarStage + as), (item >> 1) & 1)) break;
+        for (int x = 0; x < 2 * NH; ++x) {
+          const int t0 = it.n * kC + (x & 1) * kSub;
+          if (t0 < p.z.T)
+            tma_store_4d(&p.map[it.role], sb + kOOffA + as * kOSlot + x * 8192, (x >> 1) * 64, it.h, t0, it.b);
+        }
+        bulk_commit_group();
+        bulk_wait_group_read0();
+        mbar_arrive(bar(kOBarAEmpty + as));
+        ++item;
+      }
+      bulk_wait_group0();
+    }
   } else {
     // ============================ mask and output =========================
-    const int qd = warp & 3, row = 32 * qd + lane;
+    const int qd = warp & 3, row = 32 * qd + lane, hc = (warp - 2) >> 2;   // hc: half of the columns
     const uint32_t lanebase = static_cast<uint32_t>(32 * qd) << 16;
     int q = 0, ss = 0, item = 0;
     bool ok = true;
     for (int i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
       const LinItem it = lin_item(p, i);
       const int t = it.n * kC + row;
-      __nv_bfloat16 *dst = p.out[it.role] + (static_cast<size_t>(it.b) * p.z.T + t) * p.stride[it.role] + it.h * D;
       if (it.L <= 0) {                                        // rows behind the sequence
-        if (t < p.z.T)
+        if (t < p.z.T) {
+          __nv_bfloat16 *dst = p.out[it.role] + (static_cast<size_t>(it.b) * p.z.T + t) * p.stride[it.role] + it.h * D;
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4 *>(dst)[c] = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < D / 16; ++c) reinterpret_cast<uint4 *>(dst)[hc * (D / 16) + c] = make_uint4(0, 0, 0, 0);
+        }
         continue;
       }
       const bool rev = it.role >= 2;
       const float l2 = log2_decay(p.z.log_decay[it.kv]);
       const int st = it.st ? 1 : 0;
-      float pw[16];                                           // a^0 .. a^15
+      // a column's power inside a block of 16, towards its column nearest to
+      // the diagonal
+      float pw[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) pw[e] = exp2f(l2 * static_cast<float>(e));
+      for (int e = 0; e < 16; ++e) pw[e] = lexp2(l2 * static_cast<float>(rev ? e : 15 - e));
       for (int g = 0; ok && g < it.gi; ++g) {
         const int sbuf = (ss + g) & 1;
         if (!wtw(bar(kOBarS + sbuf), ((ss + g) >> 1) & 1)) {
@@ -590,7 +650,7 @@ __global__ void __launch_bounds__(kOThr, 1)
         tc::fence_after_sync();
         const uint32_t tS = tmem + lanebase + sbuf * 128;
 #pragma unroll 1
-        for (int c2 = 0; c2 < 4; ++c2) {                      // 32 columns at a time
+        for (int c2 = 2 * hc; c2 < 2 * hc + 2; ++c2) {        // 32 columns at a time
           float s[32];
           tc::ld32_wait(tS + 32 * c2, s);
           uint32_t pk[2][8];
@@ -606,11 +666,10 @@ __global__ void __launch_bounds__(kOThr, 1)
 #pragma unroll
               for (int e = 0; e < 8; ++e) pk[x][e] = 0;
             } else if (inside) {
-              const float base = p.z.scale * exp2f(l2 * static_cast<float>(rev ? c0 - row : row - c0 - 15));
+              const float base = p.z.scale * lexp2(l2 * static_cast<float>(rev ? c0 - row : row - c0 - 15));
 #pragma unroll
               for (int e = 0; e < 16; e += 2)
-                pk[x][e / 2] = rev ? lpack2(s[16 * x + e] * (base * pw[e]), s[16 * x + e + 1] * (base * pw[e + 1]))
-                                   : lpack2(s[16 * x + e] * (base * pw[15 - e]), s[16 * x + e + 1] * (base * pw[14 - e]));
+                pk[x][e / 2] = lpack2(s[16 * x + e] * (base * pw[e]), s[16 * x + e + 1] * (base * pw[e + 1]));
             } else {
 #pragma unroll
               for (int e = 0; e < 16; e += 2) {
@@ -618,7 +677,7 @@ __global__ void __launch_bounds__(kOThr, 1)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                   const int col = c0 + e + y, gap = rev ? col - row : row - col;
-                  v[y] = (gap >= 0 && col < it.L) ? s[16 * x + e + y] * (p.z.scale * exp2f(l2 * static_cast<float>(gap))) : 0.f;
+                  v[y] = (gap >= 0 && col < it.L) ? s[16 * x + e + y] * (p.z.scale * lexp2(l2 * static_cast<float>(gap))) : 0.f;
                 }
                 pk[x][e / 2] = lpack2(v[0], v[1]);
               }
@@ -633,12 +692,10 @@ __global__ void __launch_bounds__(kOThr, 1)
             ok = false;
             break;
           }
-          if (row >= it.L) {
-            unsigned char *cr = smem + (qc % kOSlots) * kOSlot + row * 128;
+          if (row >= it.L && hc < NH) {
+            unsigned char *cr = smem + (qc % kOSlots) * kOSlot + hc * 16384 + row * 128;
 #pragma unroll
-            for (int x = 0; x < NH; ++x)
-#pragma unroll
-              for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(cr + x * 16384 + 16 * e) = make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(cr + 16 * e) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
@@ -648,10 +705,11 @@ __global__ void __launch_bounds__(kOThr, 1)
       }
       if (!ok || !wtw(bar(kOBarO), item & 1)) break;
       tc::fence_after_sync();
-      const float fac = rev ? exp2f(l2 * static_cast<float>(max(it.L - 1 - row, 0)))
-                            : p.z.scale * exp2f(l2 * static_cast<float>(row + 1));
+      const float fac = rev ? lexp2(l2 * static_cast<float>(max(it.L - 1 - row, 0)))
+                            : p.z.scale * lexp2(l2 * static_cast<float>(row + 1));
+      unsigned char *stage = smem + kOOffA + (item & 1) * kOSlot + row * 128;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = hc * (D / 2); c < (hc + 1) * (D / 2); c += 32) {
         float a[32], s[32];
         if (st) {
           tc::ld32x2_wait(tmem + lanebase + 256 + c, tmem + lanebase + 384 + c, a, s);
@@ -660,18 +718,19 @@ __global__ void __launch_bounds__(kOThr, 1)
         } else {
           tc::ld32_wait(tmem + lanebase + 256 + c, a);
         }
-        if (t < p.z.T) {
-          const bool in = row < it.L;
+        // the row's 16-byte pieces, in the order of a 128-byte swizzled tile
+        const bool in = row < it.L;                           // rows behind the sequence are 0
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            reinterpret_cast<uint4 *>(dst + c)[e / 8] =
-                in ? make_uint4(lpack2(a[e], a[e + 1]), lpack2(a[e + 2], a[e + 3]), lpack2(a[e + 4], a[e + 5]),
-                                lpack2(a[e + 6], a[e + 7]))
-                   : make_uint4(0, 0, 0, 0);
-        }
+        for (int e = 0; e < 32; e += 8)
+          *reinterpret_cast<uint4 *>(stage + (c >> 6) * 16384 + ((((c & 63) + e) / 8 ^ (row & 7)) << 4)) =
+              in ? make_uint4(lpack2(a[e], a[e + 1]), lpack2(a[e + 2], a[e + 3]), lpack2(a[e + 4], a[e + 5]),
+                              lpack2(a[e + 6], a[e + 7]))
+                 : make_uint4(0, 0, 0, 0);
       }
       tc::fence_before_sync();
       mbar_arrive(bar(kOBarOEmpty));
+      fence_proxy_async_smem();
+      mbar_arrive(bar(kOBarStage + (item & 1)));
       q += st + 2 * it.gi;
       ss += it.gi;
       ++item;
@@ -798,7 +857,7 @@ bool lin_map(CUtensorMap *mp, const void *base, int D, int H, int T, int B, long
   const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(H), static_cast<uint64_t>(T),
                             static_cast<uint64_t>(B)};
   const uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, ts, ts * T};
-  const uint32_t box[4] = {64, 1, kC, 1};
+  const uint32_t box[4] = {64, 1, kSub, 1};
   return encode_tiled(mp, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
                       why);
 }
@@ -891,9 +950,11 @@ cudaError_t launch_lin_attn(const LinAttnArgs &a, const WaitCtl &w, cudaStream_t
   if (!lin_map(&tm[0], a.q, a.D, a.Hq, a.T, a.B, a.q_stride, why) ||
       !lin_map(&tm[1], a.k, a.D, a.Hkv, a.T, a.B, a.k_stride, why) ||
       !lin_map(&tm[2], a.v, a.D, a.Hkv, a.T, a.B, a.v_stride, why) ||
-      !lin_map(&tm[3], bwd ? a.dout : a.q, a.D, a.Hq, a.T, a.B, bwd ? static_cast<long long>(a.Hq) * a.D : a.q_stride,
-               why))
+      (bwd && !lin_map(&tm[3], a.dout, a.D, a.Hq, a.T, a.B, static_cast<long long>(a.Hq) * a.D, why)))
     return cudaErrorInvalidValue;
+  if (!bwd) tm[3] = tm[0];              // not read
+  for (int i = 0; i < 4; ++i)
+    if (out[i] && !lin_map(&op.map[i], out[i], a.D, i < 2 ? a.Hq : a.Hkv, a.T, a.B, os[i], why)) return cudaErrorInvalidValue;
   const bool exact = a.final_state || a.dinitial_state;   // a state leaves in fp32
   return a.D == 128 ? launch_lin<128>(tm, sp, op, exact, sms, st) : launch_lin<64>(tm, sp, op, exact, sms, st);
 }

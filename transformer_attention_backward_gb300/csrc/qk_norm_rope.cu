@@ -39,7 +39,13 @@ struct QkParams {
   float eps, inv_n;
   const int *pos;                     // [axes][ntok] or null: pos0 + t
   int axes, sec_end[4];               // first pair behind each axis' pairs
-  unsigned long long freq[kQMaxPairs];
+};
+
+// A launch's parameters are written out with it: heads of up to 128 components
+// carry a table of 64 turns, longer ones of 256 (0.5 us less per launch).
+template <int NP>
+struct QkTable : QkParams {
+  unsigned long long freq[NP];
 };
 
 template <typename T, int V>
@@ -120,7 +126,8 @@ __device__ __forceinline__ void qstore_pairs(T *row, int s, int rot, const float
 
 // cos and sin of nt tokens' angles, [nt][D / 2] each; 1 and 0 behind the
 // rotated pairs.
-__device__ __forceinline__ void fill_angles(const QkParams &p, long long tok0, int nt, float *cs, float *sn) {
+template <int NP>
+__device__ __forceinline__ void fill_angles(const QkTable<NP> &p, long long tok0, int nt, float *cs, float *sn) {
   const int h2 = p.D >> 1;
   for (int i = threadIdx.x; i < nt * h2; i += kQThr) {
     const int n = i / h2, s = i % h2;
@@ -146,9 +153,12 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
+template <int V, int L>
+constexpr int table_size() { return V == 4 && L <= 16 ? 64 : kQMaxPairs; }
+
 // N: groups of V pair slots per lane; L: lanes per row.
 template <typename XT, typename DT, bool BWD, bool INTER, int V, int N, int L>
-__global__ void __launch_bounds__(kQThr) qk_kernel(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kQThr) qk_kernel(const __grid_constant__ QkTable<table_size<V, L>()> p) {
   extern __shared__ __align__(16) float ang[];
   const int h2 = p.D >> 1;
   float *cs = ang, *sn = ang + p.tt * h2;
@@ -309,7 +319,7 @@ __global__ void __launch_bounds__(256) qk_dgamma_kernel(const float *__restrict_
 }
 
 template <typename XT, typename DT, bool BWD, bool INTER, int V, int N, int L>
-cudaError_t qk_launch(QkParams &p, int max_blocks, int sms, cudaStream_t st) {
+cudaError_t qk_launch(QkParams &p, const unsigned long long *freq, int max_blocks, int sms, cudaStream_t st) {
   // Tokens per block and step: enough rows for every row group, four times
   // over when there are tokens for all SMs.
   constexpr int kGroups = kQThr / L;
@@ -323,18 +333,37 @@ cudaError_t qk_launch(QkParams &p, int max_blocks, int sms, cudaStream_t st) {
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   size_t smem = static_cast<size_t>(tt) * p.D * 4;
   if (BWD && smem < static_cast<size_t>(kGroups) * p.D * 4) smem = static_cast<size_t>(kGroups) * p.D * 4;
-  qk_kernel<XT, DT, BWD, INTER, V, N, L><<<static_cast<unsigned>(blocks), kQThr, smem, st>>>(p);
+  QkTable<table_size<V, L>()> t;
+  static_cast<QkParams &>(t) = p;
+  for (int i = 0; i < p.rot; ++i) t.freq[i] = freq[i];
+  qk_kernel<XT, DT, BWD, INTER, V, N, L><<<static_cast<unsigned>(blocks), kQThr, smem, st>>>(t);
   p.tt = static_cast<int>(blocks);                      // for the caller: partials written
   return cudaGetLastError();
 }
 
 template <typename XT, typename DT, bool BWD, bool INTER>
-cudaError_t qk_dispatch(QkParams &p, bool vec, int max_blocks, int sms, cudaStream_t st) {
-  if (!vec) return qk_launch<XT, DT, BWD, INTER, 1, 8, 32>(p, max_blocks, sms, st);
-  if (p.D <= 64) return qk_launch<XT, DT, BWD, INTER, 4, 1, 8>(p, max_blocks, sms, st);
-  if (p.D <= 128) return qk_launch<XT, DT, BWD, INTER, 4, 1, 16>(p, max_blocks, sms, st);
-  if (p.D <= 256) return qk_launch<XT, DT, BWD, INTER, 4, 1, 32>(p, max_blocks, sms, st);
-  return qk_launch<XT, DT, BWD, INTER, 4, 2, 32>(p, max_blocks, sms, st);
+cudaError_t qk_dispatch(QkParams &p, const unsigned long long *freq, bool vec, int max_blocks, int sms, cudaStream_t st) {
+  if (!vec) return qk_launch<XT, DT, BWD, INTER, 1, 8, 32>(p, freq, max_blocks, sms, st);
+  if (p.D <= 64) return qk_launch<XT, DT, BWD, INTER, 4, 1, 8>(p, freq, max_blocks, sms, st);
+  if (p.D <= 128) return qk_launch<XT, DT, BWD, INTER, 4, 1, 16>(p, freq, max_blocks, sms, st);
+  if (p.D <= 256) return qk_launch<XT, DT, BWD, INTER, 4, 1, 32>(p, freq, max_blocks, sms, st);
+  return qk_launch<XT, DT, BWD, INTER, 4, 2, 32>(p, freq, max_blocks, sms, st);
+}
+
+// Turns per position of each pair, mod 1, as 64-bit binary fractions.  A model
+// calls with one base and size, so each thread keeps the last table it formed.
+const unsigned long long *turn_table(double base, int rotary_dim) {
+  thread_local double last_base = 0.0;
+  thread_local int last_dim = 0;
+  thread_local unsigned long long turns[kQMaxPairs];
+  if (base != last_base || rotary_dim != last_dim) {
+    for (int i = 0; i < rotary_dim / 2; ++i)
+      turns[i] = static_cast<unsigned long long>(
+          ldexp(fmod(pow(base, -2.0 * i / rotary_dim) / 6.283185307179586476925286766559, 1.0), 64));
+    last_base = base;
+    last_dim = rotary_dim;
+  }
+  return turns;
 }
 
 bool at16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -374,33 +403,29 @@ cudaError_t launch_qk_norm_rope(const QkNormRopeArgs &a, cudaStream_t st) {
     end += i < a.n_axes ? a.sections[i] : 0;
     p.sec_end[i] = end;
   }
-  for (int i = 0; i < kQMaxPairs; ++i) {
-    double turns = 0.0;
-    if (i < rot) turns = fmod(pow(a.base, -2.0 * i / a.rotary_dim) / 6.283185307179586476925286766559, 1.0);
-    p.freq[i] = static_cast<unsigned long long>(ldexp(turns, 64));
-  }
+  const unsigned long long *freq = turn_table(a.base, a.rotary_dim);
   if (p.ntok > 0) {
     if (!bwd) {
       if (a.bf16)
-        e = a.interleaved ? qk_dispatch<__nv_bfloat16, float, false, true>(p, vec, 0, sms, st)
-                          : qk_dispatch<__nv_bfloat16, float, false, false>(p, vec, 0, sms, st);
+        e = a.interleaved ? qk_dispatch<__nv_bfloat16, float, false, true>(p, freq, vec, 0, sms, st)
+                          : qk_dispatch<__nv_bfloat16, float, false, false>(p, freq, vec, 0, sms, st);
       else
-        e = a.interleaved ? qk_dispatch<float, float, false, true>(p, vec, 0, sms, st)
-                          : qk_dispatch<float, float, false, false>(p, vec, 0, sms, st);
+        e = a.interleaved ? qk_dispatch<float, float, false, true>(p, freq, vec, 0, sms, st)
+                          : qk_dispatch<float, float, false, false>(p, freq, vec, 0, sms, st);
       return e;
     }
     const int most = kQkParts < 4 * sms ? kQkParts : 4 * sms;
     const int how = (a.bf16 ? 4 : 0) | (a.dy_bf16 ? 2 : 0) | (a.interleaved ? 1 : 0);
     using bf = __nv_bfloat16;
     switch (how) {
-      case 0: e = qk_dispatch<float, float, true, false>(p, vec, most, sms, st); break;
-      case 1: e = qk_dispatch<float, float, true, true>(p, vec, most, sms, st); break;
-      case 2: e = qk_dispatch<float, bf, true, false>(p, vec, most, sms, st); break;
-      case 3: e = qk_dispatch<float, bf, true, true>(p, vec, most, sms, st); break;
-      case 4: e = qk_dispatch<bf, float, true, false>(p, vec, most, sms, st); break;
-      case 5: e = qk_dispatch<bf, float, true, true>(p, vec, most, sms, st); break;
-      case 6: e = qk_dispatch<bf, bf, true, false>(p, vec, most, sms, st); break;
-      default: e = qk_dispatch<bf, bf, true, true>(p, vec, most, sms, st); break;
+      case 0: e = qk_dispatch<float, float, true, false>(p, freq, vec, most, sms, st); break;
+      case 1: e = qk_dispatch<float, float, true, true>(p, freq, vec, most, sms, st); break;
+      case 2: e = qk_dispatch<float, bf, true, false>(p, freq, vec, most, sms, st); break;
+      case 3: e = qk_dispatch<float, bf, true, true>(p, freq, vec, most, sms, st); break;
+      case 4: e = qk_dispatch<bf, float, true, false>(p, freq, vec, most, sms, st); break;
+      case 5: e = qk_dispatch<bf, float, true, true>(p, freq, vec, most, sms, st); break;
+      case 6: e = qk_dispatch<bf, bf, true, false>(p, freq, vec, most, sms, st); break;
+      default: e = qk_dispatch<bf, bf, true, true>(p, freq, vec, most, sms, st); break;
     }
     if (e != cudaSuccess || !p.part) return e;
     qk_dgamma_kernel<<<(2 * a.D + 31) / 32, 256, 0, st>>>(p.part, a.dgamma[0], a.dgamma[1], p.tt, a.D);
