@@ -62,36 +62,43 @@ struct LinSizes {
 };
 
 // ---------------------------------------------------------------------------
-// lin_state: the recurrence over the chunks of one (batch, KV head, 64-column
-// half of the state).  Role F: X = K, Y = V, weights a^(L-1-j), chunks in
-// order.  Role R: X = Q, Y = dO of every query head of the group, weights
+// lin_state: the recurrence over the chunks of one (batch, KV head, 32 columns
+// of the state).  Role F: X = K, Y = V, weights a^(L-1-j), chunks in order.
+// Role R: X = Q, Y = dO of every query head of the group, weights
 // scale a^(t+1), chunks from the last to the first.  In steps of 64 tokens:
-//   U = X^T (w o Y)    M = D state rows, N = 64 columns a term, K = 64 tokens
+//   U = X^T (w o Y)    M = D state rows, N = 32 columns a term, K = 64 tokens
 // The fp32 product w o Y enters the tensor core as a sum of NS bf16 terms
-// (each the rounding of what the ones before leave): two terms are good to
-// 2^-17, which is far below the rounding of the bf16 state tiles; three are
-// good to 2^-25, for a state that leaves in fp32.  The state itself stays in
-// fp32 registers, and each step's U is added there: sums over steps or terms
-// inside the tensor core would cut off bits of the accumulator's size at every
-// one (measured: 5 times the error).
-// A step is short, so what counts is how many are under way: rings of 4 (X, Y)
-// stages with a buffer of weighted rows each, which two groups of warps fill
-// in turn, and two buffers of U.
+// (each the rounding of what the ones before leave), side by side as N: two
+// terms are good to 2^-17, which is far below the rounding of the bf16 state
+// tiles; three are good to 2^-25, for a state that leaves in fp32.  The state
+// itself stays in fp32 registers, and each step's U is added there: sums over
+// steps or terms inside the tensor core would cut off bits of the
+// accumulator's size at every one (measured: 5 times the error).
+// The chain of a step (load, weights, product, addition) is long and the work
+// in it small, so what counts is how many steps are under way: a ring of
+// (X, Y, weighted rows) slots as deep as shared memory allows, filled in turn by
+// two groups of warps, and two buffers of U.  32 columns, not 64: X is read by
+// twice as many CTAs (from L2), but a step moves 2/3 of the bytes through shared
+// memory and there are twice as many chains: 8192 tokens of 32 heads 59 us
+// against 103, 640 chains of 2048 tokens 83 against 83.
 // Warps: 0 TMA, 1 MMA, 2-5 and 6-9 weights (even and odd steps), 10-13 state.
 // ---------------------------------------------------------------------------
 constexpr int kSThr = 448;
-constexpr int kSRing = 4;
-constexpr int kSStage = 3 * 8192;                    // X (two 64-column parts) | Y, 64 tokens each
-constexpr int kSOffW = kSRing * kSStage;             // weighted rows, up to three terms a buffer
-constexpr int kSOffBar = kSOffW + kSRing * 3 * 8192;
-enum {
-  kSBarFull = 0, kSBarW = kSBarFull + kSRing, kSBarDone = kSBarW + kSRing, kSBarUEmpty = kSBarDone + kSRing,
-  kSBarFinal = kSBarUEmpty + 2, kSNumBars = kSBarFinal + 1
+constexpr int kCW = 32;
+
+// A slot: X (two 64-column parts of 8 KB) | Y (64 columns, of which a CTA uses
+// half) | weighted rows (two terms of 32 columns to an 8 KB part).
+template <int NS>
+struct StateShape {
+  static constexpr int kN = NS == 3 ? 128 : 64;      // columns of U (with three terms the last 32 are unused)
+  static constexpr int kSlot = 3 * 8192 + kN / 64 * 8192;
+  static constexpr int kRing = 212992 / kSlot;
+  static constexpr int kFull = 0, kW = kRing, kDone = 2 * kRing, kUEmpty = 3 * kRing, kFinal = kUEmpty + 2;
+  static constexpr int kOffBar = kRing * kSlot;
+  static constexpr int kOffTmem = kOffBar + (kFinal + 1) * 8, kOffAbort = kOffTmem + 4;
+  static constexpr int kSmem = kOffBar + 256 + 1024;                   // + alignment slack
+  static_assert(kOffAbort + 4 <= kOffBar + 256 && kSmem <= 232448, "state kernel shared memory");
 };
-constexpr int kSOffTmem = kSOffBar + kSNumBars * 8;
-constexpr int kSOffAbort = kSOffTmem + 4;
-constexpr int kSSmem = kSOffBar + 256 + 1024;        // + alignment slack
-static_assert(kSOffAbort + 4 <= kSOffBar + 256 && kSSmem <= 232448, "state kernel shared memory");
 
 struct LinStateParams {
   LinSizes z;
@@ -111,8 +118,9 @@ __global__ void __launch_bounds__(kSThr, 1)
   unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int NH = D / 64;
-  const int hf = blockIdx.x % NH, unit = blockIdx.x / NH;
+  using Z = StateShape<NS>;
+  constexpr int NH = D / 64, NP = D / kCW;
+  const int part = blockIdx.x % NP, unit = blockIdx.x / NP;   // kCW columns of the state
   const int nbh = p.z.B * p.z.Hkv;
   const int role = p.first_role + unit / nbh, bh = unit % nbh;
   const int b = bh / p.z.Hkv, kv = bh % p.z.Hkv;
@@ -123,13 +131,13 @@ __global__ void __launch_bounds__(kSThr, 1)
   const float l2 = log2_decay(p.z.log_decay[kv]);
   auto chunk = [&](int m) -> int { return role ? ncb - 1 - m : m; };
 
-  auto bar = [&](int i) -> uint32_t { return sb + kSOffBar + i * 8; };
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kSOffAbort);
+  auto bar = [&](int i) -> uint32_t { return sb + Z::kOffBar + i * 8; };
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Z::kOffAbort);
   auto wt = [&](uint32_t br, uint32_t parity) -> bool {
     if (*abort_flag) return false;
     if (mbar_wait_bounded(br, parity, p.wait.limit_ns)) return true;
     *abort_flag = 1;
-    report_timeout(p.wait.err, kSiteLinState, (br - sb - kSOffBar) / 8);
+    report_timeout(p.wait.err, kSiteLinState, (br - sb - Z::kOffBar) / 8);
     return false;
   };
   // A barrier that has completed costs one access: shared memory is busy, and
@@ -139,24 +147,24 @@ __global__ void __launch_bounds__(kSThr, 1)
   };
 
   if (tid == 0) {
-    for (int s = 0; s < kSRing; ++s) {
-      mbar_init(bar(kSBarFull + s), 1);
-      mbar_init(bar(kSBarW + s), 128);
-      mbar_init(bar(kSBarDone + s), 1);
+    for (int s = 0; s < Z::kRing; ++s) {
+      mbar_init(bar(Z::kFull + s), 1);
+      mbar_init(bar(Z::kW + s), 128);
+      mbar_init(bar(Z::kDone + s), 1);
     }
-    for (int s = 0; s < 2; ++s) mbar_init(bar(kSBarUEmpty + s), 128);
-    mbar_init(bar(kSBarFinal), 1);
+    for (int s = 0; s < 2; ++s) mbar_init(bar(Z::kUEmpty + s), 128);
+    mbar_init(bar(Z::kFinal), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
-  if (warp == 1) tc::tmem_alloc(sb + kSOffTmem, 512);
+  if (warp == 1) tc::tmem_alloc(sb + Z::kOffTmem, 512);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kSOffTmem);
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + Z::kOffTmem);
   const int steps = nst * gi;
   // step i: tokens [64 (i & 1), 64 (i & 1) + 64) of chunk i / gi, head (i % gi) / 2
-  auto phase = [](int i) -> uint32_t { return static_cast<uint32_t>(i / kSRing) & 1u; };
+  auto phase = [](int i) -> uint32_t { return static_cast<uint32_t>(i / Z::kRing) & 1u; };
 
   if (warp == 0) {
     // ============================ TMA producer ============================
@@ -165,61 +173,63 @@ __global__ void __launch_bounds__(kSThr, 1)
       prefetch_tensormap(mx);
       prefetch_tensormap(my);
       int issued = 0;
-      for (int i = 0; i < steps; ++i) {
-        const int s = i % kSRing;
-        if (!wt(bar(kSBarDone + s), phase(i) ^ 1u)) break;
-        const int h = role ? kv * p.z.G + (i % gi) / 2 : kv;
-        const int t0 = chunk(i / gi) * kC + (i & 1) * kSub;
-        const uint32_t st = sb + s * kSStage, fb = bar(kSBarFull + s);
+      for (int i = 0, s = 0, ph = 1, m = 0, g = 0; i < steps; ++i) {
+        if (!wt(bar(Z::kDone + s), ph)) break;
+        const int h = role ? kv * p.z.G + g / 2 : kv, t0 = chunk(m) * kC + (g & 1) * kSub;
+        const uint32_t st = sb + s * Z::kSlot, fb = bar(Z::kFull + s);
         mbar_arrive_expect_tx(fb, (NH + 1) * 8192);
         for (int x = 0; x < NH; ++x) tma_load_4d(st + x * 8192, mx, x * 64, h, t0, b, fb);
-        tma_load_4d(st + 16384, my, hf * 64, h, t0, b, fb);
+        tma_load_4d(st + 16384, my, part / 2 * 64, h, t0, b, fb);
         issued = i + 1;
+        if (++g == gi) g = 0, ++m;
+        if (++s == Z::kRing) s = 0, ph ^= 1;
       }
       if (*abort_flag)
-        for (int i = (issued > kSRing ? issued - kSRing : 0); i < issued; ++i)
-          mbar_wait_bounded(bar(kSBarFull + i % kSRing), phase(i), 2000000000ull);
+        for (int i = (issued > Z::kRing ? issued - Z::kRing : 0); i < issued; ++i)
+          mbar_wait_bounded(bar(Z::kFull + i % Z::kRing), phase(i), 2000000000ull);
     }
   } else if (warp == 1) {
     // ============================ MMA issuer ==============================
     // X is the M-major A operand.  For D = 64 rows 64-127 of A come from the
     // unused second part of the X slot; they only reach TMEM lanes 64-127,
     // which nobody reads.
-    constexpr uint32_t id_u = tc::idesc_bf16_f32(128, NS * 64, 1, 1);
+    constexpr uint32_t id_u = tc::idesc_bf16_f32(128, Z::kN, 1, 1);
     const uint64_t dX = tc::sdesc_sw128(sb, 8192, 1024);
-    const uint64_t dW = tc::sdesc_sw128(sb + kSOffW, 8192, 1024);
-    for (int i = 0; i < steps; ++i) {
-      const int s = i % kSRing, u = i & 1;
+    const uint64_t dW = tc::sdesc_sw128(sb + 24576, 8192, 1024);
+    for (int i = 0, s = 0, ph = 0; i < steps; ++i) {
+      const int u = i & 1;
       // (weighted rows that are there were formed from a stage that is there)
-      if (!wtw(bar(kSBarUEmpty + u), ((i >> 1) & 1) ^ 1) || !wtw(bar(kSBarW + s), phase(i))) break;
+      if (!wtw(bar(Z::kUEmpty + u), ((i >> 1) & 1) ^ 1) || !wtw(bar(Z::kW + s), ph)) break;
       tc::fence_after_sync();
-      const uint64_t so = static_cast<uint64_t>(s * kSStage) >> 4, wo = static_cast<uint64_t>(s * 3 * 8192) >> 4;
+      const uint64_t so = static_cast<uint64_t>(s * Z::kSlot) >> 4;
       // the terms side by side as N: X is read once for all of them
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        tc::mma_bf16_w(tmem + u * 256, dX + so + ((kk * 2048) >> 4), dW + wo + ((kk * 2048) >> 4), id_u, kk > 0);
+        tc::mma_bf16_w(tmem + u * 256, dX + so + ((kk * 2048) >> 4), dW + so + ((kk * 2048) >> 4), id_u, kk > 0);
       // one signal for all who wait for the step: the stage and the weighted
       // rows are free, U is there
-      tc::commit_w(bar(kSBarDone + s));
+      tc::commit_w(bar(Z::kDone + s));
+      if (++s == Z::kRing) s = 0, ph ^= 1;
     }
-    tc::commit_w(bar(kSBarFinal));
-    mbar_wait_bounded(bar(kSBarFinal), 0, 2000000000ull);   // every MMA has completed
+    tc::commit_w(bar(Z::kFinal));
+    mbar_wait_bounded(bar(Z::kFinal), 0, 2000000000ull);   // every MMA has completed
   } else if (warp < 10) {
     // ============================ weights =================================
     const int u = (warp - 2) >> 2, wtid = (tid - 64) & 127;
-    for (int i = u; i < steps; i += 2) {
-      const int s = i % kSRing;
-      if (!wtw(bar(kSBarFull + s), phase(i))) break;          // (loaded once step i - kSRing was done)
-      const int L = min(kC, len - chunk(i / gi) * kC);
-      unsigned char *st = smem + s * kSStage, *wb = smem + kSOffW + s * 3 * 8192;
+    for (int i = u, s = u, ph = 0, m = 0, g = 0; i < steps; i += 2) {
+      if (!wtw(bar(Z::kFull + s), ph)) break;                 // (loaded once the slot's last step was done)
+      const int L = min(kC, len - chunk(m) * kC);
+      unsigned char *st = smem + s * Z::kSlot;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int id = wtid + 128 * c, row = (id >> 3) + u * kSub;      // 16-byte piece, token of the chunk
+      for (int c = 0; c < kCW / 16; ++c) {
+        // 16-byte piece j of the row of token `row` of the chunk
+        const int id = wtid + 128 * c, r = id >> 2, j = id & 3, row = r + u * kSub;
         uint4 out[NS];
         if (row < L) {
           const float w = role ? p.z.scale * lexp2(l2 * static_cast<float>(row + 1))
                                : lexp2(l2 * static_cast<float>(L - 1 - row));
-          const uint4 y = *reinterpret_cast<const uint4 *>(st + 16384 + 16 * id);
+          const uint4 y = *reinterpret_cast<const uint4 *>(
+              st + 16384 + r * 128 + ((((part & 1) * 4 + j) ^ (r & 7)) << 4));
           const uint32_t yi[4] = {y.x, y.y, y.z, y.w};
           uint32_t o[NS][4];
 #pragma unroll
@@ -239,7 +249,8 @@ __global__ void __launch_bounds__(kSThr, 1)
           for (int t = 0; t < NS; ++t) out[t] = make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int t = 0; t < NS; ++t) *reinterpret_cast<uint4 *>(wb + t * 8192 + 16 * id) = out[t];
+        for (int t = 0; t < NS; ++t)
+          *reinterpret_cast<uint4 *>(st + 24576 + (t >> 1) * 8192 + r * 128 + ((((t & 1) * 4 + j) ^ (r & 7)) << 4)) = out[t];
       }
       if (L < kC) {
         // rows behind the sequence may hold anything: 0 * NaN must not reach U
@@ -247,52 +258,54 @@ __global__ void __launch_bounds__(kSThr, 1)
           if (((id >> 3) & 63) + u * kSub >= L) *reinterpret_cast<uint4 *>(st + 16 * id) = make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async_smem();
-      mbar_arrive(bar(kSBarW + s));
+      mbar_arrive(bar(Z::kW + s));
+      if ((s += 2) >= Z::kRing) s -= Z::kRing, ph ^= 1;
+      if ((g += 2) == gi) g = 0, ++m;
     }
   } else {
     // ============================ state ===================================
     const int qd = warp & 3, row = 32 * qd + lane;            // TMEM lane quarter, state row
     const uint32_t lanebase = static_cast<uint32_t>(32 * qd) << 16;
     const bool live = row < D;
-    const size_t at = (static_cast<size_t>(bh) * D + row) * D + hf * 64;
-    float S[64];
+    const size_t at = (static_cast<size_t>(bh) * D + row) * D + part * kCW;
+    float S[kCW];
 #pragma unroll
-    for (int c = 0; c < 64; ++c) S[c] = 0.f;
+    for (int c = 0; c < kCW; ++c) S[c] = 0.f;
     if (live && p.start[role]) {
       const float4 *src = reinterpret_cast<const float4 *>(p.start[role] + at);
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
+      for (int c = 0; c < kCW / 4; ++c) {
         const float4 v = src[c];
         S[4 * c] = v.x, S[4 * c + 1] = v.y, S[4 * c + 2] = v.z, S[4 * c + 3] = v.w;
       }
     }
     bool ok = true;
+    int s = 0, ph = 0, u = 0;
     for (int m = 0; m < ncb; ++m) {
       const int n = chunk(m);
       if (live && p.tiles[role] && (m > 0 || p.start[role])) {
-        // the row's 128 bytes, in the order of a 128-byte swizzled tile
+        // the row's part, in the order of a 128-byte swizzled tile
         unsigned char *dst = reinterpret_cast<unsigned char *>(p.tiles[role]) +
-                             (static_cast<size_t>(bh) * p.z.NC + n) * (D * D * 2) + hf * (D * 128) + row * 128;
+                             (static_cast<size_t>(bh) * p.z.NC + n) * (D * D * 2) + part / 2 * (D * 128) + row * 128;
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4 *>(dst + ((c ^ (row & 7)) << 4)) =
+        for (int c = 0; c < kCW / 8; ++c)
+          *reinterpret_cast<uint4 *>(dst + ((((part & 1) * 4 + c) ^ (row & 7)) << 4)) =
               make_uint4(lpack2(S[8 * c], S[8 * c + 1]), lpack2(S[8 * c + 2], S[8 * c + 3]),
                          lpack2(S[8 * c + 4], S[8 * c + 5]), lpack2(S[8 * c + 6], S[8 * c + 7]));
       }
       if (m >= nst) break;
       for (int g = 0; g < gi; ++g) {
-        const int i = m * gi + g, u = i & 1;
-        if (!wtw(bar(kSBarDone + i % kSRing), phase(i))) {
+        if (!wtw(bar(Z::kDone + s), ph)) {
           ok = false;
           break;
         }
         tc::fence_after_sync();
         const float dec = g == 0 ? lexp2(l2 * static_cast<float>(min(kC, len - n * kC))) : 1.f;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < kCW / 16; ++x) {
           uint32_t at[NS], v[16 * NS];
 #pragma unroll
-          for (int e = 0; e < NS; ++e) at[e] = tmem + lanebase + u * 256 + e * 64 + x * 16;
+          for (int e = 0; e < NS; ++e) at[e] = tmem + lanebase + u * 256 + e * kCW + x * 16;
           tc::ld16n_wait<NS>(at, v);
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
@@ -303,14 +316,16 @@ __global__ void __launch_bounds__(kSThr, 1)
           }
         }
         tc::fence_before_sync();
-        mbar_arrive(bar(kSBarUEmpty + u));
+        mbar_arrive(bar(Z::kUEmpty + u));
+        u ^= 1;
+        if (++s == Z::kRing) s = 0, ph ^= 1;
       }
       if (!ok) break;
     }
     if (ok && live && p.end[role]) {
       float4 *dst = reinterpret_cast<float4 *>(p.end[role] + at);
 #pragma unroll
-      for (int c = 0; c < 16; ++c) dst[c] = make_float4(S[4 * c], S[4 * c + 1], S[4 * c + 2], S[4 * c + 3]);
+      for (int c = 0; c < kCW / 4; ++c) dst[c] = make_float4(S[4 * c], S[4 * c + 1], S[4 * c + 2], S[4 * c + 3]);
     }
   }
   tc::fence_before_sync();
@@ -863,11 +878,13 @@ bool lin_map(CUtensorMap *mp, const void *base, int D, int H, int T, int B, long
 }
 
 template <int D, int NS>
-cudaError_t launch_state(const CUtensorMap (&tm)[4], const LinStateParams &p, unsigned grid, cudaStream_t st) {
+cudaError_t launch_state(const CUtensorMap (&tm)[4], const LinStateParams &p, cudaStream_t st) {
   const auto kern = lin_state_kernel<D, NS>;
-  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), kSSmem);
+  constexpr int smem = StateShape<NS>::kSmem;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kSThr, kSSmem, st>>>(tm[0], tm[1], tm[2], tm[3], p);
+  const unsigned grid = static_cast<unsigned>(p.nroles) * p.z.B * p.z.Hkv * (D / kCW);
+  kern<<<grid, kSThr, smem, st>>>(tm[0], tm[1], tm[2], tm[3], p);
   return cudaGetLastError();
 }
 
@@ -876,8 +893,7 @@ cudaError_t launch_lin(const CUtensorMap (&tm)[4], const LinStateParams &sp, con
                        int sms, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (sp.nroles) {
-    const unsigned grid = static_cast<unsigned>(sp.nroles) * sp.z.B * sp.z.Hkv * (D / 64);
-    e = exact ? launch_state<D, 3>(tm, sp, grid, st) : launch_state<D, 2>(tm, sp, grid, st);
+    e = exact ? launch_state<D, 3>(tm, sp, st) : launch_state<D, 2>(tm, sp, st);
     if (e != cudaSuccess) return e;
   }
   const auto kern = lin_out_kernel<D>;
@@ -913,7 +929,7 @@ cudaError_t launch_lin_attn(const LinAttnArgs &a, const WaitCtl &w, cudaStream_t
   op.z.lengths = a.lengths;
   op.backward = bwd;
   const long long items = static_cast<long long>(a.B) * op.z.NC * (bwd ? a.Hq + 2LL * a.Hkv : a.Hq);
-  if (items > 0x7ffffff0LL - sms || 4LL * a.B * a.Hkv > 0x7fffffffLL) {
+  if (items > 0x7ffffff0LL - sms || 8LL * a.B * a.Hkv > 0x7fffffffLL) {
     *why = "grid too large";
     return cudaErrorNotSupported;
   }
