@@ -54,6 +54,35 @@ __device__ __forceinline__ int seq_len(const int *lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;
 }
 
+// Waits of the two tensor-core kernels.  A barrier that has completed costs one
+// access (shared memory is busy, and each access of a warp that has little
+// else to do stands in its queue).  The rest is out of line: the kernels' warps
+// run different code side by side, and what they execute per step has to stay
+// in the instruction cache.
+struct LinWait {
+  WaitCtl ctl;
+  uint32_t bars;                      // shared address of barrier 0
+  volatile int *abort_flag;           // set by the first wait that runs out; all others then return
+  unsigned int kernel;
+
+  __device__ __forceinline__ uint32_t bar(int i) const { return bars + i * 8; }
+  __device__ __noinline__ bool slow(uint32_t br, uint32_t parity) const {
+    if (*abort_flag) return false;
+    if (mbar_wait_bounded(br, parity, ctl.limit_ns)) return true;
+    *abort_flag = 1;
+    report_timeout(ctl.err, kernel, (br - bars) / 8);
+    return false;
+  }
+  // one thread, or each lane for its own barrier
+  __device__ __forceinline__ bool one(uint32_t br, uint32_t parity) const {
+    return mbar_try_wait(br, parity) || slow(br, parity);
+  }
+  // a whole warp
+  __device__ __forceinline__ bool warp(uint32_t br, uint32_t parity) const {
+    return __all_sync(0xffffffffu, mbar_try_wait(br, parity)) || __all_sync(0xffffffffu, slow(br, parity));
+  }
+};
+
 struct LinSizes {
   int B, T, Hq, Hkv, G, NC;
   float scale;
@@ -131,20 +160,11 @@ __global__ void __launch_bounds__(kSThr, 1)
   const float l2 = log2_decay(p.z.log_decay[kv]);
   auto chunk = [&](int m) -> int { return role ? ncb - 1 - m : m; };
 
-  auto bar = [&](int i) -> uint32_t { return sb + Z::kOffBar + i * 8; };
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Z::kOffAbort);
-  auto wt = [&](uint32_t br, uint32_t parity) -> bool {
-    if (*abort_flag) return false;
-    if (mbar_wait_bounded(br, parity, p.wait.limit_ns)) return true;
-    *abort_flag = 1;
-    report_timeout(p.wait.err, kSiteLinState, (br - sb - Z::kOffBar) / 8);
-    return false;
-  };
-  // A barrier that has completed costs one access: shared memory is busy, and
-  // each access of a warp that has little else to do stands in its queue.
-  auto wtw = [&](uint32_t br, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_try_wait(br, parity)) || __shfl_sync(0xffffffffu, wt(br, parity), 0);
-  };
+  const LinWait lw{p.wait, sb + Z::kOffBar, abort_flag, kSiteLinState};
+  auto bar = [&](int i) -> uint32_t { return lw.bar(i); };
+  auto wt = [&](uint32_t br, uint32_t parity) -> bool { return lw.one(br, parity); };
+  auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return lw.warp(br, parity); };
 
   if (tid == 0) {
     for (int s = 0; s < Z::kRing; ++s) {
@@ -390,7 +410,7 @@ struct LinItem {
   bool st;                            // has a state tile
 };
 
-__device__ __forceinline__ LinItem lin_item(const LinOutParams &p, int i) {
+__device__ __noinline__ LinItem lin_item(const LinOutParams &p, int i) {
   LinItem it;
   const int NC = p.z.NC, G = p.z.G;
   int g = 0;
@@ -443,20 +463,11 @@ __global__ void __launch_bounds__(kOThr, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int NH = D / 64;
 
-  auto bar = [&](int i) -> uint32_t { return sb + kOOffBar + i * 8; };
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOOffAbort);
-  auto wt = [&](uint32_t br, uint32_t parity) -> bool {
-    if (*abort_flag) return false;
-    if (mbar_wait_bounded(br, parity, p.wait.limit_ns)) return true;
-    *abort_flag = 1;
-    report_timeout(p.wait.err, kSiteLinOut, (br - sb - kOOffBar) / 8);
-    return false;
-  };
-  // A barrier that has completed costs one access: shared memory is busy, and
-  // each access of a warp that has little else to do stands in its queue.
-  auto wtw = [&](uint32_t br, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_try_wait(br, parity)) || __shfl_sync(0xffffffffu, wt(br, parity), 0);
-  };
+  const LinWait lw{p.wait, sb + kOOffBar, abort_flag, kSiteLinOut};
+  auto bar = [&](int i) -> uint32_t { return lw.bar(i); };
+  auto wt = [&](uint32_t br, uint32_t parity) -> bool { return lw.one(br, parity); };
+  auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return lw.warp(br, parity); };
   // load number q of the ring sits in slot q % kOSlots; its phase there
   auto phase = [](int q) -> uint32_t { return static_cast<uint32_t>(q / kOSlots) & 1u; };
 
@@ -651,8 +662,10 @@ __global__ void __launch_bounds__(kOThr, 1)
       const bool rev = it.role >= 2;
       const float l2 = log2_decay(p.z.log_decay[it.kv]);
       const int st = it.st ? 1 : 0;
-      // a column's power inside a block of 16, towards its column nearest to
-      // the diagonal
+      // Inside a block of 16 columns a weight is a power for the row times
+      // one for the column (pw).  Next to the diagonal the row's is above 1,
+      // up to a^-31; where that could overflow each weight is formed by itself.
+      const bool mild = l2 > -3.8f;
       float pw[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) pw[e] = lexp2(l2 * static_cast<float>(rev ? e : 15 - e));
@@ -664,41 +677,44 @@ __global__ void __launch_bounds__(kOThr, 1)
         }
         tc::fence_after_sync();
         const uint32_t tS = tmem + lanebase + sbuf * 128;
+        // A short loop over blocks of 16 columns: what all warps run over and
+        // over stays in the instruction cache (unrolled, blocks on the
+        // diagonal took 2,000 cycles).
 #pragma unroll 1
-        for (int c2 = 2 * hc; c2 < 2 * hc + 2; ++c2) {        // 32 columns at a time
-          float s[32];
-          tc::ld32_wait(tS + 32 * c2, s);
-          uint32_t pk[2][8];
+        for (int c0 = 64 * hc; c0 < 64 * hc + 64; c0 += 16) {
+          const bool inside = rev ? (c0 >= 32 * qd + 31 && c0 + 16 <= it.L) : c0 + 15 <= 32 * qd;
+          const bool outside = rev ? c0 + 15 < 32 * qd : c0 > 32 * qd + 31;
+          uint32_t pk[8];
+          if (outside) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int c0 = 32 * c2 + 16 * x;
-            // distance from the column block's nearest column to the warp's
-            // rows: whole blocks inside the mask factor into a power per row
-            // and a power per column
-            const bool inside = rev ? (c0 >= 32 * qd + 31 && c0 + 16 <= it.L) : c0 + 15 <= 32 * qd;
-            const bool outside = rev ? c0 + 15 < 32 * qd : c0 > 32 * qd + 31;
-            if (outside) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) pk[x][e] = 0;
-            } else if (inside) {
+            for (int e = 0; e < 8; ++e) pk[e] = 0;
+          } else {
+            uint32_t sr[16];
+            float v[16];
+            tc::ld16_wait(tS + c0, sr);
+            if (inside || mild) {
               const float base = p.z.scale * lexp2(l2 * static_cast<float>(rev ? c0 - row : row - c0 - 15));
 #pragma unroll
-              for (int e = 0; e < 16; e += 2)
-                pk[x][e / 2] = lpack2(s[16 * x + e] * (base * pw[e]), s[16 * x + e + 1] * (base * pw[e + 1]));
+              for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(sr[e]) * (base * pw[e]);
             } else {
 #pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                float v[2];
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  const int col = c0 + e + y, gap = rev ? col - row : row - col;
-                  v[y] = (gap >= 0 && col < it.L) ? s[16 * x + e + y] * (p.z.scale * lexp2(l2 * static_cast<float>(gap))) : 0.f;
-                }
-                pk[x][e / 2] = lpack2(v[0], v[1]);
+              for (int e = 0; e < 16; ++e) {
+                const int gap = rev ? c0 + e - row : row - c0 - e;
+                v[e] = __uint_as_float(sr[e]) * (p.z.scale * lexp2(l2 * static_cast<float>(gap)));
               }
             }
+            if (!inside) {
+              // columns of the block that count: from row on, or up to it
+              const int lo = rev ? row - c0 : 0, hi = min(rev ? 16 : row - c0 + 1, it.L - c0);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (e < lo || e >= hi) v[e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) pk[e] = lpack2(v[2 * e], v[2 * e + 1]);
           }
-          tc::st8x2_async(tS + 32 * c2, pk[0], tS + 32 * c2 + 8, pk[1]);
+          // 16 columns c to the 8 columns 32 (c / 32) + 8 (c / 16 % 2)
+          tc::st8_async(tS + (c0 & 96) + ((c0 >> 1) & 8), pk);
         }
         if (it.L < kC) {
           // rows of C behind the sequence may hold anything: 0 * NaN must not reach the product

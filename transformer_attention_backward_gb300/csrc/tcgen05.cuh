@@ -183,6 +183,17 @@ __device__ __forceinline__ void ld16x2_async(uint32_t ta, uint32_t tb, uint32_t 
       : "r"(ta), "r"(tb)
       : "memory");
 }
+// 16 columns, one wait.
+__device__ __forceinline__ void ld16_wait(uint32_t ta, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : ABW_TC_R16(0)
+      : "r"(ta)
+      : "memory");
+}
+
 // The same 16 columns of N accumulators (N = 2 or 3), one wait.
 template <int N>
 __device__ __forceinline__ void ld16n_wait(const uint32_t (&t)[N], uint32_t (&r)[16 * N]) {
@@ -230,6 +241,11 @@ __device__ __forceinline__ void st8x2_async(uint32_t ta, const uint32_t (&ra)[8]
       "r"(tb), "r"(ra[0]), "r"(ra[1]), "r"(ra[2]), "r"(ra[3]), "r"(ra[4]), "r"(ra[5]), "r"(ra[6]), "r"(ra[7]),
       "r"(rb[0]), "r"(rb[1]), "r"(rb[2]), "r"(rb[3]), "r"(rb[4]), "r"(rb[5]), "r"(rb[6]), "r"(rb[7])
       : "memory");
+}
+__device__ __forceinline__ void st8_async(uint32_t ta, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(ta), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
