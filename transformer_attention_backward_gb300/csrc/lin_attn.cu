@@ -55,31 +55,31 @@ __device__ __forceinline__ int seq_len(const int *lengths, int b, int T) {
 }
 
 // Waits of the two tensor-core kernels.  A barrier that has completed costs one
-// access (shared memory is busy, and each access of a warp that has little
-// else to do stands in its queue).  The rest is out of line: the kernels' warps
-// run different code side by side, and what they execute per step has to stay
-// in the instruction cache.
+// access: shared memory is busy, and each access of a warp that has little
+// else to do stands in its queue.
+__device__ __forceinline__ bool lin_wait_slow(uint32_t br, uint32_t parity, uint32_t bars, volatile int *abort_flag,
+                                                  unsigned int kernel, unsigned int *err, unsigned long long limit_ns) {
+  if (*abort_flag) return false;      // a wait has run out: all others return
+  if (mbar_wait_bounded(br, parity, limit_ns)) return true;
+  *abort_flag = 1;
+  report_timeout(err, kernel, (br - bars) / 8);
+  return false;
+}
 struct LinWait {
-  WaitCtl ctl;
   uint32_t bars;                      // shared address of barrier 0
-  volatile int *abort_flag;           // set by the first wait that runs out; all others then return
+  volatile int *abort_flag;
   unsigned int kernel;
+  const WaitCtl &ctl;
 
   __device__ __forceinline__ uint32_t bar(int i) const { return bars + i * 8; }
-  __device__ __noinline__ bool slow(uint32_t br, uint32_t parity) const {
-    if (*abort_flag) return false;
-    if (mbar_wait_bounded(br, parity, ctl.limit_ns)) return true;
-    *abort_flag = 1;
-    report_timeout(ctl.err, kernel, (br - bars) / 8);
-    return false;
-  }
   // one thread, or each lane for its own barrier
   __device__ __forceinline__ bool one(uint32_t br, uint32_t parity) const {
-    return mbar_try_wait(br, parity) || slow(br, parity);
+    return mbar_try_wait(br, parity) || lin_wait_slow(br, parity, bars, abort_flag, kernel, ctl.err, ctl.limit_ns);
   }
   // a whole warp
   __device__ __forceinline__ bool warp(uint32_t br, uint32_t parity) const {
-    return __all_sync(0xffffffffu, mbar_try_wait(br, parity)) || __all_sync(0xffffffffu, slow(br, parity));
+    return __all_sync(0xffffffffu, mbar_try_wait(br, parity)) ||
+           __all_sync(0xffffffffu, lin_wait_slow(br, parity, bars, abort_flag, kernel, ctl.err, ctl.limit_ns));
   }
 };
 
@@ -104,9 +104,9 @@ struct LinSizes {
 // steps or terms inside the tensor core would cut off bits of the
 // accumulator's size at every one (measured: 5 times the error).
 // The chain of a step (load, weights, product, addition) is long and the work
-// in it small, so what counts is how many steps are under way: a ring of
-// (X, Y, weighted rows) slots as deep as shared memory allows, filled in turn by
-// two groups of warps, and two buffers of U.  32 columns, not 64: X is read by
+// in it small, so what counts is how many steps are under way: a ring of 8
+// (X, Y) slots, three buffers of weighted rows, filled in turn by two groups of
+// warps, and two buffers of U.  32 columns, not 64: X is read by
 // twice as many CTAs (from L2), but a step moves 2/3 of the bytes through shared
 // memory and there are twice as many chains: 8192 tokens of 32 heads 59 us
 // against 103, 640 chains of 2048 tokens 83 against 83.
@@ -115,18 +115,21 @@ struct LinSizes {
 constexpr int kSThr = 448;
 constexpr int kCW = 32;
 
-// A slot: X (two 64-column parts of 8 KB) | Y (64 columns, of which a CTA uses
-// half) | weighted rows (two terms of 32 columns to an 8 KB part).
+// A slot: X (two 64-column parts of 8 KB) | Y (32 columns, 4 KB); the weighted
+// rows, which live from their forming to their product only, have buffers of
+// their own (two terms of 32 columns to an 8 KB part).
 template <int NS>
 struct StateShape {
   static constexpr int kN = NS == 3 ? 128 : 64;      // columns of U (with three terms the last 32 are unused)
-  static constexpr int kSlot = 3 * 8192 + kN / 64 * 8192;
-  static constexpr int kRing = 212992 / kSlot;
-  static constexpr int kFull = 0, kW = kRing, kDone = 2 * kRing, kUEmpty = 3 * kRing, kFinal = kUEmpty + 2;
-  static constexpr int kOffBar = kRing * kSlot;
+  static constexpr int kSlot = 2 * 8192 + 4096;
+  static constexpr int kRing = 8;
+  static constexpr int kWSlot = kN / 64 * 8192, kWRing = 3;
+  static constexpr int kOffW = kRing * kSlot;
+  static constexpr int kOffBar = kOffW + kWRing * kWSlot;
+  static constexpr int kFull = 0, kDone = kRing, kW = 2 * kRing, kUEmpty = kW + kWRing, kFinal = kUEmpty + 2;
   static constexpr int kOffTmem = kOffBar + (kFinal + 1) * 8, kOffAbort = kOffTmem + 4;
   static constexpr int kSmem = kOffBar + 256 + 1024;                   // + alignment slack
-  static_assert(kOffAbort + 4 <= kOffBar + 256 && kSmem <= 232448, "state kernel shared memory");
+  static_assert(kOffAbort + 4 <= kOffBar + 256 && kSmem <= 232448 && kOffW % 1024 == 0, "state kernel shared memory");
 };
 
 struct LinStateParams {
@@ -140,8 +143,8 @@ struct LinStateParams {
 
 template <int D, int NS>
 __global__ void __launch_bounds__(kSThr, 1)
-    lin_state_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+    lin_state_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV32,
+                     const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO32,
                      const __grid_constant__ LinStateParams p) {
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(kSThr, 1)
   auto chunk = [&](int m) -> int { return role ? ncb - 1 - m : m; };
 
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + Z::kOffAbort);
-  const LinWait lw{p.wait, sb + Z::kOffBar, abort_flag, kSiteLinState};
+  const LinWait lw{sb + Z::kOffBar, abort_flag, kSiteLinState, p.wait};
   auto bar = [&](int i) -> uint32_t { return lw.bar(i); };
   auto wt = [&](uint32_t br, uint32_t parity) -> bool { return lw.one(br, parity); };
   auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return lw.warp(br, parity); };
@@ -169,9 +172,9 @@ __global__ void __launch_bounds__(kSThr, 1)
   if (tid == 0) {
     for (int s = 0; s < Z::kRing; ++s) {
       mbar_init(bar(Z::kFull + s), 1);
-      mbar_init(bar(Z::kW + s), 128);
       mbar_init(bar(Z::kDone + s), 1);
     }
+    for (int s = 0; s < Z::kWRing; ++s) mbar_init(bar(Z::kW + s), 128);
     for (int s = 0; s < 2; ++s) mbar_init(bar(Z::kUEmpty + s), 128);
     mbar_init(bar(Z::kFinal), 1);
     *abort_flag = 0;
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(kSThr, 1)
   if (warp == 0) {
     // ============================ TMA producer ============================
     if (lane == 0) {
-      const CUtensorMap *mx = role ? &tmQ : &tmK, *my = role ? &tmDO : &tmV;
+      const CUtensorMap *mx = role ? &tmQ : &tmK, *my = role ? &tmDO32 : &tmV32;
       prefetch_tensormap(mx);
       prefetch_tensormap(my);
       int issued = 0;
@@ -197,9 +200,9 @@ __global__ void __launch_bounds__(kSThr, 1)
         if (!wt(bar(Z::kDone + s), ph)) break;
         const int h = role ? kv * p.z.G + g / 2 : kv, t0 = chunk(m) * kC + (g & 1) * kSub;
         const uint32_t st = sb + s * Z::kSlot, fb = bar(Z::kFull + s);
-        mbar_arrive_expect_tx(fb, (NH + 1) * 8192);
+        mbar_arrive_expect_tx(fb, NH * 8192 + 4096);
         for (int x = 0; x < NH; ++x) tma_load_4d(st + x * 8192, mx, x * 64, h, t0, b, fb);
-        tma_load_4d(st + 16384, my, part / 2 * 64, h, t0, b, fb);
+        tma_load_4d(st + 16384, my, part * kCW, h, t0, b, fb);
         issued = i + 1;
         if (++g == gi) g = 0, ++m;
         if (++s == Z::kRing) s = 0, ph ^= 1;
@@ -215,46 +218,48 @@ __global__ void __launch_bounds__(kSThr, 1)
     // which nobody reads.
     constexpr uint32_t id_u = tc::idesc_bf16_f32(128, Z::kN, 1, 1);
     const uint64_t dX = tc::sdesc_sw128(sb, 8192, 1024);
-    const uint64_t dW = tc::sdesc_sw128(sb + 24576, 8192, 1024);
-    for (int i = 0, s = 0, ph = 0; i < steps; ++i) {
+    const uint64_t dW = tc::sdesc_sw128(sb + Z::kOffW, 8192, 1024);
+    for (int i = 0, s = 0, w = 0, wph = 0; i < steps; ++i) {
       const int u = i & 1;
       // (weighted rows that are there were formed from a stage that is there)
-      if (!wtw(bar(Z::kUEmpty + u), ((i >> 1) & 1) ^ 1) || !wtw(bar(Z::kW + s), ph)) break;
+      if (!wtw(bar(Z::kUEmpty + u), ((i >> 1) & 1) ^ 1) || !wtw(bar(Z::kW + w), wph)) break;
       tc::fence_after_sync();
-      const uint64_t so = static_cast<uint64_t>(s * Z::kSlot) >> 4;
+      const uint64_t so = static_cast<uint64_t>(s * Z::kSlot) >> 4, wo = static_cast<uint64_t>(w * Z::kWSlot) >> 4;
       // the terms side by side as N: X is read once for all of them
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk)
-        tc::mma_bf16_w(tmem + u * 256, dX + so + ((kk * 2048) >> 4), dW + so + ((kk * 2048) >> 4), id_u, kk > 0);
+        tc::mma_bf16_w(tmem + u * 256, dX + so + ((kk * 2048) >> 4), dW + wo + ((kk * 2048) >> 4), id_u, kk > 0);
       // one signal for all who wait for the step: the stage and the weighted
       // rows are free, U is there
       tc::commit_w(bar(Z::kDone + s));
-      if (++s == Z::kRing) s = 0, ph ^= 1;
+      if (++s == Z::kRing) s = 0;
+      if (++w == Z::kWRing) w = 0, wph ^= 1;
     }
     tc::commit_w(bar(Z::kFinal));
     mbar_wait_bounded(bar(Z::kFinal), 0, 2000000000ull);   // every MMA has completed
   } else if (warp < 10) {
     // ============================ weights =================================
     const int u = (warp - 2) >> 2, wtid = (tid - 64) & 127;
-    for (int i = u, s = u, ph = 0, m = 0, g = 0; i < steps; i += 2) {
-      if (!wtw(bar(Z::kFull + s), ph)) break;                 // (loaded once the slot's last step was done)
+    for (int i = u, s = u, ph = 0, w = u, m = 0, g = 0; i < steps; i += 2) {
+      if (!wtw(bar(Z::kFull + s), ph)) break;
+      // the buffer's last product, that of step i - kWRing, is done
+      if (i >= Z::kWRing && !wtw(bar(Z::kDone + (i - Z::kWRing) % Z::kRing), ((i - Z::kWRing) / Z::kRing) & 1)) break;
       const int L = min(kC, len - chunk(m) * kC);
-      unsigned char *st = smem + s * Z::kSlot;
+      unsigned char *st = smem + s * Z::kSlot, *wb = smem + Z::kOffW + w * Z::kWSlot;
 #pragma unroll
       for (int c = 0; c < kCW / 16; ++c) {
         // 16-byte piece j of the row of token `row` of the chunk
         const int id = wtid + 128 * c, r = id >> 2, j = id & 3, row = r + u * kSub;
         uint4 out[NS];
         if (row < L) {
-          const float w = role ? p.z.scale * lexp2(l2 * static_cast<float>(row + 1))
-                               : lexp2(l2 * static_cast<float>(L - 1 - row));
-          const uint4 y = *reinterpret_cast<const uint4 *>(
-              st + 16384 + r * 128 + ((((part & 1) * 4 + j) ^ (r & 7)) << 4));
+          const float wgt = role ? p.z.scale * lexp2(l2 * static_cast<float>(row + 1))
+                                 : lexp2(l2 * static_cast<float>(L - 1 - row));
+          const uint4 y = *reinterpret_cast<const uint4 *>(st + 16384 + 16 * id);
           const uint32_t yi[4] = {y.x, y.y, y.z, y.w};
           uint32_t o[NS][4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float f0 = w * bf16_lo(yi[e]), f1 = w * bf16_hi(yi[e]);
+            float f0 = wgt * bf16_lo(yi[e]), f1 = wgt * bf16_hi(yi[e]);
 #pragma unroll
             for (int t = 0; t < NS; ++t) {
               o[t][e] = lpack2(f0, f1);
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(kSThr, 1)
         }
 #pragma unroll
         for (int t = 0; t < NS; ++t)
-          *reinterpret_cast<uint4 *>(st + 24576 + (t >> 1) * 8192 + r * 128 + ((((t & 1) * 4 + j) ^ (r & 7)) << 4)) = out[t];
+          *reinterpret_cast<uint4 *>(wb + (t >> 1) * 8192 + r * 128 + ((((t & 1) * 4 + j) ^ (r & 7)) << 4)) = out[t];
       }
       if (L < kC) {
         // rows behind the sequence may hold anything: 0 * NaN must not reach U
@@ -278,7 +283,8 @@ __global__ void __launch_bounds__(kSThr, 1)
           if (((id >> 3) & 63) + u * kSub >= L) *reinterpret_cast<uint4 *>(st + 16 * id) = make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async_smem();
-      mbar_arrive(bar(Z::kW + s));
+      mbar_arrive(bar(Z::kW + w));
+      if ((w += 2) >= Z::kWRing) w -= Z::kWRing;
       if ((s += 2) >= Z::kRing) s -= Z::kRing, ph ^= 1;
       if ((g += 2) == gi) g = 0, ++m;
     }
@@ -464,7 +470,7 @@ __global__ void __launch_bounds__(kOThr, 1)
   constexpr int NH = D / 64;
 
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOOffAbort);
-  const LinWait lw{p.wait, sb + kOOffBar, abort_flag, kSiteLinOut};
+  const LinWait lw{sb + kOOffBar, abort_flag, kSiteLinOut, p.wait};
   auto bar = [&](int i) -> uint32_t { return lw.bar(i); };
   auto wt = [&](uint32_t br, uint32_t parity) -> bool { return lw.one(br, parity); };
   auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return lw.warp(br, parity); };
@@ -882,30 +888,33 @@ cudaError_t decode_groups(const LinDecodeParams &p, unsigned blocks, cudaStream_
   return cudaGetLastError();
 }
 
-// Rows of D elements at `stride` elements from token to token.
-bool lin_map(CUtensorMap *mp, const void *base, int D, int H, int T, int B, long long stride, const char **why) {
+// Rows of D elements at `stride` elements from token to token, in boxes of 64
+// tokens by 64 columns (128-byte swizzle, as the products read them) or 32
+// (plain rows).
+bool lin_map(CUtensorMap *mp, const void *base, int D, int H, int T, int B, long long stride, const char **why,
+             int cols = 64) {
   const uint64_t ts = static_cast<uint64_t>(stride) * 2;
   const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(H), static_cast<uint64_t>(T),
                             static_cast<uint64_t>(B)};
   const uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, ts, ts * T};
-  const uint32_t box[4] = {64, 1, kSub, 1};
-  return encode_tiled(mp, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
-                      why);
+  const uint32_t box[4] = {static_cast<uint32_t>(cols), 1, kSub, 1};
+  return encode_tiled(mp, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box,
+                      cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, why);
 }
 
 template <int D, int NS>
-cudaError_t launch_state(const CUtensorMap (&tm)[4], const LinStateParams &p, cudaStream_t st) {
+cudaError_t launch_state(const CUtensorMap (&tm)[6], const LinStateParams &p, cudaStream_t st) {
   const auto kern = lin_state_kernel<D, NS>;
   constexpr int smem = StateShape<NS>::kSmem;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(p.nroles) * p.z.B * p.z.Hkv * (D / kCW);
-  kern<<<grid, kSThr, smem, st>>>(tm[0], tm[1], tm[2], tm[3], p);
+  kern<<<grid, kSThr, smem, st>>>(tm[1], tm[4], tm[0], tm[5], p);
   return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_lin(const CUtensorMap (&tm)[4], const LinStateParams &sp, const LinOutParams &op, bool exact,
+cudaError_t launch_lin(const CUtensorMap (&tm)[6], const LinStateParams &sp, const LinOutParams &op, bool exact,
                        int sms, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (sp.nroles) {
@@ -978,13 +987,18 @@ cudaError_t launch_lin_attn(const LinAttnArgs &a, const WaitCtl &w, cudaStream_t
     op.stride[i] = os[i];
   }
   op.wait = w;
-  CUtensorMap tm[4];
+  CUtensorMap tm[6];                    // q, k, v, dout; v and dout in narrow boxes
   if (!lin_map(&tm[0], a.q, a.D, a.Hq, a.T, a.B, a.q_stride, why) ||
       !lin_map(&tm[1], a.k, a.D, a.Hkv, a.T, a.B, a.k_stride, why) ||
       !lin_map(&tm[2], a.v, a.D, a.Hkv, a.T, a.B, a.v_stride, why) ||
       (bwd && !lin_map(&tm[3], a.dout, a.D, a.Hq, a.T, a.B, static_cast<long long>(a.Hq) * a.D, why)))
     return cudaErrorInvalidValue;
-  if (!bwd) tm[3] = tm[0];              // not read
+  if ((f && !lin_map(&tm[4], a.v, a.D, a.Hkv, a.T, a.B, a.v_stride, why, kCW)) ||
+      (r && !lin_map(&tm[5], a.dout, a.D, a.Hq, a.T, a.B, static_cast<long long>(a.Hq) * a.D, why, kCW)))
+    return cudaErrorInvalidValue;
+  if (!bwd) tm[3] = tm[0];              // these are not read
+  if (!f) tm[4] = tm[0];
+  if (!r) tm[5] = tm[0];
   for (int i = 0; i < 4; ++i)
     if (out[i] && !lin_map(&op.map[i], out[i], a.D, i < 2 ? a.Hq : a.Hkv, a.T, a.B, os[i], why)) return cudaErrorInvalidValue;
   const bool exact = a.final_state || a.dinitial_state;   // a state leaves in fp32
