@@ -175,6 +175,8 @@ abw_status check_qk(const char *op, int B, int T, int Hq, int Hkv, int D, abw_dt
   if (B < 0 || T < 0 || Hq < 0 || Hkv < 0) return fail(ABW_EINVAL, "%s: negative size", op);
   if (D < 2 || (D & 1)) return fail(ABW_EINVAL, "%s: D=%d must be even and >= 2", op, D);
   if (D > 512) return fail(ABW_ENOTSUP, "%s: D=%d > 512", op, D);
+  if (static_cast<long long>(Hq > Hkv ? Hq : Hkv) * D > 0x7fffffff)
+    return fail(ABW_ENOTSUP, "%s: more than 2^31 elements a token", op);
   if (dtype != ABW_F32 && dtype != ABW_BF16) return fail(ABW_EINVAL, "%s: bad dtype", op);
   if (!(eps >= 0.0f)) return fail(ABW_EINVAL, "%s: eps must be >= 0", op);
   return ABW_OK;

@@ -104,15 +104,16 @@ struct LinSizes {
 // steps or terms inside the tensor core would cut off bits of the
 // accumulator's size at every one (measured: 5 times the error).
 // The chain of a step (load, weights, product, addition) is long and the work
-// in it small, so what counts is how many steps are under way: a ring of 8
-// (X, Y) slots, three buffers of weighted rows, filled in turn by two groups of
-// warps, and two buffers of U.  32 columns, not 64: X is read by
+// in it small, so what counts is how many steps are under way: a ring of 6
+// (X, Y) slots, four buffers of weighted rows, filled in turn by three groups of
+// warps (two: 59 us for 55, four: 58), and two buffers of U.  32 columns, not 64: X is read by
 // twice as many CTAs (from L2), but a step moves 2/3 of the bytes through shared
 // memory and there are twice as many chains: 8192 tokens of 32 heads 59 us
 // against 103, 640 chains of 2048 tokens 83 against 83.
-// Warps: 0 TMA, 1 MMA, 2-5 and 6-9 weights (even and odd steps), 10-13 state.
+// Warps: 0 TMA, 1 MMA, 2-13 weights, 14-17 state.
 // ---------------------------------------------------------------------------
-constexpr int kSThr = 448;
+constexpr int kSGroups = 3;                          // groups of four warps that form weighted rows
+constexpr int kSThr = 64 + kSGroups * 128 + 128;
 constexpr int kCW = 32;
 
 // A slot: X (two 64-column parts of 8 KB) | Y (32 columns, 4 KB); the weighted
@@ -122,8 +123,8 @@ template <int NS>
 struct StateShape {
   static constexpr int kN = NS == 3 ? 128 : 64;      // columns of U (with three terms the last 32 are unused)
   static constexpr int kSlot = 2 * 8192 + 4096;
-  static constexpr int kRing = 8;
-  static constexpr int kWSlot = kN / 64 * 8192, kWRing = 3;
+  static constexpr int kRing = 6;
+  static constexpr int kWSlot = kN / 64 * 8192, kWRing = 4;
   static constexpr int kOffW = kRing * kSlot;
   static constexpr int kOffBar = kOffW + kWRing * kWSlot;
   static constexpr int kFull = 0, kDone = kRing, kW = 2 * kRing, kUEmpty = kW + kWRing, kFinal = kUEmpty + 2;
@@ -237,10 +238,12 @@ __global__ void __launch_bounds__(kSThr, 1)
     }
     tc::commit_w(bar(Z::kFinal));
     mbar_wait_bounded(bar(Z::kFinal), 0, 2000000000ull);   // every MMA has completed
-  } else if (warp < 10) {
+  } else if (warp < 2 + 4 * kSGroups) {
     // ============================ weights =================================
-    const int u = (warp - 2) >> 2, wtid = (tid - 64) & 127;
-    for (int i = u, s = u, ph = 0, w = u, m = 0, g = 0; i < steps; i += 2) {
+    const int grp = (warp - 2) >> 2, wtid = (tid - 64) & 127;
+    for (int i = grp, s = grp, ph = 0, w = grp, m = 0, g = grp; i < steps; i += kSGroups) {
+      while (g >= gi) g -= gi, ++m;
+      const int u = g & 1;                                    // half of the chunk
       if (!wtw(bar(Z::kFull + s), ph)) break;
       // the buffer's last product, that of step i - kWRing, is done
       if (i >= Z::kWRing && !wtw(bar(Z::kDone + (i - Z::kWRing) % Z::kRing), ((i - Z::kWRing) / Z::kRing) & 1)) break;
@@ -284,9 +287,9 @@ __global__ void __launch_bounds__(kSThr, 1)
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(Z::kW + w));
-      if ((w += 2) >= Z::kWRing) w -= Z::kWRing;
-      if ((s += 2) >= Z::kRing) s -= Z::kRing, ph ^= 1;
-      if ((g += 2) == gi) g = 0, ++m;
+      if ((w += kSGroups) >= Z::kWRing) w -= Z::kWRing;
+      if ((s += kSGroups) >= Z::kRing) s -= Z::kRing, ph ^= 1;
+      g += kSGroups;
     }
   } else {
     // ============================ state ===================================
@@ -329,17 +332,16 @@ __global__ void __launch_bounds__(kSThr, 1)
         const float dec = g == 0 ? lexp2(l2 * static_cast<float>(min(kC, len - n * kC))) : 1.f;
 #pragma unroll
         for (int x = 0; x < kCW / 16; ++x) {
-          uint32_t at[NS], v[16 * NS];
+          float t[16];
 #pragma unroll
-          for (int e = 0; e < NS; ++e) at[e] = tmem + lanebase + u * 256 + e * kCW + x * 16;
-          tc::ld16n_wait<NS>(at, v);
+          for (int e = NS - 1; e >= 0; --e) {                 // the small terms first
+            uint32_t v[16];
+            tc::ld16_wait(tmem + lanebase + u * 256 + e * kCW + x * 16, v);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            float t = __uint_as_float(v[16 * (NS - 1) + c]);  // the small terms first
-#pragma unroll
-            for (int e = NS - 2; e >= 0; --e) t += __uint_as_float(v[16 * e + c]);
-            S[x * 16 + c] = fmaf(dec, S[x * 16 + c], t);
+            for (int c = 0; c < 16; ++c) t[c] = e == NS - 1 ? __uint_as_float(v[c]) : t[c] + __uint_as_float(v[c]);
           }
+#pragma unroll
+          for (int c = 0; c < 16; ++c) S[x * 16 + c] = fmaf(dec, S[x * 16 + c], t[c]);
         }
         tc::fence_before_sync();
         mbar_arrive(bar(Z::kUEmpty + u));

@@ -7,9 +7,7 @@
 //   dx = (dn gamma - x c / (D rms^2)) / rms,   dgamma = sum over rows dn x / rms
 //
 // Bound by memory: x is read once and y written once (backward: x and dy read,
-// dx written); the norm's sum is taken in registers.  A row belongs to 8-32
-// lanes, each with V pairs; a block takes the rows of a few tokens, so the
-// angles of a token are formed once for all its heads.
+// dx written); the norm's sum is taken in registers.
 //
 // Angles without double precision: the host forms the turns per position,
 // base^(-2i / rotary_dim) / (2 pi) mod 1, as a 64-bit binary fraction; an
@@ -30,15 +28,18 @@ struct QkParams {
   const void *dy[2];
   void *out[2];                       // y, or dx
   const float *gamma[2];              // null: no norm
-  float *part;                        // backward: [gridDim.x][2][D] partial dgamma
+  float *part;                        // backward: [gridDim.x][D] partial dgamma
+  float *dgamma[2];                   // null: not wanted
   long long xs[2], os[2];             // elements from token to token
   int H[2];
   int D, rot;                         // components per head, pairs that turn
-  int T, pos0, tt;                    // tokens per block and step
+  int T, pos0;
+  int slots[2];                       // lane groups that share a token's heads
+  int first_k;                        // first block that works on keys
   long long ntok;
   float eps, inv_n;
   const int *pos;                     // [axes][ntok] or null: pos0 + t
-  int axes, sec_end[4];               // first pair behind each axis' pairs
+  int sec_end[3];                     // first pair behind each axis' pairs, but for the last axis
 };
 
 // A launch's parameters are written out with it: heads of up to 128 components
@@ -48,103 +49,140 @@ struct QkTable : QkParams {
   unsigned long long freq[NP];
 };
 
-template <typename T, int V>
-__device__ __forceinline__ void qload(const T *p, float (&v)[V]) {
-  if constexpr (V == 4 && sizeof(T) == 2) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-    v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
-  } else if constexpr (V == 4) {
-    const float4 u = __ldg(reinterpret_cast<const float4 *>(p));
-    v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-  } else {
-    v[0] = static_cast<float>(p[0]);
-  }
+// Arithmetic on V values at a time: two float2 (packed fp32 instructions) for
+// V = 4, one float for V = 1.
+template <int V>
+struct Num;
+template <>
+struct Num<4> {
+  using F = float2;
+  static constexpr int kC = 2;
+};
+template <>
+struct Num<1> {
+  using F = float;
+  static constexpr int kC = 1;
+};
+__device__ __forceinline__ float2 f_mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 f_fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float f_sum(float2 a) { return a.x + a.y; }
+__device__ __forceinline__ float f_mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float f_fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float f_sum(float a) { return a; }
+template <typename F>
+__device__ __forceinline__ F f_all(float a);
+template <>
+__device__ __forceinline__ float2 f_all<float2>(float a) { return make_float2(a, a); }
+template <>
+__device__ __forceinline__ float f_all<float>(float a) { return a; }
+
+__device__ __forceinline__ uint32_t q_pack(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&v);
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void qstore(T *p, const float (&v)[V]) {
-  if constexpr (V == 4 && sizeof(T) == 2) {
-    __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-    *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
-  } else if constexpr (V == 4) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-    p[0] = static_cast<T>(v[0]);
-  }
-}
-
-// The V pairs (a[i], b[i]) of pair slots s .. s + V - 1.  Interleaved pairs are
-// neighbours; split pairs are rot apart.  Components behind the rotated ones
-// are paired with their neighbours (their angle is 0).
-template <typename T, int V, bool INTER>
-__device__ __forceinline__ void qload_pairs(const T *row, int s, int rot, float (&a)[V], float (&b)[V]) {
-  if constexpr (INTER || V == 1) {
-    if constexpr (V == 1) {
-      const bool near = INTER || s >= rot;
-      qload<T, 1>(row + (near ? 2 * s : s), a);
-      qload<T, 1>(row + (near ? 2 * s + 1 : s + rot), b);
-    } else {
-      float lo[4], hi[4];
-      if constexpr (sizeof(T) == 2) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(row + 2 * s));
-        lo[0] = bf16_lo(u.x), lo[1] = bf16_hi(u.x), lo[2] = bf16_lo(u.y), lo[3] = bf16_hi(u.y);
-        hi[0] = bf16_lo(u.z), hi[1] = bf16_hi(u.z), hi[2] = bf16_lo(u.w), hi[3] = bf16_hi(u.w);
-      } else {
-        qload<T, 4>(row + 2 * s, lo);
-        qload<T, 4>(row + 2 * s + 4, hi);
-      }
-      a[0] = lo[0], b[0] = lo[1], a[1] = lo[2], b[1] = lo[3];
-      a[2] = hi[0], b[2] = hi[1], a[3] = hi[2], b[3] = hi[3];
-    }
-  } else {
-    const bool near = s >= rot;
-    qload<T, V>(row + (near ? 2 * s : s), a);
-    qload<T, V>(row + (near ? 2 * s + V : s + rot), b);
-  }
-}
-
-template <typename T, int V, bool INTER>
-__device__ __forceinline__ void qstore_pairs(T *row, int s, int rot, const float (&a)[V], const float (&b)[V]) {
-  if constexpr (INTER && V == 4) {
-    const float lo[4] = {a[0], b[0], a[1], b[1]}, hi[4] = {a[2], b[2], a[3], b[3]};
-    if constexpr (sizeof(T) == 2) {
-      __nv_bfloat162 u[4] = {__floats2bfloat162_rn(lo[0], lo[1]), __floats2bfloat162_rn(lo[2], lo[3]),
-                             __floats2bfloat162_rn(hi[0], hi[1]), __floats2bfloat162_rn(hi[2], hi[3])};
-      *reinterpret_cast<uint4 *>(row + 2 * s) =
-          make_uint4(*reinterpret_cast<uint32_t *>(&u[0]), *reinterpret_cast<uint32_t *>(&u[1]),
-                     *reinterpret_cast<uint32_t *>(&u[2]), *reinterpret_cast<uint32_t *>(&u[3]));
-    } else {
-      qstore<T, 4>(row + 2 * s, lo);
-      qstore<T, 4>(row + 2 * s + 4, hi);
-    }
-  } else {
+// Where the V pairs of the pair slots s .. s + V - 1 of a row are: two runs of V
+// elements, at x and y.  Interleaved pairs are neighbours; split pairs are rot
+// apart.  Components behind the rotated ones are paired with their neighbours
+// (their angle is 0).
+template <int V, bool INTER>
+struct Place {
+  int x, y;
+  __device__ __forceinline__ Place(int s, int rot) {
     const bool near = INTER || s >= rot;
-    qstore<T, V>(row + (near ? 2 * s : s), a);
-    qstore<T, V>(row + (near ? 2 * s + V : s + rot), b);
+    x = near ? 2 * s : s;
+    y = near ? 2 * s + V : s + rot;
   }
-}
+};
 
-// cos and sin of nt tokens' angles, [nt][D / 2] each; 1 and 0 behind the
-// rotated pairs.
-template <int NP>
-__device__ __forceinline__ void fill_angles(const QkTable<NP> &p, long long tok0, int nt, float *cs, float *sn) {
-  const int h2 = p.D >> 1;
-  for (int i = threadIdx.x; i < nt * h2; i += kQThr) {
-    const int n = i / h2, s = i % h2;
-    float c = 1.f, z = 0.f;
-    if (s < p.rot) {
-      int axis = 0;
-      while (axis + 1 < p.axes && s >= p.sec_end[axis]) ++axis;
-      const long long tok = tok0 + n;
-      const long long pos = p.pos ? p.pos[axis * p.ntok + tok] : static_cast<long long>(p.pos0) + tok % p.T;
-      const unsigned long long turns = static_cast<unsigned long long>(pos) * p.freq[s];
-      const float half_turns = static_cast<float>(static_cast<int>(turns >> 32)) * 4.656612873077393e-10f;   // 2^-31
-      sincospif(half_turns, &z, &c);
+// V pairs of a row as they are in memory, so that loads of the next rows can
+// be under way while these are at work.  get / set: members a, b of the pairs.
+template <typename T, int V, bool INTER>
+struct Pairs;
+template <bool INTER>
+struct Pairs<__nv_bfloat16, 4, INTER> {
+  uint2 x, y;
+  __device__ __forceinline__ void clear() { x = y = make_uint2(0, 0); }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *row, const Place<4, INTER> &at) {
+    if constexpr (INTER) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4 *>(row + at.x));
+      x = make_uint2(u.x, u.y), y = make_uint2(u.z, u.w);
+    } else {
+      x = __ldg(reinterpret_cast<const uint2 *>(row + at.x));
+      y = __ldg(reinterpret_cast<const uint2 *>(row + at.y));
     }
-    cs[i] = c;
-    sn[i] = z;
   }
-}
+  __device__ __forceinline__ void store(__nv_bfloat16 *row, const Place<4, INTER> &at) const {
+    if constexpr (INTER) {
+      *reinterpret_cast<uint4 *>(row + at.x) = make_uint4(x.x, x.y, y.x, y.y);
+    } else {
+      *reinterpret_cast<uint2 *>(row + at.x) = x;
+      *reinterpret_cast<uint2 *>(row + at.y) = y;
+    }
+  }
+  __device__ __forceinline__ void get(float2 (&a)[2], float2 (&b)[2]) const {
+    if constexpr (INTER) {
+      a[0] = make_float2(bf16_lo(x.x), bf16_lo(x.y)), a[1] = make_float2(bf16_lo(y.x), bf16_lo(y.y));
+      b[0] = make_float2(bf16_hi(x.x), bf16_hi(x.y)), b[1] = make_float2(bf16_hi(y.x), bf16_hi(y.y));
+    } else {
+      a[0] = make_float2(bf16_lo(x.x), bf16_hi(x.x)), a[1] = make_float2(bf16_lo(x.y), bf16_hi(x.y));
+      b[0] = make_float2(bf16_lo(y.x), bf16_hi(y.x)), b[1] = make_float2(bf16_lo(y.y), bf16_hi(y.y));
+    }
+  }
+  __device__ __forceinline__ void set(const float2 (&a)[2], const float2 (&b)[2]) {
+    if constexpr (INTER) {
+      x = make_uint2(q_pack(a[0].x, b[0].x), q_pack(a[0].y, b[0].y));
+      y = make_uint2(q_pack(a[1].x, b[1].x), q_pack(a[1].y, b[1].y));
+    } else {
+      x = make_uint2(q_pack(a[0].x, a[0].y), q_pack(a[1].x, a[1].y));
+      y = make_uint2(q_pack(b[0].x, b[0].y), q_pack(b[1].x, b[1].y));
+    }
+  }
+};
+template <bool INTER>
+struct Pairs<float, 4, INTER> {
+  float4 x, y;
+  __device__ __forceinline__ void clear() { x = y = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float *row, const Place<4, INTER> &at) {
+    x = __ldg(reinterpret_cast<const float4 *>(row + at.x));
+    y = __ldg(reinterpret_cast<const float4 *>(row + at.y));
+  }
+  __device__ __forceinline__ void store(float *row, const Place<4, INTER> &at) const {
+    *reinterpret_cast<float4 *>(row + at.x) = x;
+    *reinterpret_cast<float4 *>(row + at.y) = y;
+  }
+  __device__ __forceinline__ void get(float2 (&a)[2], float2 (&b)[2]) const {
+    if constexpr (INTER) {
+      a[0] = make_float2(x.x, x.z), a[1] = make_float2(y.x, y.z);
+      b[0] = make_float2(x.y, x.w), b[1] = make_float2(y.y, y.w);
+    } else {
+      a[0] = make_float2(x.x, x.y), a[1] = make_float2(x.z, x.w);
+      b[0] = make_float2(y.x, y.y), b[1] = make_float2(y.z, y.w);
+    }
+  }
+  __device__ __forceinline__ void set(const float2 (&a)[2], const float2 (&b)[2]) {
+    if constexpr (INTER) {
+      x = make_float4(a[0].x, b[0].x, a[0].y, b[0].y);
+      y = make_float4(a[1].x, b[1].x, a[1].y, b[1].y);
+    } else {
+      x = make_float4(a[0].x, a[0].y, a[1].x, a[1].y);
+      y = make_float4(b[0].x, b[0].y, b[1].x, b[1].y);
+    }
+  }
+};
+template <typename T, bool INTER>
+struct Pairs<T, 1, INTER> {
+  T x, y;
+  __device__ __forceinline__ void clear() { x = y = static_cast<T>(0.f); }
+  __device__ __forceinline__ void load(const T *row, const Place<1, INTER> &at) { x = row[at.x], y = row[at.y]; }
+  __device__ __forceinline__ void store(T *row, const Place<1, INTER> &at) const { row[at.x] = x, row[at.y] = y; }
+  __device__ __forceinline__ void get(float (&a)[1], float (&b)[1]) const {
+    a[0] = static_cast<float>(x), b[0] = static_cast<float>(y);
+  }
+  __device__ __forceinline__ void set(const float (&a)[1], const float (&b)[1]) {
+    x = static_cast<T>(a[0]), y = static_cast<T>(b[0]);
+  }
+};
 
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
@@ -153,201 +191,410 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
+// 1 / sqrt(m): the approximation (2 ulp) and one Newton step.
+__device__ __forceinline__ float inv_root(float m) {
+  const float r = rsqrtf(m);
+  return r * fmaf(-0.5f * m * r, r, 1.5f);
+}
+
 template <int V, int L>
 constexpr int table_size() { return V == 4 && L <= 16 ? 64 : kQMaxPairs; }
 
-// N: groups of V pair slots per lane; L: lanes per row.
-template <typename XT, typename DT, bool BWD, bool INTER, int V, int N, int L>
-__global__ void __launch_bounds__(kQThr) qk_kernel(const __grid_constant__ QkTable<table_size<V, L>()> p) {
-  extern __shared__ __align__(16) float ang[];
-  const int h2 = p.D >> 1;
-  float *cs = ang, *sn = ang + p.tt * h2;
-  constexpr int kGroups = kQThr / L;
-  const int lane = threadIdx.x % L, grp = threadIdx.x / L;
-  float dga[2][N][V], dgb[2][N][V];     // dgamma of this lane's components
-  if constexpr (BWD) {
+// sin and cos of t 2^-32 turns: the nearest quarter turn, and the Taylor series
+// for what is left, at most pi / 4 (cut off at 2e-9 and 2e-10), in some 20
+// instructions.  The angle is an integer until its one rounding to float.
+__device__ __forceinline__ void turn_sincos(unsigned t, float &sn, float &cs) {
+  const unsigned q = (t + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int>(t - (q << 30))) * 1.4629180792671596e-9f;   // 2 pi 2^-32
+  const float y = x * x;
+  const float a = fmaf(fmaf(fmaf(fmaf(1.f / 362880, y, -1.f / 5040), y, 1.f / 120), y, -1.f / 6), y * x, x);
+  const float b =
+      fmaf(fmaf(fmaf(fmaf(fmaf(-1.f / 3628800, y, 1.f / 40320), y, -1.f / 720), y, 1.f / 24), y, -0.5f), y, 1.f);
+  const float s = q & 1 ? b : a, c = q & 1 ? a : b;
+  sn = __uint_as_float(__float_as_uint(s) ^ ((q & 2) << 30));
+  cs = __uint_as_float(__float_as_uint(c) ^ (((q + 1) & 2) << 30));
+}
+
+// The launch's turns in shared memory: lanes read them by an index of their
+// own, which the constant bank serves one at a time.
+template <int NP>
+__device__ __forceinline__ void load_turns(const QkTable<NP> &p, unsigned long long *turns) {
+  for (int i = threadIdx.x; i < p.rot; i += kQThr) turns[i] = p.freq[i];
+  __syncthreads();
+}
+
+// cos and sin of token tok's angles for this lane's pair slots; 1 and 0 behind
+// the rotated pairs.
+template <int V, int N, int L, typename F = typename Num<V>::F, int C = Num<V>::kC>
+__device__ __forceinline__ void lane_angles(const QkParams &p, const unsigned long long *turns, long long tok, int lane,
+                                            F (&c)[N][C], F (&z)[N][C]) {
+  long long step = 0;
+  if (!p.pos)
+    step = p.pos0 + (p.ntok <= 0x7fffffffLL
+                         ? static_cast<long long>(static_cast<unsigned>(tok) % static_cast<unsigned>(p.T))
+                         : tok % p.T);
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+  for (int k = 0; k < N; ++k) {
+    float cv[V], zv[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int s = (lane + L * k) * V + e;
+      cv[e] = 1.f, zv[e] = 0.f;
+      if (s < p.rot) {
+        const int axis = (s >= p.sec_end[0]) + (s >= p.sec_end[1]) + (s >= p.sec_end[2]);
+        const long long pos = p.pos ? p.pos[axis * p.ntok + tok] : step;
+        // the upper half of the product, modulo one turn
+        const unsigned lo = static_cast<unsigned>(turns[s]), hi = static_cast<unsigned>(turns[s] >> 32);
+        const unsigned plo = static_cast<unsigned>(pos), phi = static_cast<unsigned>(static_cast<unsigned long long>(pos) >> 32);
+        turn_sincos(__umulhi(plo, lo) + plo * hi + phi * lo, zv[e], cv[e]);
+      }
+    }
+    if constexpr (V == 4) {
+      c[k][0] = make_float2(cv[0], cv[1]), c[k][1] = make_float2(cv[2], cv[3]);
+      z[k][0] = make_float2(zv[0], zv[1]), z[k][1] = make_float2(zv[2], zv[3]);
+    } else {
+      c[k][0] = cv[0], z[k][0] = zv[0];
+    }
+  }
+}
+
+// gamma of this lane's components, 1 where there is no norm.
+template <int V, int N, int L, bool INTER, typename F = typename Num<V>::F, int C = Num<V>::kC>
+__device__ __forceinline__ void lane_gamma(const float *gamma, int lane, int rot, int h2, F (&ga)[N][C], F (&gb)[N][C]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int s = (lane + L * k) * V;
+#pragma unroll
+    for (int e = 0; e < C; ++e) ga[k][e] = gb[k][e] = f_all<F>(1.f);
+    if (gamma && s < h2) {
+      Pairs<float, V, INTER> g;
+      g.load(gamma, Place<V, INTER>(s, rot));
+      g.get(ga[k], gb[k]);
+    }
+  }
+}
+
+// What a block works on: queries or keys (blocks from p.first_k on).
+struct Side {
+  int w, block, nblocks, H, slots;
+  long long xs, os;
+  const float *gamma;
+  __device__ __forceinline__ explicit Side(const QkParams &p) {
+    w = static_cast<int>(blockIdx.x) >= p.first_k;
+    block = static_cast<int>(blockIdx.x) - (w ? p.first_k : 0);
+    nblocks = w ? static_cast<int>(gridDim.x) - p.first_k : p.first_k;
+    H = w ? p.H[1] : p.H[0];
+    slots = w ? p.slots[1] : p.slots[0];
+    xs = w ? p.xs[1] : p.xs[0];
+    os = w ? p.os[1] : p.os[0];
+    gamma = w ? p.gamma[1] : p.gamma[0];
+  }
+};
+
+// Forward.  A row belongs to L lanes, V pair slots each (N times); a group of
+// L lanes takes every slots-th head of one token, so that the token's angles
+// stay in its registers, multiplied by gamma once for all its heads.  U rows at
+// a time; the next ones are loaded while these are at work.
+// 4 x 2048 tokens, 40 heads of 128 bf16 (167 MB): the kernel is bound by
+// instruction issue before it is by memory, so what counts is instructions per
+// row: 196 a lane with rows dealt out one by one (38 us).
+template <typename XT, bool INTER, int V, int N, int L, int U>
+__global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? 3 : 1) qk_fwd_kernel(const __grid_constant__ QkTable<table_size<V, L>()> p) {
+  __shared__ unsigned long long turns[table_size<V, L>()];
+  using F = typename Num<V>::F;
+  constexpr int kGroups = kQThr / L, C = Num<V>::kC;
+  const Side sd(p);
+  const int h2 = p.D >> 1, slots = sd.slots;
+  const int lane = threadIdx.x % L, grp = threadIdx.x / L, slot = grp % slots;
+  const long long tok = static_cast<long long>(sd.block) * (kGroups / slots) + grp / slots;
+  const bool norm = sd.gamma != nullptr;
+  const int H = tok < p.ntok ? sd.H : 0;                      // heads of this group's token
+  const XT *x = static_cast<const XT *>(sd.w ? p.x[1] : p.x[0]) + tok * sd.xs;
+  XT *o = static_cast<XT *>(sd.w ? p.out[1] : p.out[0]) + tok * sd.os;
+  const int hop = slots * p.D;
+  Pairs<XT, V, INTER> raw[U][N];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int k = 0; k < N; ++k) raw[u][k].clear();            // what is not loaded adds nothing to a row's sum
+  auto fetch = [&](int h, int off) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int s = (lane + L * k) * V;
+        if (h + u * slots < H && s < h2) raw[u][k].load(x + (off + u * hop), Place<V, INTER>(s, p.rot));
+      }
+  };
+  fetch(slot, slot * p.D);
+  load_turns(p, turns);
+  // y_a = (a gamma_a cos - b gamma_b sin) / rms, y_b = (a gamma_a sin + b gamma_b cos) / rms
+  F ac[N][C], bs[N][C], as[N][C], bc[N][C];
+  {
+    F c[N][C], z[N][C];
+    lane_gamma<V, N, L, INTER>(sd.gamma, lane, p.rot, h2, ac, bc);
+    if (H) lane_angles<V, N, L>(p, turns, tok, lane, c, z);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int e = 0; e < C; ++e) {
+        as[k][e] = f_mul(ac[k][e], z[k][e]);
+        bs[k][e] = f_mul(f_mul(bc[k][e], f_all<F>(-1.f)), z[k][e]);
+        ac[k][e] = f_mul(ac[k][e], c[k][e]);
+        bc[k][e] = f_mul(bc[k][e], c[k][e]);
+      }
+  }
+  // every lane of a warp makes the same number of steps: the row sums exchange
+  // values across it
+  const int steps = (sd.H + slots - 1) / slots;
+  int h = slot, off = slot * p.D;
+  for (int i = 0; i < steps; i += U, h += U * slots, off += U * hop) {
+    F a[U][N][C], b[U][N][C];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < N; ++k) raw[u][k].get(a[u][k], b[u][k]);
+    fetch(h + U * slots, off + U * hop);
+    float inv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      F ss = f_all<F>(0.f);
 #pragma unroll
       for (int k = 0; k < N; ++k)
 #pragma unroll
-        for (int e = 0; e < V; ++e) dga[w][k][e] = dgb[w][k][e] = 0.f;
-  }
-  for (long long tok0 = static_cast<long long>(blockIdx.x) * p.tt; tok0 < p.ntok;
-       tok0 += static_cast<long long>(gridDim.x) * p.tt) {
-    const int nt = static_cast<int>(min(static_cast<long long>(p.tt), p.ntok - tok0));
-    __syncthreads();
-    fill_angles(p, tok0, nt, cs, sn);
-    __syncthreads();
+        for (int e = 0; e < C; ++e) ss = f_fma(a[u][k][e], a[u][k][e], f_fma(b[u][k][e], b[u][k][e], ss));
+      inv[u] = f_sum(ss);
+    }
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const int H = p.H[w], rows = nt * H;
-      if (rows == 0) continue;
-      const bool norm = p.gamma[w] != nullptr;
-      float ga[N][V], gb[N][V];
+    for (int u = 0; u < U; ++u) inv[u] = norm ? inv_root(fmaf(lanes_sum<L>(inv[u]), p.inv_n, p.eps)) : 1.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const F v = f_all<F>(inv[u]);
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         const int s = (lane + L * k) * V;
+        if (h + u * slots < H && s < h2) {
+          F ya[C], yb[C];
 #pragma unroll
-        for (int e = 0; e < V; ++e) ga[k][e] = gb[k][e] = 1.f;
-        if (norm && s < h2) qload_pairs<float, V, INTER>(p.gamma[w], s, p.rot, ga[k], gb[k]);
-      }
-      // every lane of a warp makes the same number of steps: the row sums
-      // exchange values across it
-      for (int r0 = 0; r0 < rows; r0 += kGroups) {
-        const int r = r0 + grp;
-        const bool on = r < rows;
-        const int n = on ? r / H : 0, h = on ? r - n * H : 0;
-        const XT *x = static_cast<const XT *>(p.x[w]) + (tok0 + n) * p.xs[w] + static_cast<long long>(h) * p.D;
-        XT *o = static_cast<XT *>(p.out[w]) + (tok0 + n) * p.os[w] + static_cast<long long>(h) * p.D;
-        float a[N][V], b[N][V], da[N][V], db[N][V];
-        float ss = 0.f, cc = 0.f;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const int s = (lane + L * k) * V;
-#pragma unroll
-          for (int e = 0; e < V; ++e) a[k][e] = b[k][e] = 0.f;
-          if constexpr (BWD) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) da[k][e] = db[k][e] = 0.f;
+          for (int e = 0; e < C; ++e) {
+            ya[e] = f_mul(f_fma(b[u][k][e], bs[k][e], f_mul(a[u][k][e], ac[k][e])), v);
+            yb[e] = f_mul(f_fma(b[u][k][e], bc[k][e], f_mul(a[u][k][e], as[k][e])), v);
           }
-          if (on && s < h2) {
-            qload_pairs<XT, V, INTER>(x, s, p.rot, a[k], b[k]);
-            if constexpr (BWD)
-              qload_pairs<DT, V, INTER>(static_cast<const DT *>(p.dy[w]) + ((tok0 + n) * H + h) * p.D, s, p.rot, da[k],
-                                        db[k]);
-          }
-#pragma unroll
-          for (int e = 0; e < V; ++e) ss = fmaf(a[k][e], a[k][e], fmaf(b[k][e], b[k][e], ss));
-        }
-        if constexpr (BWD) {
-          // dn = R(-theta) dy; with the norm, c = sum dn gamma x
-#pragma unroll
-          for (int k = 0; k < N; ++k) {
-            const int s = (lane + L * k) * V;
-            if (on && s < h2) {
-#pragma unroll
-              for (int e = 0; e < V; ++e) {
-                const float c = cs[n * h2 + s + e], z = sn[n * h2 + s + e];
-                const float u = da[k][e] * c + db[k][e] * z;
-                db[k][e] = db[k][e] * c - da[k][e] * z;
-                da[k][e] = u;
-                cc = fmaf(da[k][e] * ga[k][e], a[k][e], fmaf(db[k][e] * gb[k][e], b[k][e], cc));
-              }
-            }
-          }
-        }
-        float inv = 1.f, coef = 0.f;
-        if (norm) {
-          ss = lanes_sum<L>(ss);
-          const float ms = fmaf(ss, p.inv_n, p.eps);          // rms^2
-          inv = 1.f / sqrtf(ms);
-          if constexpr (BWD) {
-            cc = lanes_sum<L>(cc);
-            coef = cc * p.inv_n / ms;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const int s = (lane + L * k) * V;
-          if (on && s < h2) {
-            float ya[V], yb[V];
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              if constexpr (BWD) {
-                if (norm) {
-                  dga[w][k][e] = fmaf(da[k][e] * a[k][e], inv, dga[w][k][e]);
-                  dgb[w][k][e] = fmaf(db[k][e] * b[k][e], inv, dgb[w][k][e]);
-                  ya[e] = (da[k][e] * ga[k][e] - a[k][e] * coef) * inv;
-                  yb[e] = (db[k][e] * gb[k][e] - b[k][e] * coef) * inv;
-                } else {
-                  ya[e] = da[k][e];
-                  yb[e] = db[k][e];
-                }
-              } else {
-                const float c = cs[n * h2 + s + e], z = sn[n * h2 + s + e];
-                const float u = a[k][e] * inv * ga[k][e], v = b[k][e] * inv * gb[k][e];
-                ya[e] = u * c - v * z;
-                yb[e] = u * z + v * c;
-              }
-            }
-            qstore_pairs<XT, V, INTER>(o, s, p.rot, ya, yb);
-          }
+          Pairs<XT, V, INTER> out;
+          out.set(ya, yb);
+          out.store(o + (off + u * hop), Place<V, INTER>(s, p.rot));
         }
       }
     }
   }
-  if constexpr (BWD) {
-    // one partial dgamma per block, its row groups added in a fixed order
-    if (p.part == nullptr) return;
-    float *sums = ang;                  // [kGroups][D]
+}
+
+// Backward, laid out as the forward; the groups of a block go on to further
+// tokens and keep their lanes' dgamma in registers.  The next row of a group is
+// loaded while this one is at work.  Registers are held to what lets
+// bwd_blocks blocks be resident.
+template <typename XT, typename DT, bool INTER>
+constexpr int bwd_blocks() { return sizeof(XT) + sizeof(DT) == 4 && !INTER ? 4 : 3; }
+
+template <typename XT, typename DT, bool INTER, int V, int N, int L>
+__global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? bwd_blocks<XT, DT, INTER>() : 1)
+    qk_bwd_kernel(const __grid_constant__ QkTable<table_size<V, L>()> p) {
+  extern __shared__ __align__(16) float sums[];               // [kGroups][D], at the end
+  __shared__ unsigned long long turns[table_size<V, L>()];
+  using F = typename Num<V>::F;
+  constexpr int kGroups = kQThr / L, C = Num<V>::kC;
+  const Side sd(p);
+  const int h2 = p.D >> 1, slots = sd.slots, per = kGroups / slots, hop = slots * p.D;
+  const int lane = threadIdx.x % L, grp = threadIdx.x / L, slot = grp % slots;
+  const int steps = (sd.H + slots - 1) / slots;
+  const bool norm = sd.gamma != nullptr;
+  load_turns(p, turns);
+  F ga[N][C], gb[N][C], dga[N][C], dgb[N][C];                 // of this lane's components
+  lane_gamma<V, N, L, INTER>(sd.gamma, lane, p.rot, h2, ga, gb);
+  Pairs<XT, V, INTER> rx[N];
+  Pairs<DT, V, INTER> rd[N];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      __syncthreads();
+  for (int k = 0; k < N; ++k) {
+#pragma unroll
+    for (int e = 0; e < C; ++e) dga[k][e] = dgb[k][e] = f_all<F>(0.f);
+  }
+  for (long long tok0 = static_cast<long long>(sd.block) * per; tok0 < p.ntok;
+       tok0 += static_cast<long long>(sd.nblocks) * per) {
+    const long long tok = tok0 + grp / slots;
+    const int H = tok < p.ntok ? sd.H : 0;                    // heads of this group's token
+    const XT *x = static_cast<const XT *>(sd.w ? p.x[1] : p.x[0]) + tok * sd.xs;
+    const DT *d = static_cast<const DT *>(sd.w ? p.dy[1] : p.dy[0]) + tok * sd.H * p.D;
+    XT *o = static_cast<XT *>(sd.w ? p.out[1] : p.out[0]) + tok * sd.os;
+    int h = slot, off = slot * p.D;
+    auto fetch = [&](int h, int off) {
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         const int s = (lane + L * k) * V;
-        if (s < h2) qstore_pairs<float, V, INTER>(sums + grp * p.D, s, p.rot, dga[w][k], dgb[w][k]);
+        if (h < H && s < h2) {
+          rx[k].load(x + off, Place<V, INTER>(s, p.rot));
+          rd[k].load(d + off, Place<V, INTER>(s, p.rot));
+        } else {                                              // (adds nothing to sums and dgamma)
+          rx[k].clear();
+          rd[k].clear();
+        }
       }
-      __syncthreads();
-      for (int i = threadIdx.x; i < p.D; i += kQThr) {
-        float t = 0.f;
-        for (int g = 0; g < kGroups; ++g) t += sums[g * p.D + i];
-        p.part[(static_cast<size_t>(blockIdx.x) * 2 + w) * p.D + i] = t;
+    };
+    fetch(h, off);
+    F c[N][C], z[N][C];
+    if (H) {
+      lane_angles<V, N, L>(p, turns, tok, lane, c, z);
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int e = 0; e < C; ++e) c[k][e] = z[k][e] = f_all<F>(0.f);
+    }
+    // every lane of a warp makes the same number of steps: the row sums
+    // exchange values across it
+    for (int i = 0; i < steps; ++i, h += slots, off += hop) {
+      F a[N][C], b[N][C], u[N][C], v[N][C];
+      F ss = f_all<F>(0.f), cc = f_all<F>(0.f);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        F da[C], db[C];
+        rx[k].get(a[k], b[k]);
+        rd[k].get(da, db);
+        // dn = R(-theta) dy; with the norm, c = sum dn gamma x
+#pragma unroll
+        for (int e = 0; e < C; ++e) {
+          u[k][e] = f_fma(db[e], z[k][e], f_mul(da[e], c[k][e]));
+          v[k][e] = f_fma(db[e], c[k][e], f_mul(f_mul(da[e], f_all<F>(-1.f)), z[k][e]));
+        }
+      }
+      fetch(h + slots, off + hop);
+      float inv = 1.f, coef = 0.f;
+      if (norm) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+          for (int e = 0; e < C; ++e) {
+            ss = f_fma(a[k][e], a[k][e], f_fma(b[k][e], b[k][e], ss));
+            cc = f_fma(f_mul(u[k][e], ga[k][e]), a[k][e], f_fma(f_mul(v[k][e], gb[k][e]), b[k][e], cc));
+          }
+        const float s2 = lanes_sum<L>(f_sum(ss)), c2 = lanes_sum<L>(f_sum(cc));
+        inv = inv_root(fmaf(s2, p.inv_n, p.eps));
+        coef = -c2 * p.inv_n * (inv * inv);                   // -c / (D rms^2)
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+          for (int e = 0; e < C; ++e) {
+            const F r = f_all<F>(inv), xa = f_mul(a[k][e], r), xb = f_mul(b[k][e], r);
+            const F ua = f_mul(f_mul(u[k][e], ga[k][e]), r), vb = f_mul(f_mul(v[k][e], gb[k][e]), r);
+            dga[k][e] = f_fma(u[k][e], xa, dga[k][e]);
+            dgb[k][e] = f_fma(v[k][e], xb, dgb[k][e]);
+            u[k][e] = f_fma(xa, f_all<F>(coef), ua);
+            v[k][e] = f_fma(xb, f_all<F>(coef), vb);
+          }
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int s = (lane + L * k) * V;
+        if (h < H && s < h2) {
+          Pairs<XT, V, INTER> out;
+          out.set(u[k], v[k]);
+          out.store(o + off, Place<V, INTER>(s, p.rot));
+        }
       }
     }
+  }
+  // one partial dgamma per block, its row groups added in a fixed order
+  if (p.part == nullptr) return;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int s = (lane + L * k) * V;
+    if (s < h2) {
+      Pairs<float, V, INTER> out;
+      out.set(dga[k], dgb[k]);
+      out.store(sums + grp * p.D, Place<V, INTER>(s, p.rot));
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.D; i += kQThr) {
+    float t = 0.f;
+    for (int g = 0; g < kGroups; ++g) t += sums[g * p.D + i];
+    p.part[static_cast<size_t>(blockIdx.x) * p.D + i] = t;
   }
 }
 
 // dgamma = sum of the blocks' partials, in a fixed order: a block takes 32
-// columns, its 8 warps every 8th partial.
+// components of queries or keys, its 8 warps every 8th partial.
 __global__ void __launch_bounds__(256) qk_dgamma_kernel(const float *__restrict__ part, float *__restrict__ dgq,
-                                                        float *__restrict__ dgk, int nparts, int D) {
+                                                        float *__restrict__ dgk, int first_k, int nparts, int D) {
   __shared__ float red[8][32];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + lane;               // of [2][D]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + lane;
+  float *dst = blockIdx.y ? dgk : dgq;
+  const int lo = blockIdx.y ? first_k : 0, hi = blockIdx.y ? nparts : first_k;
+  if (!dst) return;
   float t = 0.f;
-  if (col < 2 * D)
-    for (int i = w; i < nparts; i += 8) t += part[static_cast<size_t>(i) * 2 * D + col];
-  red[w][lane] = t;
+  if (col < D)
+    for (int i = lo + warp; i < hi; i += 8) t += part[static_cast<size_t>(i) * D + col];
+  red[warp][lane] = t;
   __syncthreads();
-  if (w == 0 && col < 2 * D) {
+  if (warp == 0 && col < D) {
     for (int i = 1; i < 8; ++i) t += red[i][lane];
-    float *dst = col < D ? dgq : dgk;
-    if (dst) dst[col < D ? col : col - D] = t;
+    dst[col] = t;
   }
 }
 
 template <typename XT, typename DT, bool BWD, bool INTER, int V, int N, int L>
-cudaError_t qk_launch(QkParams &p, const unsigned long long *freq, int max_blocks, int sms, cudaStream_t st) {
-  // Tokens per block and step: enough rows for every row group, four times
-  // over when there are tokens for all SMs.
-  constexpr int kGroups = kQThr / L;
-  const int H = p.H[0] + p.H[1];
-  int tt = (4 * kGroups + H - 1) / H;
-  if (tt > 16) tt = 16;
-  while (tt > 1 && (p.ntok + tt - 1) / tt < 4 * sms) tt >>= 1;
-  p.tt = tt;
-  long long blocks = (p.ntok + tt - 1) / tt;
-  if (BWD && blocks > max_blocks) blocks = max_blocks;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  size_t smem = static_cast<size_t>(tt) * p.D * 4;
-  if (BWD && smem < static_cast<size_t>(kGroups) * p.D * 4) smem = static_cast<size_t>(kGroups) * p.D * 4;
+cudaError_t qk_launch(QkParams &p, const unsigned long long *freq, int sms, cudaStream_t st) {
+  // Lane groups per token: one forms the token's angles once for all its heads,
+  // more of them keep the SMs busy when tokens are few.  Up to kFill groups an
+  // SM as long as each has four rows (2050 tokens, 20 + 5 heads of 80 fp32:
+  // 12 us, with fewer rows each 16), up to a block an SM in any case.
+  constexpr int kGroups = kQThr / L, kFill = 4 * kGroups;
+  long long blocks[2];
+  for (int w = 0; w < 2; ++w) {
+    int slots = 1;
+    while (slots < kGroups && 8 * slots <= p.H[w] && p.ntok * slots < static_cast<long long>(kFill) * sms) slots *= 2;
+    while (slots < kGroups && slots < p.H[w] && p.ntok * slots < static_cast<long long>(kGroups) * sms) slots *= 2;
+    p.slots[w] = slots;
+    const int per = kGroups / slots;
+    blocks[w] = p.H[w] ? (p.ntok + per - 1) / per : 0;
+  }
+  if (BWD) {
+    // resident blocks, shared out by the number of heads
+    const long long all = (V == 4 && N == 1 ? bwd_blocks<XT, DT, INTER>() : 2) * static_cast<long long>(sms);
+    const long long most = all < kQkParts ? all : kQkParts;
+    long long q = most * p.H[0] / (p.H[0] + p.H[1]);
+    if (p.H[0] && q < 1) q = 1;
+    if (p.H[1] && q > most - 1) q = most - 1;
+    if (blocks[0] > q) blocks[0] = q;
+    if (blocks[1] > most - q) blocks[1] = most - q;
+  }
+  if (blocks[0] + blocks[1] > 0x7fffffffLL) return cudaErrorInvalidValue;
+  p.first_k = static_cast<int>(blocks[0]);
   QkTable<table_size<V, L>()> t;
   static_cast<QkParams &>(t) = p;
   for (int i = 0; i < p.rot; ++i) t.freq[i] = freq[i];
-  qk_kernel<XT, DT, BWD, INTER, V, N, L><<<static_cast<unsigned>(blocks), kQThr, smem, st>>>(t);
-  p.tt = static_cast<int>(blocks);                      // for the caller: partials written
+  const unsigned grid = static_cast<unsigned>(blocks[0] + blocks[1]);
+  if constexpr (BWD) {
+    const size_t smem = p.part ? static_cast<size_t>(kGroups) * p.D * 4 : 0;
+    qk_bwd_kernel<XT, DT, INTER, V, N, L><<<grid, kQThr, smem, st>>>(t);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !p.part) return e;
+    const dim3 g((p.D + 31) / 32, 2);
+    qk_dgamma_kernel<<<g, 256, 0, st>>>(p.part, p.dgamma[0], p.dgamma[1], p.first_k, static_cast<int>(grid), p.D);
+  } else {
+    constexpr int U = V == 1 || N > 1 ? 1 : 2;
+    qk_fwd_kernel<XT, INTER, V, N, L, U><<<grid, kQThr, 0, st>>>(t);
+  }
   return cudaGetLastError();
 }
 
 template <typename XT, typename DT, bool BWD, bool INTER>
-cudaError_t qk_dispatch(QkParams &p, const unsigned long long *freq, bool vec, int max_blocks, int sms, cudaStream_t st) {
-  if (!vec) return qk_launch<XT, DT, BWD, INTER, 1, 8, 32>(p, freq, max_blocks, sms, st);
-  if (p.D <= 64) return qk_launch<XT, DT, BWD, INTER, 4, 1, 8>(p, freq, max_blocks, sms, st);
-  if (p.D <= 128) return qk_launch<XT, DT, BWD, INTER, 4, 1, 16>(p, freq, max_blocks, sms, st);
-  if (p.D <= 256) return qk_launch<XT, DT, BWD, INTER, 4, 1, 32>(p, freq, max_blocks, sms, st);
-  return qk_launch<XT, DT, BWD, INTER, 4, 2, 32>(p, freq, max_blocks, sms, st);
+cudaError_t qk_dispatch(QkParams &p, const unsigned long long *freq, bool vec, int sms, cudaStream_t st) {
+  if (!vec) return qk_launch<XT, DT, BWD, INTER, 1, 8, 32>(p, freq, sms, st);
+  if (p.D <= 64) return qk_launch<XT, DT, BWD, INTER, 4, 1, 8>(p, freq, sms, st);
+  if (p.D <= 128) return qk_launch<XT, DT, BWD, INTER, 4, 1, 16>(p, freq, sms, st);
+  if (p.D <= 256) return qk_launch<XT, DT, BWD, INTER, 4, 1, 32>(p, freq, sms, st);
+  return qk_launch<XT, DT, BWD, INTER, 4, 2, 32>(p, freq, sms, st);
 }
 
 // Turns per position of each pair, mod 1, as 64-bit binary fractions.  A model
@@ -370,7 +617,7 @@ bool at16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
 
-size_t qk_norm_rope_bwd_workspace_bytes(int D) { return static_cast<size_t>(kQkParts) * 2 * D * 4; }
+size_t qk_norm_rope_bwd_workspace_bytes(int D) { return static_cast<size_t>(kQkParts) * D * 4; }
 
 cudaError_t launch_qk_norm_rope(const QkNormRopeArgs &a, cudaStream_t st) {
   int dev = 0, sms = 0;
@@ -386,7 +633,7 @@ cudaError_t launch_qk_norm_rope(const QkNormRopeArgs &a, cudaStream_t st) {
   bool vec = a.D % 8 == 0 && (a.interleaved || rot % 4 == 0);
   const long long unit = a.bf16 ? 8 : 4;
   for (int w = 0; w < 2; ++w) {
-    p.x[w] = a.x[w], p.dy[w] = a.dy[w], p.out[w] = a.out[w], p.gamma[w] = a.gamma[w];
+    p.x[w] = a.x[w], p.dy[w] = a.dy[w], p.out[w] = a.out[w], p.gamma[w] = a.gamma[w], p.dgamma[w] = a.dgamma[w];
     p.xs[w] = a.x_stride[w], p.os[w] = a.out_stride[w];
     p.H[w] = a.H[w];
     if (a.H[w] == 0) continue;
@@ -398,38 +645,34 @@ cudaError_t launch_qk_norm_rope(const QkNormRopeArgs &a, cudaStream_t st) {
   p.eps = a.eps;
   p.inv_n = 1.f / static_cast<float>(a.D);
   p.pos = a.positions;
-  p.axes = a.n_axes;
-  for (int i = 0, end = 0; i < 4; ++i) {
-    end += i < a.n_axes ? a.sections[i] : 0;
-    p.sec_end[i] = end;
+  for (int i = 0, end = 0; i < 3; ++i) {
+    end += a.sections[i];
+    p.sec_end[i] = i + 1 < a.n_axes ? end : 0x7fffffff;
   }
   const unsigned long long *freq = turn_table(a.base, a.rotary_dim);
-  if (p.ntok > 0) {
+  if (p.ntok > 0 && a.H[0] + a.H[1] > 0) {
     if (!bwd) {
       if (a.bf16)
-        e = a.interleaved ? qk_dispatch<__nv_bfloat16, float, false, true>(p, freq, vec, 0, sms, st)
-                          : qk_dispatch<__nv_bfloat16, float, false, false>(p, freq, vec, 0, sms, st);
+        e = a.interleaved ? qk_dispatch<__nv_bfloat16, float, false, true>(p, freq, vec, sms, st)
+                          : qk_dispatch<__nv_bfloat16, float, false, false>(p, freq, vec, sms, st);
       else
-        e = a.interleaved ? qk_dispatch<float, float, false, true>(p, freq, vec, 0, sms, st)
-                          : qk_dispatch<float, float, false, false>(p, freq, vec, 0, sms, st);
+        e = a.interleaved ? qk_dispatch<float, float, false, true>(p, freq, vec, sms, st)
+                          : qk_dispatch<float, float, false, false>(p, freq, vec, sms, st);
       return e;
     }
-    const int most = kQkParts < 4 * sms ? kQkParts : 4 * sms;
     const int how = (a.bf16 ? 4 : 0) | (a.dy_bf16 ? 2 : 0) | (a.interleaved ? 1 : 0);
     using bf = __nv_bfloat16;
     switch (how) {
-      case 0: e = qk_dispatch<float, float, true, false>(p, freq, vec, most, sms, st); break;
-      case 1: e = qk_dispatch<float, float, true, true>(p, freq, vec, most, sms, st); break;
-      case 2: e = qk_dispatch<float, bf, true, false>(p, freq, vec, most, sms, st); break;
-      case 3: e = qk_dispatch<float, bf, true, true>(p, freq, vec, most, sms, st); break;
-      case 4: e = qk_dispatch<bf, float, true, false>(p, freq, vec, most, sms, st); break;
-      case 5: e = qk_dispatch<bf, float, true, true>(p, freq, vec, most, sms, st); break;
-      case 6: e = qk_dispatch<bf, bf, true, false>(p, freq, vec, most, sms, st); break;
-      default: e = qk_dispatch<bf, bf, true, true>(p, freq, vec, most, sms, st); break;
+      case 0: e = qk_dispatch<float, float, true, false>(p, freq, vec, sms, st); break;
+      case 1: e = qk_dispatch<float, float, true, true>(p, freq, vec, sms, st); break;
+      case 2: e = qk_dispatch<float, bf, true, false>(p, freq, vec, sms, st); break;
+      case 3: e = qk_dispatch<float, bf, true, true>(p, freq, vec, sms, st); break;
+      case 4: e = qk_dispatch<bf, float, true, false>(p, freq, vec, sms, st); break;
+      case 5: e = qk_dispatch<bf, float, true, true>(p, freq, vec, sms, st); break;
+      case 6: e = qk_dispatch<bf, bf, true, false>(p, freq, vec, sms, st); break;
+      default: e = qk_dispatch<bf, bf, true, true>(p, freq, vec, sms, st); break;
     }
-    if (e != cudaSuccess || !p.part) return e;
-    qk_dgamma_kernel<<<(2 * a.D + 31) / 32, 256, 0, st>>>(p.part, a.dgamma[0], a.dgamma[1], p.tt, a.D);
-    return cudaGetLastError();
+    return e;
   }
   for (int w = 0; w < 2 && bwd && e == cudaSuccess; ++w)
     if (a.dgamma[w]) e = cudaMemsetAsync(a.dgamma[w], 0, static_cast<size_t>(a.D) * 4, st);

@@ -194,33 +194,6 @@ __device__ __forceinline__ void ld16_wait(uint32_t ta, uint32_t (&r)[16]) {
       : "memory");
 }
 
-// The same 16 columns of N accumulators (N = 2 or 3), one wait.
-template <int N>
-__device__ __forceinline__ void ld16n_wait(const uint32_t (&t)[N], uint32_t (&r)[16 * N]) {
-  static_assert(N == 2 || N == 3, "two or three accumulators");
-  if constexpr (N == 2)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : ABW_TC_R16(0), ABW_TC_R16(16)
-        : "r"(t[0]), "r"(t[1])
-        : "memory");
-  else
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%48];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%49];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47}, [%50];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : ABW_TC_R16(0), ABW_TC_R16(16), ABW_TC_R16(32)
-        : "r"(t[0]), "r"(t[1]), "r"(t[2])
-        : "memory");
-}
 #undef ABW_TC_R16
 #define ABW_TC_RW16(o) \
   "+r"(r[o + 0]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), "+r"(r[o + 5]), \
