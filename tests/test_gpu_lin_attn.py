@@ -136,6 +136,28 @@ def test_padded_batch(abw, lengths, D):
             assert bool((x[b, min(max(n, 0), 300):] == 0).all())
 
 
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(300, 6, 2, 128), (512, 4, 4, 64), (700, 3, 1, 64), (769, 2, 2, 128)])
+def test_padded_batch_without_states(abw, T, Hq, Hkv, D):
+    """No state comes in or goes out: short batches take their other chunks
+    directly, longer ones through states (both directions differ in where
+    that changes)."""
+    lengths = [T, 129, 0, 1, 128, 257]
+    t = make(T, 6, T, Hq, Hkv, D, decay=torch.tensor([-0.004, -0.5])[:Hkv] if Hkv < 3 else -0.03)
+    clean = check(abw, t, lengths)
+    for b, n in enumerate(lengths):
+        for x, bad in (("q", float("nan")), ("k", float("inf")), ("v", float("nan")), ("do", -float("inf"))):
+            t[x][b, n:] = bad
+    d = {x: cuda(y) for x, y in t.items()}
+    ln = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    o = abw.lin_attn_fwd(d["q"], d["k"], d["v"], d["ld"], 0.125, lengths=ln)
+    g = abw.lin_attn_bwd(d["q"], d["k"], d["v"], d["do"], d["ld"], 0.125, lengths=ln)
+    abw.device_check()
+    for a, b in zip(clean, o + g):
+        assert (a is None and b is None) or torch.equal(a, b)
+    for decay in (0.0, -20.0, -math.inf):
+        check(abw, make(T + 1, 1, T, Hq, Hkv, D, decay=decay))
+
+
 def test_states_wanted_or_not(abw):
     """Every mix of states that come in and go out, over one chunk and more."""
     for T in (100, 200):

@@ -361,8 +361,11 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _call(op, fn, dev, stream, *args):
-    """Launches on the tensors' device, on `stream` or its current stream."""
+def _call(op, fn, dev, stream, need, workspace, *args):
+    """Launches on the tensors' device, on `stream` or its current stream.
+    `need` bytes of workspace, where the caller gave none, are held for the
+    launch alone: the caching allocator hands them out again in that stream's
+    order."""
     index = dev.index
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
@@ -370,11 +373,22 @@ def _call(op, fn, dev, stream, *args):
         handle = stream.cuda_stream
     else:
         raise ValueError(f"{op}: stream on {stream.device}, tensors on {dev}")
-    if index == torch._C._cuda_getDevice():
-        status = fn(*args, handle)
-    else:
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
-            status = fn(*args, handle)
+            return _call(op, fn, dev, stream, need, workspace, *args)
+    if need is None:
+        status = fn(*args, handle)
+    elif workspace is not None:
+        at = _dense(workspace, "workspace", torch.uint8, getattr(workspace, "shape", ()), dev)
+        status = fn(*args, at, workspace.numel(), handle)
+    elif need == 0:
+        status = fn(*args, None, 0, handle)
+    else:
+        at = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, handle)
+        try:
+            status = fn(*args, at, need, handle)
+        finally:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(at)
     if status:
         _b.check(status, op)
 
@@ -406,8 +420,11 @@ def qk_norm_rope_fwd(q, k, gamma_q=None, gamma_k=None, eps=1e-6, rope_base=0.0, 
     dt, qshape = q.dtype, q.shape
     B, T, Hq, D = qshape
     qs = _rows(q, "q", dt, qshape, dev)
-    q_out = _empty(qshape, dt, dev, stream) if q_out is None else q_out
-    qo = _dense(q_out, "q_out", dt, qshape, dev)
+    if q_out is None:
+        q_out = _empty(qshape, dt, dev, stream)
+        qo = q_out.data_ptr()
+    else:
+        qo = _dense(q_out, "q_out", dt, qshape, dev)
     Hkv = ks = 0
     kp = ko = None
     if k is not None:
@@ -415,15 +432,18 @@ def qk_norm_rope_fwd(q, k, gamma_q=None, gamma_k=None, eps=1e-6, rope_base=0.0, 
         kshape = (B, T, Hkv, D)
         ks = _rows(k, "k", dt, kshape, dev)
         kp = k.data_ptr()
-        k_out = _empty(kshape, dt, dev, stream) if k_out is None else k_out
-        ko = _dense(k_out, "k_out", dt, kshape, dev)
+        if k_out is None:
+            k_out = _empty(kshape, dt, dev, stream)
+            ko = k_out.data_ptr()
+        else:
+            ko = _dense(k_out, "k_out", dt, kshape, dev)
     else:
         k_out = None
     gq = None if gamma_q is None else _dense(gamma_q, "gamma_q", _F32, (D,), dev)
     gk = None if gamma_k is None else _dense(gamma_k, "gamma_k", _F32, (D,), dev)
     R, pos, axes, host = _rotation(B, T, D, rope_base, rotary_dim, positions, sections, dev)
-    _call("qk_norm_rope_fwd", _fns().qk_norm_rope_fwd, dev, stream, q.data_ptr(), kp, _DT[dt], gq, gk, qo, ko, B, T, Hq,
-          Hkv, D, qs, ks, float(eps), float(rope_base), R, 1 if interleaved else 0, pos, axes, host, int(pos0))
+    _call("qk_norm_rope_fwd", _fns().qk_norm_rope_fwd, dev, stream, None, None, q.data_ptr(), kp, _DT[dt], gq, gk, qo, ko,
+          B, T, Hq, Hkv, D, qs, ks, float(eps), float(rope_base), R, 1 if interleaved else 0, pos, axes, host, int(pos0))
     return q_out, k_out
 
 
@@ -446,8 +466,11 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, gamma_q=None, gamma_k=None, eps=1e-6,
     B, T, Hq, D = qshape
     qs = _rows(q, "q", dt, qshape, dev)
     yq = _dense(dq_out, "dq_out", yt, qshape, dev)
-    dq = _empty(qshape, dt, dev, stream) if dq is None else dq
-    dqs = _rows(dq, "dq", dt, qshape, dev)
+    dqs = 0
+    if dq is None:
+        dq = _empty(qshape, dt, dev, stream)
+    else:
+        dqs = _rows(dq, "dq", dt, qshape, dev)
     Hkv = ks = dks = 0
     kp = yk = dkp = gq = gk = dgq = dgk = None
     if k is not None:
@@ -455,37 +478,37 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, gamma_q=None, gamma_k=None, eps=1e-6,
         kshape = (B, T, Hkv, D)
         ks = _rows(k, "k", dt, kshape, dev)
         yk = _dense(dk_out, "dk_out", yt, kshape, dev)
-        dk = _empty(kshape, dt, dev, stream) if dk is None else dk
-        dks = _rows(dk, "dk", dt, kshape, dev)
+        if dk is None:
+            dk = _empty(kshape, dt, dev, stream)
+        else:
+            dks = _rows(dk, "dk", dt, kshape, dev)
         kp, dkp = k.data_ptr(), dk.data_ptr()
     else:
         dk = gamma_k = None
     if gamma_q is not None:
         gq = _dense(gamma_q, "gamma_q", _F32, (D,), dev)
-        dgamma_q = _empty((D,), _F32, dev, stream) if dgamma_q is None else dgamma_q
-        dgq = _dense(dgamma_q, "dgamma_q", _F32, (D,), dev)
+        if dgamma_q is None:
+            dgamma_q = _empty((D,), _F32, dev, stream)
+            dgq = dgamma_q.data_ptr()
+        else:
+            dgq = _dense(dgamma_q, "dgamma_q", _F32, (D,), dev)
     else:
         dgamma_q = None
     if gamma_k is not None:
         gk = _dense(gamma_k, "gamma_k", _F32, (D,), dev)
-        dgamma_k = _empty((D,), _F32, dev, stream) if dgamma_k is None else dgamma_k
-        dgk = _dense(dgamma_k, "dgamma_k", _F32, (D,), dev)
+        if dgamma_k is None:
+            dgamma_k = _empty((D,), _F32, dev, stream)
+            dgk = dgamma_k.data_ptr()
+        else:
+            dgk = _dense(dgamma_k, "dgamma_k", _F32, (D,), dev)
     else:
         dgamma_k = None
     R, pos, axes, host = _rotation(B, T, D, rope_base, rotary_dim, positions, sections, dev)
-    wp, wn = _workspace(workspace, qk_norm_rope_bwd_workspace_bytes(D) if gq or gk else 0, dev, stream)
-    _call("qk_norm_rope_bwd", _fns().qk_norm_rope_bwd, dev, stream, q.data_ptr(), kp, _DT[dt], yq, yk, _DT[yt], gq, gk,
-          dq.data_ptr(), dkp, dgq, dgk, B, T, Hq, Hkv, D, qs, ks, dqs, dks, float(eps), float(rope_base), R,
-          1 if interleaved else 0, pos, axes, host, int(pos0), wp if wp is None else wp.data_ptr(), wn)
+    need = qk_norm_rope_bwd_workspace_bytes(D) if gq or gk else 0
+    _call("qk_norm_rope_bwd", _fns().qk_norm_rope_bwd, dev, stream, need, workspace, q.data_ptr(), kp, _DT[dt], yq, yk,
+          _DT[yt], gq, gk, dq.data_ptr(), dkp, dgq, dgk, B, T, Hq, Hkv, D, qs, ks, dqs, dks, float(eps), float(rope_base), R,
+          1 if interleaved else 0, pos, axes, host, int(pos0))
     return dq, dk, dgamma_q, dgamma_k
-
-
-def _workspace(given, need, dev, stream):
-    """(tensor or None, bytes): the caller's workspace, or one for this call."""
-    if given is None:
-        return (None, 0) if need == 0 else (_empty((need,), torch.uint8, dev, stream), need)
-    _dense(given, "workspace", torch.uint8, given.shape if isinstance(given, torch.Tensor) else (need,), dev)
-    return given, given.numel()
 
 
 @functools.lru_cache(maxsize=1024)
@@ -525,14 +548,16 @@ def lin_attn_fwd(q, k, v, log_decay, scale=None, initial_state=None, lengths=Non
     initial_state tensor."""
     dev, dims, _, sshape, strides, (qp, kp, vp, ldp, s0, ln) = _lin_inputs(q, k, v, log_decay, initial_state, lengths)
     B, T, Hq, Hkv, D = dims
-    o = _empty(q.shape, _BF16, dev, stream) if o is None else o
-    os = _rows(o, "o", _BF16, q.shape, dev)
+    os = 0
+    if o is None:
+        o = _empty(q.shape, _BF16, dev, stream)
+    else:
+        os = _rows(o, "o", _BF16, q.shape, dev)
     if final_state is None and want_final_state:
         final_state = _empty(sshape, _F32, dev, stream)
     fin = None if final_state is None else _dense(final_state, "final_state", _F32, sshape, dev)
-    ws, wn = _workspace(workspace, lin_attn_fwd_workspace_bytes(B, T, Hkv, D), dev, stream)
-    _call("lin_attn_fwd", _fns().lin_attn_fwd, dev, stream, qp, kp, vp, ldp, s0, ln, o.data_ptr(), fin, *dims, *strides,
-          os, 1.0 / math.sqrt(D) if scale is None else float(scale), ws if ws is None else ws.data_ptr(), wn)
+    _call("lin_attn_fwd", _fns().lin_attn_fwd, dev, stream, lin_attn_fwd_workspace_bytes(B, T, Hkv, D), workspace, qp,
+          kp, vp, ldp, s0, ln, o.data_ptr(), fin, *dims, *strides, os, 1.0 / math.sqrt(D) if scale is None else float(scale))
     return o, final_state
 
 
@@ -545,17 +570,17 @@ def lin_attn_bwd(q, k, v, dout, log_decay, scale=None, initial_state=None, dfina
     B, T, Hq, Hkv, D = dims
     dop = _dense(dout, "dout", _BF16, q.shape, dev)
     dfp = None if dfinal_state is None else _dense(dfinal_state, "dfinal_state", _F32, sshape, dev)
+    outs = (0 if dq is None else _rows(dq, "dq", _BF16, q.shape, dev),
+            0 if dk is None else _rows(dk, "dk", _BF16, kshape, dev),
+            0 if dv is None else _rows(dv, "dv", _BF16, kshape, dev))
     dq = _empty(q.shape, _BF16, dev, stream) if dq is None else dq
     dk = _empty(kshape, _BF16, dev, stream) if dk is None else dk
     dv = _empty(kshape, _BF16, dev, stream) if dv is None else dv
-    outs = (_rows(dq, "dq", _BF16, q.shape, dev), _rows(dk, "dk", _BF16, kshape, dev), _rows(dv, "dv", _BF16, kshape, dev))
     if dinitial_state is None and want_dinitial_state:
         dinitial_state = _empty(sshape, _F32, dev, stream)
     dsp = None if dinitial_state is None else _dense(dinitial_state, "dinitial_state", _F32, sshape, dev)
-    ws, wn = _workspace(workspace, lin_attn_bwd_workspace_bytes(B, T, Hkv, D), dev, stream)
-    _call("lin_attn_bwd", _fns().lin_attn_bwd, dev, stream, qp, kp, vp, dop, ldp, s0, dfp, ln, dq.data_ptr(), dk.data_ptr(),
-          dv.data_ptr(), dsp, *dims, *strides, *outs, 1.0 / math.sqrt(D) if scale is None else float(scale),
-          ws if ws is None else ws.data_ptr(), wn)
+    _call("lin_attn_bwd", _fns().lin_attn_bwd, dev, stream, lin_attn_bwd_workspace_bytes(B, T, Hkv, D), workspace, qp,
+          kp, vp, dop, ldp, s0, dfp, ln, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dsp, *dims, *strides, *outs, 1.0 / math.sqrt(D) if scale is None else float(scale))
     return dq, dk, dv, dinitial_state
 
 
@@ -574,8 +599,12 @@ def lin_attn_decode(q, k, v, state, log_decay, scale=None, slots=None, o=None, s
     qp, kp, vp = (_dense(q, "q", dt, qshape, dev), _dense(k, "k", dt, kshape, dev), _dense(v, "v", dt, kshape, dev))
     sp, lp = _dense(state, "state", _F32, (n, Hkv, D, D), dev), _dense(log_decay, "log_decay", _F32, (Hkv,), dev)
     sl = None if slots is None else _dense(slots, "slots", torch.int32, (B,), dev)
-    o = _empty(qshape, dt, dev, stream) if o is None else o
-    _call("lin_attn_decode", _fns().lin_attn_decode, dev, stream, qp, kp, vp, _DT[dt], sp, lp, sl,
-          _dense(o, "o", dt, qshape, dev), B, Hq, Hkv, D, n,
+    if o is None:
+        o = _empty(qshape, dt, dev, stream)
+        op = o.data_ptr()
+    else:
+        op = _dense(o, "o", dt, qshape, dev)
+    _call("lin_attn_decode", _fns().lin_attn_decode, dev, stream, None, None, qp, kp, vp, _DT[dt], sp, lp, sl,
+          op, B, Hq, Hkv, D, n,
           1.0 / math.sqrt(D) if scale is None else float(scale))
     return o

@@ -27,6 +27,10 @@ bool encode_tiled(CUtensorMap *map, CUtensorMapDataType dt, uint32_t rank, const
                   const uint64_t *dims, const uint64_t *strides_bytes, const uint32_t *box,
                   CUtensorMapSwizzle swizzle, const char **why);
 
+// Points an encoded map at another buffer of the same layout
+// (cuTensorMapReplaceAddress).  Returns false where that is not available.
+bool move_tiled(CUtensorMap *map, const void *base);
+
 // Raises a kernel's dynamic shared-memory limit on the current device to at
 // least `bytes`, calling the runtime only when the limit has to grow: calls
 // after the first make no runtime call for it (which keeps them free of

@@ -292,6 +292,21 @@ bool encode_tiled(CUtensorMap *map, CUtensorMapDataType dt, uint32_t rank, const
   return true;
 }
 
+bool move_tiled(CUtensorMap *map, const void *base) {
+  using Fn = CUresult (*)(CUtensorMap *, void *);
+  static Fn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapReplaceAddress", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<Fn>(p);
+  });
+  return fn && fn(map, const_cast<void *>(base)) == CUDA_SUCCESS;
+}
+
 }  // namespace abw
 
 // ============================================================================

@@ -19,6 +19,9 @@
 //               that enters each of them as a bf16 tile in the workspace
 //   lin_out   : one item per 128 output rows; everything it needs is there,
 //               so items run in any order
+// Short sequences without states at their ends take the second alone: an item
+// goes through the products of the chunks before it (behind it) as well, which
+// for a few chunks costs less than the walk and its launch.
 // No element of a decay power above a^0 is formed, so strong decays underflow
 // to 0 and never overflow.
 #include <math.h>
@@ -31,6 +34,11 @@ namespace {
 
 constexpr int kC = 128;               // tokens per chunk
 constexpr int kSub = 64;              // tokens per TMA box: half a chunk
+// Most chunks whose outputs are formed without states.  Forward / backward us,
+// with the walk and without: 2 x 512 tokens of 20/5 heads 14.8 / 24.5, 12.0 / 25.6
+// (and a launch less); 4 x 768 of 20 34 / 67, 25 / 56; 2 x 768 of 20/5 16.7 / 32,
+// 17.3 / 39; 1 x 1024 of 32 18.8 / 37, 18.6 / 39.
+constexpr int kDirectFwd = 6, kDirectBwd = 4;
 
 __device__ __forceinline__ uint32_t lpack2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -404,6 +412,7 @@ static_assert(kOOffAbort + 4 <= kOOffBar + 256 && kOSmem <= 232448, "output kern
 struct LinOutParams {
   LinSizes z;
   int backward;
+  int direct;                         // no state tiles: an item takes the other chunks itself
   int items;
   int start[2];                       // a state enters the first chunk / comes from behind the last
   const __nv_bfloat16 *tiles[2];
@@ -414,8 +423,8 @@ struct LinOutParams {
 };
 
 struct LinItem {
-  int role, b, kv, h, n, L, gi;       // h: head of the output
-  bool st;                            // has a state tile
+  int role, b, kv, h, n, len, L, ns, gi;   // h: head of the output; ns: chunks of B and C; gi: (B, C) pairs
+  bool st;                                 // has a state tile
 };
 
 __device__ __noinline__ LinItem lin_item(const LinOutParams &p, int i) {
@@ -446,16 +455,19 @@ __device__ __noinline__ LinItem lin_item(const LinOutParams &p, int i) {
   i /= p.z.Hkv;
   it.n = i % NC;
   it.b = i / NC;
-  const int len = seq_len(p.z.lengths, it.b, p.z.T);
-  it.L = min(kC, len - it.n * kC);
+  if (p.direct && it.role < 2) it.n = NC - 1 - it.n;          // the longer items first
+  it.len = seq_len(p.z.lengths, it.b, p.z.T);
+  it.L = min(kC, it.len - it.n * kC);
   if (it.role < 2) {
     it.h = it.kv * G + g;
-    it.gi = 1;
-    it.st = it.n > 0 || p.start[0];
+    it.ns = p.direct ? it.n + 1 : 1;
+    it.gi = it.ns;
+    it.st = !p.direct && (it.n > 0 || p.start[0]);
   } else {
     it.h = it.kv;
-    it.gi = G;
-    it.st = (it.n + 1) * kC < len || p.start[1];
+    it.ns = p.direct ? max((it.len + kC - 1) / kC - it.n, 1) : 1;
+    it.gi = G * it.ns;
+    it.st = !p.direct && ((it.n + 1) * kC < it.len || p.start[1]);
   }
   return it;
 }
@@ -515,11 +527,11 @@ __global__ void __launch_bounds__(kOThr, 1)
         ++q;
         return true;
       };
-      auto tile = [&](const CUtensorMap *m, const LinItem &it, int h) {
+      auto tile = [&](const CUtensorMap *m, const LinItem &it, int h, int n) {
         if (!ok || !slot(NH * 16384)) return;
         const int s = (q - 1) % kOSlots;
         for (int x = 0; x < 2 * NH; ++x)
-          tma_load_4d(sb + s * kOSlot + x * 8192, m, (x >> 1) * 64, h, it.n * kC + (x & 1) * kSub, it.b,
+          tma_load_4d(sb + s * kOSlot + x * 8192, m, (x >> 1) * 64, h, n * kC + (x & 1) * kSub, it.b,
                       bar(kOBarFull + s));
       };
       for (int i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
@@ -535,16 +547,18 @@ __global__ void __launch_bounds__(kOThr, 1)
           tma_load_4d(sb + kOOffA + as * kOSlot + x * 8192, ma, (x >> 1) * 64, it.h, it.n * kC + (x & 1) * kSub, it.b,
                       bar(kOBarAFull + as));
         ++item;
+        int hg = it.role < 2 ? it.kv : it.kv * p.z.G, far = 0;    // far: chunks away
         for (int g = 0; g < it.gi; ++g) {
-          const int hg = it.role < 2 ? it.kv : it.kv * p.z.G + g;
-          tile(mb, it, hg);
+          const int n = it.role < 2 ? it.n - far : it.n + far;
+          tile(mb, it, hg, n);
           if (g == 0 && it.st && ok && slot(D * D * 2)) {
             const int s = (q - 1) % kOSlots;
             const __nv_bfloat16 *src = p.tiles[it.role >> 1] +
                                        (static_cast<size_t>(it.b * p.z.Hkv + it.kv) * p.z.NC + it.n) * (D * D);
             bulk_load(sb + s * kOSlot, src, D * D * 2, bar(kOBarFull + s));
           }
-          tile(mc, it, hg);
+          tile(mc, it, hg, n);
+          if (++far == it.ns) far = 0, ++hg;
         }
       }
       if (*abort_flag) {
@@ -677,8 +691,10 @@ __global__ void __launch_bounds__(kOThr, 1)
       float pw[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) pw[e] = lexp2(l2 * static_cast<float>(rev ? e : 15 - e));
-      for (int g = 0; ok && g < it.gi; ++g) {
-        const int sbuf = (ss + g) & 1;
+      int far = 0;                                            // chunks between A and this step's B and C
+      for (int g = 0; ok && g < it.gi; ++g, far = far + 1 == it.ns ? 0 : far + 1) {
+        const int sbuf = (ss + g) & 1, gap0 = far * kC;
+        const int L = far ? min(kC, it.len - (it.role < 2 ? it.n - far : it.n + far) * kC) : it.L;   // columns that count
         if (!wtw(bar(kOBarS + sbuf), ((ss + g) >> 1) & 1)) {
           ok = false;
           break;
@@ -690,8 +706,8 @@ __global__ void __launch_bounds__(kOThr, 1)
         // diagonal took 2,000 cycles).
 #pragma unroll 1
         for (int c0 = 64 * hc; c0 < 64 * hc + 64; c0 += 16) {
-          const bool inside = rev ? (c0 >= 32 * qd + 31 && c0 + 16 <= it.L) : c0 + 15 <= 32 * qd;
-          const bool outside = rev ? c0 + 15 < 32 * qd : c0 > 32 * qd + 31;
+          const bool inside = rev ? ((far || c0 >= 32 * qd + 31) && c0 + 16 <= L) : far || c0 + 15 <= 32 * qd;
+          const bool outside = !far && (rev ? c0 + 15 < 32 * qd : c0 > 32 * qd + 31);
           uint32_t pk[8];
           if (outside) {
 #pragma unroll
@@ -700,8 +716,8 @@ __global__ void __launch_bounds__(kOThr, 1)
             uint32_t sr[16];
             float v[16];
             tc::ld16_wait(tS + c0, sr);
-            if (inside || mild) {
-              const float base = p.z.scale * lexp2(l2 * static_cast<float>(rev ? c0 - row : row - c0 - 15));
+            if (inside || mild || far) {
+              const float base = p.z.scale * lexp2(l2 * static_cast<float>(gap0 + (rev ? c0 - row : row - c0 - 15)));
 #pragma unroll
               for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(sr[e]) * (base * pw[e]);
             } else {
@@ -713,7 +729,7 @@ __global__ void __launch_bounds__(kOThr, 1)
             }
             if (!inside) {
               // columns of the block that count: from row on, or up to it
-              const int lo = rev ? row - c0 : 0, hi = min(rev ? 16 : row - c0 + 1, it.L - c0);
+              const int lo = rev && !far ? row - c0 : 0, hi = min(rev || far ? 16 : row - c0 + 1, L - c0);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 if (e < lo || e >= hi) v[e] = 0.f;
@@ -724,14 +740,14 @@ __global__ void __launch_bounds__(kOThr, 1)
           // 16 columns c to the 8 columns 32 (c / 32) + 8 (c / 16 % 2)
           tc::st8_async(tS + (c0 & 96) + ((c0 >> 1) & 8), pk);
         }
-        if (it.L < kC) {
+        if (L < kC) {
           // rows of C behind the sequence may hold anything: 0 * NaN must not reach the product
           const int qc = q + 1 + st + 2 * g;
           if (!wtw(bar(kOBarFull + qc % kOSlots), phase(qc))) {
             ok = false;
             break;
           }
-          if (row >= it.L && hc < NH) {
+          if (row >= L && hc < NH) {
             unsigned char *cr = smem + (qc % kOSlots) * kOSlot + hc * 16384 + row * 128;
 #pragma unroll
             for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(cr + 16 * e) = make_uint4(0, 0, 0, 0);
@@ -892,16 +908,38 @@ cudaError_t decode_groups(const LinDecodeParams &p, unsigned blocks, cudaStream_
 
 // Rows of D elements at `stride` elements from token to token, in boxes of 64
 // tokens by 64 columns (128-byte swizzle, as the products read them) or 32
-// (plain rows).
+// (plain rows).  Encoding a map takes the host about a microsecond, and a
+// backward call has nine: each thread keeps the layouts it met last and points
+// a copy at the buffer.
 bool lin_map(CUtensorMap *mp, const void *base, int D, int H, int T, int B, long long stride, const char **why,
              int cols = 64) {
+  struct Entry {
+    int D, H, T, B, cols;
+    long long stride;
+    CUtensorMap map;
+  };
+  constexpr int kKept = 16;
+  thread_local Entry kept[kKept];
+  thread_local int count = 0, oldest = 0;
+  for (int i = 0; i < count; ++i) {
+    const Entry &e = kept[i];
+    if (e.D == D && e.H == H && e.T == T && e.B == B && e.cols == cols && e.stride == stride) {
+      *mp = e.map;
+      if (move_tiled(mp, base)) return true;
+      break;
+    }
+  }
   const uint64_t ts = static_cast<uint64_t>(stride) * 2;
   const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(H), static_cast<uint64_t>(T),
                             static_cast<uint64_t>(B)};
   const uint64_t strides[3] = {static_cast<uint64_t>(D) * 2, ts, ts * T};
   const uint32_t box[4] = {static_cast<uint32_t>(cols), 1, kSub, 1};
-  return encode_tiled(mp, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box,
-                      cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, why);
+  if (!encode_tiled(mp, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box,
+                    cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, why))
+    return false;
+  const int at = count < kKept ? count++ : oldest++ % kKept;
+  kept[at] = Entry{D, H, T, B, cols, stride, *mp};
+  return true;
 }
 
 template <int D, int NS>
@@ -969,7 +1007,9 @@ cudaError_t launch_lin_attn(const LinAttnArgs &a, const WaitCtl &w, cudaStream_t
   sp.end[1] = a.dinitial_state;
   // which recurrences anything reads: the tiles of more than one chunk or of
   // a given start, and the states that leave
-  const bool tiles0 = op.z.NC > 1 || a.initial_state, tiles1 = bwd && (op.z.NC > 1 || a.dfinal_state);
+  op.direct = op.z.NC <= (bwd ? kDirectBwd : kDirectFwd) && !a.initial_state && !a.final_state && !a.dfinal_state && !a.dinitial_state;
+  const bool far = op.z.NC > 1 && !op.direct;
+  const bool tiles0 = far || a.initial_state, tiles1 = bwd && (far || a.dfinal_state);
   const bool f = tiles0 || a.final_state, r = tiles1 || a.dinitial_state;
   sp.first_role = f ? 0 : 1;
   sp.nroles = (f ? 1 : 0) + (r ? 1 : 0);
