@@ -50,8 +50,9 @@
  *     a message for the last non-OK status of the calling thread.
  *   - Nothing crosses the ABI as a C++ exception, and nothing aborts.
  *   - Calls neither synchronise nor allocate: the work they enqueue on
- *     `stream` is kernel launches (and, for rmsnorm_bwd_dgamma, a memset of
- *     its output).  The first call of an operation on a device also resolves
+ *     `stream` is kernel launches (and a memset or a copy of an output for
+ *     rmsnorm_bwd_dgamma, and where no tokens are left to work on for
+ *     qk_norm_rope_bwd and lin_attn_fwd / _bwd).  The first call of an operation on a device also resolves
  *     per-device state and raises the kernels' shared-memory limits.  So the
  *     calls can be captured into CUDA graphs; make one call of each operation
  *     on the device before capturing.
@@ -338,8 +339,10 @@ abw_status attn_bwd_causal_noalloc(const void *q, const void *k, const void *v, 
  *         pairs turn by the position on axis 0, the next sections[1] by that on
  *         axis 1, and so on (time, height and width of image and video
  *         tokens).  NULL with n_axes == 1.
- * Angles are exact to 2^-32 turns for every position; eps >= 0.
- * Supported: D even, 2 <= D <= 512.
+ * Angles are exact to 2^-32 turns for every position; eps >= 0.  The sum of
+ * squares is taken in fp32: a row that holds values above 1e18 may come out as
+ * NaN.
+ * Supported: D even, 2 <= D <= 512; below 2^31 elements a token.
  */
 abw_status qk_norm_rope_fwd(const void *q, const void *k, abw_dtype dtype, const float *gamma_q,
                             const float *gamma_k, void *q_out, void *k_out, int B, int T, int Hq, int Hkv, int D,
@@ -389,11 +392,13 @@ abw_status qk_norm_rope_bwd(const void *q, const void *k, abw_dtype dtype, const
  *   o             [B][T][Hq][D] bf16, token stride o_stride
  *   final_state   [B][Hkv][D][D] f32 or NULL: the state behind each sequence's last
  *         token (may be the same buffer as initial_state)
- *   workspace     at least lin_attn_fwd_workspace_bytes(); unspecified contents
+ *   workspace     at least lin_attn_fwd_workspace_bytes() (also for short
+ *         sequences without states, which leave it alone); unspecified contents
  * Scores and the chunk states that enter a product are rounded to bf16; sums
  * and the states themselves are fp32, and final_state is good to fp32
  * rounding.  Equal calls give equal bits.
- * Supported: D == 64 or 128; T >= 0; Hq % Hkv == 0; strides multiples of 8.
+ * Supported: D == 64 or 128; T >= 0; Hq >= 1, Hq % Hkv == 0; strides multiples
+ * of 8.
  */
 size_t lin_attn_fwd_workspace_bytes(int B, int T, int Hkv, int D);
 abw_status lin_attn_fwd(const void *q, const void *k, const void *v, const float *log_decay,

@@ -94,6 +94,7 @@ def test_lin_attn_fwd_refusals(lib, mem):
     assert lin_fwd(lib, D=96) == B.ENOTSUP
     assert lin_fwd(lib, Hkv=3) == B.EINVAL
     assert lin_fwd(lib, Hkv=0) == B.EINVAL
+    assert lin_fwd(lib, Hq=0) == B.EINVAL and "Hq=0" in B.last_error()    # keys would move the state
     assert lin_fwd(lib, T=-1, need=0) == B.EINVAL
     assert lin_fwd(lib, scale=float("nan")) == B.EINVAL
     assert lin_fwd(lib, qs=-8) == B.EINVAL
@@ -111,9 +112,10 @@ def test_lin_attn_fwd_refusals(lib, mem):
 
 
 def test_lin_attn_bwd_refusals(lib):
-    def call(D=64, Hkv=2, T=16, scale=0.1, dks=0, ws=None):
-        return lib.lin_attn_bwd(None, None, None, None, None, None, None, None, None, None, None, None, 1, T, 4, Hkv, D,
+    def call(D=64, Hkv=2, T=16, scale=0.1, dks=0, ws=None, Hq=4):
+        return lib.lin_attn_bwd(None, None, None, None, None, None, None, None, None, None, None, None, 1, T, Hq, Hkv, D,
                                 0, 0, 0, 0, dks, 0, scale, ws, 1 << 30, None)
+    assert call(Hq=0) == B.EINVAL and "Hq=0" in B.last_error()
     assert call(D=32) == B.ENOTSUP
     assert call(Hkv=3) == B.EINVAL
     assert call(scale=float("nan")) == B.EINVAL
@@ -130,6 +132,7 @@ def test_lin_attn_decode_refusals(lib, mem):
     assert call(D=256) == B.ENOTSUP
     assert call(Hq=18) == B.ENOTSUP                                        # group of 9
     assert call(Hq=5) == B.EINVAL
+    assert call(Hq=0) == B.EINVAL
     assert call(dt=3) == B.EINVAL
     assert call(n=2) == B.EINVAL                                           # fewer states than rows, no slots
     assert call(n=-1) == B.EINVAL

@@ -125,6 +125,7 @@ Rows dense(const char *name, const void *p, size_t bytes, size_t align = 16) {
 abw_status check_lin(const char *op, int B, int T, int Hq, int Hkv, int D, float scale) {
   if (B < 0 || T < 0 || Hq < 0 || Hkv < 0) return fail(ABW_EINVAL, "%s: negative size", op);
   if (Hkv == 0 || Hq % Hkv != 0) return fail(ABW_EINVAL, "%s: Hq=%d not a multiple of Hkv=%d", op, Hq, Hkv);
+  if (Hq == 0) return fail(ABW_EINVAL, "%s: Hq=0 with Hkv=%d", op, Hkv);
   if (D != 64 && D != 128) return fail(ABW_ENOTSUP, "%s: D=%d unsupported (D == 64 or 128)", op, D);
   if (!(scale == scale)) return fail(ABW_EINVAL, "%s: scale is NaN", op);
   return ABW_OK;
@@ -660,7 +661,9 @@ abw_status qk_norm_rope_fwd(const void *q, const void *k, abw_dtype dtype, const
   return from_cuda(abw::launch_qk_norm_rope(a, reinterpret_cast<cudaStream_t>(stream)), "qk_norm_rope_fwd");
 }
 
-size_t qk_norm_rope_bwd_workspace_bytes(int D) { return D < 1 || D > 512 ? 0 : abw::qk_norm_rope_bwd_workspace_bytes(D); }
+size_t qk_norm_rope_bwd_workspace_bytes(int D) {
+  return D < 1 || D > 512 ? 0 : abw::qk_norm_rope_bwd_workspace_bytes(D);
+}
 
 abw_status qk_norm_rope_bwd(const void *q, const void *k, abw_dtype dtype, const void *dq_out, const void *dk_out,
                             abw_dtype dy_dtype, const float *gamma_q, const float *gamma_k, void *dq, void *dk,
@@ -734,7 +737,7 @@ abw_status lin_attn_fwd(const void *q, const void *k, const void *v, const float
   if (st != ABW_OK) return st;
   if (q_stride < 0 || k_stride < 0 || v_stride < 0 || o_stride < 0)
     return fail(ABW_EINVAL, "lin_attn_fwd: negative token stride");
-  if (B == 0 || Hq == 0) return ABW_OK;
+  if (B == 0) return ABW_OK;
   const size_t need = abw::lin_attn_workspace_bytes(B, T, Hkv, D, 0);
   if (need && (workspace == nullptr || workspace_bytes < need))
     return fail(ABW_EWORKSPACE, "lin_attn_fwd: workspace %zu bytes at %p, need %zu", workspace_bytes, workspace, need);
@@ -782,7 +785,7 @@ abw_status lin_attn_bwd(const void *q, const void *k, const void *v, const void 
   if (st != ABW_OK) return st;
   if (q_stride < 0 || k_stride < 0 || v_stride < 0 || dq_stride < 0 || dk_stride < 0 || dv_stride < 0)
     return fail(ABW_EINVAL, "lin_attn_bwd: negative token stride");
-  if (B == 0 || Hq == 0) return ABW_OK;
+  if (B == 0) return ABW_OK;
   const size_t need = abw::lin_attn_workspace_bytes(B, T, Hkv, D, 1);
   if (need && (workspace == nullptr || workspace_bytes < need))
     return fail(ABW_EWORKSPACE, "lin_attn_bwd: workspace %zu bytes at %p, need %zu", workspace_bytes, workspace, need);
@@ -835,8 +838,8 @@ abw_status lin_attn_decode(const void *q, const void *k, const void *v, abw_dtyp
   if (dtype != ABW_F32 && dtype != ABW_BF16) return fail(ABW_EINVAL, "lin_attn_decode: bad dtype");
   if (n_states < 0 || (!slots && n_states < B))
     return fail(ABW_EINVAL, "lin_attn_decode: n_states=%d with B=%d and %s", n_states, B, slots ? "slots" : "no slots");
-  if (B == 0 || Hq == 0) return ABW_OK;
-  const size_t es = dt_size(dtype), qb = static_cast<size_t>(B) * Hq * D * es, kb = static_cast<size_t>(B) * Hkv * D * es;
+  if (B == 0) return ABW_OK;
+  const size_t es = dt_size(dtype), n = static_cast<size_t>(B) * D * es, qb = n * Hq, kb = n * Hkv;
   Rows in[] = {dense("q", q, qb), dense("k", k, kb), dense("v", v, kb),
                dense("log_decay", log_decay, static_cast<size_t>(Hkv) * 4, 4),
                dense("slots", slots, slots ? static_cast<size_t>(B) * 4 : 0, 4)};
