@@ -214,6 +214,54 @@ def test_state_in_place_continues_a_prompt(abw):
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+def test_offsets_past_32_bits(abw):
+    """Tokens some 2^23 elements apart: the last ones start behind 2^31."""
+    T, Hq, Hkv, D, gap = 150, 4, 2, 64, 1 << 23
+    t = make(15, 2, T, Hq, Hkv, D, True)
+    d = {x: cuda(y) for x, y in t.items()}
+    wide = torch.empty(2, T, gap, dtype=BF, device="cuda")
+    outs = torch.empty(2, T, gap, dtype=BF, device="cuda")
+    assert wide.numel() - gap > 2 ** 31
+    part = lambda buf, at, h: buf[:, :, at * D:(at + h) * D].view(2, T, h, D)
+    q, k, v = (part(wide, at, h).copy_(d[x]) for x, at, h in (("q", 0, Hq), ("k", Hq, Hkv), ("v", Hq + Hkv, Hkv)))
+    for s0, df in ((None, None), (d["s0"], d["df"])):
+        how = dict(initial_state=s0)
+        want = abw.lin_attn_fwd(d["q"], d["k"], d["v"], d["ld"], 0.125, want_final_state=s0 is not None, **how)
+        got = abw.lin_attn_fwd(q, k, v, d["ld"], 0.125, want_final_state=s0 is not None, o=part(outs, 0, Hq), **how)
+        how["dfinal_state"] = df
+        want += abw.lin_attn_bwd(d["q"], d["k"], d["v"], d["do"], d["ld"], 0.125, **how)
+        got += abw.lin_attn_bwd(q, k, v, d["do"], d["ld"], 0.125, dq=part(outs, Hq, Hq), dk=part(outs, 2 * Hq, Hkv),
+                                dv=part(outs, 2 * Hq + Hkv, Hkv), **how)
+        abw.device_check()
+        assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_waits_that_run_out(abw):
+    """A limit of zero: kernels that give up say so and leave the device as it
+    was, so the next call is right."""
+    from transformer_attention_backward_gb300 import _binding as B
+    t = make(16, 2, 900, 8, 4, 128, True)
+    d = {x: cuda(y) for x, y in t.items()}
+
+    def run():
+        return (abw.lin_attn_fwd(d["q"], d["k"], d["v"], d["ld"], 0.125, initial_state=d["s0"], want_final_state=True)
+                + abw.lin_attn_bwd(d["q"], d["k"], d["v"], d["do"], d["ld"], 0.125, initial_state=d["s0"],
+                                   dfinal_state=d["df"], want_dinitial_state=True))
+    want = run()
+    abw.device_check()
+    lib = abw.library()
+    lib.abw_set_wait_limit_ns(0)
+    try:
+        run()
+        status = lib.abw_device_check(torch.cuda.current_stream().cuda_stream)
+    finally:
+        lib.abw_set_wait_limit_ns(2_000_000_000)
+    assert status in (B.OK, B.ETIMEOUT)
+    got = run()
+    abw.device_check()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_no_tokens(abw):
     t = make(13, 2, 0, 4, 2, 64, True)
     d = {x: cuda(y) for x, y in t.items()}
@@ -292,6 +340,17 @@ def test_decode_slots(abw):
         assert torch.equal(st[at].cpu(), s[at])
     none = abw.lin_attn_decode(q.cuda(), k.cuda(), v.cuda(), st[:0], ld.cuda(), 0.2, slots=slots.cuda())
     assert bool((none == 0).all())
+
+
+def test_decode_state_past_32_bits(abw):
+    q, k, v, s, ld = decode_inputs(4, 2, 8, 8, 128, BF)
+    pool = torch.empty(2 ** 31 // (8 * 128 * 128) + 2, 8, 128, 128, device="cuda")
+    slots = torch.tensor([pool.shape[0] - 1, 1], dtype=torch.int32, device="cuda")
+    pool[slots.long()] = s.cuda()
+    st = s.cuda()
+    want = abw.lin_attn_decode(q.cuda(), k.cuda(), v.cuda(), st, ld.cuda())
+    got = abw.lin_attn_decode(q.cuda(), k.cuda(), v.cuda(), pool, ld.cuda(), slots=slots)
+    assert torch.equal(got, want) and torch.equal(pool[slots.long()], st)
 
 
 def test_prompt_then_tokens(abw):

@@ -174,6 +174,24 @@ def test_misaligned_rows_and_padded_strides(abw):
         close(y, ref, BF, 64)
 
 
+@pytest.mark.parametrize("D", [64, 66])
+def test_offsets_past_32_bits(abw, D):
+    """Tokens some 2^23 elements apart: the last ones start behind 2^31."""
+    T, gap = 130, 1 << 23
+    t = inputs(11, 2, T, 3, 1, D, BF)
+    wide = torch.empty(2, T, gap, dtype=BF, device="cuda")
+    outs = torch.empty(2, T, gap, dtype=BF, device="cuda")
+    assert wide.numel() - gap > 2 ** 31
+    part = lambda buf, at, h: buf[:, :, at * D:(at + h) * D].view(2, T, h, D)
+    q, k = part(wide, 0, 3).copy_(t["q"]), part(wide, 3, 1).copy_(t["k"])
+    g = (t["gq"].cuda(), t["gk"].cuda())
+    qd, kd, dq, dk = t["q"].contiguous().cuda(), t["k"].contiguous().cuda(), t["dq"].cuda(), t["dk"].cuda()
+    want = abw.qk_norm_rope_fwd(qd, kd, *g, rope_base=1e4) + abw.qk_norm_rope_bwd(qd, kd, dq, dk, *g, rope_base=1e4)
+    got = abw.qk_norm_rope_fwd(q, k, *g, rope_base=1e4) + abw.qk_norm_rope_bwd(
+        q, k, dq, dk, *g, rope_base=1e4, dq=part(outs, 0, 3), dk=part(outs, 3, 1))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_other_stream_and_graph(abw):
     t = inputs(10, 2, 300, 4, 2, 128, BF)
     q, k = views(t["qkv"], 4, 2)

@@ -316,7 +316,8 @@ def _fns():
 
 def _dense(t, name, dt, shape, dev):
     """Checks a dense tensor and returns its address."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dt and t.shape == shape and t.device == dev and t.is_contiguous()):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dt and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
         _req(t, name, (dt,), shape)
         raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
     return t.data_ptr()
@@ -442,8 +443,9 @@ def qk_norm_rope_fwd(q, k, gamma_q=None, gamma_k=None, eps=1e-6, rope_base=0.0, 
     gq = None if gamma_q is None else _dense(gamma_q, "gamma_q", _F32, (D,), dev)
     gk = None if gamma_k is None else _dense(gamma_k, "gamma_k", _F32, (D,), dev)
     R, pos, axes, host = _rotation(B, T, D, rope_base, rotary_dim, positions, sections, dev)
-    _call("qk_norm_rope_fwd", _fns().qk_norm_rope_fwd, dev, stream, None, None, q.data_ptr(), kp, _DT[dt], gq, gk, qo, ko,
-          B, T, Hq, Hkv, D, qs, ks, float(eps), float(rope_base), R, 1 if interleaved else 0, pos, axes, host, int(pos0))
+    _call("qk_norm_rope_fwd", _fns().qk_norm_rope_fwd, dev, stream, None, None, q.data_ptr(), kp, _DT[dt], gq, gk, qo,
+          ko, B, T, Hq, Hkv, D, qs, ks, float(eps), float(rope_base), R, 1 if interleaved else 0, pos, axes, host,
+          int(pos0))
     return q_out, k_out
 
 
@@ -506,8 +508,8 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, gamma_q=None, gamma_k=None, eps=1e-6,
     R, pos, axes, host = _rotation(B, T, D, rope_base, rotary_dim, positions, sections, dev)
     need = qk_norm_rope_bwd_workspace_bytes(D) if gq or gk else 0
     _call("qk_norm_rope_bwd", _fns().qk_norm_rope_bwd, dev, stream, need, workspace, q.data_ptr(), kp, _DT[dt], yq, yk,
-          _DT[yt], gq, gk, dq.data_ptr(), dkp, dgq, dgk, B, T, Hq, Hkv, D, qs, ks, dqs, dks, float(eps), float(rope_base), R,
-          1 if interleaved else 0, pos, axes, host, int(pos0))
+          _DT[yt], gq, gk, dq.data_ptr(), dkp, dgq, dgk, B, T, Hq, Hkv, D, qs, ks, dqs, dks, float(eps),
+          float(rope_base), R, 1 if interleaved else 0, pos, axes, host, int(pos0))
     return dq, dk, dgamma_q, dgamma_k
 
 
@@ -557,16 +559,19 @@ def lin_attn_fwd(q, k, v, log_decay, scale=None, initial_state=None, lengths=Non
         final_state = _empty(sshape, _F32, dev, stream)
     fin = None if final_state is None else _dense(final_state, "final_state", _F32, sshape, dev)
     _call("lin_attn_fwd", _fns().lin_attn_fwd, dev, stream, lin_attn_fwd_workspace_bytes(B, T, Hkv, D), workspace, qp,
-          kp, vp, ldp, s0, ln, o.data_ptr(), fin, *dims, *strides, os, 1.0 / math.sqrt(D) if scale is None else float(scale))
+          kp, vp, ldp, s0, ln, o.data_ptr(), fin, *dims, *strides, os,
+          1.0 / math.sqrt(D) if scale is None else float(scale))
     return o, final_state
 
 
 def lin_attn_bwd(q, k, v, dout, log_decay, scale=None, initial_state=None, dfinal_state=None, lengths=None,
-                 want_dinitial_state=False, dq=None, dk=None, dv=None, dinitial_state=None, workspace=None, stream=None):
+                 want_dinitial_state=False, dq=None, dk=None, dv=None, dinitial_state=None, workspace=None,
+                 stream=None):
     """Gradients of lin_attn_fwd: dout [B][T][Hq][D] bf16, dfinal_state
     [B][Hkv][D][D] fp32 or None.  Returns (dq, dk, dv) bf16 (given ones may be
     parts of a packed gradient) and dinitial_state fp32 or None."""
-    dev, dims, kshape, sshape, strides, (qp, kp, vp, ldp, s0, ln) = _lin_inputs(q, k, v, log_decay, initial_state, lengths)
+    dev, dims, kshape, sshape, strides, at = _lin_inputs(q, k, v, log_decay, initial_state, lengths)
+    qp, kp, vp, ldp, s0, ln = at
     B, T, Hq, Hkv, D = dims
     dop = _dense(dout, "dout", _BF16, q.shape, dev)
     dfp = None if dfinal_state is None else _dense(dfinal_state, "dfinal_state", _F32, sshape, dev)
@@ -580,7 +585,8 @@ def lin_attn_bwd(q, k, v, dout, log_decay, scale=None, initial_state=None, dfina
         dinitial_state = _empty(sshape, _F32, dev, stream)
     dsp = None if dinitial_state is None else _dense(dinitial_state, "dinitial_state", _F32, sshape, dev)
     _call("lin_attn_bwd", _fns().lin_attn_bwd, dev, stream, lin_attn_bwd_workspace_bytes(B, T, Hkv, D), workspace, qp,
-          kp, vp, dop, ldp, s0, dfp, ln, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dsp, *dims, *strides, *outs, 1.0 / math.sqrt(D) if scale is None else float(scale))
+          kp, vp, dop, ldp, s0, dfp, ln, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dsp, *dims, *strides, *outs,
+          1.0 / math.sqrt(D) if scale is None else float(scale))
     return dq, dk, dv, dinitial_state
 
 
@@ -604,7 +610,6 @@ def lin_attn_decode(q, k, v, state, log_decay, scale=None, slots=None, o=None, s
         op = o.data_ptr()
     else:
         op = _dense(o, "o", dt, qshape, dev)
-    _call("lin_attn_decode", _fns().lin_attn_decode, dev, stream, None, None, qp, kp, vp, _DT[dt], sp, lp, sl,
-          op, B, Hq, Hkv, D, n,
-          1.0 / math.sqrt(D) if scale is None else float(scale))
+    _call("lin_attn_decode", _fns().lin_attn_decode, dev, stream, None, None, qp, kp, vp, _DT[dt], sp, lp, sl, op, B,
+          Hq, Hkv, D, n, 1.0 / math.sqrt(D) if scale is None else float(scale))
     return o

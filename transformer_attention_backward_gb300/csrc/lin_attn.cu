@@ -66,7 +66,7 @@ __device__ __forceinline__ int seq_len(const int *lengths, int b, int T) {
 // access: shared memory is busy, and each access of a warp that has little
 // else to do stands in its queue.
 __device__ __forceinline__ bool lin_wait_slow(uint32_t br, uint32_t parity, uint32_t bars, volatile int *abort_flag,
-                                                  unsigned int kernel, unsigned int *err, unsigned long long limit_ns) {
+                                              unsigned int kernel, unsigned int *err, unsigned long long limit_ns) {
   if (*abort_flag) return false;      // a wait has run out: all others return
   if (mbar_wait_bounded(br, parity, limit_ns)) return true;
   *abort_flag = 1;
@@ -114,10 +114,11 @@ struct LinSizes {
 // The chain of a step (load, weights, product, addition) is long and the work
 // in it small, so what counts is how many steps are under way: a ring of 6
 // (X, Y) slots, four buffers of weighted rows, filled in turn by three groups of
-// warps (two: 59 us for 55, four: 58), and two buffers of U.  32 columns, not 64: X is read by
-// twice as many CTAs (from L2), but a step moves 2/3 of the bytes through shared
-// memory and there are twice as many chains: 8192 tokens of 32 heads 59 us
-// against 103, 640 chains of 2048 tokens 83 against 83.
+// warps (8192 tokens of 32 heads: 55 us; two groups 59, four 58), and two buffers
+// of U.  32 columns, not 64: X is read by twice as many CTAs (from L2), but a step
+// moves 2/3 of the bytes through shared memory and there are twice as many
+// chains (before the third group: 8192 tokens of 32 heads 59 us against 103, 640
+// chains of 2048 tokens 83 against 83).
 // Warps: 0 TMA, 1 MMA, 2-13 weights, 14-17 state.
 // ---------------------------------------------------------------------------
 constexpr int kSGroups = 3;                          // groups of four warps that form weighted rows
@@ -402,7 +403,8 @@ constexpr int kOOffBar = kOOffA + 2 * kOSlot;
 enum {
   kOBarFull = 0, kOBarEmpty = kOBarFull + kOSlots, kOBarAFull = kOBarEmpty + kOSlots, kOBarAEmpty = kOBarAFull + 2,
   kOBarS = kOBarAEmpty + 2, kOBarP = kOBarS + 2,
-  kOBarStage = kOBarP + 2, kOBarO = kOBarStage + 2, kOBarOEmpty = kOBarO + 1, kOBarFinal = kOBarOEmpty + 1, kONumBars = kOBarFinal + 1
+  kOBarStage = kOBarP + 2, kOBarO = kOBarStage + 2, kOBarOEmpty = kOBarO + 1, kOBarFinal = kOBarOEmpty + 1,
+  kONumBars = kOBarFinal + 1
 };
 constexpr int kOOffTmem = kOOffBar + kONumBars * 8;
 constexpr int kOOffAbort = kOOffTmem + 4;
@@ -1007,7 +1009,8 @@ cudaError_t launch_lin_attn(const LinAttnArgs &a, const WaitCtl &w, cudaStream_t
   sp.end[1] = a.dinitial_state;
   // which recurrences anything reads: the tiles of more than one chunk or of
   // a given start, and the states that leave
-  op.direct = op.z.NC <= (bwd ? kDirectBwd : kDirectFwd) && !a.initial_state && !a.final_state && !a.dfinal_state && !a.dinitial_state;
+  op.direct = op.z.NC <= (bwd ? kDirectBwd : kDirectFwd) && !a.initial_state && !a.final_state && !a.dfinal_state &&
+              !a.dinitial_state;
   const bool far = op.z.NC > 1 && !op.direct;
   const bool tiles0 = far || a.initial_state, tiles1 = bwd && (far || a.dfinal_state);
   const bool f = tiles0 || a.final_state, r = tiles1 || a.dinitial_state;
@@ -1042,7 +1045,8 @@ cudaError_t launch_lin_attn(const LinAttnArgs &a, const WaitCtl &w, cudaStream_t
   if (!f) tm[4] = tm[0];
   if (!r) tm[5] = tm[0];
   for (int i = 0; i < 4; ++i)
-    if (out[i] && !lin_map(&op.map[i], out[i], a.D, i < 2 ? a.Hq : a.Hkv, a.T, a.B, os[i], why)) return cudaErrorInvalidValue;
+    if (out[i] && !lin_map(&op.map[i], out[i], a.D, i < 2 ? a.Hq : a.Hkv, a.T, a.B, os[i], why))
+      return cudaErrorInvalidValue;
   const bool exact = a.final_state || a.dinitial_state;   // a state leaves in fp32
   return a.D == 128 ? launch_lin<128>(tm, sp, op, exact, sms, st) : launch_lin<64>(tm, sp, op, exact, sms, st);
 }

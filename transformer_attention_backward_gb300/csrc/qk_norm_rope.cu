@@ -245,7 +245,8 @@ __device__ __forceinline__ void lane_angles(const QkParams &p, const unsigned lo
         const long long pos = p.pos ? p.pos[axis * p.ntok + tok] : step;
         // the upper half of the product, modulo one turn
         const unsigned lo = static_cast<unsigned>(turns[s]), hi = static_cast<unsigned>(turns[s] >> 32);
-        const unsigned plo = static_cast<unsigned>(pos), phi = static_cast<unsigned>(static_cast<unsigned long long>(pos) >> 32);
+        const unsigned plo = static_cast<unsigned>(pos);
+        const unsigned phi = static_cast<unsigned>(static_cast<unsigned long long>(pos) >> 32);
         turn_sincos(__umulhi(plo, lo) + plo * hi + phi * lo, zv[e], cv[e]);
       }
     }
@@ -260,7 +261,8 @@ __device__ __forceinline__ void lane_angles(const QkParams &p, const unsigned lo
 
 // gamma of this lane's components, 1 where there is no norm.
 template <int V, int N, int L, bool INTER, typename F = typename Num<V>::F, int C = Num<V>::kC>
-__device__ __forceinline__ void lane_gamma(const float *gamma, int lane, int rot, int h2, F (&ga)[N][C], F (&gb)[N][C]) {
+__device__ __forceinline__ void lane_gamma(const float *gamma, int lane, int rot, int h2, F (&ga)[N][C],
+                                           F (&gb)[N][C]) {
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int s = (lane + L * k) * V;
@@ -299,7 +301,8 @@ struct Side {
 // instruction issue before it is by memory, so what counts is instructions per
 // row: 196 a lane with rows dealt out one by one (38 us).
 template <typename XT, bool INTER, int V, int N, int L, int U>
-__global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? 3 : 1) qk_fwd_kernel(const __grid_constant__ QkTable<table_size<V, L>()> p) {
+__global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? 3 : 1)
+    qk_fwd_kernel(const __grid_constant__ QkTable<table_size<V, L>()> p) {
   __shared__ unsigned long long turns[table_size<V, L>()];
   using F = typename Num<V>::F;
   constexpr int kGroups = kQThr / L, C = Num<V>::kC;
