@@ -474,6 +474,90 @@ __device__ __noinline__ LinItem lin_item(const LinOutParams &p, int i) {
   return it;
 }
 
+// The row and column powers of the weights scale a^(distance) of a score tile.
+// Inside a block of 16 columns a weight is a power for the row times one for
+// the column (pw).  Next to the diagonal the row's is above 1, up to a^-31;
+// where that could overflow each weight is formed by itself.
+struct MaskWeights {
+  float l2, pw[16];
+  bool mild;
+  __device__ __forceinline__ MaskWeights(float l2_, bool rev) : l2(l2_), mild(l2_ > -3.8f) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) pw[e] = lexp2(l2 * static_cast<float>(rev ? e : 15 - e));
+  }
+};
+
+// Scores to P in place, for one row and half of its columns: weights on and
+// below the diagonal (rev: on and above it), 0 elsewhere, rounded to bf16.  far:
+// chunks between the rows and the columns; L: columns that count.
+__device__ __forceinline__ void mask_scores(uint32_t tS, const MaskWeights &w, float scale, int row, int qd, int hc,
+                                            bool rev, int far, int L) {
+  // A short loop over blocks of 16 columns: what all warps run over and
+  // over stays in the instruction cache (unrolled, blocks on the
+  // diagonal took 2,000 cycles).
+#pragma unroll 1
+  for (int c0 = 64 * hc; c0 < 64 * hc + 64; c0 += 16) {
+    const bool inside = rev ? ((far || c0 >= 32 * qd + 31) && c0 + 16 <= L) : far || c0 + 15 <= 32 * qd;
+    const bool outside = !far && (rev ? c0 + 15 < 32 * qd : c0 > 32 * qd + 31);
+    uint32_t pk[8];
+    if (outside) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) pk[e] = 0;
+    } else {
+      uint32_t sr[16];
+      float v[16];
+      tc::ld16_wait(tS + c0, sr);
+      if (inside || w.mild || far) {
+        const float base = scale * lexp2(w.l2 * static_cast<float>(far * kC + (rev ? c0 - row : row - c0 - 15)));
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(sr[e]) * (base * w.pw[e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int gap = rev ? c0 + e - row : row - c0 - e;
+          v[e] = __uint_as_float(sr[e]) * (scale * lexp2(w.l2 * static_cast<float>(gap)));
+        }
+      }
+      if (!inside) {
+        // columns of the block that count: from row on, or up to it
+        const int lo = rev && !far ? row - c0 : 0, hi = min(rev || far ? 16 : row - c0 + 1, L - c0);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (e < lo || e >= hi) v[e] = 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) pk[e] = lpack2(v[2 * e], v[2 * e + 1]);
+    }
+    // 16 columns c to the 8 columns 32 (c / 32) + 8 (c / 16 % 2)
+    tc::st8_async(tS + (c0 & 96) + ((c0 >> 1) & 8), pk);
+  }
+}
+
+// One row and half of its columns of P C + fac (A S) to the staged output tile,
+// in the order of a 128-byte swizzled tile; rows behind the sequence are 0.
+template <int D>
+__device__ __forceinline__ void stage_rows(uint32_t tm, unsigned char *stage, int row, int hc, bool st, float fac,
+                                           bool in) {
+#pragma unroll 1
+  for (int c = hc * (D / 2); c < (hc + 1) * (D / 2); c += 32) {
+    float a[32], s[32];
+    if (st) {
+      tc::ld32x2_wait(tm + 256 + c, tm + 384 + c, a, s);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) a[e] = fmaf(fac, s[e], a[e]);
+    } else {
+      tc::ld32_wait(tm + 256 + c, a);
+    }
+    // the row's 16-byte pieces, in the order of a 128-byte swizzled tile
+#pragma unroll
+    for (int e = 0; e < 32; e += 8)
+      *reinterpret_cast<uint4 *>(stage + row * 128 + (c >> 6) * 16384 + ((((c & 63) + e) / 8 ^ (row & 7)) << 4)) =
+          in ? make_uint4(lpack2(a[e], a[e + 1]), lpack2(a[e + 2], a[e + 3]), lpack2(a[e + 4], a[e + 5]),
+                          lpack2(a[e + 6], a[e + 7]))
+             : make_uint4(0, 0, 0, 0);
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kOThr, 1)
     lin_out_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -686,16 +770,10 @@ __global__ void __launch_bounds__(kOThr, 1)
       const bool rev = it.role >= 2;
       const float l2 = log2_decay(p.z.log_decay[it.kv]);
       const int st = it.st ? 1 : 0;
-      // Inside a block of 16 columns a weight is a power for the row times
-      // one for the column (pw).  Next to the diagonal the row's is above 1,
-      // up to a^-31; where that could overflow each weight is formed by itself.
-      const bool mild = l2 > -3.8f;
-      float pw[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) pw[e] = lexp2(l2 * static_cast<float>(rev ? e : 15 - e));
+      const MaskWeights mw(l2, rev);
       int far = 0;                                            // chunks between A and this step's B and C
       for (int g = 0; ok && g < it.gi; ++g, far = far + 1 == it.ns ? 0 : far + 1) {
-        const int sbuf = (ss + g) & 1, gap0 = far * kC;
+        const int sbuf = (ss + g) & 1;
         const int L = far ? min(kC, it.len - (it.role < 2 ? it.n - far : it.n + far) * kC) : it.L;   // columns that count
         if (!wtw(bar(kOBarS + sbuf), ((ss + g) >> 1) & 1)) {
           ok = false;
@@ -703,45 +781,7 @@ __global__ void __launch_bounds__(kOThr, 1)
         }
         tc::fence_after_sync();
         const uint32_t tS = tmem + lanebase + sbuf * 128;
-        // A short loop over blocks of 16 columns: what all warps run over and
-        // over stays in the instruction cache (unrolled, blocks on the
-        // diagonal took 2,000 cycles).
-#pragma unroll 1
-        for (int c0 = 64 * hc; c0 < 64 * hc + 64; c0 += 16) {
-          const bool inside = rev ? ((far || c0 >= 32 * qd + 31) && c0 + 16 <= L) : far || c0 + 15 <= 32 * qd;
-          const bool outside = !far && (rev ? c0 + 15 < 32 * qd : c0 > 32 * qd + 31);
-          uint32_t pk[8];
-          if (outside) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) pk[e] = 0;
-          } else {
-            uint32_t sr[16];
-            float v[16];
-            tc::ld16_wait(tS + c0, sr);
-            if (inside || mild || far) {
-              const float base = p.z.scale * lexp2(l2 * static_cast<float>(gap0 + (rev ? c0 - row : row - c0 - 15)));
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(sr[e]) * (base * pw[e]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int gap = rev ? c0 + e - row : row - c0 - e;
-                v[e] = __uint_as_float(sr[e]) * (p.z.scale * lexp2(l2 * static_cast<float>(gap)));
-              }
-            }
-            if (!inside) {
-              // columns of the block that count: from row on, or up to it
-              const int lo = rev && !far ? row - c0 : 0, hi = min(rev || far ? 16 : row - c0 + 1, L - c0);
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (e < lo || e >= hi) v[e] = 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) pk[e] = lpack2(v[2 * e], v[2 * e + 1]);
-          }
-          // 16 columns c to the 8 columns 32 (c / 32) + 8 (c / 16 % 2)
-          tc::st8_async(tS + (c0 & 96) + ((c0 >> 1) & 8), pk);
-        }
+        mask_scores(tS, mw, p.z.scale, row, qd, hc, rev, far, L);
         if (L < kC) {
           // rows of C behind the sequence may hold anything: 0 * NaN must not reach the product
           const int qc = q + 1 + st + 2 * g;
@@ -764,32 +804,311 @@ __global__ void __launch_bounds__(kOThr, 1)
       tc::fence_after_sync();
       const float fac = rev ? lexp2(l2 * static_cast<float>(max(it.L - 1 - row, 0)))
                             : p.z.scale * lexp2(l2 * static_cast<float>(row + 1));
-      unsigned char *stage = smem + kOOffA + (item & 1) * kOSlot + row * 128;
-#pragma unroll 1
-      for (int c = hc * (D / 2); c < (hc + 1) * (D / 2); c += 32) {
-        float a[32], s[32];
-        if (st) {
-          tc::ld32x2_wait(tmem + lanebase + 256 + c, tmem + lanebase + 384 + c, a, s);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) a[e] = fmaf(fac, s[e], a[e]);
-        } else {
-          tc::ld32_wait(tmem + lanebase + 256 + c, a);
-        }
-        // the row's 16-byte pieces, in the order of a 128-byte swizzled tile
-        const bool in = row < it.L;                           // rows behind the sequence are 0
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4 *>(stage + (c >> 6) * 16384 + ((((c & 63) + e) / 8 ^ (row & 7)) << 4)) =
-              in ? make_uint4(lpack2(a[e], a[e + 1]), lpack2(a[e + 2], a[e + 3]), lpack2(a[e + 4], a[e + 5]),
-                              lpack2(a[e + 6], a[e + 7]))
-                 : make_uint4(0, 0, 0, 0);
-      }
+      stage_rows<D>(tmem + lanebase, smem + kOOffA + (item & 1) * kOSlot, row, hc, st, fac, row < it.L);
       tc::fence_before_sync();
       mbar_arrive(bar(kOBarOEmpty));
       fence_proxy_async_smem();
       mbar_arrive(bar(kOBarStage + (item & 1)));
       q += st + 2 * it.gi;
       ss += it.gi;
+      ++item;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// lin_grad: dq, dk and dv of one (batch, head, chunk) as one item, where every
+// query head has a KV head of its own: the three outputs (roles 1, 2, 3 of
+// lin_out, in this order) share Q, K, V, dO, S and R, so 192 KB a chunk arrive
+// in place of 384.  lin_out there is bound by those copies: without all else its
+// loads took 46 us of its 81 (4 x 2048 tokens of 20 heads).
+// Every tile has a slot of its own, dO two.  An output is staged over a tile
+// that no product needs any more (dq over S, dk over Q, dv over dO), chosen such
+// that the next item's tiles can arrive in the order in which they are needed.
+// Two sets of mask and output warps take the steps in turn; the scores of the
+// next step are formed before the product of this one.
+// TMEM as in lin_out.  Warps: 0 TMA loads, 1 MMA, 2-17 mask and output, 18 TMA
+// stores.
+// ---------------------------------------------------------------------------
+constexpr int kGThr = 608;
+constexpr int kGV = 0, kGS = 1, kGQ = 2, kGK = 3, kGR = 4, kGDO = 5;   // slots; dO: kGDO, kGDO + 1
+enum {
+  kGBarFull = 0, kGBarEmpty = kGBarFull + 7, kGBarS = kGBarEmpty + 7, kGBarP = kGBarS + 2, kGBarO = kGBarP + 2,
+  kGBarStage = kGBarO + 2, kGBarOEmpty = kGBarStage + 3, kGBarFinal = kGBarOEmpty + 1, kGNumBars = kGBarFinal + 1
+};
+static_assert(kGNumBars * 8 + 8 <= 256, "barriers of the gradient kernel");
+
+// Item i of lin_grad; false: behind the sequence.
+__device__ __noinline__ LinItem grad_item(const LinOutParams &p, int i) {
+  LinItem it;
+  it.kv = it.h = i % p.z.Hkv;
+  i /= p.z.Hkv;
+  it.n = i % p.z.NC;
+  it.b = i / p.z.NC;
+  it.len = seq_len(p.z.lengths, it.b, p.z.T);
+  it.L = min(kC, it.len - it.n * kC);
+  return it;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kGThr, 1)
+    lin_grad_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+                    const __grid_constant__ LinOutParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int NH = D / 64;
+
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOOffBar + kGNumBars * 8 + 4);
+  const LinWait lw{sb + kOOffBar, abort_flag, kSiteLinOut, p.wait};
+  auto bar = [&](int i) -> uint32_t { return lw.bar(i); };
+  auto wt = [&](uint32_t br, uint32_t parity) -> bool { return lw.one(br, parity); };
+  auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return lw.warp(br, parity); };
+  // the slot of a tile in item `item`, and the phase of its barriers there
+  auto slot = [](int tile, int item) -> int { return tile == kGDO ? kGDO + (item & 1) : tile; };
+  auto phase = [](int tile, int item) -> uint32_t { return (tile == kGDO ? item >> 1 : item) & 1; };
+  // the slot that output r = 0, 1, 2 (dq, dk, dv) is staged in
+  auto out_tile = [](int r) -> int { return r == 0 ? kGS : r == 1 ? kGQ : kGDO; };
+  auto has_s = [&](const LinItem &it) -> bool { return it.n > 0 || p.start[0]; };
+  auto has_r = [&](const LinItem &it) -> bool { return (it.n + 1) * kC < it.len || p.start[1]; };
+
+  if (tid == 0) {
+    for (int s = 0; s < 7; ++s) {
+      mbar_init(bar(kGBarFull + s), 1);
+      mbar_init(bar(kGBarEmpty + s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(kGBarS + s), 1);
+      mbar_init(bar(kGBarP + s), 256);
+      mbar_init(bar(kGBarO + s), 1);
+    }
+    for (int s = 0; s < 3; ++s) mbar_init(bar(kGBarStage + s), 256);
+    mbar_init(bar(kGBarOEmpty), 256);
+    mbar_init(bar(kGBarFinal), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tc::tmem_alloc(sb + kOOffBar + kGNumBars * 8, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kOOffBar + kGNumBars * 8);
+
+  if (warp == 0) {
+    // ============================ TMA producer ============================
+    if (lane == 0) {
+      // in the order in which the last item's tiles are done with: dO, V, S, Q, K, R
+      auto tile_at = [](int e) -> int { return e == 0 ? kGDO : e - 1; };
+      int loads = 0, item = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
+        const LinItem it = grad_item(p, i);
+        if (it.L <= 0) continue;
+#pragma unroll 1
+        for (int e = 0; e < 6; ++e) {
+          const int tile = tile_at(e), s = slot(tile, item);
+          const uint32_t fb = bar(kGBarFull + s), dst = sb + s * kOSlot;
+          if (!wt(bar(kGBarEmpty + s), phase(tile, item) ^ 1u)) {
+            ok = false;
+            break;
+          }
+          if (tile == kGS || tile == kGR) {
+            if (tile == kGS ? has_s(it) : has_r(it)) {
+              mbar_arrive_expect_tx(fb, D * D * 2);
+              bulk_load(dst, p.tiles[tile == kGR] + (static_cast<size_t>(it.b * p.z.Hkv + it.kv) * p.z.NC + it.n) * (D * D),
+                        D * D * 2, fb);
+            } else {
+              mbar_arrive(fb);
+            }
+          } else {
+            const CUtensorMap *m = tile == kGDO ? &tmDO : tile == kGV ? &tmV : tile == kGQ ? &tmQ : &tmK;
+            mbar_arrive_expect_tx(fb, NH * 16384);
+            for (int x = 0; x < 2 * NH; ++x)
+              tma_load_4d(dst + x * 8192, m, (x >> 1) * 64, it.h, it.n * kC + (x & 1) * kSub, it.b, fb);
+          }
+          ++loads;
+        }
+        if (ok) ++item;
+      }
+      if (*abort_flag)                                        // the last load of every slot
+        for (int x = (loads > 12 ? loads - 12 : 0); x < loads; ++x)
+          mbar_wait_bounded(bar(kGBarFull + slot(tile_at(x % 6), x / 6)), phase(tile_at(x % 6), x / 6), 2000000000ull);
+    }
+  } else if (warp == 1) {
+    // ============================ MMA issuer ==============================
+    constexpr uint32_t id_s = tc::idesc_bf16_f32(128, 128, 0, 0);   // A B^T
+    constexpr uint32_t id_n = tc::idesc_bf16_f32(128, D, 0, 1);     // P C and A S: B operand N-major
+    constexpr uint32_t id_k = tc::idesc_bf16_f32(128, D, 0, 0);     // A S^T: B operand K-major
+    auto kmaj = [&](int tile, int item) { return tc::sdesc_sw128(sb + slot(tile, item) * kOSlot, 16, 1024); };
+    auto nmaj = [&](int tile, int item, uint32_t half) {
+      return tc::sdesc_sw128(sb + slot(tile, item) * kOSlot, half, 1024);
+    };
+    auto kstep = [](int kk, int half) -> uint32_t { return static_cast<uint32_t>((kk >> 2) * half + (kk & 3) * 32) >> 4; };
+    auto full = [&](int tile, int item) -> bool { return wtw(bar(kGBarFull + slot(tile, item)), phase(tile, item)); };
+    auto next = [&](int &i, LinItem &it) -> bool {            // the next item that holds tokens
+      for (; i < p.items; i += gridDim.x) {
+        it = grad_item(p, i);
+        if (it.L > 0) return true;
+      }
+      return false;
+    };
+    // A B^T of output r into the buffer of step k, which held P two steps ago
+    // (its product was issued before: the tensor core works in order)
+    auto scores = [&](int r, int item, int k) -> bool {
+      const int ta = r == 0 ? kGDO : r == 1 ? kGV : kGK, tb = r == 0 ? kGV : r == 1 ? kGDO : kGQ;
+      if (!full(ta, item) || !full(tb, item)) return false;
+      tc::fence_after_sync();
+      const uint64_t dA = kmaj(ta, item), dB = kmaj(tb, item);
+      const uint32_t tS = tmem + (k & 1) * 128;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) tc::mma_bf16_w(tS, dA + kstep(kk, 16384), dB + kstep(kk, 16384), id_s, kk > 0);
+      tc::commit_w(bar(kGBarS + (k & 1)));
+      return true;
+    };
+    LinItem it, nx;
+    int i = blockIdx.x, item = 0, k = 0;
+    bool more = next(i, it), ok = !more || scores(0, 0, 0);
+    while (ok && more) {
+      i += gridDim.x;
+      more = next(i, nx);
+      for (int r = 0; ok && r < 3; ++r, ++k) {
+        const int ta = r == 0 ? kGDO : r == 1 ? kGV : kGK, ts = r == 0 ? kGS : kGR;
+        const int tb = r == 0 ? kGK : r == 1 ? kGQ : kGDO;
+        // the accumulators are free once the last output's rows have been read
+        ok = wtw(bar(kGBarOEmpty), (k & 1) ^ 1) && full(ts, item);
+        if (!ok) break;
+        tc::fence_after_sync();
+        if (r == 0 ? has_s(it) : has_r(it)) {
+          const uint64_t dA = kmaj(ta, item);
+          if (r == 2) {
+            const uint64_t dS = nmaj(ts, item, D * 128);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_bf16_w(tmem + 384, dA + kstep(kk, 16384), dS + ((kk * 2048) >> 4), id_n, kk > 0);
+          } else {
+            const uint64_t dS = kmaj(ts, item);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_bf16_w(tmem + 384, dA + kstep(kk, 16384), dS + kstep(kk, D * 128), id_k, kk > 0);
+          }
+        }
+        // the last products that read V, K and R
+        if (r == 1) tc::commit_w(bar(kGBarEmpty + kGV));
+        if (r == 2) {
+          tc::commit_w(bar(kGBarEmpty + kGK));
+          tc::commit_w(bar(kGBarEmpty + kGR));
+        }
+        ok = r < 2 ? scores(r + 1, item, k + 1) : !more || scores(0, item + 1, k + 1);
+        ok = ok && full(tb, item) && wtw(bar(kGBarP + (k & 1)), (k >> 1) & 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint64_t dC = nmaj(tb, item, 16384);
+        // P chunk c (16 columns) sits in the 8 columns 32 (c / 2) + 8 (c % 2)
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_bf16_ts_w(tmem + 256, tmem + (k & 1) * 128 + (kk >> 1) * 32 + (kk & 1) * 8, dC + ((kk * 2048) >> 4),
+                            id_n, kk > 0);
+        tc::commit_w(bar(kGBarO + (k & 1)));
+      }
+      ++item;
+      it = nx;
+    }
+    tc::commit_w(bar(kGBarFinal));
+    mbar_wait_bounded(bar(kGBarFinal), 0, 2000000000ull);   // every MMA has completed
+  } else if (warp == 18) {
+    // ============================ TMA stores ==============================
+    if (lane == 0) {
+      int item = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
+        const LinItem it = grad_item(p, i);
+        if (it.L <= 0) continue;
+        for (int r = 0; r < 3; ++r) {
+          if (!wt(bar(kGBarStage + r), item & 1)) {
+            ok = false;
+            break;
+          }
+          const int s = slot(out_tile(r), item);
+          for (int x = 0; x < 2 * NH; ++x) {
+            const int t0 = it.n * kC + (x & 1) * kSub;
+            if (t0 < p.z.T) tma_store_4d(&p.map[1 + r], sb + s * kOSlot + x * 8192, (x >> 1) * 64, it.h, t0, it.b);
+          }
+          bulk_commit_group();
+          bulk_wait_group_read0();
+          mbar_arrive(bar(kGBarEmpty + s));
+        }
+        ++item;
+      }
+      bulk_wait_group0();
+    }
+  } else {
+    // ============================ mask and output =========================
+    const int qd = warp & 3, row = 32 * qd + lane, hc = ((warp - 2) >> 2) & 1;   // hc: half of the columns
+    const int set = (warp - 2) >> 3;                          // takes the steps of one parity
+    const uint32_t lanebase = static_cast<uint32_t>(32 * qd) << 16;
+    int item = 0, k = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
+      const LinItem it = grad_item(p, i);
+      if (it.L <= 0) {                                        // rows behind the sequence
+        const int t = it.n * kC + row;
+        for (int r = 1; r < 4 && set == 0 && t < p.z.T; ++r) {
+          __nv_bfloat16 *dst = p.out[r] + (static_cast<size_t>(it.b) * p.z.T + t) * p.stride[r] + it.h * D;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) reinterpret_cast<uint4 *>(dst)[hc * (D / 16) + c] = make_uint4(0, 0, 0, 0);
+        }
+        continue;
+      }
+      const float l2 = log2_decay(p.z.log_decay[it.kv]);
+      for (int r = 0; ok && r < 3; ++r, ++k) {
+        if ((k & 1) != set) continue;
+        const bool rev = r > 0;
+        const MaskWeights mw(l2, rev);
+        if (!wtw(bar(kGBarS + set), (k >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        mask_scores(tmem + lanebase + set * 128, mw, p.z.scale, row, qd, hc, rev, 0, it.L);
+        if (it.L < kC) {
+          // rows of C behind the sequence may hold anything: 0 * NaN must not reach the product
+          const int ct = r == 0 ? kGK : r == 1 ? kGQ : kGDO, s = slot(ct, item);
+          if (!wtw(bar(kGBarFull + s), phase(ct, item))) {
+            ok = false;
+            break;
+          }
+          if (row >= it.L && hc < NH) {
+            unsigned char *cr = smem + s * kOSlot + hc * 16384 + row * 128;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4 *>(cr + 16 * e) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tc::wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(bar(kGBarP + set));
+        if (!wtw(bar(kGBarO + set), (k >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        const float fac = rev ? lexp2(l2 * static_cast<float>(max(it.L - 1 - row, 0)))
+                              : p.z.scale * lexp2(l2 * static_cast<float>(row + 1));
+        stage_rows<D>(tmem + lanebase, smem + slot(out_tile(r), item) * kOSlot, row, hc, rev ? has_r(it) : has_s(it), fac,
+                      row < it.L);
+        tc::fence_before_sync();
+        mbar_arrive(bar(kGBarOEmpty));
+        fence_proxy_async_smem();
+        mbar_arrive(bar(kGBarStage + r));
+      }
       ++item;
     }
   }
@@ -963,11 +1282,14 @@ cudaError_t launch_lin(const CUtensorMap (&tm)[6], const LinStateParams &sp, con
     e = exact ? launch_state<D, 3>(tm, sp, st) : launch_state<D, 2>(tm, sp, st);
     if (e != cudaSuccess) return e;
   }
-  const auto kern = lin_out_kernel<D>;
+  const bool grad = op.backward && op.z.G == 1 && !op.direct;
+  const auto kern = grad ? lin_grad_kernel<D> : lin_out_kernel<D>;
   e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), kOSmem);
   if (e != cudaSuccess) return e;
-  const int grid = op.items < sms ? op.items : sms;
-  kern<<<grid, kOThr, kOSmem, st>>>(tm[0], tm[1], tm[2], tm[3], op);
+  LinOutParams o = op;
+  if (grad) o.items /= 3;               // the three outputs of a chunk together
+  const int grid = o.items < sms ? o.items : sms;
+  kern<<<grid, grad ? kGThr : kOThr, kOSmem, st>>>(tm[0], tm[1], tm[2], tm[3], o);
   return cudaGetLastError();
 }
 
