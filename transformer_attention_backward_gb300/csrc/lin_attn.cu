@@ -132,8 +132,13 @@ template <int NS>
 struct StateShape {
   static constexpr int kN = NS == 3 ? 128 : 64;      // columns of U (with three terms the last 32 are unused)
   static constexpr int kSlot = 2 * 8192 + 4096;
+  // A group comes back to the slots it has waited for before: loads complete in
+  // any order, and with slots that change hands a wait could take the phase
+  // before the last for the one it waits for.
   static constexpr int kRing = 6;
+  static_assert(kRing % kSGroups == 0, "a slot belongs to one group");
   static constexpr int kWSlot = kN / 64 * 8192, kWRing = 4;
+  static_assert(kWRing >= kSGroups, "every group has a buffer to work on");
   static constexpr int kOffW = kRing * kSlot;
   static constexpr int kOffBar = kOffW + kWRing * kWSlot;
   static constexpr int kFull = 0, kDone = kRing, kW = 2 * kRing, kUEmpty = kW + kWRing, kFinal = kUEmpty + 2;
@@ -195,6 +200,9 @@ __global__ void __launch_bounds__(kSThr, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + Z::kOffTmem);
+  // the output kernel's CTAs may start on SMs that this grid's tail leaves idle;
+  // they wait for its end before they read a state
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int steps = nst * gi;
   // step i: tokens [64 (i & 1), 64 (i & 1) + 64) of chunk i / gi, head (i % gi) / 2
   auto phase = [](int i) -> uint32_t { return static_cast<uint32_t>(i / Z::kRing) & 1u; };
@@ -474,6 +482,9 @@ __device__ __noinline__ LinItem lin_item(const LinOutParams &p, int i) {
   return it;
 }
 
+// The output kernels start as programmatic dependents of lin_state.
+__device__ __forceinline__ void wait_states() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The row and column powers of the weights scale a^(distance) of a score tile.
 // Inside a block of 16 columns a weight is a power for the row times one for
 // the column (pw).  Next to the diagonal the row's is above 1, up to a^-31;
@@ -605,7 +616,7 @@ __global__ void __launch_bounds__(kOThr, 1)
     // ============================ TMA producer ============================
     if (lane == 0) {
       int q = 0, item = 0;
-      bool ok = true;
+      bool ok = true, states = false;                         // states: they are there
       auto slot = [&](uint32_t bytes) -> bool {       // claims the next slot
         const int s = q % kOSlots;
         if (!wt(bar(kOBarEmpty + s), phase(q) ^ 1u)) return ok = false;
@@ -639,6 +650,8 @@ __global__ void __launch_bounds__(kOThr, 1)
           tile(mb, it, hg, n);
           if (g == 0 && it.st && ok && slot(D * D * 2)) {
             const int s = (q - 1) % kOSlots;
+            if (!states) wait_states();
+            states = true;
             const __nv_bfloat16 *src = p.tiles[it.role >> 1] +
                                        (static_cast<size_t>(it.b * p.z.Hkv + it.kv) * p.z.NC + it.n) * (D * D);
             bulk_load(sb + s * kOSlot, src, D * D * 2, bar(kOBarFull + s));
@@ -647,6 +660,7 @@ __global__ void __launch_bounds__(kOThr, 1)
           if (++far == it.ns) far = 0, ++hg;
         }
       }
+      if (!states) wait_states();                             // nor does this grid end before
       if (*abort_flag) {
         for (int x = (q > kOSlots ? q - kOSlots : 0); x < q; ++x)
           mbar_wait_bounded(bar(kOBarFull + x % kOSlots), phase(x), 2000000000ull);
@@ -908,7 +922,7 @@ __global__ void __launch_bounds__(kGThr, 1)
       // in the order in which the last item's tiles are done with: dO, V, S, Q, K, R
       auto tile_at = [](int e) -> int { return e == 0 ? kGDO : e - 1; };
       int loads = 0, item = 0;
-      bool ok = true;
+      bool ok = true, states = false;
       for (int i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
         const LinItem it = grad_item(p, i);
         if (it.L <= 0) continue;
@@ -922,6 +936,8 @@ __global__ void __launch_bounds__(kGThr, 1)
           }
           if (tile == kGS || tile == kGR) {
             if (tile == kGS ? has_s(it) : has_r(it)) {
+              if (!states) wait_states();
+              states = true;
               mbar_arrive_expect_tx(fb, D * D * 2);
               bulk_load(dst, p.tiles[tile == kGR] + (static_cast<size_t>(it.b * p.z.Hkv + it.kv) * p.z.NC + it.n) * (D * D),
                         D * D * 2, fb);
@@ -938,6 +954,7 @@ __global__ void __launch_bounds__(kGThr, 1)
         }
         if (ok) ++item;
       }
+      if (!states) wait_states();
       if (*abort_flag)                                        // the last load of every slot
         for (int x = (loads > 12 ? loads - 12 : 0); x < loads; ++x)
           mbar_wait_bounded(bar(kGBarFull + slot(tile_at(x % 6), x / 6)), phase(tile_at(x % 6), x / 6), 2000000000ull);
@@ -1289,8 +1306,17 @@ cudaError_t launch_lin(const CUtensorMap (&tm)[6], const LinStateParams &sp, con
   LinOutParams o = op;
   if (grad) o.items /= 3;               // the three outputs of a chunk together
   const int grid = o.items < sms ? o.items : sms;
-  kern<<<grid, grad ? kGThr : kOThr, kOSmem, st>>>(tm[0], tm[1], tm[2], tm[3], o);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(grad ? kGThr : kOThr);
+  cfg.dynamicSmemBytes = kOSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = sp.nroles ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, tm[0], tm[1], tm[2], tm[3], o);
 }
 
 size_t tiles_bytes(int B, int T, int Hkv, int D) {

@@ -411,6 +411,8 @@ __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? bwd_blocks<XT, DT, I
   const int lane = threadIdx.x % L, grp = threadIdx.x / L, slot = grp % slots;
   const int steps = (sd.H + slots - 1) / slots;
   const bool norm = sd.gamma != nullptr;
+  // qk_dgamma may start; it waits for this grid's end before it reads
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   load_turns(p, turns);
   F ga[N][C], gb[N][C], dga[N][C], dgb[N][C];                 // of this lane's components
   lane_gamma<V, N, L, INTER>(sd.gamma, lane, p.rot, h2, ga, gb);
@@ -526,22 +528,24 @@ __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? bwd_blocks<XT, DT, I
 
 // dgamma = sum of the blocks' partials, in a fixed order: a block takes 32
 // components of queries or keys, its 8 warps every 8th partial.
-__global__ void __launch_bounds__(256) qk_dgamma_kernel(const float *__restrict__ part, float *__restrict__ dgq,
+__global__ void __launch_bounds__(256) qk_dgamma_kernel(const float *part, float *__restrict__ dgq,
                                                         float *__restrict__ dgk, int first_k, int nparts, int D) {
   __shared__ float red[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   float *dst = blockIdx.y ? dgk : dgq;
   const int lo = blockIdx.y ? first_k : 0, hi = blockIdx.y ? nparts : first_k;
-  if (!dst) return;
   float t = 0.f;
-  if (col < D)
-    for (int i = lo + warp; i < hi; i += 8) t += part[static_cast<size_t>(i) * D + col];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (col < D) {
+#pragma unroll 8
+    for (int i = lo + warp; i < hi; i += 8) t += __ldcg(part + static_cast<size_t>(i) * D + col);
+  }
   red[warp][lane] = t;
   __syncthreads();
   if (warp == 0 && col < D) {
     for (int i = 1; i < 8; ++i) t += red[i][lane];
-    dst[col] = t;
+    if (dst) dst[col] = t;
   }
 }
 
@@ -582,8 +586,17 @@ cudaError_t qk_launch(QkParams &p, const unsigned long long *freq, int sms, cuda
     qk_bwd_kernel<XT, DT, INTER, V, N, L><<<grid, kQThr, smem, st>>>(t);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.part) return e;
-    const dim3 g((p.D + 31) / 32, 2);
-    qk_dgamma_kernel<<<g, 256, 0, st>>>(p.part, p.dgamma[0], p.dgamma[1], p.first_k, static_cast<int>(grid), p.D);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((p.D + 31) / 32, 2);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, qk_dgamma_kernel, static_cast<const float *>(p.part), p.dgamma[0], p.dgamma[1],
+                              p.first_k, static_cast<int>(grid), p.D);
   } else {
     constexpr int U = V == 1 || N > 1 ? 1 : 2;
     qk_fwd_kernel<XT, INTER, V, N, L, U><<<grid, kQThr, 0, st>>>(t);
