@@ -465,7 +465,11 @@ __device__ __noinline__ LinItem lin_item(const LinOutParams &p, int i) {
   i /= p.z.Hkv;
   it.n = i % NC;
   it.b = i / NC;
-  if (p.direct && it.role < 2) it.n = NC - 1 - it.n;          // the longer items first
+  if (p.direct) {
+    if (it.role < 2) it.n = NC - 1 - it.n;                    // the longer items first
+  } else {
+    it.n = NC - 1 - it.n, it.b = p.z.B - 1 - it.b;            // what lin_state has read last first: L2 still holds it
+  }
   it.len = seq_len(p.z.lengths, it.b, p.z.T);
   it.L = min(kC, it.len - it.n * kC);
   if (it.role < 2) {
@@ -863,8 +867,8 @@ __device__ __noinline__ LinItem grad_item(const LinOutParams &p, int i) {
   LinItem it;
   it.kv = it.h = i % p.z.Hkv;
   i /= p.z.Hkv;
-  it.n = i % p.z.NC;
-  it.b = i / p.z.NC;
+  it.n = p.z.NC - 1 - i % p.z.NC;                             // what lin_state has read last first
+  it.b = p.z.B - 1 - i / p.z.NC;
   it.len = seq_len(p.z.lengths, it.b, p.z.T);
   it.L = min(kC, it.len - it.n * kC);
   return it;
