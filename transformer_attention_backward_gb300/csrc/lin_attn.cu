@@ -18,7 +18,8 @@
 //   lin_state : walks the chunks of one (batch, KV head) and leaves the state
 //               that enters each of them as a bf16 tile in the workspace
 //   lin_out   : one item per 128 output rows; everything it needs is there,
-//               so items run in any order
+//               so items run in any order (lin_grad, where every query head has
+//               a KV head of its own: dq, dk and dv of a chunk in one item)
 // Short sequences without states at their ends take the second alone: an item
 // goes through the products of the chunks before it (behind it) as well, which
 // for a few chunks costs less than the walk and its launch.
@@ -111,18 +112,20 @@ struct LinSizes {
 // itself stays in fp32 registers, and each step's U is added there: sums over
 // steps or terms inside the tensor core would cut off bits of the
 // accumulator's size at every one (measured: 5 times the error).
-// The chain of a step (load, weights, product, addition) is long and the work
-// in it small, so what counts is how many steps are under way: a ring of 6
-// (X, Y) slots, four buffers of weighted rows, filled in turn by three groups of
-// warps (8192 tokens of 32 heads: 55 us; two groups 59, four 58), and two buffers
-// of U.  32 columns, not 64: X is read by twice as many CTAs (from L2), but a step
-// moves 2/3 of the bytes through shared memory and there are twice as many
-// chains (before the third group: 8192 tokens of 32 heads 59 us against 103, 640
-// chains of 2048 tokens 83 against 83).
-// Warps: 0 TMA, 1 MMA, 2-13 weights, 14-17 state.
+// Bound by shared memory: a step moves 20 KB into it by TMA, 16 KB for the
+// weighted rows (read, formed, written) and 28 KB out of it to the tensor core,
+// some 500 of the 650 cycles that a step takes.  What hides the rest is steps
+// under way: a ring of 6 (X, Y) slots, four buffers of weighted rows, filled in
+// turn by three groups of warps (8192 tokens of 32 heads: 55 us; two groups 59,
+// four 58), two MMA warps and two buffers of U (deeper rings: no change).
+// 32 columns a CTA, not 64: 52 us against 95 for 8192 tokens of 32 heads, as
+// there are twice as many chains; 76 against 81 for 640 chains of 2048 tokens.
+// X once for all CTAs of a chain, by multicast: 57 and 85.
+// Warps: 0 TMA, 1 and 18 MMA, 2-13 weights, 14-17 state.
 // ---------------------------------------------------------------------------
 constexpr int kSGroups = 3;                          // groups of four warps that form weighted rows
-constexpr int kSThr = 64 + kSGroups * 128 + 128;
+constexpr int kSThr = 64 + kSGroups * 128 + 128 + 32;
+constexpr int kSMma2 = kSThr / 32 - 1;               // the second MMA warp
 constexpr int kCW = 32;
 
 // A slot: X (two 64-column parts of 8 KB) | Y (32 columns, 4 KB); the weighted
@@ -130,19 +133,19 @@ constexpr int kCW = 32;
 // their own (two terms of 32 columns to an 8 KB part).
 template <int NS>
 struct StateShape {
-  static constexpr int kN = NS == 3 ? 128 : 64;      // columns of U (with three terms the last 32 are unused)
+  static constexpr int kN = NS * kCW;                // columns of U
   static constexpr int kSlot = 2 * 8192 + 4096;
   // A group comes back to the slots it has waited for before: loads complete in
   // any order, and with slots that change hands a wait could take the phase
   // before the last for the one it waits for.
   static constexpr int kRing = 6;
   static_assert(kRing % kSGroups == 0, "a slot belongs to one group");
-  static constexpr int kWSlot = kN / 64 * 8192, kWRing = 4;
+  static constexpr int kWSlot = (kN + 63) / 64 * 8192, kWRing = 4;
   static_assert(kWRing >= kSGroups, "every group has a buffer to work on");
   static constexpr int kOffW = kRing * kSlot;
   static constexpr int kOffBar = kOffW + kWRing * kWSlot;
   static constexpr int kFull = 0, kDone = kRing, kW = 2 * kRing, kUEmpty = kW + kWRing, kFinal = kUEmpty + 2;
-  static constexpr int kOffTmem = kOffBar + (kFinal + 1) * 8, kOffAbort = kOffTmem + 4;
+  static constexpr int kOffTmem = kOffBar + (kFinal + 2) * 8, kOffAbort = kOffTmem + 4;
   static constexpr int kSmem = kOffBar + 256 + 1024;                   // + alignment slack
   static_assert(kOffAbort + 4 <= kOffBar + 256 && kSmem <= 232448 && kOffW % 1024 == 0, "state kernel shared memory");
 };
@@ -191,7 +194,7 @@ __global__ void __launch_bounds__(kSThr, 1)
     }
     for (int s = 0; s < Z::kWRing; ++s) mbar_init(bar(Z::kW + s), 128);
     for (int s = 0; s < 2; ++s) mbar_init(bar(Z::kUEmpty + s), 128);
-    mbar_init(bar(Z::kFinal), 1);
+    for (int s = 0; s < 2; ++s) mbar_init(bar(Z::kFinal + s), 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -229,18 +232,20 @@ __global__ void __launch_bounds__(kSThr, 1)
         for (int i = (issued > Z::kRing ? issued - Z::kRing : 0); i < issued; ++i)
           mbar_wait_bounded(bar(Z::kFull + i % Z::kRing), phase(i), 2000000000ull);
     }
-  } else if (warp == 1) {
-    // ============================ MMA issuer ==============================
+  } else if (warp == 1 || warp == kSMma2) {
+    // ============================ MMA issuers =============================
+    // Two warps take the steps in turn: a step's hundred instructions of one
+    // warp among busy ones take about as long as the step.
     // X is the M-major A operand.  For D = 64 rows 64-127 of A come from the
     // unused second part of the X slot; they only reach TMEM lanes 64-127,
     // which nobody reads.
     constexpr uint32_t id_u = tc::idesc_bf16_f32(128, Z::kN, 1, 1);
+    const int u = warp == 1 ? 0 : 1;
     const uint64_t dX = tc::sdesc_sw128(sb, 8192, 1024);
     const uint64_t dW = tc::sdesc_sw128(sb + Z::kOffW, 8192, 1024);
-    for (int i = 0, s = 0, w = 0, wph = 0; i < steps; ++i) {
-      const int u = i & 1;
+    for (int i = u, s = u, w = u, wph = 0, uph = 1; i < steps; i += 2, uph ^= 1) {
       // (weighted rows that are there were formed from a stage that is there)
-      if (!wtw(bar(Z::kUEmpty + u), ((i >> 1) & 1) ^ 1) || !wtw(bar(Z::kW + w), wph)) break;
+      if (!wtw(bar(Z::kUEmpty + u), uph) || !wtw(bar(Z::kW + w), wph)) break;
       tc::fence_after_sync();
       const uint64_t so = static_cast<uint64_t>(s * Z::kSlot) >> 4, wo = static_cast<uint64_t>(w * Z::kWSlot) >> 4;
       // the terms side by side as N: X is read once for all of them
@@ -250,14 +255,21 @@ __global__ void __launch_bounds__(kSThr, 1)
       // one signal for all who wait for the step: the stage and the weighted
       // rows are free, U is there
       tc::commit_w(bar(Z::kDone + s));
-      if (++s == Z::kRing) s = 0;
-      if (++w == Z::kWRing) w = 0, wph ^= 1;
+      if ((s += 2) >= Z::kRing) s -= Z::kRing;
+      if ((w += 2) >= Z::kWRing) w -= Z::kWRing, wph ^= 1;
     }
-    tc::commit_w(bar(Z::kFinal));
-    mbar_wait_bounded(bar(Z::kFinal), 0, 2000000000ull);   // every MMA has completed
+    tc::commit_w(bar(Z::kFinal + u));
+    mbar_wait_bounded(bar(Z::kFinal + u), 0, 2000000000ull);   // every MMA has completed
   } else if (warp < 2 + 4 * kSGroups) {
     // ============================ weights =================================
     const int grp = (warp - 2) >> 2, wtid = (tid - 64) & 127;
+    auto weight = [&](int row, int L) -> float {
+      return role ? p.z.scale * lexp2(l2 * static_cast<float>(row + 1)) : lexp2(l2 * static_cast<float>(L - 1 - row));
+    };
+    float whole[2][kCW / 16];                                 // of this thread's rows in a whole chunk
+#pragma unroll
+    for (int c = 0; c < 2 * (kCW / 16); ++c)
+      whole[c & 1][c >> 1] = weight(((wtid + 128 * (c >> 1)) >> 2) + (c & 1) * kSub, kC);
     for (int i = grp, s = grp, ph = 0, w = grp, m = 0, g = grp; i < steps; i += kSGroups) {
       while (g >= gi) g -= gi, ++m;
       const int u = g & 1;                                    // half of the chunk
@@ -271,20 +283,18 @@ __global__ void __launch_bounds__(kSThr, 1)
         // 16-byte piece j of the row of token `row` of the chunk
         const int id = wtid + 128 * c, r = id >> 2, j = id & 3, row = r + u * kSub;
         uint4 out[NS];
-        if (row < L) {
-          const float wgt = role ? p.z.scale * lexp2(l2 * static_cast<float>(row + 1))
-                                 : lexp2(l2 * static_cast<float>(L - 1 - row));
+        if (L == kC || row < L) {
+          const float wgt = L < kC ? weight(row, L) : u ? whole[1][c] : whole[0][c];
           const uint4 y = *reinterpret_cast<const uint4 *>(st + 16384 + 16 * id);
           const uint32_t yi[4] = {y.x, y.y, y.z, y.w};
           uint32_t o[NS][4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float f0 = wgt * bf16_lo(yi[e]), f1 = wgt * bf16_hi(yi[e]);
+            float2 f = __fmul2_rn(make_float2(bf16_lo(yi[e]), bf16_hi(yi[e])), make_float2(wgt, wgt));
 #pragma unroll
             for (int t = 0; t < NS; ++t) {
-              o[t][e] = lpack2(f0, f1);
-              f0 -= bf16_lo(o[t][e]);
-              f1 -= bf16_hi(o[t][e]);
+              o[t][e] = lpack2(f.x, f.y);
+              f = __ffma2_rn(make_float2(bf16_lo(o[t][e]), bf16_hi(o[t][e])), make_float2(-1.f, -1.f), f);
             }
           }
 #pragma unroll
@@ -314,15 +324,15 @@ __global__ void __launch_bounds__(kSThr, 1)
     const uint32_t lanebase = static_cast<uint32_t>(32 * qd) << 16;
     const bool live = row < D;
     const size_t at = (static_cast<size_t>(bh) * D + row) * D + part * kCW;
-    float S[kCW];
+    float2 S[kCW / 2];
 #pragma unroll
-    for (int c = 0; c < kCW; ++c) S[c] = 0.f;
+    for (int c = 0; c < kCW / 2; ++c) S[c] = make_float2(0.f, 0.f);
     if (live && p.start[role]) {
       const float4 *src = reinterpret_cast<const float4 *>(p.start[role] + at);
 #pragma unroll
       for (int c = 0; c < kCW / 4; ++c) {
         const float4 v = src[c];
-        S[4 * c] = v.x, S[4 * c + 1] = v.y, S[4 * c + 2] = v.z, S[4 * c + 3] = v.w;
+        S[2 * c] = make_float2(v.x, v.y), S[2 * c + 1] = make_float2(v.z, v.w);
       }
     }
     bool ok = true;
@@ -336,8 +346,8 @@ __global__ void __launch_bounds__(kSThr, 1)
 #pragma unroll
         for (int c = 0; c < kCW / 8; ++c)
           *reinterpret_cast<uint4 *>(dst + ((((part & 1) * 4 + c) ^ (row & 7)) << 4)) =
-              make_uint4(lpack2(S[8 * c], S[8 * c + 1]), lpack2(S[8 * c + 2], S[8 * c + 3]),
-                         lpack2(S[8 * c + 4], S[8 * c + 5]), lpack2(S[8 * c + 6], S[8 * c + 7]));
+              make_uint4(lpack2(S[4 * c].x, S[4 * c].y), lpack2(S[4 * c + 1].x, S[4 * c + 1].y),
+                         lpack2(S[4 * c + 2].x, S[4 * c + 2].y), lpack2(S[4 * c + 3].x, S[4 * c + 3].y));
       }
       if (m >= nst) break;
       for (int g = 0; g < gi; ++g) {
@@ -349,16 +359,19 @@ __global__ void __launch_bounds__(kSThr, 1)
         const float dec = g == 0 ? lexp2(l2 * static_cast<float>(min(kC, len - n * kC))) : 1.f;
 #pragma unroll
         for (int x = 0; x < kCW / 16; ++x) {
-          float t[16];
+          float2 t[8];
 #pragma unroll
           for (int e = NS - 1; e >= 0; --e) {                 // the small terms first
             uint32_t v[16];
             tc::ld16_wait(tmem + lanebase + u * 256 + e * kCW + x * 16, v);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) t[c] = e == NS - 1 ? __uint_as_float(v[c]) : t[c] + __uint_as_float(v[c]);
+            for (int c = 0; c < 8; ++c) {
+              const float2 w = make_float2(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
+              t[c] = e == NS - 1 ? w : __fadd2_rn(t[c], w);
+            }
           }
 #pragma unroll
-          for (int c = 0; c < 16; ++c) S[x * 16 + c] = fmaf(dec, S[x * 16 + c], t[c]);
+          for (int c = 0; c < 8; ++c) S[x * 8 + c] = __ffma2_rn(make_float2(dec, dec), S[x * 8 + c], t[c]);
         }
         tc::fence_before_sync();
         mbar_arrive(bar(Z::kUEmpty + u));
@@ -370,7 +383,7 @@ __global__ void __launch_bounds__(kSThr, 1)
     if (ok && live && p.end[role]) {
       float4 *dst = reinterpret_cast<float4 *>(p.end[role] + at);
 #pragma unroll
-      for (int c = 0; c < kCW / 4; ++c) dst[c] = make_float4(S[4 * c], S[4 * c + 1], S[4 * c + 2], S[4 * c + 3]);
+      for (int c = 0; c < kCW / 4; ++c) dst[c] = make_float4(S[2 * c].x, S[2 * c].y, S[2 * c + 1].x, S[2 * c + 1].y);
     }
   }
   tc::fence_before_sync();
@@ -402,6 +415,9 @@ __global__ void __launch_bounds__(kSThr, 1)
 // go side by side), 10 TMA stores.  The output tile is written over A, which
 // no product needs by then, and leaves from there by TMA (16-byte stores by
 // the rows' threads took 2,400 cycles of an item's 8,300).
+// Over long sequences bound by memory: the forward of 8192 tokens of 32 heads
+// takes 53 us, its copies alone 50.  (Two sets of mask warps and scores formed
+// an item ahead, as in lin_grad: no change here.)
 // ---------------------------------------------------------------------------
 constexpr int kOThr = 352;
 constexpr int kOSlots = 5;            // of the ring; the two slots of A follow
@@ -845,7 +861,8 @@ __global__ void __launch_bounds__(kOThr, 1)
 // query head has a KV head of its own: the three outputs (roles 1, 2, 3 of
 // lin_out, in this order) share Q, K, V, dO, S and R, so 192 KB a chunk arrive
 // in place of 384.  lin_out there is bound by those copies: without all else its
-// loads took 46 us of its 81 (4 x 2048 tokens of 20 heads).
+// loads took 46 us of its 81 (4 x 2048 tokens of 20 heads).  This one takes 67;
+// its copies alone, 378 MB, 51.
 // Every tile has a slot of its own, dO two.  An output is staged over a tile
 // that no product needs any more (dq over S, dk over Q, dv over dO), chosen such
 // that the next item's tiles can arrive in the order in which they are needed.
