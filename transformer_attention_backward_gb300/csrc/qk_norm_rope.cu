@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? 3 : 1)
 // tokens and keep their lanes' dgamma in registers.  The next row of a group is
 // loaded while this one is at work.  Registers are held to what lets
 // bwd_blocks blocks be resident.  4 x 2048 tokens, 20 + 20 heads of 128 bf16, dy
-// bf16 (252 MB): 59 us with dgamma, bound by instruction issue.
+// bf16 (252 MB): 57 us with dgamma, bound by instruction issue.
 template <typename XT, typename DT, bool INTER>
 constexpr int bwd_blocks() { return sizeof(XT) + sizeof(DT) == 4 && !INTER ? 4 : 3; }
 
@@ -528,10 +528,12 @@ __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? bwd_blocks<XT, DT, I
 }
 
 // dgamma = sum of the blocks' partials, in a fixed order: a block takes 32
-// components of queries or keys, its 8 warps every 8th partial.
-__global__ void __launch_bounds__(256) qk_dgamma_kernel(const float *part, float *__restrict__ dgq,
-                                                        float *__restrict__ dgk, int first_k, int nparts, int D) {
-  __shared__ float red[8][32];
+// components of queries or keys, its 32 warps every 32nd partial (8 warps: 3 us
+// more for 600 partials, all of it waiting for loads).
+constexpr int kGammaWarps = 32;
+__global__ void __launch_bounds__(32 * kGammaWarps)
+    qk_dgamma_kernel(const float *part, float *__restrict__ dgq, float *__restrict__ dgk, int first_k, int nparts, int D) {
+  __shared__ float red[kGammaWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
   float *dst = blockIdx.y ? dgk : dgq;
@@ -540,12 +542,12 @@ __global__ void __launch_bounds__(256) qk_dgamma_kernel(const float *part, float
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (col < D) {
 #pragma unroll 8
-    for (int i = lo + warp; i < hi; i += 8) t += __ldcg(part + static_cast<size_t>(i) * D + col);
+    for (int i = lo + warp; i < hi; i += kGammaWarps) t += __ldcg(part + static_cast<size_t>(i) * D + col);
   }
   red[warp][lane] = t;
   __syncthreads();
   if (warp == 0 && col < D) {
-    for (int i = 1; i < 8; ++i) t += red[i][lane];
+    for (int i = 1; i < kGammaWarps; ++i) t += red[i][lane];
     if (dst) dst[col] = t;
   }
 }
@@ -589,7 +591,7 @@ cudaError_t qk_launch(QkParams &p, const unsigned long long *freq, int sms, cuda
     if (e != cudaSuccess || !p.part) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((p.D + 31) / 32, 2);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(32 * kGammaWarps);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
