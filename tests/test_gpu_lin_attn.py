@@ -102,7 +102,7 @@ def test_more_items_than_sms(abw):
     """Persistent CTAs take several items each, ragged ones among them."""
     check(abw, make(1, 5, 330, 16, 4, 64, True), lengths=[330, 0, 129, 1, 256])
     check(abw, make(2, 3, 260, 40, 40, 64, False))
-    check(abw, make(3, 4, 700, 24, 24, 128, False), lengths=[700, 513, 0, 385])     # a KV head of its own for each
+    check(abw, make(3, 4, 800, 24, 24, 128, False), lengths=[800, 513, 0, 385])     # a KV head of its own for each
     check(abw, make(4, 2, 900, 30, 30, 64, True), lengths=[900, 129])
 
 

@@ -35,11 +35,15 @@ namespace {
 
 constexpr int kC = 128;               // tokens per chunk
 constexpr int kSub = 64;              // tokens per TMA box: half a chunk
-// Most chunks whose outputs are formed without states.  Forward / backward us,
-// with the walk and without: 2 x 512 tokens of 20/5 heads 14.8 / 24.5, 12.0 / 25.6
-// (and a launch less); 4 x 768 of 20 34 / 67, 25 / 56; 2 x 768 of 20/5 16.7 / 32,
-// 17.3 / 39; 1 x 1024 of 32 18.8 / 37, 18.6 / 39.
-constexpr int kDirectFwd = 6, kDirectBwd = 4;
+// Most chunks whose outputs are formed without states; a group of query heads
+// shares its KV head's states, so fewer where there are groups.  GPU time in us
+// of forward / backward, with the walk and directly: 2 x 512 tokens of 20/5 heads
+// 11.9 / 21.0, 9.7 / 21.0 (and a launch less); 2 x 640 13.2 / 23.5, 11.6 / 27.0; 8 x
+// 768 of 16/4 25.7 / 59, 31.3 / 72; 4 x 768 of 20/20 31 / 59, 23 / 54; 4 x 1024
+// 39 / 73, 32 / 82; 1 x 1280 of 32/32 19.3 / 39, 20.4 / 49.
+constexpr int direct_chunks(bool backward, int G) {
+  return G == 1 ? (backward ? 6 : 8) : (backward ? 4 : 5);
+}
 
 __device__ __forceinline__ uint32_t lpack2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -453,6 +457,14 @@ struct LinItem {
   bool st;                                 // has a state tile
 };
 
+// The item of a CTA's round r.  Where items differ in length rounds go back and
+// forth: who had the longest of the first has the shortest of the second (2 x
+// 512 tokens of 20/5 heads, backward: 21 us for 26).
+__device__ __forceinline__ int item_at(const LinOutParams &p, int r) {
+  const int g = gridDim.x, c = blockIdx.x;
+  return r * g + (p.direct && (r & 1) ? g - 1 - c : c);
+}
+
 __device__ __noinline__ LinItem lin_item(const LinOutParams &p, int i) {
   LinItem it;
   const int NC = p.z.NC, G = p.z.G;
@@ -481,8 +493,9 @@ __device__ __noinline__ LinItem lin_item(const LinOutParams &p, int i) {
   i /= p.z.Hkv;
   it.n = i % NC;
   it.b = i / NC;
-  if (p.direct) {
-    if (it.role < 2) it.n = NC - 1 - it.n;                    // the longer items first
+  if (p.direct) {                                             // the longer items first
+    it.b = i % p.z.B;
+    it.n = it.role < 2 ? NC - 1 - i / p.z.B : i / p.z.B;
   } else {
     it.n = NC - 1 - it.n, it.b = p.z.B - 1 - it.b;            // what lin_state has read last first: L2 still holds it
   }
@@ -651,7 +664,7 @@ __global__ void __launch_bounds__(kOThr, 1)
           tma_load_4d(sb + s * kOSlot + x * 8192, m, (x >> 1) * 64, h, n * kC + (x & 1) * kSub, it.b,
                       bar(kOBarFull + s));
       };
-      for (int i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
+      for (int r = 0, i = item_at(p, 0); ok && i < p.items; i = item_at(p, ++r)) {
         const LinItem it = lin_item(p, i);
         if (it.L <= 0) continue;
         const CUtensorMap *ma = it.role == 0 ? &tmQ : it.role == 1 ? &tmDO : it.role == 2 ? &tmV : &tmK;
@@ -699,7 +712,7 @@ __global__ void __launch_bounds__(kOThr, 1)
     int q = 0, ss = 0, item = 0;
     bool ok = true;
     auto full = [&](int x) -> bool { return wtw(bar(kOBarFull + x % kOSlots), phase(x)); };
-    for (int i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
+    for (int r = 0, i = item_at(p, 0); ok && i < p.items; i = item_at(p, ++r)) {
       const LinItem it = lin_item(p, i);
       if (it.L <= 0) continue;
       const int q0 = q, st = it.st ? 1 : 0, as = item & 1;
@@ -767,7 +780,7 @@ __global__ void __launch_bounds__(kOThr, 1)
     // ============================ TMA stores ==============================
     if (lane == 0) {
       int item = 0;
-      for (int i = blockIdx.x; i < p.items; i += gridDim.x) {
+      for (int r = 0, i = item_at(p, 0); i < p.items; i = item_at(p, ++r)) {
         const LinItem it = lin_item(p, i);
         if (it.L <= 0) continue;
         const int as = item & 1;
@@ -790,7 +803,7 @@ __global__ void __launch_bounds__(kOThr, 1)
     const uint32_t lanebase = static_cast<uint32_t>(32 * qd) << 16;
     int q = 0, ss = 0, item = 0;
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < p.items; i += gridDim.x) {
+    for (int r = 0, i = item_at(p, 0); ok && i < p.items; i = item_at(p, ++r)) {
       const LinItem it = lin_item(p, i);
       const int t = it.n * kC + row;
       if (it.L <= 0) {                                        // rows behind the sequence
@@ -1365,7 +1378,7 @@ cudaError_t launch_lin_attn(const LinAttnArgs &a, const WaitCtl &w, cudaStream_t
   op.z.lengths = a.lengths;
   op.backward = bwd;
   const long long items = static_cast<long long>(a.B) * op.z.NC * (bwd ? a.Hq + 2LL * a.Hkv : a.Hq);
-  if (items > 0x7ffffff0LL - sms || 8LL * a.B * a.Hkv > 0x7fffffffLL) {
+  if (items > 0x7ffffff0LL - 2 * sms || 8LL * a.B * a.Hkv > 0x7fffffffLL) {
     *why = "grid too large";
     return cudaErrorNotSupported;
   }
@@ -1378,7 +1391,7 @@ cudaError_t launch_lin_attn(const LinAttnArgs &a, const WaitCtl &w, cudaStream_t
   sp.end[1] = a.dinitial_state;
   // which recurrences anything reads: the tiles of more than one chunk or of
   // a given start, and the states that leave
-  op.direct = op.z.NC <= (bwd ? kDirectBwd : kDirectFwd) && !a.initial_state && !a.final_state && !a.dfinal_state &&
+  op.direct = op.z.NC <= direct_chunks(bwd, op.z.G) && !a.initial_state && !a.final_state && !a.dfinal_state &&
               !a.dinitial_state;
   const bool far = op.z.NC > 1 && !op.direct;
   const bool tiles0 = far || a.initial_state, tiles1 = bwd && (far || a.dfinal_state);
