@@ -216,9 +216,10 @@ def test_state_in_place_continues_a_prompt(abw):
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
-def test_offsets_past_32_bits(abw):
+@pytest.mark.parametrize("Hkv", [2, 4])
+def test_offsets_past_32_bits(abw, Hkv):
     """Tokens some 2^23 elements apart: the last ones start behind 2^31."""
-    T, Hq, Hkv, D, gap = 150, 4, 2, 64, 1 << 23
+    T, Hq, D, gap = 150, 4, 64, 1 << 23
     t = make(15, 2, T, Hq, Hkv, D, True)
     d = {x: cuda(y) for x, y in t.items()}
     wide = torch.empty(2, T, gap, dtype=BF, device="cuda")
@@ -238,11 +239,12 @@ def test_offsets_past_32_bits(abw):
         assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, want))
 
 
-def test_waits_that_run_out(abw):
+@pytest.mark.parametrize("Hkv", [4, 8])
+def test_waits_that_run_out(abw, Hkv):
     """A limit of zero: kernels that give up say so and leave the device as it
     was, so the next call is right."""
     from transformer_attention_backward_gb300 import _binding as B
-    t = make(16, 2, 900, 8, 4, 128, True)
+    t = make(16, 2, 900, 8, Hkv, 128, True)
     d = {x: cuda(y) for x, y in t.items()}
 
     def run():
@@ -275,8 +277,9 @@ def test_no_tokens(abw):
     assert torch.equal(g[3], d["df"])
 
 
-def test_bits_repeat_streams_and_graphs(abw):
-    t = make(14, 2, 400, 8, 4, 128, True)
+@pytest.mark.parametrize("Hkv", [4, 8])
+def test_bits_repeat_streams_and_graphs(abw, Hkv):
+    t = make(14, 2, 400, 8, Hkv, 128, True)
     d = {x: cuda(y) for x, y in t.items()}
 
     def run(**kw):
