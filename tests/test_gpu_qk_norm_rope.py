@@ -115,6 +115,21 @@ def test_tokens_and_heads(abw, B, T, Hq, Hkv):
     check(abw, B, T, Hq, Hkv, 128, 128, None, 500000.0, True, BF, F, seed=B * T)
 
 
+@pytest.mark.parametrize("inter", [True, False])
+@pytest.mark.parametrize("dtype,dy", [(BF, F), (BF, BF), (F, F), (F, BF)])
+@pytest.mark.parametrize("D,rot,Hq,Hkv", [(64, 64, 260, 3), (80, 48, 130, 2), (256, 192, 70, 70), (512, 512, 70, 1)])
+def test_many_heads(abw, D, rot, Hq, Hkv, dtype, dy, inter):
+    """Enough rows for a group of lanes that they come through shared memory."""
+    check(abw, 1, 9, Hq, Hkv, D, rot, None, 10000.0, inter, dtype, dy, seed=D)
+
+
+@pytest.mark.parametrize("inter", [True, False])
+@pytest.mark.parametrize("dtype,dy", [(BF, BF), (F, F)])
+def test_many_tokens(abw, dtype, dy, inter):
+    """The backward's groups go on from token to token, the last ones behind the end."""
+    check(abw, 2, 6001, 4, 4, 128, 96, [16, 16, 16], 10000.0, inter, dtype, dy, seed=3)
+
+
 @pytest.mark.parametrize("norm", [(False, False), (True, False), (False, True)])
 def test_without_a_norm(abw, norm):
     check(abw, 2, 11, 4, 2, 128, 64, None, 10000.0, False, BF, F, norm=norm, seed=3)

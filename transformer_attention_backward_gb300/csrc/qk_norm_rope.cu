@@ -184,6 +184,58 @@ struct Pairs<T, 1, INTER> {
   }
 };
 
+// Rows on their way: each lane copies its own pieces of the next rows into slots
+// of its own in shared memory and takes them from there, so that what is under
+// way costs no registers, and no thread waits for another.  (What bounds these
+// kernels otherwise is bytes under way: one row a lane in registers gave 4.5
+// TB/s.)  A piece that is not there is copied as zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy_piece(uint32_t dst, const void *src, bool live) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(live ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+template <typename T>
+constexpr int kPieces = 2 * sizeof(T) * 4;                    // bytes of a lane's four pairs
+// dst: this thread's slot; a float row's second piece is kQThr slots on.
+template <bool INTER>
+__device__ __forceinline__ void copy_pairs(uint32_t dst, const __nv_bfloat16 *row, const Place<4, INTER> &at, bool live) {
+  if constexpr (INTER) {
+    copy_piece<16>(dst, row + at.x, live);
+  } else {
+    copy_piece<8>(dst, row + at.x, live);
+    copy_piece<8>(dst + 8, row + at.y, live);
+  }
+}
+template <bool INTER>
+__device__ __forceinline__ void copy_pairs(uint32_t dst, const float *row, const Place<4, INTER> &at, bool live) {
+  copy_piece<16>(dst, row + at.x, live);
+  copy_piece<16>(dst + 16 * kQThr, row + at.y, live);
+}
+template <bool INTER>
+__device__ __forceinline__ void take_pairs(Pairs<__nv_bfloat16, 4, INTER> &p, const unsigned char *slot) {
+  const uint4 u = *reinterpret_cast<const uint4 *>(slot);
+  p.x = make_uint2(u.x, u.y), p.y = make_uint2(u.z, u.w);
+}
+template <bool INTER>
+__device__ __forceinline__ void take_pairs(Pairs<float, 4, INTER> &p, const unsigned char *slot) {
+  p.x = *reinterpret_cast<const float4 *>(slot);
+  p.y = *reinterpret_cast<const float4 *>(slot + 16 * kQThr);
+}
+// Stages of such a ring.  4 x 2048 tokens, 20 + 20 heads of 128 bf16, us: forward
+// with rows in registers 32.6, with rings of 2, 3, 4 stages 33.1, 28.4, 29.3;
+// backward 56.5 with registers and 3 blocks an SM, 50.7 with 3 stages and 3
+// blocks, 51.1, 48.2, 48.2 with 3, 4, 6 stages and 2 blocks.
+constexpr int kFwdStages = 3, kBwdStages = 4;
+// Rows that a group of lanes has to have for the ring to pay: with five it costs
+// a microsecond (2050 tokens, 20 + 5 heads of 80 fp32: 8.8 us, with it 10.0).
+constexpr int kRingRows = 8;
+
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
@@ -297,10 +349,10 @@ struct Side {
 // L lanes takes every slots-th head of one token, so that the token's angles
 // stay in its registers, multiplied by gamma once for all its heads.  U rows at
 // a time; the next ones are loaded while these are at work.
-// 4 x 2048 tokens, 40 heads of 128 bf16 (167 MB): 33 us, 5.1 TB/s; it is bound by
-// instruction issue before it is by memory, so what counts is instructions per
+// 4 x 2048 tokens, 40 heads of 128 bf16 (167 MB): 28 us, 5.9 TB/s; it is bound by
+// instruction issue nearly as much as by memory, so what counts is instructions per
 // row (with rows dealt out one by one 196 a lane, 38 us).
-template <typename XT, bool INTER, int V, int N, int L, int U>
+template <typename XT, bool INTER, int V, int N, int L, int U, bool RING>
 __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? 3 : 1)
     qk_fwd_kernel(const __grid_constant__ QkTable<table_size<V, L>()> p) {
   __shared__ unsigned long long turns[table_size<V, L>()];
@@ -312,24 +364,38 @@ __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? 3 : 1)
   const long long tok = static_cast<long long>(sd.block) * (kGroups / slots) + grp / slots;
   const bool norm = sd.gamma != nullptr;
   const int H = tok < p.ntok ? sd.H : 0;                      // heads of this group's token
-  const XT *x = static_cast<const XT *>(sd.w ? p.x[1] : p.x[0]) + tok * sd.xs;
+  const XT *x0 = static_cast<const XT *>(sd.w ? p.x[1] : p.x[0]), *x = x0 + tok * sd.xs;
   XT *o = static_cast<XT *>(sd.w ? p.out[1] : p.out[0]) + tok * sd.os;
   const int hop = slots * p.D;
+    extern __shared__ __align__(16) unsigned char ring[];
   Pairs<XT, V, INTER> raw[U][N];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int k = 0; k < N; ++k) raw[u][k].clear();            // what is not loaded adds nothing to a row's sum
-  auto fetch = [&](int h, int off) {
+  auto fetch = [&](int h, int off, int stage) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         const int s = (lane + L * k) * V;
-        if (h + u * slots < H && s < h2) raw[u][k].load(x + (off + u * hop), Place<V, INTER>(s, p.rot));
+        const bool live = h + u * slots < H && s < h2;
+        const Place<V, INTER> at(s, p.rot);
+        if constexpr (RING)
+          copy_pairs(smem_u32(ring) + (stage * U * N + u * N + k) * (kPieces<XT> * kQThr) + threadIdx.x * 16,
+                     live ? x + (off + u * hop) : x0, at, live);
+        else if (live)
+          raw[u][k].load(x + (off + u * hop), at);
       }
+    if constexpr (RING) copies_commit();
   };
-  fetch(slot, slot * p.D);
+  int fh = slot, foff = slot * p.D;
+  if constexpr (RING) {
+#pragma unroll
+    for (int d = 0; d < kFwdStages - 1; ++d, fh += U * slots, foff += U * hop) fetch(fh, foff, d);
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < N; ++k) raw[u][k].clear();          // what is not loaded adds nothing to a row's sum
+    fetch(fh, foff, 0);
+  }
   load_turns(p, turns);
   // y_a = (a gamma_a cos - b gamma_b sin) / rms, y_b = (a gamma_a sin + b gamma_b cos) / rms
   F ac[N][C], bs[N][C], as[N][C], bc[N][C];
@@ -350,14 +416,29 @@ __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? 3 : 1)
   // every lane of a warp makes the same number of steps: the row sums exchange
   // values across it
   const int steps = (sd.H + slots - 1) / slots;
-  int h = slot, off = slot * p.D;
+  int h = slot, off = slot * p.D, stage = 0;
   for (int i = 0; i < steps; i += U, h += U * slots, off += U * hop) {
     F a[U][N][C], b[U][N][C];
+    if constexpr (RING) {
+      copies_wait<kFwdStages - 2>();
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          take_pairs(raw[u][k], ring + (stage * U * N + u * N + k) * (kPieces<XT> * kQThr) + threadIdx.x * 16);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int k = 0; k < N; ++k) raw[u][k].get(a[u][k], b[u][k]);
-    fetch(h + U * slots, off + U * hop);
+    if constexpr (RING) {
+      // into the stage that the last step took its rows from
+      fetch(fh, foff, stage == 0 ? kFwdStages - 1 : stage - 1);
+      fh += U * slots, foff += U * hop;
+      if (++stage == kFwdStages) stage = 0;
+    } else {
+      fetch(h + U * slots, off + U * hop, 0);
+    }
     float inv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -390,20 +471,20 @@ __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? 3 : 1)
       }
     }
   }
+  if constexpr (RING) copies_wait<0>();
 }
 
 // Backward, laid out as the forward; the groups of a block go on to further
-// tokens and keep their lanes' dgamma in registers.  The next row of a group is
-// loaded while this one is at work.  Registers are held to what lets
-// bwd_blocks blocks be resident.  4 x 2048 tokens, 20 + 20 heads of 128 bf16, dy
-// bf16 (252 MB): 57 us with dgamma, bound by instruction issue.
-template <typename XT, typename DT, bool INTER>
-constexpr int bwd_blocks() { return sizeof(XT) + sizeof(DT) == 4 && !INTER ? 4 : 3; }
+// tokens and keep their lanes' dgamma in registers.  Registers are held to what
+// lets bwd_blocks blocks be resident.  4 x 2048 tokens, 20 + 20 heads of 128
+// bf16, dy bf16 (252 MB): 48 us with dgamma, 5.2 TB/s.
+constexpr int bwd_blocks(bool ring) { return ring ? 2 : 3; }
 
-template <typename XT, typename DT, bool INTER, int V, int N, int L>
-__global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? bwd_blocks<XT, DT, INTER>() : 1)
+template <typename XT, typename DT, bool INTER, int V, int N, int L, bool RING>
+__global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? bwd_blocks(RING) : 1)
     qk_bwd_kernel(const __grid_constant__ QkTable<table_size<V, L>()> p) {
-  extern __shared__ __align__(16) float sums[];               // [kGroups][D], at the end
+  extern __shared__ __align__(16) unsigned char ring[];
+  float *sums = reinterpret_cast<float *>(ring);              // [kGroups][D], at the end
   __shared__ unsigned long long turns[table_size<V, L>()];
   using F = typename Num<V>::F;
   constexpr int kGroups = kQThr / L, C = Num<V>::kC;
@@ -417,6 +498,7 @@ __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? bwd_blocks<XT, DT, I
   load_turns(p, turns);
   F ga[N][C], gb[N][C], dga[N][C], dgb[N][C];                 // of this lane's components
   lane_gamma<V, N, L, INTER>(sd.gamma, lane, p.rot, h2, ga, gb);
+  constexpr int kRow = kPieces<XT> + kPieces<DT>;
   Pairs<XT, V, INTER> rx[N];
   Pairs<DT, V, INTER> rd[N];
 #pragma unroll
@@ -424,28 +506,54 @@ __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? bwd_blocks<XT, DT, I
 #pragma unroll
     for (int e = 0; e < C; ++e) dga[k][e] = dgb[k][e] = f_all<F>(0.f);
   }
-  for (long long tok0 = static_cast<long long>(sd.block) * per; tok0 < p.ntok;
-       tok0 += static_cast<long long>(sd.nblocks) * per) {
+  // the row to fetch next: the groups' rows of one token after the other
+  const XT *x0 = static_cast<const XT *>(sd.w ? p.x[1] : p.x[0]);
+  const DT *d0 = static_cast<const DT *>(sd.w ? p.dy[1] : p.dy[0]);
+  const long long stride = static_cast<long long>(sd.nblocks) * per;
+  long long ftok = static_cast<long long>(sd.block) * per + grp / slots;
+  const XT *fx = x0 + ftok * sd.xs;
+  const DT *fd = d0 + ftok * sd.H * p.D;
+  int fi = 0, fh = slot, foff = slot * p.D;
+  auto fetch = [&](int stage) {
+    const bool in = ftok < p.ntok && fh < sd.H;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int s = (lane + L * k) * V;
+      const bool live = in && s < h2;
+      const Place<V, INTER> at(s, p.rot);
+      if constexpr (RING) {
+        const uint32_t dst = smem_u32(ring) + (stage * N + k) * (kRow * kQThr) + threadIdx.x * 16;
+        copy_pairs(dst, live ? fx + foff : x0, at, live);
+        copy_pairs(dst + kPieces<XT> * kQThr, live ? fd + foff : d0, at, live);
+      } else if (live) {
+        rx[k].load(fx + foff, at);
+        rd[k].load(fd + foff, at);
+      } else {                                                // (adds nothing to sums and dgamma)
+        rx[k].clear();
+        rd[k].clear();
+      }
+    }
+    if constexpr (RING) copies_commit();
+    fh += slots, foff += hop;
+    if (++fi == steps) {
+      fi = 0, fh = slot, foff = slot * p.D;
+      ftok += stride;
+      fx += stride * sd.xs;
+      fd += stride * sd.H * p.D;
+    }
+  };
+  int stage = 0;
+  if constexpr (RING) {
+#pragma unroll
+    for (int d = 0; d < kBwdStages - 1; ++d) fetch(d);
+  } else {
+    fetch(0);
+  }
+  for (long long tok0 = static_cast<long long>(sd.block) * per; tok0 < p.ntok; tok0 += stride) {
     const long long tok = tok0 + grp / slots;
     const int H = tok < p.ntok ? sd.H : 0;                    // heads of this group's token
-    const XT *x = static_cast<const XT *>(sd.w ? p.x[1] : p.x[0]) + tok * sd.xs;
-    const DT *d = static_cast<const DT *>(sd.w ? p.dy[1] : p.dy[0]) + tok * sd.H * p.D;
     XT *o = static_cast<XT *>(sd.w ? p.out[1] : p.out[0]) + tok * sd.os;
     int h = slot, off = slot * p.D;
-    auto fetch = [&](int h, int off) {
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int s = (lane + L * k) * V;
-        if (h < H && s < h2) {
-          rx[k].load(x + off, Place<V, INTER>(s, p.rot));
-          rd[k].load(d + off, Place<V, INTER>(s, p.rot));
-        } else {                                              // (adds nothing to sums and dgamma)
-          rx[k].clear();
-          rd[k].clear();
-        }
-      }
-    };
-    fetch(h, off);
     F c[N][C], z[N][C];
     if (H) {
       lane_angles<V, N, L>(p, turns, tok, lane, c, z);
@@ -460,6 +568,15 @@ __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? bwd_blocks<XT, DT, I
     for (int i = 0; i < steps; ++i, h += slots, off += hop) {
       F a[N][C], b[N][C], u[N][C], v[N][C];
       F ss = f_all<F>(0.f), cc = f_all<F>(0.f);
+      if constexpr (RING) {
+        copies_wait<kBwdStages - 2>();
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const unsigned char *src = ring + (stage * N + k) * (kRow * kQThr) + threadIdx.x * 16;
+          take_pairs(rx[k], src);
+          take_pairs(rd[k], src + kPieces<XT> * kQThr);
+        }
+      }
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         F da[C], db[C];
@@ -472,7 +589,13 @@ __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? bwd_blocks<XT, DT, I
           v[k][e] = f_fma(db[e], c[k][e], f_mul(f_mul(da[e], f_all<F>(-1.f)), z[k][e]));
         }
       }
-      fetch(h + slots, off + hop);
+      if constexpr (RING) {
+        // into the stage that the last step took its row from
+        fetch(stage == 0 ? kBwdStages - 1 : stage - 1);
+        if (++stage == kBwdStages) stage = 0;
+      } else {
+        fetch(0);
+      }
       float inv = 1.f, coef = 0.f;
       if (norm) {
 #pragma unroll
@@ -509,7 +632,9 @@ __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? bwd_blocks<XT, DT, I
     }
   }
   // one partial dgamma per block, its row groups added in a fixed order
+  if constexpr (RING) copies_wait<0>();
   if (p.part == nullptr) return;
+  __syncthreads();
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int s = (lane + L * k) * V;
@@ -568,9 +693,18 @@ cudaError_t qk_launch(QkParams &p, const unsigned long long *freq, int sms, cuda
     const int per = kGroups / slots;
     blocks[w] = p.H[w] ? (p.ntok + per - 1) / per : 0;
   }
+  // rows of a group of lanes: its token's heads, and in the backward those of
+  // the tokens that it goes on to
+  const int w0 = p.H[0] ? 0 : 1;
+  long long rows = (p.H[w0] + p.slots[w0] - 1) / p.slots[w0];
+  if (BWD) {
+    const long long most = bwd_blocks(false) * static_cast<long long>(sms);
+    if (blocks[0] + blocks[1] > most) rows *= (blocks[0] + blocks[1]) / most;
+  }
+  const bool ring = V == 4 && rows >= kRingRows;
   if (BWD) {
     // resident blocks, shared out by the number of heads
-    const long long all = (V == 4 && N == 1 ? bwd_blocks<XT, DT, INTER>() : 2) * static_cast<long long>(sms);
+    const long long all = (V == 4 && N == 1 ? bwd_blocks(ring) : 2) * static_cast<long long>(sms);
     const long long most = all < kQkParts ? all : kQkParts;
     long long q = most * p.H[0] / (p.H[0] + p.H[1]);
     if (p.H[0] && q < 1) q = 1;
@@ -585,8 +719,14 @@ cudaError_t qk_launch(QkParams &p, const unsigned long long *freq, int sms, cuda
   for (int i = 0; i < p.rot; ++i) t.freq[i] = freq[i];
   const unsigned grid = static_cast<unsigned>(blocks[0] + blocks[1]);
   if constexpr (BWD) {
-    const size_t smem = p.part ? static_cast<size_t>(kGroups) * p.D * 4 : 0;
-    qk_bwd_kernel<XT, DT, INTER, V, N, L><<<grid, kQThr, smem, st>>>(t);
+    const auto kern = ring ? qk_bwd_kernel<XT, DT, INTER, V, N, L, V == 4> : qk_bwd_kernel<XT, DT, INTER, V, N, L, false>;
+    const int need = p.part ? kGroups * p.D * 4 : 0, rb = ring ? kBwdStages * N * (kPieces<XT> + kPieces<DT>) * kQThr : 0;
+    const int smem = need > rb ? need : rb;
+    if (smem > 40960) {
+      const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem);
+      if (e != cudaSuccess) return e;
+    }
+    kern<<<grid, kQThr, smem, st>>>(t);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.part) return e;
     cudaLaunchConfig_t cfg = {};
@@ -602,7 +742,13 @@ cudaError_t qk_launch(QkParams &p, const unsigned long long *freq, int sms, cuda
                               p.first_k, static_cast<int>(grid), p.D);
   } else {
     constexpr int U = V == 1 || N > 1 ? 1 : 2;
-    qk_fwd_kernel<XT, INTER, V, N, L, U><<<grid, kQThr, 0, st>>>(t);
+    const auto kern = ring ? qk_fwd_kernel<XT, INTER, V, N, L, U, V == 4> : qk_fwd_kernel<XT, INTER, V, N, L, U, false>;
+    const int smem = ring ? kFwdStages * U * N * kPieces<XT> * kQThr : 0;
+    if (smem > 40960) {
+      const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(kern), smem);
+      if (e != cudaSuccess) return e;
+    }
+    kern<<<grid, kQThr, smem, st>>>(t);
   }
   return cudaGetLastError();
 }
