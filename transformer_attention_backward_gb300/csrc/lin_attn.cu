@@ -515,7 +515,9 @@ __device__ __noinline__ LinItem lin_item(const LinOutParams &p, int i) {
   return it;
 }
 
-// The output kernels start as programmatic dependents of lin_state.
+// The output kernels start as programmatic dependents of lin_state: set up and
+// with their first loads under way while it ends.  Nobody else starts before,
+// so that no bounded wait runs while lin_state does.
 __device__ __forceinline__ void wait_states() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The row and column powers of the weights scale a^(distance) of a score tile.
@@ -645,11 +647,12 @@ __global__ void __launch_bounds__(kOThr, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kOOffTmem);
 
+  if (warp != 0) wait_states();
   if (warp == 0) {
     // ============================ TMA producer ============================
     if (lane == 0) {
       int q = 0, item = 0;
-      bool ok = true, states = false;                         // states: they are there
+      bool ok = true, states = false;
       auto slot = [&](uint32_t bytes) -> bool {       // claims the next slot
         const int s = q % kOSlots;
         if (!wt(bar(kOBarEmpty + s), phase(q) ^ 1u)) return ok = false;
@@ -681,10 +684,10 @@ __global__ void __launch_bounds__(kOThr, 1)
         for (int g = 0; g < it.gi; ++g) {
           const int n = it.role < 2 ? it.n - far : it.n + far;
           tile(mb, it, hg, n);
+          if (!states) wait_states();
+          states = true;
           if (g == 0 && it.st && ok && slot(D * D * 2)) {
             const int s = (q - 1) % kOSlots;
-            if (!states) wait_states();
-            states = true;
             const __nv_bfloat16 *src = p.tiles[it.role >> 1] +
                                        (static_cast<size_t>(it.b * p.z.Hkv + it.kv) * p.z.NC + it.n) * (D * D);
             bulk_load(sb + s * kOSlot, src, D * D * 2, bar(kOBarFull + s));
@@ -693,7 +696,7 @@ __global__ void __launch_bounds__(kOThr, 1)
           if (++far == it.ns) far = 0, ++hg;
         }
       }
-      if (!states) wait_states();                             // nor does this grid end before
+      if (!states) wait_states();                             // nor does this grid end before it
       if (*abort_flag) {
         for (int x = (q > kOSlots ? q - kOSlots : 0); x < q; ++x)
           mbar_wait_bounded(bar(kOBarFull + x % kOSlots), phase(x), 2000000000ull);
@@ -950,6 +953,7 @@ __global__ void __launch_bounds__(kGThr, 1)
   tc::fence_after_sync();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kOOffBar + kGNumBars * 8);
 
+  if (warp != 0) wait_states();
   if (warp == 0) {
     // ============================ TMA producer ============================
     if (lane == 0) {
@@ -963,6 +967,10 @@ __global__ void __launch_bounds__(kGThr, 1)
 #pragma unroll 1
         for (int e = 0; e < 6; ++e) {
           const int tile = tile_at(e), s = slot(tile, item);
+          if (tile == kGS && !states) {
+            wait_states();
+            states = true;
+          }
           const uint32_t fb = bar(kGBarFull + s), dst = sb + s * kOSlot;
           if (!wt(bar(kGBarEmpty + s), phase(tile, item) ^ 1u)) {
             ok = false;
@@ -970,8 +978,6 @@ __global__ void __launch_bounds__(kGThr, 1)
           }
           if (tile == kGS || tile == kGR) {
             if (tile == kGS ? has_s(it) : has_r(it)) {
-              if (!states) wait_states();
-              states = true;
               mbar_arrive_expect_tx(fb, D * D * 2);
               bulk_load(dst, p.tiles[tile == kGR] + (static_cast<size_t>(it.b * p.z.Hkv + it.kv) * p.z.NC + it.n) * (D * D),
                         D * D * 2, fb);
