@@ -606,7 +606,9 @@ __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? bwd_blocks(RING) : 1
             cc = f_fma(f_mul(u[k][e], ga[k][e]), a[k][e], f_fma(f_mul(v[k][e], gb[k][e]), b[k][e], cc));
           }
         const float s2 = lanes_sum<L>(f_sum(ss)), c2 = lanes_sum<L>(f_sum(cc));
-        inv = inv_root(fmaf(s2, p.inv_n, p.eps));
+        // held finite: where eps is 0, a group without a row (zeros) would
+        // otherwise carry 0 * NaN into dgamma (fminf drops the NaN)
+        inv = fminf(inv_root(fmaf(s2, p.inv_n, p.eps)), 3.4028234663852886e38f);
         coef = -c2 * p.inv_n * (inv * inv);                   // -c / (D rms^2)
 #pragma unroll
         for (int k = 0; k < N; ++k)
