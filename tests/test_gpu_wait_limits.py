@@ -1,0 +1,84 @@
+"""What the tensor-core kernels do when a wait runs out: they say so, let their
+copies land, and leave the device as it was, so that the next call is right.
+Sizes whose loads all fit the rings (the loading role is through with its
+loop before any other role gives up), and larger ones."""
+import contextlib
+
+import pytest
+import torch
+
+from transformer_attention_backward_gb300 import _binding as B
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def abw():
+    import transformer_attention_backward_gb300 as m
+    m.library()
+    return m
+
+
+@contextlib.contextmanager
+def no_waiting(lib):
+    lib.abw_set_wait_limit_ns(0)
+    try:
+        yield
+    finally:
+        lib.abw_set_wait_limit_ns(2_000_000_000)
+
+
+def linear(abw, T, Hq, Hkv, D, state, backward, seed=0):
+    """One call of the linear attention, as a function without arguments."""
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g)
+    q, k, v, do = (n(2, T, h, D).to(BF).cuda() for h in (Hq, Hkv, Hkv, Hq))
+    ld = -(2.0 ** -(1.0 + torch.arange(Hkv))).cuda()
+    s0, df = (n(2, Hkv, D, D).cuda(), n(2, Hkv, D, D).cuda()) if state else (None, None)
+    if backward:
+        return lambda: [x for x in abw.lin_attn_bwd(q, k, v, do, ld, 0.125, initial_state=s0, dfinal_state=df,
+                                                    want_dinitial_state=state) if x is not None]
+    return lambda: [x for x in abw.lin_attn_fwd(q, k, v, ld, 0.125, initial_state=s0, want_final_state=state) if x is not None]
+
+
+def softmax(abw, T, Hq, Hkv, backward):
+    """One call of the causal softmax attention."""
+    g = torch.Generator().manual_seed(T)
+    q, k, v, do = (torch.randn(2, T, h, 128, generator=g).to(BF).cuda() for h in (Hq, Hkv, Hkv, Hq))
+    o, lse = abw.attn_fwd_causal(q, k, v)
+    if backward:
+        return lambda: list(abw.attn_bwd_causal(q, k, v, o, do, lse, rope_base=1e4))
+    return lambda: list(abw.attn_fwd_causal(q, k, v))
+
+
+def same(got, want):
+    """Equal bits; the softmax backward's key blocks that several blocks share
+    add their parts in any order: up to four of them, so a few roundings of
+    the largest."""
+    return all(torch.equal(a, b) or (a.dtype == torch.float32 and bool((a - b).abs().max() <= 4 * 2.0 ** -24 * b.abs().max()))
+               for a, b in zip(got, want))
+
+
+CALLS = [pytest.param(lambda m, a=a: linear(m, *a), id="lin-T%d-%d/%d-D%d-state%d-bwd%d" % a) for a in [
+    (100, 4, 2, 128, False, False), (100, 4, 2, 64, True, False), (300, 4, 2, 128, False, True), (128, 4, 4, 128, True, True),
+    (128, 2, 2, 64, True, True), (700, 4, 1, 128, True, True), (1500, 8, 8, 64, True, True), (900, 40, 40, 128, False, True)]]
+CALLS += [pytest.param(lambda m, a=a: softmax(m, *a), id="softmax-T%d-%d/%d-bwd%d" % a) for a in [
+    (100, 4, 2, False), (128, 4, 4, True), (1000, 4, 2, False), (1000, 8, 2, True)]]
+
+
+@pytest.mark.parametrize("make", CALLS)
+def test_next_call_is_right(abw, make):
+    call, lib = make(abw), abw.library()
+    want = [x.clone() for x in call()]
+    abw.device_check()
+    for _ in range(3):
+        with no_waiting(lib):
+            got = call()
+            status = lib.abw_device_check(torch.cuda.current_stream().cuda_stream)
+        assert status in (B.OK, B.ETIMEOUT)
+        if status == B.OK:
+            assert same(got, want)
+        got = call()
+        abw.device_check()
+        assert same(got, want)

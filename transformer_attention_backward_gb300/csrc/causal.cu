@@ -461,7 +461,6 @@ __global__ void __launch_bounds__(kThr, 1)
     // ============================ TMA producer ============================
     if (lane == 0) {
       // K, Q(0), V and dO(0) are already on their way (issued with the barriers)
-      const bool v_issued = true;
       int q_issued = 1, d_issued = 1;
       for (int n = 0; n < N; ++n) {
         const int h = h_first + n / nq;
@@ -485,15 +484,14 @@ __global__ void __launch_bounds__(kThr, 1)
           d_issued = n + 1;
         }
       }
-      if (*abort_flag) {
-        // let copies already in flight land before the CTA can exit
-        for (int n = (q_issued > kQStagesKv ? q_issued - kQStagesKv : 0); n < q_issued; ++n)
-          mbar_wait_bounded(bar(kBarQFull + n % kQStagesKv), (n / kQStagesKv) & 1, 2000000000ull);
-        for (int n = (d_issued > kDOStages ? d_issued - kDOStages : 0); n < d_issued; ++n)
-          mbar_wait_bounded(bar(kBarDOFull + n % kDOStages), (n / kDOStages) & 1, 2000000000ull);
-        mbar_wait_bounded(bar(kBarKV), 0, 2000000000ull);
-        if (v_issued) mbar_wait_bounded(bar(kBarV), 0, 2000000000ull);
-      }
+      // The last load of every slot has landed before the CTA can exit, whoever
+      // gives up and when (otherwise this finds every phase complete).
+      for (int n = (q_issued > kQStagesKv ? q_issued - kQStagesKv : 0); n < q_issued; ++n)
+        mbar_wait_bounded(bar(kBarQFull + n % kQStagesKv), (n / kQStagesKv) & 1, 2000000000ull);
+      for (int n = (d_issued > kDOStages ? d_issued - kDOStages : 0); n < d_issued; ++n)
+        mbar_wait_bounded(bar(kBarDOFull + n % kDOStages), (n / kDOStages) & 1, 2000000000ull);
+      mbar_wait_bounded(bar(kBarKV), 0, 2000000000ull);
+      mbar_wait_bounded(bar(kBarV), 0, 2000000000ull);
     }
   } else if (warp == 1) {
     // ============================ MMA issuer ==============================
@@ -934,11 +932,10 @@ __global__ void __launch_bounds__(kThr, 1)
                          fb, stream);
         }
       }
-      if (!ok) {
-        // let copies already in flight land before the CTA can exit
-        for (int i = (g > kQStages ? g - kQStages : 0); i < g; ++i)
-          mbar_wait_bounded(bar(kQBarFull + i % kQStages), (i / kQStages) & 1, 2000000000ull);
-      }
+      // the last load of every stage has landed before the CTA can exit, whoever
+      // gives up and when (otherwise this finds every phase complete)
+      for (int i = (g > kQStages ? g - kQStages : 0); i < g; ++i)
+        mbar_wait_bounded(bar(kQBarFull + i % kQStages), (i / kQStages) & 1, 2000000000ull);
     }
   } else if (warp == 1) {
     // ============================ MMA issuer ==============================

@@ -156,11 +156,11 @@ __global__ void __launch_bounds__(kFThr, 1)
         }
         issued = n + 1;
       }
-      if (*abort_flag) {
-        for (int n = (issued > kFStages ? issued - kFStages : 0); n < issued; ++n)
-          mbar_wait_bounded(bar(kFBarKVFull + n % kFStages), (n / kFStages) & 1, 2000000000ull);
-        mbar_wait_bounded(bar(kFBarQ), 0, 2000000000ull);
-      }
+      // The last load of every stage has landed before the block may end, whoever
+      // gives up and when (otherwise this finds every phase complete).
+      for (int n = (issued > kFStages ? issued - kFStages : 0); n < issued; ++n)
+        mbar_wait_bounded(bar(kFBarKVFull + n % kFStages), (n / kFStages) & 1, 2000000000ull);
+      mbar_wait_bounded(bar(kFBarQ), 0, 2000000000ull);
     }
   } else if (warp == 1) {
     // ============================ MMA issuer ==============================
@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(kFThr, 1)
       tc::fence_before_sync();
       mbar_arrive(bar(kFBarPFull + (n & 1)));
     }
+    if (!ok) tc::wait_st();                            // P on its way when this warp gave up
     // ---- epilogue: O / l as bf16 rows, lse = (m + log2 l) ln 2
     if (ok && wtw(bar(kFBarO), (N - 1) & 1)) {
       tc::fence_after_sync();

@@ -232,9 +232,10 @@ __global__ void __launch_bounds__(kSThr, 1)
         if (++g == gi) g = 0, ++m;
         if (++s == Z::kRing) s = 0, ph ^= 1;
       }
-      if (*abort_flag)
-        for (int i = (issued > Z::kRing ? issued - Z::kRing : 0); i < issued; ++i)
-          mbar_wait_bounded(bar(Z::kFull + i % Z::kRing), phase(i), 2000000000ull);
+      // The last load of every slot has landed before the block may end, whoever
+      // gives up and when (otherwise this finds every phase complete).
+      for (int i = (issued > Z::kRing ? issued - Z::kRing : 0); i < issued; ++i)
+        mbar_wait_bounded(bar(Z::kFull + i % Z::kRing), phase(i), 2000000000ull);
     }
   } else if (warp == 1 || warp == kSMma2) {
     // ============================ MMA issuers =============================
@@ -697,12 +698,11 @@ __global__ void __launch_bounds__(kOThr, 1)
         }
       }
       if (!states) wait_states();                             // nor does this grid end before it
-      if (*abort_flag) {
-        for (int x = (q > kOSlots ? q - kOSlots : 0); x < q; ++x)
-          mbar_wait_bounded(bar(kOBarFull + x % kOSlots), phase(x), 2000000000ull);
-        for (int x = (item > 2 ? item - 2 : 0); x < item; ++x)
-          mbar_wait_bounded(bar(kOBarAFull + (x & 1)), (x >> 1) & 1, 2000000000ull);
-      }
+      // the last load of every slot, before the block may end (as in lin_state)
+      for (int x = (q > kOSlots ? q - kOSlots : 0); x < q; ++x)
+        mbar_wait_bounded(bar(kOBarFull + x % kOSlots), phase(x), 2000000000ull);
+      for (int x = (item > 2 ? item - 2 : 0); x < item; ++x)
+        mbar_wait_bounded(bar(kOBarAFull + (x & 1)), (x >> 1) & 1, 2000000000ull);
     }
   } else if (warp == 1) {
     // ============================ MMA issuer ==============================
@@ -863,6 +863,7 @@ __global__ void __launch_bounds__(kOThr, 1)
       ss += it.gi;
       ++item;
     }
+    tc::wait_st();                                            // scores on their way when this warp gave up
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -995,9 +996,14 @@ __global__ void __launch_bounds__(kGThr, 1)
         if (ok) ++item;
       }
       if (!states) wait_states();
-      if (*abort_flag)                                        // the last load of every slot
-        for (int x = (loads > 12 ? loads - 12 : 0); x < loads; ++x)
-          mbar_wait_bounded(bar(kGBarFull + slot(tile_at(x % 6), x / 6)), phase(tile_at(x % 6), x / 6), 2000000000ull);
+      // the last load of every slot, before the block may end (as in lin_state);
+      // an older phase of a slot would pass for one that is still to come
+#pragma unroll 1
+      for (int e = 0; e < 6; ++e) {
+        const int tile = tile_at(e), n = loads / 6 + (e < loads % 6 ? 1 : 0);   // loads of this tile
+        for (int x = max(n - (tile == kGDO ? 2 : 1), 0); x < n; ++x)
+          mbar_wait_bounded(bar(kGBarFull + slot(tile, x)), phase(tile, x), 2000000000ull);
+      }
     }
   } else if (warp == 1) {
     // ============================ MMA issuer ==============================
@@ -1168,6 +1174,7 @@ __global__ void __launch_bounds__(kGThr, 1)
       }
       ++item;
     }
+    tc::wait_st();                                            // scores on their way when this warp gave up
   }
   tc::fence_before_sync();
   __syncthreads();
