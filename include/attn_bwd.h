@@ -98,7 +98,8 @@ int abw_version(void);
 abw_status abw_device_check(abw_stream stream);
 
 /* Sets the time limit, in nanoseconds, of every device-side wait of the
- * library's kernels (default 2e9, i.e. 2 s).  For tests. */
+ * library's kernels (default 2e9, i.e. 2 s).  For tests.  With 0 the
+ * tensor-core kernels of both attentions give up at their first product. */
 void abw_set_wait_limit_ns(unsigned long long ns);
 
 /* Launches one block that waits, with the library's bounded wait, on a

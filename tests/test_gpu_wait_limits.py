@@ -82,3 +82,41 @@ def test_next_call_is_right(abw, make):
         got = call()
         abw.device_check()
         assert same(got, want)
+
+
+def one_chunk(abw, Hq, Hkv):
+    """Gradients of one chunk from a given state: the walk only hands it on."""
+    g = torch.Generator().manual_seed(Hq)
+    q, k, v, do = (torch.randn(2, 100, h, 128, generator=g).to(BF).cuda() for h in (Hq, Hkv, Hkv, Hq))
+    s0, ld = torch.randn(2, Hkv, 128, 128, generator=g).cuda(), torch.full((Hkv,), -0.1, device="cuda")
+    return lambda: list(abw.lin_attn_bwd(q, k, v, do, ld, 0.125, initial_state=s0)[:3])
+
+
+KERNELS = [("linear attention output", lambda m: linear(m, 100, 4, 2, 128, False, False)),
+           ("linear attention output", lambda m: linear(m, 500, 4, 2, 64, False, True)),
+           ("linear attention output", lambda m: one_chunk(m, 4, 2)),
+           ("linear attention state", lambda m: linear(m, 100, 4, 2, 64, True, False)),
+           ("linear attention state", lambda m: linear(m, 3000, 4, 4, 128, True, True)),
+           ("linear attention", lambda m: one_chunk(m, 4, 4)),                  # its gradient kernel
+           ("causal forward", lambda m: softmax(m, 128, 4, 2, False)),
+           ("causal forward", lambda m: softmax(m, 2000, 4, 2, False)),
+           ("causal kv", lambda m: softmax(m, 128, 4, 2, True)),
+           ("causal kv", lambda m: softmax(m, 2000, 4, 2, True))]
+
+
+@pytest.mark.parametrize("kernel,make", KERNELS, ids=lambda x: x.replace(" ", "_") if isinstance(x, str) else "")
+def test_gives_up_and_says_where(abw, kernel, make):
+    """A limit of 0 is over before any wait: every such call reports it, and
+    names the kernel that came first."""
+    call, lib = make(abw), abw.library()
+    want = [x.clone() for x in call()]
+    abw.device_check()
+    for _ in range(20):
+        with no_waiting(lib):
+            call()
+            status = lib.abw_device_check(torch.cuda.current_stream().cuda_stream)
+        assert status == B.ETIMEOUT
+        assert f"first in the {kernel}" in B.last_error(), B.last_error()
+        got = call()
+        abw.device_check()
+        assert same(got, want)

@@ -35,6 +35,16 @@ static __device__ __noinline__ void report_timeout(unsigned int *err, unsigned i
   atomicOr(err, kErrWaitTimeout);
   atomicCAS(err + 1, 0u, wait_site(kernel, slot));
 }
+// False with a limit of 0: the warps that issue a kernel's products then report
+// their first wait as run out without a look at it.  So tests have a kernel give
+// up at a known place, with its loads under way.
+__device__ __forceinline__ bool may_wait(const WaitCtl &w, volatile int *abort_flag, unsigned int kernel,
+                                         unsigned int slot) {
+  if (w.limit_ns != 0) return true;
+  *abort_flag = 1;
+  report_timeout(w.err, kernel, slot);
+  return false;
+}
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

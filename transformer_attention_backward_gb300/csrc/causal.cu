@@ -515,7 +515,8 @@ __global__ void __launch_bounds__(kThr, 1)
       const uint64_t dOk = tc::sdesc_sw128(sb + kOffDO, 16, 1024);         // dO as K-major B of dP^T
       const uint64_t dQm = tc::sdesc_sw128(sb + kOffQ, kHalfQ, 1024);      // Q as MN-major B of dK
       const uint64_t dOm = tc::sdesc_sw128(sb + kOffDO, kHalfQ, 1024);     // dO as MN-major B of dV
-      bool ok = wtw(bar(kBarKV), 0);   // K (V is waited for before the first dP product)
+      // K (V is waited for before the first dP product)
+      bool ok = may_wait(p.wait, abort_flag, kSiteKv, kBarKV) && wtw(bar(kBarKV), 0);
       tc::fence_after_sync();
       auto qoff = [](int n) -> uint64_t { return static_cast<uint64_t>((n % kQStagesKv) * kBlockBytes) >> 4; };
       auto dooff = [](int n) -> uint64_t { return static_cast<uint64_t>((n % kDOStages) * kBlockBytes) >> 4; };
@@ -946,7 +947,7 @@ __global__ void __launch_bounds__(kThr, 1)
       const uint64_t dKt = tc::sdesc_sw128(sb, 16384, 1024);                  // K^T, MN-major A
       const uint64_t dSt = tc::sdesc_sw128(sb + kQOffDS, kTileBytes, 1024);   // dS^T, MN-major B
       int g = 0, j = 0;
-      bool ok = true;
+      bool ok = may_wait(p.wait, abort_flag, kSiteDq, kQBarFull);
       for (int r = 0, it = nth(0); ok && it < items; it = nth(++r), ++j) {
         const Item w = item(it);
         const int a = j & 1;

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kFThr, 1)
     const uint64_t dK = tc::sdesc_sw128(sb + kFOffKV, 16, 1024);
     const uint64_t dVm = tc::sdesc_sw128(sb + kFOffKV + 32768, 16384, 1024);
     auto kstep = [](int kk) -> uint32_t { return static_cast<uint32_t>((kk >> 2) * 16384 + (kk & 3) * 32) >> 4; };
-    bool ok = wtw(bar(kFBarQ), 0);
+    bool ok = may_wait(p.wait, abort_flag, kSiteFwd, kFBarQ) && wtw(bar(kFBarQ), 0);
     tc::fence_after_sync();
     // S(n) into buffer n & 1.  That buffer last held P(n - 2), read by
     // PV(n - 2), which was issued before (in-order execution).

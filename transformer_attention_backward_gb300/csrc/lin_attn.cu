@@ -85,6 +85,8 @@ struct LinWait {
   const WaitCtl &ctl;
 
   __device__ __forceinline__ uint32_t bar(int i) const { return bars + i * 8; }
+  // the MMA warps, before their first wait, which is on barrier i
+  __device__ __forceinline__ bool start(int i) const { return may_wait(ctl, abort_flag, kernel, i); }
   // one thread, or each lane for its own barrier
   __device__ __forceinline__ bool one(uint32_t br, uint32_t parity) const {
     return mbar_try_wait(br, parity) || lin_wait_slow(br, parity, bars, abort_flag, kernel, ctl.err, ctl.limit_ns);
@@ -248,7 +250,8 @@ __global__ void __launch_bounds__(kSThr, 1)
     const int u = warp == 1 ? 0 : 1;
     const uint64_t dX = tc::sdesc_sw128(sb, 8192, 1024);
     const uint64_t dW = tc::sdesc_sw128(sb + Z::kOffW, 8192, 1024);
-    for (int i = u, s = u, w = u, wph = 0, uph = 1; i < steps; i += 2, uph ^= 1) {
+    const bool ok = u >= steps || lw.start(Z::kW + u);
+    for (int i = u, s = u, w = u, wph = 0, uph = 1; ok && i < steps; i += 2, uph ^= 1) {
       // (weighted rows that are there were formed from a stage that is there)
       if (!wtw(bar(Z::kUEmpty + u), uph) || !wtw(bar(Z::kW + w), wph)) break;
       tc::fence_after_sync();
@@ -734,7 +737,7 @@ __global__ void __launch_bounds__(kOThr, 1)
         tc::commit_w(bar(kOBarEmpty + qb(g) % kOSlots));
         return true;
       };
-      ok = wtw(bar(kOBarAFull + as), (item >> 1) & 1) && scores(0);
+      ok = (item > 0 || lw.start(kOBarAFull)) && wtw(bar(kOBarAFull + as), (item >> 1) & 1) && scores(0);
       // the accumulators are free once the last item's rows have been read
       if (ok) ok = wtw(bar(kOBarOEmpty), (item & 1) ^ 1);
       if (ok && st) {
@@ -1038,7 +1041,7 @@ __global__ void __launch_bounds__(kGThr, 1)
     };
     LinItem it, nx;
     int i = blockIdx.x, item = 0, k = 0;
-    bool more = next(i, it), ok = !more || scores(0, 0, 0);
+    bool more = next(i, it), ok = !more || (lw.start(kGBarFull + kGDO) && scores(0, 0, 0));
     while (ok && more) {
       i += gridDim.x;
       more = next(i, nx);
