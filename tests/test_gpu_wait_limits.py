@@ -98,7 +98,7 @@ KERNELS = [("linear attention output", lambda m: linear(m, 100, 4, 2, 128, False
            ("linear attention output", lambda m: one_chunk(m, 4, 2)),
            ("linear attention state", lambda m: linear(m, 100, 4, 2, 64, True, False)),
            ("linear attention state", lambda m: linear(m, 3000, 4, 4, 128, True, True)),
-           ("linear attention", lambda m: one_chunk(m, 4, 4)),                  # its gradient kernel
+           ("linear attention gradient", lambda m: one_chunk(m, 4, 4)),
            ("causal forward", lambda m: softmax(m, 128, 4, 2, False)),
            ("causal forward", lambda m: softmax(m, 2000, 4, 2, False)),
            ("causal (kv|dq)", lambda m: softmax(m, 128, 4, 2, True)),          # dq's blocks start in kv's tail
@@ -121,3 +121,14 @@ def test_gives_up_and_says_where(abw, kernel, make):
         got = call()
         abw.device_check()
         assert same(got, want)
+
+
+def test_names_the_warp(abw):
+    """Blocks of up to 19 warps: the walk's products are issued by warps 1 and
+    18, and one of the two is the first to report."""
+    call, lib = linear(abw, 600, 8, 8, 128, True, False), abw.library()
+    for _ in range(40):
+        with no_waiting(lib):
+            call()
+            assert lib.abw_device_check(torch.cuda.current_stream().cuda_stream) == B.ETIMEOUT
+        assert re.search(r"warp (1|18), block", B.last_error()), B.last_error()

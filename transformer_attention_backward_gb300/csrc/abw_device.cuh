@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "wait_site.h"
+
 namespace abw {
 
 // Bits of the device error word.
@@ -23,11 +25,8 @@ struct WaitCtl {
   unsigned long long limit_ns;    // time limit of one wait
 };
 
-// Where a wait ran out, for the report: kernel (bits 28-31), barrier slot
-// (bits 20-27), warp (bits 16-19) and the low 16 bits of the block index.
-enum : unsigned int { kSiteKv = 1u, kSiteDq = 2u, kSiteFwd = 3u, kSiteDecode = 4u, kSiteLinState = 5u, kSiteLinOut = 6u };
 __device__ __forceinline__ unsigned int wait_site(unsigned int kernel, unsigned int slot) {
-  return (kernel << 28) | ((slot & 0xffu) << 20) | (((threadIdx.x >> 5) & 0xfu) << 16) | (blockIdx.x & 0xffffu);
+  return pack_site(WaitSite{kernel, slot, threadIdx.x >> 5, blockIdx.x});
 }
 // Records a timeout: the error bit, and the site if it is the first one.
 // Kept out of line: it runs only on the failure path.

@@ -334,13 +334,11 @@ abw_status abw_device_check(abw_stream stream) {
   if (e != cudaSuccess) return from_cuda(e, "abw_device_check");
   const unsigned int word = words[0], site = words[1];
   if (word & (abw::kErrWaitTimeout | abw::kErrSelfTest)) {
-    static const char *const kernels[] = {"?", "causal kv", "causal dq", "causal forward", "decode",
-                                          "linear attention state", "linear attention output"};
-    const unsigned int k = site >> 28;
+    const abw::WaitSite s = abw::unpack_site(site);
     return fail(ABW_ETIMEOUT,
                 "a device-side bounded wait ran out (error word 0x%x; first in the %s kernel, barrier slot %u, "
                 "warp %u, block %u)",
-                word, kernels[k < 7 ? k : 0], (site >> 20) & 0xffu, (site >> 16) & 0xfu, site & 0xffffu);
+                word, abw::site_kernel(s.kernel), s.slot, s.warp, s.block);
   }
   if (word & abw::kErrSmemAlign)
     return fail(ABW_ECUDA, "a kernel's dynamic shared memory was not 1024-byte aligned; it did no work");

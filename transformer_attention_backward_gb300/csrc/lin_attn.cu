@@ -923,7 +923,7 @@ __global__ void __launch_bounds__(kGThr, 1)
   constexpr int NH = D / 64;
 
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOOffBar + kGNumBars * 8 + 4);
-  const LinWait lw{sb + kOOffBar, abort_flag, kSiteLinOut, p.wait};
+  const LinWait lw{sb + kOOffBar, abort_flag, kSiteLinGrad, p.wait};
   auto bar = [&](int i) -> uint32_t { return lw.bar(i); };
   auto wt = [&](uint32_t br, uint32_t parity) -> bool { return lw.one(br, parity); };
   auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return lw.warp(br, parity); };
