@@ -396,8 +396,9 @@ abw_status qk_norm_rope_bwd(const void *q, const void *k, abw_dtype dtype, const
  *   workspace     at least lin_attn_fwd_workspace_bytes() (also for short
  *         sequences without states, which leave it alone); unspecified contents
  * Scores and the chunk states that enter a product are rounded to bf16; sums
- * and the states themselves are fp32, and final_state is good to fp32
- * rounding.  Equal calls give equal bits.
+ * and the states themselves are fp32.  final_state is good to some 40 2^-23 of
+ * its 2-norm, also where a head hardly decays (measured: 2e-7 after some hundred
+ * tokens, 8e-7 after 100,000).  Equal calls give equal bits.
  * Supported: D == 64 or 128; T >= 0; Hq >= 1, Hq % Hkv == 0; strides multiples
  * of 8.
  */
