@@ -394,19 +394,28 @@ def _call(op, fn, dev, stream, need, workspace, *args):
         _b.check(status, op)
 
 
-def _rotation(B, T, D, rope_base, rotary_dim, positions, sections, dev):
-    """(rotary_dim, address of the positions, axes, sections as a host array)."""
+def _int32(x, name):
+    """x as the C int it becomes (ctypes would wrap it without a word)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name}={x} does not fit 32 bits")
+    return x
+
+
+def _rotation(B, T, D, rope_base, rotary_dim, positions, sections, pos0, dev):
+    """(rotary_dim, address of the positions, axes, sections as a host array,
+    pos0)."""
     if not rope_base:
-        return 0, None, 1, None
+        return 0, None, 1, None, 0
     axes, host = 1, None
     if sections is not None:
         axes = len(sections)
-        host = (ctypes.c_int * axes)(*sections)
+        host = (ctypes.c_int * axes)(*(_int32(n, "sections") for n in sections))
     at = None
     if positions is not None:
         flat = axes == 1 and isinstance(positions, torch.Tensor) and positions.dim() == 2
         at = _dense(positions, "positions", torch.int32, (B, T) if flat else (axes, B, T), dev)
-    return D if rotary_dim is None else int(rotary_dim), at, axes, host
+    return D if rotary_dim is None else _int32(rotary_dim, "rotary_dim"), at, axes, host, _int32(pos0, "pos0")
 
 
 def qk_norm_rope_fwd(q, k, gamma_q=None, gamma_k=None, eps=1e-6, rope_base=0.0, rotary_dim=None, interleaved=True,
@@ -442,10 +451,10 @@ def qk_norm_rope_fwd(q, k, gamma_q=None, gamma_k=None, eps=1e-6, rope_base=0.0, 
         k_out = None
     gq = None if gamma_q is None else _dense(gamma_q, "gamma_q", _F32, (D,), dev)
     gk = None if gamma_k is None else _dense(gamma_k, "gamma_k", _F32, (D,), dev)
-    R, pos, axes, host = _rotation(B, T, D, rope_base, rotary_dim, positions, sections, dev)
+    R, pos, axes, host, pos0 = _rotation(B, T, D, rope_base, rotary_dim, positions, sections, pos0, dev)
     _call("qk_norm_rope_fwd", _fns().qk_norm_rope_fwd, dev, stream, None, None, q.data_ptr(), kp, _DT[dt], gq, gk, qo,
           ko, B, T, Hq, Hkv, D, qs, ks, float(eps), float(rope_base), R, 1 if interleaved else 0, pos, axes, host,
-          int(pos0))
+          pos0)
     return q_out, k_out
 
 
@@ -505,11 +514,11 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, gamma_q=None, gamma_k=None, eps=1e-6,
             dgk = _dense(dgamma_k, "dgamma_k", _F32, (D,), dev)
     else:
         dgamma_k = None
-    R, pos, axes, host = _rotation(B, T, D, rope_base, rotary_dim, positions, sections, dev)
+    R, pos, axes, host, pos0 = _rotation(B, T, D, rope_base, rotary_dim, positions, sections, pos0, dev)
     need = qk_norm_rope_bwd_workspace_bytes(D) if gq or gk else 0
     _call("qk_norm_rope_bwd", _fns().qk_norm_rope_bwd, dev, stream, need, workspace, q.data_ptr(), kp, _DT[dt], yq, yk,
           _DT[yt], gq, gk, dq.data_ptr(), dkp, dgq, dgk, B, T, Hq, Hkv, D, qs, ks, dqs, dks, float(eps),
-          float(rope_base), R, 1 if interleaved else 0, pos, axes, host, int(pos0))
+          float(rope_base), R, 1 if interleaved else 0, pos, axes, host, pos0)
     return dq, dk, dgamma_q, dgamma_k
 
 
