@@ -340,9 +340,12 @@ abw_status attn_bwd_causal_noalloc(const void *q, const void *k, const void *v, 
  *         pairs turn by the position on axis 0, the next sections[1] by that on
  *         axis 1, and so on (time, height and width of image and video
  *         tokens).  NULL with n_axes == 1.
- * Angles are exact to 2^-32 turns for every position; eps >= 0.  The sum of
- * squares is taken in fp32: a row that holds values above 1e18, or with eps 0
- * one of zeros or of nothing above 1e-19, may come out as NaN or infinite.
+ * The angle of a pair is off by at most |pos| 2^-54 + 2^-31 turns where rope_base
+ * >= 1 (2^-23 turns at the farthest position), and by (4 + |ln rope_base|) 2^-53
+ * of itself + 2^-31 turns below.  rope_base is the fp32 number given; the
+ * exponents run through the pairs of all axes.  eps >= 0.  The sum of squares is
+ * taken in fp32: a row that holds values above 1e18, or with eps 0 one of zeros or
+ * of nothing above 1e-19, may come out as NaN or infinite.
  * Supported: D even, 2 <= D <= 512; below 2^31 elements a token.
  */
 abw_status qk_norm_rope_fwd(const void *q, const void *k, abw_dtype dtype, const float *gamma_q,

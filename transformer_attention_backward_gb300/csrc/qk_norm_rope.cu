@@ -9,10 +9,13 @@
 // Bound by memory: x is read once and y written once (backward: x and dy read,
 // dx written); the norm's sum is taken in registers.
 //
-// Angles without double precision: the host forms the turns per position,
-// base^(-2i / rotary_dim) / (2 pi) mod 1, as a 64-bit binary fraction; an
-// integer product with the position, modulo 2^64, is the angle modulo one turn,
-// exact to 2^-32 turns for every 32-bit position, negative ones included.
+// Angles without double precision on the device: the host forms the turns per
+// position, base^(-2i / rotary_dim) / (2 pi) mod 1, in double and hands them on as
+// a 64-bit binary fraction; an integer product with the position, modulo 2^64, is
+// the angle modulo one turn for every 32-bit position, negative ones included.
+// The product adds no more than 2^-31 turns; the table's own error (below 2^-54
+// turns where base >= 1: pow, the division and 2 pi, each to a double's rounding of
+// at most 0.16) grows with the position, to 2^-23 turns at 2^31.
 #include <math.h>
 
 #include "abw_host.h"
