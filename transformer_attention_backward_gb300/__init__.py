@@ -306,6 +306,16 @@ def attn_bwd_causal_saved_p(q, k, v, p_attn, o, dout, scale=None, rope_base=0.0,
 _BF16, _F32 = torch.bfloat16, torch.float32
 _lib = None
 
+# torch's own entries, some microseconds a call cheaper than the public functions
+# that stand in for them in a torch that lacks them.
+_PUBLIC = {
+    "_cuda_getCurrentRawStream": lambda index: torch.cuda.current_stream(index).cuda_stream,
+    "_cuda_getDevice": torch.cuda.current_device,
+    "_cuda_cudaCachingAllocator_raw_alloc": lambda size, stream: torch.cuda.caching_allocator_alloc(size, stream=stream),
+    "_cuda_cudaCachingAllocator_raw_delete": torch.cuda.caching_allocator_delete,
+}
+_raw_stream, _device_index, _raw_alloc, _raw_delete = (getattr(torch._C, name, public) for name, public in _PUBLIC.items())
+
 
 def _fns():
     global _lib
@@ -369,12 +379,12 @@ def _call(op, fn, dev, stream, need, workspace, *args):
     order."""
     index = dev.index
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
+        handle = _raw_stream(index)
     elif stream.device == dev:
         handle = stream.cuda_stream
     else:
         raise ValueError(f"{op}: stream on {stream.device}, tensors on {dev}")
-    if index != torch._C._cuda_getDevice():
+    if index != _device_index():
         with torch.cuda.device(dev):
             return _call(op, fn, dev, stream, need, workspace, *args)
     if need is None:
@@ -385,11 +395,11 @@ def _call(op, fn, dev, stream, need, workspace, *args):
     elif need == 0:
         status = fn(*args, None, 0, handle)
     else:
-        at = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, handle)
+        at = _raw_alloc(need, handle)
         try:
             status = fn(*args, at, need, handle)
         finally:
-            torch._C._cuda_cudaCachingAllocator_raw_delete(at)
+            _raw_delete(at)
     if status:
         _b.check(status, op)
 
