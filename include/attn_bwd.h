@@ -392,7 +392,9 @@ abw_status qk_norm_rope_bwd(const void *q, const void *k, abw_dtype dtype, const
  *   initial_state [B][Hkv][D][D] f32 or NULL (zero)
  *   lengths       [B] int32 or NULL: sequence b has min(max(lengths[b], 0), T)
  *         tokens; what q, k, v hold behind them is not looked at (NaN included)
- *         and o there is written as 0
+ *         and o there is written as 0.  Inside a sequence values are finite: an
+ *         infinity or NaN of a token reaches all outputs of its 128-token chunk,
+ *         those of earlier tokens too (a weight of 0 does not hold it back)
  *   o             [B][T][Hq][D] bf16, token stride o_stride
  *   final_state   [B][Hkv][D][D] f32 or NULL: the state behind each sequence's last
  *         token (may be the same buffer as initial_state)

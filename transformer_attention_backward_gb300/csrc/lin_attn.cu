@@ -23,8 +23,9 @@
 // Short sequences without states at their ends take the second alone: an item
 // goes through the products of the chunks before it (behind it) as well, which
 // for a few chunks costs less than the walk and its launch.
-// No element of a decay power above a^0 is formed, so strong decays underflow
-// to 0 and never overflow.
+// Decay powers are a^0 and below, so strong decays underflow to 0 and never
+// overflow; next to the diagonal alone a row's factor may be above 1 (a^-31 at
+// most, where that fits, MaskWeights).
 #include <math.h>
 
 #include "abw_host.h"
@@ -138,11 +139,12 @@ struct LinSizes {
 // weighted rows (read, formed, written) and 28 KB out of it to the tensor core,
 // some 500 of the 650 cycles that a step takes.  What hides the rest is steps
 // under way: a ring of 6 (X, Y) slots, four buffers of weighted rows, filled in
-// turn by three groups of warps (8192 tokens of 32 heads: 55 us; two groups 59,
-// four 58), two MMA warps and two buffers of U (deeper rings: no change).
-// 32 columns a CTA, not 64: 52 us against 95 for 8192 tokens of 32 heads, as
-// there are twice as many chains; 76 against 81 for 640 chains of 2048 tokens.
-// X once for all CTAs of a chain, by multicast: 57 and 85.
+// turn by three groups of warps, two MMA warps and two buffers of U.  The walk
+// takes 54 us for 8192 tokens of 32 heads with states (48 where none leaves: two
+// terms) and 80 for 640 chains of 2048 tokens.  Tried, against what it took at the
+// time: two groups 59 and four 58 (55); deeper rings no change; 64 columns a CTA,
+// half as many chains, 95 and 81 (52 and 76); X once for all CTAs of a chain, by
+// multicast, 57 and 85 (55 and 79).
 // Warps: 0 TMA, 1 and 18 MMA, 2-13 weights, 14-17 state.
 // ---------------------------------------------------------------------------
 constexpr int kSGroups = 3;                          // groups of four warps that form weighted rows
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(kSThr, 1)
 // no product needs by then, and leaves from there by TMA (16-byte stores by
 // the rows' threads took 2,400 cycles of an item's 8,300).
 // Over long sequences bound by memory: the forward of 8192 tokens of 32 heads
-// takes 53 us, its copies alone 50.  (Two sets of mask warps and scores formed
+// takes 51-53 us behind the walk, its copies alone 50.  (Two sets of mask warps and scores formed
 // an item ahead, as in lin_grad: no change here.)
 // ---------------------------------------------------------------------------
 constexpr int kOThr = 352;
