@@ -24,3 +24,17 @@ BF, F = torch.bfloat16, torch.float32
 def test_groups_without_a_row(abw, B, T, Hq, Hkv, D, rot, dtype, dy):  # noqa: F811
     for inter in (True, False):
         check(abw, B, T, Hq, Hkv, D, rot, None, 10000.0, inter, dtype, dy, eps=0.0, seed=B + T + D)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_a_nan_stays_one(abw, dtype, eps):  # noqa: F811
+    """The norm of a row with a NaN is one, so all of its outputs and of dgamma."""
+    q = torch.randn(2, 5, 3, 64, generator=torch.Generator().manual_seed(2)).to(dtype).cuda()
+    q[1, 2, 1, 7] = float("nan")
+    g = torch.ones(64, device="cuda")
+    y, _ = abw.qk_norm_rope_fwd(q, None, g, eps=eps, rope_base=1e4)
+    dx, _, dg, _ = abw.qk_norm_rope_bwd(q, None, torch.ones_like(q, dtype=F), None, g, eps=eps, rope_base=1e4)
+    assert bool(torch.isnan(y[1, 2, 1]).all()) and int(torch.isnan(y).sum()) == 64
+    assert bool(torch.isnan(dx[1, 2, 1]).all()) and int(torch.isnan(dx).sum()) == 64
+    assert bool(torch.isnan(dg).all())

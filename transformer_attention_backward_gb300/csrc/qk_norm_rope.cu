@@ -246,9 +246,11 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-// 1 / sqrt(m): the approximation (2 ulp) and one Newton step.
+// 1 / sqrt(m): the approximation (2 ulp) and one Newton step.  Finite for m = 0:
+// where eps is 0, a group of lanes without a row (zeros) would otherwise carry
+// 0 * NaN into dgamma.
 __device__ __forceinline__ float inv_root(float m) {
-  const float r = rsqrtf(m);
+  const float r = fminf(rsqrtf(m), 8.5e37f);                  // (1.5 of it still fits)
   return r * fmaf(-0.5f * m * r, r, 1.5f);
 }
 
@@ -609,9 +611,7 @@ __global__ void __launch_bounds__(kQThr, V == 4 && N == 1 ? bwd_blocks(RING) : 1
             cc = f_fma(f_mul(u[k][e], ga[k][e]), a[k][e], f_fma(f_mul(v[k][e], gb[k][e]), b[k][e], cc));
           }
         const float s2 = lanes_sum<L>(f_sum(ss)), c2 = lanes_sum<L>(f_sum(cc));
-        // held finite: where eps is 0, a group without a row (zeros) would
-        // otherwise carry 0 * NaN into dgamma (fminf drops the NaN)
-        inv = fminf(inv_root(fmaf(s2, p.inv_n, p.eps)), 3.4028234663852886e38f);
+        inv = inv_root(fmaf(s2, p.inv_n, p.eps));
         coef = -c2 * p.inv_n * (inv * inv);                   // -c / (D rms^2)
 #pragma unroll
         for (int k = 0; k < N; ++k)
