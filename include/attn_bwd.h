@@ -443,7 +443,8 @@ abw_status lin_attn_bwd(const void *q, const void *k, const void *v, const void 
  *   S = a S + k v^T (in place),   o = scale S^T q.
  *   q [B][Hq][D], k, v [B][Hkv][D], o [B][Hq][D] dtype (f32 or bf16)
  *   state         [n_states][Hkv][D][D] f32, read and written
- *   log_decay     [Hkv] f32, <= 0
+ *   log_decay     [Hkv] f32, <= 0; 1 - a is good to fp32, so heads that hardly decay
+ *         keep their pace over many tokens
  *   slots         [B] int32 or NULL (then n_states >= B and row b works on state
  *         b): row b works on state slots[b].  A row whose slot is not in
  *         0 .. n_states - 1 is empty: o is 0 there and no state is touched.  Two rows

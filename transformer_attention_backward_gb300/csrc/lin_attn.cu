@@ -64,17 +64,19 @@ __device__ __forceinline__ float log2_decay(float log_decay) {
   return l2 < -1e30f ? -1e30f : l2;
 }
 
-// a^n for the decay of a whole chunk: the float below it, and the share of it
-// that is missing.  A head that hardly decays collects this share over some
-// 1 / (1 - a^n) chunks (with one float alone: 1.7e-5 of the state after 100,000
-// tokens), so 1 - a^n is what is formed to fp32; stronger decays forget sooner.
-__device__ __forceinline__ float2 chunk_decay(float log_decay, float l2, int n) {
+// a^n for the decay of a step of n tokens: the float below it, and what it misses
+// of it.  A head that hardly decays collects that over some 1 / (1 - a^n) steps
+// (one float alone: 1.7e-5 of the state after 100,000 tokens in chunks, 1.8e-4
+// after 4,000 single ones), so 1 - a^n is what is formed to fp32; stronger decays
+// forget sooner, and take strong(), a^n as one float.
+template <typename F>
+__device__ __forceinline__ float2 step_decay(float log_decay, int n, F strong) {
   const float m = -expm1f(log_decay * static_cast<float>(n));
-  if (!(m < 0.5f)) return make_float2(lexp2(l2 * static_cast<float>(n)), 0.f);
+  if (!(m < 0.5f)) return make_float2(strong(), 0.f);
   const float a = __fsub_rd(1.f, m);
-  return make_float2(a, ((1.f - a) - m) / a);                 // (both differences are exact)
+  return make_float2(a, (1.f - a) - m);                       // (both differences are exact)
 }
-// Chunks after which the state makes up for the missing shares, in one
+// Chunks after which the state makes up for what they missed, in one
 // multiplication (with each chunk 108 us for 8192 tokens of 32 heads, as the walk
 // has few issue slots to spare; so 105, with no more than one float 104).  What
 // joined the state since the last time is moved by less than kOwed 2^-24.
@@ -361,12 +363,12 @@ __global__ void __launch_bounds__(kSThr, 1)
         S[2 * c] = make_float2(v.x, v.y), S[2 * c + 1] = make_float2(v.z, v.w);
       }
     }
-    const float2 whole = chunk_decay(p.z.log_decay[kv], l2, kC);
+    const float2 whole = step_decay(p.z.log_decay[kv], kC, [&] { return lexp2(l2 * kC); });
     const float rest = lexp2(l2 * static_cast<float>(len - (ncb - 1) * kC));   // of the last chunk
     int owed = 0;
     auto settle = [&] {
       if (whole.y > 0.f) {                                    // (an infinity stays one)
-        const float f = whole.y * static_cast<float>(owed);
+        const float f = whole.y / whole.x * static_cast<float>(owed);
 #pragma unroll
         for (int c = 0; c < kCW / 2; ++c) S[c] = __ffma2_rn(make_float2(f, f), S[c], S[c]);
       }
@@ -456,8 +458,8 @@ __global__ void __launch_bounds__(kSThr, 1)
 // no product needs by then, and leaves from there by TMA (16-byte stores by
 // the rows' threads took 2,400 cycles of an item's 8,300).
 // Over long sequences bound by memory: the forward of 8192 tokens of 32 heads
-// takes 51-53 us behind the walk, its copies alone 50.  (Two sets of mask warps and scores formed
-// an item ahead, as in lin_grad: no change here.)
+// takes 51-53 us behind the walk, its copies alone 50.  (Two sets of mask warps
+// and scores formed an item ahead, as in lin_grad: no change here.)
 // ---------------------------------------------------------------------------
 constexpr int kOThr = 352;
 constexpr int kOSlots = 5;            // of the ring; the two slots of A follow
@@ -1244,8 +1246,12 @@ __device__ __forceinline__ float lin_ld(const void *p, size_t i) {
   return static_cast<float>(reinterpret_cast<const T *>(p)[i]);
 }
 
+// Blocks an SM: what is under way is what counts (64 rows of 20 heads of 128:
+// 25.0 us with six, 25.7 with five).
+constexpr int decode_blocks(int D, int G) { return D == 64 ? (G <= 4 ? 8 : 6) : G <= 2 ? 6 : G <= 4 ? 5 : 4; }
+
 template <typename T, int D, int G>
-__global__ void __launch_bounds__(kDThr) lin_decode_kernel(const LinDecodeParams p) {
+__global__ void __launch_bounds__(kDThr, decode_blocks(D, G)) lin_decode_kernel(const LinDecodeParams p) {
   __shared__ float sk[D], sq[G][D];
   __shared__ float red[kDThr / 32][G][kDCols];
   constexpr int NSL = D / kDCols, R = D / 32;
@@ -1263,7 +1269,11 @@ __global__ void __launch_bounds__(kDThr) lin_decode_kernel(const LinDecodeParams
   float4 s[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) s[r] = st[(r0 + 32 * r) * (D / 4) + c4];
-  const float a = expf(p.log_decay[kv]);
+  // a and what one float misses of it; where nothing is missing nothing is added
+  // (an infinity stays one)
+  const float ld = p.log_decay[kv];
+  const float2 dec = step_decay(ld, 1, [&] { return expf(ld); });
+  const float a = dec.x, low = dec.y;
   if (tid < D) sk[tid] = lin_ld<T>(p.k, static_cast<size_t>(bh) * D + tid);
   for (int i = tid; i < G * D; i += kDThr)
     sq[i / D][i % D] = i / D < p.G ? lin_ld<T>(p.q, (static_cast<size_t>(b) * p.Hq + kv * p.G) * D + i) : 0.f;
@@ -1278,10 +1288,13 @@ __global__ void __launch_bounds__(kDThr) lin_decode_kernel(const LinDecodeParams
   for (int r = 0; r < R; ++r) {
     const int d = r0 + 32 * r;
     const float k = sk[d];
-    s[r].x = fmaf(a, s[r].x, k * v[0]);
-    s[r].y = fmaf(a, s[r].y, k * v[1]);
-    s[r].z = fmaf(a, s[r].z, k * v[2]);
-    s[r].w = fmaf(a, s[r].w, k * v[3]);
+    float4 t = make_float4(k * v[0], k * v[1], k * v[2], k * v[3]);
+    if (low > 0.f)
+      t = make_float4(fmaf(low, s[r].x, t.x), fmaf(low, s[r].y, t.y), fmaf(low, s[r].z, t.z), fmaf(low, s[r].w, t.w));
+    s[r].x = fmaf(a, s[r].x, t.x);
+    s[r].y = fmaf(a, s[r].y, t.y);
+    s[r].z = fmaf(a, s[r].z, t.z);
+    s[r].w = fmaf(a, s[r].w, t.w);
     st[d * (D / 4) + c4] = s[r];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
