@@ -31,6 +31,10 @@
  *                    the position rotation in the same pass (one or several position axes)
  *   lin_attn_fwd, lin_attn_bwd, lin_attn_decode  linear attention with a decay for each
  *                    KV head: chunked over sequences, recurrent for single tokens
+ *   attn_fwd_window, attn_bwd_window  softmax attention over a sliding window with a few
+ *                    first tokens that stay visible
+ *   kv_pages_write, attn_decode_paged, kv_pages_evict  its serving side: a paged cache,
+ *                    one new token over it, and eviction by accumulated attention weight
  *
  * Conventions shared by every entry point
  *   - All pointers are DEVICE pointers (cudaMalloc'd or equivalent), owned by
@@ -454,6 +458,138 @@ abw_status lin_attn_bwd(const void *q, const void *k, const void *v, const void 
 abw_status lin_attn_decode(const void *q, const void *k, const void *v, abw_dtype dtype, float *state,
                            const float *log_decay, const int *slots, void *o, int B, int Hq, int Hkv, int D,
                            int n_states, float scale, abw_stream stream);
+
+/*
+ * attn_fwd_window -- causal softmax attention over a sliding window with first
+ * tokens that stay visible (sinks): query i sees key j where
+ *   j <= i  and  (j > i - window  or  j < sinks),
+ *   s_ij = scale q_i . k_j,  lse_i = log sum_j exp(s_ij),  o_i = sum_j exp(s_ij - lse_i) v_j.
+ *   q [B][T][Hq][D], k, v [B][T][Hkv][D] bf16, token strides q_stride, k_stride,
+ *         v_stride; query head h reads KV head h / (Hq / Hkv)
+ *   lengths       [B] int32 or NULL: sequence b has min(max(lengths[b], 0), T)
+ *         tokens; what q, k, v hold behind them is not looked at (NaN included), o
+ *         there is written as 0 and lse as -infinity.  Inside a sequence values are
+ *         finite: an infinity or NaN of a token may reach every query whose
+ *         128-token block meets the token's (a weight of 0 does not hold it back)
+ *   o             [B][T][Hq][D] bf16, token stride o_stride (rounded from fp32)
+ *   lse           [B][Hq][T] f32, natural log
+ *   window        >= 1 (1: the token itself; T and more: plain causal attention)
+ *   sinks         >= 0
+ * The probabilities enter the o product rounded to bf16; sums are fp32.  Equal
+ * calls give equal bits.
+ * Supported: D == 64 or 128; T >= 0; Hq >= 1, Hq % Hkv == 0; strides multiples
+ * of 8.
+ */
+abw_status attn_fwd_window(const void *q, const void *k, const void *v, const int *lengths, void *o, float *lse,
+                           int B, int T, int Hq, int Hkv, int D, long long q_stride, long long k_stride,
+                           long long v_stride, long long o_stride, int window, int sinks, float scale,
+                           abw_stream stream);
+
+/*
+ * attn_bwd_window -- gradients of attn_fwd_window from its o and lse:
+ *   P_ij = exp(s_ij - lse_i) where key j is visible to query i, else 0,
+ *   delta_i = dout_i . o_i,  dS = P (dout V^T - delta),
+ *   dq = scale dS K,  dk = scale dS^T Q,  dv = P^T dout,
+ * dk and dv summed over the query heads that share a KV head.
+ *   q, k, v, lengths, window, sinks, scale: as in the forward
+ *   o             as the forward wrote it, token stride o_stride
+ *   dout          dense [B][T][Hq][D] bf16
+ *   lse           [B][Hq][T] f32
+ *   dq, dk, dv    bf16, token strides dq_stride, dk_stride, dv_stride (so they may
+ *         be parts of a packed gradient); 0 behind each sequence's last token
+ *   workspace     at least attn_bwd_window_workspace_bytes()
+ * P and dS enter their products rounded to bf16; sums are fp32 in a fixed order:
+ * equal calls on a device give equal bits.
+ * Supported sizes: as in the forward.
+ */
+size_t attn_bwd_window_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int window, int sinks);
+abw_status attn_bwd_window(const void *q, const void *k, const void *v, const void *o, const void *dout,
+                           const float *lse, const int *lengths, void *dq, void *dk, void *dv, int B, int T, int Hq,
+                           int Hkv, int D, long long q_stride, long long k_stride, long long v_stride,
+                           long long o_stride, long long dq_stride, long long dk_stride, long long dv_stride,
+                           int window, int sinks, float scale, void *workspace, size_t workspace_bytes,
+                           abw_stream stream);
+
+/*
+ * The paged cache of the three calls below: k_pages, v_pages
+ * [n_pages][page_size][Hkv][D] bf16, and a block_table [B][max_pages] int32 that
+ * gives position p of sequence b row p % page_size of page
+ * block_table[b][p / page_size].  An entry outside 0 .. n_pages - 1 is an absent
+ * page: its tokens are neither read nor written.  (A dense cache [B][S][Hkv][D]
+ * is one of B pages of S rows.)  Any page_size >= 1 with page_size * max_pages
+ * below 2^31.
+ */
+
+/*
+ * kv_pages_write -- puts the keys and values of new tokens into their pages:
+ * token t of sequence b, t < min(max(lengths[b], 0), T), goes to position
+ * starts[b] + t.  Positions below 0, at page_size * max_pages or above, and those
+ * of absent pages are left out.
+ *   k, v          [B][T][Hkv][D] bf16, token strides k_stride, v_stride
+ *   starts        [B] int32;  lengths [B] int32 or NULL (T tokens each)
+ * Two tokens of a call must not name the same row of a page.
+ * Supported: D a multiple of 8; strides multiples of 8.
+ */
+abw_status kv_pages_write(const void *k, const void *v, void *k_pages, void *v_pages, const int *block_table,
+                          const int *starts, const int *lengths, int B, int T, int Hkv, int D, int n_pages,
+                          int page_size, int max_pages, long long k_stride, long long v_stride, abw_stream stream);
+
+/*
+ * attn_decode_paged -- one new token per sequence over the paged cache, which
+ * holds its key and value already: with n = min(max(lengths[b], 0), page_size *
+ * max_pages) the query of row b stands at position n - 1 and sees the positions
+ *   j < n  with  (window == 0  or  j >= n - window  or  j < sinks)
+ * of present pages:
+ *   s_j = scale q . k_j,  p_j = exp(s_j) / sum exp(s),  o = sum_j p_j v_j.
+ * A row that sees nothing (length 0, no page) gives o = 0.
+ *   q, o          [B][Hq][D] dtype (f32 or bf16); query head h reads KV head
+ *         h / (Hq / Hkv)
+ *   lengths       [B] int32
+ *   weight_sums   [B][Hkv][page_size * max_pages] f32 or NULL: every visible
+ *         position's entry has the sum of its p_j over the query heads of the KV
+ *         head added; the others are left as they are
+ *   window        >= 0 (0: none);  sinks >= 0 (not looked at without a window)
+ *   workspace     at least attn_decode_paged_workspace_bytes(); unspecified
+ *         contents
+ * The cache is read once, in pieces of equal length over all sequences whatever
+ * their lengths, and the pieces are joined.  q and p enter the products as sums of
+ * bf16 terms that keep 16 bits of them and more, sums are fp32.  Values of visible
+ * positions are finite; what others hold is not looked at.  Equal calls on a
+ * device give equal bits.
+ * Supported: D == 64 or 128; Hq % Hkv == 0.
+ */
+size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int D, int page_size, int max_pages, int window,
+                                         int sinks, int with_weight_sums);
+abw_status attn_decode_paged(const void *q, abw_dtype dtype, const void *k_pages, const void *v_pages,
+                             const int *block_table, const int *lengths, float *weight_sums, void *o, int B, int Hq,
+                             int Hkv, int D, int n_pages, int page_size, int max_pages, int window, int sinks,
+                             float scale, void *workspace, size_t workspace_bytes, abw_stream stream);
+
+/*
+ * kv_pages_evict -- keeps, for each sequence and KV head, at most `budget` tokens
+ * of the cache: those at positions below `sinks`, the last `recent` positions,
+ * and of the others those of the largest weight_sums (ties: the lower position; a
+ * NaN counts as -infinity).  Tokens of absent pages are not kept.  The kept
+ * ones go, in their order, to positions 0, 1, .. of the pages that new_table names
+ * (the old pages stay as they are: they may be shared with other sequences).
+ *   k_pages, v_pages  read in the pages of block_table, written in those of
+ *         new_table [B][new_max_pages] int32; no page may be named by both, nor
+ *         twice by new_table.  A row of an absent new page is not written
+ *   lengths       [B] int32, as for attn_decode_paged
+ *   weight_sums   [B][Hkv][page_size * max_pages] f32
+ *   kept          [B][Hkv][budget] int32: the positions kept, ascending, -1 behind
+ *         the last one
+ *   new_lengths   [B] int32: the tokens kept, min(budget, present ones)
+ *   new_weight_sums [B][Hkv][page_size * new_max_pages] f32: the kept tokens'
+ *         sums, 0 behind the last one
+ *   budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget <= page_size *
+ *         new_max_pages
+ * Supported: D a multiple of 8.
+ */
+abw_status kv_pages_evict(void *k_pages, void *v_pages, const int *block_table, const int *lengths,
+                          const float *weight_sums, const int *new_table, int *kept, int *new_lengths,
+                          float *new_weight_sums, int B, int Hkv, int D, int n_pages, int page_size, int max_pages,
+                          int new_max_pages, int budget, int sinks, int recent, abw_stream stream);
 
 #ifdef __cplusplus
 }

@@ -573,6 +573,134 @@ def lin_attn_decode(q, k, v, state, log_decay, scale, slots=None):
     return o, S
 
 
+def window_mask(n, window, sinks):
+    """[query][key] of a sequence of n tokens: key j <= query i, and j > i -
+    window or j < sinks."""
+    i, j = np.arange(n)[:, None], np.arange(n)[None, :]
+    return (j <= i) & ((j > i - window) | (j < sinks))
+
+
+def attn_window_forward(q, k, v, scale, window, sinks=0, lengths=None):
+    """Softmax attention under window_mask.  q [B][T][Hq][D], k, v
+    [B][T][Hkv][D].  Returns (o, lse [B][Hq][T]); behind a sequence's length o
+    is 0 and lse -infinity."""
+    q, k, v = _f64(q), _f64(k), _f64(v)
+    B, T, Hq, D = q.shape
+    G = Hq // k.shape[2]
+    o, lse = np.zeros_like(q), np.full((B, Hq, T), -np.inf)
+    for b, n in enumerate(_lengths(lengths, B, T)):
+        if n == 0:
+            continue
+        seen = window_mask(n, window, sinks)
+        for h in range(Hq):
+            s = np.where(seen, scale * (q[b, :n, h] @ k[b, :n, h // G].T), -np.inf)
+            m = s.max(-1, keepdims=True)
+            e = np.exp(s - m)
+            z = e.sum(-1, keepdims=True)
+            o[b, :n, h] = (e / z) @ v[b, :n, h // G]
+            lse[b, h, :n] = (m + np.log(z))[:, 0]
+    return o, lse
+
+
+def attn_window_backward(q, k, v, dout, scale, window, sinks=0, lengths=None, o=None):
+    """Gradients of attn_window_forward: dV = P^T dO, dS = P (dP - sum_j P dP),
+    dQ = scale dS K, dK = scale dS^T Q.  Given a saved o (a rounded one), the
+    sum is its dO . o, as in the backward's definition.  Returns (dq, dk, dv)."""
+    q, k, v, dout = _f64(q), _f64(k), _f64(v), _f64(dout)
+    B, T, Hq, D = q.shape
+    G = Hq // k.shape[2]
+    dq, dk, dv = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
+    for b, n in enumerate(_lengths(lengths, B, T)):
+        if n == 0:
+            continue
+        seen = window_mask(n, window, sinks)
+        for h in range(Hq):
+            kh, vh, do = k[b, :n, h // G], v[b, :n, h // G], dout[b, :n, h]
+            p = softmax_forward(np.where(seen, scale * (q[b, :n, h] @ kh.T), -np.inf))
+            dp = do @ vh.T
+            delta = (p * dp).sum(-1, keepdims=True) if o is None else (do * _f64(o)[b, :n, h]).sum(-1, keepdims=True)
+            ds = scale * p * (dp - delta)
+            dq[b, :n, h] = ds @ kh
+            dk[b, :n, h // G] += ds.T @ q[b, :n, h]
+            dv[b, :n, h // G] += p.T @ do
+    return dq, dk, dv
+
+
+def page_rows(table, page_size, n_pages, first, last):
+    """(position, page, row) of the positions first .. last - 1 that a row of a
+    block table gives a page."""
+    out = []
+    for p in range(max(first, 0), min(last, len(table) * page_size)):
+        page = int(table[p // page_size])
+        if 0 <= page < n_pages:
+            out.append((p, page, p % page_size))
+    return out
+
+
+def kv_pages_write(k, v, k_pages, v_pages, table, starts, lengths=None):
+    """New (k_pages, v_pages): token t of row b at position starts[b] + t."""
+    k_pages, v_pages = _f64(k_pages).copy(), _f64(v_pages).copy()
+    B, T = k.shape[:2]
+    for b, n in enumerate(_lengths(lengths, B, T)):
+        s = int(starts[b])
+        for p, page, row in page_rows(table[b], k_pages.shape[1], k_pages.shape[0], s, s + n):
+            k_pages[page, row], v_pages[page, row] = k[b, p - s], v[b, p - s]
+    return k_pages, v_pages
+
+
+def attn_decode_paged(q, k_pages, v_pages, table, lengths, scale, window=None, sinks=0, weight_sums=None):
+    """One query per row over a paged cache.  Returns (o, new weight sums or
+    None)."""
+    q = _f64(q)
+    n_pages, page_size, Hkv, _ = k_pages.shape
+    G = q.shape[1] // Hkv
+    o = np.zeros_like(q)
+    sums = None if weight_sums is None else _f64(weight_sums).copy()
+    for b, n in enumerate(lengths):
+        n = min(int(n), len(table[b]) * page_size)
+        at = [x for x in page_rows(table[b], page_size, n_pages, 0, n)
+              if window is None or x[0] >= n - window or x[0] < sinks]
+        if not at:
+            continue
+        pos, page, row = (np.array(x) for x in zip(*at))
+        k, v = _f64(k_pages[page, row]), _f64(v_pages[page, row])
+        for h in range(q.shape[1]):
+            p = softmax_forward(scale * (k[:, h // G] @ q[b, h]))
+            o[b, h] = p @ v[:, h // G]
+            if sums is not None:
+                sums[b, h // G, pos] += p
+    return o, sums
+
+
+def kv_pages_evict(k_pages, v_pages, table, lengths, weight_sums, budget, new_table, sinks=0, recent=1):
+    """Returns (k_pages, v_pages, kept [B][Hkv][budget], new_lengths, new
+    weight sums): of each sequence and head the positions below sinks, the last
+    `recent`, then those of the largest sums (NaN smallest; ties: the lower
+    position), at most `budget`, moved to the new pages in their order."""
+    n_pages, page_size, Hkv, _ = k_pages.shape
+    kp, vp = _f64(k_pages).copy(), _f64(v_pages).copy()
+    B = len(lengths)
+    kept = np.full((B, Hkv, budget), -1)
+    counts = np.zeros(B, dtype=np.int64)
+    sums = np.zeros((B, Hkv, len(new_table[0]) * page_size))
+    for b in range(B):
+        n = min(int(lengths[b]), len(table[b]) * page_size)
+        at = page_rows(table[b], page_size, n_pages, 0, n)
+        counts[b] = min(budget, len(at))
+        for h in range(Hkv):
+            def rank(x):
+                w = float(weight_sums[b, h, x[0]])
+                held = x[0] < sinks or x[0] >= n - recent
+                return (0 if held else 1, math.inf if math.isnan(w) else -w, x[0])
+            pick = sorted(sorted(at, key=rank)[:counts[b]])
+            for i, (p, page, row) in enumerate(pick):
+                kept[b, h, i], sums[b, h, i] = p, weight_sums[b, h, p]
+                to = int(new_table[b][i // page_size])
+                if 0 <= to < n_pages:
+                    kp[to, i % page_size, h], vp[to, i % page_size, h] = k_pages[page, row, h], v_pages[page, row, h]
+    return kp, vp, kept, counts, sums
+
+
 # ==========================================================================
 # Numerical gradient verification (section "Numerical Gradient Verification")
 # ==========================================================================

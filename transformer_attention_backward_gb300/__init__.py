@@ -11,7 +11,8 @@ Functions (same names as the C ABI):
   lora_bwd, attn_bwd_decode, attn_fwd_causal, attn_bwd_causal,
   attn_bwd_causal_saved_p, attn_bwd_causal_workspace_bytes, device_check,
   qk_norm_rope_fwd, qk_norm_rope_bwd, lin_attn_fwd, lin_attn_bwd,
-  lin_attn_decode and their *_workspace_bytes
+  lin_attn_decode, attn_fwd_window, attn_bwd_window, kv_pages_write,
+  attn_decode_paged, kv_pages_evict and their *_workspace_bytes
 """
 from __future__ import annotations
 
@@ -27,7 +28,9 @@ __all__ = ["softmax_bwd", "rope_bwd", "rmsnorm_bwd", "rmsnorm_bwd_dgamma", "relu
            "attn_bwd_decode", "attn_fwd_causal", "attn_bwd_causal", "attn_bwd_causal_saved_p",
            "attn_bwd_causal_workspace_bytes", "device_check", "AbwError", "library",
            "qk_norm_rope_fwd", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes", "lin_attn_fwd",
-           "lin_attn_fwd_workspace_bytes", "lin_attn_bwd", "lin_attn_bwd_workspace_bytes", "lin_attn_decode"]
+           "lin_attn_fwd_workspace_bytes", "lin_attn_bwd", "lin_attn_bwd_workspace_bytes", "lin_attn_decode",
+           "attn_fwd_window", "attn_bwd_window", "attn_bwd_window_workspace_bytes", "kv_pages_write",
+           "attn_decode_paged", "attn_decode_paged_workspace_bytes", "kv_pages_evict"]
 
 AbwError = _b.AbwError
 
@@ -632,3 +635,174 @@ def lin_attn_decode(q, k, v, state, log_decay, scale=None, slots=None, o=None, s
     _call("lin_attn_decode", _fns().lin_attn_decode, dev, stream, None, None, qp, kp, vp, _DT[dt], sp, lp, sl, op, B,
           Hq, Hkv, D, n, 1.0 / math.sqrt(D) if scale is None else float(scale))
     return o
+
+
+# --------------------------------------------------------------------------
+# Softmax attention over a sliding window, and the paged cache that serves it
+# --------------------------------------------------------------------------
+def _heads(t, dim, axis):
+    return t.shape[axis] if isinstance(t, torch.Tensor) and t.dim() == dim else 0
+
+
+def _window_inputs(q, k, v, lengths, window, sinks):
+    """Checks what both directions take: (device, sizes, [B][T][Hkv][D],
+    strides, addresses, (window, sinks))."""
+    dev = _first(q, "q", 4, (_BF16,))
+    qshape = q.shape
+    B, T, Hq, D = qshape
+    Hkv = _heads(k, 4, 2)
+    kshape = (B, T, Hkv, D)
+    strides = (_rows(q, "q", _BF16, qshape, dev), _rows(k, "k", _BF16, kshape, dev), _rows(v, "v", _BF16, kshape, dev))
+    at = (q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          None if lengths is None else _dense(lengths, "lengths", torch.int32, (B,), dev))
+    return dev, (B, T, Hq, Hkv, D), kshape, strides, at, (_int32(window, "window"), _int32(sinks, "sinks"))
+
+
+def attn_fwd_window(q, k, v, window, sinks=0, scale=None, lengths=None, o=None, lse=None, stream=None):
+    """Causal softmax attention over a sliding window: query i sees the keys j
+    <= i with j > i - window or j < sinks.  q [B][T][Hq][D], k, v
+    [B][T][Hkv][D] bf16 (possibly parts of a packed projection), lengths [B]
+    int32 or None (tokens of each sequence; behind them o is 0 and lse
+    -infinity).  Returns (o [B][T][Hq][D] bf16, lse [B][Hq][T] fp32)."""
+    dev, dims, _, strides, at, sees = _window_inputs(q, k, v, lengths, window, sinks)
+    B, T, Hq, _, D = dims
+    os = 0
+    if o is None:
+        o = _empty(q.shape, _BF16, dev, stream)
+    else:
+        os = _rows(o, "o", _BF16, q.shape, dev)
+    if lse is None:
+        lse = _empty((B, Hq, T), _F32, dev, stream)
+        lp = lse.data_ptr()
+    else:
+        lp = _dense(lse, "lse", _F32, (B, Hq, T), dev)
+    _call("attn_fwd_window", _fns().attn_fwd_window, dev, stream, None, None, *at, o.data_ptr(), lp, *dims, *strides, os,
+          *sees, 1.0 / math.sqrt(D) if scale is None else float(scale))
+    return o, lse
+
+
+@functools.lru_cache(maxsize=1024)
+def attn_bwd_window_workspace_bytes(B, T, Hq, Hkv, D, window, sinks=0) -> int:
+    return int(library().attn_bwd_window_workspace_bytes(B, T, Hq, Hkv, D, window, sinks))
+
+
+def attn_bwd_window(q, k, v, o, dout, lse, window, sinks=0, scale=None, lengths=None, dq=None, dk=None, dv=None,
+                    workspace=None, stream=None):
+    """Gradients of attn_fwd_window from its o and lse: dout [B][T][Hq][D]
+    bf16.  Returns (dq, dk, dv) bf16 (given ones may be parts of a packed
+    gradient), 0 behind each sequence's last token."""
+    dev, dims, kshape, strides, (qp, kp, vp, ln), sees = _window_inputs(q, k, v, lengths, window, sinks)
+    B, T, Hq, _, D = dims
+    os = _rows(o, "o", _BF16, q.shape, dev)
+    dop, lp = _dense(dout, "dout", _BF16, q.shape, dev), _dense(lse, "lse", _F32, (B, Hq, T), dev)
+    outs = (0 if dq is None else _rows(dq, "dq", _BF16, q.shape, dev),
+            0 if dk is None else _rows(dk, "dk", _BF16, kshape, dev),
+            0 if dv is None else _rows(dv, "dv", _BF16, kshape, dev))
+    dq = _empty(q.shape, _BF16, dev, stream) if dq is None else dq
+    dk = _empty(kshape, _BF16, dev, stream) if dk is None else dk
+    dv = _empty(kshape, _BF16, dev, stream) if dv is None else dv
+    _call("attn_bwd_window", _fns().attn_bwd_window, dev, stream, attn_bwd_window_workspace_bytes(*dims, *sees), workspace,
+          qp, kp, vp, o.data_ptr(), dop, lp, ln, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *dims, *strides, os, *outs,
+          *sees, 1.0 / math.sqrt(D) if scale is None else float(scale))
+    return dq, dk, dv
+
+
+def _cache(k_pages, v_pages, block_table, B):
+    """Checks a paged cache: (device, Hkv, D, (n_pages, page_size, max_pages),
+    addresses of the pages and the table)."""
+    dev = _first(k_pages, "k_pages", 4, (_BF16,))
+    n, page, Hkv, D = k_pages.shape
+    most = _heads(block_table, 2, 1)
+    return dev, Hkv, D, (n, page, most), (_dense(k_pages, "k_pages", _BF16, k_pages.shape, dev),
+                                          _dense(v_pages, "v_pages", _BF16, k_pages.shape, dev),
+                                          _dense(block_table, "block_table", torch.int32, (B, most), dev))
+
+
+def kv_pages_write(k, v, k_pages, v_pages, block_table, starts, lengths=None, stream=None):
+    """Puts new tokens' keys and values into a paged cache: token t of sequence
+    b goes to position starts[b] + t, row p % page_size of page
+    block_table[b][p // page_size] for position p.  k, v [B][T][Hkv][D] bf16
+    (possibly parts of a packed projection), k_pages, v_pages
+    [n_pages][page_size][Hkv][D] bf16, block_table [B][max_pages], starts [B]
+    and lengths [B] (None: T tokens each) int32.  Positions outside the table
+    and those of absent pages (entries outside 0 .. n_pages - 1) are left
+    out."""
+    B, T = _heads(k, 4, 0), _heads(k, 4, 1)
+    dev, Hkv, D, sizes, (kp, vp, tp) = _cache(k_pages, v_pages, block_table, B)
+    shape = (B, T, Hkv, D)
+    strides = (_rows(k, "k", _BF16, shape, dev), _rows(v, "v", _BF16, shape, dev))
+    sp = _dense(starts, "starts", torch.int32, (B,), dev)
+    ln = None if lengths is None else _dense(lengths, "lengths", torch.int32, (B,), dev)
+    _call("kv_pages_write", _fns().kv_pages_write, dev, stream, None, None, k.data_ptr(), v.data_ptr(), kp, vp, tp, sp,
+          ln, B, T, Hkv, D, *sizes, *strides)
+
+
+@functools.lru_cache(maxsize=1024)
+def attn_decode_paged_workspace_bytes(B, Hq, Hkv, D, page_size, max_pages, window=None, sinks=0,
+                                      with_weight_sums=False) -> int:
+    return int(library().attn_decode_paged_workspace_bytes(B, Hq, Hkv, D, page_size, max_pages, window or 0, sinks,
+                                                           1 if with_weight_sums else 0))
+
+
+def attn_decode_paged(q, k_pages, v_pages, block_table, lengths, scale=None, window=None, sinks=0, weight_sums=None,
+                      o=None, workspace=None, stream=None):
+    """Attention of one new token per sequence over a paged cache that holds
+    its key and value already.  q [B][Hq][D] fp32 or bf16, k_pages, v_pages
+    [n_pages][page_size][Hkv][D] bf16, block_table [B][max_pages] and lengths
+    [B] int32.  With a ``window`` the token sees the last ``window`` positions
+    and the first ``sinks``; absent pages (table entries outside 0 .. n_pages
+    - 1) are never seen.  weight_sums [B][Hkv][max_pages * page_size] fp32 or
+    None: gets each position's weights added, summed over the query heads of
+    the KV head.  Returns o [B][Hq][D] of q's dtype, 0 where nothing is
+    seen."""
+    qdev = _first(q, "q", 3, (_F32, _BF16))
+    dt, qshape = q.dtype, q.shape
+    B, Hq, _ = qshape
+    dev, Hkv, D, sizes, (kp, vp, tp) = _cache(k_pages, v_pages, block_table, B)
+    qp, lp = _dense(q, "q", dt, (B, Hq, D), dev), _dense(lengths, "lengths", torch.int32, (B,), dev)
+    wp = None
+    if weight_sums is not None:
+        wp = _dense(weight_sums, "weight_sums", _F32, (B, Hkv, sizes[1] * sizes[2]), dev)
+    if window is not None and window < 1:
+        raise ValueError(f"window={window} must be >= 1 (None: no window)")
+    window, sinks = _int32(window or 0, "window"), _int32(sinks, "sinks")
+    if o is None:
+        o = _empty(qshape, dt, qdev, stream)
+        op = o.data_ptr()
+    else:
+        op = _dense(o, "o", dt, qshape, dev)
+    need = attn_decode_paged_workspace_bytes(B, Hq, Hkv, D, sizes[1], sizes[2], window, sinks, wp is not None)
+    _call("attn_decode_paged", _fns().attn_decode_paged, dev, stream, need, workspace, qp, _DT[dt], kp, vp, tp, lp, wp, op,
+          B, Hq, Hkv, D, *sizes, window, sinks, 1.0 / math.sqrt(D) if scale is None else float(scale))
+    return o
+
+
+def kv_pages_evict(k_pages, v_pages, block_table, lengths, weight_sums, budget, new_table, sinks=0, recent=1, kept=None,
+                   new_lengths=None, new_weight_sums=None, stream=None):
+    """Keeps at most ``budget`` tokens of each sequence and KV head of a paged
+    cache: the first ``sinks`` positions, the last ``recent``, and of the
+    others those of the largest weight_sums [B][Hkv][max_pages * page_size]
+    fp32 (ties: the lower position).  They go, in their order, to positions 0,
+    1, .. of the pages of new_table [B][new_max_pages] int32, which must be
+    others than those of block_table; the old pages stay as they are.  Returns
+    (kept [B][Hkv][budget] int32 positions, -1 behind the last; new_lengths
+    [B] int32; new_weight_sums [B][Hkv][new_max_pages * page_size] fp32)."""
+    B = _heads(block_table, 2, 0)
+    dev, Hkv, D, sizes, (kp, vp, tp) = _cache(k_pages, v_pages, block_table, B)
+    page, fresh = sizes[1], _heads(new_table, 2, 1)
+    budget, sinks, recent = _int32(budget, "budget"), _int32(sinks, "sinks"), _int32(recent, "recent")
+    lp = _dense(lengths, "lengths", torch.int32, (B,), dev)
+    wp = _dense(weight_sums, "weight_sums", _F32, (B, Hkv, page * sizes[2]), dev)
+    np_ = _dense(new_table, "new_table", torch.int32, (B, fresh), dev)
+
+    def out(t, name, dt, shape):
+        t = _empty(shape, dt, dev, stream) if t is None else t
+        return t, _dense(t, name, dt, shape, dev)
+    if budget < 1:
+        raise ValueError(f"budget={budget} must be >= 1")
+    kept, kat = out(kept, "kept", torch.int32, (B, Hkv, budget))
+    new_lengths, nat = out(new_lengths, "new_lengths", torch.int32, (B,))
+    new_weight_sums, wat = out(new_weight_sums, "new_weight_sums", _F32, (B, Hkv, page * fresh))
+    _call("kv_pages_evict", _fns().kv_pages_evict, dev, stream, None, None, kp, vp, tp, lp, wp, np_, kat, nat, wat, B, Hkv,
+          D, *sizes, fresh, budget, sinks, recent)
+    return kept, new_lengths, new_weight_sums

@@ -56,6 +56,13 @@ SIGNATURES = {
     "lin_attn_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _ll, _ll, _ll,
                           _ll, _ll, _ll, _f, _vp, _sz, _vp]),
     "lin_attn_decode": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp]),
+    "attn_fwd_window": (_i, [_vp] * 6 + [_i] * 5 + [_ll] * 4 + [_i, _i, _f, _vp]),
+    "attn_bwd_window_workspace_bytes": (_sz, [_i] * 7),
+    "attn_bwd_window": (_i, [_vp] * 10 + [_i] * 5 + [_ll] * 7 + [_i, _i, _f, _vp, _sz, _vp]),
+    "kv_pages_write": (_i, [_vp] * 7 + [_i] * 7 + [_ll, _ll, _vp]),
+    "attn_decode_paged_workspace_bytes": (_sz, [_i] * 9),
+    "attn_decode_paged": (_i, [_vp, _i] + [_vp] * 6 + [_i] * 9 + [_f, _vp, _sz, _vp]),
+    "kv_pages_evict": (_i, [_vp] * 9 + [_i] * 10 + [_vp]),
 }
 
 

@@ -114,6 +114,38 @@ cudaError_t launch_lin_attn_decode(const void *q, const void *k, const void *v, 
                                    const int *slots, void *o, int bf16, int B, int Hq, int Hkv, int D, int nstates,
                                    float scale, cudaStream_t st);
 
+// Attention over a sliding window with first tokens that stay visible; dout
+// null: forward.  Strides are elements from token to token.
+struct WindowArgs {
+  const void *q, *k, *v, *dout;
+  const int *lengths;
+  void *o, *dq, *dk, *dv;             // o: written forward, read backward
+  float *lse;
+  int B, T, Hq, Hkv, D;
+  long long q_stride, k_stride, v_stride, o_stride, dq_stride, dk_stride, dv_stride;
+  int window, sinks;
+  float scale;
+  void *ws;
+};
+size_t window_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int window, int sinks);
+cudaError_t launch_window_fwd(const WindowArgs &a, const WaitCtl &w, cudaStream_t st, const char **why);
+cudaError_t launch_window_bwd(const WindowArgs &a, const WaitCtl &w, cudaStream_t st, const char **why);
+
+// A paged cache and the rows that a call works on.
+struct PagesArgs {
+  void *k_pages, *v_pages;
+  const int *table, *lengths;
+  int B, Hkv, D, n_pages, page_size, max_pages;
+};
+cudaError_t launch_kv_pages_write(const PagesArgs &a, const void *k, const void *v, const int *starts, int T,
+                                  long long k_stride, long long v_stride, cudaStream_t st);
+size_t decode_paged_workspace_bytes(int B, int Hq, int Hkv, int D, long long tokens, bool weights);
+cudaError_t launch_attn_decode_paged(const PagesArgs &a, const void *q, int bf16, float *weight_sums, void *o, int Hq,
+                                     int window, int sinks, float scale, void *ws, cudaStream_t st);
+cudaError_t launch_kv_pages_evict(const PagesArgs &a, const float *weight_sums, const int *new_table, int *kept,
+                                  int *new_lengths, float *new_weight_sums, int new_max_pages, int budget, int sinks,
+                                  int recent, cudaStream_t st);
+
 cudaError_t launch_selftest_wait(const WaitCtl &w, cudaStream_t st);
 
 // Size of the fixed device scratch behind attn_bwd_causal_noalloc.

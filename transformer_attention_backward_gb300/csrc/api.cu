@@ -183,6 +183,31 @@ abw_status check_qk(const char *op, int B, int T, int Hq, int Hkv, int D, abw_dt
   return ABW_OK;
 }
 
+// Argument checks that the windowed attention's entry points share.
+abw_status check_window(const char *op, int B, int T, int Hq, int Hkv, int D, int window, int sinks, float scale) {
+  abw_status st = check_lin(op, B, T, Hq, Hkv, D, scale);
+  if (st != ABW_OK) return st;
+  if (window < 1) return fail(ABW_EINVAL, "%s: window=%d must be >= 1", op, window);
+  if (sinks < 0) return fail(ABW_EINVAL, "%s: sinks=%d is negative", op, sinks);
+  return ABW_OK;
+}
+
+// ... and those of the paged cache's.
+abw_status check_pages(const char *op, int B, int Hkv, int D, int n_pages, int page_size, int max_pages) {
+  if (B < 0 || Hkv < 0 || n_pages < 0 || max_pages < 0) return fail(ABW_EINVAL, "%s: negative size", op);
+  if (page_size < 1) return fail(ABW_EINVAL, "%s: page_size=%d must be >= 1", op, page_size);
+  if (static_cast<long long>(page_size) * max_pages > 0x7fffffff)
+    return fail(ABW_ENOTSUP, "%s: page_size * max_pages = %lld is above 2^31 - 1", op,
+                static_cast<long long>(page_size) * max_pages);
+  if (D < 8 || D % 8 != 0) return fail(ABW_ENOTSUP, "%s: D=%d is not a multiple of 8", op, D);
+  if (static_cast<long long>(Hkv) * D > 0x7fffffff) return fail(ABW_ENOTSUP, "%s: more than 2^31 elements a token", op);
+  return ABW_OK;
+}
+
+size_t page_bytes(int n_pages, int page_size, int Hkv, int D) {
+  return static_cast<size_t>(n_pages) * page_size * Hkv * D * 2;
+}
+
 size_t dt_size(abw_dtype d) { return d == ABW_BF16 ? 2 : 4; }
 
 }  // namespace
@@ -847,6 +872,187 @@ abw_status lin_attn_decode(const void *q, const void *k, const void *v, abw_dtyp
   return from_cuda(abw::launch_lin_attn_decode(q, k, v, state, log_decay, slots, o, dtype == ABW_BF16, B, Hq, Hkv, D,
                                                n_states, scale, reinterpret_cast<cudaStream_t>(stream)),
                    "lin_attn_decode");
+}
+
+abw_status attn_fwd_window(const void *q, const void *k, const void *v, const int *lengths, void *o, float *lse, int B,
+                           int T, int Hq, int Hkv, int D, long long q_stride, long long k_stride, long long v_stride,
+                           long long o_stride, int window, int sinks, float scale, abw_stream stream) {
+  abw_status st = check_window("attn_fwd_window", B, T, Hq, Hkv, D, window, sinks, scale);
+  if (st != ABW_OK) return st;
+  if (q_stride < 0 || k_stride < 0 || v_stride < 0 || o_stride < 0)
+    return fail(ABW_EINVAL, "attn_fwd_window: negative token stride");
+  if (B == 0 || T == 0) return ABW_OK;
+  Rows in[] = {lin_rows("q", q, B, T, Hq, D, q_stride),
+               lin_rows("k", k, B, T, Hkv, D, k_stride),
+               lin_rows("v", v, B, T, Hkv, D, v_stride),
+               dense("lengths", lengths, lengths ? static_cast<size_t>(B) * 4 : 0, 4)};
+  Rows out[] = {lin_rows("o", o, B, T, Hq, D, o_stride),
+                dense("lse", lse, static_cast<size_t>(B) * Hq * T * 4, 4)};
+  st = check_rows("attn_fwd_window", in, 4, out, 2);
+  if (st != ABW_OK) return st;
+  abw::WaitCtl w = abw::wait_ctl();
+  if (!w.err) return fail(ABW_ECUDA, "attn_fwd_window: no CUDA device");
+  abw::WindowArgs a = {};
+  a.q = q, a.k = k, a.v = v, a.lengths = lengths;
+  a.o = o, a.lse = lse;
+  a.B = B, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.D = D;
+  const long long qn = static_cast<long long>(Hq) * D, kn = static_cast<long long>(Hkv) * D;
+  a.q_stride = token_stride(q_stride, B, T, qn), a.k_stride = token_stride(k_stride, B, T, kn);
+  a.v_stride = token_stride(v_stride, B, T, kn), a.o_stride = token_stride(o_stride, B, T, qn);
+  a.window = window, a.sinks = sinks;
+  a.scale = scale;
+  const char *why = nullptr;
+  return from_cuda(abw::launch_window_fwd(a, w, reinterpret_cast<cudaStream_t>(stream), &why), "attn_fwd_window", why);
+}
+
+size_t attn_bwd_window_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int window, int sinks) {
+  if (B <= 0 || T <= 0 || Hkv <= 0 || Hq < Hkv || Hq % Hkv != 0 || (D != 64 && D != 128) || window < 1 || sinks < 0)
+    return 0;
+  return abw::window_bwd_workspace_bytes(B, T, Hq, Hkv, D, window, sinks);
+}
+
+abw_status attn_bwd_window(const void *q, const void *k, const void *v, const void *o, const void *dout,
+                           const float *lse, const int *lengths, void *dq, void *dk, void *dv, int B, int T, int Hq,
+                           int Hkv, int D, long long q_stride, long long k_stride, long long v_stride,
+                           long long o_stride, long long dq_stride, long long dk_stride, long long dv_stride,
+                           int window, int sinks, float scale, void *workspace, size_t workspace_bytes,
+                           abw_stream stream) {
+  abw_status st = check_window("attn_bwd_window", B, T, Hq, Hkv, D, window, sinks, scale);
+  if (st != ABW_OK) return st;
+  if (q_stride < 0 || k_stride < 0 || v_stride < 0 || o_stride < 0 || dq_stride < 0 || dk_stride < 0 || dv_stride < 0)
+    return fail(ABW_EINVAL, "attn_bwd_window: negative token stride");
+  if (B == 0 || T == 0) return ABW_OK;
+  const size_t need = abw::window_bwd_workspace_bytes(B, T, Hq, Hkv, D, window, sinks);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(ABW_EWORKSPACE, "attn_bwd_window: workspace %zu bytes at %p, need %zu", workspace_bytes, workspace,
+                need);
+  Rows in[] = {lin_rows("q", q, B, T, Hq, D, q_stride),
+               lin_rows("k", k, B, T, Hkv, D, k_stride),
+               lin_rows("v", v, B, T, Hkv, D, v_stride),
+               lin_rows("o", o, B, T, Hq, D, o_stride),
+               lin_rows("dout", dout, B, T, Hq, D, 0),
+               dense("lse", lse, static_cast<size_t>(B) * Hq * T * 4, 4),
+               dense("lengths", lengths, lengths ? static_cast<size_t>(B) * 4 : 0, 4)};
+  Rows out[] = {lin_rows("dq", dq, B, T, Hq, D, dq_stride),
+                lin_rows("dk", dk, B, T, Hkv, D, dk_stride),
+                lin_rows("dv", dv, B, T, Hkv, D, dv_stride),
+                dense("workspace", workspace, need)};
+  st = check_rows("attn_bwd_window", in, 7, out, 4);
+  if (st != ABW_OK) return st;
+  abw::WaitCtl w = abw::wait_ctl();
+  if (!w.err) return fail(ABW_ECUDA, "attn_bwd_window: no CUDA device");
+  abw::WindowArgs a = {};
+  a.q = q, a.k = k, a.v = v, a.dout = dout, a.lengths = lengths;
+  a.o = const_cast<void *>(o), a.lse = const_cast<float *>(lse);
+  a.dq = dq, a.dk = dk, a.dv = dv;
+  a.B = B, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.D = D;
+  const long long qn = static_cast<long long>(Hq) * D, kn = static_cast<long long>(Hkv) * D;
+  a.q_stride = token_stride(q_stride, B, T, qn), a.k_stride = token_stride(k_stride, B, T, kn);
+  a.v_stride = token_stride(v_stride, B, T, kn), a.o_stride = token_stride(o_stride, B, T, qn);
+  a.dq_stride = token_stride(dq_stride, B, T, qn), a.dk_stride = token_stride(dk_stride, B, T, kn);
+  a.dv_stride = token_stride(dv_stride, B, T, kn);
+  a.window = window, a.sinks = sinks;
+  a.scale = scale;
+  a.ws = workspace;
+  const char *why = nullptr;
+  return from_cuda(abw::launch_window_bwd(a, w, reinterpret_cast<cudaStream_t>(stream), &why), "attn_bwd_window", why);
+}
+
+abw_status kv_pages_write(const void *k, const void *v, void *k_pages, void *v_pages, const int *block_table,
+                          const int *starts, const int *lengths, int B, int T, int Hkv, int D, int n_pages,
+                          int page_size, int max_pages, long long k_stride, long long v_stride, abw_stream stream) {
+  abw_status st = check_pages("kv_pages_write", B, Hkv, D, n_pages, page_size, max_pages);
+  if (st != ABW_OK) return st;
+  if (T < 0) return fail(ABW_EINVAL, "kv_pages_write: negative size");
+  if (k_stride < 0 || v_stride < 0) return fail(ABW_EINVAL, "kv_pages_write: negative token stride");
+  if (B == 0 || T == 0 || Hkv == 0) return ABW_OK;
+  const size_t bb = static_cast<size_t>(B) * 4, pb = page_bytes(n_pages, page_size, Hkv, D);
+  Rows in[] = {lin_rows("k", k, B, T, Hkv, D, k_stride), lin_rows("v", v, B, T, Hkv, D, v_stride),
+               dense("block_table", block_table, bb * max_pages, 4), dense("starts", starts, bb, 4),
+               dense("lengths", lengths, lengths ? bb : 0, 4)};
+  Rows out[] = {dense("k_pages", k_pages, pb), dense("v_pages", v_pages, pb)};
+  st = check_rows("kv_pages_write", in, 5, out, 2);
+  if (st != ABW_OK) return st;
+  if (n_pages == 0 || max_pages == 0) return ABW_OK;
+  const abw::PagesArgs a = {k_pages, v_pages, block_table, lengths, B, Hkv, D, n_pages, page_size, max_pages};
+  const long long kn = static_cast<long long>(Hkv) * D;
+  return from_cuda(abw::launch_kv_pages_write(a, k, v, starts, T, token_stride(k_stride, B, T, kn),
+                                              token_stride(v_stride, B, T, kn),
+                                              reinterpret_cast<cudaStream_t>(stream)),
+                   "kv_pages_write");
+}
+
+size_t attn_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int D, int page_size, int max_pages, int window,
+                                         int sinks, int with_weight_sums) {
+  if (B <= 0 || Hkv <= 0 || Hq < Hkv || Hq % Hkv != 0 || (D != 64 && D != 128) || page_size < 1 || max_pages < 0 ||
+      window < 0 || sinks < 0)
+    return 0;
+  long long tokens = static_cast<long long>(page_size) * max_pages;
+  if (window > 0 && static_cast<long long>(window) + sinks < tokens) tokens = static_cast<long long>(window) + sinks;
+  return abw::decode_paged_workspace_bytes(B, Hq, Hkv, D, tokens, with_weight_sums != 0);
+}
+
+abw_status attn_decode_paged(const void *q, abw_dtype dtype, const void *k_pages, const void *v_pages,
+                             const int *block_table, const int *lengths, float *weight_sums, void *o, int B, int Hq,
+                             int Hkv, int D, int n_pages, int page_size, int max_pages, int window, int sinks,
+                             float scale, void *workspace, size_t workspace_bytes, abw_stream stream) {
+  abw_status st = check_lin("attn_decode_paged", B, 1, Hq, Hkv, D, scale);
+  if (st == ABW_OK) st = check_pages("attn_decode_paged", B, Hkv, D, n_pages, page_size, max_pages);
+  if (st != ABW_OK) return st;
+  if (dtype != ABW_F32 && dtype != ABW_BF16) return fail(ABW_EINVAL, "attn_decode_paged: bad dtype");
+  if (window < 0) return fail(ABW_EINVAL, "attn_decode_paged: window=%d is negative", window);
+  if (sinks < 0) return fail(ABW_EINVAL, "attn_decode_paged: sinks=%d is negative", sinks);
+  if (B == 0) return ABW_OK;
+  const size_t need = attn_decode_paged_workspace_bytes(B, Hq, Hkv, D, page_size, max_pages, window, sinks,
+                                                        weight_sums != nullptr);
+  if (need && (workspace == nullptr || workspace_bytes < need))
+    return fail(ABW_EWORKSPACE, "attn_decode_paged: workspace %zu bytes at %p, need %zu", workspace_bytes, workspace,
+                need);
+  const size_t bb = static_cast<size_t>(B) * 4, pb = page_bytes(n_pages, page_size, Hkv, D);
+  const size_t qb = static_cast<size_t>(B) * Hq * D * dt_size(dtype);
+  Rows in[] = {dense("q", q, qb), dense("k_pages", k_pages, pb), dense("v_pages", v_pages, pb),
+               dense("block_table", block_table, bb * max_pages, 4), dense("lengths", lengths, bb, 4)};
+  Rows out[] = {dense("o", o, qb),
+                dense("weight_sums", weight_sums, weight_sums ? bb * Hkv * page_size * max_pages : 0, 4),
+                dense("workspace", workspace, need)};
+  st = check_rows("attn_decode_paged", in, 5, out, 3);
+  if (st != ABW_OK) return st;
+  const abw::PagesArgs a = {const_cast<void *>(k_pages), const_cast<void *>(v_pages), block_table, lengths, B, Hkv, D,
+                            n_pages, page_size, max_pages};
+  return from_cuda(abw::launch_attn_decode_paged(a, q, dtype == ABW_BF16, weight_sums, o, Hq, window, sinks, scale,
+                                                 workspace, reinterpret_cast<cudaStream_t>(stream)),
+                   "attn_decode_paged");
+}
+
+abw_status kv_pages_evict(void *k_pages, void *v_pages, const int *block_table, const int *lengths,
+                          const float *weight_sums, const int *new_table, int *kept, int *new_lengths,
+                          float *new_weight_sums, int B, int Hkv, int D, int n_pages, int page_size, int max_pages,
+                          int new_max_pages, int budget, int sinks, int recent, abw_stream stream) {
+  abw_status st = check_pages("kv_pages_evict", B, Hkv, D, n_pages, page_size, max_pages);
+  if (st == ABW_OK) st = check_pages("kv_pages_evict", B, Hkv, D, n_pages, page_size, new_max_pages);
+  if (st != ABW_OK) return st;
+  if (Hkv < 1) return fail(ABW_EINVAL, "kv_pages_evict: Hkv=%d must be >= 1", Hkv);
+  if (budget < 1 || sinks < 0 || recent < 0 || static_cast<long long>(sinks) + recent > budget)
+    return fail(ABW_EINVAL, "kv_pages_evict: budget=%d must be >= 1 and hold sinks=%d and recent=%d", budget, sinks,
+                recent);
+  if (budget > static_cast<long long>(page_size) * new_max_pages)
+    return fail(ABW_EINVAL, "kv_pages_evict: budget=%d, but new_table holds %lld tokens", budget,
+                static_cast<long long>(page_size) * new_max_pages);
+  if (B == 0) return ABW_OK;
+  const size_t bb = static_cast<size_t>(B) * 4, pb = page_bytes(n_pages, page_size, Hkv, D);
+  Rows in[] = {dense("block_table", block_table, bb * max_pages, 4), dense("lengths", lengths, bb, 4),
+               dense("weight_sums", weight_sums, bb * Hkv * page_size * max_pages, 4),
+               dense("new_table", new_table, bb * new_max_pages, 4)};
+  Rows out[] = {dense("k_pages", k_pages, pb), dense("v_pages", v_pages, pb),
+                dense("kept", kept, bb * Hkv * budget, 4), dense("new_lengths", new_lengths, bb, 4),
+                dense("new_weight_sums", new_weight_sums, bb * Hkv * page_size * new_max_pages, 4)};
+  st = check_rows("kv_pages_evict", in, 4, out, 5);
+  if (st != ABW_OK) return st;
+  const abw::PagesArgs a = {k_pages, v_pages, block_table, lengths, B, Hkv, D, n_pages, page_size, max_pages};
+  return from_cuda(abw::launch_kv_pages_evict(a, weight_sums, new_table, kept, new_lengths, new_weight_sums,
+                                              new_max_pages, budget, sinks, recent,
+                                              reinterpret_cast<cudaStream_t>(stream)),
+                   "kv_pages_evict");
 }
 
 }  // extern "C"

@@ -1,0 +1,1026 @@
+// Serving side of the softmax attention: a paged cache of keys and values,
+// attention of one new token per sequence over it, and the eviction of the
+// tokens that got the least attention.
+//
+// Cache: k_pages, v_pages [n_pages][page_size][Hkv][D] bf16; position p of
+// sequence b stands in row p % page_size of page block_table[b][p / page_size].
+// Every entry is tested against n_pages before it becomes an address.
+//
+// attn_decode_paged, two launches:
+//   split : the visible positions of all sequences and heads as one list of
+//           16-token tiles, cut into equal runs, one per CTA, whatever the
+//           sequences' lengths.  A run's part of one (sequence, KV head) is a
+//           piece; a piece that is the whole of it leaves as output, another as
+//           (max, sum, unnormalised output) in the workspace.
+//   finish: joins the pieces of each (sequence, head) that was cut, and with
+//           weight sums adds 2^(score - lse) of every position.
+// Per query row the softmax statistics run along (max m, sum l, output O, all
+// fp32): a tile with a larger max rescales l and O by 2^(m_old - m_new).
+//
+// The bound is the cache's bytes.  Each lane copies (cp.async) the very 16-byte
+// units that it later feeds to the tensor core, into slots of its own: no
+// barrier and no bank conflict, 3 tiles (24 KB at D = 128) under way per warp.
+// The units are fragments as they stand, because the contraction index of q k
+// and the column index of p v may be permuted at will:
+//   S = Q K^T  (m16n8k16: rows = query heads, columns = keys): lane (g, t) holds
+//     key g, components 32 c + 8 t .. + 7, whose pairs are the k indices
+//     (2t, 2t+1, 2t+8, 2t+9) of two steps; Q is laid out to match.
+//   O = P V    (rows = query heads, columns = components): lane (g, t) holds
+//     keys 2t, 2t+1, 2t+8, 2t+9, components 64 c + 8 g .. + 7; a byte
+//     permutation pairs the keys.  P's fragment is S's as it stands.
+// P enters as bf16 terms (two of them for bf16 outputs, three for fp32), fp32
+// queries as three, so nothing but the output is rounded to bf16.
+#include <math.h>
+
+#include <algorithm>
+
+#include "abw_host.h"
+
+namespace abw {
+namespace {
+
+// ------------------------------------------------------------------- writing
+// One block per `tpb` tokens; 16-byte units, up to four of k and of v in
+// flight per thread.
+constexpr int kWrThr = 256;
+constexpr int kWrUnroll = 4;
+
+struct WriteParams {
+  const uint4 *k, *v;
+  uint4 *kp, *vp;
+  const int *table, *starts, *lengths;
+  long long ntok, k_stride, v_stride;   // strides in 16-byte units
+  int T, units, tpb, n_pages, page_size, max_pages;
+};
+
+__global__ void __launch_bounds__(kWrThr) kv_pages_write_kernel(const __grid_constant__ WriteParams p) {
+  const long long t0 = static_cast<long long>(blockIdx.x) * p.tpb;
+  const int total = p.units * static_cast<int>(min(static_cast<long long>(p.tpb), p.ntok - t0));
+  for (int e0 = threadIdx.x; e0 < total; e0 += kWrThr * kWrUnroll) {
+    uint4 a[kWrUnroll], c[kWrUnroll];
+    long long to[kWrUnroll];
+#pragma unroll
+    for (int i = 0; i < kWrUnroll; ++i) {
+      const int e = e0 + i * kWrThr;
+      to[i] = -1;
+      if (e >= total) continue;
+      const int rel = e / p.units, unit = e - rel * p.units;
+      const long long tok = t0 + rel;
+      const int b = static_cast<int>(tok / p.T), t = static_cast<int>(tok - static_cast<long long>(b) * p.T);
+      if (p.lengths && t >= p.lengths[b]) continue;
+      const long long pos = static_cast<long long>(p.starts[b]) + t;
+      if (pos < 0 || pos >= static_cast<long long>(p.page_size) * p.max_pages) continue;
+      const int at = static_cast<int>(pos), pg = at / p.page_size;
+      const int page = p.table[static_cast<long long>(b) * p.max_pages + pg];
+      if (page < 0 || page >= p.n_pages) continue;
+      to[i] = (static_cast<long long>(page) * p.page_size + (at - pg * p.page_size)) * p.units + unit;
+      a[i] = p.k[tok * p.k_stride + unit];
+      c[i] = p.v[tok * p.v_stride + unit];
+    }
+#pragma unroll
+    for (int i = 0; i < kWrUnroll; ++i)
+      if (to[i] >= 0) {
+        p.kp[to[i]] = a[i];
+        p.vp[to[i]] = c[i];
+      }
+  }
+}
+
+// -------------------------------------------------------------------- decode
+constexpr int kDecWarps = 4, kDecThr = 32 * kDecWarps;
+constexpr int kDecStages = 3;
+constexpr int kTile = 16;            // positions per tile
+constexpr int kMinTiles = 8;         // tiles a CTA takes at least, while there are few
+constexpr int kDecCtas = 304;        // two per SM
+constexpr int kWtPos = 2048;         // positions per block of the weight sums
+constexpr uint32_t kNoRow = 0xffffffffu;
+
+struct DecParams {
+  const void *q;
+  void *o;
+  const __nv_bfloat16 *kp, *vp;
+  const int *table, *lengths;
+  float *weight_sums;
+  float *slots;        // [2 per CTA][rows * (D + 4)]: O [rows][D], m [rows], l [rows]
+  float2 *stats;       // [B][Hq] (m, l) of what one CTA had whole (with weight sums)
+  float *scores;       // [B][Hq][score_stride] scores in base-2 units (with weight sums)
+  long long score_stride;
+  int B, Hq, Hkv, D, G, ng, rows;    // ng groups of up to 16 query heads per KV head, rows = min(G, 16)
+  int n_pages, page_size, page_shift, max_pages, cap, window, sinks;
+  int q_bf16, ctas, wt_chunks;
+  float sl2;           // scale * log2(e)
+};
+
+// Visible positions of a sequence: [0, s) and [lo, n); index x of them.
+struct Seq {
+  int n, lo, s, vis;
+};
+__device__ __forceinline__ Seq seq_of(const DecParams &p, int b) {
+  Seq r;
+  r.n = min(max(p.lengths[b], 0), p.cap);
+  r.lo = p.window > 0 ? max(0, r.n - p.window) : 0;
+  r.s = min(p.sinks, r.lo);
+  r.vis = r.s + r.n - r.lo;
+  return r;
+}
+__device__ __forceinline__ int tiles_of(const Seq &s) { return (s.vis + kTile - 1) / kTile; }
+__device__ __forceinline__ int position(const Seq &s, int x) { return x < s.s ? x : x - s.s + s.lo; }
+
+// The list of tiles: sequence by sequence, in it unit by unit (KV head, group
+// of query heads), in it tile by tile.  Thread i of a block holds the counts of
+// sequences first(i) .. first(i + 1) - 1: `before` tiles stand ahead of them.
+struct Share {
+  long long total, before, mine;
+  int b0, b1;
+};
+template <int kThreads>
+__device__ Share share_of(const DecParams &p) {
+  __shared__ long long warp_sum_s[kThreads / 32];
+  const int per = (p.B + kThreads - 1) / kThreads;
+  Share r;
+  r.b0 = min(p.B, static_cast<int>(threadIdx.x) * per);
+  r.b1 = min(p.B, r.b0 + per);
+  r.mine = 0;
+  for (int b = r.b0; b < r.b1; ++b) r.mine += tiles_of(seq_of(p, b));
+  r.mine *= static_cast<long long>(p.Hkv) * p.ng;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long incl = r.mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) warp_sum_s[warp] = incl;
+  __syncthreads();
+  long long ahead = 0;
+  r.total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) ahead += warp_sum_s[w];
+    r.total += warp_sum_s[w];
+  }
+  __syncthreads();
+  r.before = ahead + incl - r.mine;
+  return r;
+}
+
+// Runs of the tile list: CTA c takes tiles start(c) .. start(c + 1) - 1.
+struct Runs {
+  long long each, extra;
+  int n;
+  __device__ Runs(long long total, int ctas) {
+    const long long want = (total + kMinTiles - 1) / kMinTiles;
+    n = static_cast<int>(min(static_cast<long long>(ctas), max(want, 1LL)));
+    each = total / n;
+    extra = total - each * n;
+  }
+  __device__ long long start(int c) const { return c * each + min(static_cast<long long>(c), extra); }
+  __device__ int owner(long long x) const {   // the CTA of tile x
+    const long long big = extra * (each + 1);
+    return static_cast<int>(x < big ? x / (each + 1) : extra + (x - big) / each);
+  }
+};
+
+// The sequence, unit and tile of tile x of the list, found by the thread whose
+// share holds it; all threads get it (x < total).
+struct Place {
+  int b, u, tile;
+  long long seg;   // index of the unit's first tile
+};
+__device__ __forceinline__ Place place_of(const DecParams &p, const Share &sh, long long x) {
+  __shared__ Place found;
+  if (x >= sh.before && x < sh.before + sh.mine) {
+    long long at = sh.before;
+    for (int b = sh.b0; b < sh.b1; ++b) {
+      const int tiles = tiles_of(seq_of(p, b));
+      const long long all = static_cast<long long>(tiles) * p.Hkv * p.ng;
+      if (x < at + all) {
+        const long long rel = x - at;
+        found.b = b;
+        found.u = static_cast<int>(rel / tiles);
+        found.tile = static_cast<int>(rel - static_cast<long long>(found.u) * tiles);
+        found.seg = at + static_cast<long long>(found.u) * tiles;
+        break;
+      }
+      at += all;
+    }
+  }
+  __syncthreads();
+  const Place r = found;
+  __syncthreads();
+  return r;
+}
+
+// A walk over the pieces of a CTA's run, the tiles of each dealt to the warps.
+struct Walk {
+  Seq s;
+  int b, u, tiles, tile0, tend;
+  long long left;      // tiles of the run behind this piece
+  __device__ __forceinline__ void begin(const DecParams &p, const Place &at, long long count) {
+    b = at.b;
+    u = at.u;
+    s = seq_of(p, b);
+    tiles = tiles_of(s);
+    tile0 = at.tile;
+    tend = static_cast<int>(min(static_cast<long long>(tiles), tile0 + count));
+    left = count - (tend - tile0);
+  }
+  // the next piece; false behind the last one
+  __device__ __forceinline__ bool next(const DecParams &p) {
+    if (left <= 0) return false;
+    if (++u == p.Hkv * p.ng) {
+      u = 0;
+      do {
+        ++b;
+        s = seq_of(p, b);
+        tiles = tiles_of(s);
+      } while (tiles == 0);
+    }
+    tile0 = 0;
+    tend = static_cast<int>(min(static_cast<long long>(tiles), left));
+    left -= tend;
+    return true;
+  }
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there) {
+  const int bytes = there ? 16 : 0;   // 0: the slot is filled with zeros and nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&v);
+}
+// bf16 terms of a pair of fp32 values, largest first.
+template <int kN>
+__device__ __forceinline__ void terms(float x, float y, uint32_t (&out)[kN]) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    out[i] = bf2(x, y);
+    if (i + 1 < kN) {
+      x -= bf16_lo(out[i]);
+      y -= bf16_hi(out[i]);
+    }
+  }
+}
+
+template <int kD, bool kWide>
+constexpr int dec_smem() {
+  return kDecWarps * kDecStages * kTile * kD * 4 + kDecWarps * 8 * (kD + 4) * 4 + kDecWarps * 16 * 2 * 4;
+}
+
+// kF32: fp32 queries and outputs; kWide: more than 8 query heads per KV head;
+// kScores: scores are kept for the weight sums.
+template <int kD, bool kF32, bool kWide, bool kScores>
+__global__ void __launch_bounds__(kDecThr, 2) decode_split_kernel(const __grid_constant__ DecParams p) {
+  constexpr int kQT = kF32 ? 3 : 1, kPT = kF32 ? 3 : 2;   // terms of q and of p
+  constexpr int kC = kD / 32, kV = kD / 64;               // 64-byte pieces of a k row, 128-byte pieces of a v row
+  constexpr int kSlots = 2 * kC + 4 * kV;                 // 16-byte slots of a lane and tile
+  constexpr int kR = kWide ? 2 : 1;                       // row halves
+  extern __shared__ __align__(128) unsigned char smem[];
+  float *mo = reinterpret_cast<float *>(smem + kDecWarps * kDecStages * kTile * kD * 4);   // [warps][8][kD + 4]
+  float *ms = mo + kDecWarps * 8 * (kD + 4);              // [warps][16] max, then [warps][16] sum
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const Share sh = share_of<kDecThr>(p);
+  // rows that see nothing
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+    if (seq_of(p, b).vis == 0) {
+      const size_t bytes = static_cast<size_t>(p.Hq) * kD * (kF32 ? 4 : 2);
+      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<unsigned char *>(p.o) + b * bytes);
+      for (size_t i = tid; i < bytes / 16; i += kDecThr) dst[i] = make_uint4(0, 0, 0, 0);
+    }
+  if (sh.total == 0) return;
+  const Runs runs(sh.total, p.ctas);
+  const int cta = blockIdx.x;
+  if (cta >= runs.n) return;
+  const long long r0 = runs.start(cta), count = runs.start(cta + 1) - r0;
+  if (count == 0) return;
+  const Place at = place_of(p, sh, r0);
+
+  Walk now, ahead;
+  now.begin(p, at, count);
+  ahead = now;
+  const uint32_t ring = smem_u32(smem) + warp * (kDecStages * kTile * kD * 4) + lane * 16;
+  const unsigned char *ring_p = smem + warp * (kDecStages * kTile * kD * 4) + lane * 16;
+
+  // ---- loads: tile `lt` of the piece `ahead`, whose rows `row` holds (lanes 0 .. 15)
+  int lt = ahead.tile0 + warp;
+  bool more = true;
+  uint32_t row = kNoRow;
+  auto settle = [&]() {   // moves on to a piece that has a tile for this warp
+    while (more && lt >= ahead.tend) {
+      more = ahead.next(p);
+      lt = warp;
+    }
+  };
+  auto look_up = [&]() {
+    row = kNoRow;
+    if (!more || lane >= kTile) return;
+    const int x = lt * kTile + lane;
+    if (x >= ahead.s.vis) return;
+    const int pos = position(ahead.s, x);
+    const int pg = p.page_shift >= 0 ? pos >> p.page_shift : pos / p.page_size;
+    const int page = p.table[static_cast<long long>(ahead.b) * p.max_pages + pg];
+    if (page >= 0 && page < p.n_pages)
+      row = static_cast<uint32_t>(page) * static_cast<uint32_t>(p.page_size) + static_cast<uint32_t>(pos - pg * p.page_size);
+  };
+  static_assert(kDecStages == 3, "a word of its own for each stage");
+  uint32_t seen0 = 0, seen1 = 0, seen2 = 0;   // positions of each tile under way that are there
+  auto issue = [&](int stage) {
+    const uint32_t there_all = __ballot_sync(0xffffffffu, row != kNoRow);
+    if (stage == 0) seen0 = there_all;
+    if (stage == 1) seen1 = there_all;
+    if (stage == 2) seen2 = there_all;
+    if (more) {
+      const uint32_t dst = ring + stage * (kTile * kD * 4);
+      const size_t head = static_cast<size_t>(ahead.u / p.ng) * kD;
+      const size_t pitch = static_cast<size_t>(p.Hkv) * kD;
+      const __nv_bfloat16 *nothing = static_cast<const __nv_bfloat16 *>(p.q);   // an address that no byte is read from
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const uint32_t r = __shfl_sync(0xffffffffu, row, g + 8 * n);
+        const bool there = r != kNoRow;
+        const __nv_bfloat16 *src = there ? p.kp + (r * pitch + head + 8 * t) : nothing;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) cp_async16(dst + (n * kC + c) * 512, src + (there ? 32 * c : 0), there);
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const uint32_t r = __shfl_sync(0xffffffffu, row, 2 * t + (n & 1) + 8 * (n >> 1));
+        const bool there = r != kNoRow;
+        const __nv_bfloat16 *src = there ? p.vp + (r * pitch + head + 8 * g) : nothing;
+#pragma unroll
+        for (int c = 0; c < kV; ++c) cp_async16(dst + (2 * kC + n * kV + c) * 512, src + (there ? 64 * c : 0), there);
+      }
+      lt += kDecWarps;
+      settle();
+      look_up();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  settle();
+  look_up();
+#pragma unroll
+  for (int i = 0; i < kDecStages; ++i) issue(i);
+
+  int stage = 0;
+  bool first = true;
+  do {
+    // ---- this piece's queries, as fragments
+    const int kvh = now.u / p.ng, grp = now.u - kvh * p.ng;
+    const int h0 = kvh * p.G + grp * 16, nrows = min(16, p.G - grp * 16);
+    uint32_t qf[kQT][kR][kC][4];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const bool live = g + 8 * r < nrows;
+      const size_t src = (static_cast<size_t>(now.b) * p.Hq + h0 + (live ? g + 8 * r : 0)) * kD + 8 * t;
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        if constexpr (kF32) {
+          const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + src + 32 * c);
+          const float4 z = make_float4(0.f, 0.f, 0.f, 0.f), x = live ? f[0] : z, y = live ? f[1] : z;
+          const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t tm[kQT];
+            terms<kQT>(v[2 * i], v[2 * i + 1], tm);
+#pragma unroll
+            for (int k = 0; k < kQT; ++k) qf[k][r][c][i] = tm[k];
+          }
+        } else {
+          const uint4 x = live ? *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + src + 32 * c)
+                               : make_uint4(0, 0, 0, 0);
+          qf[0][r][c][0] = x.x;
+          qf[0][r][c][1] = x.y;
+          qf[0][r][c][2] = x.z;
+          qf[0][r][c][3] = x.w;
+        }
+      }
+    }
+    float m[kR], l[kR], O[kV][8][4];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) m[r] = -INFINITY, l[r] = 0.f;
+#pragma unroll
+    for (int c = 0; c < kV; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) O[c][i][e] = 0.f;
+
+    for (int tile = now.tile0 + warp; tile < now.tend; tile += kDecWarps) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kDecStages - 1) : "memory");
+      const unsigned char *src = ring_p + stage * (kTile * kD * 4);
+      const uint32_t mask = stage == 0 ? seen0 : stage == 1 ? seen1 : seen2;
+      // ---- S = Q K^T
+      float S[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[n][e] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+          const uint4 k = *reinterpret_cast<const uint4 *>(src + (n * kC + c) * 512);
+#pragma unroll
+          for (int x = 0; x < kQT; ++x) {
+            mma16816(S[n], qf[x][0][c][0], kWide ? qf[x][kR - 1][c][0] : 0u, qf[x][0][c][1],
+                     kWide ? qf[x][kR - 1][c][1] : 0u, k.x, k.y);
+            mma16816(S[n], qf[x][0][c][2], kWide ? qf[x][kR - 1][c][2] : 0u, qf[x][0][c][3],
+                     kWide ? qf[x][kR - 1][c][3] : 0u, k.z, k.w);
+          }
+        }
+      }
+      // ---- running softmax of each row over the 16 positions
+      uint32_t pf[kPT][2][2];   // [term][row half][keys 2t, 2t+1 | 2t+8, 2t+9]
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (r >= kR) {
+#pragma unroll
+          for (int k = 0; k < kPT; ++k) pf[k][r][0] = pf[k][r][1] = 0u;
+          continue;
+        }
+        float s[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          s[i] = (mask >> (2 * t + (i & 1) + 8 * (i >> 1))) & 1u ? S[i >> 1][2 * r + (i & 1)] * p.sl2 : -INFINITY;
+        if constexpr (kScores) {
+          if (g + 8 * r < nrows) {
+            float *dst = p.scores + (static_cast<size_t>(now.b) * p.Hq + h0 + g + 8 * r) * p.score_stride +
+                         static_cast<size_t>(tile) * kTile + 2 * t;
+            *reinterpret_cast<float2 *>(dst) = make_float2(s[0], s[1]);
+            *reinterpret_cast<float2 *>(dst + 8) = make_float2(s[2], s[3]);
+          }
+        }
+        float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float mn = fmaxf(m[r], top);
+        const float base = mn == -INFINITY ? 0.f : mn;   // nothing seen yet: 2^(-inf - 0) = 0
+        if (__any_sync(0xffffffffu, mn > m[r])) {
+          const float f = ex2(m[r] - base);
+          l[r] *= f;
+#pragma unroll
+          for (int c = 0; c < kV; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              O[c][i][2 * r] *= f;
+              O[c][i][2 * r + 1] *= f;
+            }
+          m[r] = mn;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = ex2(s[i] - base);
+        l[r] += (s[0] + s[1]) + (s[2] + s[3]);
+        uint32_t lo[kPT], hi[kPT];
+        terms<kPT>(s[0], s[1], lo);
+        terms<kPT>(s[2], s[3], hi);
+#pragma unroll
+        for (int k = 0; k < kPT; ++k) pf[k][r][0] = lo[k], pf[k][r][1] = hi[k];
+      }
+      // ---- O += P V
+#pragma unroll
+      for (int c = 0; c < kV; ++c) {
+        uint32_t v[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(src + (2 * kC + n * kV + c) * 512);
+          v[n][0] = x.x, v[n][1] = x.y, v[n][2] = x.z, v[n][3] = x.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t sel = (i & 1) ? 0x7632 : 0x5410;
+          const uint32_t b0 = __byte_perm(v[0][i >> 1], v[1][i >> 1], sel), b1 = __byte_perm(v[2][i >> 1], v[3][i >> 1], sel);
+#pragma unroll
+          for (int k = 0; k < kPT; ++k) mma16816(O[c][i], pf[k][0][0], pf[k][1][0], pf[k][0][1], pf[k][1][1], b0, b1);
+        }
+      }
+      issue(stage);
+      stage = stage + 1 == kDecStages ? 0 : stage + 1;
+    }
+
+    // ---- the warps' parts of the piece, joined through shared memory, eight rows at a time
+    const bool whole = now.tile0 == 0 && now.tend == now.tiles;
+    float *slot = p.slots + (static_cast<size_t>(cta) * 2 + (first ? 0 : 1)) * p.rows * (kD + 4);
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      float sum = l[r];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (t == 0) {
+        ms[warp * 16 + g] = m[r];
+        ms[warp * 16 + 8 + g] = sum;
+      }
+#pragma unroll
+      for (int c = 0; c < kV; ++c) {   // components 64 c + 16 t + 8 j + i of row g
+        float *dst = mo + (warp * 8 + g) * (kD + 4) + 64 * c + 16 * t;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; i += 4)
+            *reinterpret_cast<float4 *>(dst + 8 * j + i) = make_float4(O[c][i][2 * r + j], O[c][i + 1][2 * r + j],
+                                                                       O[c][i + 2][2 * r + j], O[c][i + 3][2 * r + j]);
+      }
+      __syncthreads();
+      for (int e = tid; e < 8 * kD / 4; e += kDecThr) {
+        const int rr = e / (kD / 4), d = (e - rr * (kD / 4)) * 4, hrow = 8 * r + rr;
+        if (hrow >= nrows) continue;
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ms[w * 16 + rr]);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+          const float mw = ms[w * 16 + rr];
+          const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
+          const float4 x = *reinterpret_cast<const float4 *>(mo + (w * 8 + rr) * (kD + 4) + d);
+          L = fmaf(f, ms[w * 16 + 8 + rr], L);
+          acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y);
+          acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
+        }
+        if (whole) {
+          const float inv = L > 0.f ? 1.f / L : 0.f;
+          const size_t dst = (static_cast<size_t>(now.b) * p.Hq + h0 + hrow) * kD + d;
+          if constexpr (kF32)
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + dst) =
+                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+          else
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + dst) =
+                make_uint2(bf2(acc.x * inv, acc.y * inv), bf2(acc.z * inv, acc.w * inv));
+          if (kScores && d == 0) p.stats[static_cast<size_t>(now.b) * p.Hq + h0 + hrow] = make_float2(M, L);
+        } else {
+          *reinterpret_cast<float4 *>(slot + hrow * kD + d) = acc;
+          if (d == 0) {
+            slot[p.rows * kD + hrow] = M;
+            slot[p.rows * (kD + 1) + hrow] = L;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    first = false;
+  } while (now.next(p));
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Blocks 0 .. ctas - 1: block c joins the unit that begins in CTA c's run and
+// goes on behind it.  Blocks behind them, with weight sums: kWtPos positions of
+// a sequence and KV head each.
+constexpr int kFinThr = 128;
+
+// Slot of the i-th piece of a unit whose first tile is `seg`.
+__device__ __forceinline__ const float *piece_slot(const DecParams &p, const Runs &runs, long long seg, int c0, int i) {
+  const int second = i == 0 && seg != runs.start(c0);
+  return p.slots + (static_cast<size_t>(c0 + i) * 2 + second) * p.rows * (p.D + 4);
+}
+
+// Max and sum of row `row` of a unit over its pieces, by one warp.
+__device__ __forceinline__ float2 joined_stats(const DecParams &p, const Runs &runs, long long seg, int c0, int pieces,
+                                               int row) {
+  const int lane = threadIdx.x & 31;
+  float M = -INFINITY, L = 0.f;
+  for (int i = lane; i < pieces; i += 32) {
+    const float *s = piece_slot(p, runs, seg, c0, i) + p.rows * p.D;
+    const float m = s[row], l = s[p.rows + row], mn = fmaxf(M, m);
+    if (mn == -INFINITY) continue;
+    L = L * ex2(M - mn) + l * ex2(m - mn);
+    M = mn;
+  }
+  const float top = warp_max(M);
+  L = warp_sum(top == -INFINITY || M == -INFINITY ? 0.f : L * ex2(M - top));
+  return make_float2(top, L);
+}
+
+__global__ void __launch_bounds__(kFinThr) decode_finish_kernel(const __grid_constant__ DecParams p) {
+  __shared__ float2 st[16];
+  __shared__ long long wt_before;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Share sh = share_of<kFinThr>(p);
+  // every block waits, also one without work: what follows on the stream then
+  // finds the launch before this one complete
+  if (sh.total == 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  const Runs runs(sh.total, p.ctas);
+  if (static_cast<int>(blockIdx.x) < p.ctas) {
+    const int c = blockIdx.x;
+    const long long r0 = runs.start(min(c, runs.n - 1)), r1 = runs.start(min(c, runs.n - 1) + 1);
+    const Place at = place_of(p, sh, r1 - 1);
+    const int tiles = tiles_of(seq_of(p, at.b));
+    const long long end = at.seg + tiles;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (c >= runs.n || end <= r1 || at.seg < r0) return;
+    const int pieces = runs.owner(end - 1) - c + 1;
+    const int kvh = at.u / p.ng, grp = at.u - kvh * p.ng;
+    const int h0 = kvh * p.G + grp * 16, nrows = min(16, p.G - grp * 16);
+    for (int r = warp; r < nrows; r += kFinThr / 32) {
+      const float2 x = joined_stats(p, runs, at.seg, c, pieces, r);
+      if (lane == 0) st[r] = x;
+    }
+    __syncthreads();
+    for (int e = tid; e < nrows * (p.D / 4); e += kFinThr) {
+      const int r = e / (p.D / 4), d = (e - r * (p.D / 4)) * 4;
+      const float M = st[r].x, L = st[r].y;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int i = 0; i < pieces; ++i) {
+        const float *s = piece_slot(p, runs, at.seg, c, i);
+        const float m = s[p.rows * p.D + r];
+        const float4 x = *reinterpret_cast<const float4 *>(s + r * p.D + d);
+        const float f = m == -INFINITY ? 0.f : ex2(m - M);
+        acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y);
+        acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
+      }
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      const size_t dst = (static_cast<size_t>(at.b) * p.Hq + h0 + r) * p.D + d;
+      if (p.q_bf16)
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + dst) =
+            make_uint2(bf2(acc.x * inv, acc.y * inv), bf2(acc.z * inv, acc.w * inv));
+      else
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + dst) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    }
+    return;
+  }
+  // ---- weight sums
+  const long long w = static_cast<long long>(blockIdx.x) - p.ctas;
+  const int chunk = static_cast<int>(w % p.wt_chunks);
+  const int kvh = static_cast<int>(w / p.wt_chunks % p.Hkv), b = static_cast<int>(w / p.wt_chunks / p.Hkv);
+  const Seq s = seq_of(p, b);
+  if (b >= sh.b0 && b < sh.b1) {   // tiles ahead of this sequence
+    long long at = 0;
+    for (int i = sh.b0; i < b; ++i) at += tiles_of(seq_of(p, i));
+    wt_before = sh.before + at * p.Hkv * p.ng;
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (static_cast<long long>(chunk) * kWtPos >= s.vis) return;
+  const int tiles = tiles_of(s);
+  const int end = static_cast<int>(min(static_cast<long long>(s.vis), (chunk + 1LL) * kWtPos));
+  float acc[kWtPos / kFinThr];
+#pragma unroll
+  for (int i = 0; i < kWtPos / kFinThr; ++i) acc[i] = 0.f;
+  for (int grp = 0; grp < p.ng; ++grp) {
+    const long long seg = wt_before + (static_cast<long long>(kvh) * p.ng + grp) * tiles;
+    const int c0 = runs.owner(seg), c1 = runs.owner(seg + tiles - 1);
+    const int h0 = kvh * p.G + grp * 16, nrows = min(16, p.G - grp * 16);
+    __syncthreads();
+    for (int r = warp; r < nrows; r += kFinThr / 32) {
+      const float2 x = c0 == c1 ? p.stats[static_cast<size_t>(b) * p.Hq + h0 + r]
+                                : joined_stats(p, runs, seg, c0, c1 - c0 + 1, r);
+      if (lane == 0) st[r] = make_float2(x.x, x.y > 0.f ? 1.f / x.y : 0.f);
+    }
+    __syncthreads();
+    for (int r = 0; r < nrows; ++r) {
+      const float *sc = p.scores + (static_cast<size_t>(b) * p.Hq + h0 + r) * p.score_stride;
+      const float M = st[r].x, inv = st[r].y;
+      if (inv == 0.f) continue;
+#pragma unroll
+      for (int i = 0; i < kWtPos / kFinThr; ++i) {
+        const int x = chunk * kWtPos + i * kFinThr + tid;
+        if (x < end) acc[i] = fmaf(ex2(sc[x] - M), inv, acc[i]);
+      }
+    }
+  }
+  float *dst = p.weight_sums + (static_cast<size_t>(b) * p.Hkv + kvh) * p.cap;
+#pragma unroll
+  for (int i = 0; i < kWtPos / kFinThr; ++i) {
+    const int x = chunk * kWtPos + i * kFinThr + tid;
+    if (x < end && acc[i] > 0.f) dst[position(s, x)] += acc[i];
+  }
+}
+
+// ------------------------------------------------------------------ eviction
+// One block per (sequence, KV head) finds the tokens to keep: a radix select
+// over the weights' bits (8 at a time, from the top) gives the weight of the last
+// one and how many equal ones go with it, a scan in the order of the positions
+// writes them down.  A second launch moves the rows.
+constexpr int kEvThr = 1024;
+
+struct EvictParams {
+  uint4 *kp, *vp;
+  const int *table, *lengths, *new_table;
+  const float *sums;
+  int *kept, *new_lengths;
+  float *new_sums;
+  int B, Hkv, units;                  // units: 16-byte units of a head's row
+  int n_pages, page_size, max_pages, cap, new_max_pages, new_cap, budget, sinks, recent;
+};
+
+__device__ __forceinline__ bool present(const EvictParams &p, int b, int j) {
+  const int page = p.table[static_cast<long long>(b) * p.max_pages + j / p.page_size];
+  return page >= 0 && page < p.n_pages;
+}
+
+// Order of the weights as unsigned numbers: larger weight, larger number;
+// NaN counts as -infinity, -0 as 0.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+  const uint32_t u = __float_as_uint(w != w ? -INFINITY : w + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Sum over the block of a count, for every thread.
+__device__ __forceinline__ int block_count(int x, int *warp_s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  x = __reduce_add_sync(0xffffffffu, x);
+  __syncthreads();
+  if (lane == 0) warp_s[warp] = x;
+  __syncthreads();
+  return __reduce_add_sync(0xffffffffu, warp_s[lane]);
+}
+
+__global__ void __launch_bounds__(kEvThr, 1) evict_select_kernel(const __grid_constant__ EvictParams p) {
+  __shared__ int hist[256], warp_s[32], warp_e[32];
+  __shared__ uint32_t digit_s;
+  __shared__ int need_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int b = blockIdx.x / p.Hkv, h = blockIdx.x - b * p.Hkv;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int n = min(max(p.lengths[b], 0), p.cap);
+  const int late = max(n - p.recent, 0);   // positions from here on are recent
+  const float *sums = p.sums + static_cast<size_t>(blockIdx.x) * p.cap;
+  int *kept = p.kept + static_cast<size_t>(blockIdx.x) * p.budget;
+  float *new_sums = p.new_sums + static_cast<size_t>(blockIdx.x) * p.new_cap;
+
+  int here = 0, held = 0;
+  for (int j = tid; j < n; j += kEvThr) {
+    if (!present(p, b, j)) continue;
+    ++here;
+    held += j < p.sinks || j >= late;
+  }
+  here = block_count(here, warp_s);
+  held = block_count(held, warp_s);
+  const int m = min(here, p.budget);
+  // the smallest key that is kept, and how many of its equals (the first ones)
+  uint32_t least = 0;
+  int ties = n;
+  if (here > p.budget) {
+    int need = p.budget - held;            // of the others; held <= sinks + recent <= budget
+    uint32_t prefix = 0;
+    if (need == 0) {
+      least = 0xffffffffu;                 // above every weight's key
+      ties = 0;
+    }
+    for (int shift = 24; need > 0 && shift >= 0; shift -= 8) {
+      __syncthreads();
+      if (tid < 256) hist[tid] = 0;
+      __syncthreads();
+      for (int j = tid; j < n; j += kEvThr) {
+        if (j < p.sinks || j >= late || !present(p, b, j)) continue;
+        const uint32_t k = weight_key(sums[j]);
+        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1);
+      }
+      __syncthreads();
+      if (warp == 0) {                     // lane i: bins 8 i .. 8 i + 7; those above it are counted first
+        int c[8], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += c[i] = hist[8 * lane + i];
+        int above = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int o = __shfl_down_sync(0xffffffffu, above, d);
+          if (lane + d < 32) above += o;
+        }
+        above -= sum;
+        if (above < need && above + sum >= need) {
+#pragma unroll
+          for (int i = 7; i >= 0; --i) {
+            if (above + c[i] >= need) {
+              digit_s = 8 * lane + i;
+              need_s = need - above;
+              break;
+            }
+            above += c[i];
+          }
+        }
+      }
+      __syncthreads();
+      prefix |= digit_s << shift;
+      need = need_s;
+      least = prefix;
+      ties = need;
+    }
+  }
+  // ---- in the order of the positions
+  int out = 0, equal = 0;
+  for (int j0 = 0; j0 < n; j0 += kEvThr) {
+    const int j = j0 + tid;
+    const bool there = j < n && present(p, b, j);
+    const bool hold = there && (j < p.sinks || j >= late);
+    const float w = there ? sums[j] : 0.f;
+    const uint32_t k = weight_key(w);
+    const bool eq = there && !hold && k == least;
+    const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
+    if (lane == 0) warp_e[warp] = __popc(eqs);
+    __syncthreads();
+    const int e = warp_e[lane];
+    const int eq_before = equal + __reduce_add_sync(0xffffffffu, lane < warp ? e : 0) + __popc(eqs & ((1u << lane) - 1));
+    equal += __reduce_add_sync(0xffffffffu, e);
+    const bool keep = hold || (there && k > least) || (eq && eq_before < ties);
+    const uint32_t ks = __ballot_sync(0xffffffffu, keep);
+    if (lane == 0) warp_s[warp] = __popc(ks);
+    __syncthreads();
+    const int c = warp_s[lane];
+    const int at = out + __reduce_add_sync(0xffffffffu, lane < warp ? c : 0) + __popc(ks & ((1u << lane) - 1));
+    out += __reduce_add_sync(0xffffffffu, c);
+    if (keep && at < m) {
+      kept[at] = j;
+      new_sums[at] = w;
+    }
+    __syncthreads();
+  }
+  for (int i = m + tid; i < p.budget; i += kEvThr) kept[i] = -1;
+  for (int i = m + tid; i < p.new_cap; i += kEvThr) new_sums[i] = 0.f;
+  if (h == 0 && tid == 0) p.new_lengths[b] = m;
+}
+
+// Rows of the kept tokens, 16 bytes per thread and step; consecutive threads
+// take the units of a row, then its heads.
+constexpr int kMvThr = 256, kMvUnroll = 4;
+
+__global__ void __launch_bounds__(kMvThr) evict_move_kernel(const __grid_constant__ EvictParams p, long long total) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int per_tok = p.Hkv * p.units;
+  for (long long e0 = static_cast<long long>(blockIdx.x) * kMvThr * kMvUnroll + threadIdx.x; e0 < total;
+       e0 += static_cast<long long>(gridDim.x) * kMvThr * kMvUnroll) {
+    uint4 a[kMvUnroll], c[kMvUnroll];
+    long long to[kMvUnroll];
+#pragma unroll
+    for (int i = 0; i < kMvUnroll; ++i) {
+      to[i] = -1;
+      const long long e = e0 + i * kMvThr;
+      if (e >= total) continue;
+      const long long tok = e / per_tok;
+      const int in_tok = static_cast<int>(e - tok * per_tok), h = in_tok / p.units;
+      const int b = static_cast<int>(tok / p.budget), slot = static_cast<int>(tok - static_cast<long long>(b) * p.budget);
+      const int j = p.kept[(static_cast<long long>(b) * p.Hkv + h) * p.budget + slot];
+      if (j < 0) continue;
+      const int np = slot / p.page_size, op = j / p.page_size;
+      const int dst = p.new_table[static_cast<long long>(b) * p.new_max_pages + np];
+      const int src = p.table[static_cast<long long>(b) * p.max_pages + op];
+      if (dst < 0 || dst >= p.n_pages || src < 0 || src >= p.n_pages) continue;
+      const long long from = (static_cast<long long>(src) * p.page_size + (j - op * p.page_size)) * per_tok + in_tok;
+      to[i] = (static_cast<long long>(dst) * p.page_size + (slot - np * p.page_size)) * per_tok + in_tok;
+      a[i] = p.kp[from];
+      c[i] = p.vp[from];
+    }
+#pragma unroll
+    for (int i = 0; i < kMvUnroll; ++i)
+      if (to[i] >= 0) {
+        p.kp[to[i]] = a[i];
+        p.vp[to[i]] = c[i];
+      }
+  }
+}
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// Sizes of a decode call that its launch and its workspace share.
+struct DecSizes {
+  int ctas, rows, ng, wt_chunks;
+  long long score_stride;
+  size_t slots, stats, scores;   // bytes, multiples of 16
+};
+DecSizes dec_sizes(int B, int Hq, int Hkv, int D, long long tokens, bool weights) {
+  DecSizes s;
+  const int G = Hq / Hkv;
+  s.rows = std::min(G, 16);
+  s.ng = (G + 15) / 16;
+  const long long tiles = ceil_div(tokens, kTile);
+  s.ctas = static_cast<int>(std::max(1LL, std::min<long long>(kDecCtas, ceil_div(tiles * B * Hkv * s.ng, kMinTiles))));
+  s.score_stride = tiles * kTile;
+  s.wt_chunks = weights ? static_cast<int>(ceil_div(std::max(tokens, 1LL), kWtPos)) : 0;
+  s.slots = static_cast<size_t>(s.ctas) * 2 * s.rows * (D + 4) * 4;
+  s.stats = weights ? (static_cast<size_t>(B) * Hq * 8 + 15) / 16 * 16 : 0;
+  s.scores = weights ? static_cast<size_t>(B) * Hq * s.score_stride * 4 : 0;
+  return s;
+}
+
+template <int kD, bool kF32, bool kWide, bool kScores>
+cudaError_t launch_split(const DecParams &p, cudaStream_t st) {
+  constexpr int smem = dec_smem<kD, kWide>();
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(decode_split_kernel<kD, kF32, kWide, kScores>), smem);
+  if (e != cudaSuccess) return e;
+  decode_split_kernel<kD, kF32, kWide, kScores><<<p.ctas, kDecThr, smem, st>>>(p);
+  return cudaGetLastError();
+}
+template <int kD, bool kF32>
+cudaError_t launch_split(const DecParams &p, cudaStream_t st) {
+  if (p.G > 8)
+    return p.weight_sums ? launch_split<kD, kF32, true, true>(p, st) : launch_split<kD, kF32, true, false>(p, st);
+  return p.weight_sums ? launch_split<kD, kF32, false, true>(p, st) : launch_split<kD, kF32, false, false>(p, st);
+}
+
+// Launches `kernel` so that it may start while the launch before it drains; it
+// waits (griddepcontrol.wait) before it reads what that one writes.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_pages_write(const PagesArgs &a, const void *k, const void *v, const int *starts, int T,
+                                  long long k_stride, long long v_stride, cudaStream_t st) {
+  WriteParams p;
+  p.k = static_cast<const uint4 *>(k), p.v = static_cast<const uint4 *>(v);
+  p.kp = static_cast<uint4 *>(a.k_pages), p.vp = static_cast<uint4 *>(a.v_pages);
+  p.table = a.table, p.starts = starts, p.lengths = a.lengths;
+  p.ntok = static_cast<long long>(a.B) * T;
+  p.k_stride = k_stride / 8, p.v_stride = v_stride / 8;
+  p.T = T;
+  p.units = a.Hkv * a.D / 8;
+  p.n_pages = a.n_pages, p.page_size = a.page_size, p.max_pages = a.max_pages;
+  // as many tokens per block as give each thread kWrUnroll units, fewer while
+  // the grid would not fill the GPU
+  p.tpb = static_cast<int>(std::max(1LL, std::min<long long>(kWrThr * kWrUnroll / p.units, ceil_div(p.ntok, 1216))));
+  const long long blocks = ceil_div(p.ntok, p.tpb);
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  kv_pages_write_kernel<<<static_cast<unsigned>(blocks), kWrThr, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+size_t decode_paged_workspace_bytes(int B, int Hq, int Hkv, int D, long long tokens, bool weights) {
+  const DecSizes s = dec_sizes(B, Hq, Hkv, D, tokens, weights);
+  return s.slots + s.stats + s.scores;
+}
+
+cudaError_t launch_attn_decode_paged(const PagesArgs &a, const void *q, int bf16, float *weight_sums, void *o, int Hq,
+                                     int window, int sinks, float scale, void *ws, cudaStream_t st) {
+  long long tokens = static_cast<long long>(a.page_size) * a.max_pages;
+  DecParams p;
+  p.cap = static_cast<int>(tokens);
+  if (window > 0) tokens = std::min(tokens, static_cast<long long>(window) + sinks);
+  const DecSizes s = dec_sizes(a.B, Hq, a.Hkv, a.D, tokens, weight_sums != nullptr);
+  p.q = q, p.o = o;
+  p.kp = static_cast<const __nv_bfloat16 *>(a.k_pages), p.vp = static_cast<const __nv_bfloat16 *>(a.v_pages);
+  p.table = a.table, p.lengths = a.lengths;
+  p.weight_sums = weight_sums;
+  unsigned char *w = static_cast<unsigned char *>(ws);
+  p.slots = reinterpret_cast<float *>(w);
+  p.stats = reinterpret_cast<float2 *>(w + s.slots);
+  p.scores = reinterpret_cast<float *>(w + s.slots + s.stats);
+  p.score_stride = s.score_stride;
+  p.B = a.B, p.Hq = Hq, p.Hkv = a.Hkv, p.D = a.D, p.G = Hq / a.Hkv, p.ng = s.ng, p.rows = s.rows;
+  p.n_pages = a.n_pages, p.page_size = a.page_size, p.max_pages = a.max_pages;
+  p.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.page_size == 1 << i) p.page_shift = i;
+  p.window = window, p.sinks = sinks;
+  p.q_bf16 = bf16, p.ctas = s.ctas, p.wt_chunks = s.wt_chunks;
+  p.sl2 = scale * 1.4426950408889634f;
+  cudaError_t e = a.D == 64 ? (bf16 ? launch_split<64, false>(p, st) : launch_split<64, true>(p, st))
+                            : (bf16 ? launch_split<128, false>(p, st) : launch_split<128, true>(p, st));
+  if (e != cudaSuccess) return e;
+  const long long blocks = p.ctas + static_cast<long long>(s.wt_chunks) * a.B * a.Hkv;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_dependent(decode_finish_kernel, static_cast<unsigned>(blocks), kFinThr, st, p);
+}
+
+cudaError_t launch_kv_pages_evict(const PagesArgs &a, const float *weight_sums, const int *new_table, int *kept,
+                                  int *new_lengths, float *new_weight_sums, int new_max_pages, int budget, int sinks,
+                                  int recent, cudaStream_t st) {
+  EvictParams p;
+  p.kp = static_cast<uint4 *>(a.k_pages), p.vp = static_cast<uint4 *>(a.v_pages);
+  p.table = a.table, p.lengths = a.lengths, p.new_table = new_table;
+  p.sums = weight_sums;
+  p.kept = kept, p.new_lengths = new_lengths, p.new_sums = new_weight_sums;
+  p.B = a.B, p.Hkv = a.Hkv, p.units = a.D / 8;
+  p.n_pages = a.n_pages, p.page_size = a.page_size, p.max_pages = a.max_pages;
+  p.cap = a.page_size * a.max_pages;
+  p.new_max_pages = new_max_pages, p.new_cap = a.page_size * new_max_pages;
+  p.budget = budget, p.sinks = sinks, p.recent = recent;
+  const long long blocks = static_cast<long long>(a.B) * a.Hkv;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  evict_select_kernel<<<static_cast<unsigned>(blocks), kEvThr, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.n_pages == 0 || a.max_pages == 0) return e;
+  const long long total = blocks * budget * p.units;
+  const long long grid = std::min<long long>(ceil_div(total, kMvThr * kMvUnroll), 152 * 32);
+  return launch_dependent(evict_move_kernel, static_cast<unsigned>(grid), kMvThr, st, p, total);
+}
+
+}  // namespace abw
