@@ -72,7 +72,7 @@ def check(abw, t, window, sinks=0, lengths=None, scale=0.125):
     l = to_np(got[1])
     live = np.isfinite(rl)
     assert np.array_equal(np.isneginf(l), ~live)
-    most = max(1.0, float(np.abs(f["q"]).max() * np.abs(f["k"]).max()) * t["q"].shape[-1] * scale)
+    most = max(1.0, float(np.abs(f["q"]).max() * np.abs(f["k"]).max()) * t["q"].shape[-1] * abs(scale))
     assert np.all(np.abs(l[live] - rl[live]) <= 2.0 ** -20 * most)
     rg = O.attn_window_backward(f["q"], f["k"], f["v"], f["do"], scale, window, sinks, lengths, to_np(got[0]))
     for a, b in zip(got[2:], rg):

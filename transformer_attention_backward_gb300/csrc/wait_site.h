@@ -5,7 +5,8 @@
 namespace abw {
 
 enum : unsigned int {
-  kSiteKv = 1u, kSiteDq, kSiteFwd, kSiteDecode, kSiteLinState, kSiteLinOut, kSiteLinGrad, kSiteEnd
+  kSiteKv = 1u, kSiteDq, kSiteFwd, kSiteDecode, kSiteLinState, kSiteLinOut, kSiteLinGrad, kSiteEnd,
+  kSiteWinFwd = kSiteEnd, kSiteWinKv, kSiteWinDq, kSiteWinEnd   // the windowed attention's
 };
 
 struct WaitSite {
@@ -20,7 +21,7 @@ constexpr unsigned int pack_site(const WaitSite &s) {
 constexpr WaitSite unpack_site(unsigned int w) {
   return WaitSite{w >> 28, (w >> 21) & 0x7fu, (w >> 16) & 0x1fu, w & 0xffffu};
 }
-static_assert(kSiteEnd <= 16, "four bits for the kernel");
+static_assert(kSiteWinEnd <= 16, "four bits for the kernel");
 
 inline const char *site_kernel(unsigned int kernel) {
   switch (kernel) {
@@ -31,6 +32,9 @@ inline const char *site_kernel(unsigned int kernel) {
     case kSiteLinState: return "linear attention state";
     case kSiteLinOut: return "linear attention output";
     case kSiteLinGrad: return "linear attention gradient";
+    case kSiteWinFwd: return "window forward";
+    case kSiteWinKv: return "window kv";
+    case kSiteWinDq: return "window dq";
     default: return "?";
   }
 }

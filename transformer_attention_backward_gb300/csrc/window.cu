@@ -164,15 +164,6 @@ size_t window_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int wind
   return static_cast<size_t>(B) * T * Hq * 4;
 }
 
-cudaError_t launch_window_fwd(const WindowArgs &a, const WaitCtl &w, cudaStream_t st, const char **why) {
-  (void)w, (void)why;
-  const WinParams p = params(a);
-  const unsigned grid = blocks_of(static_cast<long long>(a.B) * a.T * a.Hq);
-  if (a.D == 64) window_query_kernel<64, false><<<grid, kThr, 0, st>>>(p);
-  else window_query_kernel<128, false><<<grid, kThr, 0, st>>>(p);
-  return cudaGetLastError();
-}
-
 cudaError_t launch_window_bwd(const WindowArgs &a, const WaitCtl &w, cudaStream_t st, const char **why) {
   (void)w, (void)why;
   const WinParams p = params(a);

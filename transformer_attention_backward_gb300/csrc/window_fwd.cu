@@ -1,0 +1,501 @@
+// Softmax attention over a sliding window with first tokens that stay visible,
+// forward: query i sees key j where j <= i and (j > i - window or j < sinks).
+//
+// Per query row, over blocks of 128 keys: m = running max, l = running sum of
+// 2^(s - m) (base-2 units, fp32), O = running sum of 2^(s - m) v in TMEM.  The
+// rescale is lazy: m moves only when a block's max exceeds it by more than 8, so
+// P <= 2^8 between rescales.  O / l and (m + log2 l) ln 2 come out.
+//
+// One persistent CTA per SM works on two tiles of 128 queries at once, in turn:
+// while the softmax warps of one form P, the tensor core runs the products of the
+// other.  The tiles share their K and V blocks: two heads of a KV head where the
+// group is even, else two neighbouring blocks of queries.  Only blocks that a
+// tile meets are multiplied: the window's, and the first tokens' in front of it.
+//   S = Q K^T   M=128 queries, N=128 keys      (TMEM [0,128) and [128,256))
+//   O += P V    M=128 queries, N=D, A = P in TMEM over S   (behind [256, ..))
+// Order of the products, block after block: per tile PV of its last block, then
+// S of the next, so S (and Q, O) need one buffer per tile; the order runs on
+// over the CTA's items.
+// Warps: 0 loads (K, V through a ring, Q per tile), 1 issues products, 4-7 and
+// 8-11 softmax of tile 0 and 1 (thread = query row), with most of the registers.
+// Padding behind a sequence is not looked at: its keys are never visible, and
+// its rows of V, which meet weights of 0, are cleared in shared memory.
+#include <algorithm>
+
+#include "window.cuh"
+
+namespace abw {
+namespace {
+
+using namespace win;
+
+constexpr int kThr = 384;
+constexpr float kRescale = 8.f;       // lazy-rescale threshold (base-2 units)
+constexpr int kHeadGroup = 8;         // tile pairs of heads per scheduling group
+
+// Bits of the columns 32 wd .. 32 wd + 31 that are below x.
+__device__ __forceinline__ uint32_t below(int x, int wd) {
+  const int n = min(max(x - 32 * wd, 0), 32);
+  return n == 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// kN columns of a thread's row.
+template <int kN>
+__device__ __forceinline__ void ld_row(uint32_t taddr, float (&v)[kN]) {
+#pragma unroll
+  for (int c = 0; c < kN; c += 64) {
+    float(&lo)[32] = *reinterpret_cast<float(*)[32]>(&v[c]);
+    float(&hi)[32] = *reinterpret_cast<float(*)[32]>(&v[c + 32]);
+    tc::ld32x2_wait(taddr + c, taddr + c + 32, lo, hi);
+  }
+}
+
+template <int kD>
+struct FwdSmem {
+  static constexpr int kTile = kBlk * kD * 2;               // one block of Q, K or V
+  static constexpr int kStages = kD == 128 ? 4 : 8;
+  static constexpr int kQ = 0;                              // two tiles
+  static constexpr int kRing = 2 * kTile;
+  static constexpr int kOut = kRing + kStages * kTile;      // 4 KB per softmax warp: 32 rows x 64 components
+  static constexpr int kBar = kOut + 8 * 4096;
+  enum {
+    kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kOEmpty = 10, kRaw = 12, kFinal = 13, kKVFull = 14,
+    kKVEmpty = kKVFull + kStages, kBars = kKVEmpty + kStages
+  };
+  static constexpr int kTmem = kBar + kBars * 8, kAbort = kTmem + 4;
+  static constexpr int kBytes = kAbort + 4 + 1024;          // + alignment slack
+  static_assert(kBytes <= 232448, "forward kernel shared memory");
+};
+
+struct FwdParams {
+  float *lse;
+  const int *lengths;
+  int B, T, Hq, Hkv, G, nqb, per_head, units, items;
+  int pair_heads;         // tiles: 1 two heads of a group, 0 two blocks of queries
+  int window, sinks, sink_blocks;
+  float scale;
+  WaitCtl wait;
+};
+
+// A tile and its blocks of keys, in the order of the products: `lead` blocks of
+// first tokens in front of the window's, lo .. hi; hi < 0: no block.
+struct Tile {
+  int h, q0, lo, hi, lead;
+  bool exists;
+  __device__ __forceinline__ int steps() const { return hi < 0 ? 0 : lead + hi - lo + 1; }
+  __device__ __forceinline__ int block(int x) const { return x < lead ? x : lo + (x - lead); }
+  __device__ __forceinline__ bool meets(int n) const { return n <= hi && (n >= lo || n < lead); }
+};
+struct Unit {
+  int b, u, m, n;   // batch, head unit, place along the queries, tokens
+};
+
+__device__ __forceinline__ Unit unit_of(const FwdParams &p, int it) {
+  // (batch, head unit) in groups of kHeadGroup; in a group the late blocks of
+  // queries first, so that what runs at one time shares K and V in L2
+  const int grp = it / (kHeadGroup * p.per_head);
+  const int gsz = min(kHeadGroup, p.units - grp * kHeadGroup);
+  const int in_grp = it - grp * kHeadGroup * p.per_head;
+  const int unit = grp * kHeadGroup + in_grp % gsz;
+  const int per_b = p.pair_heads ? p.Hq / 2 : p.Hq;
+  Unit r;
+  r.m = p.per_head - 1 - in_grp / gsz;
+  r.b = unit / per_b;
+  r.u = unit - r.b * per_b;
+  r.n = tokens_of(p.lengths, r.b, p.T);
+  return r;
+}
+__device__ __forceinline__ Tile tile_of(const FwdParams &p, const Unit &w, int t) {
+  Tile x;
+  const int blk = p.pair_heads ? w.m : 2 * w.m + t;
+  x.h = p.pair_heads ? 2 * w.u + t : w.u;
+  x.q0 = blk * kBlk;
+  x.exists = blk < p.nqb;
+  x.hi = x.exists && x.q0 < w.n ? blk : -1;
+  x.lo = max(0, x.q0 - p.window + 1) / kBlk;
+  x.lead = min(p.sink_blocks, x.lo);
+  return x;
+}
+// The blocks of both tiles: tile 1 meets all that tile 0 meets in front of the
+// window's, and no window begins more than a block behind the other's.
+__device__ __forceinline__ Tile both_tiles(const Tile &a, const Tile &b) {
+  Tile x = a;
+  if (b.hi >= 0) {
+    x.hi = b.hi;            // where b is there, so is a, and not behind it
+    x.lo = min(a.lo, b.lo);
+    x.lead = min(a.lead, b.lead);
+  }
+  return x;
+}
+
+template <int kD>
+__global__ void __launch_bounds__(kThr, 1)
+    window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                      const __grid_constant__ FwdParams p) {
+  using M = FwdSmem<kD>;
+  constexpr int kHalves = kD / 64;
+  constexpr uint32_t kColO = 256;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  auto bar = [&](int i) -> uint32_t { return sb + M::kBar + i * 8; };
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + M::kAbort);
+  auto wt = [&](uint32_t br, uint32_t parity) -> bool {
+    if (*abort_flag) return false;
+    if (mbar_wait_bounded(br, parity, p.wait.limit_ns)) return true;
+    *abort_flag = 1;
+    report_timeout(p.wait.err, kSiteWinFwd, (br - sb - M::kBar) / 8);
+    return false;
+  };
+  // lane 0's outcome for the whole warp
+  auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return __shfl_sync(0xffffffffu, wt(br, parity), 0); };
+
+  if (tid == 0) {
+    for (int i = 0; i < M::kBars; ++i)
+      mbar_init(bar(i), i == M::kPFull || i == M::kPFull + 1 || i == M::kOEmpty || i == M::kOEmpty + 1 ? 128 : 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tc::tmem_alloc(sb + M::kTmem, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + M::kTmem);
+
+  if (warp < 4) {
+    regs_down<88>();
+    if (warp == 0) {
+      // ============================ loads ================================
+      if (lane == 0) {
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+      }
+      int r = 0, raw = 0, nq[2] = {0, 0};   // ring position, repaired blocks, Q tiles so far
+      bool ok = true;
+      for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+        const Unit w = unit_of(p, it);
+        const Tile t0 = tile_of(p, w, 0), t1 = tile_of(p, w, 1), all = both_tiles(t0, t1);
+        const int kvh = t0.h / p.G;
+        auto load = [&](const CUtensorMap *map, int n, bool value) -> bool {
+          const int s = r % M::kStages;
+          if (!wtw(bar(M::kKVEmpty + s), ((r / M::kStages) & 1) ^ 1)) return false;
+          const uint32_t dst = sb + M::kRing + s * M::kTile;
+          // rows of V behind the sequence's last token: cleared before the products see them
+          const int live = w.n - n * kBlk;
+          const bool repair = value && live < kBlk && w.n < p.T;
+          const uint32_t fb = bar(repair ? M::kRaw : M::kKVFull + s);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(fb, M::kTile);
+            for (int hx = 0; hx < kHalves; ++hx) tma_load_4d(dst + hx * 16384, map, hx * 64, kvh, n * kBlk, w.b, fb);
+          }
+          ++r;
+          if (repair) {
+            // the copy has landed before anything else happens to the slot, even where the wait gives up
+            if (!mbar_wait_bounded(fb, raw & 1, p.wait.limit_ns)) {
+              if (lane == 0) report_timeout(p.wait.err, kSiteWinFwd, M::kRaw);
+              *abort_flag = 1;
+              mbar_wait_bounded(fb, raw & 1, 2000000000ull);
+            }
+            ++raw;
+            unsigned char *at = smem + M::kRing + s * M::kTile;
+            for (int i = max(live, 0) * 8 + lane; i < kBlk * 8; i += 32)
+#pragma unroll
+              for (int hx = 0; hx < kHalves; ++hx) *reinterpret_cast<uint4 *>(at + hx * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(M::kKVFull + s));
+          }
+          return true;
+        };
+        for (int x = 0; ok && x < all.steps(); ++x) {
+          const int n = all.block(x);
+          ok = load(&tmK, n, false);
+          for (int t = 0; ok && x == 0 && t < 2; ++t) {
+            const Tile &tile = t == 0 ? t0 : t1;
+            if (tile.hi < 0) continue;
+            ok = wtw(bar(M::kQEmpty + t), (nq[t] & 1) ^ 1);
+            if (!ok) break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(bar(M::kQFull + t), M::kTile);
+              for (int hx = 0; hx < kHalves; ++hx)
+                tma_load_4d(sb + M::kQ + t * M::kTile + hx * 16384, &tmQ, hx * 64, tile.h, tile.q0, w.b, bar(M::kQFull + t));
+            }
+            ++nq[t];
+          }
+          if (ok) ok = load(&tmV, n, true);
+        }
+      }
+      // The last copy of every slot has landed before the block may end, whoever gives
+      // up and when (otherwise this finds every phase complete).
+      for (int i = max(r - M::kStages, 0); i < r; ++i)
+        mbar_wait_bounded(bar(M::kKVFull + i % M::kStages), (i / M::kStages) & 1, 2000000000ull);
+      for (int t = 0; t < 2; ++t)
+        if (nq[t] > 0) mbar_wait_bounded(bar(M::kQFull + t), (nq[t] - 1) & 1, 2000000000ull);
+    } else if (warp == 1) {
+      // ============================ products =============================
+      constexpr uint32_t id_s = tc::idesc_bf16_f32(128, 128, 0, 0);   // S = Q K^T, both K-major
+      constexpr uint32_t id_o = tc::idesc_bf16_f32(128, kD, 0, 1);    // O += P V, V MN-major
+      const uint64_t dQ = tc::sdesc_sw128(sb + M::kQ, 16, 1024);
+      const uint64_t dK = tc::sdesc_sw128(sb + M::kRing, 16, 1024);
+      const uint64_t dV = tc::sdesc_sw128(sb + M::kRing, 16384, 1024);
+      auto slot = [](int r) -> uint64_t { return static_cast<uint64_t>((r % M::kStages) * M::kTile) >> 4; };
+      int r = 0;                              // ring position of the next K block; its V block follows
+      int vr = 0;                             // ring position of the V block that pending PV products read
+      bool v_due = false;                     // its slot has not been handed back
+      bool pend[2] = {false, false}, opens[2] = {false, false}, closes[2] = {false, false};
+      int np[2] = {0, 0}, ni[2] = {0, 0}, nq[2] = {0, 0};   // P tiles, outputs and Q tiles so far
+      bool ok = may_wait(p.wait, abort_flag, kSiteWinFwd, M::kQFull);
+      // O_t += P_t V of the tile's last block
+      auto pv = [&](int t) -> bool {
+        if (!pend[t]) return true;
+        if (!wtw(bar(M::kKVFull + vr % M::kStages), (vr / M::kStages) & 1)) return false;
+        if (opens[t] && !wtw(bar(M::kOEmpty + t), (ni[t] & 1) ^ 1)) return false;
+        if (!wtw(bar(M::kPFull + t), np[t] & 1)) return false;
+        tc::fence_after_sync();
+        const uint64_t v = dV + slot(vr);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_bf16_ts_w(tmem + kColO + t * kD, tmem + t * 128 + kk * 8, v + ((kk * 2048) >> 4), id_o,
+                            !opens[t] || kk > 0);
+        ++np[t];
+        if (closes[t]) {
+          tc::commit_w(bar(M::kOFull + t));
+          ++ni[t];
+        }
+        pend[t] = opens[t] = false;
+        return true;
+      };
+      auto hand_back_v = [&]() {
+        if (v_due) tc::commit_w(bar(M::kKVEmpty + vr % M::kStages));
+        v_due = false;
+      };
+      for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+        const Unit w = unit_of(p, it);
+        const Tile tile[2] = {tile_of(p, w, 0), tile_of(p, w, 1)}, all = both_tiles(tile[0], tile[1]);
+        bool begun[2] = {false, false};
+        for (int x = 0; ok && x < all.steps(); ++x, r += 2) {
+          const int n = all.block(x);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            ok = ok && pv(t);
+            if (t == 1) hand_back_v();
+            if (!ok || !tile[t].meets(n)) continue;
+            if (!begun[t]) {
+              ok = wtw(bar(M::kQFull + t), nq[t] & 1);
+              ++nq[t];
+            }
+            ok = ok && wtw(bar(M::kKVFull + r % M::kStages), (r / M::kStages) & 1);
+            if (!ok) continue;
+            tc::fence_after_sync();
+            const uint64_t q = dQ + (static_cast<uint64_t>(t * M::kTile) >> 4), k = dK + slot(r);
+#pragma unroll
+            for (int kk = 0; kk < kD / 16; ++kk) {
+              const uint32_t off = static_cast<uint32_t>((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+              tc::mma_bf16_w(tmem + t * 128, q + off, k + off, id_s, kk > 0);
+            }
+            tc::commit_w(bar(M::kSFull + t));
+            pend[t] = true;
+            opens[t] = !begun[t];
+            begun[t] = true;
+            closes[t] = n == tile[t].hi;
+            if (closes[t]) tc::commit_w(bar(M::kQEmpty + t));
+          }
+          if (!ok) break;
+          tc::commit_w(bar(M::kKVEmpty + r % M::kStages));   // K
+          vr = r + 1;
+          v_due = true;
+        }
+      }
+      if (ok) ok = pv(0) && pv(1);
+      tc::commit_w(bar(M::kFinal));
+      mbar_wait_bounded(bar(M::kFinal), 0, 2000000000ull);   // every product has completed
+    }
+  } else {
+    // ============================ softmax ================================
+    regs_up<208>();
+    const int t = (warp >> 2) - 1;                      // tile
+    const int qd = warp & 3;                            // TMEM lane quarter
+    const int row = 32 * qd + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
+    const uint32_t tS = tmem + lanes + t * 128, tO = tmem + lanes + kColO + t * kD;
+    const float sl2 = p.scale * kLog2e;                 // scores in base-2 units
+    unsigned char *stage = smem + M::kOut + (t * 4 + qd) * 4096;
+    int ns = 0, no = 0;                                 // S tiles, outputs so far
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+      const Unit w = unit_of(p, it);
+      const Tile x = tile_of(p, w, t);
+      if (!x.exists) continue;
+      const int i = x.q0 + row;
+      float m = -INFINITY, l = 0.f;
+      const int steps = x.steps();
+      for (int step = 0; step < steps; ++step) {
+        const int n = x.block(step);
+        ok = wtw(bar(M::kSFull + t), ns & 1);
+        if (!ok) break;
+        ++ns;
+        tc::fence_after_sync();
+        float s[128];
+        ld_row(tS, s);
+        const int k0 = n * kBlk;
+        // every key of the block is visible to every query of the tile
+        const bool full = k0 + kBlk - 1 <= x.q0 && (k0 > x.q0 + kBlk - 1 - p.window || p.sinks - k0 >= kBlk);
+        float a = sl2;
+        if (!full) {
+          const int end = i - k0 + 1, first = end - p.window, stay = min(p.sinks - k0, end);
+#pragma unroll
+          for (int wd = 0; wd < 4; ++wd) {
+            const uint32_t see = (below(end, wd) & ~below(first, wd)) | below(stay, wd);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[32 * wd + c] = (see >> c) & 1u ? s[32 * wd + c] * sl2 : -INFINITY;
+          }
+          a = 1.f;
+        } else if (sl2 < 0.f) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c) s[c] *= sl2;
+          a = 1.f;
+        }
+        float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < 128; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[e] = fmaxf(fmaxf(top[e], s[c + e]), c + 4 + e < 128 ? s[c + 4 + e] : s[c + e]);
+        const float mb = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a;
+        const bool need = mb > m + kRescale;
+        if (__any_sync(0xffffffffu, need)) {
+          const float mn = need ? mb : m;
+          const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+          l *= f;
+          m = mn;
+          // O holds the blocks before this one: their PV came before this S
+          if (__any_sync(0xffffffffu, l != 0.f)) {
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 16) {           // 16 columns at a time: s[] stays live
+              uint32_t o[16];
+              tc::ld16_wait(tO + c, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tc::st16_wait(tO + c, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m;     // nothing seen yet: 2^(-inf - 0) = 0
+        const float2 a2 = make_float2(a, a), b2 = make_float2(-base, -base);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float2 e = fma2(make_float2(s[64 * half + c], s[64 * half + c + 1]), a2, b2);
+            const float2 v = make_float2(ex2(e.x), ex2(e.y));
+            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], v);
+            pk[c / 2] = pack_bf16(v.x, v.y);
+          }
+          tc::st32_async(tS + 32 * half, pk);
+        }
+        const float2 both = add2(sum[0], sum[1]);
+        l += both.x + both.y;
+        tc::wait_st();
+        tc::fence_before_sync();
+        mbar_arrive(bar(M::kPFull + t));
+      }
+      if (!ok) break;
+      // ---- O / l as bf16 rows through shared memory, lse = (m + log2 l) ln 2
+      const bool live = i < w.n;
+      const float inv = live ? 1.f / l : 0.f;
+      if (x.hi >= 0) {
+        ok = wtw(bar(M::kOFull + t), no & 1);
+        if (!ok) break;
+        ++no;
+        tc::fence_after_sync();
+      }
+#pragma unroll 1
+      for (int hx = 0; hx < kHalves; ++hx) {
+        if (lane == 0) bulk_wait_group_read0();          // the copy before has read the buffer
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 32) {
+          float o[32];
+          if (x.hi >= 0) tc::ld32_wait(tO + 64 * hx + c, o);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float *y = o + 8 * u;
+            uint4 v = make_uint4(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv),
+                                 pack_bf16(y[4] * inv, y[5] * inv), pack_bf16(y[6] * inv, y[7] * inv));
+            if (!live) v = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(stage + lane * 128 + (((c / 8 + u) ^ (lane & 7)) << 4)) = v;
+          }
+        }
+        if (hx == kHalves - 1 && x.hi >= 0) {
+          tc::fence_before_sync();
+          mbar_arrive(bar(M::kOEmpty + t));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && x.q0 + 32 * qd < p.T) {         // rows past T are not written
+          tma_store_4d(&tmO, sb + M::kOut + (t * 4 + qd) * 4096, hx * 64, x.h, x.q0 + 32 * qd, w.b);
+          bulk_commit_group();
+        }
+      }
+      if (i < p.T)
+        p.lse[(static_cast<size_t>(w.b) * p.Hq + x.h) * p.T + i] = live ? (m + __log2f(l)) * kLn2 : -INFINITY;
+    }
+    tc::wait_st();                                       // P on its way when this warp gave up
+    if (lane == 0) bulk_wait_group_read0();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int kD>
+cudaError_t launch(const WindowArgs &a, const FwdParams &p, int grid, cudaStream_t st, const char **why) {
+  CUtensorMap q, k, v, o;
+  if (!token_map(&q, a.q, a.Hq, a.T, a.B, kD, a.q_stride, kBlk, why) ||
+      !token_map(&k, a.k, a.Hkv, a.T, a.B, kD, a.k_stride, kBlk, why) ||
+      !token_map(&v, a.v, a.Hkv, a.T, a.B, kD, a.v_stride, kBlk, why) ||
+      !token_map(&o, a.o, a.Hq, a.T, a.B, kD, a.o_stride, 32, why))
+    return cudaErrorInvalidValue;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(window_fwd_kernel<kD>), FwdSmem<kD>::kBytes);
+  if (e != cudaSuccess) return e;
+  window_fwd_kernel<kD><<<grid, kThr, FwdSmem<kD>::kBytes, st>>>(q, k, v, o, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_window_fwd(const WindowArgs &a, const WaitCtl &w, cudaStream_t st, const char **why) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  FwdParams p;
+  p.lse = a.lse, p.lengths = a.lengths;
+  p.B = a.B, p.T = a.T, p.Hq = a.Hq, p.Hkv = a.Hkv, p.G = a.Hq / a.Hkv;
+  p.nqb = (a.T + kBlk - 1) / kBlk;
+  p.pair_heads = p.G % 2 == 0;
+  p.per_head = p.pair_heads ? p.nqb : (p.nqb + 1) / 2;
+  const long long units = static_cast<long long>(a.B) * (p.pair_heads ? a.Hq / 2 : a.Hq);
+  const long long items = units * p.per_head;
+  if (items > 0x7fffffffLL) {
+    *why = "grid too large";
+    return cudaErrorNotSupported;
+  }
+  p.units = static_cast<int>(units), p.items = static_cast<int>(items);
+  p.window = a.window, p.sinks = a.sinks;
+  p.sink_blocks = a.sinks / kBlk + (a.sinks % kBlk != 0);
+  p.scale = a.scale;
+  p.wait = w;
+  const int grid = static_cast<int>(std::min<long long>(items, sms));
+  return a.D == 64 ? launch<64>(a, p, grid, st, why) : launch<128>(a, p, grid, st, why);
+}
+
+}  // namespace abw
