@@ -1,0 +1,976 @@
+// Softmax attention over a sliding window with first tokens that stay visible,
+// backward:
+//   P_ij = exp(s_ij - lse_i) where key j is visible to query i, else 0,
+//   delta_i = dout_i . o_i,  dS = P (dout V^T - delta),
+//   dq = scale dS K,  dk = scale dS^T Q,  dv = P^T dout.
+//
+// Launches per call:
+//   1. prep : -delta and -lse log2(e) per query, padded to whole blocks of 128
+//             (padding: 0 and -inf, so P = 0 there)
+//   2. kv   : dK and dV of a block of 128 keys accumulate in TMEM over the blocks
+//             of 128 queries that meet it; each bf16 dS tile leaves for the workspace
+//   3. dq   : dQ of a block of 128 queries accumulates over its dS tiles and K blocks
+//   4. join : where a key block's queries were dealt to several CTAs, the sum of
+//             their parts in a fixed order
+// Only pairs of blocks that meet are visited: the window's, and for the first
+// tokens' blocks all queries behind them.  Those blocks have many times the others'
+// queries, so their pairs go to several CTAs (and all blocks' do while the grid
+// would not fill the GPU); parts are fp32 in the workspace.
+//
+// kv (persistent, one CTA per SM, 12 warps: 0 loads, 1 products, 3 copies out, 4-11
+// softmax): per pair of blocks the products go out in the order
+//   S(n) dP(n) | P(n) ready: dV(n) S(n+1) | dS(n) ready: dK(n) dP(n+1)
+// with S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q (M = 128 keys, P and
+// dS as A operands in TMEM over S and dP), so P is formed while dP runs, dS while
+// dV and the next S run.  n runs on across items: K and V of the next one arrive
+// while the last pair of this one is worked on.  Per slot of dO, once dV has read
+// it, the dS tile is staged there for its copy to the workspace, and behind an
+// item's last pair dV and dK as bf16 rows.
+// dq (persistent): dQ += dS K with A = dS^T tiles as they stand (queries contiguous)
+// and B = K, into two accumulators in turn.
+// Rows behind a sequence's last token are cleared in shared memory before a
+// product sees them, so nothing there (NaN included) is looked at.
+#include <algorithm>
+
+#include "window.cuh"
+
+namespace abw {
+namespace {
+
+using namespace win;
+
+constexpr int kThr = 384;
+constexpr int kTileBytes = kBlk * kBlk * 2;    // one dS^T tile: [2 query halves][128 keys][64 queries]
+
+// Which blocks meet, and where their dS tiles stand within a head.
+struct Grid {
+  int nb;        // blocks of 128 tokens
+  int wq;        // query blocks that a key block behind the first tokens' meets
+  int first;     // key blocks of first tokens
+  int window, sinks;
+  __host__ __device__ int queries(int kb) const { return kb < first || nb - kb < wq ? nb - kb : wq; }
+  // dS tiles in front of key block kb's
+  __host__ __device__ long long tile0(int kb) const {
+    const int a = kb < first ? kb : first;
+    long long n = static_cast<long long>(a) * nb - static_cast<long long>(a) * (a - 1) / 2;
+    if (kb <= first) return n;
+    int e = nb - wq > first ? nb - wq : first;   // from here on fewer than wq follow
+    if (e > kb) e = kb;
+    n += static_cast<long long>(e - first) * wq;
+    const long long k = kb - e;
+    return n + k * (nb - e) - k * (k - 1) / 2;
+  }
+  // a query block's key blocks: lead of first tokens, then lo .. m
+  __host__ __device__ int lo(int m) const {
+    const int x = m * kBlk - window + 1;
+    return x > 0 ? x / kBlk : 0;
+  }
+  __host__ __device__ int lead(int m) const { return first < lo(m) ? first : lo(m); }
+};
+
+Grid grid_of(int T, int window, int sinks) {
+  Grid g;
+  g.nb = (T + kBlk - 1) / kBlk;
+  g.window = std::min(window, T);
+  g.sinks = std::min(sinks, T);
+  g.wq = std::min(g.nb, 1 + (g.window + kBlk - 2) / kBlk);
+  g.first = (g.sinks + kBlk - 1) / kBlk;
+  return g;
+}
+
+struct BwdParams {
+  const __nv_bfloat16 *o, *dout;
+  const float *lse;
+  const int *lengths;
+  float *ndelta, *nlse2;          // [B][Hq][Tp]
+  __nv_bfloat16 *ds;              // [B][Hq][tiles]
+  float *parts;                   // [units][slots][2][128][D]: dV, dK
+  __nv_bfloat16 *dq, *dk, *dv;
+  int B, T, Tp, Hq, Hkv, G;
+  long long o_stride, dk_stride, dv_stride, tiles;
+  Grid g;
+  int first_parts, parts_each;    // CTAs per key block: first tokens', others
+  int per_unit, slots;            // items and part slots per (batch, KV head)
+  int items, dq_items;
+  float scale;
+  WaitCtl wait;
+};
+
+// ---------------------------------------------------------------------- prep
+// A row of o and dout per kD / 8 lanes, four rows each.
+constexpr int kPrepThr = 256, kPrepRows = 4;
+
+__device__ __forceinline__ float dot8(uint4 a, uint4 g) {
+  return bf16_lo(a.x) * bf16_lo(g.x) + bf16_hi(a.x) * bf16_hi(g.x) + bf16_lo(a.y) * bf16_lo(g.y) +
+         bf16_hi(a.y) * bf16_hi(g.y) + bf16_lo(a.z) * bf16_lo(g.z) + bf16_hi(a.z) * bf16_hi(g.z) +
+         bf16_lo(a.w) * bf16_lo(g.w) + bf16_hi(a.w) * bf16_hi(g.w);
+}
+
+template <int kD>
+__global__ void __launch_bounds__(kPrepThr) window_prep_kernel(const __grid_constant__ BwdParams p) {
+  constexpr int kL = kD / 8;   // lanes of a row
+  const long long gid = static_cast<long long>(blockIdx.x) * kPrepThr + threadIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const long long npad = static_cast<long long>(p.B) * p.Hq * (p.Tp - p.T);
+  if (gid < npad) {
+    const long long bh = gid / (p.Tp - p.T);
+    const size_t at = static_cast<size_t>(bh) * p.Tp + p.T + (gid - bh * (p.Tp - p.T));
+    p.ndelta[at] = 0.f;
+    p.nlse2[at] = -INFINITY;
+  }
+  const int sub = threadIdx.x % kL;
+  const long long rows = static_cast<long long>(p.B) * p.T * p.Hq, r0 = gid / kL * kPrepRows;
+  const long long tok0 = r0 / p.Hq;
+  int h = static_cast<int>(r0 - tok0 * p.Hq), b = static_cast<int>(tok0 / p.T), t = static_cast<int>(tok0 - static_cast<long long>(b) * p.T);
+  uint4 x[kPrepRows], y[kPrepRows];
+  size_t at[kPrepRows];
+  float l[kPrepRows];
+  int have = 0;
+#pragma unroll
+  for (int k = 0; k < kPrepRows; ++k) {
+    x[k] = y[k] = make_uint4(0, 0, 0, 0);
+    l[k] = INFINITY;
+    at[k] = 0;
+    if (r0 + k < rows) {
+      have = k + 1;
+      at[k] = (static_cast<size_t>(b) * p.Hq + h) * p.Tp + t;
+      if (t < tokens_of(p.lengths, b, p.T)) {
+        const long long tok = static_cast<long long>(b) * p.T + t;
+        x[k] = *reinterpret_cast<const uint4 *>(p.o + tok * p.o_stride + static_cast<size_t>(h) * kD + 8 * sub);
+        y[k] = *reinterpret_cast<const uint4 *>(p.dout + (tok * p.Hq + h) * kD + 8 * sub);
+        l[k] = p.lse[(static_cast<size_t>(b) * p.Hq + h) * p.T + t];
+      }
+      if (++h == p.Hq) {
+        h = 0;
+        if (++t == p.T) t = 0, ++b;
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kPrepRows; ++k) {
+    float v = dot8(x[k], y[k]);
+#pragma unroll
+    for (int d = kL / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);   // within the row's lanes
+    if (k < have && sub == 0) {
+      p.ndelta[at[k]] = -v;
+      p.nlse2[at[k]] = -l[k] * kLog2e;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------ kv
+template <int kD>
+struct KvSmem {
+  static constexpr int kIn = kBlk * kD * 2;                  // one block of Q, K, V or dO
+  static constexpr int kQs = 3, kDOs = 2;
+  static constexpr int kDOPitch = kTileBytes;                // a dO slot also stages a dS tile
+  static constexpr int kK = 0, kV = kIn, kQ = 2 * kIn, kDO = kQ + kQs * kIn;
+  static constexpr int kLse = kDO + kDOs * kDOPitch;         // 512 B per Q slot
+  static constexpr int kDelta = kLse + kQs * 512;            // 512 B per dO slot
+  static constexpr int kBar = kDelta + kDOs * 512;
+  enum {
+    kKFull = 0, kVFull, kKEmpty, kVEmpty, kQFull, kQEmpty = kQFull + kQs, kDOFull = kQEmpty + kQs,
+    kDOEmpty = kDOFull + kDOs, kSFull = kDOEmpty + kDOs, kDPFull, kPFull, kDSFull, kDVDone, kStaged,
+    kDVFinal = kStaged + 4, kDKFinal, kAccFree, kStageFree, kEpi, kRaw, kFinal, kBars
+  };
+  static constexpr int kTmem = kBar + kBars * 8, kAbort = kTmem + 4;
+  static constexpr int kBytes = kAbort + 4;                  // the kernel checks that the base is aligned
+  static_assert(kBytes <= 232448, "kv kernel shared memory");
+};
+
+struct KvItem {
+  int b, kvh, kb, part, nparts, n, qn;   // tokens, live query blocks per head
+  int it0, it1;                          // its pairs: (head, query block) = it / qn, it % qn
+  long long slot;                        // of its part (nparts > 1)
+};
+
+__device__ __forceinline__ KvItem kv_item(const BwdParams &p, int idx) {
+  KvItem r;
+  const int unit = idx / p.per_unit;
+  int rem = idx - unit * p.per_unit;
+  r.b = unit / p.Hkv;
+  r.kvh = unit - r.b * p.Hkv;
+  const int head = p.g.first * p.first_parts;
+  if (rem < head) {
+    r.kb = rem / p.first_parts;
+    r.part = rem - r.kb * p.first_parts;
+    r.nparts = p.first_parts;
+    r.slot = rem;
+  } else {
+    const int first_slots = p.first_parts > 1 ? head : 0;
+    rem -= head;
+    r.kb = rem / p.parts_each;
+    r.part = rem - r.kb * p.parts_each;
+    r.kb += p.g.first;
+    r.nparts = p.parts_each;
+    r.slot = first_slots + rem;
+  }
+  r.slot += static_cast<long long>(unit) * p.slots;
+  r.n = tokens_of(p.lengths, r.b, p.T);
+  const int live = (r.n + kBlk - 1) / kBlk;
+  r.qn = max(0, min(r.kb + p.g.queries(r.kb), live) - r.kb);
+  const int all = p.G * r.qn;
+  r.it0 = static_cast<int>(static_cast<long long>(all) * r.part / r.nparts);
+  r.it1 = static_cast<int>(static_cast<long long>(all) * (r.part + 1) / r.nparts);
+  return r;
+}
+
+// The pairs of a CTA's items, one after the other.
+struct KvStream {
+  KvItem w;
+  int idx, it;
+  bool valid;
+  __device__ __forceinline__ void find(const BwdParams &p) {
+    for (; idx < p.items; idx += gridDim.x) {
+      w = kv_item(p, idx);
+      if (w.it0 < w.it1) {
+        it = w.it0;
+        valid = true;
+        return;
+      }
+    }
+    valid = false;
+  }
+  __device__ __forceinline__ void begin(const BwdParams &p) {
+    idx = blockIdx.x;
+    find(p);
+  }
+  __device__ __forceinline__ void next(const BwdParams &p) {
+    if (++it < w.it1) return;
+    idx += gridDim.x;
+    find(p);
+  }
+  __device__ __forceinline__ bool opens() const { return it == w.it0; }
+  __device__ __forceinline__ bool closes() const { return it == w.it1 - 1; }
+  __device__ __forceinline__ int head(const BwdParams &p) const { return w.kvh * p.G + it / w.qn; }
+  __device__ __forceinline__ int block() const { return w.kb + it % w.qn; }
+};
+
+template <int kD>
+__global__ void __launch_bounds__(kThr, 1)
+    window_kv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
+                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ CUtensorMap tmdK, const __grid_constant__ CUtensorMap tmdV,
+                     const __grid_constant__ BwdParams p) {
+  using M = KvSmem<kD>;
+  constexpr int kHalves = kD / 64;
+  constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 256, kColDK = 256 + kD;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (sb & 1023) {
+    if (tid == 0) atomicOr(p.wait.err, kErrSmemAlign);
+    return;
+  }
+  auto bar = [&](int i) -> uint32_t { return sb + M::kBar + i * 8; };
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + M::kAbort);
+  auto wt = [&](uint32_t br, uint32_t parity) -> bool {
+    if (*abort_flag) return false;
+    if (mbar_wait_bounded(br, parity, p.wait.limit_ns)) return true;
+    *abort_flag = 1;
+    report_timeout(p.wait.err, kSiteWinKv, (br - sb - M::kBar) / 8);
+    return false;
+  };
+  // lane 0's outcome for the whole warp
+  auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return __shfl_sync(0xffffffffu, wt(br, parity), 0); };
+  // query half `half` of dO slot `slot` has been staged
+  auto staged_bar = [&](int slot, int half) -> uint32_t { return bar(M::kStaged + 2 * slot + half); };
+
+  if (tid == 0) {
+    for (int i = 0; i < M::kBars; ++i) {
+      int count = 1;
+      if (i == M::kPFull || i == M::kDSFull || i == M::kAccFree || i == M::kEpi) count = 256;   // every softmax thread
+      if (i >= M::kStaged && i < M::kStaged + 4) count = 128;
+      mbar_init(bar(i), count);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 2) tc::tmem_alloc(sb + M::kTmem, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + M::kTmem);
+
+  if (warp == 0) {
+    // ============================ loads ================================
+    if (lane == 0) {
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmQ);
+      prefetch_tensormap(&tmV);
+      prefetch_tensormap(&tmDO);
+    }
+    int raw = 0, nq = 0, nd = 0, nk = 0, nv = 0;   // copies so far: repaired, Q, dO, K, V
+    // one block of 128 rows (and 512 B of row statistics), rows from `live` on cleared
+    auto load = [&](const CUtensorMap *map, uint32_t off, int h, int row0, int b, int live, uint32_t full, uint32_t stat_off,
+                    const float *stat) {
+      const bool repair = live < kBlk && row0 + live < p.T;
+      const uint32_t fb = repair ? bar(M::kRaw) : full;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(fb, M::kIn + (stat ? 512 : 0));
+        for (int hx = 0; hx < kHalves; ++hx) tma_load_4d(sb + off + hx * 16384, map, hx * 64, h, row0, b, fb);
+        if (stat) bulk_load(sb + stat_off, stat, 512, fb);
+      }
+      if (!repair) return;
+      // the copy has landed before anything else happens to the slot, even where the wait gives up
+      if (!mbar_wait_bounded(fb, raw & 1, p.wait.limit_ns)) {
+        if (lane == 0) report_timeout(p.wait.err, kSiteWinKv, M::kRaw);
+        *abort_flag = 1;
+        mbar_wait_bounded(fb, raw & 1, 2000000000ull);
+      }
+      ++raw;
+      for (int i = max(live, 0) * 8 + lane; i < kBlk * 8; i += 32)
+#pragma unroll
+        for (int hx = 0; hx < kHalves; ++hx) *reinterpret_cast<uint4 *>(smem + off + hx * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full);
+    };
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the statistics come from prep
+    KvStream s;
+    for (s.begin(p); s.valid; s.next(p)) {
+      const KvItem &w = s.w;
+      const int h = s.head(p), q0 = s.block() * kBlk, k0 = w.kb * kBlk;
+      const int qs = nq % M::kQs, ds = nd % M::kDOs;
+      const size_t ro = (static_cast<size_t>(w.b) * p.Hq + h) * p.Tp + q0;
+      if (s.opens()) {
+        if (!wtw(bar(M::kKEmpty), (nk & 1) ^ 1)) break;
+        load(&tmK, M::kK, w.kvh, k0, w.b, w.n - k0, bar(M::kKFull), 0, nullptr);
+        ++nk;
+      }
+      if (!wtw(bar(M::kQEmpty + qs), ((nq / M::kQs) & 1) ^ 1)) break;
+      load(&tmQ, M::kQ + qs * M::kIn, h, q0, w.b, w.n - q0, bar(M::kQFull + qs), M::kLse + qs * 512, p.nlse2 + ro);
+      ++nq;
+      if (s.opens()) {
+        if (!wtw(bar(M::kVEmpty), (nv & 1) ^ 1)) break;
+        load(&tmV, M::kV, w.kvh, k0, w.b, w.n - k0, bar(M::kVFull), 0, nullptr);
+        ++nv;
+      }
+      if (!wtw(bar(M::kDOEmpty + ds), ((nd / M::kDOs) & 1) ^ 1)) break;
+      load(&tmDO, M::kDO + ds * M::kDOPitch, h, q0, w.b, w.n - q0, bar(M::kDOFull + ds), M::kDelta + ds * 512, p.ndelta + ro);
+      ++nd;
+    }
+    // The last copy of every slot has landed before the CTA may end, whoever gives up
+    // and when (otherwise this finds every phase complete).
+    for (int i = max(nq - M::kQs, 0); i < nq; ++i) mbar_wait_bounded(bar(M::kQFull + i % M::kQs), (i / M::kQs) & 1, 2000000000ull);
+    for (int i = max(nd - M::kDOs, 0); i < nd; ++i) mbar_wait_bounded(bar(M::kDOFull + i % M::kDOs), (i / M::kDOs) & 1, 2000000000ull);
+    if (nk > 0) mbar_wait_bounded(bar(M::kKFull), (nk - 1) & 1, 2000000000ull);
+    if (nv > 0) mbar_wait_bounded(bar(M::kVFull), (nv - 1) & 1, 2000000000ull);
+  } else if (warp == 1) {
+    // ============================ products =============================
+    constexpr uint32_t id_sdp = tc::idesc_bf16_f32(128, 128, 0, 0);   // S^T, dP^T
+    constexpr uint32_t id_kv = tc::idesc_bf16_f32(128, kD, 0, 1);     // dV, dK (A from TMEM)
+    const uint64_t dK = tc::sdesc_sw128(sb + M::kK, 16, 1024), dV = tc::sdesc_sw128(sb + M::kV, 16, 1024);
+    const uint64_t dQk = tc::sdesc_sw128(sb + M::kQ, 16, 1024);          // Q as K-major B of S^T
+    const uint64_t dOk = tc::sdesc_sw128(sb + M::kDO, 16, 1024);         // dO as K-major B of dP^T
+    const uint64_t dQm = tc::sdesc_sw128(sb + M::kQ, 16384, 1024);       // Q as MN-major B of dK
+    const uint64_t dOm = tc::sdesc_sw128(sb + M::kDO, 16384, 1024);      // dO as MN-major B of dV
+    auto qoff = [](int n) -> uint64_t { return static_cast<uint64_t>((n % M::kQs) * M::kIn) >> 4; };
+    auto dooff = [](int n) -> uint64_t { return static_cast<uint64_t>((n % M::kDOs) * M::kDOPitch) >> 4; };
+    auto kstep = [](int kk) -> uint32_t { return static_cast<uint32_t>((kk >> 2) * 16384 + (kk & 3) * 32) >> 4; };
+    int items = 0, nk = 0, nv = 0;          // items whose outputs were begun; K and V blocks waited for
+    auto issue_s = [&](const KvStream &s, int n) -> bool {
+      if (s.opens() && !wtw(bar(M::kKFull), nk++ & 1)) return false;
+      if (!wtw(bar(M::kQFull + n % M::kQs), (n / M::kQs) & 1)) return false;
+      tc::fence_after_sync();
+      const uint64_t so = qoff(n);
+#pragma unroll
+      for (int kk = 0; kk < kD / 16; ++kk) tc::mma_bf16_w(tmem + kColS, dK + kstep(kk), dQk + so + kstep(kk), id_sdp, kk > 0);
+      tc::commit_w(bar(M::kSFull));
+      if (s.closes()) tc::commit_w(bar(M::kKEmpty));
+      return true;
+    };
+    auto issue_dp = [&](const KvStream &s, int n) -> bool {
+      if (s.opens() && !wtw(bar(M::kVFull), nv++ & 1)) return false;
+      if (!wtw(bar(M::kDOFull + n % M::kDOs), (n / M::kDOs) & 1)) return false;
+      tc::fence_after_sync();
+      const uint64_t so = dooff(n);
+#pragma unroll
+      for (int kk = 0; kk < kD / 16; ++kk) tc::mma_bf16_w(tmem + kColDP, dV + kstep(kk), dOk + so + kstep(kk), id_sdp, kk > 0);
+      tc::commit_w(bar(M::kDPFull));
+      if (s.closes()) tc::commit_w(bar(M::kVEmpty));
+      return true;
+    };
+    KvStream cur;
+    cur.begin(p);
+    bool ok = may_wait(p.wait, abort_flag, kSiteWinKv, M::kKFull) && (!cur.valid || (issue_s(cur, 0) && issue_dp(cur, 0)));
+    for (int n = 0; ok && cur.valid; ++n) {
+      KvStream nxt = cur;
+      nxt.next(p);
+      const bool opens = cur.opens();
+      if (!wtw(bar(M::kPFull), n & 1)) break;
+      // the accumulators of the item before have been read
+      if (opens && !wtw(bar(M::kAccFree), (items++ & 1) ^ 1)) break;
+      tc::fence_after_sync();
+      const uint64_t dso = dooff(n), qso = qoff(n);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)   // dV += P^T dO
+        tc::mma_bf16_ts_w(tmem + kColDV, tmem + kColS + (kk >> 1) * 32 + (kk & 1) * 8, dOm + dso + ((kk * 2048) >> 4), id_kv,
+                          !opens || kk > 0);
+      tc::commit_w(bar(M::kDVDone));
+      if (cur.closes()) tc::commit_w(bar(M::kDVFinal));
+      if (nxt.valid && !issue_s(nxt, n + 1)) break;
+      if (!wtw(bar(M::kDSFull), n & 1)) break;
+      tc::fence_after_sync();
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)   // dK += dS^T Q
+        tc::mma_bf16_ts_w(tmem + kColDK, tmem + kColDP + (kk >> 1) * 32 + (kk & 1) * 8, dQm + qso + ((kk * 2048) >> 4), id_kv,
+                          !opens || kk > 0);
+      tc::commit_w(bar(M::kQEmpty + n % M::kQs));
+      if (cur.closes()) tc::commit_w(bar(M::kDKFinal));
+      if (nxt.valid && !issue_dp(nxt, n + 1)) break;
+      cur = nxt;
+    }
+    tc::commit_w(bar(M::kFinal));
+    mbar_wait_bounded(bar(M::kFinal), 0, 2000000000ull);   // every product has completed
+  } else if (warp == 3) {
+    // ============================ copies out ===========================
+    if (lane == 0) {
+      KvStream s;
+      int n = 0, free_ = 0, epi = 0;
+      bool ok = true;
+      for (s.begin(p); ok && s.valid; s.next(p), ++n) {
+        const KvItem &w = s.w;
+        const int slot = n % M::kDOs, qi = s.block() - w.kb;
+        const uint32_t at = sb + M::kDO + slot * M::kDOPitch;
+        unsigned char *dst = reinterpret_cast<unsigned char *>(p.ds) +
+                             ((static_cast<long long>(w.b) * p.Hq + s.head(p)) * p.tiles + p.g.tile0(w.kb) + qi) * kTileBytes;
+        for (int hf = 0; hf < 2 && ok; ++hf) {
+          ok = wt(staged_bar(slot, hf), (n / M::kDOs) & 1);
+          if (ok) bulk_store(dst + hf * (kTileBytes / 2), at + hf * (kTileBytes / 2), kTileBytes / 2);
+        }
+        bulk_commit_group();
+        if (!ok) break;
+        bulk_wait_group_read0();
+        if (s.closes() && w.nparts == 1) {
+          // dV, then dK, as bf16 rows in this slot
+          for (int x = 0; x < 2 && ok; ++x) {
+            mbar_arrive(bar(M::kStageFree));
+            ++free_;
+            ok = wt(bar(M::kEpi), epi++ & 1);
+            if (!ok) break;
+            for (int hx = 0; hx < kHalves; ++hx)
+              tma_store_4d(x == 0 ? &tmdV : &tmdK, at + hx * 16384, hx * 64, w.kvh, w.kb * kBlk, w.b);
+            bulk_commit_group();
+            bulk_wait_group_read0();
+          }
+        }
+        if (ok) mbar_arrive(bar(M::kDOEmpty + slot));
+      }
+      bulk_wait_group0();
+    }
+  } else if (warp >= 4) {
+    // ============================ softmax ================================
+    // Warp w: keys 32 (w % 4) .. of the block (thread = key), half (w - 4) / 4 of its
+    // 128 queries.
+    const int qd = warp & 3, ch = (warp - 4) >> 2;
+    const int j = 32 * qd + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
+    const float sl2 = p.scale * kLog2e;
+    const float2 sl22 = make_float2(sl2, sl2);
+    const uint32_t tS = tmem + lanes + kColS + 64 * ch, tD = tmem + lanes + kColDP + 64 * ch;
+    KvStream s;
+    int n = 0, items = 0, epi = 0;
+    bool ok = true;
+    for (s.begin(p); ok && s.valid; s.next(p), ++n) {
+      const KvItem &w = s.w;
+      const int k0 = w.kb * kBlk, key = k0 + j, qblk = s.block() * kBlk, q0 = qblk + 64 * ch;
+      const float *nl = reinterpret_cast<const float *>(smem + M::kLse + (n % M::kQs) * 512) + 64 * ch;
+      const float *nd = reinterpret_cast<const float *>(smem + M::kDelta + (n % M::kDOs) * 512) + 64 * ch;
+      // ---- P = 2^(S scale log2 e - lse log2 e)
+      float2 P[32];
+      uint32_t pk[32];
+      ok = wtw(bar(M::kSFull), n & 1);
+      if (!ok) break;
+      tc::fence_after_sync();
+      {
+        float(&lo)[32] = *reinterpret_cast<float(*)[32]>(&P[0]);
+        float(&hi)[32] = *reinterpret_cast<float(*)[32]>(&P[16]);
+        tc::ld32x2_wait(tS, tS + 32, lo, hi);
+      }
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        const float4 l4 = *reinterpret_cast<const float4 *>(nl + 2 * e);
+        const float2 x = fma2(P[e], sl22, make_float2(l4.x, l4.y)), y = fma2(P[e + 1], sl22, make_float2(l4.z, l4.w));
+        P[e] = make_float2(ex2(x.x), ex2(x.y));
+        P[e + 1] = make_float2(ex2(y.x), ex2(y.y));
+      }
+      // every query of the block sees every key of it
+      const bool full = qblk > k0 && (qblk + kBlk - 1 - k0 < p.g.window || p.g.sinks - k0 >= kBlk);
+      if (!full) {
+        const int first = key - q0, end = key < p.g.sinks ? 64 : first + p.g.window;   // of this half's queries
+        uint32_t see[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int a = min(max(first - 32 * x, 0), 32), z = min(max(end - 32 * x, 0), 32);
+          see[x] = (z == 32 ? 0xffffffffu : (1u << z) - 1u) & ~(a == 32 ? 0xffffffffu : (1u << a) - 1u);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          P[e].x = (see[e >> 4] >> (2 * e & 31)) & 1u ? P[e].x : 0.f;
+          P[e].y = (see[e >> 4] >> ((2 * e + 1) & 31)) & 1u ? P[e].y : 0.f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(P[e].x, P[e].y);
+      {
+        const uint32_t(&c0)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&pk[0]);
+        const uint32_t(&c1)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&pk[8]);
+        const uint32_t(&c2)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&pk[16]);
+        const uint32_t(&c3)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&pk[24]);
+        tc::st8x2_async(tS, c0, tS + 8, c1);
+        tc::st8x2_async(tS + 32, c2, tS + 40, c3);
+      }
+      tc::wait_st();
+      tc::fence_before_sync();
+      mbar_arrive(bar(M::kPFull));
+      // ---- dS = P (dP - delta), over dP and for the workspace
+      ok = wtw(bar(M::kDPFull), n & 1);
+      if (!ok) break;
+      tc::fence_after_sync();
+      uint4 U[8];   // this key's dS^T as eight 16-byte units of 8 queries
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float d[32];
+        tc::ld32_wait(tD + 32 * half, d);
+        uint32_t dk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 d4 = *reinterpret_cast<const float4 *>(nd + 32 * half + e);
+          const float2 x = add2(make_float2(d[e], d[e + 1]), make_float2(d4.x, d4.y));
+          const float2 y = add2(make_float2(d[e + 2], d[e + 3]), make_float2(d4.z, d4.w));
+          const float2 a = P[16 * half + e / 2], c = P[16 * half + e / 2 + 1];
+          dk[e / 2] = pack_bf16(a.x * x.x, a.y * x.y);
+          dk[e / 2 + 1] = pack_bf16(c.x * y.x, c.y * y.y);
+        }
+        {
+          const uint32_t(&c0)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&dk[0]);
+          const uint32_t(&c1)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&dk[8]);
+          tc::st8x2_async(tD + 32 * half, c0, tD + 32 * half + 8, c1);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) U[4 * half + u] = make_uint4(dk[4 * u], dk[4 * u + 1], dk[4 * u + 2], dk[4 * u + 3]);
+      }
+      tc::wait_st();
+      tc::fence_before_sync();
+      mbar_arrive(bar(M::kDSFull));
+      // once dV has read dO, its slot stages the dS tile
+      ok = wtw(bar(M::kDVDone), n & 1);
+      if (!ok) break;
+      tc::fence_after_sync();
+      unsigned char *slot = smem + M::kDO + (n % M::kDOs) * M::kDOPitch;
+      {
+        unsigned char *stg = slot + ch * (kTileBytes / 2) + j * 128;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4 *>(stg + ((u ^ (lane & 7)) << 4)) = U[u];
+        fence_proxy_async_smem();
+        mbar_arrive(staged_bar(n % M::kDOs, ch));
+      }
+      if (!s.closes()) continue;
+      // ---- the item's dV and dK (scaled): thread (key, half ch of the components)
+      const bool whole = w.nparts == 1;
+      float *part = whole ? nullptr : p.parts + (w.slot * 2 * kBlk + j) * kD + ch * (kD / 2);
+#pragma unroll 1
+      for (int x = 0; x < 2 && ok; ++x) {
+        ok = wtw(bar(x == 0 ? M::kDVFinal : M::kDKFinal), items & 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        float v[kD / 2];
+#pragma unroll
+        for (int c = 0; c < kD / 2; c += 32) {
+          float(&y)[32] = *reinterpret_cast<float(*)[32]>(&v[c]);
+          tc::ld32_wait(tmem + lanes + (x == 0 ? kColDV : kColDK) + ch * (kD / 2) + c, y);
+        }
+        if (x == 1) {
+          tc::fence_before_sync();
+          mbar_arrive(bar(M::kAccFree));
+        }
+        const float f = x == 0 ? 1.f : p.scale;
+        if (whole) {
+          ok = wtw(bar(M::kStageFree), epi & 1);
+          if (!ok) break;
+          ++epi;
+#pragma unroll
+          for (int u = 0; u < kD / 16; ++u) {
+            const int unit = ch * (kD / 16) + u;   // of the row's kD / 8 units
+            const float *y = v + 8 * u;
+            *reinterpret_cast<uint4 *>(slot + (unit >> 3) * 16384 + j * 128 + (((unit & 7) ^ (j & 7)) << 4)) =
+                make_uint4(pack_bf16(y[0] * f, y[1] * f), pack_bf16(y[2] * f, y[3] * f), pack_bf16(y[4] * f, y[5] * f),
+                           pack_bf16(y[6] * f, y[7] * f));
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(bar(M::kEpi));
+        } else {
+          float4 *dst = reinterpret_cast<float4 *>(part + static_cast<size_t>(x) * kBlk * kD);
+#pragma unroll
+          for (int u = 0; u < kD / 8; ++u) dst[u] = make_float4(v[4 * u] * f, v[4 * u + 1] * f, v[4 * u + 2] * f, v[4 * u + 3] * f);
+        }
+      }
+      ++items;
+    }
+    tc::wait_st();
+    // key blocks that no query meets (behind the sequence): 0
+    for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
+      const KvItem w = kv_item(p, idx);
+      if (w.it0 < w.it1 || w.nparts > 1 || w.kb * kBlk + j >= p.T) continue;
+      const long long tok = static_cast<long long>(w.b) * p.T + w.kb * kBlk + j;
+      const size_t c = static_cast<size_t>(w.kvh) * kD + ch * (kD / 2);
+#pragma unroll
+      for (int u = 0; u < kD / 16; ++u) {
+        reinterpret_cast<uint4 *>(p.dv + tok * p.dv_stride + c)[u] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4 *>(p.dk + tok * p.dk_stride + c)[u] = make_uint4(0, 0, 0, 0);
+      }
+    }
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 2) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------- join
+// Parts of the key blocks that went to several CTAs, summed in their order: a
+// block per (batch, KV head, key block) and 32 keys.
+constexpr int kJoinThr = 256;
+
+template <int kD>
+__global__ void __launch_bounds__(kJoinThr) window_join_kernel(const __grid_constant__ BwdParams p, int blocks) {
+  const int nk = p.parts_each > 1 ? p.g.nb : p.g.first;   // key blocks with parts
+  const int quarter = blockIdx.x & 3;
+  const int unit = (blockIdx.x >> 2) / nk, kb = (blockIdx.x >> 2) - unit * nk;
+  if (static_cast<int>(blockIdx.x) >= blocks) return;
+  const int idx = unit * p.per_unit + (kb < p.g.first ? kb * p.first_parts : p.g.first * p.first_parts + (kb - p.g.first) * p.parts_each);
+  const KvItem w = kv_item(p, idx);
+  const int all = p.G * w.qn;
+  for (int e = threadIdx.x; e < 2 * 32 * kD / 4; e += kJoinThr) {
+    const int x = e / (32 * kD / 4), r = 32 * quarter + e / (kD / 4) % 32, c = e % (kD / 4) * 4;
+    const int tok = kb * kBlk + r;
+    if (tok >= p.T) continue;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < w.nparts; ++i) {
+      const int a = static_cast<int>(static_cast<long long>(all) * i / w.nparts), z = static_cast<int>(static_cast<long long>(all) * (i + 1) / w.nparts);
+      if (a == z) continue;
+      const float4 v = *reinterpret_cast<const float4 *>(p.parts + (((w.slot + i) * 2 + x) * kBlk + r) * kD + c);
+      s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+    }
+    const long long at = static_cast<long long>(w.b) * p.T + tok;
+    __nv_bfloat16 *dst = (x == 0 ? p.dv + at * p.dv_stride : p.dk + at * p.dk_stride) + static_cast<size_t>(w.kvh) * kD + c;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+  }
+}
+
+// ------------------------------------------------------------------------ dq
+template <int kD>
+struct DqSmem {
+  static constexpr int kK = kBlk * kD * 2, kStage = kK + kTileBytes, kStages = 3;
+  static constexpr int kOut = kStages * kStage;              // 4 KB per epilogue warp
+  static constexpr int kBar = kOut + 8 * 4096;
+  enum { kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + 2, kRaw = kAccEmpty + 2, kFinal, kBars };
+  static constexpr int kTmem = kBar + kBars * 8, kAbort = kTmem + 4;
+  static constexpr int kBytes = kAbort + 4 + 1024;
+  static_assert(kBytes <= 232448, "dq kernel shared memory");
+};
+
+struct DqItem {
+  int b, h, m, n, lo, lead, steps;
+  __device__ __forceinline__ int block(int x) const { return x < lead ? x : lo + (x - lead); }
+};
+__device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
+  DqItem r;
+  const int hb = idx / p.g.nb;
+  r.m = p.g.nb - 1 - (idx - hb * p.g.nb);
+  r.b = hb / p.Hq;
+  r.h = hb - r.b * p.Hq;
+  r.n = tokens_of(p.lengths, r.b, p.T);
+  r.lo = p.g.lo(r.m);
+  r.lead = p.g.lead(r.m);
+  r.steps = r.m * kBlk < r.n ? r.lead + r.m - r.lo + 1 : 0;
+  return r;
+}
+
+template <int kD>
+__global__ void __launch_bounds__(kThr, 1)
+    window_dq_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmdQ,
+                     const __grid_constant__ BwdParams p) {
+  using M = DqSmem<kD>;
+  constexpr int kHalves = kD / 64;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto bar = [&](int i) -> uint32_t { return sb + M::kBar + i * 8; };
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + M::kAbort);
+  auto wt = [&](uint32_t br, uint32_t parity) -> bool {
+    if (*abort_flag) return false;
+    if (mbar_wait_bounded(br, parity, p.wait.limit_ns)) return true;
+    *abort_flag = 1;
+    report_timeout(p.wait.err, kSiteWinDq, (br - sb - M::kBar) / 8);
+    return false;
+  };
+  auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return __shfl_sync(0xffffffffu, wt(br, parity), 0); };
+
+  if (tid == 0) {
+    for (int i = 0; i < M::kBars; ++i) mbar_init(bar(i), i == M::kAccEmpty || i == M::kAccEmpty + 1 ? 128 * kHalves : 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 2) tc::tmem_alloc(sb + M::kTmem, 2 * kD);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + M::kTmem);
+
+  if (warp == 0) {
+    // ============================ loads ================================
+    if (lane == 0) prefetch_tensormap(&tmK);
+    const uint64_t keep = l2_evict_last(), stream = l2_evict_first();
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the dS tiles come from the kv kernel
+    int g = 0, raw = 0;
+    bool ok = true;
+    for (int idx = blockIdx.x; ok && idx < p.dq_items; idx += gridDim.x) {
+      const DqItem w = dq_item(p, idx);
+      const unsigned char *tiles = reinterpret_cast<const unsigned char *>(p.ds) +
+                                   (static_cast<long long>(w.b) * p.Hq + w.h) * p.tiles * kTileBytes;
+      for (int x = 0; x < w.steps; ++x, ++g) {
+        const int s = g % M::kStages, kb = w.block(x);
+        ok = wtw(bar(M::kEmpty + s), ((g / M::kStages) & 1) ^ 1);
+        if (!ok) break;
+        const uint32_t st = sb + s * M::kStage;
+        const int live = w.n - kb * kBlk;
+        const bool repair = live < kBlk && w.n < p.T;      // rows of K behind the last token: cleared
+        const uint32_t fb = bar(repair ? M::kRaw : M::kFull + s);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(fb, M::kStage);
+          for (int hx = 0; hx < kHalves; ++hx)
+            tma_load_4d_hint(st + hx * 16384, &tmK, hx * 64, w.h / p.G, kb * kBlk, w.b, fb, keep);
+          bulk_load_hint(st + M::kK, tiles + (p.g.tile0(kb) + (w.m - kb)) * kTileBytes, kTileBytes, fb, stream);
+        }
+        if (repair) {
+          if (!mbar_wait_bounded(fb, raw & 1, p.wait.limit_ns)) {
+            if (lane == 0) report_timeout(p.wait.err, kSiteWinDq, M::kRaw);
+            *abort_flag = 1;
+            mbar_wait_bounded(fb, raw & 1, 2000000000ull);
+          }
+          ++raw;
+          for (int i = max(live, 0) * 8 + lane; i < kBlk * 8; i += 32)
+#pragma unroll
+            for (int hx = 0; hx < kHalves; ++hx)
+              *reinterpret_cast<uint4 *>(smem + s * M::kStage + hx * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(M::kFull + s));
+        }
+      }
+    }
+    // the last copy of every slot has landed before the CTA may end
+    for (int i = max(g - M::kStages, 0); i < g; ++i)
+      mbar_wait_bounded(bar(M::kFull + i % M::kStages), (i / M::kStages) & 1, 2000000000ull);
+  } else if (warp == 1) {
+    // ============================ products =============================
+    constexpr uint32_t id = tc::idesc_bf16_f32(128, kD, 1, 1);              // dQ += dS K, both MN-major
+    const uint64_t dS = tc::sdesc_sw128(sb + M::kK, kTileBytes / 2, 1024);  // queries contiguous
+    const uint64_t dK = tc::sdesc_sw128(sb, 16384, 1024);
+    int g = 0, j = 0;
+    bool ok = may_wait(p.wait, abort_flag, kSiteWinDq, M::kFull);
+    for (int idx = blockIdx.x; ok && idx < p.dq_items; idx += gridDim.x) {
+      const DqItem w = dq_item(p, idx);
+      if (w.steps == 0) continue;
+      const int a = j & 1;
+      if (!wtw(bar(M::kAccEmpty + a), ((j >> 1) & 1) ^ 1)) break;
+      tc::fence_after_sync();
+      for (int x = 0; x < w.steps; ++x, ++g) {
+        const int s = g % M::kStages;
+        ok = wtw(bar(M::kFull + s), (g / M::kStages) & 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint64_t so = static_cast<uint64_t>(s * M::kStage) >> 4;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_bf16_w(tmem + a * kD, dS + so + ((kk * 2048) >> 4), dK + so + ((kk * 2048) >> 4), id, x > 0 || kk > 0);
+        tc::commit_w(bar(M::kEmpty + s));
+      }
+      if (ok) tc::commit_w(bar(M::kAccFull + a));
+      ++j;
+    }
+    tc::commit_w(bar(M::kFinal));
+    mbar_wait_bounded(bar(M::kFinal), 0, 2000000000ull);   // every product has completed
+  } else if (warp >= 4 && warp < 4 + 4 * kHalves) {
+    // ============================ epilogue ================================
+    // Warp w: queries 32 (w % 4) .. of the block, 64 components
+    const int qd = warp & 3, hx = (warp - 4) >> 2;
+    const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
+    unsigned char *stage = smem + M::kOut + (warp - 4) * 4096;
+    int j = 0;
+    for (int idx = blockIdx.x; idx < p.dq_items; idx += gridDim.x) {
+      const DqItem w = dq_item(p, idx);
+      const int a = j & 1, row = w.m * kBlk + 32 * qd + lane;
+      if (w.steps > 0) {
+        if (!wtw(bar(M::kAccFull + a), (j >> 1) & 1)) break;
+        tc::fence_after_sync();
+        ++j;
+      }
+      float v[2][32];
+      if (w.steps > 0) {
+        tc::ld32x2_wait(tmem + lanes + a * kD + 64 * hx, tmem + lanes + a * kD + 64 * hx + 32, v[0], v[1]);
+        tc::fence_before_sync();
+        mbar_arrive(bar(M::kAccEmpty + a));
+      }
+      if (lane == 0) bulk_wait_group_read0();              // the copy before has read the buffer
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float *y = &v[u >> 2][8 * (u & 3)];
+        uint4 x = make_uint4(pack_bf16(y[0] * p.scale, y[1] * p.scale), pack_bf16(y[2] * p.scale, y[3] * p.scale),
+                             pack_bf16(y[4] * p.scale, y[5] * p.scale), pack_bf16(y[6] * p.scale, y[7] * p.scale));
+        if (row >= w.n) x = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = x;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && w.m * kBlk + 32 * qd < p.T) {
+        tma_store_4d(&tmdQ, sb + M::kOut + (warp - 4) * 4096, hx * 64, w.h, w.m * kBlk + 32 * qd, w.b);
+        bulk_commit_group();
+      }
+    }
+    if (lane == 0) bulk_wait_group_read0();
+  }
+  __syncwarp();
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 2) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 2 * kD);
+  }
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Sizes that the launch and the workspace share.
+struct BwdSizes {
+  Grid g;
+  int Tp, first_parts, parts_each, per_unit, slots;
+  long long tiles;
+  size_t stats, ds, parts;   // bytes
+};
+
+BwdSizes bwd_sizes(int B, int T, int Hq, int Hkv, int D, int window, int sinks) {
+  BwdSizes s;
+  s.g = grid_of(T, window, sinks);
+  const Grid &g = s.g;
+  const int G = Hq / Hkv;
+  const long long units = static_cast<long long>(B) * Hkv;
+  s.Tp = g.nb * kBlk;
+  s.tiles = g.tile0(g.nb);
+  // Pairs per CTA: a key block's own while there are items enough to fill 152 SMs
+  // twice, else an equal share of all pairs, at least 2.  The first tokens' blocks
+  // have more pairs and are cut to about that.
+  const long long each = static_cast<long long>(G) * std::min(g.nb, g.wq), total = units * G * s.tiles;
+  long long most = std::max(2LL, std::min(each, (total + 151) / 152));
+  if (units * g.nb >= 304) most = each;
+  s.parts_each = static_cast<int>((each + most - 1) / most);
+  s.first_parts = static_cast<int>((static_cast<long long>(G) * g.nb + most - 1) / most);
+  s.per_unit = g.first * s.first_parts + (g.nb - g.first) * s.parts_each;
+  s.slots = (s.first_parts > 1 ? g.first * s.first_parts : 0) + (s.parts_each > 1 ? (g.nb - g.first) * s.parts_each : 0);
+  s.stats = up256(static_cast<size_t>(B) * Hq * s.Tp * 4);
+  s.ds = static_cast<size_t>(B) * Hq * s.tiles * kTileBytes;
+  s.parts = static_cast<size_t>(units) * s.slots * 2 * kBlk * D * 4;
+  return s;
+}
+
+template <int kD>
+cudaError_t launch(const WindowArgs &a, BwdParams &p, const BwdSizes &s, int sms, cudaStream_t st, const char **why) {
+  CUtensorMap q, dout, k, v, dq, dk, dv;
+  const long long qn = static_cast<long long>(a.Hq) * kD;
+  if (!token_map(&q, a.q, a.Hq, a.T, a.B, kD, a.q_stride, kBlk, why) ||
+      !token_map(&dout, a.dout, a.Hq, a.T, a.B, kD, qn, kBlk, why) ||
+      !token_map(&k, a.k, a.Hkv, a.T, a.B, kD, a.k_stride, kBlk, why) ||
+      !token_map(&v, a.v, a.Hkv, a.T, a.B, kD, a.v_stride, kBlk, why) ||
+      !token_map(&dq, a.dq, a.Hq, a.T, a.B, kD, a.dq_stride, 32, why) ||
+      !token_map(&dk, a.dk, a.Hkv, a.T, a.B, kD, a.dk_stride, kBlk, why) ||
+      !token_map(&dv, a.dv, a.Hkv, a.T, a.B, kD, a.dv_stride, kBlk, why))
+    return cudaErrorInvalidValue;
+  const void *kv_fn = reinterpret_cast<const void *>(window_kv_kernel<kD>);
+  const void *dq_fn = reinterpret_cast<const void *>(window_dq_kernel<kD>);
+  cudaError_t e = ensure_dynamic_smem(kv_fn, KvSmem<kD>::kBytes);
+  if (e == cudaSuccess) e = ensure_dynamic_smem(dq_fn, DqSmem<kD>::kBytes);
+  if (e != cudaSuccess) return e;
+  const long long rows = static_cast<long long>(a.B) * a.T * a.Hq;
+  const long long threads = std::max((rows + kPrepRows - 1) / kPrepRows * (kD / 8), static_cast<long long>(a.B) * a.Hq * (s.Tp - a.T));
+  const long long blocks = (threads + kPrepThr - 1) / kPrepThr;
+  if (blocks > 0x7fffffffLL) {
+    *why = "grid too large";
+    return cudaErrorNotSupported;
+  }
+  window_prep_kernel<kD><<<static_cast<unsigned>(blocks), kPrepThr, 0, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kThr);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(std::min(p.items, sms));
+  cfg.dynamicSmemBytes = KvSmem<kD>::kBytes;
+  e = cudaLaunchKernelEx(&cfg, window_kv_kernel<kD>, q, dout, k, v, dk, dv, p);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(std::min(p.dq_items, sms));
+  cfg.dynamicSmemBytes = DqSmem<kD>::kBytes;
+  e = cudaLaunchKernelEx(&cfg, window_dq_kernel<kD>, k, dq, p);
+  if (e != cudaSuccess) return e;
+  if (s.slots > 0) {
+    const int nk = s.parts_each > 1 ? s.g.nb : s.g.first;
+    const int join = a.B * a.Hkv * nk * 4;
+    window_join_kernel<kD><<<join, kJoinThr, 0, st>>>(p, join);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t window_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int window, int sinks) {
+  const BwdSizes s = bwd_sizes(B, T, Hq, Hkv, D, window, sinks);
+  return 256 + 2 * s.stats + s.ds + s.parts;
+}
+
+cudaError_t launch_window_bwd(const WindowArgs &a, const WaitCtl &w, cudaStream_t st, const char **why) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const BwdSizes s = bwd_sizes(a.B, a.T, a.Hq, a.Hkv, a.D, a.window, a.sinks);
+  const long long items = static_cast<long long>(a.B) * a.Hkv * s.per_unit;
+  const long long dq_items = static_cast<long long>(a.B) * a.Hq * s.g.nb;
+  if (std::max(items, dq_items) > 0x1fffffffLL) {
+    *why = "grid too large";
+    return cudaErrorNotSupported;
+  }
+  BwdParams p;
+  p.o = static_cast<const __nv_bfloat16 *>(a.o), p.dout = static_cast<const __nv_bfloat16 *>(a.dout);
+  p.lse = a.lse, p.lengths = a.lengths;
+  unsigned char *ws = static_cast<unsigned char *>(a.ws);
+  ws += (256 - (reinterpret_cast<uintptr_t>(ws) & 255)) & 255;
+  p.ndelta = reinterpret_cast<float *>(ws);
+  p.nlse2 = reinterpret_cast<float *>(ws + s.stats);
+  p.ds = reinterpret_cast<__nv_bfloat16 *>(ws + 2 * s.stats);
+  p.parts = reinterpret_cast<float *>(ws + 2 * s.stats + s.ds);
+  p.dq = static_cast<__nv_bfloat16 *>(a.dq);
+  p.dk = static_cast<__nv_bfloat16 *>(a.dk), p.dv = static_cast<__nv_bfloat16 *>(a.dv);
+  p.B = a.B, p.T = a.T, p.Tp = s.Tp, p.Hq = a.Hq, p.Hkv = a.Hkv, p.G = a.Hq / a.Hkv;
+  p.o_stride = a.o_stride, p.dk_stride = a.dk_stride, p.dv_stride = a.dv_stride;
+  p.tiles = s.tiles;
+  p.g = s.g;
+  p.first_parts = s.first_parts, p.parts_each = s.parts_each, p.per_unit = s.per_unit, p.slots = s.slots;
+  p.items = static_cast<int>(items), p.dq_items = static_cast<int>(dq_items);
+  p.scale = a.scale;
+  p.wait = w;
+  return a.D == 64 ? launch<64>(a, p, s, sms, st, why) : launch<128>(a, p, s, sms, st, why);
+}
+
+}  // namespace abw

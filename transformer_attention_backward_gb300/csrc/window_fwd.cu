@@ -490,8 +490,8 @@ cudaError_t launch_window_fwd(const WindowArgs &a, const WaitCtl &w, cudaStream_
     return cudaErrorNotSupported;
   }
   p.units = static_cast<int>(units), p.items = static_cast<int>(items);
-  p.window = a.window, p.sinks = a.sinks;
-  p.sink_blocks = a.sinks / kBlk + (a.sinks % kBlk != 0);
+  p.window = std::min(a.window, a.T), p.sinks = std::min(a.sinks, a.T);
+  p.sink_blocks = (p.sinks + kBlk - 1) / kBlk;
   p.scale = a.scale;
   p.wait = w;
   const int grid = static_cast<int>(std::min<long long>(items, sms));
