@@ -184,7 +184,7 @@ struct KvItem {
   long long slot;                        // of its part (nparts > 1)
 };
 
-__device__ __forceinline__ KvItem kv_item(const BwdParams &p, int idx) {
+__device__ __noinline__ KvItem kv_item(const BwdParams &p, int idx) {
   KvItem r;
   const int unit = idx / p.per_unit;
   int rem = idx - unit * p.per_unit;
@@ -265,17 +265,8 @@ __global__ void __launch_bounds__(kThr, 1)
   }
   auto bar = [&](int i) -> uint32_t { return sb + M::kBar + i * 8; };
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + M::kAbort);
-  auto wt = [&](uint32_t br, uint32_t parity) -> bool {
-    if (*abort_flag) return false;
-    if (mbar_wait_bounded(br, parity, p.wait.limit_ns)) return true;
-    *abort_flag = 1;
-    report_timeout(p.wait.err, kSiteWinKv, (br - sb - M::kBar) / 8);
-    return false;
-  };
-  // lane 0's outcome for the whole warp
-  auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return __shfl_sync(0xffffffffu, wt(br, parity), 0); };
-  // query half `half` of dO slot `slot` has been staged
-  auto staged_bar = [&](int slot, int half) -> uint32_t { return bar(M::kStaged + 2 * slot + half); };
+  const Waits wts{sb + M::kBar, abort_flag, &p.wait, kSiteWinKv};
+  auto wtw = [&](int slot, uint32_t parity) -> bool { return wait_warp(wts, slot, parity); };
 
   if (tid == 0) {
     for (int i = 0; i < M::kBars; ++i) {
@@ -312,20 +303,7 @@ __global__ void __launch_bounds__(kThr, 1)
         for (int hx = 0; hx < kHalves; ++hx) tma_load_4d(sb + off + hx * 16384, map, hx * 64, h, row0, b, fb);
         if (stat) bulk_load(sb + stat_off, stat, 512, fb);
       }
-      if (!repair) return;
-      // the copy has landed before anything else happens to the slot, even where the wait gives up
-      if (!mbar_wait_bounded(fb, raw & 1, p.wait.limit_ns)) {
-        if (lane == 0) report_timeout(p.wait.err, kSiteWinKv, M::kRaw);
-        *abort_flag = 1;
-        mbar_wait_bounded(fb, raw & 1, 2000000000ull);
-      }
-      ++raw;
-      for (int i = max(live, 0) * 8 + lane; i < kBlk * 8; i += 32)
-#pragma unroll
-        for (int hx = 0; hx < kHalves; ++hx) *reinterpret_cast<uint4 *>(smem + off + hx * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full);
+      if (repair) clear_tail<kHalves>(wts, smem + off, live, M::kRaw, raw++ & 1, full);
     };
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the statistics come from prep
     KvStream s;
@@ -335,28 +313,28 @@ __global__ void __launch_bounds__(kThr, 1)
       const int qs = nq % M::kQs, ds = nd % M::kDOs;
       const size_t ro = (static_cast<size_t>(w.b) * p.Hq + h) * p.Tp + q0;
       if (s.opens()) {
-        if (!wtw(bar(M::kKEmpty), (nk & 1) ^ 1)) break;
+        if (!wtw(M::kKEmpty, (nk & 1) ^ 1)) break;
         load(&tmK, M::kK, w.kvh, k0, w.b, w.n - k0, bar(M::kKFull), 0, nullptr);
         ++nk;
       }
-      if (!wtw(bar(M::kQEmpty + qs), ((nq / M::kQs) & 1) ^ 1)) break;
+      if (!wtw(M::kQEmpty + qs, ((nq / M::kQs) & 1) ^ 1)) break;
       load(&tmQ, M::kQ + qs * M::kIn, h, q0, w.b, w.n - q0, bar(M::kQFull + qs), M::kLse + qs * 512, p.nlse2 + ro);
       ++nq;
       if (s.opens()) {
-        if (!wtw(bar(M::kVEmpty), (nv & 1) ^ 1)) break;
+        if (!wtw(M::kVEmpty, (nv & 1) ^ 1)) break;
         load(&tmV, M::kV, w.kvh, k0, w.b, w.n - k0, bar(M::kVFull), 0, nullptr);
         ++nv;
       }
-      if (!wtw(bar(M::kDOEmpty + ds), ((nd / M::kDOs) & 1) ^ 1)) break;
+      if (!wtw(M::kDOEmpty + ds, ((nd / M::kDOs) & 1) ^ 1)) break;
       load(&tmDO, M::kDO + ds * M::kDOPitch, h, q0, w.b, w.n - q0, bar(M::kDOFull + ds), M::kDelta + ds * 512, p.ndelta + ro);
       ++nd;
     }
     // The last copy of every slot has landed before the CTA may end, whoever gives up
     // and when (otherwise this finds every phase complete).
-    for (int i = max(nq - M::kQs, 0); i < nq; ++i) mbar_wait_bounded(bar(M::kQFull + i % M::kQs), (i / M::kQs) & 1, 2000000000ull);
-    for (int i = max(nd - M::kDOs, 0); i < nd; ++i) mbar_wait_bounded(bar(M::kDOFull + i % M::kDOs), (i / M::kDOs) & 1, 2000000000ull);
-    if (nk > 0) mbar_wait_bounded(bar(M::kKFull), (nk - 1) & 1, 2000000000ull);
-    if (nv > 0) mbar_wait_bounded(bar(M::kVFull), (nv - 1) & 1, 2000000000ull);
+    for (int i = max(nq - M::kQs, 0); i < nq; ++i) wait_landed(bar(M::kQFull + i % M::kQs), (i / M::kQs) & 1);
+    for (int i = max(nd - M::kDOs, 0); i < nd; ++i) wait_landed(bar(M::kDOFull + i % M::kDOs), (i / M::kDOs) & 1);
+    if (nk > 0) wait_landed(bar(M::kKFull), (nk - 1) & 1);
+    if (nv > 0) wait_landed(bar(M::kVFull), (nv - 1) & 1);
   } else if (warp == 1) {
     // ============================ products =============================
     constexpr uint32_t id_sdp = tc::idesc_bf16_f32(128, 128, 0, 0);   // S^T, dP^T
@@ -368,26 +346,23 @@ __global__ void __launch_bounds__(kThr, 1)
     const uint64_t dOm = tc::sdesc_sw128(sb + M::kDO, 16384, 1024);      // dO as MN-major B of dV
     auto qoff = [](int n) -> uint64_t { return static_cast<uint64_t>((n % M::kQs) * M::kIn) >> 4; };
     auto dooff = [](int n) -> uint64_t { return static_cast<uint64_t>((n % M::kDOs) * M::kDOPitch) >> 4; };
-    auto kstep = [](int kk) -> uint32_t { return static_cast<uint32_t>((kk >> 2) * 16384 + (kk & 3) * 32) >> 4; };
     int items = 0, nk = 0, nv = 0;          // items whose outputs were begun; K and V blocks waited for
     auto issue_s = [&](const KvStream &s, int n) -> bool {
-      if (s.opens() && !wtw(bar(M::kKFull), nk++ & 1)) return false;
-      if (!wtw(bar(M::kQFull + n % M::kQs), (n / M::kQs) & 1)) return false;
+      if (s.opens() && !wtw(M::kKFull, nk++ & 1)) return false;
+      if (!wtw(M::kQFull + n % M::kQs, (n / M::kQs) & 1)) return false;
       tc::fence_after_sync();
       const uint64_t so = qoff(n);
-#pragma unroll
-      for (int kk = 0; kk < kD / 16; ++kk) tc::mma_bf16_w(tmem + kColS, dK + kstep(kk), dQk + so + kstep(kk), id_sdp, kk > 0);
+      product_k<kD>(tmem + kColS, dK, dQk + so, id_sdp);
       tc::commit_w(bar(M::kSFull));
       if (s.closes()) tc::commit_w(bar(M::kKEmpty));
       return true;
     };
     auto issue_dp = [&](const KvStream &s, int n) -> bool {
-      if (s.opens() && !wtw(bar(M::kVFull), nv++ & 1)) return false;
-      if (!wtw(bar(M::kDOFull + n % M::kDOs), (n / M::kDOs) & 1)) return false;
+      if (s.opens() && !wtw(M::kVFull, nv++ & 1)) return false;
+      if (!wtw(M::kDOFull + n % M::kDOs, (n / M::kDOs) & 1)) return false;
       tc::fence_after_sync();
       const uint64_t so = dooff(n);
-#pragma unroll
-      for (int kk = 0; kk < kD / 16; ++kk) tc::mma_bf16_w(tmem + kColDP, dV + kstep(kk), dOk + so + kstep(kk), id_sdp, kk > 0);
+      product_k<kD>(tmem + kColDP, dV, dOk + so, id_sdp);
       tc::commit_w(bar(M::kDPFull));
       if (s.closes()) tc::commit_w(bar(M::kVEmpty));
       return true;
@@ -399,31 +374,25 @@ __global__ void __launch_bounds__(kThr, 1)
       KvStream nxt = cur;
       nxt.next(p);
       const bool opens = cur.opens();
-      if (!wtw(bar(M::kPFull), n & 1)) break;
+      if (!wtw(M::kPFull, n & 1)) break;
       // the accumulators of the item before have been read
-      if (opens && !wtw(bar(M::kAccFree), (items++ & 1) ^ 1)) break;
+      if (opens && !wtw(M::kAccFree, (items++ & 1) ^ 1)) break;
       tc::fence_after_sync();
       const uint64_t dso = dooff(n), qso = qoff(n);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)   // dV += P^T dO
-        tc::mma_bf16_ts_w(tmem + kColDV, tmem + kColS + (kk >> 1) * 32 + (kk & 1) * 8, dOm + dso + ((kk * 2048) >> 4), id_kv,
-                          !opens || kk > 0);
+      tc::mma8_ts32_w(tmem + kColDV, tmem + kColS, dOm + dso, id_kv, !opens);   // dV += P^T dO
       tc::commit_w(bar(M::kDVDone));
       if (cur.closes()) tc::commit_w(bar(M::kDVFinal));
       if (nxt.valid && !issue_s(nxt, n + 1)) break;
-      if (!wtw(bar(M::kDSFull), n & 1)) break;
+      if (!wtw(M::kDSFull, n & 1)) break;
       tc::fence_after_sync();
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)   // dK += dS^T Q
-        tc::mma_bf16_ts_w(tmem + kColDK, tmem + kColDP + (kk >> 1) * 32 + (kk & 1) * 8, dQm + qso + ((kk * 2048) >> 4), id_kv,
-                          !opens || kk > 0);
+      tc::mma8_ts32_w(tmem + kColDK, tmem + kColDP, dQm + qso, id_kv, !opens);   // dK += dS^T Q
       tc::commit_w(bar(M::kQEmpty + n % M::kQs));
       if (cur.closes()) tc::commit_w(bar(M::kDKFinal));
       if (nxt.valid && !issue_dp(nxt, n + 1)) break;
       cur = nxt;
     }
     tc::commit_w(bar(M::kFinal));
-    mbar_wait_bounded(bar(M::kFinal), 0, 2000000000ull);   // every product has completed
+    wait_landed(bar(M::kFinal), 0);   // every product has completed
   } else if (warp == 3) {
     // ============================ copies out ===========================
     if (lane == 0) {
@@ -437,7 +406,7 @@ __global__ void __launch_bounds__(kThr, 1)
         unsigned char *dst = reinterpret_cast<unsigned char *>(p.ds) +
                              ((static_cast<long long>(w.b) * p.Hq + s.head(p)) * p.tiles + p.g.tile0(w.kb) + qi) * kTileBytes;
         for (int hf = 0; hf < 2 && ok; ++hf) {
-          ok = wt(staged_bar(slot, hf), (n / M::kDOs) & 1);
+          ok = wait_one(wts, M::kStaged + 2 * slot + hf, (n / M::kDOs) & 1);
           if (ok) bulk_store(dst + hf * (kTileBytes / 2), at + hf * (kTileBytes / 2), kTileBytes / 2);
         }
         bulk_commit_group();
@@ -448,7 +417,7 @@ __global__ void __launch_bounds__(kThr, 1)
           for (int x = 0; x < 2 && ok; ++x) {
             mbar_arrive(bar(M::kStageFree));
             ++free_;
-            ok = wt(bar(M::kEpi), epi++ & 1);
+            ok = wait_one(wts, M::kEpi, epi++ & 1);
             if (!ok) break;
             for (int hx = 0; hx < kHalves; ++hx)
               tma_store_4d(x == 0 ? &tmdV : &tmdK, at + hx * 16384, hx * 64, w.kvh, w.kb * kBlk, w.b);
@@ -481,7 +450,7 @@ __global__ void __launch_bounds__(kThr, 1)
       // ---- P = 2^(S scale log2 e - lse log2 e)
       float2 P[32];
       uint32_t pk[32];
-      ok = wtw(bar(M::kSFull), n & 1);
+      ok = wtw(M::kSFull, n & 1);
       if (!ok) break;
       tc::fence_after_sync();
       {
@@ -526,7 +495,7 @@ __global__ void __launch_bounds__(kThr, 1)
       tc::fence_before_sync();
       mbar_arrive(bar(M::kPFull));
       // ---- dS = P (dP - delta), over dP and for the workspace
-      ok = wtw(bar(M::kDPFull), n & 1);
+      ok = wtw(M::kDPFull, n & 1);
       if (!ok) break;
       tc::fence_after_sync();
       uint4 U[8];   // this key's dS^T as eight 16-byte units of 8 queries
@@ -556,7 +525,7 @@ __global__ void __launch_bounds__(kThr, 1)
       tc::fence_before_sync();
       mbar_arrive(bar(M::kDSFull));
       // once dV has read dO, its slot stages the dS tile
-      ok = wtw(bar(M::kDVDone), n & 1);
+      ok = wtw(M::kDVDone, n & 1);
       if (!ok) break;
       tc::fence_after_sync();
       unsigned char *slot = smem + M::kDO + (n % M::kDOs) * M::kDOPitch;
@@ -565,7 +534,7 @@ __global__ void __launch_bounds__(kThr, 1)
 #pragma unroll
         for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4 *>(stg + ((u ^ (lane & 7)) << 4)) = U[u];
         fence_proxy_async_smem();
-        mbar_arrive(staged_bar(n % M::kDOs, ch));
+        mbar_arrive(bar(M::kStaged + 2 * (n % M::kDOs) + ch));   // this query half
       }
       if (!s.closes()) continue;
       // ---- the item's dV and dK (scaled): thread (key, half ch of the components)
@@ -573,7 +542,7 @@ __global__ void __launch_bounds__(kThr, 1)
       float *part = whole ? nullptr : p.parts + (w.slot * 2 * kBlk + j) * kD + ch * (kD / 2);
 #pragma unroll 1
       for (int x = 0; x < 2 && ok; ++x) {
-        ok = wtw(bar(x == 0 ? M::kDVFinal : M::kDKFinal), items & 1);
+        ok = wtw(x == 0 ? M::kDVFinal : M::kDKFinal, items & 1);
         if (!ok) break;
         tc::fence_after_sync();
         float v[kD / 2];
@@ -588,7 +557,7 @@ __global__ void __launch_bounds__(kThr, 1)
         }
         const float f = x == 0 ? 1.f : p.scale;
         if (whole) {
-          ok = wtw(bar(M::kStageFree), epi & 1);
+          ok = wtw(M::kStageFree, epi & 1);
           if (!ok) break;
           ++epi;
 #pragma unroll
@@ -679,7 +648,7 @@ struct DqItem {
   int b, h, m, n, lo, lead, steps;
   __device__ __forceinline__ int block(int x) const { return x < lead ? x : lo + (x - lead); }
 };
-__device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
+__device__ __noinline__ DqItem dq_item(const BwdParams &p, int idx) {
   DqItem r;
   const int hb = idx / p.g.nb;
   r.m = p.g.nb - 1 - (idx - hb * p.g.nb);
@@ -704,14 +673,8 @@ __global__ void __launch_bounds__(kThr, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bar = [&](int i) -> uint32_t { return sb + M::kBar + i * 8; };
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + M::kAbort);
-  auto wt = [&](uint32_t br, uint32_t parity) -> bool {
-    if (*abort_flag) return false;
-    if (mbar_wait_bounded(br, parity, p.wait.limit_ns)) return true;
-    *abort_flag = 1;
-    report_timeout(p.wait.err, kSiteWinDq, (br - sb - M::kBar) / 8);
-    return false;
-  };
-  auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return __shfl_sync(0xffffffffu, wt(br, parity), 0); };
+  const Waits wts{sb + M::kBar, abort_flag, &p.wait, kSiteWinDq};
+  auto wtw = [&](int slot, uint32_t parity) -> bool { return wait_warp(wts, slot, parity); };
 
   if (tid == 0) {
     for (int i = 0; i < M::kBars; ++i) mbar_init(bar(i), i == M::kAccEmpty || i == M::kAccEmpty + 1 ? 128 * kHalves : 1);
@@ -737,7 +700,7 @@ __global__ void __launch_bounds__(kThr, 1)
                                    (static_cast<long long>(w.b) * p.Hq + w.h) * p.tiles * kTileBytes;
       for (int x = 0; x < w.steps; ++x, ++g) {
         const int s = g % M::kStages, kb = w.block(x);
-        ok = wtw(bar(M::kEmpty + s), ((g / M::kStages) & 1) ^ 1);
+        ok = wtw(M::kEmpty + s, ((g / M::kStages) & 1) ^ 1);
         if (!ok) break;
         const uint32_t st = sb + s * M::kStage;
         const int live = w.n - kb * kBlk;
@@ -749,26 +712,12 @@ __global__ void __launch_bounds__(kThr, 1)
             tma_load_4d_hint(st + hx * 16384, &tmK, hx * 64, w.h / p.G, kb * kBlk, w.b, fb, keep);
           bulk_load_hint(st + M::kK, tiles + (p.g.tile0(kb) + (w.m - kb)) * kTileBytes, kTileBytes, fb, stream);
         }
-        if (repair) {
-          if (!mbar_wait_bounded(fb, raw & 1, p.wait.limit_ns)) {
-            if (lane == 0) report_timeout(p.wait.err, kSiteWinDq, M::kRaw);
-            *abort_flag = 1;
-            mbar_wait_bounded(fb, raw & 1, 2000000000ull);
-          }
-          ++raw;
-          for (int i = max(live, 0) * 8 + lane; i < kBlk * 8; i += 32)
-#pragma unroll
-            for (int hx = 0; hx < kHalves; ++hx)
-              *reinterpret_cast<uint4 *>(smem + s * M::kStage + hx * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(M::kFull + s));
-        }
+        if (repair) clear_tail<kHalves>(wts, smem + s * M::kStage, live, M::kRaw, raw++ & 1, bar(M::kFull + s));
       }
     }
     // the last copy of every slot has landed before the CTA may end
     for (int i = max(g - M::kStages, 0); i < g; ++i)
-      mbar_wait_bounded(bar(M::kFull + i % M::kStages), (i / M::kStages) & 1, 2000000000ull);
+      wait_landed(bar(M::kFull + i % M::kStages), (i / M::kStages) & 1);
   } else if (warp == 1) {
     // ============================ products =============================
     constexpr uint32_t id = tc::idesc_bf16_f32(128, kD, 1, 1);              // dQ += dS K, both MN-major
@@ -780,24 +729,22 @@ __global__ void __launch_bounds__(kThr, 1)
       const DqItem w = dq_item(p, idx);
       if (w.steps == 0) continue;
       const int a = j & 1;
-      if (!wtw(bar(M::kAccEmpty + a), ((j >> 1) & 1) ^ 1)) break;
+      if (!wtw(M::kAccEmpty + a, ((j >> 1) & 1) ^ 1)) break;
       tc::fence_after_sync();
       for (int x = 0; x < w.steps; ++x, ++g) {
         const int s = g % M::kStages;
-        ok = wtw(bar(M::kFull + s), (g / M::kStages) & 1);
+        ok = wtw(M::kFull + s, (g / M::kStages) & 1);
         if (!ok) break;
         tc::fence_after_sync();
         const uint64_t so = static_cast<uint64_t>(s * M::kStage) >> 4;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma_bf16_w(tmem + a * kD, dS + so + ((kk * 2048) >> 4), dK + so + ((kk * 2048) >> 4), id, x > 0 || kk > 0);
+        tc::mma8_mn_w(tmem + a * kD, dS + so, dK + so, id, x > 0);
         tc::commit_w(bar(M::kEmpty + s));
       }
       if (ok) tc::commit_w(bar(M::kAccFull + a));
       ++j;
     }
     tc::commit_w(bar(M::kFinal));
-    mbar_wait_bounded(bar(M::kFinal), 0, 2000000000ull);   // every product has completed
+    wait_landed(bar(M::kFinal), 0);   // every product has completed
   } else if (warp >= 4 && warp < 4 + 4 * kHalves) {
     // ============================ epilogue ================================
     // Warp w: queries 32 (w % 4) .. of the block, 64 components
@@ -809,7 +756,7 @@ __global__ void __launch_bounds__(kThr, 1)
       const DqItem w = dq_item(p, idx);
       const int a = j & 1, row = w.m * kBlk + 32 * qd + lane;
       if (w.steps > 0) {
-        if (!wtw(bar(M::kAccFull + a), (j >> 1) & 1)) break;
+        if (!wtw(M::kAccFull + a, (j >> 1) & 1)) break;
         tc::fence_after_sync();
         ++j;
       }

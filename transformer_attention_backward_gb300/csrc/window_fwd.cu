@@ -17,7 +17,7 @@
 // S of the next, so S (and Q, O) need one buffer per tile; the order runs on
 // over the CTA's items.
 // Warps: 0 loads (K, V through a ring, Q per tile), 1 issues products, 4-7 and
-// 8-11 softmax of tile 0 and 1 (thread = query row), with most of the registers.
+// 8-11 softmax of tile 0 and 1 (thread = query row).
 // Padding behind a sequence is not looked at: its keys are never visible, and
 // its rows of V, which meet weights of 0, are cleared in shared memory.
 #include <algorithm>
@@ -33,20 +33,22 @@ constexpr int kThr = 384;
 constexpr float kRescale = 8.f;       // lazy-rescale threshold (base-2 units)
 constexpr int kHeadGroup = 8;         // tile pairs of heads per scheduling group
 
-// Bits of the columns 32 wd .. 32 wd + 31 that are below x.
-__device__ __forceinline__ uint32_t below(int x, int wd) {
-  const int n = min(max(x - 32 * wd, 0), 32);
+// The lowest x of 32 bits.
+__device__ __forceinline__ uint32_t below(int x) {
+  const int n = min(max(x, 0), 32);
   return n == 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
-// kN columns of a thread's row.
-template <int kN>
-__device__ __forceinline__ void ld_row(uint32_t taddr, float (&v)[kN]) {
+// A row of O times f; seldom.
+template <int kD>
+__device__ __noinline__ void rescale(uint32_t taddr, float f) {
+#pragma unroll 1
+  for (int c = 0; c < kD; c += 16) {
+    uint32_t o[16];
+    tc::ld16_wait(taddr + c, o);
 #pragma unroll
-  for (int c = 0; c < kN; c += 64) {
-    float(&lo)[32] = *reinterpret_cast<float(*)[32]>(&v[c]);
-    float(&hi)[32] = *reinterpret_cast<float(*)[32]>(&v[c + 32]);
-    tc::ld32x2_wait(taddr + c, taddr + c + 32, lo, hi);
+    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+    tc::st16_wait(taddr + c, o);
   }
 }
 
@@ -90,7 +92,7 @@ struct Unit {
   int b, u, m, n;   // batch, head unit, place along the queries, tokens
 };
 
-__device__ __forceinline__ Unit unit_of(const FwdParams &p, int it) {
+__device__ __noinline__ Unit unit_of(const FwdParams &p, int it) {
   // (batch, head unit) in groups of kHeadGroup; in a group the late blocks of
   // queries first, so that what runs at one time shares K and V in L2
   const int grp = it / (kHeadGroup * p.per_head);
@@ -143,15 +145,8 @@ __global__ void __launch_bounds__(kThr, 1)
 
   auto bar = [&](int i) -> uint32_t { return sb + M::kBar + i * 8; };
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + M::kAbort);
-  auto wt = [&](uint32_t br, uint32_t parity) -> bool {
-    if (*abort_flag) return false;
-    if (mbar_wait_bounded(br, parity, p.wait.limit_ns)) return true;
-    *abort_flag = 1;
-    report_timeout(p.wait.err, kSiteWinFwd, (br - sb - M::kBar) / 8);
-    return false;
-  };
-  // lane 0's outcome for the whole warp
-  auto wtw = [&](uint32_t br, uint32_t parity) -> bool { return __shfl_sync(0xffffffffu, wt(br, parity), 0); };
+  const Waits wts{sb + M::kBar, abort_flag, &p.wait, kSiteWinFwd};
+  auto wtw = [&](int slot, uint32_t parity) -> bool { return wait_warp(wts, slot, parity); };
 
   if (tid == 0) {
     for (int i = 0; i < M::kBars; ++i)
@@ -166,7 +161,6 @@ __global__ void __launch_bounds__(kThr, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + M::kTmem);
 
   if (warp < 4) {
-    regs_down<88>();
     if (warp == 0) {
       // ============================ loads ================================
       if (lane == 0) {
@@ -182,7 +176,7 @@ __global__ void __launch_bounds__(kThr, 1)
         const int kvh = t0.h / p.G;
         auto load = [&](const CUtensorMap *map, int n, bool value) -> bool {
           const int s = r % M::kStages;
-          if (!wtw(bar(M::kKVEmpty + s), ((r / M::kStages) & 1) ^ 1)) return false;
+          if (!wtw(M::kKVEmpty + s, ((r / M::kStages) & 1) ^ 1)) return false;
           const uint32_t dst = sb + M::kRing + s * M::kTile;
           // rows of V behind the sequence's last token: cleared before the products see them
           const int live = w.n - n * kBlk;
@@ -193,22 +187,8 @@ __global__ void __launch_bounds__(kThr, 1)
             for (int hx = 0; hx < kHalves; ++hx) tma_load_4d(dst + hx * 16384, map, hx * 64, kvh, n * kBlk, w.b, fb);
           }
           ++r;
-          if (repair) {
-            // the copy has landed before anything else happens to the slot, even where the wait gives up
-            if (!mbar_wait_bounded(fb, raw & 1, p.wait.limit_ns)) {
-              if (lane == 0) report_timeout(p.wait.err, kSiteWinFwd, M::kRaw);
-              *abort_flag = 1;
-              mbar_wait_bounded(fb, raw & 1, 2000000000ull);
-            }
-            ++raw;
-            unsigned char *at = smem + M::kRing + s * M::kTile;
-            for (int i = max(live, 0) * 8 + lane; i < kBlk * 8; i += 32)
-#pragma unroll
-              for (int hx = 0; hx < kHalves; ++hx) *reinterpret_cast<uint4 *>(at + hx * 16384 + i * 16) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(M::kKVFull + s));
-          }
+          if (repair)
+            clear_tail<kHalves>(wts, smem + M::kRing + s * M::kTile, live, M::kRaw, raw++ & 1, bar(M::kKVFull + s));
           return true;
         };
         for (int x = 0; ok && x < all.steps(); ++x) {
@@ -217,7 +197,7 @@ __global__ void __launch_bounds__(kThr, 1)
           for (int t = 0; ok && x == 0 && t < 2; ++t) {
             const Tile &tile = t == 0 ? t0 : t1;
             if (tile.hi < 0) continue;
-            ok = wtw(bar(M::kQEmpty + t), (nq[t] & 1) ^ 1);
+            ok = wtw(M::kQEmpty + t, (nq[t] & 1) ^ 1);
             if (!ok) break;
             if (lane == 0) {
               mbar_arrive_expect_tx(bar(M::kQFull + t), M::kTile);
@@ -232,9 +212,9 @@ __global__ void __launch_bounds__(kThr, 1)
       // The last copy of every slot has landed before the block may end, whoever gives
       // up and when (otherwise this finds every phase complete).
       for (int i = max(r - M::kStages, 0); i < r; ++i)
-        mbar_wait_bounded(bar(M::kKVFull + i % M::kStages), (i / M::kStages) & 1, 2000000000ull);
+        wait_landed(bar(M::kKVFull + i % M::kStages), (i / M::kStages) & 1);
       for (int t = 0; t < 2; ++t)
-        if (nq[t] > 0) mbar_wait_bounded(bar(M::kQFull + t), (nq[t] - 1) & 1, 2000000000ull);
+        if (nq[t] > 0) wait_landed(bar(M::kQFull + t), (nq[t] - 1) & 1);
     } else if (warp == 1) {
       // ============================ products =============================
       constexpr uint32_t id_s = tc::idesc_bf16_f32(128, 128, 0, 0);   // S = Q K^T, both K-major
@@ -243,80 +223,82 @@ __global__ void __launch_bounds__(kThr, 1)
       const uint64_t dK = tc::sdesc_sw128(sb + M::kRing, 16, 1024);
       const uint64_t dV = tc::sdesc_sw128(sb + M::kRing, 16384, 1024);
       auto slot = [](int r) -> uint64_t { return static_cast<uint64_t>((r % M::kStages) * M::kTile) >> 4; };
-      int r = 0;                              // ring position of the next K block; its V block follows
-      int vr = 0;                             // ring position of the V block that pending PV products read
-      bool v_due = false;                     // its slot has not been handed back
-      bool pend[2] = {false, false}, opens[2] = {false, false}, closes[2] = {false, false};
-      int np[2] = {0, 0}, ni[2] = {0, 0}, nq[2] = {0, 0};   // P tiles, outputs and Q tiles so far
+      int r = 0;                    // ring position of the next K block; its V block follows
+      int vr = -1;                  // ring position of the V block that the PV products to come read
+      // bit t: a PV product of tile t is to come, it is its output's first, its last;
+      // and the parities of its P tiles, outputs and Q tiles
+      uint32_t pend = 0, opens = 0, closes = 0, np = 0, ni = 0, nq = 0;
       bool ok = may_wait(p.wait, abort_flag, kSiteWinFwd, M::kQFull);
-      // O_t += P_t V of the tile's last block
-      auto pv = [&](int t) -> bool {
-        if (!pend[t]) return true;
-        if (!wtw(bar(M::kKVFull + vr % M::kStages), (vr / M::kStages) & 1)) return false;
-        if (opens[t] && !wtw(bar(M::kOEmpty + t), (ni[t] & 1) ^ 1)) return false;
-        if (!wtw(bar(M::kPFull + t), np[t] & 1)) return false;
-        tc::fence_after_sync();
-        const uint64_t v = dV + slot(vr);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma_bf16_ts_w(tmem + kColO + t * kD, tmem + t * 128 + kk * 8, v + ((kk * 2048) >> 4), id_o,
-                            !opens[t] || kk > 0);
-        ++np[t];
-        if (closes[t]) {
-          tc::commit_w(bar(M::kOFull + t));
-          ++ni[t];
-        }
-        pend[t] = opens[t] = false;
-        return true;
-      };
-      auto hand_back_v = [&]() {
-        if (v_due) tc::commit_w(bar(M::kKVEmpty + vr % M::kStages));
-        v_due = false;
-      };
-      for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
-        const Unit w = unit_of(p, it);
-        const Tile tile[2] = {tile_of(p, w, 0), tile_of(p, w, 1)}, all = both_tiles(tile[0], tile[1]);
-        bool begun[2] = {false, false};
-        for (int x = 0; ok && x < all.steps(); ++x, r += 2) {
-          const int n = all.block(x);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            ok = ok && pv(t);
-            if (t == 1) hand_back_v();
-            if (!ok || !tile[t].meets(n)) continue;
-            if (!begun[t]) {
-              ok = wtw(bar(M::kQFull + t), nq[t] & 1);
-              ++nq[t];
-            }
-            ok = ok && wtw(bar(M::kKVFull + r % M::kStages), (r / M::kStages) & 1);
-            if (!ok) continue;
-            tc::fence_after_sync();
-            const uint64_t q = dQ + (static_cast<uint64_t>(t * M::kTile) >> 4), k = dK + slot(r);
-#pragma unroll
-            for (int kk = 0; kk < kD / 16; ++kk) {
-              const uint32_t off = static_cast<uint32_t>((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-              tc::mma_bf16_w(tmem + t * 128, q + off, k + off, id_s, kk > 0);
-            }
-            tc::commit_w(bar(M::kSFull + t));
-            pend[t] = true;
-            opens[t] = !begun[t];
-            begun[t] = true;
-            closes[t] = n == tile[t].hi;
-            if (closes[t]) tc::commit_w(bar(M::kQEmpty + t));
+      int it = blockIdx.x, x = 0;
+      Unit w = {};
+      Tile ta = {}, tb = {}, all = {};
+      all.hi = -1;
+      uint32_t begun = 0;
+      // Steps: the blocks of the items, one after the other, and a last one for the
+      // products that are still to come.  In each, per tile: PV of the tile's block
+      // before, then S of this one.
+      for (bool more = true; ok && more;) {
+        if (x >= all.steps()) {
+          x = 0;
+          begun = 0;
+          more = it < p.items;
+          all.hi = -1;
+          if (more) {
+            w = unit_of(p, it);
+            ta = tile_of(p, w, 0);
+            tb = tile_of(p, w, 1);
+            all = both_tiles(ta, tb);
+            it += gridDim.x;
+            if (all.hi < 0) continue;
           }
-          if (!ok) break;
-          tc::commit_w(bar(M::kKVEmpty + r % M::kStages));   // K
-          vr = r + 1;
-          v_due = true;
         }
+        const int n = more ? all.block(x) : 0;
+#pragma unroll 1
+        for (int t = 0; ok && t < 2; ++t) {
+          const uint32_t bit = 1u << t;
+          const int hi = t ? tb.hi : ta.hi;
+          if (pend & bit) {         // O_t += P_t V
+            ok = wtw(M::kKVFull + vr % M::kStages, (vr / M::kStages) & 1) &&
+                 (!(opens & bit) || wtw(M::kOEmpty + t, ((ni >> t) & 1) ^ 1)) && wtw(M::kPFull + t, (np >> t) & 1);
+            if (!ok) break;
+            tc::fence_after_sync();
+            tc::mma8_ts_w(tmem + kColO + t * kD, tmem + t * 128 + 64, dV + slot(vr), id_o, !(opens & bit));
+            np ^= bit;
+            if (closes & bit) {
+              tc::commit_w(bar(M::kOFull + t));
+              ni ^= bit;
+            }
+            pend &= ~bit;
+          }
+          if (t == 1 && vr >= 0) {  // both tiles are through with the V block
+            tc::commit_w(bar(M::kKVEmpty + vr % M::kStages));
+            vr = -1;
+          }
+          if (!more || !(t ? tb : ta).meets(n)) continue;
+          const bool first = !(begun & bit);
+          ok = (!first || wtw(M::kQFull + t, (nq >> t) & 1)) && wtw(M::kKVFull + r % M::kStages, (r / M::kStages) & 1);
+          if (!ok) break;
+          tc::fence_after_sync();
+          product_k<kD>(tmem + t * 128, dQ + (static_cast<uint64_t>(t * M::kTile) >> 4), dK + slot(r), id_s);
+          tc::commit_w(bar(M::kSFull + t));
+          pend |= bit;
+          opens = first ? opens | bit : opens & ~bit;
+          begun |= bit;
+          if (first) nq ^= bit;
+          closes = n == hi ? closes | bit : closes & ~bit;
+          if (n == hi) tc::commit_w(bar(M::kQEmpty + t));
+        }
+        if (!ok || !more) break;
+        tc::commit_w(bar(M::kKVEmpty + r % M::kStages));   // K
+        vr = r + 1;
+        r += 2;
+        ++x;
       }
-      if (ok) ok = pv(0) && pv(1);
       tc::commit_w(bar(M::kFinal));
-      mbar_wait_bounded(bar(M::kFinal), 0, 2000000000ull);   // every product has completed
+      wait_landed(bar(M::kFinal), 0);   // every product has completed
     }
   } else {
     // ============================ softmax ================================
-    regs_up<208>();
     const int t = (warp >> 2) - 1;                      // tile
     const int qd = warp & 3;                            // TMEM lane quarter
     const int row = 32 * qd + lane;
@@ -335,36 +317,42 @@ __global__ void __launch_bounds__(kThr, 1)
       const int steps = x.steps();
       for (int step = 0; step < steps; ++step) {
         const int n = x.block(step);
-        ok = wtw(bar(M::kSFull + t), ns & 1);
+        ok = wtw(M::kSFull + t, ns & 1);
         if (!ok) break;
         ++ns;
         tc::fence_after_sync();
-        float s[128];
-        ld_row(tS, s);
         const int k0 = n * kBlk;
         // every key of the block is visible to every query of the tile
         const bool full = k0 + kBlk - 1 <= x.q0 && (k0 > x.q0 + kBlk - 1 - p.window || p.sinks - k0 >= kBlk);
-        float a = sl2;
-        if (!full) {
-          const int end = i - k0 + 1, first = end - p.window, stay = min(p.sinks - k0, end);
+        // 64 columns at a time: the first half is read again after the maximum is known
+        const float a = full && sl2 >= 0.f ? sl2 : 1.f;
+        float s[64];
+        auto scores = [&](int half) {
+          float(&lo)[32] = *reinterpret_cast<float(*)[32]>(&s[0]);
+          float(&hi)[32] = *reinterpret_cast<float(*)[32]>(&s[32]);
+          tc::ld32x2_wait(tS + 64 * half, tS + 64 * half + 32, lo, hi);
+          if (full && sl2 >= 0.f) return;
+          const int end = full ? kBlk : i - k0 + 1, first = full ? 0 : end - p.window, stay = min(p.sinks - k0, end);
 #pragma unroll
-          for (int wd = 0; wd < 4; ++wd) {
-            const uint32_t see = (below(end, wd) & ~below(first, wd)) | below(stay, wd);
+          for (int wd = 0; wd < 2; ++wd) {
+            const int c0 = 64 * half + 32 * wd;
+            const uint32_t see = (below(end - c0) & ~below(first - c0)) | below(stay - c0);
 #pragma unroll
             for (int c = 0; c < 32; ++c) s[32 * wd + c] = (see >> c) & 1u ? s[32 * wd + c] * sl2 : -INFINITY;
           }
-          a = 1.f;
-        } else if (sl2 < 0.f) {
+        };
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          scores(half);
+          float u[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int c = 0; c < 128; ++c) s[c] *= sl2;
-          a = 1.f;
+          for (int c = 4; c < 64; c += 4)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[e] = fmaxf(u[e], s[c + e]);
+          top = fmaxf(fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])), top);
         }
-        float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int c = 4; c < 128; c += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top[e] = fmaxf(fmaxf(top[e], s[c + e]), c + 4 + e < 128 ? s[c + 4 + e] : s[c + e]);
-        const float mb = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a;
+        const float mb = top * a;
         const bool need = mb > m + kRescale;
         if (__any_sync(0xffffffffu, need)) {
           const float mn = need ? mb : m;
@@ -372,31 +360,26 @@ __global__ void __launch_bounds__(kThr, 1)
           l *= f;
           m = mn;
           // O holds the blocks before this one: their PV came before this S
-          if (__any_sync(0xffffffffu, l != 0.f)) {
-#pragma unroll 1
-            for (int c = 0; c < kD; c += 16) {           // 16 columns at a time: s[] stays live
-              uint32_t o[16];
-              tc::ld16_wait(tO + c, o);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tc::st16_wait(tO + c, o);
-            }
-          }
+          if (__any_sync(0xffffffffu, l != 0.f)) rescale<kD>(tO, f);
         }
         const float base = m == -INFINITY ? 0.f : m;     // nothing seen yet: 2^(-inf - 0) = 0
         const float2 a2 = make_float2(a, a), b2 = make_float2(-base, -base);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+        for (int half = 1;; half = 0) {
           uint32_t pk[32];
 #pragma unroll
           for (int c = 0; c < 64; c += 2) {
-            const float2 e = fma2(make_float2(s[64 * half + c], s[64 * half + c + 1]), a2, b2);
+            const float2 e = fma2(make_float2(s[c], s[c + 1]), a2, b2);
             const float2 v = make_float2(ex2(e.x), ex2(e.y));
             sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], v);
             pk[c / 2] = pack_bf16(v.x, v.y);
           }
-          tc::st32_async(tS + 32 * half, pk);
+          // Over the 32 columns behind the scores of half 1, then over those of half
+          // 0: columns that are read again are not written before
+          tc::st32_async(tS + 64 + 32 * half, pk);
+          if (half == 0) break;
+          scores(0);
         }
         const float2 both = add2(sum[0], sum[1]);
         l += both.x + both.y;
@@ -409,7 +392,7 @@ __global__ void __launch_bounds__(kThr, 1)
       const bool live = i < w.n;
       const float inv = live ? 1.f / l : 0.f;
       if (x.hi >= 0) {
-        ok = wtw(bar(M::kOFull + t), no & 1);
+        ok = wtw(M::kOFull + t, no & 1);
         if (!ok) break;
         ++no;
         tc::fence_after_sync();
