@@ -17,6 +17,12 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 __device__ __forceinline__ int tokens_of(const int *lengths, int b, int T) {
   return lengths ? min(max(lengths[b], 0), T) : T;
 }
+// The same where a whole warp asks for one b: a value that the compiler knows to
+// be uniform, so what follows from it stays in uniform registers, which the
+// tensor core's instructions take their operands from.
+__device__ __forceinline__ int tokens_warp(const int *lengths, int b, int T) {
+  return lengths ? __shfl_sync(0xffffffffu, tokens_of(lengths, b, T), 0) : T;
+}
 
 // 2^x on the MUFU unit, to some 2^-22; 2^-inf = 0.
 __device__ __forceinline__ float ex2(float x) {
@@ -73,6 +79,29 @@ __device__ __forceinline__ bool wait_one(const Waits &w, int slot, uint32_t pari
   const uint32_t bar = w.bars + slot * 8;
   return mbar_try_wait(bar, parity) || wait_slowly(bar, parity, w);
 }
+// In line and without a call, for the warp that issues products: a call would
+// empty its uniform registers.  `gave_up` is 1 + the slot of a wait that ran out,
+// which the warp reports behind its loop.
+__device__ __forceinline__ bool wait_issuer(const Waits &w, int slot, uint32_t parity, int &gave_up) {
+  const uint32_t bar = w.bars + slot * 8;
+  bool done = mbar_try_wait(bar, parity);
+  if (!done) {
+    WaitClock wc(w.ctl->limit_ns);
+    while (!*w.abort_flag) {
+#pragma unroll 1
+      for (int i = 0; i < 32 && !done; ++i) done = mbar_try_wait(bar, parity);
+      if (done) break;
+      if (wc.expired()) {
+        gave_up = slot + 1;
+        *w.abort_flag = 1;
+      }
+    }
+  }
+  return __shfl_sync(0xffffffffu, done, 0);
+}
+__device__ __forceinline__ void report_issuer(const Waits &w, int gave_up) {
+  if (gave_up != 0) report_timeout(w.ctl->err, w.site, gave_up - 1);
+}
 // Whole-warp form: lane 0's outcome for every lane, so that a warp never splits
 // in front of a warp-collective instruction.
 __device__ __forceinline__ bool wait_warp(const Waits &w, int slot, uint32_t parity) {
@@ -98,15 +127,6 @@ static __device__ __noinline__ void clear_tail(const Waits &w, unsigned char *at
   fence_proxy_async_smem();
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(full);
-}
-
-// D[tmem] = A B^T over kD components, both K-major.
-template <int kD>
-__device__ __forceinline__ void product_k(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
-  if constexpr (kD == 128)
-    tc::mma8_k_w(d, a, b, idesc, 0);
-  else
-    tc::mma4_k_w(d, a, b, idesc, 0);
 }
 
 // bf16 [B][T][H][kD] rows with a token stride (elements), in boxes of 64

@@ -210,8 +210,9 @@ __device__ __noinline__ KvItem kv_item(const BwdParams &p, int idx) {
   const int live = (r.n + kBlk - 1) / kBlk;
   r.qn = max(0, min(r.kb + p.g.queries(r.kb), live) - r.kb);
   const int all = p.G * r.qn;
-  r.it0 = static_cast<int>(static_cast<long long>(all) * r.part / r.nparts);
-  r.it1 = static_cast<int>(static_cast<long long>(all) * (r.part + 1) / r.nparts);
+  const unsigned each = static_cast<unsigned>(all) / r.nparts, extra = all - each * r.nparts;   // the first `extra` have one more
+  r.it0 = r.part * each + min(static_cast<unsigned>(r.part), extra);
+  r.it1 = r.it0 + each + (static_cast<unsigned>(r.part) < extra);
   return r;
 }
 
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kThr, 1)
   constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 256, kColDK = 256 + kD;
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t sb = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (sb & 1023) {
     if (tid == 0) atomicOr(p.wait.err, kErrSmemAlign);
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kThr, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + M::kTmem);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(smem + M::kTmem), 0);
 
   if (warp == 0) {
     // ============================ loads ================================
@@ -344,91 +345,120 @@ __global__ void __launch_bounds__(kThr, 1)
     const uint64_t dOk = tc::sdesc_sw128(sb + M::kDO, 16, 1024);         // dO as K-major B of dP^T
     const uint64_t dQm = tc::sdesc_sw128(sb + M::kQ, 16384, 1024);       // Q as MN-major B of dK
     const uint64_t dOm = tc::sdesc_sw128(sb + M::kDO, 16384, 1024);      // dO as MN-major B of dV
+    int gave_up = 0;
+    auto wti = [&](int slot, uint32_t parity) -> bool { return wait_issuer(wts, slot, parity, gave_up); };
     auto qoff = [](int n) -> uint64_t { return static_cast<uint64_t>((n % M::kQs) * M::kIn) >> 4; };
     auto dooff = [](int n) -> uint64_t { return static_cast<uint64_t>((n % M::kDOs) * M::kDOPitch) >> 4; };
     int items = 0, nk = 0, nv = 0;          // items whose outputs were begun; K and V blocks waited for
-    auto issue_s = [&](const KvStream &s, int n) -> bool {
-      if (s.opens() && !wtw(M::kKFull, nk++ & 1)) return false;
-      if (!wtw(M::kQFull + n % M::kQs, (n / M::kQs) & 1)) return false;
+    auto issue_s = [&](int n, bool opens, bool closes) -> bool {
+      if (opens && !wti(M::kKFull, nk++ & 1)) return false;
+      if (!wti(M::kQFull + n % M::kQs, (n / M::kQs) & 1)) return false;
       tc::fence_after_sync();
-      const uint64_t so = qoff(n);
-      product_k<kD>(tmem + kColS, dK, dQk + so, id_sdp);
-      tc::commit_w(bar(M::kSFull));
-      if (s.closes()) tc::commit_w(bar(M::kKEmpty));
+      if (tc::elect()) {
+        tc::product_k<kD>(tmem + kColS, dK, dQk + qoff(n), id_sdp);
+        tc::commit(bar(M::kSFull));
+        if (closes) tc::commit(bar(M::kKEmpty));
+      }
+      __syncwarp();
       return true;
     };
-    auto issue_dp = [&](const KvStream &s, int n) -> bool {
-      if (s.opens() && !wtw(M::kVFull, nv++ & 1)) return false;
-      if (!wtw(M::kDOFull + n % M::kDOs, (n / M::kDOs) & 1)) return false;
+    auto issue_dp = [&](int n, bool opens, bool closes) -> bool {
+      if (opens && !wti(M::kVFull, nv++ & 1)) return false;
+      if (!wti(M::kDOFull + n % M::kDOs, (n / M::kDOs) & 1)) return false;
       tc::fence_after_sync();
-      const uint64_t so = dooff(n);
-      product_k<kD>(tmem + kColDP, dV, dOk + so, id_sdp);
-      tc::commit_w(bar(M::kDPFull));
-      if (s.closes()) tc::commit_w(bar(M::kVEmpty));
+      if (tc::elect()) {
+        tc::product_k<kD>(tmem + kColDP, dV, dOk + dooff(n), id_sdp);
+        tc::commit(bar(M::kDPFull));
+        if (closes) tc::commit(bar(M::kVEmpty));
+      }
+      __syncwarp();
       return true;
     };
-    KvStream cur;
-    cur.begin(p);
-    bool ok = may_wait(p.wait, abort_flag, kSiteWinKv, M::kKFull) && (!cur.valid || (issue_s(cur, 0) && issue_dp(cur, 0)));
-    for (int n = 0; ok && cur.valid; ++n) {
-      KvStream nxt = cur;
-      nxt.next(p);
-      const bool opens = cur.opens();
-      if (!wtw(M::kPFull, n & 1)) break;
-      // the accumulators of the item before have been read
-      if (opens && !wtw(M::kAccFree, (items++ & 1) ^ 1)) break;
-      tc::fence_after_sync();
-      const uint64_t dso = dooff(n), qso = qoff(n);
-      tc::mma8_ts32_w(tmem + kColDV, tmem + kColS, dOm + dso, id_kv, !opens);   // dV += P^T dO
-      tc::commit_w(bar(M::kDVDone));
-      if (cur.closes()) tc::commit_w(bar(M::kDVFinal));
-      if (nxt.valid && !issue_s(nxt, n + 1)) break;
-      if (!wtw(M::kDSFull, n & 1)) break;
-      tc::fence_after_sync();
-      tc::mma8_ts32_w(tmem + kColDK, tmem + kColDP, dQm + qso, id_kv, !opens);   // dK += dS^T Q
-      tc::commit_w(bar(M::kQEmpty + n % M::kQs));
-      if (cur.closes()) tc::commit_w(bar(M::kDKFinal));
-      if (nxt.valid && !issue_dp(nxt, n + 1)) break;
-      cur = nxt;
+    // pairs of the next item that has some; 0: there is none
+    int idx = blockIdx.x;
+    auto next_item = [&]() -> int {
+      int pairs = 0;
+      for (; pairs == 0 && idx < p.items; idx += gridDim.x) {
+        const KvItem w = kv_item(p, idx);
+        pairs = __shfl_sync(0xffffffffu, w.it1 - w.it0, 0);
+      }
+      return pairs;
+    };
+    // `left` pairs of the item from this one on, `then` from the next one on (of the
+    // next item behind the last); n = -1: only S and dP of pair 0
+    int left = 1, then = next_item();
+    bool opens = false, ok = may_wait(p.wait, abort_flag, kSiteWinKv, M::kKFull);
+#pragma unroll 1
+    for (int n = -1; ok && left > 0; ++n) {
+      const bool closes = left == 1;
+      if (n >= 0) {
+        if (!wti(M::kPFull, n & 1)) break;
+        // the accumulators of the item before have been read
+        if (opens && !wti(M::kAccFree, (items++ & 1) ^ 1)) break;
+        tc::fence_after_sync();
+        if (tc::elect()) {
+          tc::product_ts<32>(tmem + kColDV, tmem + kColS, dOm + dooff(n), id_kv, !opens);   // dV += P^T dO
+          tc::commit(bar(M::kDVDone));
+          if (closes) tc::commit(bar(M::kDVFinal));
+        }
+        __syncwarp();
+      }
+      if (then > 0 && !issue_s(n + 1, closes, then == 1)) break;
+      if (n >= 0) {
+        if (!wti(M::kDSFull, n & 1)) break;
+        tc::fence_after_sync();
+        if (tc::elect()) {
+          tc::product_ts<32>(tmem + kColDK, tmem + kColDP, dQm + qoff(n), id_kv, !opens);   // dK += dS^T Q
+          tc::commit(bar(M::kQEmpty + n % M::kQs));
+          if (closes) tc::commit(bar(M::kDKFinal));
+        }
+        __syncwarp();
+      }
+      if (then > 0 && !issue_dp(n + 1, closes, then == 1)) break;
+      opens = closes;
+      left = then;
+      then = left == 1 ? next_item() : left - 1;
     }
     tc::commit_w(bar(M::kFinal));
+    report_issuer(wts, gave_up);
     wait_landed(bar(M::kFinal), 0);   // every product has completed
   } else if (warp == 3) {
     // ============================ copies out ===========================
-    if (lane == 0) {
-      KvStream s;
-      int n = 0, free_ = 0, epi = 0;
-      bool ok = true;
-      for (s.begin(p); ok && s.valid; s.next(p), ++n) {
-        const KvItem &w = s.w;
-        const int slot = n % M::kDOs, qi = s.block() - w.kb;
-        const uint32_t at = sb + M::kDO + slot * M::kDOPitch;
-        unsigned char *dst = reinterpret_cast<unsigned char *>(p.ds) +
-                             ((static_cast<long long>(w.b) * p.Hq + s.head(p)) * p.tiles + p.g.tile0(w.kb) + qi) * kTileBytes;
-        for (int hf = 0; hf < 2 && ok; ++hf) {
-          ok = wait_one(wts, M::kStaged + 2 * slot + hf, (n / M::kDOs) & 1);
-          if (ok) bulk_store(dst + hf * (kTileBytes / 2), at + hf * (kTileBytes / 2), kTileBytes / 2);
+    KvStream s;
+    int n = 0, epi = 0;
+    bool ok = true;
+    for (s.begin(p); ok && s.valid; s.next(p), ++n) {
+      const KvItem &w = s.w;
+      const int slot = n % M::kDOs, qi = s.block() - w.kb;
+      const uint32_t at = sb + M::kDO + slot * M::kDOPitch;
+      unsigned char *dst = reinterpret_cast<unsigned char *>(p.ds) +
+                           ((static_cast<long long>(w.b) * p.Hq + s.head(p)) * p.tiles + p.g.tile0(w.kb) + qi) * kTileBytes;
+#pragma unroll 1
+      for (int hf = 0; hf < 2 && ok; ++hf) {
+        ok = wtw(M::kStaged + 2 * slot + hf, (n / M::kDOs) & 1);
+        if (ok && lane == 0) {
+          bulk_store(dst + hf * (kTileBytes / 2), at + hf * (kTileBytes / 2), kTileBytes / 2);
+          bulk_commit_group();
         }
-        bulk_commit_group();
-        if (!ok) break;
-        bulk_wait_group_read0();
-        if (s.closes() && w.nparts == 1) {
-          // dV, then dK, as bf16 rows in this slot
-          for (int x = 0; x < 2 && ok; ++x) {
-            mbar_arrive(bar(M::kStageFree));
-            ++free_;
-            ok = wait_one(wts, M::kEpi, epi++ & 1);
-            if (!ok) break;
-            for (int hx = 0; hx < kHalves; ++hx)
-              tma_store_4d(x == 0 ? &tmdV : &tmdK, at + hx * 16384, hx * 64, w.kvh, w.kb * kBlk, w.b);
-            bulk_commit_group();
-            bulk_wait_group_read0();
-          }
-        }
-        if (ok) mbar_arrive(bar(M::kDOEmpty + slot));
       }
-      bulk_wait_group0();
+      if (!ok) break;
+      if (lane == 0) bulk_wait_group_read0();
+      if (s.closes() && w.nparts == 1) {
+        // dV, then dK, as bf16 rows in this slot
+#pragma unroll 1
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (lane == 0) mbar_arrive(bar(M::kStageFree));
+          ok = wtw(M::kEpi, epi++ & 1);
+          if (!ok || lane != 0) continue;
+          for (int hx = 0; hx < kHalves; ++hx)
+            tma_store_4d(x == 0 ? &tmdV : &tmdK, at + hx * 16384, hx * 64, w.kvh, w.kb * kBlk, w.b);
+          bulk_commit_group();
+          bulk_wait_group_read0();
+        }
+      }
+      if (ok && lane == 0) mbar_arrive(bar(M::kDOEmpty + slot));
     }
+    if (lane == 0) bulk_wait_group0();
   } else if (warp >= 4) {
     // ============================ softmax ================================
     // Warp w: keys 32 (w % 4) .. of the block (thread = key), half (w - 4) / 4 of its
@@ -614,16 +644,18 @@ __global__ void __launch_bounds__(kJoinThr) window_join_kernel(const __grid_cons
   if (static_cast<int>(blockIdx.x) >= blocks) return;
   const int idx = unit * p.per_unit + (kb < p.g.first ? kb * p.first_parts : p.g.first * p.first_parts + (kb - p.g.first) * p.parts_each);
   const KvItem w = kv_item(p, idx);
+  // of fewer pairs than parts only the first parts have one and were written
   const int all = p.G * w.qn;
   for (int e = threadIdx.x; e < 2 * 32 * kD / 4; e += kJoinThr) {
     const int x = e / (32 * kD / 4), r = 32 * quarter + e / (kD / 4) % 32, c = e % (kD / 4) * 4;
     const int tok = kb * kBlk + r;
     if (tok >= p.T) continue;
+    const float *src = p.parts + ((w.slot * 2 + x) * kBlk + r) * kD + c;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
     for (int i = 0; i < w.nparts; ++i) {
-      const int a = static_cast<int>(static_cast<long long>(all) * i / w.nparts), z = static_cast<int>(static_cast<long long>(all) * (i + 1) / w.nparts);
-      if (a == z) continue;
-      const float4 v = *reinterpret_cast<const float4 *>(p.parts + (((w.slot + i) * 2 + x) * kBlk + r) * kD + c);
+      if (i >= all) break;
+      const float4 v = *reinterpret_cast<const float4 *>(src + static_cast<size_t>(i) * 2 * kBlk * kD);
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
     const long long at = static_cast<long long>(w.b) * p.T + tok;
@@ -648,13 +680,13 @@ struct DqItem {
   int b, h, m, n, lo, lead, steps;
   __device__ __forceinline__ int block(int x) const { return x < lead ? x : lo + (x - lead); }
 };
-__device__ __noinline__ DqItem dq_item(const BwdParams &p, int idx) {
+__device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
   DqItem r;
   const int hb = idx / p.g.nb;
   r.m = p.g.nb - 1 - (idx - hb * p.g.nb);
   r.b = hb / p.Hq;
   r.h = hb - r.b * p.Hq;
-  r.n = tokens_of(p.lengths, r.b, p.T);
+  r.n = tokens_warp(p.lengths, r.b, p.T);
   r.lo = p.g.lo(r.m);
   r.lead = p.g.lead(r.m);
   r.steps = r.m * kBlk < r.n ? r.lead + r.m - r.lo + 1 : 0;
@@ -670,7 +702,7 @@ __global__ void __launch_bounds__(kThr, 1)
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sb = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   auto bar = [&](int i) -> uint32_t { return sb + M::kBar + i * 8; };
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + M::kAbort);
   const Waits wts{sb + M::kBar, abort_flag, &p.wait, kSiteWinDq};
@@ -685,7 +717,7 @@ __global__ void __launch_bounds__(kThr, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + M::kTmem);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(smem + M::kTmem), 0);
 
   if (warp == 0) {
     // ============================ loads ================================
@@ -723,27 +755,32 @@ __global__ void __launch_bounds__(kThr, 1)
     constexpr uint32_t id = tc::idesc_bf16_f32(128, kD, 1, 1);              // dQ += dS K, both MN-major
     const uint64_t dS = tc::sdesc_sw128(sb + M::kK, kTileBytes / 2, 1024);  // queries contiguous
     const uint64_t dK = tc::sdesc_sw128(sb, 16384, 1024);
-    int g = 0, j = 0;
+    int g = 0, j = 0, gave_up = 0;
+    auto wti = [&](int slot, uint32_t parity) -> bool { return wait_issuer(wts, slot, parity, gave_up); };
     bool ok = may_wait(p.wait, abort_flag, kSiteWinDq, M::kFull);
     for (int idx = blockIdx.x; ok && idx < p.dq_items; idx += gridDim.x) {
       const DqItem w = dq_item(p, idx);
       if (w.steps == 0) continue;
       const int a = j & 1;
-      if (!wtw(M::kAccEmpty + a, ((j >> 1) & 1) ^ 1)) break;
+      if (!wti(M::kAccEmpty + a, ((j >> 1) & 1) ^ 1)) break;
       tc::fence_after_sync();
       for (int x = 0; x < w.steps; ++x, ++g) {
         const int s = g % M::kStages;
-        ok = wtw(M::kFull + s, (g / M::kStages) & 1);
+        ok = wti(M::kFull + s, (g / M::kStages) & 1);
         if (!ok) break;
         tc::fence_after_sync();
         const uint64_t so = static_cast<uint64_t>(s * M::kStage) >> 4;
-        tc::mma8_mn_w(tmem + a * kD, dS + so, dK + so, id, x > 0);
-        tc::commit_w(bar(M::kEmpty + s));
+        if (tc::elect()) {
+          tc::product_mn(tmem + a * kD, dS + so, dK + so, id, x > 0);
+          tc::commit(bar(M::kEmpty + s));
+          if (x == w.steps - 1) tc::commit(bar(M::kAccFull + a));
+        }
+        __syncwarp();
       }
-      if (ok) tc::commit_w(bar(M::kAccFull + a));
       ++j;
     }
     tc::commit_w(bar(M::kFinal));
+    report_issuer(wts, gave_up);
     wait_landed(bar(M::kFinal), 0);   // every product has completed
   } else if (warp >= 4 && warp < 4 + 4 * kHalves) {
     // ============================ epilogue ================================

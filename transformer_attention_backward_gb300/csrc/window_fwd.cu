@@ -92,7 +92,7 @@ struct Unit {
   int b, u, m, n;   // batch, head unit, place along the queries, tokens
 };
 
-__device__ __noinline__ Unit unit_of(const FwdParams &p, int it) {
+__device__ __forceinline__ Unit unit_of(const FwdParams &p, int it) {
   // (batch, head unit) in groups of kHeadGroup; in a group the late blocks of
   // queries first, so that what runs at one time shares K and V in L2
   const int grp = it / (kHeadGroup * p.per_head);
@@ -104,7 +104,7 @@ __device__ __noinline__ Unit unit_of(const FwdParams &p, int it) {
   r.m = p.per_head - 1 - in_grp / gsz;
   r.b = unit / per_b;
   r.u = unit - r.b * per_b;
-  r.n = tokens_of(p.lengths, r.b, p.T);
+  r.n = tokens_warp(p.lengths, r.b, p.T);
   return r;
 }
 __device__ __forceinline__ Tile tile_of(const FwdParams &p, const Unit &w, int t) {
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThr, 1)
   extern __shared__ unsigned char smem_raw[];
   unsigned char *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sb = smem_u32(smem);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   auto bar = [&](int i) -> uint32_t { return sb + M::kBar + i * 8; };
   volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + M::kAbort);
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThr, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + M::kTmem);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t *>(smem + M::kTmem), 0);
 
   if (warp < 4) {
     if (warp == 0) {
@@ -222,9 +222,11 @@ __global__ void __launch_bounds__(kThr, 1)
       const uint64_t dQ = tc::sdesc_sw128(sb + M::kQ, 16, 1024);
       const uint64_t dK = tc::sdesc_sw128(sb + M::kRing, 16, 1024);
       const uint64_t dV = tc::sdesc_sw128(sb + M::kRing, 16384, 1024);
+      int gave_up = 0;
+      auto wti = [&](int slot, uint32_t parity) -> bool { return wait_issuer(wts, slot, parity, gave_up); };
       auto slot = [](int r) -> uint64_t { return static_cast<uint64_t>((r % M::kStages) * M::kTile) >> 4; };
       int r = 0;                    // ring position of the next K block; its V block follows
-      int vr = -1;                  // ring position of the V block that the PV products to come read
+      int vr = 0;                   // ring position of the V block that the PV products to come read
       // bit t: a PV product of tile t is to come, it is its output's first, its last;
       // and the parities of its P tiles, outputs and Q tiles
       uint32_t pend = 0, opens = 0, closes = 0, np = 0, ni = 0, nq = 0;
@@ -258,43 +260,47 @@ __global__ void __launch_bounds__(kThr, 1)
           const uint32_t bit = 1u << t;
           const int hi = t ? tb.hi : ta.hi;
           if (pend & bit) {         // O_t += P_t V
-            ok = wtw(M::kKVFull + vr % M::kStages, (vr / M::kStages) & 1) &&
-                 (!(opens & bit) || wtw(M::kOEmpty + t, ((ni >> t) & 1) ^ 1)) && wtw(M::kPFull + t, (np >> t) & 1);
+            ok = wti(M::kKVFull + vr % M::kStages, (vr / M::kStages) & 1) &&
+                 (!(opens & bit) || wti(M::kOEmpty + t, ((ni >> t) & 1) ^ 1)) && wti(M::kPFull + t, (np >> t) & 1);
             if (!ok) break;
             tc::fence_after_sync();
-            tc::mma8_ts_w(tmem + kColO + t * kD, tmem + t * 128 + 64, dV + slot(vr), id_o, !(opens & bit));
-            np ^= bit;
-            if (closes & bit) {
-              tc::commit_w(bar(M::kOFull + t));
-              ni ^= bit;
+            if (tc::elect()) {
+              tc::product_ts<16>(tmem + kColO + t * kD, tmem + t * 128 + 64, dV + slot(vr), id_o, !(opens & bit));
+              if (closes & bit) tc::commit(bar(M::kOFull + t));
+              // both tiles are through with the V block
+              if (t == 1 || !(pend & 2u)) tc::commit(bar(M::kKVEmpty + vr % M::kStages));
             }
+            __syncwarp();
+            np ^= bit;
+            if (closes & bit) ni ^= bit;
             pend &= ~bit;
-          }
-          if (t == 1 && vr >= 0) {  // both tiles are through with the V block
-            tc::commit_w(bar(M::kKVEmpty + vr % M::kStages));
-            vr = -1;
           }
           if (!more || !(t ? tb : ta).meets(n)) continue;
           const bool first = !(begun & bit);
-          ok = (!first || wtw(M::kQFull + t, (nq >> t) & 1)) && wtw(M::kKVFull + r % M::kStages, (r / M::kStages) & 1);
+          ok = (!first || wti(M::kQFull + t, (nq >> t) & 1)) && wti(M::kKVFull + r % M::kStages, (r / M::kStages) & 1);
           if (!ok) break;
           tc::fence_after_sync();
-          product_k<kD>(tmem + t * 128, dQ + (static_cast<uint64_t>(t * M::kTile) >> 4), dK + slot(r), id_s);
-          tc::commit_w(bar(M::kSFull + t));
+          if (tc::elect()) {
+            tc::product_k<kD>(tmem + t * 128, dQ + (static_cast<uint64_t>(t * M::kTile) >> 4), dK + slot(r), id_s);
+            tc::commit(bar(M::kSFull + t));
+            if (n == hi) tc::commit(bar(M::kQEmpty + t));
+            // both tiles are through with the K block
+            if (t == 1 || !tb.meets(n)) tc::commit(bar(M::kKVEmpty + r % M::kStages));
+          }
+          __syncwarp();
           pend |= bit;
           opens = first ? opens | bit : opens & ~bit;
           begun |= bit;
           if (first) nq ^= bit;
           closes = n == hi ? closes | bit : closes & ~bit;
-          if (n == hi) tc::commit_w(bar(M::kQEmpty + t));
         }
         if (!ok || !more) break;
-        tc::commit_w(bar(M::kKVEmpty + r % M::kStages));   // K
         vr = r + 1;
         r += 2;
         ++x;
       }
       tc::commit_w(bar(M::kFinal));
+      report_issuer(wts, gave_up);
       wait_landed(bar(M::kFinal), 0);   // every product has completed
     }
   } else {
