@@ -55,6 +55,8 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, in
          | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
 
+constexpr uint32_t kNegateA = 1u << 13;   // A enters with its sign turned
+
 // ------------------------------------------------------------ MMA
 // D[tmem] (+)= A[smem] * B[smem], issued by one thread.
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, int accumulate) {
@@ -124,13 +126,13 @@ __device__ __forceinline__ void product_mn(uint32_t d_tmem, uint64_t a, uint64_t
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk) mma_bf16(d_tmem, a + ((kk * 2048) >> 4), b + ((kk * 2048) >> 4), idesc, accumulate || kk > 0);
 }
-// A in TMEM, chunk c of 16 in columns kPair (c / 2) + 8 (c % 2); B MN-major over 128
-// rows of 128 bytes.
-template <int kPair>
+// A in TMEM, chunk c of 16 in columns kPitch (c / kRun) + 8 (c % kRun); B MN-major over
+// 128 rows of 128 bytes.
+template <int kRun, int kPitch>
 __device__ __forceinline__ void product_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool accumulate) {
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk)
-    mma_bf16_ts(d_tmem, a_tmem + (kk >> 1) * kPair + (kk & 1) * 8, b + ((kk * 2048) >> 4), idesc, accumulate || kk > 0);
+    mma_bf16_ts(d_tmem, a_tmem + kk / kRun * kPitch + kk % kRun * 8, b + ((kk * 2048) >> 4), idesc, accumulate || kk > 0);
 }
 
 __device__ __forceinline__ void commit_w(uint32_t bar) {
@@ -244,6 +246,16 @@ __device__ __forceinline__ void ld16_wait(uint32_t ta, uint32_t (&r)[16]) {
       : "memory");
 }
 
+// 8 columns, one wait.
+__device__ __forceinline__ void ld8_wait(uint32_t ta, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(ta)
+      : "memory");
+}
+
 #undef ABW_TC_R16
 #define ABW_TC_RW16(o) \
   "+r"(r[o + 0]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), "+r"(r[o + 5]), \
@@ -269,6 +281,15 @@ __device__ __forceinline__ void st8_async(uint32_t ta, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(ta), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+// Asynchronous 16-column store; complete it with wait_st().
+__device__ __forceinline__ void st16_async(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 // Asynchronous 32-column store; complete it with wait_st().
 __device__ __forceinline__ void st32_async(uint32_t taddr, const uint32_t (&r)[32]) {

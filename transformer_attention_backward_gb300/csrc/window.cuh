@@ -24,6 +24,27 @@ __device__ __forceinline__ int tokens_warp(const int *lengths, int b, int T) {
   return lengths ? __shfl_sync(0xffffffffu, tokens_of(lengths, b, T), 0) : T;
 }
 
+// n / d for 0 <= n < 2^31 by a product: m = ceil(2^(31 + k) / d) with 2^k >= d > 2^(k - 1)
+// is off by e < d 2^-(31 + k) <= 2^-31 from 2^(31 + k) / d, relative to it below 1 / n.
+struct Div {
+  unsigned d, mul, shift;
+  static Div by(int x) {
+    Div r;
+    r.d = x;
+    unsigned k = 0;
+    while ((1ull << k) < r.d) ++k;
+    r.mul = static_cast<unsigned>(((1ull << (31 + k)) + r.d - 1) / r.d);
+    r.shift = k;
+    return r;
+  }
+  // quotient; n becomes the remainder
+  __device__ __forceinline__ int operator()(int &n) const {
+    const unsigned q = static_cast<unsigned>((static_cast<unsigned long long>(mul) * static_cast<unsigned>(n)) >> 31) >> shift;
+    n -= q * d;
+    return q;
+  }
+};
+
 // 2^x on the MUFU unit, to some 2^-22; 2^-inf = 0.
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -33,6 +54,24 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&v);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Barrier over `count` threads that also tells whether `pred` holds in any of them.
+__device__ __forceinline__ bool named_barrier_or(int id, int count, bool pred) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(pred ? 1 : 0), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
 }
 // Two fp32 operations at once.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {

@@ -17,8 +17,8 @@
 // queries, so their pairs go to several CTAs (and all blocks' do while the grid
 // would not fill the GPU); parts are fp32 in the workspace.
 //
-// kv (persistent, one CTA per SM, 12 warps: 0 loads, 1 products, 3 copies out, 4-11
-// softmax): per pair of blocks the products go out in the order
+// kv (persistent, one CTA per SM, 12 warps: 0 loads, 1 and 2 products, 3 copies out,
+// 4-11 softmax): per pair of blocks the products go out in the order
 //   S(n) dP(n) | P(n) ready: dV(n) S(n+1) | dS(n) ready: dK(n) dP(n+1)
 // with S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q (M = 128 keys, P and
 // dS as A operands in TMEM over S and dP), so P is formed while dP runs, dS while
@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(kThr, 1)
       int count = 1;
       if (i == M::kPFull || i == M::kDSFull || i == M::kAccFree || i == M::kEpi) count = 256;   // every softmax thread
       if (i >= M::kStaged && i < M::kStaged + 4) count = 128;
+      if (i == M::kFinal) count = 2;
       mbar_init(bar(i), count);
     }
     *abort_flag = 0;
@@ -336,44 +337,25 @@ __global__ void __launch_bounds__(kThr, 1)
     for (int i = max(nd - M::kDOs, 0); i < nd; ++i) wait_landed(bar(M::kDOFull + i % M::kDOs), (i / M::kDOs) & 1);
     if (nk > 0) wait_landed(bar(M::kKFull), (nk - 1) & 1);
     if (nv > 0) wait_landed(bar(M::kVFull), (nv - 1) & 1);
-  } else if (warp == 1) {
+  } else if (warp < 3) {
     // ============================ products =============================
+    // Warp 1 issues S and dV, which share TMEM columns with P, warp 2 dP and dK.
+    // Between two products an issuer waits and looks things up for some 400 cycles;
+    // two of them do so in turn.
     constexpr uint32_t id_sdp = tc::idesc_bf16_f32(128, 128, 0, 0);   // S^T, dP^T
     constexpr uint32_t id_kv = tc::idesc_bf16_f32(128, kD, 0, 1);     // dV, dK (A from TMEM)
-    const uint64_t dK = tc::sdesc_sw128(sb + M::kK, 16, 1024), dV = tc::sdesc_sw128(sb + M::kV, 16, 1024);
-    const uint64_t dQk = tc::sdesc_sw128(sb + M::kQ, 16, 1024);          // Q as K-major B of S^T
-    const uint64_t dOk = tc::sdesc_sw128(sb + M::kDO, 16, 1024);         // dO as K-major B of dP^T
-    const uint64_t dQm = tc::sdesc_sw128(sb + M::kQ, 16384, 1024);       // Q as MN-major B of dK
-    const uint64_t dOm = tc::sdesc_sw128(sb + M::kDO, 16384, 1024);      // dO as MN-major B of dV
     int gave_up = 0;
     auto wti = [&](int slot, uint32_t parity) -> bool { return wait_issuer(wts, slot, parity, gave_up); };
+    const bool first = warp == 1;
+    // The first's operands: K, Q (K-major B of S^T), dO (MN-major B of dV); the
+    // second's: V, dO, Q.
+    const uint64_t dA = tc::sdesc_sw128(sb + (first ? M::kK : M::kV), 16, 1024);
+    const uint64_t dBk = tc::sdesc_sw128(sb + (first ? M::kQ : M::kDO), 16, 1024);
+    const uint64_t dBm = tc::sdesc_sw128(sb + (first ? M::kDO : M::kQ), 16384, 1024);
+    const uint32_t tX = tmem + (first ? kColS : kColDP), tY = tmem + (first ? kColDV : kColDK);
     auto qoff = [](int n) -> uint64_t { return static_cast<uint64_t>((n % M::kQs) * M::kIn) >> 4; };
     auto dooff = [](int n) -> uint64_t { return static_cast<uint64_t>((n % M::kDOs) * M::kDOPitch) >> 4; };
-    int items = 0, nk = 0, nv = 0;          // items whose outputs were begun; K and V blocks waited for
-    auto issue_s = [&](int n, bool opens, bool closes) -> bool {
-      if (opens && !wti(M::kKFull, nk++ & 1)) return false;
-      if (!wti(M::kQFull + n % M::kQs, (n / M::kQs) & 1)) return false;
-      tc::fence_after_sync();
-      if (tc::elect()) {
-        tc::product_k<kD>(tmem + kColS, dK, dQk + qoff(n), id_sdp);
-        tc::commit(bar(M::kSFull));
-        if (closes) tc::commit(bar(M::kKEmpty));
-      }
-      __syncwarp();
-      return true;
-    };
-    auto issue_dp = [&](int n, bool opens, bool closes) -> bool {
-      if (opens && !wti(M::kVFull, nv++ & 1)) return false;
-      if (!wti(M::kDOFull + n % M::kDOs, (n / M::kDOs) & 1)) return false;
-      tc::fence_after_sync();
-      if (tc::elect()) {
-        tc::product_k<kD>(tmem + kColDP, dV, dOk + dooff(n), id_sdp);
-        tc::commit(bar(M::kDPFull));
-        if (closes) tc::commit(bar(M::kVEmpty));
-      }
-      __syncwarp();
-      return true;
-    };
+    int items = 0, na = 0;                  // items whose output was begun; K (V) blocks waited for
     // pairs of the next item that has some; 0: there is none
     int idx = blockIdx.x;
     auto next_item = [&]() -> int {
@@ -391,37 +373,38 @@ __global__ void __launch_bounds__(kThr, 1)
 #pragma unroll 1
     for (int n = -1; ok && left > 0; ++n) {
       const bool closes = left == 1;
-      if (n >= 0) {
-        if (!wti(M::kPFull, n & 1)) break;
+      if (n >= 0) {                         // dV += P^T dO (dK += dS^T Q)
         // the accumulators of the item before have been read
         if (opens && !wti(M::kAccFree, (items++ & 1) ^ 1)) break;
+        if (!wti(first ? M::kDOFull + n % M::kDOs : M::kQFull + n % M::kQs, (n / (first ? M::kDOs : M::kQs)) & 1)) break;
+        if (!wti(first ? M::kPFull : M::kDSFull, n & 1)) break;
         tc::fence_after_sync();
         if (tc::elect()) {
-          tc::product_ts<32>(tmem + kColDV, tmem + kColS, dOm + dooff(n), id_kv, !opens);   // dV += P^T dO
-          tc::commit(bar(M::kDVDone));
-          if (closes) tc::commit(bar(M::kDVFinal));
+          tc::product_ts<2, 32>(tY, tX, dBm + (first ? dooff(n) : qoff(n)), id_kv, !opens);
+          tc::commit(bar(first ? M::kDVDone : M::kQEmpty + n % M::kQs));
+          if (closes) tc::commit(bar(first ? M::kDVFinal : M::kDKFinal));
         }
         __syncwarp();
       }
-      if (then > 0 && !issue_s(n + 1, closes, then == 1)) break;
-      if (n >= 0) {
-        if (!wti(M::kDSFull, n & 1)) break;
+      const int m = n + 1;                  // S^T = K Q^T (dP^T = V dO^T) of the next pair
+      if (then > 0) {
+        if (closes && !wti(first ? M::kKFull : M::kVFull, na++ & 1)) break;
+        if (!wti(first ? M::kQFull + m % M::kQs : M::kDOFull + m % M::kDOs, (m / (first ? M::kQs : M::kDOs)) & 1)) break;
         tc::fence_after_sync();
         if (tc::elect()) {
-          tc::product_ts<32>(tmem + kColDK, tmem + kColDP, dQm + qoff(n), id_kv, !opens);   // dK += dS^T Q
-          tc::commit(bar(M::kQEmpty + n % M::kQs));
-          if (closes) tc::commit(bar(M::kDKFinal));
+          tc::product_k<kD>(tX, dA, dBk + (first ? qoff(m) : dooff(m)), id_sdp);
+          tc::commit(bar(first ? M::kSFull : M::kDPFull));
+          if (then == 1) tc::commit(bar(first ? M::kKEmpty : M::kVEmpty));
         }
         __syncwarp();
       }
-      if (then > 0 && !issue_dp(n + 1, closes, then == 1)) break;
       opens = closes;
       left = then;
       then = left == 1 ? next_item() : left - 1;
     }
     tc::commit_w(bar(M::kFinal));
     report_issuer(wts, gave_up);
-    wait_landed(bar(M::kFinal), 0);   // every product has completed
+    wait_landed(bar(M::kFinal), 0);   // every product of both has completed
   } else if (warp == 3) {
     // ============================ copies out ===========================
     KvStream s;

@@ -16,8 +16,8 @@
 // Order of the products, block after block: per tile PV of its last block, then
 // S of the next, so S (and Q, O) need one buffer per tile; the order runs on
 // over the CTA's items.
-// Warps: 0 loads (K, V through a ring, Q per tile), 1 issues products, 4-7 and
-// 8-11 softmax of tile 0 and 1 (thread = query row).
+// Warps: 0 loads (K, V through a ring, Q per tile), 1 issues products, 4-7 and 8-11
+// softmax of tile 0 and 1, 12-15 outputs (thread = query row).
 // Padding behind a sequence is not looked at: its keys are never visible, and
 // its rows of V, which meet weights of 0, are cleared in shared memory.
 #include <algorithm>
@@ -29,7 +29,7 @@ namespace {
 
 using namespace win;
 
-constexpr int kThr = 384;
+constexpr int kThr = 512;
 constexpr float kRescale = 8.f;       // lazy-rescale threshold (base-2 units)
 constexpr int kHeadGroup = 8;         // tile pairs of heads per scheduling group
 
@@ -39,29 +39,18 @@ __device__ __forceinline__ uint32_t below(int x) {
   return n == 32 ? 0xffffffffu : (1u << n) - 1u;
 }
 
-// A row of O times f; seldom.
-template <int kD>
-__device__ __noinline__ void rescale(uint32_t taddr, float f) {
-#pragma unroll 1
-  for (int c = 0; c < kD; c += 16) {
-    uint32_t o[16];
-    tc::ld16_wait(taddr + c, o);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-    tc::st16_wait(taddr + c, o);
-  }
-}
-
 template <int kD>
 struct FwdSmem {
   static constexpr int kTile = kBlk * kD * 2;               // one block of Q, K or V
   static constexpr int kStages = kD == 128 ? 4 : 8;
   static constexpr int kQ = 0;                              // two tiles
   static constexpr int kRing = 2 * kTile;
-  static constexpr int kOut = kRing + kStages * kTile;      // 4 KB per softmax warp: 32 rows x 64 components
-  static constexpr int kBar = kOut + 8 * 4096;
+  static constexpr int kOut = kRing + kStages * kTile;      // 4 KB per output warp: 32 rows x 64 components
+  static constexpr int kStat = kOut + 4 * 4096;             // [tile][128] (m, l)
+  static constexpr int kBar = kStat + 2048;
   enum {
-    kQFull = 0, kQEmpty = 2, kSFull = 4, kPFull = 6, kOFull = 8, kOEmpty = 10, kRaw = 12, kFinal = 13, kKVFull = 14,
+    kQFull = 0, kQEmpty = 2, kSFull = 4, kOFull = 6, kPFull = 8, kOEmpty = 10, kLFull = 12, kLEmpty = 14, kRaw = 16,
+    kFinal = 17, kKVFull = 18,
     kKVEmpty = kKVFull + kStages, kBars = kKVEmpty + kStages
   };
   static constexpr int kTmem = kBar + kBars * 8, kAbort = kTmem + 4;
@@ -73,6 +62,7 @@ struct FwdParams {
   float *lse;
   const int *lengths;
   int B, T, Hq, Hkv, G, nqb, per_head, units, items;
+  Div by_group, by_width, by_last, by_heads, by_g;   // items of a scheduling group, its width (the last one's), head units, G
   int pair_heads;         // tiles: 1 two heads of a group, 0 two blocks of queries
   int window, sinks, sink_blocks;
   float scale;
@@ -95,15 +85,12 @@ struct Unit {
 __device__ __forceinline__ Unit unit_of(const FwdParams &p, int it) {
   // (batch, head unit) in groups of kHeadGroup; in a group the late blocks of
   // queries first, so that what runs at one time shares K and V in L2
-  const int grp = it / (kHeadGroup * p.per_head);
-  const int gsz = min(kHeadGroup, p.units - grp * kHeadGroup);
-  const int in_grp = it - grp * kHeadGroup * p.per_head;
-  const int unit = grp * kHeadGroup + in_grp % gsz;
-  const int per_b = p.pair_heads ? p.Hq / 2 : p.Hq;
   Unit r;
-  r.m = p.per_head - 1 - in_grp / gsz;
-  r.b = unit / per_b;
-  r.u = unit - r.b * per_b;
+  const int grp = p.by_group(it);             // `it` becomes the place in the group
+  const int m = (grp + 1) * kHeadGroup <= p.units ? p.by_width(it) : p.by_last(it);
+  r.m = p.per_head - 1 - m;
+  r.u = grp * kHeadGroup + it;
+  r.b = p.by_heads(r.u);
   r.n = tokens_warp(p.lengths, r.b, p.T);
   return r;
 }
@@ -150,7 +137,7 @@ __global__ void __launch_bounds__(kThr, 1)
 
   if (tid == 0) {
     for (int i = 0; i < M::kBars; ++i)
-      mbar_init(bar(i), i == M::kPFull || i == M::kPFull + 1 || i == M::kOEmpty || i == M::kOEmpty + 1 ? 128 : 1);
+      mbar_init(bar(i), i >= M::kPFull && i < M::kRaw ? 128 : 1);   // threads of a warpgroup
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -173,7 +160,8 @@ __global__ void __launch_bounds__(kThr, 1)
       for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
         const Unit w = unit_of(p, it);
         const Tile t0 = tile_of(p, w, 0), t1 = tile_of(p, w, 1), all = both_tiles(t0, t1);
-        const int kvh = t0.h / p.G;
+        int rest = t0.h;
+        const int kvh = p.by_g(rest);
         auto load = [&](const CUtensorMap *map, int n, bool value) -> bool {
           const int s = r % M::kStages;
           if (!wtw(M::kKVEmpty + s, ((r / M::kStages) & 1) ^ 1)) return false;
@@ -217,7 +205,8 @@ __global__ void __launch_bounds__(kThr, 1)
         if (nq[t] > 0) wait_landed(bar(M::kQFull + t), (nq[t] - 1) & 1);
     } else if (warp == 1) {
       // ============================ products =============================
-      constexpr uint32_t id_s = tc::idesc_bf16_f32(128, 128, 0, 0);   // S = Q K^T, both K-major
+      // S = Q K^T, both K-major; -Q K^T where the scale is negative
+      const uint32_t id_s = tc::idesc_bf16_f32(128, 128, 0, 0) | (p.scale < 0.f ? tc::kNegateA : 0u);
       constexpr uint32_t id_o = tc::idesc_bf16_f32(128, kD, 0, 1);    // O += P V, V MN-major
       const uint64_t dQ = tc::sdesc_sw128(sb + M::kQ, 16, 1024);
       const uint64_t dK = tc::sdesc_sw128(sb + M::kRing, 16, 1024);
@@ -265,7 +254,7 @@ __global__ void __launch_bounds__(kThr, 1)
             if (!ok) break;
             tc::fence_after_sync();
             if (tc::elect()) {
-              tc::product_ts<16>(tmem + kColO + t * kD, tmem + t * 128 + 64, dV + slot(vr), id_o, !(opens & bit));
+              tc::product_ts<8, 0>(tmem + kColO + t * kD, tmem + t * 128 + 64, dV + slot(vr), id_o, !(opens & bit));
               if (closes & bit) tc::commit(bar(M::kOFull + t));
               // both tiles are through with the V block
               if (t == 1 || !(pend & 2u)) tc::commit(bar(M::kKVEmpty + vr % M::kStages));
@@ -303,89 +292,103 @@ __global__ void __launch_bounds__(kThr, 1)
       report_issuer(wts, gave_up);
       wait_landed(bar(M::kFinal), 0);   // every product has completed
     }
-  } else {
+  } else if (warp < 12) {
     // ============================ softmax ================================
     const int t = (warp >> 2) - 1;                      // tile
     const int qd = warp & 3;                            // TMEM lane quarter
     const int row = 32 * qd + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
     const uint32_t tS = tmem + lanes + t * 128, tO = tmem + lanes + kColO + t * kD;
-    const float sl2 = p.scale * kLog2e;                 // scores in base-2 units
-    unsigned char *stage = smem + M::kOut + (t * 4 + qd) * 4096;
+    const float sl2 = fabsf(p.scale) * kLog2e;          // scores in base-2 units
+    float2 *stat = reinterpret_cast<float2 *>(smem + M::kStat) + t * 128 + row;
     int ns = 0, no = 0;                                 // S tiles, outputs so far
     bool ok = true;
     for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
       const Unit w = unit_of(p, it);
       const Tile x = tile_of(p, w, t);
-      if (!x.exists) continue;
       const int i = x.q0 + row;
       float m = -INFINITY, l = 0.f;
       const int steps = x.steps();
+      if (steps == 0) continue;
       for (int step = 0; step < steps; ++step) {
-        const int n = x.block(step);
+        const int n = x.block(step), k0 = n * kBlk;
+        // every key of the block is visible to every query of the tile
+        const bool full = k0 + kBlk - 1 <= x.q0 && (k0 > x.q0 + kBlk - 1 - p.window || p.sinks - k0 >= kBlk);
         ok = wtw(M::kSFull + t, ns & 1);
         if (!ok) break;
         ++ns;
         tc::fence_after_sync();
-        const int k0 = n * kBlk;
-        // every key of the block is visible to every query of the tile
-        const bool full = k0 + kBlk - 1 <= x.q0 && (k0 > x.q0 + kBlk - 1 - p.window || p.sinks - k0 >= kBlk);
-        // 64 columns at a time: the first half is read again after the maximum is known
-        const float a = full && sl2 >= 0.f ? sl2 : 1.f;
+        // 64 columns at a time, each with its mask: one loop for whole and cut blocks,
+        // which stays in the instruction cache.  Halves that no row of the warp sees are
+        // left out.
         float s[64];
-        auto scores = [&](int half) {
+        uint32_t see[2];
+        auto load = [&](int half) -> bool {
+          see[0] = see[1] = 0xffffffffu;
+          if (!full) {
+            const int end = i - k0 + 1 - 64 * half, first = end - p.window, stay = min(p.sinks - k0 - 64 * half, end);
+#pragma unroll
+            for (int wd = 0; wd < 2; ++wd)
+              see[wd] = (below(end - 32 * wd) & ~below(first - 32 * wd)) | below(stay - 32 * wd);
+            if (!__any_sync(0xffffffffu, (see[0] | see[1]) != 0)) return false;
+          }
           float(&lo)[32] = *reinterpret_cast<float(*)[32]>(&s[0]);
           float(&hi)[32] = *reinterpret_cast<float(*)[32]>(&s[32]);
           tc::ld32x2_wait(tS + 64 * half, tS + 64 * half + 32, lo, hi);
-          if (full && sl2 >= 0.f) return;
-          const int end = full ? kBlk : i - k0 + 1, first = full ? 0 : end - p.window, stay = min(p.sinks - k0, end);
-#pragma unroll
-          for (int wd = 0; wd < 2; ++wd) {
-            const int c0 = 64 * half + 32 * wd;
-            const uint32_t see = (below(end - c0) & ~below(first - c0)) | below(stay - c0);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) s[32 * wd + c] = (see >> c) & 1u ? s[32 * wd + c] * sl2 : -INFINITY;
-          }
+          return true;
         };
+        auto masked = [&](int c, float v) -> float { return see[c >> 5] & (1u << (c & 31)) ? v : -INFINITY; };
         float top = -INFINITY;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          scores(half);
-          float u[4] = {s[0], s[1], s[2], s[3]};
+          if (!load(half)) continue;
+          float u[2] = {top, -INFINITY};
 #pragma unroll
-          for (int c = 4; c < 64; c += 4)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) u[e] = fmaxf(u[e], s[c + e]);
-          top = fmaxf(fmaxf(fmaxf(u[0], u[1]), fmaxf(u[2], u[3])), top);
+          for (int c = 0; c < 64; c += 2) u[(c >> 1) & 1] = max3(u[(c >> 1) & 1], masked(c, s[c]), masked(c + 1, s[c + 1]));
+          top = fmaxf(u[0], u[1]);
         }
-        const float mb = top * a;
-        const bool need = mb > m + kRescale;
+        if (top > -INFINITY) top *= sl2;
+        const bool need = top > m + kRescale;
         if (__any_sync(0xffffffffu, need)) {
-          const float mn = need ? mb : m;
+          const float mn = need ? top : m;
           const float f = m == -INFINITY ? 0.f : ex2(m - mn);
           l *= f;
           m = mn;
           // O holds the blocks before this one: their PV came before this S
-          if (__any_sync(0xffffffffu, l != 0.f)) rescale<kD>(tO, f);
+          if (step > 0) {
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 8) {
+              uint32_t o[8];
+              tc::ld8_wait(tO + c, o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tc::st8_async(tO + c, o);
+            }
+          }
         }
         const float base = m == -INFINITY ? 0.f : m;     // nothing seen yet: 2^(-inf - 0) = 0
-        const float2 a2 = make_float2(a, a), b2 = make_float2(-base, -base);
+        const float2 b2 = make_float2(-base, -base);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 a2 = make_float2(sl2, sl2);
+        // P of keys 2 c, 2 c + 1 in column 64 + c, from the last keys to the first:
+        // what it overwrites has been read for the last time
 #pragma unroll 1
         for (int half = 1;; half = 0) {
-          uint32_t pk[32];
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float2 e = fma2(make_float2(s[c], s[c + 1]), a2, b2);
-            const float2 v = make_float2(ex2(e.x), ex2(e.y));
-            sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], v);
-            pk[c / 2] = pack_bf16(v.x, v.y);
+          for (int part = 0; part < 2; ++part) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const int k = 32 * part + c;
+              const float2 e = fma2(make_float2(s[k], s[k + 1]), a2, b2);
+              const float2 v = make_float2(ex2(masked(k, e.x)), ex2(masked(k + 1, e.y)));
+              sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], v);
+              pk[c / 2] = pack_bf16(v.x, v.y);
+            }
+            tc::st16_async(tS + 64 + 32 * half + 16 * part, pk);
           }
-          // Over the 32 columns behind the scores of half 1, then over those of half
-          // 0: columns that are read again are not written before
-          tc::st32_async(tS + 64 + 32 * half, pk);
           if (half == 0) break;
-          scores(0);
+          load(0);
         }
         const float2 both = add2(sum[0], sum[1]);
         l += both.x + both.y;
@@ -394,47 +397,75 @@ __global__ void __launch_bounds__(kThr, 1)
         mbar_arrive(bar(M::kPFull + t));
       }
       if (!ok) break;
-      // ---- O / l as bf16 rows through shared memory, lse = (m + log2 l) ln 2
-      const bool live = i < w.n;
-      const float inv = live ? 1.f / l : 0.f;
-      if (x.hi >= 0) {
-        ok = wtw(M::kOFull + t, no & 1);
-        if (!ok) break;
-        ++no;
-        tc::fence_after_sync();
-      }
-#pragma unroll 1
-      for (int hx = 0; hx < kHalves; ++hx) {
-        if (lane == 0) bulk_wait_group_read0();          // the copy before has read the buffer
-        __syncwarp();
-#pragma unroll 1
-        for (int c = 0; c < 64; c += 32) {
-          float o[32];
-          if (x.hi >= 0) tc::ld32_wait(tO + 64 * hx + c, o);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float *y = o + 8 * u;
-            uint4 v = make_uint4(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv),
-                                 pack_bf16(y[4] * inv, y[5] * inv), pack_bf16(y[6] * inv, y[7] * inv));
-            if (!live) v = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(stage + lane * 128 + (((c / 8 + u) ^ (lane & 7)) << 4)) = v;
-          }
-        }
-        if (hx == kHalves - 1 && x.hi >= 0) {
-          tc::fence_before_sync();
-          mbar_arrive(bar(M::kOEmpty + t));
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && x.q0 + 32 * qd < p.T) {         // rows past T are not written
-          tma_store_4d(&tmO, sb + M::kOut + (t * 4 + qd) * 4096, hx * 64, x.h, x.q0 + 32 * qd, w.b);
-          bulk_commit_group();
-        }
-      }
-      if (i < p.T)
-        p.lse[(static_cast<size_t>(w.b) * p.Hq + x.h) * p.T + i] = live ? (m + __log2f(l)) * kLn2 : -INFINITY;
+      ok = wtw(M::kLEmpty + t, (no & 1) ^ 1);
+      if (!ok) break;
+      ++no;
+      *stat = make_float2(m, l);
+      mbar_arrive(bar(M::kLFull + t));
     }
     tc::wait_st();                                       // P on its way when this warp gave up
+  } else {
+    // ============================ outputs ================================
+    // O / l as bf16 rows, lse = (m + log2 l) ln 2, of the tiles in turn, while the
+    // softmax warps work on the next ones (thread = query row)
+    const int qd = warp & 3, row = 32 * qd + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
+    unsigned char *stage = smem + M::kOut + qd * 4096;
+    uint32_t no = 0;                                     // parities of the tiles' outputs so far
+    bool ok = true;
+    for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+      const Unit w = unit_of(p, it);
+#pragma unroll 1
+      for (int t = 0; ok && t < 2; ++t) {
+        const Tile x = tile_of(p, w, t);
+        if (!x.exists) continue;
+        const uint32_t tO = tmem + lanes + kColO + t * kD;
+        const int i = x.q0 + row;
+        float2 ml = make_float2(0.f, 1.f);
+        if (x.hi >= 0) {
+          const uint32_t parity = (no >> t) & 1;
+          no ^= 1u << t;
+          ok = wtw(M::kLFull + t, parity) && wtw(M::kOFull + t, parity);
+          if (!ok) break;
+          tc::fence_after_sync();
+          ml = reinterpret_cast<const float2 *>(smem + M::kStat)[t * 128 + row];
+          mbar_arrive(bar(M::kLEmpty + t));
+        }
+        const bool live = i < w.n;
+        const float inv = 1.f / ml.y;
+#pragma unroll 1
+        for (int hx = 0; hx < kHalves; ++hx) {
+          if (lane == 0) bulk_wait_group_read0();        // the copy before has read the buffer
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            float o[32];
+            if (x.hi >= 0) tc::ld32_wait(tO + 64 * hx + c, o);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float *y = o + 8 * u;
+              uint4 v = make_uint4(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv),
+                                   pack_bf16(y[4] * inv, y[5] * inv), pack_bf16(y[6] * inv, y[7] * inv));
+              if (!live) v = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4 *>(stage + lane * 128 + (((c / 8 + u) ^ (lane & 7)) << 4)) = v;
+            }
+          }
+          if (hx == kHalves - 1 && x.hi >= 0) {
+            tc::fence_before_sync();
+            mbar_arrive(bar(M::kOEmpty + t));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && x.q0 + 32 * qd < p.T) {       // rows past T are not written
+            tma_store_4d(&tmO, sb + M::kOut + qd * 4096, hx * 64, x.h, x.q0 + 32 * qd, w.b);
+            bulk_commit_group();
+          }
+        }
+        if (i < p.T)
+          p.lse[(static_cast<size_t>(w.b) * p.Hq + x.h) * p.T + i] = live ? (ml.x + __log2f(ml.y)) * kLn2 : -INFINITY;
+        __syncwarp();
+      }
+    }
     if (lane == 0) bulk_wait_group_read0();
   }
   tc::fence_before_sync();
@@ -474,7 +505,7 @@ cudaError_t launch_window_fwd(const WindowArgs &a, const WaitCtl &w, cudaStream_
   p.per_head = p.pair_heads ? p.nqb : (p.nqb + 1) / 2;
   const long long units = static_cast<long long>(a.B) * (p.pair_heads ? a.Hq / 2 : a.Hq);
   const long long items = units * p.per_head;
-  if (items > 0x7fffffffLL) {
+  if (items > 0x7fff0000LL || p.per_head > 0x7fff0000 / kHeadGroup) {
     *why = "grid too large";
     return cudaErrorNotSupported;
   }
@@ -483,6 +514,11 @@ cudaError_t launch_window_fwd(const WindowArgs &a, const WaitCtl &w, cudaStream_
   p.sink_blocks = (p.sinks + kBlk - 1) / kBlk;
   p.scale = a.scale;
   p.wait = w;
+  p.by_group = Div::by(kHeadGroup * p.per_head);
+  p.by_width = Div::by(kHeadGroup);
+  p.by_last = Div::by(std::max(1, p.units % kHeadGroup));
+  p.by_heads = Div::by(p.pair_heads ? a.Hq / 2 : a.Hq);
+  p.by_g = Div::by(p.G);
   const int grid = static_cast<int>(std::min<long long>(items, sms));
   return a.D == 64 ? launch<64>(a, p, grid, st, why) : launch<128>(a, p, grid, st, why);
 }
