@@ -318,34 +318,44 @@ __global__ void __launch_bounds__(kThr, 1)
         if (!ok) break;
         ++ns;
         tc::fence_after_sync();
-        // 64 columns at a time, each with its mask: one loop for whole and cut blocks,
-        // which stays in the instruction cache.  Halves that no row of the warp sees are
-        // left out.
+        // 64 columns at a time, in loops of their own for whole blocks and for cut ones,
+        // whose halves that no row of the warp sees are left out
         float s[64];
         uint32_t see[2];
-        auto load = [&](int half) -> bool {
-          see[0] = see[1] = 0xffffffffu;
-          if (!full) {
-            const int end = i - k0 + 1 - 64 * half, first = end - p.window, stay = min(p.sinks - k0 - 64 * half, end);
-#pragma unroll
-            for (int wd = 0; wd < 2; ++wd)
-              see[wd] = (below(end - 32 * wd) & ~below(first - 32 * wd)) | below(stay - 32 * wd);
-            if (!__any_sync(0xffffffffu, (see[0] | see[1]) != 0)) return false;
-          }
+        auto load = [&](int half) {
           float(&lo)[32] = *reinterpret_cast<float(*)[32]>(&s[0]);
           float(&hi)[32] = *reinterpret_cast<float(*)[32]>(&s[32]);
           tc::ld32x2_wait(tS + 64 * half, tS + 64 * half + 32, lo, hi);
+        };
+        auto load_cut = [&](int half) -> bool {
+          const int end = i - k0 + 1 - 64 * half, first = end - p.window, stay = min(p.sinks - k0 - 64 * half, end);
+#pragma unroll
+          for (int wd = 0; wd < 2; ++wd)
+            see[wd] = (below(end - 32 * wd) & ~below(first - 32 * wd)) | below(stay - 32 * wd);
+          if (!__any_sync(0xffffffffu, (see[0] | see[1]) != 0)) return false;
+          load(half);
           return true;
         };
         auto masked = [&](int c, float v) -> float { return see[c >> 5] & (1u << (c & 31)) ? v : -INFINITY; };
         float top = -INFINITY;
+        if (full) {
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (!load(half)) continue;
-          float u[2] = {top, -INFINITY};
+          for (int half = 0; half < 2; ++half) {
+            load(half);
+            float u[4] = {top, s[0], s[1], s[2]};
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) u[(c >> 1) & 1] = max3(u[(c >> 1) & 1], masked(c, s[c]), masked(c + 1, s[c + 1]));
-          top = fmaxf(u[0], u[1]);
+            for (int c = 3; c + 1 < 64; c += 2) u[(c >> 1) & 3] = max3(u[(c >> 1) & 3], s[c], s[c + 1]);
+            top = max3(max3(u[0], u[1], s[63]), u[2], u[3]);
+          }
+        } else {
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            if (!load_cut(half)) continue;
+            float u[2] = {top, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) u[(c >> 1) & 1] = max3(u[(c >> 1) & 1], masked(c, s[c]), masked(c + 1, s[c + 1]));
+            top = fmaxf(u[0], u[1]);
+          }
         }
         if (top > -INFINITY) top *= sl2;
         const bool need = top > m + kRescale;
@@ -372,23 +382,43 @@ __global__ void __launch_bounds__(kThr, 1)
         const float2 a2 = make_float2(sl2, sl2);
         // P of keys 2 c, 2 c + 1 in column 64 + c, from the last keys to the first:
         // what it overwrites has been read for the last time
+        if (full) {
 #pragma unroll 1
-        for (int half = 1;; half = 0) {
+          for (int half = 1;; half = 0) {
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            uint32_t pk[16];
+            for (int part = 0; part < 2; ++part) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const int k = 32 * part + c;
-              const float2 e = fma2(make_float2(s[k], s[k + 1]), a2, b2);
-              const float2 v = make_float2(ex2(masked(k, e.x)), ex2(masked(k + 1, e.y)));
-              sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], v);
-              pk[c / 2] = pack_bf16(v.x, v.y);
+              for (int c = 0; c < 32; c += 2) {
+                const float2 e = fma2(make_float2(s[32 * part + c], s[32 * part + c + 1]), a2, b2);
+                const float2 v = make_float2(ex2(e.x), ex2(e.y));
+                sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], v);
+                pk[c / 2] = pack_bf16(v.x, v.y);
+              }
+              tc::st16_async(tS + 64 + 32 * half + 16 * part, pk);
             }
-            tc::st16_async(tS + 64 + 32 * half + 16 * part, pk);
+            if (half == 0) break;
+            load(0);
           }
-          if (half == 0) break;
-          load(0);
+        } else {
+#pragma unroll 1
+          for (int half = 1;; half = 0) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                const int k = 32 * part + c;
+                const float2 e = fma2(make_float2(s[k], s[k + 1]), a2, b2);
+                const float2 v = make_float2(ex2(masked(k, e.x)), ex2(masked(k + 1, e.y)));
+                sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], v);
+                pk[c / 2] = pack_bf16(v.x, v.y);
+              }
+              tc::st16_async(tS + 64 + 32 * half + 16 * part, pk);
+            }
+            if (half == 0) break;
+            load_cut(0);
+          }
         }
         const float2 both = add2(sum[0], sum[1]);
         l += both.x + both.y;
