@@ -84,7 +84,7 @@ struct BwdParams {
   const int *lengths;
   float *ndelta, *nlse2;          // [B][Hq][Tp]
   __nv_bfloat16 *ds;              // [B][Hq][tiles]
-  float *parts;                   // [units][slots][2][128][D]: dV, dK
+  float *parts;                   // [units][slots][2: dV, dK][D / 4][128 keys][4]
   __nv_bfloat16 *dq, *dk, *dv;
   int B, T, Tp, Hq, Hkv, G;
   long long o_stride, dk_stride, dv_stride, tiles;
@@ -178,6 +178,13 @@ struct KvSmem {
   static_assert(kBytes <= 232448, "kv kernel shared memory");
 };
 
+// Item of a CTA's r-th round: rounds go through the CTAs back and forth, so that
+// items whose lengths repeat with a period that divides the grid spread over all.
+__device__ __forceinline__ int nth_item(int r) {
+  const int c = blockIdx.x, n = gridDim.x;
+  return r * n + ((r & 1) ? n - 1 - c : c);
+}
+
 struct KvItem {
   int b, kvh, kb, part, nparts, n, qn;   // tokens, live query blocks per head
   int it0, it1;                          // its pairs: (head, query block) = it / qn, it % qn
@@ -219,10 +226,12 @@ __device__ __noinline__ KvItem kv_item(const BwdParams &p, int idx) {
 // The pairs of a CTA's items, one after the other.
 struct KvStream {
   KvItem w;
-  int idx, it;
+  int round, it;
   bool valid;
   __device__ __forceinline__ void find(const BwdParams &p) {
-    for (; idx < p.items; idx += gridDim.x) {
+    for (; round * static_cast<int>(gridDim.x) < p.items; ++round) {
+      const int idx = nth_item(round);
+      if (idx >= p.items) continue;
       w = kv_item(p, idx);
       if (w.it0 < w.it1) {
         it = w.it0;
@@ -233,12 +242,12 @@ struct KvStream {
     valid = false;
   }
   __device__ __forceinline__ void begin(const BwdParams &p) {
-    idx = blockIdx.x;
+    round = 0;
     find(p);
   }
   __device__ __forceinline__ void next(const BwdParams &p) {
     if (++it < w.it1) return;
-    idx += gridDim.x;
+    ++round;
     find(p);
   }
   __device__ __forceinline__ bool opens() const { return it == w.it0; }
@@ -357,10 +366,12 @@ __global__ void __launch_bounds__(kThr, 1)
     auto dooff = [](int n) -> uint64_t { return static_cast<uint64_t>((n % M::kDOs) * M::kDOPitch) >> 4; };
     int items = 0, na = 0;                  // items whose output was begun; K (V) blocks waited for
     // pairs of the next item that has some; 0: there is none
-    int idx = blockIdx.x;
+    int round = 0;
     auto next_item = [&]() -> int {
       int pairs = 0;
-      for (; pairs == 0 && idx < p.items; idx += gridDim.x) {
+      for (; pairs == 0 && round * static_cast<int>(gridDim.x) < p.items; ++round) {
+        const int idx = nth_item(round);
+        if (idx >= p.items) continue;
         const KvItem w = kv_item(p, idx);
         pairs = __shfl_sync(0xffffffffu, w.it1 - w.it0, 0);
       }
@@ -552,7 +563,7 @@ __global__ void __launch_bounds__(kThr, 1)
       if (!s.closes()) continue;
       // ---- the item's dV and dK (scaled): thread (key, half ch of the components)
       const bool whole = w.nparts == 1;
-      float *part = whole ? nullptr : p.parts + (w.slot * 2 * kBlk + j) * kD + ch * (kD / 2);
+      float4 *part = reinterpret_cast<float4 *>(p.parts) + (w.slot * 2 * (kD / 4) + ch * (kD / 8)) * kBlk + j;
 #pragma unroll 1
       for (int x = 0; x < 2 && ok; ++x) {
         ok = wtw(x == 0 ? M::kDVFinal : M::kDKFinal, items & 1);
@@ -584,9 +595,9 @@ __global__ void __launch_bounds__(kThr, 1)
           fence_proxy_async_smem();
           mbar_arrive(bar(M::kEpi));
         } else {
-          float4 *dst = reinterpret_cast<float4 *>(part + static_cast<size_t>(x) * kBlk * kD);
+          float4 *dst = part + x * (kD / 4) * kBlk;   // a warp's 32 keys next to one another
 #pragma unroll
-          for (int u = 0; u < kD / 8; ++u) dst[u] = make_float4(v[4 * u] * f, v[4 * u + 1] * f, v[4 * u + 2] * f, v[4 * u + 3] * f);
+          for (int u = 0; u < kD / 8; ++u) dst[u * kBlk] = make_float4(v[4 * u] * f, v[4 * u + 1] * f, v[4 * u + 2] * f, v[4 * u + 3] * f);
         }
       }
       ++items;
@@ -630,19 +641,19 @@ __global__ void __launch_bounds__(kJoinThr) window_join_kernel(const __grid_cons
   // of fewer pairs than parts only the first parts have one and were written
   const int all = p.G * w.qn;
   for (int e = threadIdx.x; e < 2 * 32 * kD / 4; e += kJoinThr) {
-    const int x = e / (32 * kD / 4), r = 32 * quarter + e / (kD / 4) % 32, c = e % (kD / 4) * 4;
+    const int x = e / (32 * kD / 4), r = 32 * quarter + e % 32, c = e / 32 % (kD / 4);
     const int tok = kb * kBlk + r;
     if (tok >= p.T) continue;
-    const float *src = p.parts + ((w.slot * 2 + x) * kBlk + r) * kD + c;
+    const float4 *src = reinterpret_cast<const float4 *>(p.parts) + ((w.slot * 2 + x) * (kD / 4) + c) * kBlk + r;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int i = 0; i < w.nparts; ++i) {
       if (i >= all) break;
-      const float4 v = *reinterpret_cast<const float4 *>(src + static_cast<size_t>(i) * 2 * kBlk * kD);
+      const float4 v = src[static_cast<size_t>(i) * 2 * (kD / 4) * kBlk];
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
     const long long at = static_cast<long long>(w.b) * p.T + tok;
-    __nv_bfloat16 *dst = (x == 0 ? p.dv + at * p.dv_stride : p.dk + at * p.dk_stride) + static_cast<size_t>(w.kvh) * kD + c;
+    __nv_bfloat16 *dst = (x == 0 ? p.dv + at * p.dv_stride : p.dk + at * p.dk_stride) + static_cast<size_t>(w.kvh) * kD + 4 * c;
     *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
   }
 }
@@ -709,7 +720,8 @@ __global__ void __launch_bounds__(kThr, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the dS tiles come from the kv kernel
     int g = 0, raw = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; ok && idx < p.dq_items; idx += gridDim.x) {
+    for (int round = 0, idx = nth_item(0); ok && round * static_cast<int>(gridDim.x) < p.dq_items; idx = nth_item(++round)) {
+      if (idx >= p.dq_items) continue;
       const DqItem w = dq_item(p, idx);
       const unsigned char *tiles = reinterpret_cast<const unsigned char *>(p.ds) +
                                    (static_cast<long long>(w.b) * p.Hq + w.h) * p.tiles * kTileBytes;
@@ -741,7 +753,8 @@ __global__ void __launch_bounds__(kThr, 1)
     int g = 0, j = 0, gave_up = 0;
     auto wti = [&](int slot, uint32_t parity) -> bool { return wait_issuer(wts, slot, parity, gave_up); };
     bool ok = may_wait(p.wait, abort_flag, kSiteWinDq, M::kFull);
-    for (int idx = blockIdx.x; ok && idx < p.dq_items; idx += gridDim.x) {
+    for (int round = 0, idx = nth_item(0); ok && round * static_cast<int>(gridDim.x) < p.dq_items; idx = nth_item(++round)) {
+      if (idx >= p.dq_items) continue;
       const DqItem w = dq_item(p, idx);
       if (w.steps == 0) continue;
       const int a = j & 1;
@@ -772,7 +785,8 @@ __global__ void __launch_bounds__(kThr, 1)
     const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
     unsigned char *stage = smem + M::kOut + (warp - 4) * 4096;
     int j = 0;
-    for (int idx = blockIdx.x; idx < p.dq_items; idx += gridDim.x) {
+    for (int round = 0, idx = nth_item(0); round * static_cast<int>(gridDim.x) < p.dq_items; idx = nth_item(++round)) {
+      if (idx >= p.dq_items) continue;
       const DqItem w = dq_item(p, idx);
       const int a = j & 1, row = w.m * kBlk + 32 * qd + lane;
       if (w.steps > 0) {
