@@ -45,6 +45,12 @@ struct Div {
   }
 };
 
+// The lowest x of 32 bits.
+__device__ __forceinline__ uint32_t below(int x) {
+  const int n = min(max(x, 0), 32);
+  return n == 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
 // 2^x on the MUFU unit, to some 2^-22; 2^-inf = 0.
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -39,7 +39,8 @@ namespace {
 
 using namespace win;
 
-constexpr int kThr = 384;
+constexpr int kThr = 384;        // dq kernel
+constexpr int kKvThr = 512;      // kv kernel
 constexpr int kTileBytes = kBlk * kBlk * 2;    // one dS^T tile: [2 query halves][128 keys][64 queries]
 
 // Which blocks meet, and where their dS tiles stand within a head.
@@ -92,6 +93,7 @@ struct BwdParams {
   int first_parts, parts_each;    // CTAs per key block: first tokens', others
   int per_unit, slots;            // items and part slots per (batch, KV head)
   int items, dq_items;
+  Div by_unit, by_hkv, by_first, by_each;   // per_unit, Hkv, first_parts, parts_each
   float scale;
   WaitCtl wait;
 };
@@ -170,8 +172,8 @@ struct KvSmem {
   static constexpr int kBar = kDelta + kDOs * 512;
   enum {
     kKFull = 0, kVFull, kKEmpty, kVEmpty, kQFull, kQEmpty = kQFull + kQs, kDOFull = kQEmpty + kQs,
-    kDOEmpty = kDOFull + kDOs, kSFull = kDOEmpty + kDOs, kDPFull, kPFull, kDSFull, kDVDone, kStaged,
-    kDVFinal = kStaged + 4, kDKFinal, kAccFree, kStageFree, kEpi, kRaw, kFinal, kBars
+    kDOEmpty = kDOFull + kDOs, kSFull = kDOEmpty + kDOs, kDPFull, kPFull, kDSFull, kDSRead, kDVDone, kDKFinal = kDVDone + kDOs,
+    kAccFree, kRaw, kFinal, kBars
   };
   static constexpr int kTmem = kBar + kBars * 8, kAbort = kTmem + 4;
   static constexpr int kBytes = kAbort + 4;                  // the kernel checks that the base is aligned
@@ -193,71 +195,59 @@ struct KvItem {
 
 __device__ __noinline__ KvItem kv_item(const BwdParams &p, int idx) {
   KvItem r;
-  const int unit = idx / p.per_unit;
-  int rem = idx - unit * p.per_unit;
-  r.b = unit / p.Hkv;
-  r.kvh = unit - r.b * p.Hkv;
+  const int unit = p.by_unit(idx);          // idx becomes the place in the unit
+  r.kvh = unit;
+  r.b = p.by_hkv(r.kvh);
   const int head = p.g.first * p.first_parts;
-  if (rem < head) {
-    r.kb = rem / p.first_parts;
-    r.part = rem - r.kb * p.first_parts;
-    r.nparts = p.first_parts;
-    r.slot = rem;
-  } else {
-    const int first_slots = p.first_parts > 1 ? head : 0;
-    rem -= head;
-    r.kb = rem / p.parts_each;
-    r.part = rem - r.kb * p.parts_each;
-    r.kb += p.g.first;
-    r.nparts = p.parts_each;
-    r.slot = first_slots + rem;
-  }
-  r.slot += static_cast<long long>(unit) * p.slots;
+  const bool lead = idx < head;
+  r.slot = static_cast<long long>(unit) * p.slots + (lead ? idx : (p.first_parts > 1 ? head : 0) + idx - head);
+  r.part = lead ? idx : idx - head;
+  const Div &div = lead ? p.by_first : p.by_each;
+  r.kb = div(r.part) + (lead ? 0 : p.g.first);
+  r.nparts = div.d;
   r.n = tokens_of(p.lengths, r.b, p.T);
   const int live = (r.n + kBlk - 1) / kBlk;
   r.qn = max(0, min(r.kb + p.g.queries(r.kb), live) - r.kb);
-  const int all = p.G * r.qn;
-  const unsigned each = static_cast<unsigned>(all) / r.nparts, extra = all - each * r.nparts;   // the first `extra` have one more
-  r.it0 = r.part * each + min(static_cast<unsigned>(r.part), extra);
-  r.it1 = r.it0 + each + (static_cast<unsigned>(r.part) < extra);
+  int extra = p.G * r.qn;                   // the first `extra` parts have one more
+  const int each = div(extra);
+  r.it0 = r.part * each + min(r.part, extra);
+  r.it1 = r.it0 + each + (r.part < extra);
   return r;
 }
 
 // The pairs of a CTA's items, one after the other.
 struct KvStream {
   KvItem w;
-  int round, it;
+  int round, it, h, qb;       // pair `it` of the item: query head h, block qb of queries
   bool valid;
   __device__ __forceinline__ void find(const BwdParams &p) {
-    for (; round * static_cast<int>(gridDim.x) < p.items; ++round) {
+    valid = false;
+    for (; !valid && round * static_cast<int>(gridDim.x) < p.items; ++round) {
       const int idx = nth_item(round);
       if (idx >= p.items) continue;
       w = kv_item(p, idx);
-      if (w.it0 < w.it1) {
-        it = w.it0;
-        valid = true;
-        return;
-      }
+      if (w.it0 == w.it1) continue;
+      it = w.it0;
+      h = it / w.qn;
+      qb = w.kb + it - h * w.qn;
+      h += w.kvh * p.G;
+      valid = true;
     }
-    valid = false;
   }
   __device__ __forceinline__ void begin(const BwdParams &p) {
     round = 0;
     find(p);
   }
   __device__ __forceinline__ void next(const BwdParams &p) {
-    if (++it < w.it1) return;
-    ++round;
-    find(p);
+    if (++it == w.it1) return find(p);
+    if (++qb == w.kb + w.qn) qb = w.kb, ++h;
   }
   __device__ __forceinline__ bool opens() const { return it == w.it0; }
   __device__ __forceinline__ bool closes() const { return it == w.it1 - 1; }
-  __device__ __forceinline__ int head(const BwdParams &p) const { return w.kvh * p.G + it / w.qn; }
-  __device__ __forceinline__ int block() const { return w.kb + it % w.qn; }
 };
 
 template <int kD>
-__global__ void __launch_bounds__(kThr, 1)
+__global__ void __launch_bounds__(kKvThr, 1)
     window_kv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmdK, const __grid_constant__ CUtensorMap tmdV,
@@ -281,8 +271,9 @@ __global__ void __launch_bounds__(kThr, 1)
   if (tid == 0) {
     for (int i = 0; i < M::kBars; ++i) {
       int count = 1;
-      if (i == M::kPFull || i == M::kDSFull || i == M::kAccFree || i == M::kEpi) count = 256;   // every softmax thread
-      if (i >= M::kStaged && i < M::kStaged + 4) count = 128;
+      if (i == M::kPFull || i == M::kDSFull) count = 256;                            // softmax threads
+      if (i == M::kDSRead || i == M::kAccFree) count = 128;                          // output threads
+      if (i == M::kDOEmpty || i == M::kDOEmpty + 1) count = 4;                       // output warps
       if (i == M::kFinal) count = 2;
       mbar_init(bar(i), count);
     }
@@ -320,7 +311,7 @@ __global__ void __launch_bounds__(kThr, 1)
     KvStream s;
     for (s.begin(p); s.valid; s.next(p)) {
       const KvItem &w = s.w;
-      const int h = s.head(p), q0 = s.block() * kBlk, k0 = w.kb * kBlk;
+      const int h = s.h, q0 = s.qb * kBlk, k0 = w.kb * kBlk;
       const int qs = nq % M::kQs, ds = nd % M::kDOs;
       const size_t ro = (static_cast<size_t>(w.b) * p.Hq + h) * p.Tp + q0;
       if (s.opens()) {
@@ -392,8 +383,8 @@ __global__ void __launch_bounds__(kThr, 1)
         tc::fence_after_sync();
         if (tc::elect()) {
           tc::product_ts<2, 32>(tY, tX, dBm + (first ? dooff(n) : qoff(n)), id_kv, !opens);
-          tc::commit(bar(first ? M::kDVDone : M::kQEmpty + n % M::kQs));
-          if (closes) tc::commit(bar(first ? M::kDVFinal : M::kDKFinal));
+          tc::commit(bar(first ? M::kDVDone + n % M::kDOs : M::kQEmpty + n % M::kQs));
+          if (closes && !first) tc::commit(bar(M::kDKFinal));
         }
         __syncwarp();
       }
@@ -401,6 +392,7 @@ __global__ void __launch_bounds__(kThr, 1)
       if (then > 0) {
         if (closes && !wti(first ? M::kKFull : M::kVFull, na++ & 1)) break;
         if (!wti(first ? M::kQFull + m % M::kQs : M::kDOFull + m % M::kDOs, (m / (first ? M::kQs : M::kDOs)) & 1)) break;
+        if (!first && n >= 0 && !wti(M::kDSRead, n & 1)) break;   // the dS tile has been read for the workspace
         tc::fence_after_sync();
         if (tc::elect()) {
           tc::product_k<kD>(tX, dA, dBk + (first ? qoff(m) : dooff(m)), id_sdp);
@@ -416,44 +408,7 @@ __global__ void __launch_bounds__(kThr, 1)
     tc::commit_w(bar(M::kFinal));
     report_issuer(wts, gave_up);
     wait_landed(bar(M::kFinal), 0);   // every product of both has completed
-  } else if (warp == 3) {
-    // ============================ copies out ===========================
-    KvStream s;
-    int n = 0, epi = 0;
-    bool ok = true;
-    for (s.begin(p); ok && s.valid; s.next(p), ++n) {
-      const KvItem &w = s.w;
-      const int slot = n % M::kDOs, qi = s.block() - w.kb;
-      const uint32_t at = sb + M::kDO + slot * M::kDOPitch;
-      unsigned char *dst = reinterpret_cast<unsigned char *>(p.ds) +
-                           ((static_cast<long long>(w.b) * p.Hq + s.head(p)) * p.tiles + p.g.tile0(w.kb) + qi) * kTileBytes;
-#pragma unroll 1
-      for (int hf = 0; hf < 2 && ok; ++hf) {
-        ok = wtw(M::kStaged + 2 * slot + hf, (n / M::kDOs) & 1);
-        if (ok && lane == 0) {
-          bulk_store(dst + hf * (kTileBytes / 2), at + hf * (kTileBytes / 2), kTileBytes / 2);
-          bulk_commit_group();
-        }
-      }
-      if (!ok) break;
-      if (lane == 0) bulk_wait_group_read0();
-      if (s.closes() && w.nparts == 1) {
-        // dV, then dK, as bf16 rows in this slot
-#pragma unroll 1
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (lane == 0) mbar_arrive(bar(M::kStageFree));
-          ok = wtw(M::kEpi, epi++ & 1);
-          if (!ok || lane != 0) continue;
-          for (int hx = 0; hx < kHalves; ++hx)
-            tma_store_4d(x == 0 ? &tmdV : &tmdK, at + hx * 16384, hx * 64, w.kvh, w.kb * kBlk, w.b);
-          bulk_commit_group();
-          bulk_wait_group_read0();
-        }
-      }
-      if (ok && lane == 0) mbar_arrive(bar(M::kDOEmpty + slot));
-    }
-    if (lane == 0) bulk_wait_group0();
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 12) {
     // ============================ softmax ================================
     // Warp w: keys 32 (w % 4) .. of the block (thread = key), half (w - 4) / 4 of its
     // 128 queries.
@@ -464,18 +419,21 @@ __global__ void __launch_bounds__(kThr, 1)
     const float2 sl22 = make_float2(sl2, sl2);
     const uint32_t tS = tmem + lanes + kColS + 64 * ch, tD = tmem + lanes + kColDP + 64 * ch;
     KvStream s;
-    int n = 0, items = 0, epi = 0;
-    bool ok = true;
-    for (s.begin(p); ok && s.valid; s.next(p), ++n) {
-      const KvItem &w = s.w;
-      const int k0 = w.kb * kBlk, key = k0 + j, qblk = s.block() * kBlk, q0 = qblk + 64 * ch;
+    int n = 0;
+    for (s.begin(p); s.valid; s.next(p), ++n) {
+      const int k0 = s.w.kb * kBlk, key = k0 + j, qblk = s.qb * kBlk, q0 = qblk + 64 * ch;
       const float *nl = reinterpret_cast<const float *>(smem + M::kLse + (n % M::kQs) * 512) + 64 * ch;
       const float *nd = reinterpret_cast<const float *>(smem + M::kDelta + (n % M::kDOs) * 512) + 64 * ch;
+      // this half's queries that see the key; all of them where the block is whole
+      uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+      if (!(qblk > k0 && (qblk + kBlk - 1 - k0 < p.g.window || p.g.sinks - k0 >= kBlk))) {
+        const int first = key - q0, end = key < p.g.sinks ? 64 : first + p.g.window;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) see[x] = below(end - 32 * x) & ~below(first - 32 * x);
+      }
       // ---- P = 2^(S scale log2 e - lse log2 e)
       float2 P[32];
-      uint32_t pk[32];
-      ok = wtw(M::kSFull, n & 1);
-      if (!ok) break;
+      if (!wtw(M::kSFull, n & 1)) break;
       tc::fence_after_sync();
       {
         float(&lo)[32] = *reinterpret_cast<float(*)[32]>(&P[0]);
@@ -483,134 +441,159 @@ __global__ void __launch_bounds__(kThr, 1)
         tc::ld32x2_wait(tS, tS + 32, lo, hi);
       }
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        const float4 l4 = *reinterpret_cast<const float4 *>(nl + 2 * e);
-        const float2 x = fma2(P[e], sl22, make_float2(l4.x, l4.y)), y = fma2(P[e + 1], sl22, make_float2(l4.z, l4.w));
-        P[e] = make_float2(ex2(x.x), ex2(x.y));
-        P[e + 1] = make_float2(ex2(y.x), ex2(y.y));
-      }
-      // every query of the block sees every key of it
-      const bool full = qblk > k0 && (qblk + kBlk - 1 - k0 < p.g.window || p.g.sinks - k0 >= kBlk);
-      if (!full) {
-        const int first = key - q0, end = key < p.g.sinks ? 64 : first + p.g.window;   // of this half's queries
-        uint32_t see[2];
+      for (int c = 0; c < 4; ++c) {   // chunk c of 16 queries: columns 32 (c / 2) + 8 (c % 2)
+        uint32_t pk[8];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int a = min(max(first - 32 * x, 0), 32), z = min(max(end - 32 * x, 0), 32);
-          see[x] = (z == 32 ? 0xffffffffu : (1u << z) - 1u) & ~(a == 32 ? 0xffffffffu : (1u << a) - 1u);
+        for (int e = 0; e < 8; e += 2) {
+          const float4 l4 = *reinterpret_cast<const float4 *>(nl + 16 * c + 2 * e);
+          float2 &a = P[8 * c + e], &b = P[8 * c + e + 1];
+          a = fma2(a, sl22, make_float2(l4.x, l4.y));
+          b = fma2(b, sl22, make_float2(l4.z, l4.w));
+          const uint32_t m = see[c >> 1] >> ((16 * c + 2 * e) & 31);
+          a = make_float2(m & 1u ? ex2(a.x) : 0.f, m & 2u ? ex2(a.y) : 0.f);
+          b = make_float2(m & 4u ? ex2(b.x) : 0.f, m & 8u ? ex2(b.y) : 0.f);
+          pk[e] = pack_bf16(a.x, a.y);
+          pk[e + 1] = pack_bf16(b.x, b.y);
         }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          P[e].x = (see[e >> 4] >> (2 * e & 31)) & 1u ? P[e].x : 0.f;
-          P[e].y = (see[e >> 4] >> ((2 * e + 1) & 31)) & 1u ? P[e].y : 0.f;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) pk[e] = pack_bf16(P[e].x, P[e].y);
-      {
-        const uint32_t(&c0)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&pk[0]);
-        const uint32_t(&c1)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&pk[8]);
-        const uint32_t(&c2)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&pk[16]);
-        const uint32_t(&c3)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&pk[24]);
-        tc::st8x2_async(tS, c0, tS + 8, c1);
-        tc::st8x2_async(tS + 32, c2, tS + 40, c3);
+        tc::st8_async(tS + (c >> 1) * 32 + (c & 1) * 8, pk);
       }
       tc::wait_st();
       tc::fence_before_sync();
       mbar_arrive(bar(M::kPFull));
-      // ---- dS = P (dP - delta), over dP and for the workspace
-      ok = wtw(M::kDPFull, n & 1);
-      if (!ok) break;
+      // ---- dS = P (dP - delta), over dP
+      if (!wtw(M::kDPFull, n & 1)) break;
       tc::fence_after_sync();
-      uint4 U[8];   // this key's dS^T as eight 16-byte units of 8 queries
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float d[32];
         tc::ld32_wait(tD + 32 * half, d);
-        uint32_t dk[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 d4 = *reinterpret_cast<const float4 *>(nd + 32 * half + e);
-          const float2 x = add2(make_float2(d[e], d[e + 1]), make_float2(d4.x, d4.y));
-          const float2 y = add2(make_float2(d[e + 2], d[e + 3]), make_float2(d4.z, d4.w));
-          const float2 a = P[16 * half + e / 2], c = P[16 * half + e / 2 + 1];
-          dk[e / 2] = pack_bf16(a.x * x.x, a.y * x.y);
-          dk[e / 2 + 1] = pack_bf16(c.x * y.x, c.y * y.y);
-        }
-        {
-          const uint32_t(&c0)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&dk[0]);
-          const uint32_t(&c1)[8] = *reinterpret_cast<const uint32_t(*)[8]>(&dk[8]);
-          tc::st8x2_async(tD + 32 * half, c0, tD + 32 * half + 8, c1);
-        }
+        for (int c = 0; c < 2; ++c) {
+          uint32_t pk[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) U[4 * half + u] = make_uint4(dk[4 * u], dk[4 * u + 1], dk[4 * u + 2], dk[4 * u + 3]);
+          for (int e = 0; e < 8; e += 2) {
+            const int i = 16 * c + 2 * e;
+            const float4 d4 = *reinterpret_cast<const float4 *>(nd + 32 * half + i);
+            const float2 x = add2(make_float2(d[i], d[i + 1]), make_float2(d4.x, d4.y));
+            const float2 y = add2(make_float2(d[i + 2], d[i + 3]), make_float2(d4.z, d4.w));
+            const float2 a = P[16 * half + i / 2], b = P[16 * half + i / 2 + 1];
+            pk[e] = pack_bf16(a.x * x.x, a.y * x.y);
+            pk[e + 1] = pack_bf16(b.x * y.x, b.y * y.y);
+          }
+          tc::st8_async(tD + 32 * half + 8 * c, pk);
+        }
       }
       tc::wait_st();
       tc::fence_before_sync();
       mbar_arrive(bar(M::kDSFull));
-      // once dV has read dO, its slot stages the dS tile
-      ok = wtw(M::kDVDone, n & 1);
-      if (!ok) break;
-      tc::fence_after_sync();
-      unsigned char *slot = smem + M::kDO + (n % M::kDOs) * M::kDOPitch;
-      {
-        unsigned char *stg = slot + ch * (kTileBytes / 2) + j * 128;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4 *>(stg + ((u ^ (lane & 7)) << 4)) = U[u];
-        fence_proxy_async_smem();
-        mbar_arrive(bar(M::kStaged + 2 * (n % M::kDOs) + ch));   // this query half
-      }
-      if (!s.closes()) continue;
-      // ---- the item's dV and dK (scaled): thread (key, half ch of the components)
-      const bool whole = w.nparts == 1;
-      float4 *part = reinterpret_cast<float4 *>(p.parts) + (w.slot * 2 * (kD / 4) + ch * (kD / 8)) * kBlk + j;
-#pragma unroll 1
-      for (int x = 0; x < 2 && ok; ++x) {
-        ok = wtw(x == 0 ? M::kDVFinal : M::kDKFinal, items & 1);
-        if (!ok) break;
-        tc::fence_after_sync();
-        float v[kD / 2];
-#pragma unroll
-        for (int c = 0; c < kD / 2; c += 32) {
-          float(&y)[32] = *reinterpret_cast<float(*)[32]>(&v[c]);
-          tc::ld32_wait(tmem + lanes + (x == 0 ? kColDV : kColDK) + ch * (kD / 2) + c, y);
-        }
-        if (x == 1) {
-          tc::fence_before_sync();
-          mbar_arrive(bar(M::kAccFree));
-        }
-        const float f = x == 0 ? 1.f : p.scale;
-        if (whole) {
-          ok = wtw(M::kStageFree, epi & 1);
-          if (!ok) break;
-          ++epi;
-#pragma unroll
-          for (int u = 0; u < kD / 16; ++u) {
-            const int unit = ch * (kD / 16) + u;   // of the row's kD / 8 units
-            const float *y = v + 8 * u;
-            *reinterpret_cast<uint4 *>(slot + (unit >> 3) * 16384 + j * 128 + (((unit & 7) ^ (j & 7)) << 4)) =
-                make_uint4(pack_bf16(y[0] * f, y[1] * f), pack_bf16(y[2] * f, y[3] * f), pack_bf16(y[4] * f, y[5] * f),
-                           pack_bf16(y[6] * f, y[7] * f));
-          }
-          fence_proxy_async_smem();
-          mbar_arrive(bar(M::kEpi));
-        } else {
-          float4 *dst = part + x * (kD / 4) * kBlk;   // a warp's 32 keys next to one another
-#pragma unroll
-          for (int u = 0; u < kD / 8; ++u) dst[u * kBlk] = make_float4(v[4 * u] * f, v[4 * u + 1] * f, v[4 * u + 2] * f, v[4 * u + 3] * f);
-        }
-      }
-      ++items;
     }
     tc::wait_st();
+  } else if (warp >= 12) {
+    // ============================ outputs ================================
+    // Warp w: keys 32 (w % 4) .. (thread = key).  Each pair's dS^T goes from TMEM
+    // through the pair's dO slot, once dV has read that, to the workspace; behind an
+    // item's last pair dV and dK go the same way as bf16 rows (or, a part, as fp32).
+    // A warp's rows are 4 KB of each half, which it writes and sends by itself.
+    const int qd = warp & 3, j = 32 * qd + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
+    KvStream s;
+    int n = 0, items = 0;
+    for (s.begin(p); s.valid; s.next(p), ++n) {
+      const KvItem &w = s.w;
+      const uint32_t off = M::kDO + (n % M::kDOs) * M::kDOPitch;
+      unsigned char *rows = smem + off + j * 128;        // of half 0; half 1 is 16 KB behind
+      if (!wtw(M::kDSFull, n & 1)) break;
+      tc::fence_after_sync();
+      uint32_t u[64];                                    // 128 queries, two to a register
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc::ld16_wait(tmem + lanes + kColDP + 32 * c, *reinterpret_cast<uint32_t(*)[16]>(&u[16 * c]));
+      tc::fence_before_sync();
+      mbar_arrive(bar(M::kDSRead));
+      // per slot: dV may be a pair ahead of this warp, but not of this slot
+      if (!wtw(M::kDVDone + n % M::kDOs, (n / M::kDOs) & 1)) break;
+#pragma unroll
+      for (int x = 0; x < 16; ++x)
+        *reinterpret_cast<uint4 *>(rows + (x >> 3) * 16384 + (((x & 7) ^ (j & 7)) << 4)) =
+            make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        unsigned char *dst = reinterpret_cast<unsigned char *>(p.ds) +
+                             ((static_cast<long long>(w.b) * p.Hq + s.h) * p.tiles + p.g.tile0(w.kb) + s.qb - w.kb) * kTileBytes +
+                             qd * 4096;
+        bulk_store(dst, sb + off + qd * 4096, 4096);
+        bulk_store(dst + 16384, sb + off + 16384 + qd * 4096, 4096);
+        bulk_commit_group();
+      }
+      bool ok = true;
+      if (s.closes()) {
+        tc::fence_after_sync();
+        float4 *part = reinterpret_cast<float4 *>(p.parts) + w.slot * 2 * (kD / 4) * kBlk + j;
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {                    // dV, dK
+          if (x == 1) {
+            ok = wtw(M::kDKFinal, items & 1);
+            if (!ok) break;
+            tc::fence_after_sync();
+          }
+          const float f = x == 0 ? 1.f : p.scale;
+          const uint32_t from = tmem + lanes + (x == 0 ? kColDV : kColDK);
+          if (w.nparts == 1) {
+#pragma unroll
+            for (int c = 0; c < kD; c += 32) {
+              float v[32];
+              tc::ld32_wait(from + c, v);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) u[c / 2 + e] = pack_bf16(v[2 * e] * f, v[2 * e + 1] * f);
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 32) {
+              float v[32];
+              tc::ld32_wait(from + c, v);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)                // a warp's 32 keys next to one another
+                part[(x * (kD / 4) + c / 4 + e) * kBlk] = make_float4(v[4 * e] * f, v[4 * e + 1] * f, v[4 * e + 2] * f, v[4 * e + 3] * f);
+            }
+          }
+          if (x == 1) {                                  // the next item's products may begin
+            tc::fence_before_sync();
+            mbar_arrive(bar(M::kAccFree));
+          }
+          if (w.nparts > 1) continue;
+          if (lane == 0) bulk_wait_group_read0();        // the copies out of the rows have read them
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < kD / 8; ++e)
+            *reinterpret_cast<uint4 *>(rows + (e >> 3) * 16384 + (((e & 7) ^ (j & 7)) << 4)) =
+                make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          const int row0 = w.kb * kBlk + 32 * qd;
+          if (lane == 0 && row0 < p.T) {                 // rows past T are not written
+            for (int hx = 0; hx < kHalves; ++hx)
+              tma_store_4d(x == 0 ? &tmdV : &tmdK, sb + off + hx * 16384 + qd * 4096, hx * 64, w.kvh, row0, w.b);
+            bulk_commit_group();
+          }
+        }
+        if (!ok) break;
+        ++items;
+      }
+      if (lane == 0) {
+        bulk_wait_group_read0();
+        mbar_arrive(bar(M::kDOEmpty + n % M::kDOs));
+      }
+      __syncwarp();
+    }
+    if (lane == 0) bulk_wait_group0();
     // key blocks that no query meets (behind the sequence): 0
     for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
       const KvItem w = kv_item(p, idx);
       if (w.it0 < w.it1 || w.nparts > 1 || w.kb * kBlk + j >= p.T) continue;
       const long long tok = static_cast<long long>(w.b) * p.T + w.kb * kBlk + j;
-      const size_t c = static_cast<size_t>(w.kvh) * kD + ch * (kD / 2);
-#pragma unroll
-      for (int u = 0; u < kD / 16; ++u) {
+      const size_t c = static_cast<size_t>(w.kvh) * kD;
+#pragma unroll 1
+      for (int u = 0; u < kD / 8; ++u) {
         reinterpret_cast<uint4 *>(p.dv + tok * p.dv_stride + c)[u] = make_uint4(0, 0, 0, 0);
         reinterpret_cast<uint4 *>(p.dk + tok * p.dk_stride + c)[u] = make_uint4(0, 0, 0, 0);
       }
@@ -871,8 +854,8 @@ cudaError_t launch(const WindowArgs &a, BwdParams &p, const BwdSizes &s, int sms
       !token_map(&k, a.k, a.Hkv, a.T, a.B, kD, a.k_stride, kBlk, why) ||
       !token_map(&v, a.v, a.Hkv, a.T, a.B, kD, a.v_stride, kBlk, why) ||
       !token_map(&dq, a.dq, a.Hq, a.T, a.B, kD, a.dq_stride, 32, why) ||
-      !token_map(&dk, a.dk, a.Hkv, a.T, a.B, kD, a.dk_stride, kBlk, why) ||
-      !token_map(&dv, a.dv, a.Hkv, a.T, a.B, kD, a.dv_stride, kBlk, why))
+      !token_map(&dk, a.dk, a.Hkv, a.T, a.B, kD, a.dk_stride, 32, why) ||
+      !token_map(&dv, a.dv, a.Hkv, a.T, a.B, kD, a.dv_stride, 32, why))
     return cudaErrorInvalidValue;
   const void *kv_fn = reinterpret_cast<const void *>(window_kv_kernel<kD>);
   const void *dq_fn = reinterpret_cast<const void *>(window_dq_kernel<kD>);
@@ -893,7 +876,7 @@ cudaError_t launch(const WindowArgs &a, BwdParams &p, const BwdSizes &s, int sms
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(kThr);
+  cfg.blockDim = dim3(kKvThr);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -901,6 +884,7 @@ cudaError_t launch(const WindowArgs &a, BwdParams &p, const BwdSizes &s, int sms
   cfg.dynamicSmemBytes = KvSmem<kD>::kBytes;
   e = cudaLaunchKernelEx(&cfg, window_kv_kernel<kD>, q, dout, k, v, dk, dv, p);
   if (e != cudaSuccess) return e;
+  cfg.blockDim = dim3(kThr);
   cfg.gridDim = dim3(std::min(p.dq_items, sms));
   cfg.dynamicSmemBytes = DqSmem<kD>::kBytes;
   e = cudaLaunchKernelEx(&cfg, window_dq_kernel<kD>, k, dq, p);
@@ -949,6 +933,8 @@ cudaError_t launch_window_bwd(const WindowArgs &a, const WaitCtl &w, cudaStream_
   p.g = s.g;
   p.first_parts = s.first_parts, p.parts_each = s.parts_each, p.per_unit = s.per_unit, p.slots = s.slots;
   p.items = static_cast<int>(items), p.dq_items = static_cast<int>(dq_items);
+  p.by_unit = Div::by(s.per_unit), p.by_hkv = Div::by(a.Hkv);
+  p.by_first = Div::by(s.first_parts), p.by_each = Div::by(s.parts_each);
   p.scale = a.scale;
   p.wait = w;
   return a.D == 64 ? launch<64>(a, p, s, sms, st, why) : launch<128>(a, p, s, sms, st, why);

@@ -33,12 +33,6 @@ constexpr int kThr = 512;
 constexpr float kRescale = 8.f;       // lazy-rescale threshold (base-2 units)
 constexpr int kHeadGroup = 8;         // tile pairs of heads per scheduling group
 
-// The lowest x of 32 bits.
-__device__ __forceinline__ uint32_t below(int x) {
-  const int n = min(max(x, 0), 32);
-  return n == 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
 template <int kD>
 struct FwdSmem {
   static constexpr int kTile = kBlk * kD * 2;               // one block of Q, K or V
