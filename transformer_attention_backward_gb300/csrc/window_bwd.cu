@@ -93,14 +93,18 @@ struct BwdParams {
   int first_parts, parts_each;    // CTAs per key block: first tokens', others
   int per_unit, slots;            // items and part slots per (batch, KV head)
   int items, dq_items;
-  Div by_unit, by_hkv, by_first, by_each;   // per_unit, Hkv, first_parts, parts_each
+  Div by_unit, by_hkv, by_first, by_each, by_hq, by_chunks, by_nb, by_g;   // per_unit, Hkv, first_parts, parts_each, ..
   float scale;
   WaitCtl wait;
 };
 
 // ---------------------------------------------------------------------- prep
-// A row of o and dout per kD / 8 lanes, four rows each.
-constexpr int kPrepThr = 256, kPrepRows = 4;
+// A block per 32 (64) tokens of a head, heads next to one another: what runs at one
+// time reads o and dout in order, and the statistics are written in whole lines.  A
+// row per kD / 8 lanes, two rows each.
+constexpr int kPrepThr = 256, kPrepRows = 2;
+template <int kD>
+constexpr int kPrepTokens = kPrepRows * kPrepThr * 8 / kD;
 
 __device__ __forceinline__ float dot8(uint4 a, uint4 g) {
   return bf16_lo(a.x) * bf16_lo(g.x) + bf16_hi(a.x) * bf16_hi(g.x) + bf16_lo(a.y) * bf16_lo(g.y) +
@@ -111,51 +115,37 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 g) {
 template <int kD>
 __global__ void __launch_bounds__(kPrepThr) window_prep_kernel(const __grid_constant__ BwdParams p) {
   constexpr int kL = kD / 8;   // lanes of a row
-  const long long gid = static_cast<long long>(blockIdx.x) * kPrepThr + threadIdx.x;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const long long npad = static_cast<long long>(p.B) * p.Hq * (p.Tp - p.T);
-  if (gid < npad) {
-    const long long bh = gid / (p.Tp - p.T);
-    const size_t at = static_cast<size_t>(bh) * p.Tp + p.T + (gid - bh * (p.Tp - p.T));
-    p.ndelta[at] = 0.f;
-    p.nlse2[at] = -INFINITY;
-  }
   const int sub = threadIdx.x % kL;
-  const long long rows = static_cast<long long>(p.B) * p.T * p.Hq, r0 = gid / kL * kPrepRows;
-  const long long tok0 = r0 / p.Hq;
-  int h = static_cast<int>(r0 - tok0 * p.Hq), b = static_cast<int>(tok0 / p.T), t = static_cast<int>(tok0 - static_cast<long long>(b) * p.T);
+  int h = blockIdx.x;
+  int b = p.by_hq(h);          // a quotient; h becomes the remainder
+  int chunk = b;
+  b = p.by_chunks(chunk);
+  const int n = tokens_of(p.lengths, b, p.T), t0 = chunk * kPrepTokens<kD> + threadIdx.x / kL;
+  const size_t row = static_cast<size_t>(b) * p.Hq + h;
   uint4 x[kPrepRows], y[kPrepRows];
-  size_t at[kPrepRows];
   float l[kPrepRows];
-  int have = 0;
 #pragma unroll
   for (int k = 0; k < kPrepRows; ++k) {
+    const int t = t0 + k * (kPrepThr / kL);
     x[k] = y[k] = make_uint4(0, 0, 0, 0);
-    l[k] = INFINITY;
-    at[k] = 0;
-    if (r0 + k < rows) {
-      have = k + 1;
-      at[k] = (static_cast<size_t>(b) * p.Hq + h) * p.Tp + t;
-      if (t < tokens_of(p.lengths, b, p.T)) {
-        const long long tok = static_cast<long long>(b) * p.T + t;
-        x[k] = *reinterpret_cast<const uint4 *>(p.o + tok * p.o_stride + static_cast<size_t>(h) * kD + 8 * sub);
-        y[k] = *reinterpret_cast<const uint4 *>(p.dout + (tok * p.Hq + h) * kD + 8 * sub);
-        l[k] = p.lse[(static_cast<size_t>(b) * p.Hq + h) * p.T + t];
-      }
-      if (++h == p.Hq) {
-        h = 0;
-        if (++t == p.T) t = 0, ++b;
-      }
+    l[k] = INFINITY;           // padding: P = 2^(s - inf) = 0
+    if (t < n) {
+      const long long tok = static_cast<long long>(b) * p.T + t;
+      x[k] = *reinterpret_cast<const uint4 *>(p.o + tok * p.o_stride + static_cast<size_t>(h) * kD + 8 * sub);
+      y[k] = *reinterpret_cast<const uint4 *>(p.dout + (tok * p.Hq + h) * kD + 8 * sub);
+      if (sub == 0) l[k] = p.lse[row * p.T + t];
     }
   }
 #pragma unroll
   for (int k = 0; k < kPrepRows; ++k) {
+    const int t = t0 + k * (kPrepThr / kL);
     float v = dot8(x[k], y[k]);
 #pragma unroll
     for (int d = kL / 2; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);   // within the row's lanes
-    if (k < have && sub == 0) {
-      p.ndelta[at[k]] = -v;
-      p.nlse2[at[k]] = -l[k] * kLog2e;
+    if (sub == 0 && t < p.Tp) {
+      p.ndelta[row * p.Tp + t] = -v;
+      p.nlse2[row * p.Tp + t] = -l[k] * kLog2e;
     }
   }
 }
@@ -610,15 +600,15 @@ __global__ void __launch_bounds__(kKvThr, 1)
 
 // ---------------------------------------------------------------------- join
 // Parts of the key blocks that went to several CTAs, summed in their order: a
-// block per (batch, KV head, key block) and 32 keys.
+// block per (batch, KV head, key block) and 32 keys.  Runs beside the dq kernel,
+// which lets it start once the kv kernel has completed.
 constexpr int kJoinThr = 256;
 
 template <int kD>
-__global__ void __launch_bounds__(kJoinThr) window_join_kernel(const __grid_constant__ BwdParams p, int blocks) {
+__global__ void __launch_bounds__(kJoinThr) window_join_kernel(const __grid_constant__ BwdParams p) {
   const int nk = p.parts_each > 1 ? p.g.nb : p.g.first;   // key blocks with parts
   const int quarter = blockIdx.x & 3;
   const int unit = (blockIdx.x >> 2) / nk, kb = (blockIdx.x >> 2) - unit * nk;
-  if (static_cast<int>(blockIdx.x) >= blocks) return;
   const int idx = unit * p.per_unit + (kb < p.g.first ? kb * p.first_parts : p.g.first * p.first_parts + (kb - p.g.first) * p.parts_each);
   const KvItem w = kv_item(p, idx);
   // of fewer pairs than parts only the first parts have one and were written
@@ -639,6 +629,8 @@ __global__ void __launch_bounds__(kJoinThr) window_join_kernel(const __grid_cons
     __nv_bfloat16 *dst = (x == 0 ? p.dv + at * p.dv_stride : p.dk + at * p.dk_stride) + static_cast<size_t>(w.kvh) * kD + 4 * c;
     *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
   }
+  // what follows on the stream follows the dq kernel too
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------------------ dq
@@ -659,10 +651,9 @@ struct DqItem {
 };
 __device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
   DqItem r;
-  const int hb = idx / p.g.nb;
-  r.m = p.g.nb - 1 - (idx - hb * p.g.nb);
-  r.b = hb / p.Hq;
-  r.h = hb - r.b * p.Hq;
+  r.h = p.by_nb(idx);               // idx becomes the place in the head
+  r.m = p.g.nb - 1 - idx;
+  r.b = p.by_hq(r.h);
   r.n = tokens_warp(p.lengths, r.b, p.T);
   r.lo = p.g.lo(r.m);
   r.lead = p.g.lead(r.m);
@@ -701,11 +692,16 @@ __global__ void __launch_bounds__(kThr, 1)
     if (lane == 0) prefetch_tensormap(&tmK);
     const uint64_t keep = l2_evict_last(), stream = l2_evict_first();
     asm volatile("griddepcontrol.wait;" ::: "memory");   // the dS tiles come from the kv kernel
+    // the join may start beside this kernel: what it reads is there, and it waits for
+    // this grid behind its work
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int g = 0, raw = 0;
     bool ok = true;
     for (int round = 0, idx = nth_item(0); ok && round * static_cast<int>(gridDim.x) < p.dq_items; idx = nth_item(++round)) {
       if (idx >= p.dq_items) continue;
       const DqItem w = dq_item(p, idx);
+      int rest = w.h;
+      const int kvh = p.by_g(rest);
       const unsigned char *tiles = reinterpret_cast<const unsigned char *>(p.ds) +
                                    (static_cast<long long>(w.b) * p.Hq + w.h) * p.tiles * kTileBytes;
       for (int x = 0; x < w.steps; ++x, ++g) {
@@ -719,7 +715,7 @@ __global__ void __launch_bounds__(kThr, 1)
         if (lane == 0) {
           mbar_arrive_expect_tx(fb, M::kStage);
           for (int hx = 0; hx < kHalves; ++hx)
-            tma_load_4d_hint(st + hx * 16384, &tmK, hx * 64, w.h / p.G, kb * kBlk, w.b, fb, keep);
+            tma_load_4d_hint(st + hx * 16384, &tmK, hx * 64, kvh, kb * kBlk, w.b, fb, keep);
           bulk_load_hint(st + M::kK, tiles + (p.g.tile0(kb) + (w.m - kb)) * kTileBytes, kTileBytes, fb, stream);
         }
         if (repair) clear_tail<kHalves>(wts, smem + s * M::kStage, live, M::kRaw, raw++ & 1, bar(M::kFull + s));
@@ -862,9 +858,9 @@ cudaError_t launch(const WindowArgs &a, BwdParams &p, const BwdSizes &s, int sms
   cudaError_t e = ensure_dynamic_smem(kv_fn, KvSmem<kD>::kBytes);
   if (e == cudaSuccess) e = ensure_dynamic_smem(dq_fn, DqSmem<kD>::kBytes);
   if (e != cudaSuccess) return e;
-  const long long rows = static_cast<long long>(a.B) * a.T * a.Hq;
-  const long long threads = std::max((rows + kPrepRows - 1) / kPrepRows * (kD / 8), static_cast<long long>(a.B) * a.Hq * (s.Tp - a.T));
-  const long long blocks = (threads + kPrepThr - 1) / kPrepThr;
+  const int chunks = s.Tp / kPrepTokens<kD>;   // whole ones: Tp is a multiple of 128
+  p.by_chunks = Div::by(chunks);
+  const long long blocks = static_cast<long long>(a.B) * chunks * a.Hq;
   if (blocks > 0x7fffffffLL) {
     *why = "grid too large";
     return cudaErrorNotSupported;
@@ -891,8 +887,11 @@ cudaError_t launch(const WindowArgs &a, BwdParams &p, const BwdSizes &s, int sms
   if (e != cudaSuccess) return e;
   if (s.slots > 0) {
     const int nk = s.parts_each > 1 ? s.g.nb : s.g.first;
-    const int join = a.B * a.Hkv * nk * 4;
-    window_join_kernel<kD><<<join, kJoinThr, 0, st>>>(p, join);
+    cfg.gridDim = dim3(a.B * a.Hkv * nk * 4);
+    cfg.blockDim = dim3(kJoinThr);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, window_join_kernel<kD>, p);
+    if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();
 }
@@ -935,6 +934,7 @@ cudaError_t launch_window_bwd(const WindowArgs &a, const WaitCtl &w, cudaStream_
   p.items = static_cast<int>(items), p.dq_items = static_cast<int>(dq_items);
   p.by_unit = Div::by(s.per_unit), p.by_hkv = Div::by(a.Hkv);
   p.by_first = Div::by(s.first_parts), p.by_each = Div::by(s.parts_each);
+  p.by_hq = Div::by(a.Hq), p.by_nb = Div::by(s.g.nb), p.by_g = Div::by(p.G);
   p.scale = a.scale;
   p.wait = w;
   return a.D == 64 ? launch<64>(a, p, s, sms, st, why) : launch<128>(a, p, s, sms, st, why);
