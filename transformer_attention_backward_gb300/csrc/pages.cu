@@ -17,19 +17,22 @@
 // Per query row the softmax statistics run along (max m, sum l, output O, all
 // fp32): a tile with a larger max rescales l and O by 2^(m_old - m_new).
 //
-// The bound is the cache's bytes.  Each lane copies (cp.async) the very 16-byte
-// units that it later feeds to the tensor core, into slots of its own: no
-// barrier and no bank conflict, 3 tiles (24 KB at D = 128) under way per warp.
-// The units are fragments as they stand, because the contraction index of q k
-// and the column index of p v may be permuted at will:
-//   S = Q K^T  (m16n8k16: rows = query heads, columns = keys): lane (g, t) holds
-//     key g, components 32 c + 8 t .. + 7, whose pairs are the k indices
-//     (2t, 2t+1, 2t+8, 2t+9) of two steps; Q is laid out to match.
-//   O = P V    (rows = query heads, columns = components): lane (g, t) holds
-//     keys 2t, 2t+1, 2t+8, 2t+9, components 64 c + 8 g .. + 7; a byte
-//     permutation pairs the keys.  P's fragment is S's as it stands.
+// The bound is the cache's bytes.  A warp copies (cp.async) its tile's rows whole, two
+// 256-byte rows an instruction, into a ring of three tiles (24 KB at D = 128) of its
+// own, each 16-byte unit to where the lane that feeds it to the tensor core reads it:
+// no barrier between warps, no bank conflict.  (With each lane copying its own units,
+// 64 bytes of eight rows an instruction, the copies alone ran at 5.3 of 7.2 TB/s.)
+// The units are fragments as they stand, because the contraction index of k q and the
+// row index of v p may be permuted at will (m16n8k16, lane = 4 g + t):
+//   S^T = K Q^T (rows = 16 keys, columns = 8 query heads): lane (g, t) reads keys g and
+//     g + 8, components 32 c + 8 t .. + 7, whose pairs are the k indices (2t, 2t+1,
+//     2t+8, 2t+9) of two steps; Q is laid out to match.
+//   O^T = V^T P^T (rows = components, columns = heads): lane (g, t) reads keys 2t, 2t+1,
+//     2t+8, 2t+9, components 64 c + 8 g .. + 7; a byte permutation pairs the keys.
+//     P's fragment is the transpose of S's (movmatrix).
 // P enters as bf16 terms (two of them for bf16 outputs, three for fp32), fp32
-// queries as three, so nothing but the output is rounded to bf16.
+// queries as three, so nothing but the output is rounded to bf16.  The maximum is
+// lazy: it moves only when a score exceeds it by more than 8 (base 2).
 #include <math.h>
 
 #include <algorithm>
@@ -94,6 +97,7 @@ constexpr int kMinTiles = 8;         // tiles a CTA takes at least, while there 
 constexpr int kDecCtas = 304;        // two per SM
 constexpr int kWtPos = 2048;         // positions per block of the weight sums
 constexpr uint32_t kNoRow = 0xffffffffu;
+constexpr float kLazy = 8.f;         // base-2 units a score may exceed the running maximum by
 
 struct DecParams {
   const void *q;
@@ -250,6 +254,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The transpose of an 8 x 8 matrix of 16-bit elements.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool there) {
   const int bytes = there ? 16 : 0;   // 0: the slot is filled with zeros and nothing is read
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -287,7 +297,6 @@ template <int kD, bool kF32, bool kWide, bool kScores>
 __global__ void __launch_bounds__(kDecThr, 2) decode_split_kernel(const __grid_constant__ DecParams p) {
   constexpr int kQT = kF32 ? 3 : 1, kPT = kF32 ? 3 : 2;   // terms of q and of p
   constexpr int kC = kD / 32, kV = kD / 64;               // 64-byte pieces of a k row, 128-byte pieces of a v row
-  constexpr int kSlots = 2 * kC + 4 * kV;                 // 16-byte slots of a lane and tile
   constexpr int kR = kWide ? 2 : 1;                       // row halves
   extern __shared__ __align__(128) unsigned char smem[];
   float *mo = reinterpret_cast<float *>(smem + kDecWarps * kDecStages * kTile * kD * 4);   // [warps][8][kD + 4]
@@ -314,8 +323,12 @@ __global__ void __launch_bounds__(kDecThr, 2) decode_split_kernel(const __grid_c
   Walk now, ahead;
   now.begin(p, at, count);
   ahead = now;
-  const uint32_t ring = smem_u32(smem) + warp * (kDecStages * kTile * kD * 4) + lane * 16;
-  const unsigned char *ring_p = smem + warp * (kDecStages * kTile * kD * 4) + lane * 16;
+  const unsigned char *ring_p = smem + warp * (kDecStages * kTile * kD * 4);
+  // copies: lane -> unit `q` of row `hi` of the kRows that an instruction takes
+  constexpr int kUnits = kD / 8, kRows = 32 / kUnits;
+  const int hi = lane / kUnits, q = lane % kUnits;
+  const uint32_t to_k = smem_u32(ring_p) + (hi * 4 + (q & 3)) * 16 + (q >> 2) * 512;
+  const uint32_t to_v = smem_u32(ring_p) + (2 * kC + (hi & 1) * kV + (q >> 3)) * 512 + (hi >> 1) * 128 + (q & 7) * 16;
 
   // ---- loads: tile `lt` of the piece `ahead`, whose rows `row` holds (lanes 0 .. 15)
   int lt = ahead.tile0 + warp;
@@ -346,25 +359,17 @@ __global__ void __launch_bounds__(kDecThr, 2) decode_split_kernel(const __grid_c
     if (stage == 1) seen1 = there_all;
     if (stage == 2) seen2 = there_all;
     if (more) {
-      const uint32_t dst = ring + stage * (kTile * kD * 4);
-      const size_t head = static_cast<size_t>(ahead.u / p.ng) * kD;
+      const size_t unit = static_cast<size_t>(ahead.u / p.ng) * kD + 8 * q;
       const size_t pitch = static_cast<size_t>(p.Hkv) * kD;
       const __nv_bfloat16 *nothing = static_cast<const __nv_bfloat16 *>(p.q);   // an address that no byte is read from
+      const uint32_t st = stage * (kTile * kD * 4);
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const uint32_t r = __shfl_sync(0xffffffffu, row, g + 8 * n);
+      for (int i = 0; i < kTile; i += kRows) {
+        const uint32_t r = __shfl_sync(0xffffffffu, row, i + hi);
         const bool there = r != kNoRow;
-        const __nv_bfloat16 *src = there ? p.kp + (r * pitch + head + 8 * t) : nothing;
-#pragma unroll
-        for (int c = 0; c < kC; ++c) cp_async16(dst + (n * kC + c) * 512, src + (there ? 32 * c : 0), there);
-      }
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const uint32_t r = __shfl_sync(0xffffffffu, row, 2 * t + (n & 1) + 8 * (n >> 1));
-        const bool there = r != kNoRow;
-        const __nv_bfloat16 *src = there ? p.vp + (r * pitch + head + 8 * g) : nothing;
-#pragma unroll
-        for (int c = 0; c < kV; ++c) cp_async16(dst + (2 * kC + n * kV + c) * 512, src + (there ? 64 * c : 0), there);
+        const size_t at = r * pitch + unit;
+        cp_async16(to_k + st + (i >> 3) * kC * 512 + (i & 7) * 64, there ? p.kp + at : nothing, there);
+        cp_async16(to_v + st + 2 * (i >> 3) * kV * 512 + (i >> 1 & 3) * 128, there ? p.vp + at : nothing, there);
       }
       lt += kDecWarps;
       settle();
@@ -380,7 +385,7 @@ __global__ void __launch_bounds__(kDecThr, 2) decode_split_kernel(const __grid_c
   int stage = 0;
   bool first = true;
   do {
-    // ---- this piece's queries, as fragments
+    // ---- this piece's queries, as fragments: head g of each eight
     const int kvh = now.u / p.ng, grp = now.u - kvh * p.ng;
     const int h0 = kvh * p.G + grp * 16, nrows = min(16, p.G - grp * 16);
     uint32_t qf[kQT][kR][kC][4];
@@ -411,102 +416,113 @@ __global__ void __launch_bounds__(kDecThr, 2) decode_split_kernel(const __grid_c
         }
       }
     }
-    float m[kR], l[kR], O[kV][8][4];
+    // of heads 2 t and 2 t + 1 (of each eight): maximum, this lane's sum, outputs of
+    // components 64 c + 8 g + 2 j (elements 0, 1) and + 1 (2, 3)
+    float m[kR][2], l[kR][2], O[kR][kV][4][4];
 #pragma unroll
-    for (int r = 0; r < kR; ++r) m[r] = -INFINITY, l[r] = 0.f;
+    for (int r = 0; r < kR; ++r) {
+      m[r][0] = m[r][1] = -INFINITY;
+      l[r][0] = l[r][1] = 0.f;
 #pragma unroll
-    for (int c = 0; c < kV; ++c)
+      for (int c = 0; c < kV; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) O[c][i][e] = 0.f;
+          for (int e = 0; e < 4; ++e) O[r][c][j][e] = 0.f;
+    }
 
     for (int tile = now.tile0 + warp; tile < now.tend; tile += kDecWarps) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kDecStages - 1) : "memory");
+      __syncwarp();                        // the other lanes' copies too
       const unsigned char *src = ring_p + stage * (kTile * kD * 4);
       const uint32_t mask = stage == 0 ? seen0 : stage == 1 ? seen1 : seen2;
-      // ---- S = Q K^T
-      float S[2][4];
+      // ---- S^T = K Q^T, in two chains
+      float S[kR][2][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+      for (int r = 0; r < kR; ++r)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) S[r][0][e] = S[r][1][e] = 0.f;
 #pragma unroll
-        for (int c = 0; c < kC; ++c) {
-          const uint4 k = *reinterpret_cast<const uint4 *>(src + (n * kC + c) * 512);
+      for (int c = 0; c < kC; ++c) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(src + c * 512 + lane * 16);
+        const uint4 b = *reinterpret_cast<const uint4 *>(src + (kC + c) * 512 + lane * 16);
+#pragma unroll
+        for (int r = 0; r < kR; ++r)
 #pragma unroll
           for (int x = 0; x < kQT; ++x) {
-            mma16816(S[n], qf[x][0][c][0], kWide ? qf[x][kR - 1][c][0] : 0u, qf[x][0][c][1],
-                     kWide ? qf[x][kR - 1][c][1] : 0u, k.x, k.y);
-            mma16816(S[n], qf[x][0][c][2], kWide ? qf[x][kR - 1][c][2] : 0u, qf[x][0][c][3],
-                     kWide ? qf[x][kR - 1][c][3] : 0u, k.z, k.w);
+            mma16816(S[r][0], a.x, b.x, a.y, b.y, qf[x][r][c][0], qf[x][r][c][1]);
+            mma16816(S[r][1], a.z, b.z, a.w, b.w, qf[x][r][c][2], qf[x][r][c][3]);
           }
-        }
       }
-      // ---- running softmax of each row over the 16 positions
-      uint32_t pf[kPT][2][2];   // [term][row half][keys 2t, 2t+1 | 2t+8, 2t+9]
+      // ---- running softmax of each head over the 16 positions
+      uint32_t pf[kR][kPT][2];             // [term][keys 2t, 2t+1 | 2t+8, 2t+9] of head g
+      const bool in0 = mask >> g & 1u, in1 = mask >> (g + 8) & 1u;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (r >= kR) {
+      for (int r = 0; r < kR; ++r) {
+        float s[4];                        // (key g, head 2t), (g, 2t+1), (g + 8, 2t), (g + 8, 2t+1)
 #pragma unroll
-          for (int k = 0; k < kPT; ++k) pf[k][r][0] = pf[k][r][1] = 0u;
-          continue;
-        }
-        float s[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          s[i] = (mask >> (2 * t + (i & 1) + 8 * (i >> 1))) & 1u ? S[i >> 1][2 * r + (i & 1)] * p.sl2 : -INFINITY;
+        for (int e = 0; e < 4; ++e) s[e] = (e < 2 ? in0 : in1) ? (S[r][0][e] + S[r][1][e]) * p.sl2 : -INFINITY;
         if constexpr (kScores) {
-          if (g + 8 * r < nrows) {
-            float *dst = p.scores + (static_cast<size_t>(now.b) * p.Hq + h0 + g + 8 * r) * p.score_stride +
-                         static_cast<size_t>(tile) * kTile + 2 * t;
-            *reinterpret_cast<float2 *>(dst) = make_float2(s[0], s[1]);
-            *reinterpret_cast<float2 *>(dst + 8) = make_float2(s[2], s[3]);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int head = 8 * r + 2 * t + x;
+            if (head < nrows) {
+              float *dst = p.scores + (static_cast<size_t>(now.b) * p.Hq + h0 + head) * p.score_stride +
+                           static_cast<size_t>(tile) * kTile + g;
+              dst[0] = s[x];
+              dst[8] = s[2 + x];
+            }
           }
         }
-        float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float mn = fmaxf(m[r], top);
-        const float base = mn == -INFINITY ? 0.f : mn;   // nothing seen yet: 2^(-inf - 0) = 0
-        if (__any_sync(0xffffffffu, mn > m[r])) {
-          const float f = ex2(m[r] - base);
-          l[r] *= f;
+        float top[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
+        if (__any_sync(0xffffffffu, top[0] > m[r][0] + kLazy || top[1] > m[r][1] + kLazy)) {
 #pragma unroll
-          for (int c = 0; c < kV; ++c)
+          for (int x = 0; x < 2; ++x) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              O[c][i][2 * r] *= f;
-              O[c][i][2 * r + 1] *= f;
-            }
-          m[r] = mn;
+            for (int d = 4; d < 32; d <<= 1) top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], d));
+            const float mn = fmaxf(m[r][x], top[x]);
+            const float f = mn == -INFINITY ? 1.f : ex2(m[r][x] - mn);
+            m[r][x] = mn;
+            l[r][x] *= f;
+#pragma unroll
+            for (int c = 0; c < kV; ++c)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) O[r][c][j][x] *= f, O[r][c][j][2 + x] *= f;
+          }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] = ex2(s[i] - base);
-        l[r] += (s[0] + s[1]) + (s[2] + s[3]);
-        uint32_t lo[kPT], hi[kPT];
+        for (int x = 0; x < 2; ++x) {
+          const float base = m[r][x] == -INFINITY ? 0.f : m[r][x];   // nothing seen yet: 2^(-inf - 0) = 0
+          s[x] = ex2(s[x] - base);
+          s[2 + x] = ex2(s[2 + x] - base);
+          l[r][x] += s[x] + s[2 + x];
+        }
+        uint32_t lo[kPT], up[kPT];
         terms<kPT>(s[0], s[1], lo);
-        terms<kPT>(s[2], s[3], hi);
+        terms<kPT>(s[2], s[3], up);
 #pragma unroll
-        for (int k = 0; k < kPT; ++k) pf[k][r][0] = lo[k], pf[k][r][1] = hi[k];
+        for (int k = 0; k < kPT; ++k) pf[r][k][0] = transposed(lo[k]), pf[r][k][1] = transposed(up[k]);
       }
-      // ---- O += P V
+      // ---- O^T += V^T P^T
 #pragma unroll
       for (int c = 0; c < kV; ++c) {
         uint32_t v[4][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint4 x = *reinterpret_cast<const uint4 *>(src + (2 * kC + n * kV + c) * 512);
+        for (int n = 0; n < 4; ++n) {      // keys 2t, 2t+1, 2t+8, 2t+9
+          const uint4 x = *reinterpret_cast<const uint4 *>(src + (2 * kC + n * kV + c) * 512 + (8 * t + g) * 16);
           v[n][0] = x.x, v[n][1] = x.y, v[n][2] = x.z, v[n][3] = x.w;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t sel = (i & 1) ? 0x7632 : 0x5410;
-          const uint32_t b0 = __byte_perm(v[0][i >> 1], v[1][i >> 1], sel), b1 = __byte_perm(v[2][i >> 1], v[3][i >> 1], sel);
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t a0 = __byte_perm(v[0][j], v[1][j], 0x5410), a1 = __byte_perm(v[0][j], v[1][j], 0x7632);
+          const uint32_t a2 = __byte_perm(v[2][j], v[3][j], 0x5410), a3 = __byte_perm(v[2][j], v[3][j], 0x7632);
 #pragma unroll
-          for (int k = 0; k < kPT; ++k) mma16816(O[c][i], pf[k][0][0], pf[k][1][0], pf[k][0][1], pf[k][1][1], b0, b1);
+          for (int r = 0; r < kR; ++r)
+#pragma unroll
+            for (int k = 0; k < kPT; ++k) mma16816(O[r][c][j], a0, a1, a2, a3, pf[r][k][0], pf[r][k][1]);
         }
       }
+      __syncwarp();                        // every lane has read the tile
       issue(stage);
       stage = stage + 1 == kDecStages ? 0 : stage + 1;
     }
@@ -516,22 +532,23 @@ __global__ void __launch_bounds__(kDecThr, 2) decode_split_kernel(const __grid_c
     float *slot = p.slots + (static_cast<size_t>(cta) * 2 + (first ? 0 : 1)) * p.rows * (kD + 4);
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      float sum = l[r];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (t == 0) {
-        ms[warp * 16 + g] = m[r];
-        ms[warp * 16 + 8 + g] = sum;
-      }
 #pragma unroll
-      for (int c = 0; c < kV; ++c) {   // components 64 c + 16 t + 8 j + i of row g
-        float *dst = mo + (warp * 8 + g) * (kD + 4) + 64 * c + 16 * t;
+      for (int x = 0; x < 2; ++x) {
+        float sum = l[r][x];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (g == 0) {
+          ms[warp * 16 + 2 * t + x] = m[r][x];
+          ms[warp * 16 + 8 + 2 * t + x] = sum;
+        }
 #pragma unroll
-          for (int i = 0; i < 8; i += 4)
-            *reinterpret_cast<float4 *>(dst + 8 * j + i) = make_float4(O[c][i][2 * r + j], O[c][i + 1][2 * r + j],
-                                                                       O[c][i + 2][2 * r + j], O[c][i + 3][2 * r + j]);
+        for (int c = 0; c < kV; ++c) {
+          float *dst = mo + (warp * 8 + 2 * t + x) * (kD + 4) + 64 * c + 8 * g;
+#pragma unroll
+          for (int j = 0; j < 4; j += 2)
+            *reinterpret_cast<float4 *>(dst + 2 * j) =
+                make_float4(O[r][c][j][x], O[r][c][j][2 + x], O[r][c][j + 1][x], O[r][c][j + 1][2 + x]);
+        }
       }
       __syncthreads();
       for (int e = tid; e < 8 * kD / 4; e += kDecThr) {
