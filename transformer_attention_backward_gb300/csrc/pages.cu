@@ -90,12 +90,18 @@ __global__ void __launch_bounds__(kWrThr) kv_pages_write_kernel(const __grid_con
 }
 
 // -------------------------------------------------------------------- decode
-constexpr int kDecWarps = 4, kDecThr = 32 * kDecWarps;
-constexpr int kDecStages = 3;
+// Warps per CTA, two CTAs per SM: a tile's chain of waits and products takes some 1,500
+// cycles, so more warps with two tiles each under way beat fewer with three (4 x 3
+// stages 164 us, 6 x 2 138 us for 8 long sequences with weight sums).  fp32 queries
+// of wide groups take the registers of four.
+constexpr int dec_warps(bool f32, bool wide) { return f32 && wide ? 4 : 6; }
+constexpr int kDecStages = 2;
 constexpr int kTile = 16;            // positions per tile
 constexpr int kMinTiles = 8;         // tiles a CTA takes at least, while there are few
 constexpr int kDecCtas = 304;        // two per SM
-constexpr int kWtPos = 2048;         // positions per block of the weight sums
+constexpr int kWtPos = 1024;         // positions per block of the weight sums, at least
+constexpr int kWtBlocks = 1216;      // ... and blocks to spread them over
+constexpr int kWtUnroll = 4;
 constexpr uint32_t kNoRow = 0xffffffffu;
 constexpr float kLazy = 8.f;         // base-2 units a score may exceed the running maximum by
 
@@ -111,7 +117,7 @@ struct DecParams {
   long long score_stride;
   int B, Hq, Hkv, D, G, ng, rows;    // ng groups of up to 16 query heads per KV head, rows = min(G, 16)
   int n_pages, page_size, page_shift, max_pages, cap, window, sinks;
-  int q_bf16, ctas, wt_chunks;
+  int q_bf16, ctas, wt_chunks, wt_len;
   float sl2;           // scale * log2(e)
 };
 
@@ -286,15 +292,15 @@ __device__ __forceinline__ void terms(float x, float y, uint32_t (&out)[kN]) {
   }
 }
 
-template <int kD, bool kWide>
-constexpr int dec_smem() {
-  return kDecWarps * kDecStages * kTile * kD * 4 + kDecWarps * 8 * (kD + 4) * 4 + kDecWarps * 16 * 2 * 4;
+constexpr int dec_smem(int D, int warps) {
+  return warps * kDecStages * kTile * D * 4 + warps * 8 * (D + 4) * 4 + warps * 16 * 4;
 }
 
 // kF32: fp32 queries and outputs; kWide: more than 8 query heads per KV head;
 // kScores: scores are kept for the weight sums.
 template <int kD, bool kF32, bool kWide, bool kScores>
-__global__ void __launch_bounds__(kDecThr, 2) decode_split_kernel(const __grid_constant__ DecParams p) {
+__global__ void __launch_bounds__(32 * dec_warps(kF32, kWide), 2) decode_split_kernel(const __grid_constant__ DecParams p) {
+  constexpr int kDecWarps = dec_warps(kF32, kWide), kDecThr = 32 * kDecWarps;
   constexpr int kQT = kF32 ? 3 : 1, kPT = kF32 ? 3 : 2;   // terms of q and of p
   constexpr int kC = kD / 32, kV = kD / 64;               // 64-byte pieces of a k row, 128-byte pieces of a v row
   constexpr int kR = kWide ? 2 : 1;                       // row halves
@@ -351,13 +357,12 @@ __global__ void __launch_bounds__(kDecThr, 2) decode_split_kernel(const __grid_c
     if (page >= 0 && page < p.n_pages)
       row = static_cast<uint32_t>(page) * static_cast<uint32_t>(p.page_size) + static_cast<uint32_t>(pos - pg * p.page_size);
   };
-  static_assert(kDecStages == 3, "a word of its own for each stage");
-  uint32_t seen0 = 0, seen1 = 0, seen2 = 0;   // positions of each tile under way that are there
+  static_assert(kDecStages == 2, "a word of its own for each stage");
+  uint32_t seen0 = 0, seen1 = 0;   // positions of each tile under way that are there
   auto issue = [&](int stage) {
     const uint32_t there_all = __ballot_sync(0xffffffffu, row != kNoRow);
     if (stage == 0) seen0 = there_all;
     if (stage == 1) seen1 = there_all;
-    if (stage == 2) seen2 = there_all;
     if (more) {
       const size_t unit = static_cast<size_t>(ahead.u / p.ng) * kD + 8 * q;
       const size_t pitch = static_cast<size_t>(p.Hkv) * kD;
@@ -435,7 +440,7 @@ __global__ void __launch_bounds__(kDecThr, 2) decode_split_kernel(const __grid_c
       asm volatile("cp.async.wait_group %0;" ::"n"(kDecStages - 1) : "memory");
       __syncwarp();                        // the other lanes' copies too
       const unsigned char *src = ring_p + stage * (kTile * kD * 4);
-      const uint32_t mask = stage == 0 ? seen0 : stage == 1 ? seen1 : seen2;
+      const uint32_t mask = stage == 0 ? seen0 : seen1;
       // ---- S^T = K Q^T, in two chains
       float S[kR][2][4];
 #pragma unroll
@@ -595,7 +600,7 @@ __global__ void __launch_bounds__(kDecThr, 2) decode_split_kernel(const __grid_c
 // Blocks 0 .. ctas - 1: block c joins the unit that begins in CTA c's run and
 // goes on behind it.  Blocks behind them, with weight sums: kWtPos positions of
 // a sequence and KV head each.
-constexpr int kFinThr = 128;
+constexpr int kFinThr = 256;
 
 // Slot of the i-th piece of a unit whose first tile is `seg`.
 __device__ __forceinline__ const float *piece_slot(const DecParams &p, const Runs &runs, long long seg, int c0, int i) {
@@ -684,12 +689,11 @@ __global__ void __launch_bounds__(kFinThr) decode_finish_kernel(const __grid_con
   }
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (static_cast<long long>(chunk) * kWtPos >= s.vis) return;
+  const int x0 = static_cast<int>(min(static_cast<long long>(chunk) * p.wt_len, static_cast<long long>(s.vis)));
+  const int x1 = static_cast<int>(min(static_cast<long long>(x0) + p.wt_len, static_cast<long long>(s.vis)));
+  if (x0 >= x1) return;
   const int tiles = tiles_of(s);
-  const int end = static_cast<int>(min(static_cast<long long>(s.vis), (chunk + 1LL) * kWtPos));
-  float acc[kWtPos / kFinThr];
-#pragma unroll
-  for (int i = 0; i < kWtPos / kFinThr; ++i) acc[i] = 0.f;
+  float *dst = p.weight_sums + (static_cast<size_t>(b) * p.Hkv + kvh) * p.cap;
   for (int grp = 0; grp < p.ng; ++grp) {
     const long long seg = wt_before + (static_cast<long long>(kvh) * p.ng + grp) * tiles;
     const int c0 = runs.owner(seg), c1 = runs.owner(seg + tiles - 1);
@@ -698,25 +702,28 @@ __global__ void __launch_bounds__(kFinThr) decode_finish_kernel(const __grid_con
     for (int r = warp; r < nrows; r += kFinThr / 32) {
       const float2 x = c0 == c1 ? p.stats[static_cast<size_t>(b) * p.Hq + h0 + r]
                                 : joined_stats(p, runs, seg, c0, c1 - c0 + 1, r);
-      if (lane == 0) st[r] = make_float2(x.x, x.y > 0.f ? 1.f / x.y : 0.f);
+      if (lane == 0) st[r] = x.y > 0.f ? make_float2(x.x, 1.f / x.y) : make_float2(0.f, 0.f);
     }
     __syncthreads();
-    for (int r = 0; r < nrows; ++r) {
-      const float *sc = p.scores + (static_cast<size_t>(b) * p.Hq + h0 + r) * p.score_stride;
-      const float M = st[r].x, inv = st[r].y;
-      if (inv == 0.f) continue;
+    const float *sc = p.scores + (static_cast<size_t>(b) * p.Hq + h0) * p.score_stride;
+    for (int x = x0 + tid; x < x1; x += kFinThr * kWtUnroll) {
+      float acc[kWtUnroll], old[kWtUnroll];
 #pragma unroll
-      for (int i = 0; i < kWtPos / kFinThr; ++i) {
-        const int x = chunk * kWtPos + i * kFinThr + tid;
-        if (x < end) acc[i] = fmaf(ex2(sc[x] - M), inv, acc[i]);
+      for (int i = 0; i < kWtUnroll; ++i) {
+        acc[i] = 0.f;
+        old[i] = x + i * kFinThr < x1 ? dst[position(s, x + i * kFinThr)] : 0.f;
       }
-    }
-  }
-  float *dst = p.weight_sums + (static_cast<size_t>(b) * p.Hkv + kvh) * p.cap;
+#pragma unroll 4
+      for (int r = 0; r < nrows; ++r) {
+        const float M = st[r].x, inv = st[r].y;          // 0, 0 where nothing is seen
 #pragma unroll
-  for (int i = 0; i < kWtPos / kFinThr; ++i) {
-    const int x = chunk * kWtPos + i * kFinThr + tid;
-    if (x < end && acc[i] > 0.f) dst[position(s, x)] += acc[i];
+        for (int i = 0; i < kWtUnroll; ++i)
+          if (x + i * kFinThr < x1) acc[i] = fmaf(ex2(sc[r * p.score_stride + x + i * kFinThr] - M), inv, acc[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kWtUnroll; ++i)
+        if (x + i * kFinThr < x1 && acc[i] > 0.f) dst[position(s, x + i * kFinThr)] = old[i] + acc[i];
+    }
   }
 }
 
@@ -919,7 +926,8 @@ DecSizes dec_sizes(int B, int Hq, int Hkv, int D, long long tokens, bool weights
   const long long tiles = ceil_div(tokens, kTile);
   s.ctas = static_cast<int>(std::max(1LL, std::min<long long>(kDecCtas, ceil_div(tiles * B * Hkv * s.ng, kMinTiles))));
   s.score_stride = tiles * kTile;
-  s.wt_chunks = weights ? static_cast<int>(ceil_div(std::max(tokens, 1LL), kWtPos)) : 0;
+  s.wt_chunks = !weights ? 0 : static_cast<int>(std::min(ceil_div(std::max(tokens, 1LL), kWtPos),
+                                                         std::max<long long>(1, kWtBlocks / (static_cast<long long>(B) * Hkv))));
   s.slots = static_cast<size_t>(s.ctas) * 2 * s.rows * (D + 4) * 4;
   s.stats = weights ? (static_cast<size_t>(B) * Hq * 8 + 15) / 16 * 16 : 0;
   s.scores = weights ? static_cast<size_t>(B) * Hq * s.score_stride * 4 : 0;
@@ -928,10 +936,10 @@ DecSizes dec_sizes(int B, int Hq, int Hkv, int D, long long tokens, bool weights
 
 template <int kD, bool kF32, bool kWide, bool kScores>
 cudaError_t launch_split(const DecParams &p, cudaStream_t st) {
-  constexpr int smem = dec_smem<kD, kWide>();
+  constexpr int warps = dec_warps(kF32, kWide), smem = dec_smem(kD, warps);
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(decode_split_kernel<kD, kF32, kWide, kScores>), smem);
   if (e != cudaSuccess) return e;
-  decode_split_kernel<kD, kF32, kWide, kScores><<<p.ctas, kDecThr, smem, st>>>(p);
+  decode_split_kernel<kD, kF32, kWide, kScores><<<p.ctas, 32 * warps, smem, st>>>(p);
   return cudaGetLastError();
 }
 template <int kD, bool kF32>
@@ -1008,6 +1016,7 @@ cudaError_t launch_attn_decode_paged(const PagesArgs &a, const void *q, int bf16
     if (a.page_size == 1 << i) p.page_shift = i;
   p.window = window, p.sinks = sinks;
   p.q_bf16 = bf16, p.ctas = s.ctas, p.wt_chunks = s.wt_chunks;
+  p.wt_len = s.wt_chunks ? static_cast<int>(ceil_div(std::max(tokens, 1LL), s.wt_chunks)) : 0;
   p.sl2 = scale * 1.4426950408889634f;
   cudaError_t e = a.D == 64 ? (bf16 ? launch_split<64, false>(p, st) : launch_split<64, true>(p, st))
                             : (bf16 ? launch_split<128, false>(p, st) : launch_split<128, true>(p, st));
