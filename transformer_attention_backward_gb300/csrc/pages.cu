@@ -728,11 +728,18 @@ __global__ void __launch_bounds__(kFinThr) decode_finish_kernel(const __grid_con
 }
 
 // ------------------------------------------------------------------ eviction
-// One block per (sequence, KV head) finds the tokens to keep: a radix select
-// over the weights' bits (8 at a time, from the top) gives the weight of the last
-// one and how many equal ones go with it, a scan in the order of the positions
-// writes them down.  A second launch moves the rows.
-constexpr int kEvThr = 1024;
+// One block per (sequence, KV head) finds the tokens to keep: their weights become
+// unsigned keys of the same order (0: absent page; the largest: kept whatever its
+// weight), a radix select over the keys' bits (11, 11 and 10 at a time, from the top)
+// gives the key of the last one kept and how many equal ones go with it, and a walk in
+// the order of the positions, a stretch per warp, writes them down.  A second launch
+// moves the rows.  The keys stay in shared memory where all positions fit (8192 of
+// them in each of 128 blocks: 16 us, 26 us without), else each step forms them
+// again from the weights.
+constexpr int kEvThr = 1024, kEvWarps = kEvThr / 32;
+constexpr int kEvBins = 2048;
+constexpr int kEvCached = 40960;      // positions whose keys fit shared memory
+constexpr uint32_t kKeyHeld = 0xffffffffu;   // above every weight's
 
 struct EvictParams {
   uint4 *kp, *vp;
@@ -741,35 +748,21 @@ struct EvictParams {
   int *kept, *new_lengths;
   float *new_sums;
   int B, Hkv, units;                  // units: 16-byte units of a head's row
-  int n_pages, page_size, max_pages, cap, new_max_pages, new_cap, budget, sinks, recent;
+  int n_pages, page_size, page_shift, max_pages, cap, new_max_pages, new_cap, budget, sinks, recent;
 };
 
-__device__ __forceinline__ bool present(const EvictParams &p, int b, int j) {
-  const int page = p.table[static_cast<long long>(b) * p.max_pages + j / p.page_size];
-  return page >= 0 && page < p.n_pages;
-}
-
-// Order of the weights as unsigned numbers: larger weight, larger number;
-// NaN counts as -infinity, -0 as 0.
+// Order of the weights as unsigned numbers: larger weight, larger number, from
+// 0x007fffff (-infinity, and NaN) to 0xff800000; -0 counts as 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
   const uint32_t u = __float_as_uint(w != w ? -INFINITY : w + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Sum over the block of a count, for every thread.
-__device__ __forceinline__ int block_count(int x, int *warp_s) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  x = __reduce_add_sync(0xffffffffu, x);
-  __syncthreads();
-  if (lane == 0) warp_s[warp] = x;
-  __syncthreads();
-  return __reduce_add_sync(0xffffffffu, warp_s[lane]);
-}
-
+template <bool kCache>
 __global__ void __launch_bounds__(kEvThr, 1) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ int hist[256], warp_s[32], warp_e[32];
-  __shared__ uint32_t digit_s;
-  __shared__ int need_s;
+  extern __shared__ uint32_t keys[];
+  __shared__ int hist[kEvBins], warp_a[kEvWarps], warp_b[kEvWarps];
+  __shared__ int digit_s, need_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / p.Hkv, h = blockIdx.x - b * p.Hkv;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -778,93 +771,98 @@ __global__ void __launch_bounds__(kEvThr, 1) evict_select_kernel(const __grid_co
   const float *sums = p.sums + static_cast<size_t>(blockIdx.x) * p.cap;
   int *kept = p.kept + static_cast<size_t>(blockIdx.x) * p.budget;
   float *new_sums = p.new_sums + static_cast<size_t>(blockIdx.x) * p.new_cap;
+  auto form = [&](int j) -> uint32_t {
+    const int pg = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
+    const int page = p.table[static_cast<long long>(b) * p.max_pages + pg];
+    if (page < 0 || page >= p.n_pages) return 0u;
+    return j < p.sinks || j >= late ? kKeyHeld : weight_key(sums[j]);
+  };
+  auto key = [&](int j) -> uint32_t { return kCache ? keys[j] : form(j); };
 
-  int here = 0, held = 0;
+  int here = 0;
+#pragma unroll 4
   for (int j = tid; j < n; j += kEvThr) {
-    if (!present(p, b, j)) continue;
-    ++here;
-    held += j < p.sinks || j >= late;
+    const uint32_t k = form(j);
+    if (kCache) keys[j] = k;
+    here += k != 0u;
   }
-  here = block_count(here, warp_s);
-  held = block_count(held, warp_s);
+  here = __reduce_add_sync(0xffffffffu, here);
+  if (lane == 0) warp_a[warp] = here;
+  __syncthreads();
+  here = __reduce_add_sync(0xffffffffu, warp_a[lane]);
   const int m = min(here, p.budget);
-  // the smallest key that is kept, and how many of its equals (the first ones)
-  uint32_t least = 0;
+  // the smallest key that is kept, and how many of its equals (the first ones); those
+  // that are held are at most sinks + recent <= budget
+  uint32_t least = 1u;
   int ties = n;
   if (here > p.budget) {
-    int need = p.budget - held;            // of the others; held <= sinks + recent <= budget
-    uint32_t prefix = 0;
-    if (need == 0) {
-      least = 0xffffffffu;                 // above every weight's key
-      ties = 0;
-    }
-    for (int shift = 24; need > 0 && shift >= 0; shift -= 8) {
+    int need = m;
+    uint32_t prefix = 0u;
+    for (int step = 0; step < 3; ++step) {
+      const int shift = step == 0 ? 21 : step == 1 ? 10 : 0, bits = step == 2 ? 10 : 11;
       __syncthreads();
-      if (tid < 256) hist[tid] = 0;
+      for (int i = tid; i < kEvBins; i += kEvThr) hist[i] = 0;
       __syncthreads();
+#pragma unroll 4
       for (int j = tid; j < n; j += kEvThr) {
-        if (j < p.sinks || j >= late || !present(p, b, j)) continue;
-        const uint32_t k = weight_key(sums[j]);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255], 1);
+        const uint32_t k = key(j);
+        if (step == 0 || (k >> (shift + bits)) == (prefix >> (shift + bits))) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1);
       }
       __syncthreads();
-      if (warp == 0) {                     // lane i: bins 8 i .. 8 i + 7; those above it are counted first
-        int c[8], sum = 0;
+      // thread i: bins 2 i and 2 i + 1; what is above them in its warp, then in others
+      const int lo = hist[2 * tid], hi = hist[2 * tid + 1];
+      int above = lo + hi;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += c[i] = hist[8 * lane + i];
-        int above = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int o = __shfl_down_sync(0xffffffffu, above, d);
-          if (lane + d < 32) above += o;
-        }
-        above -= sum;
-        if (above < need && above + sum >= need) {
-#pragma unroll
-          for (int i = 7; i >= 0; --i) {
-            if (above + c[i] >= need) {
-              digit_s = 8 * lane + i;
-              need_s = need - above;
-              break;
-            }
-            above += c[i];
-          }
-        }
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_down_sync(0xffffffffu, above, d);
+        if (lane + d < 32) above += o;
+      }
+      if (lane == 0) warp_a[warp] = above;
+      __syncthreads();
+      above += __reduce_add_sync(0xffffffffu, lane > warp ? warp_a[lane] : 0) - lo - hi;
+      if (above < need && above + hi >= need) {
+        digit_s = 2 * tid + 1;
+        need_s = need - above;
+      } else if (above + hi < need && above + hi + lo >= need) {
+        digit_s = 2 * tid;
+        need_s = need - above - hi;
       }
       __syncthreads();
-      prefix |= digit_s << shift;
+      prefix |= static_cast<uint32_t>(digit_s) << shift;
       need = need_s;
-      least = prefix;
-      ties = need;
     }
+    least = prefix;
+    ties = need;
   }
-  // ---- in the order of the positions
-  int out = 0, equal = 0;
-  for (int j0 = 0; j0 < n; j0 += kEvThr) {
-    const int j = j0 + tid;
-    const bool there = j < n && present(p, b, j);
-    const bool hold = there && (j < p.sinks || j >= late);
-    const float w = there ? sums[j] : 0.f;
-    const uint32_t k = weight_key(w);
-    const bool eq = there && !hold && k == least;
-    const uint32_t eqs = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) warp_e[warp] = __popc(eqs);
-    __syncthreads();
-    const int e = warp_e[lane];
-    const int eq_before = equal + __reduce_add_sync(0xffffffffu, lane < warp ? e : 0) + __popc(eqs & ((1u << lane) - 1));
-    equal += __reduce_add_sync(0xffffffffu, e);
-    const bool keep = hold || (there && k > least) || (eq && eq_before < ties);
+  // ---- in the order of the positions: warp w takes a stretch of them
+  const int stretch = ((n + kEvThr - 1) / kEvThr) * 32;
+  const int j0 = min(n, warp * stretch), j1 = min(n, j0 + stretch);
+  int more = 0, equal = 0;                 // above `least` and equal to it
+  for (int j = j0 + lane; j - lane < j1; j += 32) {
+    const uint32_t k = j < j1 ? key(j) : 0u;
+    more += __popc(__ballot_sync(0xffffffffu, k > least));
+    equal += __popc(__ballot_sync(0xffffffffu, k == least && k != 0u));
+  }
+  // with `least` 1 (all are kept) no key equals it: weights' keys begin higher
+  __syncthreads();
+  if (lane == 0) warp_a[warp] = more, warp_b[warp] = equal;
+  __syncthreads();
+  more = __reduce_add_sync(0xffffffffu, lane < warp ? warp_a[lane] : 0);
+  equal = __reduce_add_sync(0xffffffffu, lane < warp ? warp_b[lane] : 0);
+  int out = more + min(equal, ties);
+  const uint32_t before = (1u << lane) - 1u;
+  for (int j = j0 + lane; j - lane < j1; j += 32) {
+    const uint32_t k = j < j1 ? key(j) : 0u;
+    const uint32_t eq = __ballot_sync(0xffffffffu, k == least);
+    const bool keep = k > least || (k == least && equal + __popc(eq & before) < ties);
     const uint32_t ks = __ballot_sync(0xffffffffu, keep);
-    if (lane == 0) warp_s[warp] = __popc(ks);
-    __syncthreads();
-    const int c = warp_s[lane];
-    const int at = out + __reduce_add_sync(0xffffffffu, lane < warp ? c : 0) + __popc(ks & ((1u << lane) - 1));
-    out += __reduce_add_sync(0xffffffffu, c);
+    const int at = out + __popc(ks & before);
     if (keep && at < m) {
       kept[at] = j;
-      new_sums[at] = w;
+      new_sums[at] = sums[j];
     }
-    __syncthreads();
+    equal += __popc(eq);
+    out += __popc(ks);
   }
   for (int i = m + tid; i < p.budget; i += kEvThr) kept[i] = -1;
   for (int i = m + tid; i < p.new_cap; i += kEvThr) new_sums[i] = 0.f;
@@ -910,6 +908,12 @@ __global__ void __launch_bounds__(kMvThr) evict_move_kernel(const __grid_constan
   }
 }
 
+// log2 of a power of two, else -1
+int shift_of(int x) {
+  for (int i = 0; i < 31; ++i)
+    if (x == 1 << i) return i;
+  return -1;
+}
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // Sizes of a decode call that its launch and its workspace share.
@@ -1011,9 +1015,7 @@ cudaError_t launch_attn_decode_paged(const PagesArgs &a, const void *q, int bf16
   p.score_stride = s.score_stride;
   p.B = a.B, p.Hq = Hq, p.Hkv = a.Hkv, p.D = a.D, p.G = Hq / a.Hkv, p.ng = s.ng, p.rows = s.rows;
   p.n_pages = a.n_pages, p.page_size = a.page_size, p.max_pages = a.max_pages;
-  p.page_shift = -1;
-  for (int i = 0; i < 31; ++i)
-    if (a.page_size == 1 << i) p.page_shift = i;
+  p.page_shift = shift_of(a.page_size);
   p.window = window, p.sinks = sinks;
   p.q_bf16 = bf16, p.ctas = s.ctas, p.wt_chunks = s.wt_chunks;
   p.wt_len = s.wt_chunks ? static_cast<int>(ceil_div(std::max(tokens, 1LL), s.wt_chunks)) : 0;
@@ -1041,8 +1043,14 @@ cudaError_t launch_kv_pages_evict(const PagesArgs &a, const float *weight_sums, 
   p.budget = budget, p.sinks = sinks, p.recent = recent;
   const long long blocks = static_cast<long long>(a.B) * a.Hkv;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  evict_select_kernel<<<static_cast<unsigned>(blocks), kEvThr, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+  p.page_shift = shift_of(a.page_size);
+  const bool cached = p.cap <= kEvCached;
+  auto select = cached ? evict_select_kernel<true> : evict_select_kernel<false>;
+  const int smem = cached ? p.cap * 4 : 0;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(select), cached ? kEvCached * 4 : 0);
+  if (e != cudaSuccess) return e;
+  select<<<static_cast<unsigned>(blocks), kEvThr, smem, st>>>(p);
+  e = cudaGetLastError();
   if (e != cudaSuccess || a.n_pages == 0 || a.max_pages == 0) return e;
   const long long total = blocks * budget * p.units;
   const long long grid = std::min<long long>(ceil_div(total, kMvThr * kMvUnroll), 152 * 32);
