@@ -517,7 +517,7 @@ abw_status attn_bwd_window(const void *q, const void *k, const void *v, const vo
  * block_table[b][p / page_size].  An entry outside 0 .. n_pages - 1 is an absent
  * page: its tokens are neither read nor written.  (A dense cache [B][S][Hkv][D]
  * is one of B pages of S rows.)  Any page_size >= 1 with page_size * max_pages
- * below 2^31.
+ * at most 2^31 - 2^16.
  */
 
 /*

@@ -110,6 +110,17 @@ def decode(lib, mem=None, dt=1, Bn=2, Hq=4, Hkv=2, D=64, n=4, page=8, most=2, wi
                                  None)
 
 
+def test_tables_end_where_positions_leave_32_bits(lib, mem):
+    """The walks over positions step past the last one by up to a block's
+    stretch of them; 2^31 - 2^16 positions leave the room for it."""
+    for most in (0x7fff0001, 0x7fffffff):
+        assert decode(lib, page=1, most=most) == B.ENOTSUP and write(lib, page=1, most=most) == B.ENOTSUP
+        assert evict(lib, page=1, most=most) == B.ENOTSUP and evict(lib, page=1, fresh=most) == B.ENOTSUP
+    most = 0x7fff0000                                                       # on to the next check: NULL
+    assert decode(lib, page=1, most=most) == B.EWORKSPACE and write(lib, page=1, most=most) == B.EINVAL
+    assert evict(lib, page=1, most=most) == B.EINVAL and evict(lib, page=1, fresh=most) == B.EINVAL
+
+
 def test_attn_decode_paged_refusals(lib, mem):
     size = lib.attn_decode_paged_workspace_bytes
     assert decode(lib, D=32) == B.ENOTSUP and decode(lib, D=256) == B.ENOTSUP

@@ -196,8 +196,9 @@ abw_status check_window(const char *op, int B, int T, int Hq, int Hkv, int D, in
 abw_status check_pages(const char *op, int B, int Hkv, int D, int n_pages, int page_size, int max_pages) {
   if (B < 0 || Hkv < 0 || n_pages < 0 || max_pages < 0) return fail(ABW_EINVAL, "%s: negative size", op);
   if (page_size < 1) return fail(ABW_EINVAL, "%s: page_size=%d must be >= 1", op, page_size);
-  if (static_cast<long long>(page_size) * max_pages > 0x7fffffff)
-    return fail(ABW_ENOTSUP, "%s: page_size * max_pages = %lld is above 2^31 - 1", op,
+  // the kernels step past the last position by up to a block's stretch, in 32 bits
+  if (static_cast<long long>(page_size) * max_pages > 0x7fff0000)
+    return fail(ABW_ENOTSUP, "%s: page_size * max_pages = %lld is above 2^31 - 2^16", op,
                 static_cast<long long>(page_size) * max_pages);
   if (D < 8 || D % 8 != 0) return fail(ABW_ENOTSUP, "%s: D=%d is not a multiple of 8", op, D);
   if (static_cast<long long>(Hkv) * D > 0x7fffffff) return fail(ABW_ENOTSUP, "%s: more than 2^31 elements a token", op);

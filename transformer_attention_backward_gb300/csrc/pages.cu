@@ -1020,11 +1020,11 @@ cudaError_t launch_attn_decode_paged(const PagesArgs &a, const void *q, int bf16
   p.q_bf16 = bf16, p.ctas = s.ctas, p.wt_chunks = s.wt_chunks;
   p.wt_len = s.wt_chunks ? static_cast<int>(ceil_div(std::max(tokens, 1LL), s.wt_chunks)) : 0;
   p.sl2 = scale * 1.4426950408889634f;
+  const long long blocks = p.ctas + static_cast<long long>(s.wt_chunks) * a.B * a.Hkv;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaError_t e = a.D == 64 ? (bf16 ? launch_split<64, false>(p, st) : launch_split<64, true>(p, st))
                             : (bf16 ? launch_split<128, false>(p, st) : launch_split<128, true>(p, st));
   if (e != cudaSuccess) return e;
-  const long long blocks = p.ctas + static_cast<long long>(s.wt_chunks) * a.B * a.Hkv;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   return launch_dependent(decode_finish_kernel, static_cast<unsigned>(blocks), kFinThr, st, p);
 }
 
