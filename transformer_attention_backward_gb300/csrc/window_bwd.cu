@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kJoinThr) window_join_kernel(const __grid_cons
 #pragma unroll 4
     for (int i = 0; i < w.nparts; ++i) {
       if (i >= all) break;
-      const float4 v = src[static_cast<size_t>(i) * 2 * (kD / 4) * kBlk];
+      const float4 v = __ldcg(src + static_cast<size_t>(i) * 2 * (kD / 4) * kBlk);
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
     const long long at = static_cast<long long>(w.b) * p.T + tok;
@@ -651,8 +651,9 @@ struct DqItem {
 };
 __device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
   DqItem r;
+  idx = p.dq_items - 1 - idx;
   r.h = p.by_nb(idx);               // idx becomes the place in the head
-  r.m = p.g.nb - 1 - idx;
+  r.m = idx;
   r.b = p.by_hq(r.h);
   r.n = tokens_warp(p.lengths, r.b, p.T);
   r.lo = p.g.lo(r.m);
