@@ -41,6 +41,7 @@ using namespace win;
 
 constexpr int kThr = 384;        // dq kernel
 constexpr int kKvThr = 512;      // kv kernel
+constexpr long long kGroupBytes = 72 << 20;
 constexpr int kTileBytes = kBlk * kBlk * 2;    // one dS^T tile: [2 query halves][128 keys][64 queries]
 
 // Which blocks meet, and where their dS tiles stand within a head.
@@ -91,9 +92,13 @@ struct BwdParams {
   long long o_stride, dk_stride, dv_stride, tiles;
   Grid g;
   int first_parts, parts_each;    // CTAs per key block: first tokens', others
-  int per_unit, slots;            // items and part slots per (batch, KV head)
+  int per_unit, slots;            // items (without the first tokens') and part slots per (batch, KV head)
   int items, dq_items;
-  Div by_unit, by_hkv, by_first, by_each, by_hq, by_chunks, by_nb, by_g;   // per_unit, Hkv, first_parts, parts_each, ..
+  int units, group;               // (batch, KV head)s, in scheduling groups
+  int lead_items, lead_rounds, lead_rest, span, rounds;   // see kv_nth
+  Div by_units, by_group, by_width, by_last;  // units, items of a group, its units (the last one's)
+  Div by_dq_group, by_dq_width, by_dq_last;   // the same of the dq kernel's items, heads
+  Div by_hkv, by_first, by_each, by_hq, by_chunks, by_g;   // Hkv, first_parts, parts_each, ..
   float scale;
   WaitCtl wait;
 };
@@ -170,11 +175,32 @@ struct KvSmem {
   static_assert(kBytes <= 232448, "kv kernel shared memory");
 };
 
-// Item of a CTA's r-th round: rounds go through the CTAs back and forth, so that
-// items whose lengths repeat with a period that divides the grid spread over all.
+// Item of a CTA's r-th round, in rounds that go through the CTAs back and forth: where
+// the items become shorter towards their end, the CTAs' sums come out alike.
 __device__ __forceinline__ int nth_item(int r) {
   const int c = blockIdx.x, n = gridDim.x;
   return r * n + ((r & 1) ? n - 1 - c : c);
+}
+
+// The same for the kv kernel, whose items are first the first tokens' blocks of keys,
+// dealt in turn, then the others, block of keys by block of keys through the units of
+// a group, so that the short ones, whose queries end with the sequence, come last.
+// `lead_rest` CTAs have one of the long items more; while they work on it the others
+// take `span` of the others.
+__device__ __forceinline__ int kv_nth(const BwdParams &p, int r) {
+  const int c = blockIdx.x, n = gridDim.x, rest = p.lead_rest;
+  const int lead = p.lead_rounds + (c < rest);
+  if (r < lead) return c + r * n;
+  r -= lead;
+  int from = p.lead_items;
+  if (rest > 0) {
+    if (c >= rest) {
+      if (r < p.span) return from + r * (n - rest) + c - rest;
+      r -= p.span;
+    }
+    from += p.span * (n - rest);
+  }
+  return from + nth_item(r);
 }
 
 struct KvItem {
@@ -185,13 +211,21 @@ struct KvItem {
 
 __device__ __noinline__ KvItem kv_item(const BwdParams &p, int idx) {
   KvItem r;
-  const int unit = p.by_unit(idx);          // idx becomes the place in the unit
+  const bool lead = idx < p.lead_items;
+  int unit, head = 0;                       // slots in front of the place's
+  if (lead) {
+    r.part = p.by_units(idx);
+    unit = idx;
+  } else {
+    idx -= p.lead_items;
+    unit = p.by_group(idx) * p.group;       // idx becomes the place in the group
+    r.part = unit + p.group <= p.units ? p.by_width(idx) : p.by_last(idx);
+    unit += idx;
+    if (p.first_parts > 1) head = p.g.first * p.first_parts;
+  }
   r.kvh = unit;
   r.b = p.by_hkv(r.kvh);
-  const int head = p.g.first * p.first_parts;
-  const bool lead = idx < head;
-  r.slot = static_cast<long long>(unit) * p.slots + (lead ? idx : (p.first_parts > 1 ? head : 0) + idx - head);
-  r.part = lead ? idx : idx - head;
+  r.slot = static_cast<long long>(unit) * p.slots + head + r.part;
   const Div &div = lead ? p.by_first : p.by_each;
   r.kb = div(r.part) + (lead ? 0 : p.g.first);
   r.nparts = div.d;
@@ -212,8 +246,8 @@ struct KvStream {
   bool valid;
   __device__ __forceinline__ void find(const BwdParams &p) {
     valid = false;
-    for (; !valid && round * static_cast<int>(gridDim.x) < p.items; ++round) {
-      const int idx = nth_item(round);
+    for (; !valid && round < p.rounds; ++round) {
+      const int idx = kv_nth(p, round);
       if (idx >= p.items) continue;
       w = kv_item(p, idx);
       if (w.it0 == w.it1) continue;
@@ -350,8 +384,8 @@ __global__ void __launch_bounds__(kKvThr, 1)
     int round = 0;
     auto next_item = [&]() -> int {
       int pairs = 0;
-      for (; pairs == 0 && round * static_cast<int>(gridDim.x) < p.items; ++round) {
-        const int idx = nth_item(round);
+      for (; pairs == 0 && round < p.rounds; ++round) {
+        const int idx = kv_nth(p, round);
         if (idx >= p.items) continue;
         const KvItem w = kv_item(p, idx);
         pairs = __shfl_sync(0xffffffffu, w.it1 - w.it0, 0);
@@ -599,29 +633,33 @@ __global__ void __launch_bounds__(kKvThr, 1)
 }
 
 // ---------------------------------------------------------------------- join
-// Parts of the key blocks that went to several CTAs, summed in their order: a
-// block per (batch, KV head, key block) and 32 keys.  Runs beside the dq kernel,
-// which lets it start once the kv kernel has completed.
+// Parts of the key blocks that went to several CTAs, summed in their order: four
+// components of dV or dK per thread, with all its loads under way at one time (a block
+// for each 32 keys that goes through them took 11 us of a layer's 33, now JOIN).  Runs
+// beside the dq kernel, which lets it start once the kv kernel has completed.
 constexpr int kJoinThr = 256;
+template <int kD>
+constexpr int kJoinBlocks = 4 * 2 * 32 * (kD / 4) / kJoinThr;   // per (batch, KV head, key block)
 
 template <int kD>
 __global__ void __launch_bounds__(kJoinThr) window_join_kernel(const __grid_constant__ BwdParams p) {
   const int nk = p.parts_each > 1 ? p.g.nb : p.g.first;   // key blocks with parts
-  const int quarter = blockIdx.x & 3;
-  const int unit = (blockIdx.x >> 2) / nk, kb = (blockIdx.x >> 2) - unit * nk;
-  const int idx = unit * p.per_unit + (kb < p.g.first ? kb * p.first_parts : p.g.first * p.first_parts + (kb - p.g.first) * p.parts_each);
+  const int sub = blockIdx.x % kJoinBlocks<kD>, block = blockIdx.x / kJoinBlocks<kD>;
+  const int unit = block / nk, kb = block - unit * nk;
+  const int group = unit / p.group * p.group, width = min(p.group, p.units - group);
+  const int idx = kb < p.g.first ? kb * p.first_parts * p.units + unit
+                                 : p.lead_items + group * p.per_unit + (kb - p.g.first) * p.parts_each * width + unit - group;
   const KvItem w = kv_item(p, idx);
   // of fewer pairs than parts only the first parts have one and were written
   const int all = p.G * w.qn;
-  for (int e = threadIdx.x; e < 2 * 32 * kD / 4; e += kJoinThr) {
-    const int x = e / (32 * kD / 4), r = 32 * quarter + e % 32, c = e / 32 % (kD / 4);
-    const int tok = kb * kBlk + r;
-    if (tok >= p.T) continue;
+  const int e = sub * kJoinThr + threadIdx.x, r = e % kBlk, c = e / kBlk % (kD / 4), x = e / kBlk / (kD / 4);
+  const int tok = kb * kBlk + r;
+  if (tok < p.T) {
     const float4 *src = reinterpret_cast<const float4 *>(p.parts) + ((w.slot * 2 + x) * (kD / 4) + c) * kBlk + r;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < w.nparts; ++i) {
-      if (i >= all) break;
+    const int n = min(w.nparts, all);
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
       const float4 v = __ldcg(src + static_cast<size_t>(i) * 2 * (kD / 4) * kBlk);
       s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
@@ -652,8 +690,9 @@ struct DqItem {
 __device__ __forceinline__ DqItem dq_item(const BwdParams &p, int idx) {
   DqItem r;
   idx = p.dq_items - 1 - idx;
-  r.h = p.by_nb(idx);               // idx becomes the place in the head
-  r.m = idx;
+  const int unit = p.by_dq_group(idx) * p.group;   // idx becomes the place in the group
+  r.m = unit + p.group <= p.units ? p.by_dq_width(idx) : p.by_dq_last(idx);
+  r.h = unit * p.G + idx;
   r.b = p.by_hq(r.h);
   r.n = tokens_warp(p.lengths, r.b, p.T);
   r.lo = p.g.lo(r.m);
@@ -814,7 +853,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 struct BwdSizes {
   Grid g;
   int Tp, first_parts, parts_each, per_unit, slots;
-  long long tiles;
+  long long tiles, first_pairs, each_pairs;   // dS tiles per head; pairs of an item, at most
   size_t stats, ds, parts;   // bytes
 };
 
@@ -826,15 +865,17 @@ BwdSizes bwd_sizes(int B, int T, int Hq, int Hkv, int D, int window, int sinks) 
   const long long units = static_cast<long long>(B) * Hkv;
   s.Tp = g.nb * kBlk;
   s.tiles = g.tile0(g.nb);
-  // Pairs per CTA: a key block's own while there are items enough to fill 152 SMs
+  // Pairs per item: a key block's own while there are items enough to fill 152 SMs
   // twice, else an equal share of all pairs, at least 2.  The first tokens' blocks
-  // have more pairs and are cut to about that.
+  // have more pairs and are cut to an equal share of all.
   const long long each = static_cast<long long>(G) * std::min(g.nb, g.wq), total = units * G * s.tiles;
-  long long most = std::max(2LL, std::min(each, (total + 151) / 152));
-  if (units * g.nb >= 304) most = each;
+  const long long share = std::max(2LL, (total + 151) / 152), most = units * g.nb >= 304 ? each : std::min(each, share);
   s.parts_each = static_cast<int>((each + most - 1) / most);
-  s.first_parts = static_cast<int>((static_cast<long long>(G) * g.nb + most - 1) / most);
-  s.per_unit = g.first * s.first_parts + (g.nb - g.first) * s.parts_each;
+  s.first_pairs = static_cast<long long>(G) * g.nb;
+  s.first_parts = static_cast<int>((s.first_pairs + share - 1) / share);
+  s.each_pairs = (each + s.parts_each - 1) / s.parts_each;
+  s.first_pairs = (s.first_pairs + s.first_parts - 1) / s.first_parts;
+  s.per_unit = (g.nb - g.first) * s.parts_each;
   s.slots = (s.first_parts > 1 ? g.first * s.first_parts : 0) + (s.parts_each > 1 ? (g.nb - g.first) * s.parts_each : 0);
   s.stats = up256(static_cast<size_t>(B) * Hq * s.Tp * 4);
   s.ds = static_cast<size_t>(B) * Hq * s.tiles * kTileBytes;
@@ -888,7 +929,7 @@ cudaError_t launch(const WindowArgs &a, BwdParams &p, const BwdSizes &s, int sms
   if (e != cudaSuccess) return e;
   if (s.slots > 0) {
     const int nk = s.parts_each > 1 ? s.g.nb : s.g.first;
-    cfg.gridDim = dim3(a.B * a.Hkv * nk * 4);
+    cfg.gridDim = dim3(a.B * a.Hkv * nk * kJoinBlocks<kD>);
     cfg.blockDim = dim3(kJoinThr);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, window_join_kernel<kD>, p);
@@ -910,9 +951,10 @@ cudaError_t launch_window_bwd(const WindowArgs &a, const WaitCtl &w, cudaStream_
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const BwdSizes s = bwd_sizes(a.B, a.T, a.Hq, a.Hkv, a.D, a.window, a.sinks);
-  const long long items = static_cast<long long>(a.B) * a.Hkv * s.per_unit;
+  const long long units = static_cast<long long>(a.B) * a.Hkv, lead_items = units * s.g.first * s.first_parts;
+  const long long items = lead_items + units * s.per_unit;
   const long long dq_items = static_cast<long long>(a.B) * a.Hq * s.g.nb;
-  if (std::max(items, dq_items) > 0x1fffffffLL) {
+  if (items > 0x03ffffffLL || dq_items > 0x1fffffffLL) {   // the join's grid is up to 32 times the items
     *why = "grid too large";
     return cudaErrorNotSupported;
   }
@@ -933,9 +975,21 @@ cudaError_t launch_window_bwd(const WindowArgs &a, const WaitCtl &w, cudaStream_
   p.g = s.g;
   p.first_parts = s.first_parts, p.parts_each = s.parts_each, p.per_unit = s.per_unit, p.slots = s.slots;
   p.items = static_cast<int>(items), p.dq_items = static_cast<int>(dq_items);
-  p.by_unit = Div::by(s.per_unit), p.by_hkv = Div::by(a.Hkv);
+  p.units = static_cast<int>(units), p.lead_items = static_cast<int>(lead_items);
+  const int grid = std::min(p.items, sms);
+  p.lead_rounds = p.lead_items / grid, p.lead_rest = p.lead_items % grid;
+  p.span = static_cast<int>(std::min((s.first_pairs + s.each_pairs / 2) / s.each_pairs, 1LL * (p.items / grid + 1)));
+  p.rounds = p.lead_rounds + 1 + p.span + (p.items - p.lead_items + grid - 1) / grid;
+  // Units of a group: what the blocks of keys that are worked on at one time meet of
+  // q and dout is to stay in L2
+  const long long meets = static_cast<long long>(p.G) * (s.g.wq + 1) * kBlk * a.D * 4;
+  p.group = p.items <= grid ? 1 : static_cast<int>(std::max(1LL, std::min<long long>(p.units, kGroupBytes / meets)));
+  const int last = (p.units - 1) % p.group + 1;
+  p.by_units = Div::by(p.units), p.by_group = Div::by(std::max(1, p.group * s.per_unit)), p.by_width = Div::by(p.group), p.by_last = Div::by(last);
+  p.by_dq_group = Div::by(p.group * p.G * s.g.nb), p.by_dq_width = Div::by(p.group * p.G), p.by_dq_last = Div::by(last * p.G);
+  p.by_hkv = Div::by(a.Hkv);
   p.by_first = Div::by(s.first_parts), p.by_each = Div::by(s.parts_each);
-  p.by_hq = Div::by(a.Hq), p.by_nb = Div::by(s.g.nb), p.by_g = Div::by(p.G);
+  p.by_hq = Div::by(a.Hq), p.by_g = Div::by(p.G);
   p.scale = a.scale;
   p.wait = w;
   return a.D == 64 ? launch<64>(a, p, s, sms, st, why) : launch<128>(a, p, s, sms, st, why);
