@@ -31,7 +31,10 @@ using namespace win;
 
 constexpr int kThr = 512;
 constexpr float kRescale = 8.f;       // lazy-rescale threshold (base-2 units)
-constexpr int kHeadGroup = 8;         // tile pairs of heads per scheduling group
+// K and V that a scheduling group's tiles meet at one time: many head units, so that the
+// CTAs' sums come out alike (8192 tokens of 32 heads, all keys: 36 MB 666, 72 480, 144 389
+// us), but not all of them (16 x 4096 tokens: 144 MB 1.73, no groups 1.81 ms).
+constexpr long long kGroupBytes = 144 << 20;
 
 template <int kD>
 struct FwdSmem {
@@ -55,7 +58,7 @@ struct FwdSmem {
 struct FwdParams {
   float *lse;
   const int *lengths;
-  int B, T, Hq, Hkv, G, nqb, per_head, units, items;
+  int B, T, Hq, Hkv, G, nqb, per_head, units, group, items;
   Div by_group, by_width, by_last, by_heads, by_g;   // items of a scheduling group, its width (the last one's), head units, G
   int pair_heads;         // tiles: 1 two heads of a group, 0 two blocks of queries
   int window, sinks, sink_blocks;
@@ -76,14 +79,21 @@ struct Unit {
   int b, u, m, n;   // batch, head unit, place along the queries, tokens
 };
 
+// Item of a CTA's r-th round, in rounds that go through the CTAs back and forth: items
+// become shorter towards the list's end, so the CTAs' sums come out alike.
+__device__ __forceinline__ int nth_item(int r) {
+  const int c = blockIdx.x, n = gridDim.x;
+  return r * n + ((r & 1) ? n - 1 - c : c);
+}
+
 __device__ __forceinline__ Unit unit_of(const FwdParams &p, int it) {
-  // (batch, head unit) in groups of kHeadGroup; in a group the late blocks of
-  // queries first, so that what runs at one time shares K and V in L2
+  // (batch, head unit) in groups; in a group the late blocks of queries first, so that
+  // what runs at one time shares K and V in L2 and the short items come last
   Unit r;
-  const int grp = p.by_group(it);             // `it` becomes the place in the group
-  const int m = (grp + 1) * kHeadGroup <= p.units ? p.by_width(it) : p.by_last(it);
+  const int first = p.by_group(it) * p.group;   // `it` becomes the place in the group
+  const int m = first + p.group <= p.units ? p.by_width(it) : p.by_last(it);
   r.m = p.per_head - 1 - m;
-  r.u = grp * kHeadGroup + it;
+  r.u = first + it;
   r.b = p.by_heads(r.u);
   r.n = tokens_warp(p.lengths, r.b, p.T);
   return r;
@@ -151,7 +161,9 @@ __global__ void __launch_bounds__(kThr, 1)
       }
       int r = 0, raw = 0, nq[2] = {0, 0};   // ring position, repaired blocks, Q tiles so far
       bool ok = true;
-      for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+      for (int rd = 0; ok; ++rd) {
+        const int it = nth_item(rd);
+        if (it >= p.items) break;
         const Unit w = unit_of(p, it);
         const Tile t0 = tile_of(p, w, 0), t1 = tile_of(p, w, 1), all = both_tiles(t0, t1);
         int rest = t0.h;
@@ -214,7 +226,7 @@ __global__ void __launch_bounds__(kThr, 1)
       // and the parities of its P tiles, outputs and Q tiles
       uint32_t pend = 0, opens = 0, closes = 0, np = 0, ni = 0, nq = 0;
       bool ok = may_wait(p.wait, abort_flag, kSiteWinFwd, M::kQFull);
-      int it = blockIdx.x, x = 0;
+      int rd = 0, x = 0;
       Unit w = {};
       Tile ta = {}, tb = {}, all = {};
       all.hi = -1;
@@ -226,6 +238,7 @@ __global__ void __launch_bounds__(kThr, 1)
         if (x >= all.steps()) {
           x = 0;
           begun = 0;
+          const int it = nth_item(rd++);
           more = it < p.items;
           all.hi = -1;
           if (more) {
@@ -233,7 +246,6 @@ __global__ void __launch_bounds__(kThr, 1)
             ta = tile_of(p, w, 0);
             tb = tile_of(p, w, 1);
             all = both_tiles(ta, tb);
-            it += gridDim.x;
             if (all.hi < 0) continue;
           }
         }
@@ -297,7 +309,9 @@ __global__ void __launch_bounds__(kThr, 1)
     float2 *stat = reinterpret_cast<float2 *>(smem + M::kStat) + t * 128 + row;
     int ns = 0, no = 0;                                 // S tiles, outputs so far
     bool ok = true;
-    for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+    for (int rd = 0; ok; ++rd) {
+        const int it = nth_item(rd);
+        if (it >= p.items) break;
       const Unit w = unit_of(p, it);
       const Tile x = tile_of(p, w, t);
       const int i = x.q0 + row;
@@ -437,7 +451,9 @@ __global__ void __launch_bounds__(kThr, 1)
     unsigned char *stage = smem + M::kOut + qd * 4096;
     uint32_t no = 0;                                     // parities of the tiles' outputs so far
     bool ok = true;
-    for (int it = blockIdx.x; ok && it < p.items; it += gridDim.x) {
+    for (int rd = 0; ok; ++rd) {
+        const int it = nth_item(rd);
+        if (it >= p.items) break;
       const Unit w = unit_of(p, it);
 #pragma unroll 1
       for (int t = 0; ok && t < 2; ++t) {
@@ -529,7 +545,7 @@ cudaError_t launch_window_fwd(const WindowArgs &a, const WaitCtl &w, cudaStream_
   p.per_head = p.pair_heads ? p.nqb : (p.nqb + 1) / 2;
   const long long units = static_cast<long long>(a.B) * (p.pair_heads ? a.Hq / 2 : a.Hq);
   const long long items = units * p.per_head;
-  if (items > 0x7fff0000LL || p.per_head > 0x7fff0000 / kHeadGroup) {
+  if (items > 0x7fff0000LL) {
     *why = "grid too large";
     return cudaErrorNotSupported;
   }
@@ -538,9 +554,12 @@ cudaError_t launch_window_fwd(const WindowArgs &a, const WaitCtl &w, cudaStream_
   p.sink_blocks = (p.sinks + kBlk - 1) / kBlk;
   p.scale = a.scale;
   p.wait = w;
-  p.by_group = Div::by(kHeadGroup * p.per_head);
-  p.by_width = Div::by(kHeadGroup);
-  p.by_last = Div::by(std::max(1, p.units % kHeadGroup));
+  // what the tiles that are worked on at one time meet of K and V is to stay in L2
+  const long long meets = static_cast<long long>(std::min(p.nqb, (p.window + kBlk - 1) / kBlk + 2)) * kBlk * a.D * 4;
+  p.group = static_cast<int>(std::max(1LL, std::min(units, kGroupBytes / meets * (p.pair_heads ? p.G / 2 : p.G))));
+  p.by_group = Div::by(p.group * p.per_head);
+  p.by_width = Div::by(p.group);
+  p.by_last = Div::by((p.units - 1) % p.group + 1);
   p.by_heads = Div::by(p.pair_heads ? a.Hq / 2 : a.Hq);
   p.by_g = Div::by(p.G);
   const int grid = static_cast<int>(std::min<long long>(items, sms));
