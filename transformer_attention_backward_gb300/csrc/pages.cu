@@ -18,7 +18,7 @@
 // fp32): a tile with a larger max rescales l and O by 2^(m_old - m_new).
 //
 // The bound is the cache's bytes.  A warp copies (cp.async) its tile's rows whole, two
-// 256-byte rows an instruction, into a ring of three tiles (24 KB at D = 128) of its
+// 256-byte rows an instruction, into a ring of two tiles (16 KB at D = 128) of its
 // own, each 16-byte unit to where the lane that feeds it to the tensor core reads it:
 // no barrier between warps, no bank conflict.  (With each lane copying its own units,
 // 64 bytes of eight rows an instruction, the copies alone ran at 5.3 of 7.2 TB/s.)
@@ -33,6 +33,11 @@
 // P enters as bf16 terms (two of them for bf16 outputs, three for fp32), fp32
 // queries as three, so nothing but the output is rounded to bf16.  The maximum is
 // lazy: it moves only when a score exceeds it by more than 8 (base 2).
+//
+// 8 sequences of up to 32768 tokens, 32 / 8 heads of 128, with weight sums: 131 us for
+// 668 MB of pages and 21 MB of scores (5.3 TB/s; the split alone 5.9).  64 sequences of
+// up to 1024, 20 / 5 heads: 38.5 us for 125 MB: a CTA has 33 tiles, and its launch, its
+// search for its place and the first copies take as long as they do.
 #include <math.h>
 
 #include <algorithm>
@@ -44,7 +49,9 @@ namespace {
 
 // ------------------------------------------------------------------- writing
 // One block per `tpb` tokens; 16-byte units, up to four of k and of v in
-// flight per thread.
+// flight per thread.  Bound by the bytes: 4 x up to 2048 tokens of 20 heads of 128 in 22
+// us (5.1 TB/s; two in flight 28, eight 29, pages looked up beside the rows 23); a step
+// of 64 tokens is a launch, 2.6 us.
 constexpr int kWrThr = 256;
 constexpr int kWrUnroll = 4;
 
@@ -870,7 +877,8 @@ __global__ void __launch_bounds__(kEvThr, 1) evict_select_kernel(const __grid_co
 }
 
 // Rows of the kept tokens, 16 bytes per thread and step; consecutive threads
-// take the units of a row, then its heads.
+// take the units of a row, then its heads.  Rows of 256 bytes from anywhere: 16 x 2048
+// of 8 heads move at 5.8 TB/s, and the whole call (8192 tokens each) takes 60 us.
 constexpr int kMvThr = 256, kMvUnroll = 4;
 
 __global__ void __launch_bounds__(kMvThr) evict_move_kernel(const __grid_constant__ EvictParams p, long long total) {

@@ -20,6 +20,15 @@
 // softmax of tile 0 and 1, 12-15 outputs (thread = query row).
 // Padding behind a sequence is not looked at: its keys are never visible, and
 // its rows of V, which meet weights of 0, are cleared in shared memory.
+//
+// The bound is the tensor core with the softmax beside it: a block of 128 x 128 at D =
+// 128 takes it 1024 cycles for the two products, and the exponentials of two such
+// blocks (32 a cycle and SM) as long as the products of one.  8192 tokens of 32 heads,
+// window 1024: 136 us, 950 TFLOP/s of the visible pairs; the products of the blocks
+// alone, cut ones whole, are some 100, the softmax alone 124; the rest is the change
+// from item to item.  All keys: 390 us, 1400 TFLOP/s.  What measured no better: an
+// issuer per tile, eight softmax warps per tile, cut blocks 32 columns at a time,
+// prefetches of the next queries into L2, outputs read out of TMEM before they are staged.
 #include <algorithm>
 
 #include "window.cuh"
