@@ -112,6 +112,17 @@ def test_more_items_than_sms(abw):
     check(abw, make(4, 2, 1100, 20, 5, 128), 400, 2)
 
 
+@pytest.mark.parametrize("B,T,Hq,Hkv,window,sinks,lengths", [
+    (3, 600, 20, 20, 64, 400, None),             # more blocks of first tokens than SMs
+    (2, 900, 40, 10, 128, 4, [900, 77]),         # theirs cut to parts, the others whole
+    (2, 1100, 16, 16, 130, 200, None),
+    (1, 1300, 6, 2, 300, 700, None),             # all cut
+    (3, 700, 30, 30, 1, 4, [0, 700, 350])])
+def test_long_items_among_short_ones(abw, B, T, Hq, Hkv, window, sinks, lengths):
+    """First tokens' blocks of keys meet many times the others' queries."""
+    check(abw, make(T, B, T, Hq, Hkv, 64), window, sinks, lengths)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("lengths", [[0, 300, 1], [128, 129, 255], [-5, 1000, 256], [0, 0, 0]])
 def test_padded_batch(abw, lengths, D):
