@@ -36,8 +36,8 @@
 //
 // 8 sequences of up to 32768 tokens, 32 / 8 heads of 128, with weight sums: 131 us for
 // 668 MB of pages and 21 MB of scores (5.3 TB/s; the split alone 5.9).  64 sequences of
-// up to 1024, 20 / 5 heads: 38.5 us for 125 MB: a CTA has 33 tiles, and its launch, its
-// search for its place and the first copies take as long as they do.
+// up to 1024, 20 / 5 heads: 31 us for 125 MB: a CTA has 33 tiles, and its launch, its
+// search for its place and the first copies take half as long as they do.
 #include <math.h>
 
 #include <algorithm>
@@ -300,8 +300,9 @@ __device__ __forceinline__ void terms(float x, float y, uint32_t (&out)[kN]) {
 }
 
 constexpr int dec_smem(int D, int warps) {
-  return warps * kDecStages * kTile * D * 4 + warps * 8 * (D + 4) * 4 + warps * 16 * 4;
+  return warps * kDecStages * kTile * D * 4 + warps * 4 * (D + 4) * 4 + warps * 8 * 4;
 }
+static_assert(2 * (dec_smem(128, 6) + 1024) <= 228 * 1024, "two CTAs per SM");
 
 // kF32: fp32 queries and outputs; kWide: more than 8 query heads per KV head;
 // kScores: scores are kept for the weight sums.
@@ -312,8 +313,8 @@ __global__ void __launch_bounds__(32 * dec_warps(kF32, kWide), 2) decode_split_k
   constexpr int kC = kD / 32, kV = kD / 64;               // 64-byte pieces of a k row, 128-byte pieces of a v row
   constexpr int kR = kWide ? 2 : 1;                       // row halves
   extern __shared__ __align__(128) unsigned char smem[];
-  float *mo = reinterpret_cast<float *>(smem + kDecWarps * kDecStages * kTile * kD * 4);   // [warps][8][kD + 4]
-  float *ms = mo + kDecWarps * 8 * (kD + 4);              // [warps][16] max, then [warps][16] sum
+  float *mo = reinterpret_cast<float *>(smem + kDecWarps * kDecStages * kTile * kD * 4);   // [warps][4][kD + 4]
+  float *ms = mo + kDecWarps * 4 * (kD + 4);              // [warps][4 max, 4 sum]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -539,23 +540,24 @@ __global__ void __launch_bounds__(32 * dec_warps(kF32, kWide), 2) decode_split_k
       stage = stage + 1 == kDecStages ? 0 : stage + 1;
     }
 
-    // ---- the warps' parts of the piece, joined through shared memory, eight rows at a time
+    // ---- the warps' parts of the piece, joined through shared memory, four rows at a time
+    // (with eight two CTAs do not fit an SM)
     const bool whole = now.tile0 == 0 && now.tend == now.tiles;
     float *slot = p.slots + (static_cast<size_t>(cta) * 2 + (first ? 0 : 1)) * p.rows * (kD + 4);
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
+    for (int rx = 0; rx < 2 * kR; ++rx) {
+      const int r = rx >> 1, x = rx & 1;                 // heads 8 r + 2 t + x
+      {
         float sum = l[r][x];
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (g == 0) {
-          ms[warp * 16 + 2 * t + x] = m[r][x];
-          ms[warp * 16 + 8 + 2 * t + x] = sum;
+          ms[warp * 8 + t] = m[r][x];
+          ms[warp * 8 + 4 + t] = sum;
         }
 #pragma unroll
         for (int c = 0; c < kV; ++c) {
-          float *dst = mo + (warp * 8 + 2 * t + x) * (kD + 4) + 64 * c + 8 * g;
+          float *dst = mo + (warp * 4 + t) * (kD + 4) + 64 * c + 8 * g;
 #pragma unroll
           for (int j = 0; j < 4; j += 2)
             *reinterpret_cast<float4 *>(dst + 2 * j) =
@@ -563,21 +565,21 @@ __global__ void __launch_bounds__(32 * dec_warps(kF32, kWide), 2) decode_split_k
         }
       }
       __syncthreads();
-      for (int e = tid; e < 8 * kD / 4; e += kDecThr) {
-        const int rr = e / (kD / 4), d = (e - rr * (kD / 4)) * 4, hrow = 8 * r + rr;
+      for (int e = tid; e < 4 * kD / 4; e += kDecThr) {
+        const int rr = e / (kD / 4), d = (e - rr * (kD / 4)) * 4, hrow = 8 * r + 2 * rr + x;
         if (hrow >= nrows) continue;
         float M = -INFINITY, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ms[w * 16 + rr]);
+        for (int w = 0; w < kDecWarps; ++w) M = fmaxf(M, ms[w * 8 + rr]);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) {
-          const float mw = ms[w * 16 + rr];
+          const float mw = ms[w * 8 + rr];
           const float f = mw == -INFINITY ? 0.f : ex2(mw - M);
-          const float4 x = *reinterpret_cast<const float4 *>(mo + (w * 8 + rr) * (kD + 4) + d);
-          L = fmaf(f, ms[w * 16 + 8 + rr], L);
-          acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y);
-          acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
+          const float4 y = *reinterpret_cast<const float4 *>(mo + (w * 4 + rr) * (kD + 4) + d);
+          L = fmaf(f, ms[w * 8 + 4 + rr], L);
+          acc.x = fmaf(f, y.x, acc.x), acc.y = fmaf(f, y.y, acc.y);
+          acc.z = fmaf(f, y.z, acc.z), acc.w = fmaf(f, y.w, acc.w);
         }
         if (whole) {
           const float inv = L > 0.f ? 1.f / L : 0.f;
