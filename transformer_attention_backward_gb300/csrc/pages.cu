@@ -34,8 +34,8 @@
 // queries as three, so nothing but the output is rounded to bf16.  The maximum is
 // lazy: it moves only when a score exceeds it by more than 8 (base 2).
 //
-// 8 sequences of up to 32768 tokens, 32 / 8 heads of 128, with weight sums: 131 us for
-// 668 MB of pages and 21 MB of scores (5.3 TB/s; the split alone 5.9).  64 sequences of
+// 8 sequences of up to 32768 tokens, 32 / 8 heads of 128, with weight sums: 128 us for
+// 668 MB of pages and 21 MB of scores (5.4 TB/s; the split alone 6.1).  64 sequences of
 // up to 1024, 20 / 5 heads: 31 us for 125 MB: a CTA has 33 tiles, and its launch, its
 // search for its place and the first copies take half as long as they do.
 #include <math.h>
