@@ -879,9 +879,11 @@ __global__ void __launch_bounds__(kEvThr, 1) evict_select_kernel(const __grid_co
 }
 
 // Rows of the kept tokens, 16 bytes per thread and step; consecutive threads
-// take the units of a row, then its heads.  Rows of 256 bytes from anywhere: 16 x 2048
-// of 8 heads move at 5.8 TB/s, and the whole call (8192 tokens each) takes 60 us.
-constexpr int kMvThr = 256, kMvUnroll = 4;
+// take the units of a row, then its heads.  Rows of 256 bytes from anywhere, each read and
+// written once and so streamed past L2: 16 x 8192 tokens of 8 heads to 2048 take 55 us a
+// call (60 with ordinary loads and stores), one sequence of 1025 to 512 8.8 us (9.8
+// with four steps of a thread under way in place of two).
+constexpr int kMvThr = 256, kMvUnroll = 2;
 
 __global__ void __launch_bounds__(kMvThr) evict_move_kernel(const __grid_constant__ EvictParams p, long long total) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -906,14 +908,14 @@ __global__ void __launch_bounds__(kMvThr) evict_move_kernel(const __grid_constan
       if (dst < 0 || dst >= p.n_pages || src < 0 || src >= p.n_pages) continue;
       const long long from = (static_cast<long long>(src) * p.page_size + (j - op * p.page_size)) * per_tok + in_tok;
       to[i] = (static_cast<long long>(dst) * p.page_size + (slot - np * p.page_size)) * per_tok + in_tok;
-      a[i] = p.kp[from];
-      c[i] = p.vp[from];
+      a[i] = __ldcs(p.kp + from);
+      c[i] = __ldcs(p.vp + from);
     }
 #pragma unroll
     for (int i = 0; i < kMvUnroll; ++i)
       if (to[i] >= 0) {
-        p.kp[to[i]] = a[i];
-        p.vp[to[i]] = c[i];
+        __stcs(p.kp + to[i], a[i]);
+        __stcs(p.vp + to[i], c[i]);
       }
   }
 }
