@@ -45,6 +45,13 @@ struct Div {
   }
 };
 
+// Item of a CTA's r-th round, in rounds that go through the CTAs back and forth: items
+// become shorter towards the list's end, so the CTAs' sums come out alike.
+__device__ __forceinline__ int nth_item(int r) {
+  const int c = blockIdx.x, n = gridDim.x;
+  return r * n + ((r & 1) ? n - 1 - c : c);
+}
+
 // The lowest x of 32 bits.
 __device__ __forceinline__ uint32_t below(int x) {
   const int n = min(max(x, 0), 32);

@@ -185,14 +185,7 @@ struct KvSmem {
   static_assert(kBytes <= 232448, "kv kernel shared memory");
 };
 
-// Item of a CTA's r-th round, in rounds that go through the CTAs back and forth: where
-// the items become shorter towards their end, the CTAs' sums come out alike.
-__device__ __forceinline__ int nth_item(int r) {
-  const int c = blockIdx.x, n = gridDim.x;
-  return r * n + ((r & 1) ? n - 1 - c : c);
-}
-
-// The same for the kv kernel, whose items are first the first tokens' blocks of keys,
+// nth_item for the kv kernel, whose items are first the first tokens' blocks of keys,
 // dealt in turn, then the others, block of keys by block of keys through the units of
 // a group, so that the short ones, whose queries end with the sequence, come last.
 // `lead_rest` CTAs have one of the long items more; while they work on it the others

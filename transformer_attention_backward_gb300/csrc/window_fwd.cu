@@ -88,13 +88,6 @@ struct Unit {
   int b, u, m, n;   // batch, head unit, place along the queries, tokens
 };
 
-// Item of a CTA's r-th round, in rounds that go through the CTAs back and forth: items
-// become shorter towards the list's end, so the CTAs' sums come out alike.
-__device__ __forceinline__ int nth_item(int r) {
-  const int c = blockIdx.x, n = gridDim.x;
-  return r * n + ((r & 1) ? n - 1 - c : c);
-}
-
 __device__ __forceinline__ Unit unit_of(const FwdParams &p, int it) {
   // (batch, head unit) in groups; in a group the late blocks of queries first, so that
   // what runs at one time shares K and V in L2 and the short items come last
