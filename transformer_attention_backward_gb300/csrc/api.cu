@@ -6,10 +6,12 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <string>
 
 #include "../../include/attn_bwd.h"
 #include "abw_host.h"
+#include "smem_limits.h"
 
 namespace {
 
@@ -248,27 +250,12 @@ cudaError_t ensure_dynamic_smem(const void *func, int bytes) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const unsigned long long ctx = context_id();
-  struct Entry {
-    const void *func;
-    int dev, bytes;
-    unsigned long long ctx;
-  };
   static std::mutex mu;
-  static Entry seen[64];
-  static int nseen = 0;
+  static SmemLimits *const limits = new (std::nothrow) SmemLimits;   // never freed: calls may come as the process ends
   std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < nseen; ++i) {
-    if (seen[i].func != func || seen[i].dev != dev) continue;
-    if (ctx != 0 && seen[i].ctx == ctx && seen[i].bytes >= bytes) return cudaSuccess;
-    e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) {
-      seen[i].bytes = bytes;
-      seen[i].ctx = ctx;
-    }
-    return e;
-  }
+  if (limits && limits->reaches(dev, func, ctx, bytes)) return cudaSuccess;
   e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && nseen < 64) seen[nseen++] = Entry{func, dev, bytes, ctx};
+  if (e == cudaSuccess && limits) limits->raised(dev, func, ctx, bytes);
   return e;
 }
 

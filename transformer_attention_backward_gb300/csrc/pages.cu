@@ -1059,7 +1059,7 @@ cudaError_t launch_kv_pages_evict(const PagesArgs &a, const float *weight_sums, 
   const bool cached = p.cap <= kEvCached;
   auto select = cached ? evict_select_kernel<true> : evict_select_kernel<false>;
   const int smem = cached ? p.cap * 4 : 0;
-  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void *>(select), cached ? kEvCached * 4 : 0);
+  cudaError_t e = cached ? ensure_dynamic_smem(reinterpret_cast<const void *>(select), kEvCached * 4) : cudaSuccess;
   if (e != cudaSuccess) return e;
   select<<<static_cast<unsigned>(blocks), kEvThr, smem, st>>>(p);
   e = cudaGetLastError();
