@@ -497,7 +497,11 @@ abw_status attn_fwd_window(const void *q, const void *k, const void *v, const in
  *   lse           [B][Hq][T] f32
  *   dq, dk, dv    bf16, token strides dq_stride, dk_stride, dv_stride (so they may
  *         be parts of a packed gradient); 0 behind each sequence's last token
- *   workspace     at least attn_bwd_window_workspace_bytes()
+ *   workspace     at least attn_bwd_window_workspace_bytes(): 32 KB for each query head
+ *         and pair of 128-token blocks that meet (T (min(window, T) + 256) / 16384 pairs
+ *         and less, and T / 128 for each 128 of the first tokens), of as many (sequence,
+ *         KV head)s as fit 2 GiB, one at least, which the call goes through in turn; with
+ *         8 bytes a query head and token, and sums of up to some 100 MB
  * P and dS enter their products rounded to bf16; sums are fp32 in a fixed order:
  * equal calls on a device give equal bits.
  * Supported sizes: as in the forward.

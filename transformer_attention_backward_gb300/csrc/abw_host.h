@@ -122,7 +122,7 @@ struct WindowArgs {
   void *o, *dq, *dk, *dv;             // o: written forward, read backward
   float *lse;
   int B, T, Hq, Hkv, D;
-  long long q_stride, k_stride, v_stride, o_stride, dq_stride, dk_stride, dv_stride;
+  long long q_stride, k_stride, v_stride, o_stride, dout_stride, dq_stride, dk_stride, dv_stride;
   int window, sinks;
   float scale;
   void *ws;

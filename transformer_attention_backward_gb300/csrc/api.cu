@@ -936,7 +936,7 @@ abw_status attn_bwd_window(const void *q, const void *k, const void *v, const vo
   a.B = B, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.D = D;
   const long long qn = static_cast<long long>(Hq) * D, kn = static_cast<long long>(Hkv) * D;
   a.q_stride = token_stride(q_stride, B, T, qn), a.k_stride = token_stride(k_stride, B, T, kn);
-  a.v_stride = token_stride(v_stride, B, T, kn), a.o_stride = token_stride(o_stride, B, T, qn);
+  a.v_stride = token_stride(v_stride, B, T, kn), a.o_stride = token_stride(o_stride, B, T, qn), a.dout_stride = qn;
   a.dq_stride = token_stride(dq_stride, B, T, qn), a.dk_stride = token_stride(dk_stride, B, T, kn);
   a.dv_stride = token_stride(dv_stride, B, T, kn);
   a.window = window, a.sinks = sinks;

@@ -99,7 +99,7 @@ struct BwdParams {
   float *parts;                   // [units][slots][2: dV, dK][D / 4][128 keys][4]
   __nv_bfloat16 *dq, *dk, *dv;
   int B, T, Tp, Hq, Hkv, G;
-  long long o_stride, dk_stride, dv_stride, tiles;
+  long long o_stride, dout_stride, dk_stride, dv_stride, tiles;
   Grid g;
   int first_parts, parts_each;    // CTAs per key block: first tokens', others
   int per_unit, slots;            // items (without the first tokens') and part slots per (batch, KV head)
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kPrepThr) window_prep_kernel(const __grid_cons
     if (t < n) {
       const long long tok = static_cast<long long>(b) * p.T + t;
       x[k] = *reinterpret_cast<const uint4 *>(p.o + tok * p.o_stride + static_cast<size_t>(h) * kD + 8 * sub);
-      y[k] = *reinterpret_cast<const uint4 *>(p.dout + (tok * p.Hq + h) * kD + 8 * sub);
+      y[k] = *reinterpret_cast<const uint4 *>(p.dout + tok * p.dout_stride + static_cast<size_t>(h) * kD + 8 * sub);
       if (sub == 0) l[k] = p.lse[row * p.T + t];
     }
   }
@@ -890,9 +890,8 @@ BwdSizes bwd_sizes(int B, int T, int Hq, int Hkv, int D, int window, int sinks) 
 template <int kD>
 cudaError_t launch(const WindowArgs &a, BwdParams &p, const BwdSizes &s, int sms, cudaStream_t st, const char **why) {
   CUtensorMap q, dout, k, v, dq, dk, dv;
-  const long long qn = static_cast<long long>(a.Hq) * kD;
   if (!token_map(&q, a.q, a.Hq, a.T, a.B, kD, a.q_stride, kBlk, why) ||
-      !token_map(&dout, a.dout, a.Hq, a.T, a.B, kD, qn, kBlk, why) ||
+      !token_map(&dout, a.dout, a.Hq, a.T, a.B, kD, a.dout_stride, kBlk, why) ||
       !token_map(&k, a.k, a.Hkv, a.T, a.B, kD, a.k_stride, kBlk, why) ||
       !token_map(&v, a.v, a.Hkv, a.T, a.B, kD, a.v_stride, kBlk, why) ||
       !token_map(&dq, a.dq, a.Hq, a.T, a.B, kD, a.dq_stride, 32, why) ||
@@ -942,18 +941,47 @@ cudaError_t launch(const WindowArgs &a, BwdParams &p, const BwdSizes &s, int sms
   return cudaGetLastError();
 }
 
-}  // namespace
+// The dS tiles of a call may be more than a card holds (one sequence of 131,072 tokens, 32
+// heads, window 1024: 10 GB; all keys: 550 GB), so a call goes through its (batch, KV head)s
+// in slabs of at most this much: whole sequences, or KV heads of one.  Calls of 2.1 to 8.3 GB,
+// us at 256 MB, 512 MB, 1 GB, 2 GB and in one go: 1 x 8192 tokens of 32 heads, all keys, 1727,
+// 1318, 1210, 1202, 1210; 1 x 32768 of 32, window 4096, 5630, 5225, 4700, 4550, 4590; 1 x 65536
+// of 16, window 1024, 1990, 1832, 1725, 1689, 1681: a slab's last CTAs end alone.
+constexpr long long kSlabBytes = 2LL << 30;
 
-size_t window_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int window, int sinks) {
-  const BwdSizes s = bwd_sizes(B, T, Hq, Hkv, D, window, sinks);
-  return 256 + 2 * s.stats + s.ds + s.parts;
+struct Slab {
+  int seqs, heads;   // sequences with all KV heads, or KV heads of one sequence
+};
+Slab slab_of(int B, int T, int Hq, int Hkv, int window, int sinks) {
+  const Grid g = grid_of(T, window, sinks);
+  const long long head = g.tile0(g.nb) * kTileBytes * (Hq / Hkv), fit = std::max(1LL, kSlabBytes / head);
+  auto even = [](long long n, long long most) {   // of as many slabs of at most `most` as it takes, the size of one
+    const long long slabs = (n + most - 1) / most;
+    return static_cast<int>((n + slabs - 1) / slabs);
+  };
+  return fit >= Hkv ? Slab{even(B, fit / Hkv), Hkv} : Slab{1, even(Hkv, fit)};
 }
 
-cudaError_t launch_window_bwd(const WindowArgs &a, const WaitCtl &w, cudaStream_t st, const char **why) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
+// The call on sequences b .. b + seqs - 1 and KV heads h .. h + heads - 1 (all of them, or one sequence).
+WindowArgs part_of(const WindowArgs &a, long long b, long long seqs, long long h, long long heads) {
+  const int G = a.Hq / a.Hkv;
+  const long long tok = b * a.T, qh = h * G;
+  auto at = [&](const void *x, long long stride, long long head) {
+    return static_cast<const __nv_bfloat16 *>(x) + tok * stride + head * a.D;
+  };
+  auto out = [&](void *x, long long stride, long long head) { return const_cast<__nv_bfloat16 *>(at(x, stride, head)); };
+  WindowArgs r = a;
+  r.q = at(a.q, a.q_stride, qh), r.dout = at(a.dout, a.dout_stride, qh);
+  r.k = at(a.k, a.k_stride, h), r.v = at(a.v, a.v_stride, h);
+  r.o = out(a.o, a.o_stride, qh), r.dq = out(a.dq, a.dq_stride, qh);
+  r.dk = out(a.dk, a.dk_stride, h), r.dv = out(a.dv, a.dv_stride, h);
+  r.lse = a.lse + (b * a.Hq + qh) * a.T;
+  if (a.lengths) r.lengths = a.lengths + b;
+  r.B = static_cast<int>(seqs), r.Hq = static_cast<int>(heads * G), r.Hkv = static_cast<int>(heads);
+  return r;
+}
+
+cudaError_t launch_slab(const WindowArgs &a, const WaitCtl &w, int sms, cudaStream_t st, const char **why) {
   const BwdSizes s = bwd_sizes(a.B, a.T, a.Hq, a.Hkv, a.D, a.window, a.sinks);
   const long long units = static_cast<long long>(a.B) * a.Hkv, lead_items = units * s.g.first * s.first_parts;
   const long long items = lead_items + units * s.per_unit;
@@ -974,7 +1002,7 @@ cudaError_t launch_window_bwd(const WindowArgs &a, const WaitCtl &w, cudaStream_
   p.dq = static_cast<__nv_bfloat16 *>(a.dq);
   p.dk = static_cast<__nv_bfloat16 *>(a.dk), p.dv = static_cast<__nv_bfloat16 *>(a.dv);
   p.B = a.B, p.T = a.T, p.Tp = s.Tp, p.Hq = a.Hq, p.Hkv = a.Hkv, p.G = a.Hq / a.Hkv;
-  p.o_stride = a.o_stride, p.dk_stride = a.dk_stride, p.dv_stride = a.dv_stride;
+  p.o_stride = a.o_stride, p.dout_stride = a.dout_stride, p.dk_stride = a.dk_stride, p.dv_stride = a.dv_stride;
   p.tiles = s.tiles;
   p.g = s.g;
   p.first_parts = s.first_parts, p.parts_each = s.parts_each, p.per_unit = s.per_unit, p.slots = s.slots;
@@ -997,6 +1025,31 @@ cudaError_t launch_window_bwd(const WindowArgs &a, const WaitCtl &w, cudaStream_
   p.scale = a.scale;
   p.wait = w;
   return a.D == 64 ? launch<64>(a, p, s, sms, st, why) : launch<128>(a, p, s, sms, st, why);
+}
+
+}  // namespace
+
+size_t window_bwd_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int window, int sinks) {
+  const Slab s = slab_of(B, T, Hq, Hkv, window, sinks);
+  const int G = Hq / Hkv;
+  size_t most = 0;
+  for (int seqs : {s.seqs, (B - 1) % s.seqs + 1})                     // a slab, the last one
+    for (int heads : {s.heads, (Hkv - 1) % s.heads + 1}) {
+      const BwdSizes z = bwd_sizes(seqs, T, heads * G, heads, D, window, sinks);
+      most = std::max(most, 256 + 2 * z.stats + z.ds + z.parts);
+    }
+  return most;
+}
+
+cudaError_t launch_window_bwd(const WindowArgs &a, const WaitCtl &w, cudaStream_t st, const char **why) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const Slab s = slab_of(a.B, a.T, a.Hq, a.Hkv, a.window, a.sinks);
+  for (long long b = 0; b < a.B; b += s.seqs)
+    for (long long h = 0; e == cudaSuccess && h < a.Hkv; h += s.heads)
+      e = launch_slab(part_of(a, b, std::min<long long>(s.seqs, a.B - b), h, std::min<long long>(s.heads, a.Hkv - h)), w, sms, st, why);
+  return e;
 }
 
 }  // namespace abw
