@@ -800,9 +800,11 @@ def kv_pages_evict(k_pages, v_pages, block_table, lengths, weight_sums, budget, 
         return t, _dense(t, name, dt, shape, dev)
     if budget < 1:
         raise ValueError(f"budget={budget} must be >= 1")
-    kept, kat = out(kept, "kept", torch.int32, (B, Hkv, budget))
-    new_lengths, nat = out(new_lengths, "new_lengths", torch.int32, (B,))
-    new_weight_sums, wat = out(new_weight_sums, "new_weight_sums", _F32, (B, Hkv, page * fresh))
+    kat = nat = wat = None
+    if budget <= page * fresh:        # more is the library's to refuse, with no output of that size made
+        kept, kat = out(kept, "kept", torch.int32, (B, Hkv, budget))
+        new_lengths, nat = out(new_lengths, "new_lengths", torch.int32, (B,))
+        new_weight_sums, wat = out(new_weight_sums, "new_weight_sums", _F32, (B, Hkv, page * fresh))
     _call("kv_pages_evict", _fns().kv_pages_evict, dev, stream, None, None, kp, vp, tp, lp, wp, np_, kat, nat, wat, B, Hkv,
           D, *sizes, fresh, budget, sinks, recent)
     return kept, new_lengths, new_weight_sums
