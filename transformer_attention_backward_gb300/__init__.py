@@ -683,7 +683,7 @@ def attn_fwd_window(q, k, v, window, sinks=0, scale=None, lengths=None, o=None, 
 
 @functools.lru_cache(maxsize=1024)
 def attn_bwd_window_workspace_bytes(B, T, Hq, Hkv, D, window, sinks=0) -> int:
-    return int(library().attn_bwd_window_workspace_bytes(B, T, Hq, Hkv, D, window, sinks))
+    return int(library().attn_bwd_window_workspace_bytes(B, T, Hq, Hkv, D, _int32(window, "window"), _int32(sinks, "sinks")))
 
 
 def attn_bwd_window(q, k, v, o, dout, lse, window, sinks=0, scale=None, lengths=None, dq=None, dk=None, dv=None,
@@ -740,8 +740,8 @@ def kv_pages_write(k, v, k_pages, v_pages, block_table, starts, lengths=None, st
 @functools.lru_cache(maxsize=1024)
 def attn_decode_paged_workspace_bytes(B, Hq, Hkv, D, page_size, max_pages, window=None, sinks=0,
                                       with_weight_sums=False) -> int:
-    return int(library().attn_decode_paged_workspace_bytes(B, Hq, Hkv, D, page_size, max_pages, window or 0, sinks,
-                                                           1 if with_weight_sums else 0))
+    return int(library().attn_decode_paged_workspace_bytes(B, Hq, Hkv, D, page_size, max_pages, _int32(window or 0, "window"),
+                                                           _int32(sinks, "sinks"), 1 if with_weight_sums else 0))
 
 
 def attn_decode_paged(q, k_pages, v_pages, block_table, lengths, scale=None, window=None, sinks=0, weight_sums=None,
