@@ -42,7 +42,8 @@
  *     where an operation needs it, is a caller-provided workspace.
  *   - Work is enqueued on `stream` (NULL = the legacy default stream) and the
  *     call returns without synchronizing.  Outputs are overwritten, never
- *     accumulated into.
+ *     accumulated into (but weight_sums of attn_decode_paged, and pages, of
+ *     which a call writes the rows that it names).
  *   - Inputs and outputs must not overlap, except where stated (rope_bwd allows
  *     dx == dy).
  *   - Every tensor is dense and row-major in the layout given, with its base
@@ -554,7 +555,9 @@ abw_status kv_pages_write(const void *k, const void *v, void *k_pages, void *v_p
  *         head added; the others are left as they are
  *   window        >= 0 (0: none);  sinks >= 0 (not looked at without a window)
  *   workspace     at least attn_decode_paged_workspace_bytes(); unspecified
- *         contents
+ *         contents.  Some MB (the pieces of 304 CTAs), with weight_sums and 4 bytes for each
+ *         row, query head and position that the table has room for (with a window:
+ *         at most window + sinks), whatever the lengths
  * The cache is read once, in pieces of equal length over all sequences whatever
  * their lengths, and the pieces are joined.  q and p enter the products as sums of
  * bf16 terms that keep 16 bits of them and more, sums are fp32.  Values of visible
@@ -573,7 +576,9 @@ abw_status attn_decode_paged(const void *q, abw_dtype dtype, const void *k_pages
  * kv_pages_evict -- keeps, for each sequence and KV head, at most `budget` tokens
  * of the cache: those at positions below `sinks`, the last `recent` positions,
  * and of the others those of the largest weight_sums (ties: the lower position; a
- * NaN counts as -infinity).  Tokens of absent pages are not kept.  The kept
+ * NaN counts as -infinity).  Tokens of absent pages are not kept.  Only
+ * attn_decode_paged adds to the sums: right behind a prompt they are what the
+ * caller put there, and of equal ones (all 0) the lowest positions stay.  The kept
  * ones go, in their order, to positions 0, 1, .. of the pages that new_table names
  * (the old pages stay as they are: they may be shared with other sequences).
  *   k_pages, v_pages  read in the pages of block_table, written in those of

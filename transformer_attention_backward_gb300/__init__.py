@@ -690,7 +690,8 @@ def attn_bwd_window(q, k, v, o, dout, lse, window, sinks=0, scale=None, lengths=
                     workspace=None, stream=None):
     """Gradients of attn_fwd_window from its o and lse: dout [B][T][Hq][D]
     bf16.  Returns (dq, dk, dv) bf16 (given ones may be parts of a packed
-    gradient), 0 behind each sequence's last token."""
+    gradient), 0 behind each sequence's last token.  The workspace is some 2
+    GiB at most, or what one KV head needs."""
     dev, dims, kshape, strides, (qp, kp, vp, ln), sees = _window_inputs(q, k, v, lengths, window, sinks)
     B, T, Hq, _, D = dims
     os = _rows(o, "o", _BF16, q.shape, dev)
@@ -782,8 +783,9 @@ def kv_pages_evict(k_pages, v_pages, block_table, lengths, weight_sums, budget, 
     """Keeps at most ``budget`` tokens of each sequence and KV head of a paged
     cache: the first ``sinks`` positions, the last ``recent``, and of the
     others those of the largest weight_sums [B][Hkv][max_pages * page_size]
-    fp32 (ties: the lower position).  They go, in their order, to positions 0,
-    1, .. of the pages of new_table [B][new_max_pages] int32, which must be
+    fp32 (ties: the lower position; right behind a prompt, before any decode
+    has added to the sums, all are equal).  They go, in their order, to positions
+    0, 1, .. of the pages of new_table [B][new_max_pages] int32, which must be
     others than those of block_table; the old pages stay as they are.  Returns
     (kept [B][Hkv][budget] int32 positions, -1 behind the last; new_lengths
     [B] int32; new_weight_sums [B][Hkv][new_max_pages * page_size] fp32)."""

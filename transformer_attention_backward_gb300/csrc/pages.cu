@@ -106,8 +106,9 @@ constexpr int kDecStages = 2;
 constexpr int kTile = 16;            // positions per tile
 constexpr int kMinTiles = 8;         // tiles a CTA takes at least, while there are few
 constexpr int kDecCtas = 304;        // two per SM
-constexpr int kWtPos = 1024;         // positions per block of the weight sums, at least
-constexpr int kWtBlocks = 1216;      // ... and blocks to spread them over
+// Blocks of the weight sums: as many for each sequence and KV head as give a full table
+// kWtPos positions a block, one at least, while that makes no more than kWtBlocks.
+constexpr int kWtPos = 1024, kWtBlocks = 1216;
 constexpr int kWtUnroll = 4;
 constexpr uint32_t kNoRow = 0xffffffffu;
 constexpr float kLazy = 8.f;         // base-2 units a score may exceed the running maximum by
@@ -607,8 +608,9 @@ __global__ void __launch_bounds__(32 * dec_warps(kF32, kWide), 2) decode_split_k
 }
 
 // Blocks 0 .. ctas - 1: block c joins the unit that begins in CTA c's run and
-// goes on behind it.  Blocks behind them, with weight sums: kWtPos positions of
-// a sequence and KV head each.
+// goes on behind it.  Blocks behind them, with weight sums: wt_len visible positions
+// of a sequence and KV head each, wt_chunks blocks for the table's capacity (so a short
+// sequence in a wide table is left to its first blocks).
 constexpr int kFinThr = 256;
 
 // Slot of the i-th piece of a unit whose first tile is `seg`.

@@ -31,10 +31,12 @@
 // Rows behind a sequence's last token are cleared in shared memory before a
 // product sees them, so nothing there (NaN included) is looked at.
 //
-// 4 x 2048 tokens of 20 heads, window 512: 175 us.  prep 16: memory.  kv 113: a pair of
-// blocks takes 1.8 us, of which the four products are 1.05; S, the exponentials, dV
-// and dP, dS, dK are two chains that depend on one another, and an item's outputs
-// stand between its last pair and the next one's first.  dq 47: memory, mostly the dS
+// 4 x 2048 tokens of 20 heads, window 512: 175 us.  prep 16: memory.  kv 112: a CTA has
+// 43 pairs of blocks in 8 items.  A pair takes 2.0 us (windows of 512, 1024 and all keys:
+// 112, 150, 170 us for 43, 61, 72 pairs), of which the four products are 1.05: S, the
+// exponentials, dV and dP, dS, dK are two chains that depend on one another.  The other 27
+// us are the changes of item: both accumulators and a slot of dO are handed on only when
+// the output warps have dV and dK out of TMEM.  dq 45: memory, mostly the dS
 // tiles, which are written once and read once (212 MB each; recomputing S and dP
 // there would take three products in place of one).  What measured worse: dS tiles,
 // dV and dK stored from registers (217 and 213 us in place of 194: a store of 32 rows

@@ -21,12 +21,16 @@
 // Padding behind a sequence is not looked at: its keys are never visible, and
 // its rows of V, which meet weights of 0, are cleared in shared memory.
 //
-// The bound is the tensor core with the softmax beside it: a block of 128 x 128 at D =
-// 128 takes it 1024 cycles for the two products, and the exponentials of two such
-// blocks (32 a cycle and SM) as long as the products of one.  8192 tokens of 32 heads,
-// window 1024: 136 us, 950 TFLOP/s of the visible pairs; the products of the blocks
-// alone, cut ones whole, are some 100, the softmax alone 124; the rest is the change
-// from item to item.  All keys: 390 us, 1400 TFLOP/s.  What measured no better: an
+// 8192 tokens of 32 heads, window 1024: 136 us, 950 TFLOP/s of the visible pairs; all
+// keys 390 us, 1400 TFLOP/s.  What bounds it is the softmax warps' chain.  A block of 128
+// x 128 at D = 128 is 1024 cycles of products and 512 of exponentials (32 a cycle and SM),
+// which run beside one another: the first call's 125 blocks a CTA are 68 us of the one
+// and 34 of the other at 1.9 GHz.  A whole block more takes 0.81 us, some 1,500 cycles
+// (the two calls' difference): its scores come out of TMEM one and a half times (128
+// registers a thread do not hold a row of them), are converted and go back, each step
+// behind a wait.  34 of the 136 us are what cut blocks' masks and the changes of item
+// cost on top.  (With the softmax taken out the kernel took 100 us, with the products
+// out 124: each with the other waits still in place.)  What measured no better: an
 // issuer per tile, eight softmax warps per tile, cut blocks 32 columns at a time,
 // prefetches of the next queries into L2, outputs read out of TMEM before they are staged.
 #include <algorithm>
